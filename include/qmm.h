@@ -1,7 +1,8 @@
 /*
  * qmm.h -- C ABI of the quantized projection matmul library for one GB300 (sm_103a).
  *
- * Two halves, and two widenings of the second:
+ * Two halves, two widenings of the second, and what runs between the
+ * projections of a decoding step:
  *   (I)   an exact int8 GEMM with zero-point correction, per-column weight
  *         scale, optional int32 bias and float or requantised output, and the
  *         int8 quantisation of its activations;
@@ -9,7 +10,9 @@
  *         its MUL_MAT_ID (mixture-of-experts) variant;
  *   (III) W8A16: int8 weights with block scales times bf16 activations;
  *   (IV)  more weight formats: Q4_K repacked into q4_1 tiles, and 8-bit (Q8)
- *         tiles in two code layouts.
+ *         tiles in two code layouts;
+ *   (V)   a paged key/value cache (bf16 or int8): the plan of a step, the
+ *         append of its rows, and attention of drafted token trees over it.
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -30,8 +33,10 @@
  *   caller sets to 0 (it may be NULL).  These are a bounded wait that ran out
  *   (QMM_ERR_TIMEOUT), an expert id outside [0, n_expert)
  *   (QMM_ERR_BAD_EXPERT_ID), a per-axis zero point outside its operand's
- *   domain (QMM_ERR_INVALID_ARG), and a weight block that the f16 tensor-core
- *   route cannot form (QMM_ERR_RANGE).  The library only ever replaces a 0
+ *   domain (QMM_ERR_INVALID_ARG), a weight block that the f16 tensor-core
+ *   route cannot form (QMM_ERR_RANGE), and lengths, slots, parents or page ids
+ *   of a step that do not fit its buffers (QMM_ERR_INVALID_ARG,
+ *   QMM_ERR_NO_PAGES).  The library only ever replaces a 0
  *   there with an error code, so the caller reads it after synchronising.
  * - Shapes the library has no kernel for return QMM_ERR_UNSUPPORTED.  There
  *   is no fallback path.
@@ -56,8 +61,9 @@ typedef enum {
   QMM_ERR_TIMEOUT = 5,         /* device: a bounded pipeline wait gave up */
   QMM_ERR_BAD_EXPERT_ID = 6,   /* device: an expert id was outside [0, n_expert) */
   QMM_ERR_WORKSPACE = 7,       /* workspace pointer NULL, misaligned or smaller than required */
-  QMM_ERR_RANGE = 8            /* device: a weight block beyond f16's range (|w| could pass 65504) on a
+  QMM_ERR_RANGE = 8,           /* device: a weight block beyond f16's range (|w| could pass 65504) on a
                                   route that forms f16 weights; the results of that call are not valid */
+  QMM_ERR_NO_PAGES = 9         /* device: a plan takes more pages than the free list holds */
 } qmm_status;
 
 typedef enum {
@@ -612,6 +618,158 @@ qmm_status qmm_q8_gemm_workspace_size(int64_t M, int64_t K, int64_t N, size_t* w
 qmm_status qmm_q8_gemm(const void* tiles, qmm_q8_layout layout, int64_t N, int64_t K, const void* X, int64_t M,
                        int64_t ldx, float* Y, int64_t ldy, void* workspace, size_t ws_bytes, int32_t* dev_status,
                        cudaStream_t stream);
+
+/* ========================================================================
+ * (V) Paged key/value cache and tree attention
+ *
+ * What a decoding step runs between the q/k/v and the output projections.  No
+ * counterpart on the pages, which stop at the projections.
+ *
+ * A cache is n_pages pages of page_size places; place p of page g is slot
+ * g * page_size + p.  Request r owns the pages block_table[r][0..]: its token
+ * number j (from 0) sits at place j % page_size of page
+ * block_table[r][j / page_size].  A step adds new_lens[r] tokens to the
+ * ctx_lens[r] cached ones; the step's tokens of all requests lie one after
+ * another ("rows" 0..T-1), request r's from cu_new[r] to cu_new[r+1] - 1.
+ * Lengths, tables and slots are device data, so that a captured graph serves
+ * every step of the same capacity.
+ *
+ * One step:  qmm_kv_plan once; then per layer the q/k/v projections,
+ * qmm_kv_append, qmm_tree_attention and the output projection (which takes
+ * the attention's bf16 output as its X).
+ * ======================================================================== */
+
+/* Pages, slots, positions and tree masks of a step, in one launch.
+ *
+ * ctx_lens, new_lens  int32 [R], >= 0: cached and new tokens of each request.
+ * free_pages   int32 [n_free]: ids of unused pages, taken from the front in
+ *              the order of the requests (NULL when n_free is 0).
+ * block_table  int32 [R][max_blocks], row stride ld_table, in and out: the
+ *              entries of the pages that the step begins are written (request
+ *              r's columns ceil(ctx/P) .. ceil((ctx+new)/P) - 1); entries of
+ *              older pages are read, others left alone.
+ * parents      int32 [max_tokens] or NULL.  With it the new tokens are drafted
+ *              trees: parents[row] is the parent's number among the request's
+ *              new tokens (0-based, smaller than the token's own), or -1 for a
+ *              root, which follows the cached tokens.
+ * mask         with parents: uint32 [max_tokens][mask_words] out, row stride
+ *              ld_mask: bit j % 32 of word j / 32 of a token's row is set when
+ *              j is the token itself or one of its ancestors.  NULL, with
+ *              mask_words 0, without parents.
+ * max_tokens   capacity in rows of slots, positions, parents and mask; rows
+ *              past the step's tokens get slot -1, position 0 and mask 0.
+ * cu_new       int32 [R+1] out: exclusive sums of new_lens.
+ * slots        int64 [max_tokens] out: where qmm_kv_append puts each token.
+ * positions    int32 [max_tokens] out: ctx + number (ctx + depth in a tree).
+ * pages_taken  int32 [1] out: how many of free_pages the step uses.
+ * The call reads only what it does not write: on the same inputs it gives the
+ * same results again.
+ * Device status: QMM_ERR_NO_PAGES (pages_taken > n_free) and
+ * QMM_ERR_INVALID_ARG (a negative length, more than max_tokens tokens, more
+ * than max_blocks pages of a request, a parent that is not an earlier token, a
+ * token number that the mask has no bit for); a token without a page gets
+ * slot -1.
+ * Errors: QMM_ERR_INVALID_ARG for null or misaligned pointers, R < 1, a short
+ * stride, page_size or max_blocks < 1, negative sizes, a mask without parents
+ * or the reverse; QMM_ERR_UNSUPPORTED for R > 16384, or page_size or
+ * max_tokens >= 2^31.
+ */
+qmm_status qmm_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t R, const int32_t* free_pages,
+                       int64_t n_free, int32_t* block_table, int64_t ld_table, int64_t max_blocks,
+                       int64_t page_size, const int32_t* parents, uint32_t* mask, int64_t ld_mask,
+                       int64_t mask_words, int64_t max_tokens, int32_t* cu_new, int64_t* slots,
+                       int32_t* positions, int32_t* pages_taken, int32_t* dev_status, cudaStream_t stream);
+
+/* A cache: the row of (page, place, key head) starts at element
+ *   page * stride_page + place * stride_token + head * stride_head
+ * of k and of v, head_dim consecutive elements (both layouts of a page,
+ * [place][head] and [head][place], are strides).  Passed by host pointer.
+ * type QMM_BF16: the rows as they are.  QMM_S8: int8 codes, value =
+ * code * scale with one fp32 scale per (page, head, place):
+ * k_scale, v_scale [n_pages][n_heads][page_size] (NULL for QMM_BF16).
+ * head_dim 64 or 128 (else QMM_ERR_UNSUPPORTED); k and v 16-byte aligned,
+ * strides of whole 16 bytes (of a dimension of one row: anything), scales
+ * 4-byte aligned; the rows of different (page, place, head) must not overlap. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  qmm_dtype type;
+  int64_t n_pages, page_size, n_heads, head_dim;
+  int64_t stride_page, stride_token, stride_head;
+} qmm_kv_cache;
+
+/* Store T tokens' key and value rows at their slots.
+ *
+ * K, V    [T][n_heads][head_dim], fp32 or bf16 (type), element strides
+ *         (token, head), 16-byte aligned with strides of whole 16 bytes; the
+ *         head's elements are contiguous.
+ * slots   int64 [T]: -1 skips the token; any other slot outside the cache is
+ *         skipped with QMM_ERR_INVALID_ARG in dev_status.  Two tokens with one
+ *         slot leave either one's values there.
+ * bf16 cache: rounded once to nearest even.  int8 cache, per (token, head):
+ *   s = fl(amax / 127), q = clamp(rint_even(fl(x / s)), -127, 127), 0 where
+ * s == 0 (packB's rule, bit-exact); x must be finite there, else that row's
+ * codes and scale are unspecified.
+ * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
+ * pointers, bad types, sizes or strides; QMM_ERR_UNSUPPORTED for another
+ * head_dim, T * n_heads >= 2^31 * 8 or page_size >= 2^31.
+ */
+qmm_status qmm_kv_append(const void* K, int64_t k_stride_token, int64_t k_stride_head, const void* V,
+                         int64_t v_stride_token, int64_t v_stride_head, qmm_dtype type, int64_t T,
+                         const int64_t* slots, const qmm_kv_cache* cache, int32_t* dev_status,
+                         cudaStream_t stream);
+
+/* Workspace of qmm_tree_attention on the current device (partial results of
+ * work that is split between blocks): a function of max_new * n_q_heads /
+ * n_kv_heads, not of the contexts' lengths. */
+qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
+                                             int64_t max_new, size_t* ws_bytes);
+
+/* Attention of a step's tokens over the cache, the step's own rows (already
+ * appended) included:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)
+ * with the keys and values of key head h / (n_q_heads / n_kv_heads), over the
+ * j that row t of request r sees: every j < ctx_lens[r], and of the new tokens
+ * (j - ctx_lens[r] = number i) those whose bit is set in its mask row, or
+ * without a mask those up to its own number (a causal chunk; one token per
+ * request is plain decoding).  A row that sees nothing gets zeros.
+ *
+ * q         [T][n_q_heads][head_dim] fp32 or bf16 (q_type; fp32 is rounded
+ *           once to bf16), element strides, 16-byte aligned with strides of
+ *           whole 16 bytes.
+ * block_table, ctx_lens, cu_new  as above; cu_new[R] <= T.  Rows of q and out
+ *           that belong to no request are neither read nor written.
+ * max_new   no request has more new tokens (it chooses the kernel).
+ * mask      uint32 [T][ld_mask] or NULL; ld_mask * 32 >= max_new.
+ * scale     > 0, finite (1 / sqrt(head_dim) usually).
+ * out       bf16, element strides, aligned as q.
+ * workspace at least qmm_tree_attention_workspace_size bytes, 256-byte
+ *           aligned, rewritten by the call.
+ * What a row does not see never reaches its result, whatever it holds: places
+ * past a request's length, and infinities or NaN in hidden tokens.  Products
+ * are of bf16 values (int8 codes are exact in bf16; their scales are applied
+ * in fp32), and every sum is fp32, in a fixed order: results are the same from
+ * run to run.  The weights exp(s - max) multiply v as two bf16 terms (within
+ * 2^-16) with up to 32 query rows per key head (max_new * n_q_heads / n_heads),
+ * and rounded to bf16 once (2^-8) with more; the output is rounded once.
+ * Device status: QMM_ERR_INVALID_ARG for lengths that do not fit (negative,
+ * more than max_new or T, more than max_blocks pages): that request's rows of
+ * out are left alone; and for a page id outside [0, n_pages), whose request's
+ * rows are then unspecified.
+ * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
+ * pointers, bad types, sizes, strides or scale, n_q_heads not a multiple of
+ * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for another head_dim, or
+ * max_new * n_q_heads / n_heads, R, T or page_size >= 2^30.
+ */
+qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_token, int64_t q_stride_head,
+                              int64_t n_q_heads, const qmm_kv_cache* cache, const int32_t* block_table,
+                              int64_t ld_table, int64_t max_blocks, const int32_t* ctx_lens,
+                              const int32_t* cu_new, int64_t R, int64_t T, int64_t max_new,
+                              const uint32_t* mask, int64_t ld_mask, float scale, void* out,
+                              int64_t out_stride_token, int64_t out_stride_head, void* workspace,
+                              size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
 
 /* ========================================================================
  * Diagnostics

@@ -1,0 +1,603 @@
+// Attention of a step's new tokens (a drafted tree, one token, or a causal
+// chunk) over a paged cache, for few query rows per key head.
+//
+//   s_j = scale * q . k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+// over the visible j: every cached token before the step, and the new tokens
+// that the row's mask (or the chain) names.  One pass over the cache with a
+// running maximum and sum in fp32 (the exponentials in base 2).
+//
+// Decoding has 2 operations per row and cached byte at bf16, so up to 64 rows
+// or so the cache's bytes are all that costs.  The kernel is a stream: four
+// warps per block, each with its own ring of 16-token groups (cp.async, no
+// block barrier inside an item), two blocks per SM; a group's rows are
+// multiplied with mma.sync (16 x 8 x 16, bf16 with fp32 sums) straight from
+// the ring.  The warps' running values are joined at the end of an item in
+// shared memory, and items cut between blocks by the combine kernel.
+//
+// Operand layouts.  The order of the head's dimensions inside a product is
+// free as long as q and k agree: a thread of the quad takes 16-byte pieces
+// 4 i + c of a key row, which are its B fragments as they lie (bf16: two
+// steps of 16 per piece; int8: four), and the query fragments are gathered
+// to match, once per item.  bf16 values go through ldmatrix.trans; int8
+// values are read as 16-byte pieces of four tokens and interleaved by byte
+// permutes.  int8 codes become bf16 exactly; a token's key scale multiplies
+// its column of s, its value scale the weight.  A weight meets v as two bf16
+// terms (within 2^-16 of itself): one term alone would be 2^-8 off, as much as
+// the output's own rounding, and the second product is free under the loads.
+// The sums are fp32.
+//
+// Rows of the cache past a request's length are never read (cp.async writes
+// zeros in their place).  A new token's value row is read by all query rows
+// of the tile, also by those whose mask hides it, and 0 * inf would not be 0:
+// non-finite values among the new tokens are taken out of the ring, and added
+// at the end to the rows that do see them.
+#include <algorithm>
+
+#include "attn_work.cuh"
+#include "umma.cuh"
+
+namespace qmm {
+namespace {
+
+using namespace umma;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 16;                       // cached tokens per warp step
+constexpr int kTileTokens = kGroup * kWarps;     // a unit
+constexpr int kBlocksPerSm = 2;
+constexpr int kRingBytes = 24576;                // per warp
+
+template <int D, bool kS8>
+struct Geo {
+  static constexpr int kRow = D * (kS8 ? 1 : 2);             // bytes of a row
+  static constexpr int kPieces = kRow / 16;                  // 16-byte pieces of a row
+  static constexpr int kSide = kGroup * kRow;                // K or V of a group
+  static constexpr int kStage = 2 * kSide + (kS8 ? 2 * kGroup * 4 : 0);
+  static constexpr int kStages = kRingBytes / kStage < 8 ? kRingBytes / kStage : 8;
+  static constexpr int kRing = kStages * kStage;
+  // Place of piece p of key row t: a quarter warp reads 4 pieces of 2 rows.
+  QMM_DEV static uint32_t k_at(int t, int p) {
+    if constexpr (kPieces >= 8) return t * kRow + ((p ^ ((t & 1) << 2)) << 4);
+    else return t * kRow + (p << 4);                         // 64-byte rows: two rows fill the banks
+  }
+  // Place of piece p of value row t.  bf16: ldmatrix reads one piece of 8
+  // rows; int8: 8 lanes read 2 pieces of the rows 2c (64-byte rows: pieces of
+  // the 128-byte line that holds two rows).
+  QMM_DEV static uint32_t v_at(int t, int p) {
+    if constexpr (!kS8) return t * kRow + ((p ^ (t & 7)) << 4);
+    else if constexpr (kPieces == 8) return t * kRow + ((p ^ (((t >> 1) & 3) << 1)) << 4);
+    else return (t >> 1) * 128 + (((((t & 1) << 2) | p) ^ (((t >> 1) & 3) << 1)) << 4);
+  }
+};
+
+QMM_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+QMM_DEV uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+QMM_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+QMM_DEV void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+QMM_DEV uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// Two int8 codes in the low bytes of 16-bit lanes -> bf16x2, exactly: the low
+// seven bits on top of 128, and -128 or (sign bit) -256 added.
+QMM_DEV uint32_t s8_lanes_to_bf16(uint32_t x) {
+  uint32_t lo, hi, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(x), "r"(0x007F007Fu), "r"(0x43004300u));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(x), "r"(0x00800080u), "r"(0xC300C300u));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+QMM_DEV uint32_t s8_low_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4140)); }
+QMM_DEV uint32_t s8_high_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4342)); }
+
+QMM_DEV bool bf16_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+// One element of the cache's value rows.
+QMM_DEV float cached_v(const AttnArgs& a, int r, int h, int tok, int d) {
+  const int32_t page = a.table[(int64_t)r * a.ld_table + tok / a.cache.page_size];
+  const int64_t off = attn_row_offset(a, page, tok);
+  if (off < 0) return 0.f;
+  const uint8_t* p = a.cache.v + h * a.cache.st_head + off + 2 * d;
+  return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+}
+
+template <int D, bool kS8, bool kQF32, int MT>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+  using G = Geo<D, kS8>;
+  constexpr int kRows = 16 * MT;
+  constexpr int kSteps = D / 16;                 // mma steps over the head's dimensions
+  constexpr int kTiles = D / 8;                  // 8-column tiles of the output
+  constexpr int kPitch = D + 8;                  // fp32 per row of the joining buffer
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ AttnFindScratch find;
+  __shared__ float s_ml[2][kWarps][kRows];
+  __shared__ int s_bad;
+  uint8_t* smem = smem_align(smem_raw, 128);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(smem) + wid * G::kRing;
+  float* joined = reinterpret_cast<float*>(smem);   // [kWarps][kRows][kPitch], after the ring is drained
+
+  pdl_launch_dependents();
+  pdl_wait();
+  AttnWork w;
+  if (!attn_find_work<kThreads>(a, kRows, kTileTokens, &find, w)) {
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  int4 owned = make_int4(0, 0, 0, 0);            // the item that this block begins and another ends
+
+  int r = w.r;
+  int64_t off = w.off, u = w.u0;
+  AttnReq rq = attn_req(a, r, kRows, kTileTokens);
+  while (u < w.u1) {
+    while (off >= rq.units) {                    // to the next request that has work
+      off -= rq.units;
+      rq = attn_req(a, ++r, kRows, kTileTokens);
+    }
+    const int item = (int)(off / rq.kv_tiles), kv0 = (int)(off % rq.kv_tiles);
+    const int h = item / rq.row_tiles, row0 = (item % rq.row_tiles) * kRows;
+    const int seg = (int)min((int64_t)(rq.kv_tiles - kv0), w.u1 - u);
+    const int L = rq.L, len = rq.L + rq.n, n_rows = min(kRows, rq.n * a.group - row0);
+    const int tok_first = kv0 * kTileTokens + wid * kGroup;
+
+    // ---- the ring ----
+    const int32_t* trow = a.table + (int64_t)r * a.ld_table;
+    const uint8_t* kbase = a.cache.k + h * a.cache.st_head;
+    const uint8_t* vbase = a.cache.v + h * a.cache.st_head;
+    auto page_of = [&](int it) -> int32_t {      // of this lane's token of step it, -1 past the end
+      const int tok = tok_first + it * kTileTokens + (lane & 15);
+      return it < seg && tok < len ? trow[(uint32_t)tok / a.cache.page_size] : -1;
+    };
+    auto issue = [&](int it, int32_t page) {
+      const int tok = tok_first + it * kTileTokens + (lane & 15);
+      const bool live = it < seg && tok < len;
+      const int64_t at = live ? attn_row_offset(a, page, tok) : -1;
+      if (live && at < 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+      const uint32_t dst = ring + (it % G::kStages) * G::kStage;
+      if (it < seg) {
+        constexpr int kRowsPer = 32 / G::kPieces;
+        const int p = lane % G::kPieces;
+#pragma unroll
+        for (int i = 0; i < kGroup / kRowsPer; ++i) {
+          const int t = lane / G::kPieces + i * kRowsPer;
+          const int64_t ro = __shfl_sync(0xffffffffu, at, t);
+          const uint32_t bytes = ro >= 0 ? 16u : 0u;
+          const int64_t src = ro >= 0 ? ro + p * 16 : 0;
+          cp_async16_zfill(dst + G::k_at(t, p), kbase + src, bytes);
+          cp_async16_zfill(dst + G::kSide + G::v_at(t, p), vbase + src, bytes);
+        }
+        if constexpr (kS8) {                     // lanes 0..15: key scales, 16..31: value scales
+          const float* sc = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
+          const uint32_t bytes = at >= 0 ? 4u : 0u;
+          if (at >= 0)
+            sc += ((int64_t)page * a.cache.n_heads + h) * a.cache.page_size + (uint32_t)tok % a.cache.page_size;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 2 * G::kSide + lane * 4), "l"(sc),
+                       "r"(bytes)
+                       : "memory");
+        }
+      }
+      cp_async_commit();
+    };
+    {
+      int32_t pages[G::kStages];
+#pragma unroll
+      for (int s = 0; s < G::kStages; ++s) pages[s] = page_of(s);
+#pragma unroll
+      for (int s = 0; s < G::kStages; ++s) issue(s, pages[s]);
+    }
+
+    // ---- the query rows, as A fragments in the order of the key's pieces ----
+    uint32_t qf[MT][kSteps][4];
+    int node[MT][2];                             // the new token of each of the thread's rows, -1: no row
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int rr = mt * 16 + hf * 8 + g;
+        const bool live = rr < n_rows;
+        const int row = row0 + rr, i = row / a.group;
+        node[mt][hf] = live ? i : -1;
+        const int64_t qo = (int64_t)(rq.first + i) * a.q_st + (int64_t)(h * a.group + row % a.group) * a.q_sh;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const int d = kS8 ? 16 * c + 64 * (s >> 2) + 4 * (s & 3) : 8 * c + 32 * (s >> 1) + 4 * (s & 1);
+          uint2 v = make_uint2(0, 0);
+          if (live) {
+            if constexpr (kQF32) {
+              const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qo + d);
+              v = make_uint2(bf16_pair(f.x, f.y), bf16_pair(f.z, f.w));
+            } else {
+              v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + qo + d);
+            }
+          }
+          qf[mt][s][hf] = v.x;
+          qf[mt][s][2 + hf] = v.y;
+        }
+      }
+    }
+
+    float o[MT][kTiles][4];
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+    bool bad = false;
+
+    for (int it = 0; it < seg; ++it) {
+      const int32_t next_page = page_of(it + G::kStages);
+      cp_async_wait<G::kStages - 1>();
+      __syncwarp();
+      const int tok0 = tok_first + it * kTileTokens;
+      if (tok0 < len) {
+        const uint32_t kst = ring + (it % G::kStages) * G::kStage, vst = kst + G::kSide;
+        float ks[2][2] = {}, vs[2][2] = {};
+        if constexpr (kS8) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint2 k2 = lds64(kst + 2 * G::kSide + (8 * nt + 2 * c) * 4);
+            const uint2 v2 = lds64(kst + 2 * G::kSide + 64 + (8 * nt + 2 * c) * 4);
+            ks[nt][0] = __uint_as_float(k2.x) * a.scale_log2, ks[nt][1] = __uint_as_float(k2.y) * a.scale_log2;
+            vs[nt][0] = __uint_as_float(v2.x), vs[nt][1] = __uint_as_float(v2.y);
+          }
+        }
+        // s = q k^T
+        float s[MT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < G::kPieces / 4; ++i) {
+            const uint4 kk = lds128(kst + G::k_at(8 * nt + g, 4 * i + c));
+            if constexpr (kS8) {
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                const uint32_t word = u4_get(kk, q4);
+                const uint32_t b0 = s8_low_pair(word), b1 = s8_high_pair(word);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma_bf16(s[mt][nt], qf[mt][4 * i + q4], b0, b1);
+              }
+            } else {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma_bf16(s[mt][nt], qf[mt][2 * i], kk.x, kk.y);
+                mma_bf16(s[mt][nt], qf[mt][2 * i + 1], kk.z, kk.w);
+              }
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] *= kS8 ? ks[nt][e & 1] : a.scale_log2;
+        }
+        const bool masked = tok0 + kGroup > L;   // the group holds new tokens, or ends the request
+        uint32_t seen[MT];                       // bit nt * 4 + e
+        if (masked) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            seen[mt] = 0;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = tok0 + 8 * nt + 2 * c + (e & 1), i = node[mt][e >> 1];
+                const bool v = tok < L || (tok < len && i >= 0 && attn_sees(a, rq.first, i, tok - L));
+                if (v) seen[mt] |= 1u << (nt * 4 + e);
+                else s[mt][nt][e] = -INFINITY;
+              }
+          }
+          if constexpr (!kS8) {
+            // non-finite values of new tokens: zeros in the ring
+            bool found = false;
+            for (int q16 = lane; q16 < kGroup * G::kPieces; q16 += 32) {
+              const int t = q16 / G::kPieces;
+              if (tok0 + t < L || tok0 + t >= len) continue;
+              const uint32_t at = vst + G::v_at(t, q16 % G::kPieces);
+              const uint4 v = lds128(at);
+              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              bool hit = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (bf16_nonfinite(x[e])) x[e] &= 0xFFFF0000u, hit = true;
+                if (bf16_nonfinite(x[e] >> 16)) x[e] &= 0x0000FFFFu, hit = true;
+              }
+              if (hit) sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+              found |= hit;
+            }
+            bad |= __any_sync(0xffffffffu, found);   // also orders the stores before the loads below
+            __syncwarp();
+          }
+        }
+        // running maximum and sum, and the weights as A fragments
+        uint32_t pf[MT][4], pl[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float mx = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
+                             fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(m[mt][hf], mx);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;
+            if (__any_sync(0xffffffffu, m_new > m[mt][hf])) {
+              const float f = exp2_approx(m[mt][hf] - m_use);
+              l[mt][hf] *= f;
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) o[mt][j][2 * hf] *= f, o[mt][j][2 * hf + 1] *= f;
+            }
+            m[mt][hf] = m_new;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              float p0 = exp2_approx(s[mt][nt][2 * hf] - m_use), p1 = exp2_approx(s[mt][nt][2 * hf + 1] - m_use);
+              l[mt][hf] += p0 + p1;
+              if constexpr (kS8) {
+                p0 *= vs[nt][0], p1 *= vs[nt][1];
+                if (masked) {                    // a hidden token's scale may not be a number
+                  if (!(seen[mt] >> (nt * 4 + 2 * hf) & 1)) p0 = 0.f;
+                  if (!(seen[mt] >> (nt * 4 + 2 * hf + 1) & 1)) p1 = 0.f;
+                }
+              }
+              const uint32_t hi = bf16_pair(p0, p1);
+              pf[mt][2 * nt + hf] = hi;
+              pl[mt][2 * nt + hf] = bf16_pair(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
+            }
+          }
+        }
+        // o += p v
+        if constexpr (!kS8) {
+          const int vt = (lane & 7) + (lane & 8), vp = lane >> 4;
+#pragma unroll
+          for (int j = 0; j < kTiles / 2; ++j) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_trans(vst + G::v_at(vt, 2 * j + vp), b0, b1, b2, b3);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_bf16(o[mt][2 * j], pf[mt], b0, b1);
+              mma_bf16(o[mt][2 * j + 1], pf[mt], b2, b3);
+              mma_bf16(o[mt][2 * j], pl[mt], b0, b1);
+              mma_bf16(o[mt][2 * j + 1], pl[mt], b2, b3);
+            }
+          }
+        } else {
+          // this thread's d of output tile j is (D / 8) g + j: tokens 2c, 2c+1, 2c+8, 2c+9
+          constexpr int kWords = D / 32;         // 32-bit words of its D / 8 codes of a token
+          uint32_t x[4][kWords];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int t = 2 * c + (q4 & 1) + (q4 >> 1) * 8;
+            if constexpr (kWords == 4) {
+              const uint4 v = lds128(vst + G::v_at(t, g));
+              x[q4][0] = v.x, x[q4][1] = v.y, x[q4][2] = v.z, x[q4][3] = v.w;
+            } else {
+              const uint2 v = lds64(vst + G::v_at(t, g >> 1) + (g & 1) * 8);
+              x[q4][0] = v.x, x[q4][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) {
+            const uint32_t a01 = __byte_perm(x[0][q], x[1][q], 0x5140), a23 = __byte_perm(x[0][q], x[1][q], 0x7362);
+            const uint32_t b01 = __byte_perm(x[2][q], x[3][q], 0x5140), b23 = __byte_perm(x[2][q], x[3][q], 0x7362);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t aw = e < 2 ? a01 : a23, bw = e < 2 ? b01 : b23;
+              const uint32_t b0 = (e & 1) ? s8_high_pair(aw) : s8_low_pair(aw);
+              const uint32_t b1 = (e & 1) ? s8_high_pair(bw) : s8_low_pair(bw);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma_bf16(o[mt][4 * q + e], pf[mt], b0, b1);
+                mma_bf16(o[mt][4 * q + e], pl[mt], b0, b1);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();                              // every lane is done with the stage
+      issue(it + G::kStages, next_page);
+    }
+
+    // ---- join the four warps ----
+    cp_async_wait<0>();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+        if (c == 0) {
+          s_ml[0][wid][mt * 16 + hf * 8 + g] = m[mt][hf];
+          s_ml[1][wid][mt * 16 + hf * 8 + g] = l[mt][hf];
+        }
+      }
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();                             // the ring is drained: its memory joins the outputs
+    if (bad && lane == 0) s_bad = 1;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int rr = mt * 16 + hf * 8 + g;
+        float top = s_ml[0][0][rr];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_ml[0][i][rr]);
+        const float f = m[mt][hf] == -INFINITY ? 0.f : exp2_approx(m[mt][hf] - top);
+        float* dst = joined + (wid * kRows + rr) * kPitch;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          const float x0 = o[mt][j][2 * hf] * f, x1 = o[mt][j][2 * hf + 1] * f;
+          if constexpr (kS8) {                   // columns 2c and 2c + 1 of tile j are d = (D / 8) (2c) + j, ...
+            dst[kTiles * (2 * c) + j] = x0;
+            dst[kTiles * (2 * c + 1) + j] = x1;
+          } else {
+            *reinterpret_cast<float2*>(dst + 8 * j + 2 * c) = make_float2(x0, x1);
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = seg == rq.kv_tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (kv0 > 0 ? 0 : 1);
+    constexpr int kLanes = D / 4;                // threads per row, four values each
+    for (int rr = threadIdx.x / kLanes; rr < n_rows; rr += kThreads / kLanes) {
+      const int d = (threadIdx.x % kLanes) * 4;
+      float top = s_ml[0][0][rr], sum = 0.f;
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_ml[0][i][rr]);
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float mi = s_ml[0][i][rr];
+        sum += s_ml[1][i][rr] * (mi == -INFINITY ? 0.f : exp2_approx(mi - top));
+        const float4 v = *reinterpret_cast<const float4*>(joined + (i * kRows + rr) * kPitch + d);
+        x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+      }
+      const int row = row0 + rr, i = row / a.group;
+      if (!kS8 && s_bad) {                       // what was taken out, for the rows that see it
+        const int j1 = min(len, (kv0 + seg) * kTileTokens) - L;
+        for (int j = max(0, kv0 * kTileTokens - L); j < j1; ++j) {
+          if (!attn_sees(a, rq.first, i, j)) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = cached_v(a, r, h, L + j, d + e);
+            if (!isfinite(v)) x[e] += v;
+          }
+        }
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
+        __nv_bfloat16* out = a.out + (int64_t)(rq.first + i) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
+        *reinterpret_cast<uint2*>(out + d) =
+            make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot * kRows + rr) * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+        if (d == 0) a.part_ml[slot * kRows + rr] = make_float2(top, sum);
+      }
+    }
+    if (!whole && kv0 == 0)
+      owned = make_int4(r, item, (int)(attn_block_of(w, u + rq.kv_tiles - 1) - blockIdx.x) + 1, 0);
+    __syncthreads();                             // the buffer is the next item's ring
+    u += seg;
+    off += seg;
+  }
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = owned;
+}
+
+// Joins the pieces of an item that several blocks computed: piece 0 is the
+// owner block's slot 1, the others the following blocks' slot 0.  One block
+// per (owner, four or eight rows), a thread per four values of a row.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 own = a.desc[blockIdx.x];
+  if (own.z == 0) return;
+  constexpr int kLanes = D / 4;
+  const int r = own.x, first = a.cu[r], n = a.cu[r + 1] - first;
+  const int row_tiles = (n * a.group + rows_per_tile - 1) / rows_per_tile;
+  const int h = own.y / row_tiles, row0 = (own.y % row_tiles) * rows_per_tile;
+  const int rr = blockIdx.y * (kThreads / kLanes) + threadIdx.x / kLanes, row = row0 + rr;
+  if (rr >= rows_per_tile || row >= n * a.group) return;
+  const int d = (threadIdx.x % kLanes) * 4;
+  const int64_t b = blockIdx.x;
+  auto at = [&](int p) { return (p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
+  float top = -INFINITY;
+  for (int p = 0; p < own.z; ++p) top = fmaxf(top, a.part_ml[at(p)].x);
+  float x[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < own.z; ++p) {
+    const float2 ml = a.part_ml[at(p)];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + d);
+    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
+    sum += ml.y * f;
+    x[0] += v.x * f, x[1] += v.y * f, x[2] += v.z * f, x[3] += v.w * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = row / a.group;
+  __nv_bfloat16* out = a.out + (int64_t)(first + i) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
+  *reinterpret_cast<uint2*>(out + d) = make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
+}
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : 32; }
+
+template <int D, bool kS8, bool kQF32, int MT>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+  constexpr int kJoin = kWarps * 16 * MT * (D + 8) * 4;
+  constexpr int kSmem = 128 + std::max(kWarps * Geo<D, kS8>::kRing, kJoin);
+  auto kern = attn_rows_kernel<D, kS8, kQF32, MT>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (err != cudaSuccess) return err;
+  if ((err = launch_pdl(kern, dim3(a.grid), dim3(kThreads), kSmem, stream, a)) != cudaSuccess) return err;
+  constexpr int kRowsPerBlock = kThreads / (D / 4);
+  return launch_pdl(attn_combine_kernel<D>, dim3(a.grid, 16 * MT / kRowsPerBlock), dim3(kThreads), 0, stream, a,
+                    16 * MT);
+}
+
+template <int D, bool kS8>
+cudaError_t launch_typed(const AttnArgs& a, bool q_f32, cudaStream_t stream) {
+  const bool one = rows_per_tile((int64_t)a.max_new * a.group) == 16;
+  if (q_f32) return one ? launch_rows<D, kS8, true, 1>(a, stream) : launch_rows<D, kS8, true, 2>(a, stream);
+  return one ? launch_rows<D, kS8, false, 1>(a, stream) : launch_rows<D, kS8, false, 2>(a, stream);
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int64_t rows, int head_dim) {
+  const size_t slots = 2 * (size_t)(kBlocksPerSm * sm_count()), t = rows_per_tile(rows);
+  return slots * t * (head_dim * sizeof(float) + sizeof(float2)) + slots / 2 * sizeof(int4);
+}
+
+void attn_carve(AttnArgs& a, int64_t rows, int head_dim, void* workspace) {
+  a.grid = kBlocksPerSm * sm_count();
+  const size_t slots = 2 * (size_t)a.grid, t = rows_per_tile(rows);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * t * head_dim);
+  a.desc = reinterpret_cast<int4*>(a.part_ml + slots * t);
+}
+
+cudaError_t launch_attn(const AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, cudaStream_t stream) {
+  if (head_dim == 128)
+    return cache_s8 ? launch_typed<128, true>(a, q_f32, stream) : launch_typed<128, false>(a, q_f32, stream);
+  return cache_s8 ? launch_typed<64, true>(a, q_f32, stream) : launch_typed<64, false>(a, q_f32, stream);
+}
+
+}  // namespace qmm

@@ -44,11 +44,12 @@ const char* qmm_status_string(qmm_status s) {
     case QMM_ERR_BAD_EXPERT_ID: return "QMM_ERR_BAD_EXPERT_ID";
     case QMM_ERR_WORKSPACE: return "QMM_ERR_WORKSPACE";
     case QMM_ERR_RANGE: return "QMM_ERR_RANGE";
+    case QMM_ERR_NO_PAGES: return "QMM_ERR_NO_PAGES";
   }
   return "QMM_ERR_UNKNOWN";
 }
 
-int qmm_version(void) { return 200; }
+int qmm_version(void) { return 300; }
 
 // ---------------------------------------------------------------------------
 // int8

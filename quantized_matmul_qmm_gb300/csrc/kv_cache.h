@@ -1,0 +1,88 @@
+// Host-side declarations of the paged key/value cache: the plan of a step, the
+// append of its rows and the attention that reads them.
+#pragma once
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+// ---- plan (kv_plan.cu) ----
+constexpr int64_t kPlanMaxRequests = 16384;   // three int32 per request fit one block's shared memory
+struct KvPlanArgs {
+  const int32_t* ctx;        // [R]
+  const int32_t* fresh;      // [R] new tokens of each request
+  int R;
+  const int32_t* free_pages; // [n_free]
+  int64_t n_free;
+  int32_t* table;            // [R][ld_table]
+  int64_t ld_table;
+  int64_t max_blocks;
+  uint32_t page_size;
+  const int32_t* parents;    // [max_tokens] or null
+  int max_tokens;
+  int32_t* cu;               // [R + 1]
+  int64_t* slots;            // [max_tokens]
+  int32_t* positions;        // [max_tokens]
+  uint32_t* mask;            // [max_tokens][ld_mask], with parents
+  int64_t ld_mask;
+  int mask_words;
+  int32_t* taken;            // [1]
+  int32_t* dev_status;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
+
+// ---- the cache as the kernels see it (strides in bytes) ----
+struct KvView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;            // int8 cache: [n_pages][n_heads][page_size]
+  float* v_scale;
+  int64_t st_page, st_token, st_head;
+  int64_t n_pages;
+  uint32_t page_size;
+  int n_heads;
+};
+
+// ---- append (kv_append.cu) ----
+struct KvAppendArgs {
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_st, k_sh, v_st, v_sh;   // bytes
+  int T;
+  const int64_t* slots;
+  KvView cache;
+  int32_t* dev_status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool rows_bf16, bool cache_s8, int head_dim,
+                             cudaStream_t stream);
+
+// ---- tree attention (attn_rows.cu) ----
+struct AttnArgs {
+  const void* q;
+  int64_t q_st, q_sh;        // elements
+  KvView cache;
+  const int32_t* table;      // [R][ld_table]
+  int64_t ld_table;
+  int64_t max_blocks;
+  const int32_t* ctx;        // [R]
+  const int32_t* cu;         // [R + 1]
+  int R, T, max_new;
+  int n_q_heads, group;      // query heads, and query heads per key head
+  const uint32_t* mask;      // [T][ld_mask] or null (causal)
+  int64_t ld_mask;
+  float scale_log2;          // softmax scale * log2(e)
+  __nv_bfloat16* out;
+  int64_t o_st, o_sh;        // elements
+  float* part_o;             // workspace: [2 * grid][rows][head_dim]
+  float2* part_ml;           // workspace: [2 * grid][rows]: running maximum (log2 domain) and sum
+  int4* desc;                // workspace: [grid]: request, head and row tile, segments, unused
+  int grid;
+  int32_t* dev_status;
+};
+// Workspace bytes of a call whose requests have up to `rows` query rows per key head.
+size_t attn_workspace_bytes(int64_t rows, int head_dim);
+// Fills the workspace pointers and the grid of `a` from `workspace`.
+void attn_carve(AttnArgs& a, int64_t rows, int head_dim, void* workspace);
+cudaError_t launch_attn(const AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, cudaStream_t stream);
+
+}  // namespace qmm

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libqmm.so")
 
 QMM_OK, QMM_ERR_INVALID_ARG, QMM_ERR_UNSUPPORTED, QMM_ERR_OVERFLOW_BOUND = 0, 1, 2, 3
 QMM_ERR_CUDA, QMM_ERR_TIMEOUT, QMM_ERR_BAD_EXPERT_ID, QMM_ERR_WORKSPACE, QMM_ERR_RANGE = 4, 5, 6, 7, 8
+QMM_ERR_NO_PAGES = 9
 QMM_U8, QMM_S8, QMM_S32, QMM_F32, QMM_BF16 = 1, 2, 3, 4, 5
 DTYPES = {"u8": QMM_U8, "s8": QMM_S8, "s32": QMM_S32, "f32": QMM_F32, "bf16": QMM_BF16}
 TORCH_OUT = {"s32": torch.int32, "f32": torch.float32, "s8": torch.int8, "u8": torch.uint8}
@@ -41,6 +42,12 @@ class QmmInt8Problem(ctypes.Structure):
 
 class QmmQ4GemvProblem(ctypes.Structure):
     _fields_ = [("tiles", _vp), ("N", _i64), ("K", _i64), ("x", _vp), ("y", _vp)]
+
+
+class QmmKvCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("type", _c.c_int), ("n_pages", _i64),
+                ("page_size", _i64), ("n_heads", _i64), ("head_dim", _i64), ("stride_page", _i64),
+                ("stride_token", _i64), ("stride_head", _i64)]
 
 
 SIGNATURES = {
@@ -84,6 +91,14 @@ SIGNATURES = {
     "qmm_pack_q8": (_c.c_int, [_vp, _i64, _i64, _i64, _c.c_int, _vp, _sz, _vp]),
     "qmm_q8_gemm_workspace_size": (_c.c_int, [_i64, _i64, _i64, _szp]),
     "qmm_q8_gemm": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _sz, _vp, _vp]),
+    "qmm_kv_plan": (_c.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                               _vp, _vp, _vp, _vp]),
+    "qmm_kv_append": (_c.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _c.c_int, _i64, _vp, _c.POINTER(QmmKvCache), _vp,
+                                 _vp]),
+    "qmm_tree_attention_workspace_size": (_c.c_int, [_i64, _i64, _i64, _i64, _szp]),
+    "qmm_tree_attention": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.POINTER(QmmKvCache), _vp, _i64, _i64, _vp,
+                                      _vp, _i64, _i64, _i64, _vp, _i64, _c.c_float, _vp, _i64, _i64, _vp, _sz, _vp,
+                                      _vp]),
     "qmm_probe_hbm_read": (_c.c_int, [_vp, _sz, _c.c_int, _vp, _vp, _vp]),
     "qmm_selftest_wait_timeout": (_c.c_int, [_c.c_uint64, _vp, _vp, _vp]),
 }
@@ -474,6 +489,104 @@ def q8_gemm(tiles: torch.Tensor, layout: int, N: int, K: int, X: torch.Tensor, Y
         _ptr(tiles), int(layout), N, K, _ptr(X), M, X.stride(0), _ptr(Y), Y.stride(0), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream()))
     return Y
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache and tree attention
+# ---------------------------------------------------------------------------
+
+_KV_TYPES = {torch.bfloat16: QMM_BF16, torch.int8: QMM_S8}
+_ROW_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> QmmKvCache:
+    n_pages, page_size, n_heads, head_dim = k_cache.shape
+    sp, st, sh, sd = strides = k_cache.stride()
+    if v_cache.shape != k_cache.shape or v_cache.stride() != strides or v_cache.dtype != k_cache.dtype or sd != 1:
+        raise ValueError("k_cache and v_cache must have one shape, type and strides, with contiguous heads")
+    if k_cache.dtype == torch.int8:
+        for sc in (k_scale, v_scale):
+            if sc is None or sc.dtype != torch.float32 or sc.shape != (n_pages, n_heads, page_size) \
+                    or not sc.is_contiguous():
+                raise ValueError("an int8 cache needs contiguous fp32 scales [pages][heads][page_size]")
+    return QmmKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                      _KV_TYPES[k_cache.dtype], n_pages, page_size, n_heads, head_dim, sp, st, sh)
+
+
+def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+            page_size: int, slots: torch.Tensor, positions: torch.Tensor, cu_new=None, pages_taken=None, parents=None,
+            mask=None, dev_status=None):
+    """Pages, slots, positions and tree masks of a step through qmm_kv_plan.
+    block_table int32 [R][max_blocks] is updated in place; slots int64 and
+    positions int32 [max_tokens] are written, and with parents (int32
+    [max_tokens]) the mask int32 [max_tokens][words].  Returns (cu_new int32
+    [R+1], pages_taken int32 [1])."""
+    R, T = ctx_lens.shape[0], slots.shape[0]
+    if cu_new is None:
+        cu_new = torch.empty(R + 1, dtype=torch.int32, device=ctx_lens.device)
+    if pages_taken is None:
+        pages_taken = torch.empty(1, dtype=torch.int32, device=ctx_lens.device)
+    if new_lens.shape[0] != R or block_table.shape[0] != R or positions.shape[0] != T or cu_new.shape[0] != R + 1 \
+            or (parents is not None and parents.shape[0] != T) or (mask is not None and mask.shape[0] != T):
+        raise ValueError("kv_plan: shapes do not agree")
+    ld_mask, words = (0, 0) if mask is None else (mask.stride(0), mask.shape[1])
+    _check("qmm_kv_plan", lib.qmm_kv_plan(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.shape[0],
+        block_table.data_ptr(), block_table.stride(0), block_table.shape[1], page_size, _addr(parents), _addr(mask),
+        ld_mask, words, T, cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), pages_taken.data_ptr(),
+        _addr(dev_status), _stream()))
+    return cu_new, pages_taken
+
+
+def kv_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              k_scale=None, v_scale=None, dev_status=None):
+    """Store the rows K, V (fp32 or bf16 [T][heads][head_dim]) at slots (int64
+    [T], -1 skips) of a cache [pages][page_size][heads][head_dim], bf16 or int8
+    with scales fp32 [pages][heads][page_size], through qmm_kv_append."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    (kt, kh, kd), (vt, vh, vd) = K.stride(), V.stride()
+    if V.shape != K.shape or V.dtype != K.dtype or kd != 1 or vd != 1 or K.shape[0] != slots.shape[0] \
+            or K.shape[1:] != k_cache.shape[2:]:
+        raise ValueError("kv_append: K, V, slots and the cache do not agree")
+    _check("qmm_kv_append", lib.qmm_kv_append(
+        K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, _ROW_TYPES[K.dtype], K.shape[0], slots.data_ptr(),
+        ctypes.byref(cache), _addr(dev_status), _stream()))
+
+
+def tree_attention_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
+    return _size("qmm_tree_attention_workspace_size", n_q_heads, n_kv_heads, head_dim, max_new)
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                   ctx_lens: torch.Tensor, cu_new: torch.Tensor, max_new: int, mask=None, scale=None, k_scale=None,
+                   v_scale=None, out=None, workspace=None, dev_status=None):
+    """Attention of a step's tokens q (fp32 or bf16 [T][q heads][head_dim]) over
+    the paged cache through qmm_tree_attention; mask int32 [T][words] (kv_plan's)
+    or None for causal chunks and plain decoding; scale 1 / sqrt(head_dim) by
+    default.  Returns out, bf16 [T][q heads][head_dim]."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    T, heads, head_dim = q.shape
+    if out is None:
+        out = torch.empty((T, heads, head_dim), dtype=torch.bfloat16, device=q.device)
+    (qt, qh, qd), (ot, oh, od) = q.stride(), out.stride()
+    if head_dim != k_cache.shape[3] or out.shape != q.shape or out.dtype != torch.bfloat16 or qd != 1 or od != 1 \
+            or cu_new.shape[0] != ctx_lens.shape[0] + 1 or block_table.shape[0] != ctx_lens.shape[0] \
+            or (mask is not None and mask.shape[0] != T):
+        raise ValueError("tree_attention: shapes do not agree")
+    if workspace is None:
+        workspace = torch.empty(tree_attention_workspace_size(heads, k_cache.shape[2], head_dim, max_new),
+                                dtype=torch.uint8, device=q.device)
+    _check("qmm_tree_attention", lib.qmm_tree_attention(
+        q.data_ptr(), _ROW_TYPES[q.dtype], qt, qh, heads, ctypes.byref(cache), block_table.data_ptr(),
+        block_table.stride(0), block_table.shape[1], ctx_lens.data_ptr(), cu_new.data_ptr(), ctx_lens.shape[0], T,
+        max_new, _addr(mask), 0 if mask is None else mask.stride(0),
+        head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _addr(dev_status), _stream()))
+    return out
 
 
 # ---------------------------------------------------------------------------
