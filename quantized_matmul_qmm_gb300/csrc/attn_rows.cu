@@ -47,6 +47,8 @@ constexpr int kGroup = 16;                       // cached tokens per warp step
 constexpr int kTileTokens = kGroup * kWarps;     // a unit
 constexpr int kBlocksPerSm = 2;
 constexpr int kRingBytes = 24576;                // per warp
+// More query rows per key head than this go to the tile kernel (attn_tiles.cu).
+constexpr int64_t kRowsKernelMax = 32;
 
 template <int D, bool kS8>
 struct Geo {
@@ -71,18 +73,6 @@ struct Geo {
   }
 };
 
-QMM_DEV float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-QMM_DEV uint32_t bf16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 QMM_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -100,29 +90,6 @@ QMM_DEV uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
-}
-
-// Two int8 codes in the low bytes of 16-bit lanes -> bf16x2, exactly: the low
-// seven bits on top of 128, and -128 or (sign bit) -256 added.
-QMM_DEV uint32_t s8_lanes_to_bf16(uint32_t x) {
-  uint32_t lo, hi, r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(x), "r"(0x007F007Fu), "r"(0x43004300u));
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(x), "r"(0x00800080u), "r"(0xC300C300u));
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-QMM_DEV uint32_t s8_low_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4140)); }
-QMM_DEV uint32_t s8_high_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4342)); }
-
-QMM_DEV bool bf16_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
-
-// One element of the cache's value rows.
-QMM_DEV float cached_v(const AttnArgs& a, int r, int h, int tok, int d) {
-  const int32_t page = a.table[(int64_t)r * a.ld_table + tok / a.cache.page_size];
-  const int64_t off = attn_row_offset(a, page, tok);
-  if (off < 0) return 0.f;
-  const uint8_t* p = a.cache.v + h * a.cache.st_head + off + 2 * d;
-  return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
 template <int D, bool kS8, bool kQF32, int MT>
@@ -151,23 +118,17 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
     return;
   }
   int4 owned = make_int4(0, 0, 0, 0);            // the item that this block begins and another ends
-
-  int r = w.r;
-  int64_t off = w.off, u = w.u0;
-  AttnReq rq = attn_req(a, r, kRows, kTileTokens);
-  while (u < w.u1) {
-    while (off >= rq.units) {                    // to the next request that has work
-      off -= rq.units;
-      rq = attn_req(a, ++r, kRows, kTileTokens);
-    }
-    const int item = (int)(off / rq.kv_tiles), kv0 = (int)(off % rq.kv_tiles);
-    const int h = item / rq.row_tiles, row0 = (item % rq.row_tiles) * kRows;
-    const int seg = (int)min((int64_t)(rq.kv_tiles - kv0), w.u1 - u);
-    const int L = rq.L, len = rq.L + rq.n, n_rows = min(kRows, rq.n * a.group - row0);
+  AttnWalk walk;
+  walk.start(a, w, kRows, kTileTokens);
+  AttnItem im;
+  while (walk.next(a, kRows, kTileTokens, im)) {
+    const AttnReq& rq = im.q;
+    const int h = im.h, row0 = im.row0, kv0 = im.kv0, seg = im.seg, L = rq.L, len = im.len, n_rows = im.n_rows;
+    if (im.pieces > 0) owned = make_int4(im.r, im.id, im.pieces, 0);
     const int tok_first = kv0 * kTileTokens + wid * kGroup;
 
     // ---- the ring ----
-    const int32_t* trow = a.table + (int64_t)r * a.ld_table;
+    const int32_t* trow = a.table + (int64_t)im.r * a.ld_table;
     const uint8_t* kbase = a.cache.k + h * a.cache.st_head;
     const uint8_t* vbase = a.cache.v + h * a.cache.st_head;
     auto page_of = [&](int it) -> int32_t {      // of this lane's token of step it, -1 past the end
@@ -223,7 +184,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
         const bool live = rr < n_rows;
         const int row = row0 + rr, i = row / a.group;
         node[mt][hf] = live ? i : -1;
-        const int64_t qo = (int64_t)(rq.first + i) * a.q_st + (int64_t)(h * a.group + row % a.group) * a.q_sh;
+        const int64_t qo = attn_q_row(a, rq, h, row);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           const int d = kS8 ? 16 * c + 64 * (s >> 2) + 4 * (s & 3) : 8 * c + 32 * (s >> 1) + 4 * (s & 1);
@@ -327,15 +288,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
               const int t = q16 / G::kPieces;
               if (tok0 + t < L || tok0 + t >= len) continue;
               const uint32_t at = vst + G::v_at(t, q16 % G::kPieces);
-              const uint4 v = lds128(at);
-              uint32_t x[4] = {v.x, v.y, v.z, v.w};
-              bool hit = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (bf16_nonfinite(x[e])) x[e] &= 0xFFFF0000u, hit = true;
-                if (bf16_nonfinite(x[e] >> 16)) x[e] &= 0x0000FFFFu, hit = true;
-              }
-              if (hit) sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+              uint4 v = lds128(at);
+              const bool hit = bf16_drop_nonfinite(v);
+              if (hit) sts128(at, v);
               found |= hit;
             }
             bad |= __any_sync(0xffffffffu, found);   // also orders the stores before the loads below
@@ -468,7 +423,6 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     __syncthreads();
-    const bool whole = seg == rq.kv_tiles;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (kv0 > 0 ? 0 : 1);
     constexpr int kLanes = D / 4;                // threads per row, four values each
     for (int rr = threadIdx.x / kLanes; rr < n_rows; rr += kThreads / kLanes) {
@@ -484,40 +438,25 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
         const float4 v = *reinterpret_cast<const float4*>(joined + (i * kRows + rr) * kPitch + d);
         x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
       }
-      const int row = row0 + rr, i = row / a.group;
-      if (!kS8 && s_bad) {                       // what was taken out, for the rows that see it
-        const int j1 = min(len, (kv0 + seg) * kTileTokens) - L;
-        for (int j = max(0, kv0 * kTileTokens - L); j < j1; ++j) {
-          if (!attn_sees(a, rq.first, i, j)) continue;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = cached_v(a, r, h, L + j, d + e);
-            if (!isfinite(v)) x[e] += v;
-          }
-        }
-      }
-      if (whole) {
+      if (!kS8 && s_bad) attn_add_nonfinite(a, im, kTileTokens, (row0 + rr) / a.group, d, x);
+      if (im.whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
-        __nv_bfloat16* out = a.out + (int64_t)(rq.first + i) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
-        *reinterpret_cast<uint2*>(out + d) =
+        *reinterpret_cast<uint2*>(attn_out_row(a, rq, h, row0 + rr) + d) =
             make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot * kRows + rr) * D + d) = make_float4(x[0], x[1], x[2], x[3]);
         if (d == 0) a.part_ml[slot * kRows + rr] = make_float2(top, sum);
       }
     }
-    if (!whole && kv0 == 0)
-      owned = make_int4(r, item, (int)(attn_block_of(w, u + rq.kv_tiles - 1) - blockIdx.x) + 1, 0);
     __syncthreads();                             // the buffer is the next item's ring
-    u += seg;
-    off += seg;
   }
   if (threadIdx.x == 0) a.desc[blockIdx.x] = owned;
 }
 
 // Joins the pieces of an item that several blocks computed: piece 0 is the
 // owner block's slot 1, the others the following blocks' slot 0.  One block
-// per (owner, four or eight rows), a thread per four values of a row.
+// per (owner, 16 rows), a thread per four values of a row.
+constexpr int kCombineRows = 16;
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
@@ -526,38 +465,35 @@ attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
   const int4 own = a.desc[blockIdx.x];
   if (own.z == 0) return;
   constexpr int kLanes = D / 4;
-  const int r = own.x, first = a.cu[r], n = a.cu[r + 1] - first;
-  const int row_tiles = (n * a.group + rows_per_tile - 1) / rows_per_tile;
+  AttnReq q{};
+  q.first = a.cu[own.x];
+  q.n = a.cu[own.x + 1] - q.first;
+  const int row_tiles = (q.n * a.group + rows_per_tile - 1) / rows_per_tile;
   const int h = own.y / row_tiles, row0 = (own.y % row_tiles) * rows_per_tile;
-  const int rr = blockIdx.y * (kThreads / kLanes) + threadIdx.x / kLanes, row = row0 + rr;
-  if (rr >= rows_per_tile || row >= n * a.group) return;
+  const int n_rows = min(rows_per_tile, q.n * a.group - row0);
   const int d = (threadIdx.x % kLanes) * 4;
   const int64_t b = blockIdx.x;
-  auto at = [&](int p) { return (p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
-  float top = -INFINITY;
-  for (int p = 0; p < own.z; ++p) top = fmaxf(top, a.part_ml[at(p)].x);
-  float x[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  const int r1 = min(n_rows, (int)(blockIdx.y + 1) * kCombineRows);
+  for (int rr = blockIdx.y * kCombineRows + threadIdx.x / kLanes; rr < r1; rr += kThreads / kLanes) {
+    auto at = [&](int p) { return (p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
+    float top = -INFINITY;
 #pragma unroll 4
-  for (int p = 0; p < own.z; ++p) {
-    const float2 ml = a.part_ml[at(p)];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + d);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
-    sum += ml.y * f;
-    x[0] += v.x * f, x[1] += v.y * f, x[2] += v.z * f, x[3] += v.w * f;
+    for (int p = 0; p < own.z; ++p) top = fmaxf(top, a.part_ml[at(p)].x);
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < own.z; ++p) {
+      const float2 ml = a.part_ml[at(p)];
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + d);
+      // a piece without a maximum has no weight, unless its scores were not numbers
+      const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
+      sum += ml.y * f;
+      x[0] += v.x * f, x[1] += v.y * f, x[2] += v.z * f, x[3] += v.w * f;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(attn_out_row(a, q, h, row0 + rr) + d) =
+        make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = row / a.group;
-  __nv_bfloat16* out = a.out + (int64_t)(first + i) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
-  *reinterpret_cast<uint2*>(out + d) = make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
 }
-
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
-int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : 32; }
 
 template <int D, bool kS8, bool kQF32, int MT>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
@@ -566,38 +502,77 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   auto kern = attn_rows_kernel<D, kS8, kQF32, MT>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
-  if ((err = launch_pdl(kern, dim3(a.grid), dim3(kThreads), kSmem, stream, a)) != cudaSuccess) return err;
-  constexpr int kRowsPerBlock = kThreads / (D / 4);
-  return launch_pdl(attn_combine_kernel<D>, dim3(a.grid, 16 * MT / kRowsPerBlock), dim3(kThreads), 0, stream, a,
-                    16 * MT);
+  return launch_pdl(kern, dim3(a.grid), dim3(kThreads), kSmem, stream, a);
 }
 
 template <int D, bool kS8>
-cudaError_t launch_typed(const AttnArgs& a, bool q_f32, cudaStream_t stream) {
-  const bool one = rows_per_tile((int64_t)a.max_new * a.group) == 16;
+cudaError_t launch_typed(const AttnArgs& a, int rows_per_tile, bool q_f32, cudaStream_t stream) {
+  const bool one = rows_per_tile == 16;
   if (q_f32) return one ? launch_rows<D, kS8, true, 1>(a, stream) : launch_rows<D, kS8, true, 2>(a, stream);
   return one ? launch_rows<D, kS8, false, 1>(a, stream) : launch_rows<D, kS8, false, 2>(a, stream);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int64_t rows, int head_dim) {
-  const size_t slots = 2 * (size_t)(kBlocksPerSm * sm_count()), t = rows_per_tile(rows);
-  return slots * t * (head_dim * sizeof(float) + sizeof(float2)) + slots / 2 * sizeof(int4);
-}
-
-void attn_carve(AttnArgs& a, int64_t rows, int head_dim, void* workspace) {
-  a.grid = kBlocksPerSm * sm_count();
-  const size_t slots = 2 * (size_t)a.grid, t = rows_per_tile(rows);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * t * head_dim);
-  a.desc = reinterpret_cast<int4*>(a.part_ml + slots * t);
-}
-
-cudaError_t launch_attn(const AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, cudaStream_t stream) {
+cudaError_t launch_attn_rows(const AttnArgs& a, int rows_per_tile, bool q_f32, bool cache_s8, int head_dim,
+                             cudaStream_t stream) {
   if (head_dim == 128)
-    return cache_s8 ? launch_typed<128, true>(a, q_f32, stream) : launch_typed<128, false>(a, q_f32, stream);
-  return cache_s8 ? launch_typed<64, true>(a, q_f32, stream) : launch_typed<64, false>(a, q_f32, stream);
+    return cache_s8 ? launch_typed<128, true>(a, rows_per_tile, q_f32, stream)
+                    : launch_typed<128, false>(a, rows_per_tile, q_f32, stream);
+  return cache_s8 ? launch_typed<64, true>(a, rows_per_tile, q_f32, stream)
+                  : launch_typed<64, false>(a, rows_per_tile, q_f32, stream);
+}
+
+cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_tile, int head_dim, cudaStream_t stream) {
+  const dim3 grid(a.grid, (rows_per_tile + kCombineRows - 1) / kCombineRows);
+  return head_dim == 128 ? launch_pdl(attn_combine_kernel<128>, grid, dim3(kThreads), 0, stream, a, rows_per_tile)
+                         : launch_pdl(attn_combine_kernel<64>, grid, dim3(kThreads), 0, stream, a, rows_per_tile);
+}
+
+// ---- the choice of a kernel, shared by the size query and the call ----
+
+int attn_sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+bool attn_pages_tile(const KvView& c, bool s8) {
+  // TMA boxes of whole 8-row groups inside a page, strides that a tensor map
+  // holds, and bulk copies of 16-byte aligned scales
+  constexpr int64_t kMaxStride = (int64_t)1 << 40;
+  return c.page_size % 8 == 0 && c.st_page < kMaxStride && c.st_token < kMaxStride && c.st_head < kMaxStride &&
+         (!s8 || (aligned(c.k_scale, 16) && aligned(c.v_scale, 16)));
+}
+
+AttnPlan attn_plan(int64_t rows, bool pages_tile) {
+  const int sms = attn_sm_count();
+  if (rows > kRowsKernelMax && pages_tile) return {true, rows <= 128 ? 128 : 256, sms};
+  return {false, rows <= 16 ? 16 : 32, kBlocksPerSm * sms};
+}
+
+namespace {
+size_t plan_bytes(const AttnPlan& p, int head_dim) {
+  return 2 * (size_t)p.grid * p.rows_per_tile * (head_dim * sizeof(float) + sizeof(float2)) +
+         (size_t)p.grid * sizeof(int4);
+}
+}  // namespace
+
+size_t attn_workspace_bytes(int64_t rows, int head_dim) {
+  return std::max(plan_bytes(attn_plan(rows, true), head_dim), plan_bytes(attn_plan(rows, false), head_dim));
+}
+
+cudaError_t launch_attn(AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, void* workspace, cudaStream_t stream) {
+  const AttnPlan p = attn_plan((int64_t)a.max_new * a.group, attn_pages_tile(a.cache, cache_s8));
+  a.grid = p.grid;
+  const size_t rows = 2 * (size_t)p.grid * p.rows_per_tile;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * head_dim);
+  a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
+  const cudaError_t err = p.tiles ? launch_attn_tiles(a, p.rows_per_tile, q_f32, cache_s8, head_dim, stream)
+                                  : launch_attn_rows(a, p.rows_per_tile, q_f32, cache_s8, head_dim, stream);
+  if (err != cudaSuccess) return err;
+  return launch_attn_combine(a, p.rows_per_tile, head_dim, stream);
 }
 
 }  // namespace qmm

@@ -1,0 +1,764 @@
+// Tree attention for many query rows per key head, on the tcgen05 tensor cores.
+//
+// An item is up to 128 (kRT = 1) or 256 (kRT = 2) query rows of one key head;
+// cached tokens come in tiles of 128.  Per tile of 128 rows x 128 tokens:
+//   S = Q K^T   into TMEM (128 columns of fp32), Q and K in shared memory;
+//   p = exp2(c s - c m) by four warps, one row per thread, m a running
+//       reference that follows the row's maximum;
+//   O += P V    with P (bf16) over S's columns in TMEM as the A operand and V
+//       as it lies in memory (MN-major B operand).
+// Two streams of S / P / O fill TMEM's 512 columns, so that one stream's
+// exponentials run under the other's products: with kRT = 1 they take the
+// even and the odd cached tiles of the same rows (joined when the item ends),
+// with kRT = 2 the two halves of 256 rows, and each cached tile is fetched
+// once for both.  All products of a block are issued by one thread, in the
+// order S(i + 2), PV(i) of a stream: the tensor pipe runs them in order, so
+// S(i + 2) may overwrite the columns of P(i) behind PV(i), and when S(i + 2)
+// is there, O holds all of PV(i).
+//
+// Up to 64 rows the tile's other 64 lanes hold the same rows again, and their P
+// the part of each weight that the first bf16 rounding left over: the padded
+// products then give the weights 16 bits for nothing (see attn_rows.cu).
+//
+// The reference m moves only when a tile's maximum passes it by 2^8 in the
+// weights, so that O is rarely rescaled (it is in TMEM, not in registers).
+//
+// Warps: 0 loads (TMA boxes of page_size's power of two; the pages of a tile
+// looked up by one lane each), 1 issues the products, 2 and 3 clean the
+// value tiles that hold the step's own tokens (zeros past the request's end
+// and for non-finite values, see attn_rows.cu), 4..11 are the two streams'
+// rows.  An int8 cache has four more: tiles arrive as codes and are written
+// out as bf16 in the products' layout; a token's key scale multiplies its
+// column of s, its value scale the weight.
+//
+// What bounds it: 4 * 128 operations per row and token against 512 (bf16) or
+// 264 (int8) bytes per token: the cache's bytes up to about 128 rows, the
+// tensor pipe and the exponentials above.
+#include <algorithm>
+
+#include "attn_work.cuh"
+#include "umma.cuh"
+
+namespace qmm {
+namespace {
+
+using namespace umma;
+
+constexpr int kTok = 128;                        // cached tokens per tile
+constexpr int kHalf = 128 * 128;                 // bytes of 128 rows x 64 bf16
+constexpr int kScaleRing = 4;
+
+template <int D, bool kS8, int kRT>
+struct Tg {
+  static constexpr int kNH = D / 64;             // 64-column halves of a row
+  static constexpr int kTile = kNH * kHalf;      // bytes of a bf16 tile
+  static constexpr int kRaw = kTok * D;          // bytes of a tile of codes
+  static constexpr int kSlots = D == 64 ? (kS8 ? 6 : 8) : kS8 ? 3 : (kRT == 1 ? 6 : 5);
+  static constexpr int kRawSlots = !kS8 ? 0 : D == 64 ? 8 : (kRT == 1 ? 5 : 3);
+  static constexpr int kThreads = kS8 ? 512 : 384;
+  static constexpr int kOffSlots = kRT * kTile;
+  static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
+  static constexpr int kOffScale = kOffRaw + kRawSlots * kRaw;
+  static constexpr int kBytes = kOffScale + (kS8 ? kScaleRing * 2 * kTok * 4 : 0);
+  static constexpr int kAhead = kRT == 1 ? 2 : 1;   // key tiles fetched ahead of the value tiles
+};
+
+struct TBars {
+  uint64_t full[8], empty[8];        // bf16 tiles
+  uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full, o_free, sync;
+  uint64_t done;
+};
+
+struct TShared {
+  TBars bar;
+  AttnFindScratch find;
+  float m[2][128], l[2][128];
+  int bad[16];                       // per item, by its number: a non-finite value was taken out
+  uint32_t tmem;
+  int abort;
+};
+
+constexpr int kColS = 0, kColO = 256;            // stream st: + 128 * st
+
+struct Ctx {
+  const AttnArgs& a;
+  TShared* sh;
+  uint8_t* smem;
+  uint32_t tmem;
+  AttnWork w;
+  uint32_t box;                                  // tokens of a TMA box
+  QMM_DEV bool wait(uint64_t* bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, &sh->abort, a.dev_status);
+  }
+  QMM_DEV bool wait_all(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  }
+};
+
+// Calls f(is_value, tile, page-lookup tile) in the order in which tiles are fetched and used.
+template <int kAhead, typename F>
+QMM_DEV bool tile_order(int seg, F f) {
+  for (int i = 0; i < min(kAhead, seg); ++i)
+    if (!f(false, i)) return false;
+  for (int i = 0; i < seg; ++i) {
+    if (!f(true, i)) return false;
+    if (i + kAhead < seg && !f(false, i + kAhead)) return false;
+  }
+  return true;
+}
+
+// ---- warp 0: tiles into shared memory ----
+template <int D, bool kS8, int kRT>
+QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& mv) {
+  using G = Tg<D, kS8, kRT>;
+  const AttnArgs& a = x.a;
+  const int lane = threadIdx.x & 31;
+  constexpr int kN = kS8 ? G::kRawSlots : G::kSlots;
+  uint64_t* full = kS8 ? x.sh->bar.raw_full : x.sh->bar.full;
+  uint64_t* empty = kS8 ? x.sh->bar.raw_empty : x.sh->bar.empty;
+  const uint32_t base = smem_u32(x.smem) + (kS8 ? G::kOffRaw : G::kOffSlots);
+  const uint32_t P = a.cache.page_size;
+  uint32_t n = 0, m = 0;                         // tiles fetched; key tiles fetched
+  if (lane == 0) {
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
+  AttnWalk walk;
+  walk.start(a, x.w, 128 * kRT, kTok);
+  AttnItem it;
+  while (walk.next(a, 128 * kRT, kTok, it)) {
+    const int32_t* trow = a.table + (int64_t)it.r * a.ld_table;
+    // lane b's box of tile i starts at this token; its page, looked up one key tile ahead
+    auto token = [&](int i) { return (it.kv0 + i) * kTok + lane * (int)x.box; };
+    auto page_of = [&](int i) -> int32_t {
+      if (i >= it.seg || lane * (int)x.box >= kTok || token(i) >= it.len) return -1;
+      return trow[(uint32_t)token(i) / P];
+    };
+    int32_t page[G::kAhead + 2];                 // of tiles v .. v + kAhead + 1, v the next value tile
+#pragma unroll
+    for (int j = 0; j < G::kAhead + 2; ++j) page[j] = page_of(j);
+    int v = 0;
+    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
+      const int slot = n % kN;
+      if (!x.wait_all(&empty[slot], ((n / kN) & 1) ^ 1)) return false;
+      const int tok0 = (it.kv0 + i) * kTok;
+      const int boxes = (min(it.len - tok0, kTok) + (int)x.box - 1) / (int)x.box;
+      uint64_t* landed = !kS8 && value && tok0 + kTok > it.q.L ? &x.sh->bar.tail_full[slot] : &full[slot];
+      if (lane == 0) mbar_arrive_expect_tx(landed, boxes * x.box * D * (kS8 ? 1 : 2));
+      const int sc = m % kScaleRing;
+      if (kS8 && !value) {
+        if (!x.wait_all(&x.sh->bar.sc_empty[sc], ((m / kScaleRing) & 1) ^ 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&x.sh->bar.sc_full[sc], boxes * x.box * 8);
+      }
+      __syncwarp();
+      int32_t pg = page[0];
+#pragma unroll
+      for (int j = 1; j < G::kAhead + 2; ++j)
+        if (i - v == j) pg = page[j];
+      if (lane < boxes) {
+        if (pg < 0 || pg >= a.cache.n_pages) {   // reported; page 0 stands in
+          set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+          pg = 0;
+        }
+        const int place = (int)((uint32_t)token(i) % P);
+        const CUtensorMap* map = value ? &mv : &mk;
+        if constexpr (kS8) {
+          tma_load_4d(base + slot * G::kRaw + lane * x.box * D, map, landed, 0, place, it.h, pg);
+          if (!value) {
+            const uint32_t dst = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4) + lane * x.box * 4;
+            const int64_t at = ((int64_t)pg * a.cache.n_heads + it.h) * P + place;
+            bulk_g2s(dst, a.cache.k_scale + at, x.box * 4, &x.sh->bar.sc_full[sc]);
+            bulk_g2s(dst + kTok * 4, a.cache.v_scale + at, x.box * 4, &x.sh->bar.sc_full[sc]);
+          }
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < G::kNH; ++hf)
+            tma_load_4d(base + slot * G::kTile + hf * kHalf + lane * x.box * 128, map, landed, 64 * hf, place,
+                        it.h, pg);
+        }
+      }
+      ++n;
+      if (!value) ++m;
+      if (value) {                               // the window moves on
+#pragma unroll
+        for (int j = 0; j < G::kAhead + 1; ++j) page[j] = page[j + 1];
+        ++v;
+        page[G::kAhead + 1] = page_of(v + G::kAhead + 1);
+      }
+      return true;
+    });
+    if (!ok) return;
+  }
+}
+
+// ---- int8: four warps write codes out as bf16 ----
+template <int D, int kRT>
+QMM_DEV void convert_warps(const Ctx& x) {
+  using G = Tg<D, true, kRT>;
+  const AttnArgs& a = x.a;
+  const int lane = threadIdx.x & 31, tid = threadIdx.x & 127;
+  constexpr int kPieces = D / 16;                // 16-code pieces of a row
+  uint32_t n = 0;
+  AttnWalk walk;
+  walk.start(a, x.w, 128 * kRT, kTok);
+  AttnItem it;
+  while (walk.next(a, 128 * kRT, kTok, it)) {
+    for (int i = 0; i < 2 * it.seg; ++i, ++n) {
+      const int rs = n % G::kRawSlots, cs = n % G::kSlots;
+      if (!x.wait_all(&x.sh->bar.raw_full[rs], (n / G::kRawSlots) & 1)) return;
+      if (!x.wait_all(&x.sh->bar.empty[cs], ((n / G::kSlots) & 1) ^ 1)) return;
+      const uint32_t src = smem_u32(x.smem) + G::kOffRaw + rs * G::kRaw;
+      const uint32_t dst = smem_u32(x.smem) + G::kOffSlots + cs * G::kTile;
+#pragma unroll 4
+      for (int k = 0; k < kPieces; ++k) {
+        const int id = tid + 128 * k, row = id / kPieces, p = id % kPieces;
+        const uint4 c = lds128(src + id * 16);
+        const uint4 lo = make_uint4(s8_low_pair(c.x), s8_high_pair(c.x), s8_low_pair(c.y), s8_high_pair(c.y));
+        const uint4 hi = make_uint4(s8_low_pair(c.z), s8_high_pair(c.z), s8_low_pair(c.w), s8_high_pair(c.w));
+        const uint32_t line = dst + (p >> 2) * kHalf + row * 128;
+        const int u = (p & 3) * 2;
+        // the second half's lanes store their odd 16 bytes first: no two lanes of a phase on one bank
+        const bool swap = p >= 4;
+        sts128(line + (((u + (swap ? 1 : 0)) ^ (row & 7)) << 4), swap ? hi : lo);
+        sts128(line + (((u + (swap ? 0 : 1)) ^ (row & 7)) << 4), swap ? lo : hi);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&x.sh->bar.full[cs]);
+        mbar_arrive(&x.sh->bar.raw_empty[rs]);
+      }
+    }
+  }
+}
+
+// ---- bf16: warps 2 and 3 clean the value tiles that reach past the context
+// (one warp each of two consecutive ones) and hand them on ----
+template <int D, int kRT>
+QMM_DEV void clean_warps(const Ctx& x) {
+  using G = Tg<D, false, kRT>;
+  const AttnArgs& a = x.a;
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = (threadIdx.x >> 5) & 1;
+  uint32_t n = 0, seq = 0, tails = 0, phases = 0;   // phases: a bit per slot
+  AttnWalk walk;
+  walk.start(a, x.w, 128 * kRT, kTok);
+  AttnItem it;
+  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
+    // an item's flag is cleared eight items ahead: the ring holds four items at most
+    if (mine == 0 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
+    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
+      const int slot = n++ % G::kSlots;
+      const int tok0 = (it.kv0 + i) * kTok;
+      if (!value || tok0 + kTok <= it.q.L) return true;
+      const uint32_t parity = (phases >> slot) & 1;
+      phases ^= 1u << slot;
+      if ((tails++ & 1) != mine) return true;
+      if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return false;
+      const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile;
+      bool bad = false;
+#pragma unroll 4
+      for (int q = lane; q < kTok * (D / 8); q += 32) {
+        const int t = q / (D / 8), p = q % (D / 8);
+        if (tok0 + t < it.q.L) continue;
+        const uint32_t at = base + (p >> 3) * kHalf + t * 128 + (((p & 7) ^ (t & 7)) << 4);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (tok0 + t < it.len) {
+          v = lds128(at);
+          if (!bf16_drop_nonfinite(v)) continue;
+          bad = true;
+        }
+        sts128(at, v);
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&x.sh->bad[seq & 15], 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x.sh->bar.full[slot]);
+      return true;
+    });
+    if (!ok) return;
+  }
+}
+
+// ---- warp 1, one thread: the products ----
+template <int D, bool kS8, int kRT>
+QMM_DEV void mma_thread(const Ctx& x) {
+  using G = Tg<D, kS8, kRT>;
+  const AttnArgs& a = x.a;
+  TBars& b = x.sh->bar;
+  constexpr uint32_t kIdS = idesc_f16(128, kTok, true), kIdO = idesc_f16(128, D, true) | kIdescBMnMajor;
+  const uint32_t q_s = smem_u32(x.smem), slots = q_s + G::kOffSlots;
+  uint32_t n = 0, seq = 0, p_count[2] = {0, 0};
+  AttnWalk walk;
+  walk.start(a, x.w, 128 * kRT, kTok);
+  AttnItem it;
+  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
+    if (!x.wait(&b.q_full, seq & 1)) return;
+    const bool both = kRT == 2 && it.n_rows > 128;   // both streams on every tile
+    auto scores = [&](int st, uint32_t tile) {
+      const uint32_t qa = q_s + (kRT == 2 ? st * G::kTile : 0);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+        umma_f16(x.tmem + kColS + 128 * st, desc_kmajor_sw128(qa + at), desc_kmajor_sw128(tile + at), kIdS, k > 0);
+      }
+      umma_commit(&b.s_full[st]);
+    };
+    auto values = [&](int st, int i, uint32_t tile, bool first, bool last) {
+#pragma unroll
+      for (int k = 0; k < kTok / 16; ++k)
+        umma_f16_ta(x.tmem + kColO + 128 * st, x.tmem + kColS + 128 * st + 8 * k,
+                    desc_mnmajor_sw128(tile + k * 2048, kHalf), kIdO, !(first && k == 0));
+      if (last) umma_commit(&b.o_done[st]);
+    };
+    uint32_t v_tile = 0;
+    int v_slot = 0;
+    // Key tile i + kAhead comes right behind value tile i; with both streams on
+    // a tile, stream 1's products of value tile i wait until stream 0's next
+    // scores are queued, and the value tile is released then.
+    auto finish1 = [&](int i) {                  // kRT == 2: stream 1 of value tile i
+      if (!x.wait(&b.p_ready[1], p_count[1]++ & 1)) return false;
+      tc_fence_after();
+      values(1, i, v_tile, i == 0, i == it.seg - 1);
+      umma_commit(&b.empty[v_slot]);
+      return true;
+    };
+    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
+      const int slot = n % G::kSlots;
+      const uint32_t parity = (n / G::kSlots) & 1, tile = slots + slot * G::kTile;
+      ++n;
+      const int st = kRT == 1 ? i & 1 : 0;
+      if (!value) {
+        if (!x.wait(&b.full[slot], parity)) return false;
+        tc_fence_after();
+        scores(st, tile);
+        if (both) {
+          if (i > 0 && !finish1(i - 1)) return false;
+          scores(1, tile);
+        }
+        umma_commit(&b.empty[slot]);
+        return true;
+      }
+      if (!x.wait(&b.p_ready[st], p_count[st]++ & 1)) return false;
+      if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return false;
+      if (!x.wait(&b.full[slot], parity)) return false;
+      tc_fence_after();
+      v_tile = tile;
+      v_slot = slot;
+      values(st, i, tile, i < G::kAhead, i + G::kAhead >= it.seg);
+      if (!both) umma_commit(&b.empty[slot]);
+      else if (i == it.seg - 1 && !finish1(i)) return false;
+      return true;
+    });
+    if (!ok) return;
+  }
+}
+
+// ---- warps 4..11: the rows ----
+template <int D, bool kS8, bool kQF32, int kRT>
+QMM_DEV int4 row_warps(const Ctx& x) {
+  using G = Tg<D, kS8, kRT>;
+  const AttnArgs& a = x.a;
+  TBars& b = x.sh->bar;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int st = (wid - 4) >> 2, quarter = wid & 3;
+  const int trow = 32 * quarter + lane;          // lane of TMEM, row of the tile
+  const uint32_t tlane = x.tmem + ((uint32_t)(32 * quarter) << 16);
+  const uint32_t t_s = tlane + kColS + 128 * st;
+  const float c = a.scale_log2, slack = 8.f / c;
+  int4 owned = make_int4(0, 0, 0, 0);
+  uint32_t seq = 0, s_count = 0, o_count = 0, tiles = 0, syncs = 0;
+  auto sync8 = [&]() {                           // the eight warps
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.sync);
+    return x.wait_all(&b.sync, syncs++ & 1);
+  };
+  AttnWalk walk;
+  walk.start(a, x.w, 128 * kRT, kTok);
+  AttnItem it;
+  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
+    if (it.pieces > 0) owned = make_int4(it.r, it.id, it.pieces, 0);
+    const bool split = kRT == 1 && it.n_rows <= 64;   // lanes 64..127: the same rows, the weights' low parts
+    const bool low = split && trow >= 64;
+    const int rr = kRT == 2 ? 128 * st + trow : split ? trow & 63 : trow;
+    const bool live = rr < it.n_rows, active = __any_sync(0xffffffffu, live);
+    const int row = it.row0 + rr, node = row / a.group;
+    // the query row (with kRT == 1 each stream's thread takes half of it)
+    {
+      constexpr int kChunks = kRT == 1 ? D / 16 : D / 8;
+      const int c0 = kRT == 1 ? st * kChunks : 0;
+      const uint32_t line = smem_u32(x.smem) + (kRT == 2 ? st * G::kTile : 0) + trow * 128;
+      const int64_t qo = live ? attn_q_row(a, it.q, it.h, row) : 0;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        const int ch = c0 + j;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) {
+          if constexpr (kQF32) {
+            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qo + 8 * ch);
+            const float4 f0 = f[0], f1 = f[1];
+            v = make_uint4(bf16_pair(f0.x, f0.y), bf16_pair(f0.z, f0.w), bf16_pair(f1.x, f1.y), bf16_pair(f1.z, f1.w));
+          } else {
+            v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qo + 8 * ch);
+          }
+        }
+        sts128(line + (ch >> 3) * kHalf + (((ch & 7) ^ (trow & 7)) << 4), v);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.q_full);
+      // a stream without rows must not get an item ahead of the other
+      if (kRT == 2 && !x.wait_all(&b.q_full, seq & 1)) return owned;
+    }
+
+    float m = -INFINITY, l = 0.f;
+    const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
+    const int step = kRT == 1 ? 2 : 1;
+    for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
+      const uint32_t sc = (tiles + i) % kScaleRing;
+      uint32_t ksc = 0;
+      if constexpr (kS8) {
+        if (!x.wait_all(&b.sc_full[sc], ((tiles + i) / kScaleRing) & 1)) return owned;
+        ksc = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4);
+      }
+      if (has) {
+        if (!x.wait_all(&b.s_full[st], s_count++ & 1)) return owned;
+        tc_fence_after();
+        if (active) {
+          const int tok0 = (it.kv0 + i) * kTok;
+          const bool masked = tok0 + kTok > it.q.L;
+          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) seen[q] = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
+          }
+          // 32 scores of the row, hidden ones at -infinity (int8: times the key's scale)
+          auto load32 = [&](int q, float (&s)[32]) {
+            uint32_t r[32];
+            tmem_ld32(t_s + 32 * q, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(r[e]);
+            if constexpr (kS8) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const uint4 k = lds128(ksc + (32 * q + e) * 4);
+                s[e] *= __uint_as_float(k.x), s[e + 1] *= __uint_as_float(k.y);
+                s[e + 2] *= __uint_as_float(k.z), s[e + 3] *= __uint_as_float(k.w);
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((seen[q] >> e) & 1)) s[e] = -INFINITY;
+            }
+          };
+          float s[32], top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            load32(q, s);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+          }
+          const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            const float next = move ? top : m;
+            const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
+            l *= f;
+            if (i >= step) {                     // O exists: bring it to the new reference
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t r[32];
+                tmem_ld32(tlane + kColO + 128 * st + 32 * q, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                tmem_st32(tlane + kColO + 128 * st + 32 * q, r);
+              }
+            }
+            m = next;
+          }
+          const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            load32(q, s);
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              s[e] = exp2_approx(fmaf(s[e], c, -mc));
+              l += s[e];
+            }
+            if constexpr (kS8) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const uint4 v = lds128(ksc + kTok * 4 + (32 * q + e) * 4);
+                s[e] *= __uint_as_float(v.x), s[e + 1] *= __uint_as_float(v.y);
+                s[e + 2] *= __uint_as_float(v.z), s[e + 3] *= __uint_as_float(v.w);
+              }
+              if (masked) {                      // a hidden token's scale may not be a number
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((seen[q] >> e) & 1)) s[e] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = bf16_pair(s[2 * e], s[2 * e + 1]);
+            if (low) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                p[e] = bf16_pair(s[2 * e] - bf16lo_to_f32(p[e]), s[2 * e + 1] - bf16hi_to_f32(p[e]));
+            }
+            tmem_st16(t_s + 16 * q, p);          // over columns whose scores have been read
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.p_ready[st]);
+      }
+      if (kS8) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.sc_empty[sc]);
+      }
+    }
+    tiles += it.seg;
+
+    // ---- the item's end ----
+    const bool own_tiles = has && (kRT == 2 || it.seg > st);
+    if (own_tiles) {
+      if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
+    }
+    float f[2] = {1.f, 1.f}, top = m, sum = l;   // each stream's factor; maximum and sum of the row
+    if constexpr (kRT == 1) {
+      x.sh->m[st][trow] = m;
+      x.sh->l[st][trow] = l;
+      if (!sync8()) return owned;                // both streams' O and sums are there
+      top = fmaxf(x.sh->m[0][rr], x.sh->m[1][rr]);
+      sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // the row's own reference, for the lanes of its low parts another one;
+        // without a maximum there is no weight, unless the scores were not numbers
+        const float mk = x.sh->m[k][trow], ms = x.sh->m[k][rr], ls = x.sh->l[k][rr];
+        f[k] = mk == -INFINITY ? (x.sh->l[k][trow] == 0.f ? 0.f : 1.f) : exp2_approx((mk - top) * c);
+        sum += ls * (ms == -INFINITY ? (ls == 0.f ? 0.f : 1.f) : exp2_approx((ms - top) * c));
+      }
+    }
+    tc_fence_after();
+    const bool bad = !kS8 && x.sh->bad[seq & 15] != 0;
+    // chunks of 32 columns of O, of both streams with kRT == 1 (each takes half of the columns)
+    constexpr int kCols = kRT == 1 ? D / 2 : D;
+    const int d_first = kRT == 1 ? st * kCols : 0;
+    float* lows = reinterpret_cast<float*>(x.smem);   // [64][D + 4]: the low rows' part, over the query tile
+    constexpr int kLowPitch = D;
+    auto load_o = [&](int d, float (&o)[32]) {
+      uint32_t r[32];
+      if constexpr (kRT == 1) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (k >= it.seg) continue;             // stream 1 had no tile
+          tmem_ld32(tlane + kColO + 128 * k + d, r);
+          tmem_wait_ld();
+          if (f[k] != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f[k], o[e]);
+          }
+        }
+      } else {
+        tmem_ld32(tlane + kColO + 128 * st + d, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]);
+      }
+    };
+    if (split) {
+      if (quarter >= 2 && active) {
+        for (int d = d_first; d < d_first + kCols; d += 32) {
+          float o[32];
+          load_o(d, o);
+          // 16-byte pieces rotated by the row: the lanes of a phase on different banks
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int at = d / 4 + ((e + trow) & 7);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (((e + trow) & 7) == k) v = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            reinterpret_cast<float4*>(lows + (trow - 64) * kLowPitch)[at] = v;
+          }
+        }
+      }
+      if (!sync8()) return owned;
+    }
+    if (active && has && !(split && quarter >= 2)) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
+      const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kv0 > 0 ? 0 : 1)) * (128 * kRT) + rr;
+      __nv_bfloat16* out = live ? attn_out_row(a, it.q, it.h, row) : nullptr;
+      for (int d = d_first; d < d_first + kCols; d += 32) {
+        float o[32];
+        load_o(d, o);
+        if (!live) continue;
+        if (split) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = reinterpret_cast<const float4*>(lows + trow * kLowPitch)[d / 4 + e];
+            o[4 * e] += v.x, o[4 * e + 1] += v.y, o[4 * e + 2] += v.z, o[4 * e + 3] += v.w;
+          }
+        }
+        if (bad) attn_add_nonfinite(a, it, kTok, node, d, o);
+        if (it.whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(out + d + e) =
+                make_uint4(bf16_pair(o[e] * inv, o[e + 1] * inv), bf16_pair(o[e + 2] * inv, o[e + 3] * inv),
+                           bf16_pair(o[e + 4] * inv, o[e + 5] * inv), bf16_pair(o[e + 6] * inv, o[e + 7] * inv));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(a.part_o + slot * D + d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (live && !it.whole && d_first == 0) a.part_ml[slot] = make_float2(top == -INFINITY ? top : top * c, sum);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.o_free);
+    // the query tile, the sums and (split) the low parts are written again for the next item
+    if (kRT == 1 && !sync8()) return owned;
+  }
+  return owned;
+}
+
+template <int D, bool kS8, bool kQF32, int kRT>
+__global__ void __launch_bounds__(Tg<D, kS8, kRT>::kThreads, 1)
+attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, uint32_t box) {
+  using G = Tg<D, kS8, kRT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TShared& sh = *reinterpret_cast<TShared*>(smem + G::kBytes);
+  if (smem_u32(smem) & 1023u) {                  // the swizzled tiles need it; no static shared memory precedes
+    set_status(a.dev_status, QMM_ERR_UNSUPPORTED);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TBars& b = sh.bar;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kSlots; ++i) {
+      mbar_init(&b.full[i], kS8 ? 4 : 1);        // converters, or the loads
+      mbar_init(&b.empty[i], 1);
+      mbar_init(&b.tail_full[i], 1);
+    }
+    for (int i = 0; i < G::kRawSlots; ++i) {
+      mbar_init(&b.raw_full[i], 1);
+      mbar_init(&b.raw_empty[i], 4);
+    }
+    for (int i = 0; i < kScaleRing; ++i) {
+      mbar_init(&b.sc_full[i], 1);
+      mbar_init(&b.sc_empty[i], kRT == 1 ? 4 : 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.s_full[i], 1);
+      mbar_init(&b.p_ready[i], 4);
+      mbar_init(&b.o_done[i], 1);
+    }
+    mbar_init(&b.q_full, 8);
+    mbar_init(&b.o_free, 8);
+    mbar_init(&b.sync, 8);
+    mbar_init(&b.done, 1);
+    sh.abort = 0;
+    for (int i = 0; i < 16; ++i) sh.bad[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  Ctx x{a, &sh, smem, sh.tmem, {}, box};
+  int4 owned = make_int4(0, 0, 0, 0);
+  if (attn_find_work<G::kThreads>(a, 128 * kRT, kTok, &sh.find, x.w)) {
+    if (warp == 0) {
+      load_warp<D, kS8, kRT>(x, mk, mv);
+    } else if (warp == 1) {
+      if (lane == 0) mma_thread<D, kS8, kRT>(x);
+    } else if (warp < 4) {
+      if constexpr (!kS8) clean_warps<D, kRT>(x);
+    } else if (warp < 12) {
+      owned = row_warps<D, kS8, kQF32, kRT>(x);
+    } else {
+      if constexpr (kS8) convert_warps<D, kRT>(x);
+    }
+    __syncwarp();
+  }
+  if (warp == 4 && lane == 0) a.desc[blockIdx.x] = owned;
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (sh.abort && warp == 0 && lane == 0) {
+    // copies that nobody waited for may still be in flight
+    auto drain = [](uint64_t* bars, int n) {
+      for (int i = 0; i < n; ++i)
+        for (uint32_t ph = 0; ph < 2; ++ph) mbar_drain(&bars[i], ph, 10000000ull);
+    };
+    drain(kS8 ? b.raw_full : b.full, kS8 ? G::kRawSlots : G::kSlots);
+    if (kS8) drain(b.sc_full, kScaleRing);
+    else drain(b.tail_full, G::kSlots);
+  }
+  if (warp == 1) {
+    if (lane == 0) {
+      umma_commit(&b.done);                      // every product has completed before TMEM is freed
+      mbar_drain(&b.done, 0, 100000000ull);
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(sh.tmem, 512);
+  }
+}
+
+template <int D, bool kS8, bool kQF32, int kRT>
+cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t stream) {
+  using G = Tg<D, kS8, kRT>;
+  constexpr int kSmem = G::kBytes + (int)sizeof(TShared);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  uint32_t box = 8;
+  while (box < (uint32_t)kTok && a.cache.page_size % (2 * box) == 0) box *= 2;
+  CUtensorMap mk, mv;
+  const KvView& c = a.cache;
+  if (!make_tmap_kv(&mk, c.k, kS8, D, c.page_size, c.n_heads, c.n_pages, c.st_token, c.st_head, c.st_page, box) ||
+      !make_tmap_kv(&mv, c.v, kS8, D, c.page_size, c.n_heads, c.n_pages, c.st_token, c.st_head, c.st_page, box))
+    return cudaErrorInvalidValue;
+  auto kern = attn_tiles_kernel<D, kS8, kQF32, kRT>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kern, dim3(a.grid), dim3(G::kThreads), kSmem, stream, a, mk, mv, box);
+}
+
+template <int D, bool kS8>
+cudaError_t launch_typed(const AttnArgs& a, int rows_per_tile, bool q_f32, cudaStream_t stream) {
+  if (rows_per_tile == 128)
+    return q_f32 ? launch_tiles<D, kS8, true, 1>(a, stream) : launch_tiles<D, kS8, false, 1>(a, stream);
+  return q_f32 ? launch_tiles<D, kS8, true, 2>(a, stream) : launch_tiles<D, kS8, false, 2>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, int rows_per_tile, bool q_f32, bool cache_s8, int head_dim,
+                              cudaStream_t stream) {
+  if (head_dim == 128)
+    return cache_s8 ? launch_typed<128, true>(a, rows_per_tile, q_f32, stream)
+                    : launch_typed<128, false>(a, rows_per_tile, q_f32, stream);
+  return cache_s8 ? launch_typed<64, true>(a, rows_per_tile, q_f32, stream)
+                  : launch_typed<64, false>(a, rows_per_tile, q_f32, stream);
+}
+
+}  // namespace qmm

@@ -99,10 +99,55 @@ QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_token
   return true;
 }
 
-// The block that has unit e.
-QMM_DEV int64_t attn_block_of(const AttnWork& w, int64_t e) {
-  return ((e + 1) * w.blocks + w.total - 1) / w.total - 1;
-}
+// A block's part of one item: cached tiles [kv0, kv0 + seg) of kv_tiles.
+struct AttnItem {
+  AttnReq q;
+  int r, id;          // request; key head * row_tiles + row tile
+  int h, row0, n_rows;
+  int kv0, seg, len;
+  bool whole;
+  int pieces;         // of an item that this block begins and another ends; else 0
+};
+
+// Walks a block's units item by item.
+struct AttnWalk {
+  AttnWork w;
+  AttnReq q;
+  int r;
+  int64_t off, u;
+  QMM_DEV void start(const AttnArgs& a, const AttnWork& work, int rows_per_tile, int tile_tokens) {
+    w = work;
+    r = w.r;
+    off = w.off;
+    u = w.u0;
+    q = attn_req(a, r, rows_per_tile, tile_tokens);
+  }
+  QMM_DEV bool next(const AttnArgs& a, int rows_per_tile, int tile_tokens, AttnItem& it) {
+    if (u >= w.u1) return false;
+    while (off >= q.units) {   // to the next request that has work
+      off -= q.units;
+      q = attn_req(a, ++r, rows_per_tile, tile_tokens);
+    }
+    it.q = q;
+    it.r = r;
+    it.id = (int)(off / q.kv_tiles);
+    it.kv0 = (int)(off % q.kv_tiles);
+    it.h = it.id / q.row_tiles;
+    it.row0 = (it.id % q.row_tiles) * rows_per_tile;
+    it.n_rows = min(rows_per_tile, q.n * a.group - it.row0);
+    it.seg = (int)min((int64_t)(q.kv_tiles - it.kv0), w.u1 - u);
+    it.len = q.L + q.n;
+    it.whole = it.seg == q.kv_tiles;
+    it.pieces = 0;
+    if (!it.whole && it.kv0 == 0) {   // up to the block that has the item's last unit
+      const int64_t e = u + q.kv_tiles - 1;
+      it.pieces = (int)(((e + 1) * w.blocks + w.total - 1) / w.total - 1 - blockIdx.x) + 1;
+    }
+    u += it.seg;
+    off += it.seg;
+    return true;
+  }
+};
 
 // Whether new token i (of the request whose first new token is row `first`)
 // sees new token j; without a mask the tokens are a chain.
@@ -116,6 +161,92 @@ QMM_DEV bool attn_sees(const AttnArgs& a, int first, int i, int j) {
 QMM_DEV int64_t attn_row_offset(const AttnArgs& a, int32_t page, uint32_t tok) {
   if (page < 0 || page >= a.cache.n_pages) return -1;
   return page * a.cache.st_page + (int64_t)(tok % a.cache.page_size) * a.cache.st_token;
+}
+
+// Which of the 32 tokens from tok0 on new token i sees: bit b for tok0 + b.
+QMM_DEV uint32_t attn_sees32(const AttnArgs& a, const AttnReq& q, int i, int tok0) {
+  const int j0 = tok0 - q.L;
+  if (j0 + 32 <= 0) return ~0u;
+  auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
+  if (a.mask == nullptr) return below(i + 1 - j0);
+  const uint32_t* row = a.mask + (int64_t)(q.first + i) * a.ld_mask;
+  const int words = (q.n + 31) >> 5;
+  uint32_t w;
+  if (j0 >= 0) {
+    const int k = j0 >> 5;
+    w = __funnelshift_r(k < words ? row[k] : 0u, k + 1 < words ? row[k + 1] : 0u, j0 & 31);
+  } else {
+    w = (row[0] << -j0) | below(-j0);
+  }
+  return w & below(q.n - j0);
+}
+
+QMM_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+QMM_DEV uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two int8 codes in the low bytes of 16-bit lanes -> bf16x2, exactly: the low
+// seven bits on top of 128, and -128 or (sign bit) -256 added.
+QMM_DEV uint32_t s8_lanes_to_bf16(uint32_t x) {
+  uint32_t lo, hi, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(x), "r"(0x007F007Fu), "r"(0x43004300u));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(x), "r"(0x00800080u), "r"(0xC300C300u));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+QMM_DEV uint32_t s8_low_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4140)); }
+QMM_DEV uint32_t s8_high_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4342)); }
+
+// Zeros in place of the non-finite ones of eight bf16 values; whether there were any.
+QMM_DEV bool bf16_drop_nonfinite(uint4& v) {
+  uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  bool hit = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u, hit = true;
+    if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0x0000FFFFu, hit = true;
+  }
+  v = make_uint4(x[0], x[1], x[2], x[3]);
+  return hit;
+}
+
+// One element of a bf16 cache's value rows.
+QMM_DEV float attn_cached_v(const AttnArgs& a, int r, int h, int tok, int d) {
+  const int32_t page = a.table[(int64_t)r * a.ld_table + tok / a.cache.page_size];
+  const int64_t off = attn_row_offset(a, page, tok);
+  if (off < 0) return 0.f;
+  const uint8_t* p = a.cache.v + h * a.cache.st_head + off + 2 * d;
+  return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+}
+
+// The non-finite value elements of an item's new tokens (which the products
+// leave out) added to the outputs d0 .. d0 + N - 1 of a row that sees them.
+template <int N>
+QMM_DEV void attn_add_nonfinite(const AttnArgs& a, const AttnItem& it, int tile_tokens, int i, int d0, float (&x)[N]) {
+  const int j1 = min(it.len, (it.kv0 + it.seg) * tile_tokens) - it.q.L;
+  for (int j = max(0, it.kv0 * tile_tokens - it.q.L); j < j1; ++j) {
+    if (!attn_sees(a, it.q.first, i, j)) continue;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float v = attn_cached_v(a, it.r, it.h, it.q.L + j, d0 + e);
+      if (!isfinite(v)) x[e] += v;
+    }
+  }
+}
+
+QMM_DEV __nv_bfloat16* attn_out_row(const AttnArgs& a, const AttnReq& q, int h, int row) {
+  return a.out + (int64_t)(q.first + row / a.group) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
+}
+QMM_DEV int64_t attn_q_row(const AttnArgs& a, const AttnReq& q, int h, int row) {
+  return (int64_t)(q.first + row / a.group) * a.q_st + (int64_t)(h * a.group + row % a.group) * a.q_sh;
 }
 
 }  // namespace qmm

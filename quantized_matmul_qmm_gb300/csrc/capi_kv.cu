@@ -197,8 +197,7 @@ qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_
   a.o_st = used(out_stride_token, T);
   a.o_sh = used(out_stride_head, n_q_heads);
   a.dev_status = dev_status;
-  attn_carve(a, rows, (int)cache->head_dim, workspace);
-  return kv_status(launch_attn(a, q_type == QMM_F32, cache->type == QMM_S8, (int)cache->head_dim, stream));
+  return kv_status(launch_attn(a, q_type == QMM_F32, cache->type == QMM_S8, (int)cache->head_dim, workspace, stream));
 }
 
 }  // extern "C"

@@ -79,10 +79,29 @@ struct AttnArgs {
   int grid;
   int32_t* dev_status;
 };
-// Workspace bytes of a call whose requests have up to `rows` query rows per key head.
-size_t attn_workspace_bytes(int64_t rows, int head_dim);
-// Fills the workspace pointers and the grid of `a` from `workspace`.
-void attn_carve(AttnArgs& a, int64_t rows, int head_dim, void* workspace);
-cudaError_t launch_attn(const AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, cudaStream_t stream);
+// A cache side as a 4-D tensor {head_dim, place, head, page} for TMA: boxes of
+// box_tokens places x 64 bf16 dimensions (128-byte swizzle) or x all int8 codes
+// of a row (no swizzle).
+bool make_tmap_kv(CUtensorMap* map, const void* base, bool s8, int head_dim, uint32_t page_size, uint64_t n_heads,
+                  uint64_t n_pages, int64_t st_token, int64_t st_head, int64_t st_page, uint32_t box_tokens);
+
+// What a call needs of the device, and how its workspace is laid out.
+struct AttnPlan {
+  bool tiles;          // attn_tiles.cu (tcgen05), else attn_rows.cu
+  int rows_per_tile;   // query rows of an item
+  int grid;            // blocks
+};
+int attn_sm_count();
+// `pages_tile`: the cache's pages and scales allow TMA boxes (attn_pages_tile).
+AttnPlan attn_plan(int64_t rows, bool pages_tile);
+bool attn_pages_tile(const KvView& c, bool s8);
+size_t attn_workspace_bytes(int64_t rows, int head_dim);   // for either kernel
+cudaError_t launch_attn(AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, void* workspace, cudaStream_t stream);
+// one of the two kernels, and the joining of items that blocks share (attn_rows.cu)
+cudaError_t launch_attn_rows(const AttnArgs& a, int rows_per_tile, bool q_f32, bool cache_s8, int head_dim,
+                             cudaStream_t stream);
+cudaError_t launch_attn_tiles(const AttnArgs& a, int rows_per_tile, bool q_f32, bool cache_s8, int head_dim,
+                              cudaStream_t stream);
+cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_tile, int head_dim, cudaStream_t stream);
 
 }  // namespace qmm

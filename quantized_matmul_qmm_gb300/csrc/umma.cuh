@@ -338,6 +338,14 @@ QMM_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+QMM_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 QMM_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, K-major operand in the 128-byte swizzle
@@ -354,6 +362,21 @@ QMM_DEV uint64_t desc_kmajor_sw128(uint32_t saddr) {
   d |= (uint64_t)2u << 61;                   // 128-byte swizzle
   return d;
 }
+
+// MN-major operand (the rows of the tile are k, 128 bytes = 64 elements along
+// M/N) in the same 128-byte swizzle: atoms of 8 k rows x 128 bytes, stacked
+// along k (stride 1024), and `mn_stride` bytes from one 64-element block of M/N
+// to the next.  Stepping K by 16 adds 2048 bytes to the start address.
+QMM_DEV uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(mn_stride >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;   // instruction descriptor: B is MN-major
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B both f16 or
 // both bf16, both K-major, shape M x N.
