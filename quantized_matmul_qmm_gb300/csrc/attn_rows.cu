@@ -47,6 +47,7 @@ constexpr int kGroup = 16;                       // cached tokens per warp step
 constexpr int kTileTokens = kGroup * kWarps;     // a unit
 constexpr int kBlocksPerSm = 2;
 constexpr int kRingBytes = 24576;                // per warp
+constexpr int kCombineMaxOwners = 512;           // blocks of an attention grid, at most
 // More query rows per key head than this go to the tile kernel (attn_tiles.cu).
 constexpr int64_t kRowsKernelMax = 32;
 
@@ -114,17 +115,17 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   AttnWork w;
   if (!attn_find_work<kThreads>(a, kRows, kTileTokens, &find, w)) {
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) attn_post_owned(a, AttnOwned{});
     return;
   }
-  int4 owned = make_int4(0, 0, 0, 0);            // the item that this block begins and another ends
+  AttnOwned owned{};                             // the item that this block begins and another ends
   AttnWalk walk;
-  walk.start(a, w, kRows, kTileTokens);
+  walk.start(w);
   AttnItem im;
-  while (walk.next(a, kRows, kTileTokens, im)) {
+  while (walk.next(a, w, kRows, kTileTokens, im)) {
     const AttnReq& rq = im.q;
     const int h = im.h, row0 = im.row0, kv0 = im.kv0, seg = im.seg, L = rq.L, len = im.len, n_rows = im.n_rows;
-    if (im.pieces > 0) owned = make_int4(im.r, im.id, im.pieces, 0);
+    if (im.pieces > 0) owned = attn_owned(im);
     const int tok_first = kv0 * kTileTokens + wid * kGroup;
 
     // ---- the ring ----
@@ -441,7 +442,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
       if (!kS8 && s_bad) attn_add_nonfinite(a, im, kTileTokens, (row0 + rr) / a.group, d, x);
       if (im.whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
-        *reinterpret_cast<uint2*>(attn_out_row(a, rq, h, row0 + rr) + d) =
+        *reinterpret_cast<uint2*>(attn_out_row(a, rq.first, h, row0 + rr) + d) =
             make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot * kRows + rr) * D + d) = make_float4(x[0], x[1], x[2], x[3]);
@@ -450,48 +451,100 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
     }
     __syncthreads();                             // the buffer is the next item's ring
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = owned;
+  if (threadIdx.x == 0) attn_post_owned(a, owned);
 }
 
-// Joins the pieces of an item that several blocks computed: piece 0 is the
-// owner block's slot 1, the others the following blocks' slot 0.  One block
-// per (owner, 16 rows), a thread per four values of a row.
-constexpr int kCombineRows = 16;
+// Joins the pieces of the items that several blocks computed: piece 0 is the
+// owner block's slot 1, the others the following blocks' slot 0.  Each block
+// adds up all owners' rows and its warps take rows at the grid's pitch, so that
+// a few long items keep the whole GPU busy; a warp first holds the pieces'
+// maxima and sums, one per lane, then four (two) columns per lane, eight
+// pieces' loads in flight.  What costs is the chain of loads (owners, maxima,
+// values), a few us however little there is to join.
+constexpr int kCombineThreads = 256;
+constexpr int kCombinePerSm = 4;
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kCombineThreads, kCombinePerSm)
 attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
+  __shared__ int s_end[kCombineMaxOwners];       // running sum of the owners' rows
+  __shared__ int s_warp[kCombineThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const int4 own = a.desc[blockIdx.x];
-  if (own.z == 0) return;
-  constexpr int kLanes = D / 4;
-  AttnReq q{};
-  q.first = a.cu[own.x];
-  q.n = a.cu[own.x + 1] - q.first;
-  const int row_tiles = (q.n * a.group + rows_per_tile - 1) / rows_per_tile;
-  const int h = own.y / row_tiles, row0 = (own.y % row_tiles) * rows_per_tile;
-  const int n_rows = min(rows_per_tile, q.n * a.group - row0);
-  const int d = (threadIdx.x % kLanes) * 4;
-  const int64_t b = blockIdx.x;
-  const int r1 = min(n_rows, (int)(blockIdx.y + 1) * kCombineRows);
-  for (int rr = blockIdx.y * kCombineRows + threadIdx.x / kLanes; rr < r1; rr += kThreads / kLanes) {
-    auto at = [&](int p) { return (p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < own.z; ++p) top = fmaxf(top, a.part_ml[at(p)].x);
-    float x[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < own.z; ++p) {
-      const float2 ml = a.part_ml[at(p)];
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + d);
-      // a piece without a maximum has no weight, unless its scores were not numbers
-      const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
-      sum += ml.y * f;
-      x[0] += v.x * f, x[1] += v.y * f, x[2] += v.z * f, x[3] += v.w * f;
+  constexpr int kV = D / 32;                     // columns per lane
+  constexpr int kPer = kCombineMaxOwners / kCombineThreads;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int rows[kPer], incl = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int b = threadIdx.x * kPer + k;
+    rows[k] = b < a.grid ? a.owned_rows[b] : 0;
+    incl += rows[k];
+  }
+  const int mine = incl;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) s_warp[wid] = incl;
+  __syncthreads();
+  int run = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kCombineThreads / 32; ++i) {
+    if (i < wid) run += s_warp[i];
+    total += s_warp[i];
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) s_end[threadIdx.x * kPer + k] = run += rows[k];
+  __syncthreads();
+#pragma unroll 1
+  for (int i = wid * gridDim.x + blockIdx.x; i < total; i += gridDim.x * (kCombineThreads / 32)) {
+    int lo = 0, hi = kCombineMaxOwners - 1;      // the first owner whose running sum passes i
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > i) hi = mid; else lo = mid + 1;
     }
+    const int b = lo, rr = i - (lo > 0 ? s_end[lo - 1] : 0);
+    const int4 own = a.owned[b];                 // h, row0, pieces, first
+    const int pieces = own.z;
+    auto at = [&](int p, int rr) { return (int64_t)(p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
+    float top = -INFINITY;
+    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, a.part_ml[at(p, rr)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float x[kV] = {}, sum = 0.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < pieces; p0 += 32) {
+      const int n = min(32, pieces - p0);
+      float f = 0.f;
+      if (lane < n) {
+        const float2 ml = a.part_ml[at(p0 + lane, rr)];
+        // a piece without a maximum has no weight, unless its scores were not numbers
+        f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
+        sum += ml.y * f;
+      }
+#pragma unroll 8
+      for (int p = 0; p < n; ++p) {
+        const float fp = __shfl_sync(0xffffffffu, f, p);
+        const float* src = a.part_o + at(p0 + p, rr) * D + lane * kV;
+        if constexpr (kV == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[0] += v.x * fp, x[1] += v.y * fp, x[2] += v.z * fp, x[3] += v.w * fp;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[0] += v.x * fp, x[1] += v.y * fp;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(attn_out_row(a, q, h, row0 + rr) + d) =
-        make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
+    __nv_bfloat16* out = attn_out_row(a, own.w, own.x, own.y + rr) + lane * kV;
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(out) = bf16_pair(x[0] * inv, x[1] * inv);
   }
 }
 
@@ -523,10 +576,19 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int rows_per_tile, bool q_f32, b
                   : launch_typed<64, false>(a, rows_per_tile, q_f32, stream);
 }
 
+template <int D>
+static cudaError_t launch_combine(const AttnArgs& a, int rows_per_tile, cudaStream_t stream) {
+  // the attention kernels' shared-memory configuration: an SM that had to
+  // change it would drain first
+  cudaError_t err = cudaFuncSetAttribute(attn_combine_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(attn_combine_kernel<D>, dim3(kCombinePerSm * attn_sm_count()), dim3(kCombineThreads), 0, stream, a,
+                    rows_per_tile);
+}
+
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_tile, int head_dim, cudaStream_t stream) {
-  const dim3 grid(a.grid, (rows_per_tile + kCombineRows - 1) / kCombineRows);
-  return head_dim == 128 ? launch_pdl(attn_combine_kernel<128>, grid, dim3(kThreads), 0, stream, a, rows_per_tile)
-                         : launch_pdl(attn_combine_kernel<64>, grid, dim3(kThreads), 0, stream, a, rows_per_tile);
+  return head_dim == 128 ? launch_combine<128>(a, rows_per_tile, stream) : launch_combine<64>(a, rows_per_tile, stream);
 }
 
 // ---- the choice of a kernel, shared by the size query and the call ----
@@ -546,7 +608,7 @@ bool attn_pages_tile(const KvView& c, bool s8) {
 }
 
 AttnPlan attn_plan(int64_t rows, bool pages_tile) {
-  const int sms = attn_sm_count();
+  const int sms = std::min(attn_sm_count(), kCombineMaxOwners / kBlocksPerSm);
   if (rows > kRowsKernelMax && pages_tile) return {true, rows <= 128 ? 128 : 256, sms};
   return {false, rows <= 16 ? 16 : 32, kBlocksPerSm * sms};
 }
@@ -554,7 +616,7 @@ AttnPlan attn_plan(int64_t rows, bool pages_tile) {
 namespace {
 size_t plan_bytes(const AttnPlan& p, int head_dim) {
   return 2 * (size_t)p.grid * p.rows_per_tile * (head_dim * sizeof(float) + sizeof(float2)) +
-         (size_t)p.grid * sizeof(int4);
+         (size_t)p.grid * (sizeof(int4) + sizeof(int));
 }
 }  // namespace
 
@@ -568,7 +630,8 @@ cudaError_t launch_attn(AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, vo
   const size_t rows = 2 * (size_t)p.grid * p.rows_per_tile;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * head_dim);
-  a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
+  a.owned = reinterpret_cast<int4*>(a.part_ml + rows);
+  a.owned_rows = reinterpret_cast<int*>(a.owned + p.grid);
   const cudaError_t err = p.tiles ? launch_attn_tiles(a, p.rows_per_tile, q_f32, cache_s8, head_dim, stream)
                                   : launch_attn_rows(a, p.rows_per_tile, q_f32, cache_s8, head_dim, stream);
   if (err != cudaSuccess) return err;

@@ -76,6 +76,7 @@ struct TBars {
 struct TShared {
   TBars bar;
   AttnFindScratch find;
+  AttnWork work;                                 // out of the roles' registers
   float m[2][128], l[2][128];
   int bad[16];                       // per item, by its number: a non-finite value was taken out
   uint32_t tmem;
@@ -89,109 +90,126 @@ struct Ctx {
   TShared* sh;
   uint8_t* smem;
   uint32_t tmem;
-  AttnWork w;
   uint32_t box;                                  // tokens of a TMA box
+  // The first tries suspend the thread until the phase completes; only then
+  // does the wait read the clock for its limit (the read itself takes long).
   QMM_DEV bool wait(uint64_t* bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, &sh->abort, a.dev_status);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      if (mbar_try_wait_suspend(bar, parity, kSuspendHintNs)) return true;
+    return mbar_wait(bar, parity, &sh->abort, a.dev_status);
   }
-  QMM_DEV bool wait_all(uint64_t* bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait(bar, parity));
+  QMM_DEV bool wait_all(uint64_t* bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait(bar, parity)); }
+};
+
+// The order in which an item's tiles are fetched and used: kAhead key tiles,
+// then value tile i and key tile i + kAhead in turn.  Every role walks it in
+// one loop with one body: a block runs most of its code for a few tiles only,
+// and code seen for the first time costs more to fetch than to run.
+template <int kAhead>
+struct TileOrder {
+  int seg, keys = 0, values = 0;
+  QMM_DEV bool next(bool& value, int& i) {
+    if (values >= seg) return false;
+    value = keys >= seg || keys - values >= kAhead;
+    i = value ? values++ : keys++;
+    return true;
   }
 };
 
-// Calls f(is_value, tile, page-lookup tile) in the order in which tiles are fetched and used.
-template <int kAhead, typename F>
-QMM_DEV bool tile_order(int seg, F f) {
-  for (int i = 0; i < min(kAhead, seg); ++i)
-    if (!f(false, i)) return false;
-  for (int i = 0; i < seg; ++i) {
-    if (!f(true, i)) return false;
-    if (i + kAhead < seg && !f(false, i + kAhead)) return false;
-  }
-  return true;
-}
-
 // ---- warp 0: tiles into shared memory ----
+// One warp's chain of instructions per tile has to stay well under the tile's
+// time at HBM rate (0.8 to 1.5 us): places of a tile follow from the last
+// tile's by an addition (no division), and the page table is read two tiles
+// ahead.
 template <int D, bool kS8, int kRT>
 QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& mv) {
   using G = Tg<D, kS8, kRT>;
   const AttnArgs& a = x.a;
   const int lane = threadIdx.x & 31;
-  constexpr int kN = kS8 ? G::kRawSlots : G::kSlots;
+  constexpr uint32_t kN = kS8 ? G::kRawSlots : G::kSlots, kStage = kS8 ? G::kRaw : G::kTile;
+  constexpr uint32_t kRow = kS8 ? D : 128;       // bytes of a row of a box
+  constexpr int kWin = G::kAhead + 2;            // tiles looked up and not yet fetched
   uint64_t* full = kS8 ? x.sh->bar.raw_full : x.sh->bar.full;
   uint64_t* empty = kS8 ? x.sh->bar.raw_empty : x.sh->bar.empty;
-  const uint32_t base = smem_u32(x.smem) + (kS8 ? G::kOffRaw : G::kOffSlots);
-  const uint32_t P = a.cache.page_size;
-  uint32_t n = 0, m = 0;                         // tiles fetched; key tiles fetched
+  const uint32_t box = x.box, P = a.cache.page_size, lane_off = lane * box * kRow;
+  const uint32_t base = smem_u32(x.smem) + (kS8 ? G::kOffRaw : G::kOffSlots) + lane_off;
+  const uint32_t box_bytes = box * D * (kS8 ? 1 : 2);
+  const int lane_tok = lane * (int)box;
+  const uint32_t step_blk = kTok / P, step_place = kTok % P;
+  uint32_t slot = 0, phase = 1, sc = 0, sc_phase = 1;
   if (lane == 0) {
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
   }
   AttnWalk walk;
-  walk.start(a, x.w, 128 * kRT, kTok);
+  walk.start(x.sh->work);
   AttnItem it;
-  while (walk.next(a, 128 * kRT, kTok, it)) {
+  while (walk.next(a, x.sh->work, 128 * kRT, kTok, it)) {
     const int32_t* trow = a.table + (int64_t)it.r * a.ld_table;
-    // lane b's box of tile i starts at this token; its page, looked up one key tile ahead
-    auto token = [&](int i) { return (it.kv0 + i) * kTok + lane * (int)x.box; };
-    auto page_of = [&](int i) -> int32_t {
-      if (i >= it.seg || lane * (int)x.box >= kTok || token(i) >= it.len) return -1;
-      return trow[(uint32_t)token(i) / P];
+    // lane b's box of each tile: block and place of the next tile to look up
+    int tok = it.kv0 * kTok + lane_tok;
+    uint32_t blk = (uint32_t)tok / P, place = (uint32_t)tok % P;
+    const int tok_end = lane_tok < kTok ? min(it.len, (it.kv0 + it.seg) * kTok) : 0;
+    int32_t page[kWin];                          // page[j]: of tile (value tiles fetched) + j
+    uint32_t places[kWin];
+    auto look_up = [&](int32_t& pg, uint32_t& pl) {
+      pg = tok < tok_end ? trow[blk] : -1;
+      pl = place;
+      tok += kTok;
+      blk += step_blk;
+      place += step_place;
+      if (place >= P) place -= P, ++blk;
     };
-    int32_t page[G::kAhead + 2];                 // of tiles v .. v + kAhead + 1, v the next value tile
 #pragma unroll
-    for (int j = 0; j < G::kAhead + 2; ++j) page[j] = page_of(j);
-    int v = 0;
-    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
-      const int slot = n % kN;
-      if (!x.wait_all(&empty[slot], ((n / kN) & 1) ^ 1)) return false;
-      const int tok0 = (it.kv0 + i) * kTok;
-      const int boxes = (min(it.len - tok0, kTok) + (int)x.box - 1) / (int)x.box;
-      uint64_t* landed = !kS8 && value && tok0 + kTok > it.q.L ? &x.sh->bar.tail_full[slot] : &full[slot];
-      if (lane == 0) mbar_arrive_expect_tx(landed, boxes * x.box * D * (kS8 ? 1 : 2));
-      const int sc = m % kScaleRing;
+    for (int j = 0; j < kWin; ++j) look_up(page[j], places[j]);
+    TileOrder<G::kAhead> order{it.seg};
+    bool value;
+    int i;
+#pragma unroll 1
+    while (order.next(value, i)) {
+      // value tile i: page[0]; key tile i: page[i - value tiles], kAhead - 1 but for the first
+      int32_t pg = page[0];
+      uint32_t pl = places[0];
+      if (!value && i - order.values > 0) pg = page[G::kAhead - 1], pl = places[G::kAhead - 1];
+      if (!x.wait_all(&empty[slot], phase)) return;
+      const int left = it.len - (it.kv0 + i) * kTok;
+      const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
+      uint64_t* landed = !kS8 && value && it.q.n + kTok > left ? &x.sh->bar.tail_full[slot] : &full[slot];
+      if (lane == 0) mbar_arrive_expect_tx(landed, boxes * box_bytes);
       if (kS8 && !value) {
-        if (!x.wait_all(&x.sh->bar.sc_empty[sc], ((m / kScaleRing) & 1) ^ 1)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&x.sh->bar.sc_full[sc], boxes * x.box * 8);
+        if (!x.wait_all(&x.sh->bar.sc_empty[sc], sc_phase)) return;
+        if (lane == 0) mbar_arrive_expect_tx(&x.sh->bar.sc_full[sc], boxes * box * 8);
       }
       __syncwarp();
-      int32_t pg = page[0];
-#pragma unroll
-      for (int j = 1; j < G::kAhead + 2; ++j)
-        if (i - v == j) pg = page[j];
       if (lane < boxes) {
-        if (pg < 0 || pg >= a.cache.n_pages) {   // reported; page 0 stands in
+        if ((uint32_t)pg >= (uint64_t)a.cache.n_pages) {   // reported; page 0 stands in
           set_status(a.dev_status, QMM_ERR_INVALID_ARG);
           pg = 0;
         }
-        const int place = (int)((uint32_t)token(i) % P);
         const CUtensorMap* map = value ? &mv : &mk;
+        const uint32_t dst = base + slot * kStage;
         if constexpr (kS8) {
-          tma_load_4d(base + slot * G::kRaw + lane * x.box * D, map, landed, 0, place, it.h, pg);
+          tma_load_4d(dst, map, landed, 0, pl, it.h, pg);
           if (!value) {
-            const uint32_t dst = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4) + lane * x.box * 4;
-            const int64_t at = ((int64_t)pg * a.cache.n_heads + it.h) * P + place;
-            bulk_g2s(dst, a.cache.k_scale + at, x.box * 4, &x.sh->bar.sc_full[sc]);
-            bulk_g2s(dst + kTok * 4, a.cache.v_scale + at, x.box * 4, &x.sh->bar.sc_full[sc]);
+            const uint32_t to = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4) + lane_tok * 4;
+            const int64_t at = ((int64_t)pg * a.cache.n_heads + it.h) * P + pl;
+            bulk_g2s(to, a.cache.k_scale + at, box * 4, &x.sh->bar.sc_full[sc]);
+            bulk_g2s(to + kTok * 4, a.cache.v_scale + at, box * 4, &x.sh->bar.sc_full[sc]);
           }
         } else {
 #pragma unroll
-          for (int hf = 0; hf < G::kNH; ++hf)
-            tma_load_4d(base + slot * G::kTile + hf * kHalf + lane * x.box * 128, map, landed, 64 * hf, place,
-                        it.h, pg);
+          for (int hf = 0; hf < G::kNH; ++hf) tma_load_4d(dst + hf * kHalf, map, landed, 64 * hf, pl, it.h, pg);
         }
       }
-      ++n;
-      if (!value) ++m;
-      if (value) {                               // the window moves on
+      if (++slot == kN) slot = 0, phase ^= 1;
+      if (kS8 && !value && ++sc == kScaleRing) sc = 0, sc_phase ^= 1;
+      if (value) {
 #pragma unroll
-        for (int j = 0; j < G::kAhead + 1; ++j) page[j] = page[j + 1];
-        ++v;
-        page[G::kAhead + 1] = page_of(v + G::kAhead + 1);
+        for (int j = 0; j < kWin - 1; ++j) page[j] = page[j + 1], places[j] = places[j + 1];
+        look_up(page[kWin - 1], places[kWin - 1]);
       }
-      return true;
-    });
-    if (!ok) return;
+    }
   }
 }
 
@@ -204,9 +222,9 @@ QMM_DEV void convert_warps(const Ctx& x) {
   constexpr int kPieces = D / 16;                // 16-code pieces of a row
   uint32_t n = 0;
   AttnWalk walk;
-  walk.start(a, x.w, 128 * kRT, kTok);
+  walk.start(x.sh->work);
   AttnItem it;
-  while (walk.next(a, 128 * kRT, kTok, it)) {
+  while (walk.next(a, x.sh->work, 128 * kRT, kTok, it)) {
     for (int i = 0; i < 2 * it.seg; ++i, ++n) {
       const int rs = n % G::kRawSlots, cs = n % G::kSlots;
       if (!x.wait_all(&x.sh->bar.raw_full[rs], (n / G::kRawSlots) & 1)) return;
@@ -246,19 +264,23 @@ QMM_DEV void clean_warps(const Ctx& x) {
   const uint32_t mine = (threadIdx.x >> 5) & 1;
   uint32_t n = 0, seq = 0, tails = 0, phases = 0;   // phases: a bit per slot
   AttnWalk walk;
-  walk.start(a, x.w, 128 * kRT, kTok);
+  walk.start(x.sh->work);
   AttnItem it;
-  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
+  for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
     // an item's flag is cleared eight items ahead: the ring holds four items at most
     if (mine == 0 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
-    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
+    TileOrder<G::kAhead> order{it.seg};
+    bool value;
+    int i;
+#pragma unroll 1
+    while (order.next(value, i)) {
       const int slot = n++ % G::kSlots;
       const int tok0 = (it.kv0 + i) * kTok;
-      if (!value || tok0 + kTok <= it.q.L) return true;
+      if (!value || tok0 + kTok <= it.q.L) continue;
       const uint32_t parity = (phases >> slot) & 1;
       phases ^= 1u << slot;
-      if ((tails++ & 1) != mine) return true;
-      if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return false;
+      if ((tails++ & 1) != mine) continue;
+      if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return;
       const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile;
       bool bad = false;
 #pragma unroll 4
@@ -278,9 +300,7 @@ QMM_DEV void clean_warps(const Ctx& x) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.sh->bar.full[slot]);
-      return true;
-    });
-    if (!ok) return;
+    }
   }
 }
 
@@ -292,75 +312,102 @@ QMM_DEV void mma_thread(const Ctx& x) {
   TBars& b = x.sh->bar;
   constexpr uint32_t kIdS = idesc_f16(128, kTok, true), kIdO = idesc_f16(128, D, true) | kIdescBMnMajor;
   const uint32_t q_s = smem_u32(x.smem), slots = q_s + G::kOffSlots;
-  uint32_t n = 0, seq = 0, p_count[2] = {0, 0};
+  uint32_t slot = 0, phase = 0, seq = 0, p_count[2] = {0, 0};
   AttnWalk walk;
-  walk.start(a, x.w, 128 * kRT, kTok);
+  walk.start(x.sh->work);
   AttnItem it;
-  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
+  for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
     if (!x.wait(&b.q_full, seq & 1)) return;
     const bool both = kRT == 2 && it.n_rows > 128;   // both streams on every tile
     auto scores = [&](int st, uint32_t tile) {
-      const uint32_t qa = q_s + (kRT == 2 ? st * G::kTile : 0);
-#pragma unroll
+      // the address fields do not carry past their 14 bits: shared memory ends below 2^18
+      uint64_t q_desc = desc_kmajor_sw128(q_s + (kRT == 2 ? st * G::kTile : 0)), k_desc = desc_kmajor_sw128(tile);
+      const uint32_t d = x.tmem + kColS + 128 * st;
+#pragma unroll 2
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
-        umma_f16(x.tmem + kColS + 128 * st, desc_kmajor_sw128(qa + at), desc_kmajor_sw128(tile + at), kIdS, k > 0);
+        umma_f16(d, q_desc, k_desc, kIdS, k > 0);
+        const uint32_t step = (k & 3) == 3 ? (kHalf - 96) >> 4 : 32 >> 4;   // the next 16 dimensions
+        q_desc += step;
+        k_desc += step;
       }
       umma_commit(&b.s_full[st]);
     };
-    auto values = [&](int st, int i, uint32_t tile, bool first, bool last) {
-#pragma unroll
-      for (int k = 0; k < kTok / 16; ++k)
-        umma_f16_ta(x.tmem + kColO + 128 * st, x.tmem + kColS + 128 * st + 8 * k,
-                    desc_mnmajor_sw128(tile + k * 2048, kHalf), kIdO, !(first && k == 0));
+    auto values = [&](int st, uint32_t tile, bool first, bool last) {
+      uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
+      const uint32_t d = x.tmem + kColO + 128 * st, p = x.tmem + kColS + 128 * st;
+#pragma unroll 2
+      for (int k = 0; k < kTok / 16; ++k) {
+        umma_f16_ta(d, p + 8 * k, v_desc, kIdO, !(first && k == 0));
+        v_desc += 2048 >> 4;
+      }
       if (last) umma_commit(&b.o_done[st]);
     };
     uint32_t v_tile = 0;
-    int v_slot = 0;
-    // Key tile i + kAhead comes right behind value tile i; with both streams on
-    // a tile, stream 1's products of value tile i wait until stream 0's next
-    // scores are queued, and the value tile is released then.
-    auto finish1 = [&](int i) {                  // kRT == 2: stream 1 of value tile i
-      if (!x.wait(&b.p_ready[1], p_count[1]++ & 1)) return false;
-      tc_fence_after();
-      values(1, i, v_tile, i == 0, i == it.seg - 1);
-      umma_commit(&b.empty[v_slot]);
-      return true;
-    };
-    const bool ok = tile_order<G::kAhead>(it.seg, [&](bool value, int i) {
-      const int slot = n % G::kSlots;
-      const uint32_t parity = (n / G::kSlots) & 1, tile = slots + slot * G::kTile;
-      ++n;
+    int v_slot = 0, v_i = 0;
+    bool v_open = false;                         // kRT == 2: stream 1 has value tile v_i still to come
+    TileOrder<G::kAhead> order{it.seg};
+    bool value;
+    int i;
+    // Key tile i + kAhead comes right behind value tile i.  With both streams
+    // on a tile, stream 1's products of value tile i wait until stream 0's
+    // next scores are queued, and the value tile is released then.
+#pragma unroll 1
+    for (;;) {
+      const bool more = order.next(value, i);
       const int st = kRT == 1 ? i & 1 : 0;
-      if (!value) {
-        if (!x.wait(&b.full[slot], parity)) return false;
-        tc_fence_after();
-        scores(st, tile);
-        if (both) {
-          if (i > 0 && !finish1(i - 1)) return false;
-          scores(1, tile);
+      const uint32_t tile = slots + slot * G::kTile;
+      if (more) {
+        if (value) {
+          if (!x.wait(&b.p_ready[st], p_count[st]++ & 1)) return;
+          if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return;
         }
-        umma_commit(&b.empty[slot]);
-        return true;
+        if (!x.wait(&b.full[slot], phase)) return;
+        tc_fence_after();
+        if (value) {
+          values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg);
+          v_tile = tile;
+          v_slot = slot;
+          v_i = i;
+          v_open = both;
+        } else {
+          scores(st, tile);
+        }
       }
-      if (!x.wait(&b.p_ready[st], p_count[st]++ & 1)) return false;
-      if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return false;
-      if (!x.wait(&b.full[slot], parity)) return false;
-      tc_fence_after();
-      v_tile = tile;
-      v_slot = slot;
-      values(st, i, tile, i < G::kAhead, i + G::kAhead >= it.seg);
-      if (!both) umma_commit(&b.empty[slot]);
-      else if (i == it.seg - 1 && !finish1(i)) return false;
-      return true;
-    });
-    if (!ok) return;
+      if (kRT == 2 && v_open && (!more || !value || i == it.seg - 1)) {
+        if (!x.wait(&b.p_ready[1], p_count[1]++ & 1)) return;
+        tc_fence_after();
+        values(1, v_tile, v_i == 0, v_i == it.seg - 1);
+        umma_commit(&b.empty[v_slot]);
+        v_open = false;
+      }
+      if (!more) break;
+      if (!value && both) scores(1, tile);
+      if (!value || !both) umma_commit(&b.empty[slot]);
+      if (++slot == G::kSlots) slot = 0, phase ^= 1;
+    }
   }
 }
 
 // ---- warps 4..11: the rows ----
+// s[e] *= the e-th of 32 fp32 values in shared memory; with `guard`, zeros stay
+// zeros whatever they meet.
+QMM_DEV void scale32(float (&s)[32], uint32_t addr, bool guard = false) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const uint4 k = lds128(addr + e * 4);
+    const float f[4] = {__uint_as_float(k.x), __uint_as_float(k.y), __uint_as_float(k.z), __uint_as_float(k.w)};
+    if (guard) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[e + j] = s[e + j] == 0.f ? 0.f : s[e + j] * f[j];
+    } else {
+      f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(f[0], f[1])), s[e], s[e + 1]);
+      f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(f[2], f[3])), s[e + 2], s[e + 3]);
+    }
+  }
+}
+
 template <int D, bool kS8, bool kQF32, int kRT>
-QMM_DEV int4 row_warps(const Ctx& x) {
+QMM_DEV AttnOwned row_warps(const Ctx& x) {
   using G = Tg<D, kS8, kRT>;
   const AttnArgs& a = x.a;
   TBars& b = x.sh->bar;
@@ -370,7 +417,7 @@ QMM_DEV int4 row_warps(const Ctx& x) {
   const uint32_t tlane = x.tmem + ((uint32_t)(32 * quarter) << 16);
   const uint32_t t_s = tlane + kColS + 128 * st;
   const float c = a.scale_log2, slack = 8.f / c;
-  int4 owned = make_int4(0, 0, 0, 0);
+  AttnOwned owned{};
   uint32_t seq = 0, s_count = 0, o_count = 0, tiles = 0, syncs = 0;
   auto sync8 = [&]() {                           // the eight warps
     __syncwarp();
@@ -378,10 +425,10 @@ QMM_DEV int4 row_warps(const Ctx& x) {
     return x.wait_all(&b.sync, syncs++ & 1);
   };
   AttnWalk walk;
-  walk.start(a, x.w, 128 * kRT, kTok);
+  walk.start(x.sh->work);
   AttnItem it;
-  for (; walk.next(a, 128 * kRT, kTok, it); ++seq) {
-    if (it.pieces > 0) owned = make_int4(it.r, it.id, it.pieces, 0);
+  for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
+    if (it.pieces > 0) owned = attn_owned(it);
     const bool split = kRT == 1 && it.n_rows <= 64;   // lanes 64..127: the same rows, the weights' low parts
     const bool low = split && trow >= 64;
     const int rr = kRT == 2 ? 128 * st + trow : split ? trow & 63 : trow;
@@ -393,7 +440,7 @@ QMM_DEV int4 row_warps(const Ctx& x) {
       const int c0 = kRT == 1 ? st * kChunks : 0;
       const uint32_t line = smem_u32(x.smem) + (kRT == 2 ? st * G::kTile : 0) + trow * 128;
       const int64_t qo = live ? attn_q_row(a, it.q, it.h, row) : 0;
-#pragma unroll
+#pragma unroll 4
       for (int j = 0; j < kChunks; ++j) {
         const int ch = c0 + j;
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -415,7 +462,8 @@ QMM_DEV int4 row_warps(const Ctx& x) {
       if (kRT == 2 && !x.wait_all(&b.q_full, seq & 1)) return owned;
     }
 
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY;                         // the reference, before the scale
+    uint64_t l = 0;                              // sum, in two halves
     const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
     const int step = kRT == 1 ? 2 : 1;
     for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
@@ -431,89 +479,76 @@ QMM_DEV int4 row_warps(const Ctx& x) {
         if (active) {
           const int tok0 = (it.kv0 + i) * kTok;
           const bool masked = tok0 + kTok > it.q.L;
-          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-          if (masked) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) seen[q] = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
-          }
-          // 32 scores of the row, hidden ones at -infinity (int8: times the key's scale)
+          // 32 scores of the row (int8: times the keys' scales), hidden ones at
+          // -infinity; they are read twice, for the maximum and for the weights
           auto load32 = [&](int q, float (&s)[32]) {
             uint32_t r[32];
             tmem_ld32(t_s + 32 * q, r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(r[e]);
-            if constexpr (kS8) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const uint4 k = lds128(ksc + (32 * q + e) * 4);
-                s[e] *= __uint_as_float(k.x), s[e + 1] *= __uint_as_float(k.y);
-                s[e + 2] *= __uint_as_float(k.z), s[e + 3] *= __uint_as_float(k.w);
-              }
-            }
+            if constexpr (kS8) scale32(s, ksc + 128 * q);
             if (masked) {
+              const uint32_t seen = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!((seen[q] >> e) & 1)) s[e] = -INFINITY;
+                if (!((seen >> e) & 1)) s[e] = -INFINITY;
             }
           };
           float s[32], top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             load32(q, s);
+            float t4[4] = {top, s[0], s[1], s[2]};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+            for (int e = 3; e < 31; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
+            top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[31]);
           }
           const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
             const float next = move ? top : m;
             const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
-            l *= f;
+            l = f2_mul(l, f2_pack(f, f));
             if (i >= step) {                     // O exists: bring it to the new reference
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t r[32];
-                tmem_ld32(tlane + kColO + 128 * st + 32 * q, r);
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t r[16];
+                tmem_ld16(tlane + kColO + 128 * st + 16 * q, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                tmem_st32(tlane + kColO + 128 * st + 32 * q, r);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                tmem_st16(tlane + kColO + 128 * st + 16 * q, r);
               }
             }
             m = next;
           }
           const float mc = m == -INFINITY ? 0.f : m * c;
-#pragma unroll
+          const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+          uint64_t l2 = 0;
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             load32(q, s);
             uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s[e] = exp2_approx(fmaf(s[e], c, -mc));
-              l += s[e];
+            for (int e = 0; e < 32; e += 2) {
+              f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
+              s[e] = exp2_approx(s[e]);
+              s[e + 1] = exp2_approx(s[e + 1]);
+              if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
+              else l = f2_add(l, f2_pack(s[e], s[e + 1]));
             }
             if constexpr (kS8) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const uint4 v = lds128(ksc + kTok * 4 + (32 * q + e) * 4);
-                s[e] *= __uint_as_float(v.x), s[e + 1] *= __uint_as_float(v.y);
-                s[e + 2] *= __uint_as_float(v.z), s[e + 3] *= __uint_as_float(v.w);
-              }
-              if (masked) {                      // a hidden token's scale may not be a number
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((seen[q] >> e) & 1)) s[e] = 0.f;
-              }
+              // a hidden token's value scale may not be a number: its weight is 0 all the same
+              scale32(s, ksc + kTok * 4 + 128 * q, masked);
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = bf16_pair(s[2 * e], s[2 * e + 1]);
-            if (low) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                p[e] = bf16_pair(s[2 * e] - bf16lo_to_f32(p[e]), s[2 * e + 1] - bf16hi_to_f32(p[e]));
+            for (int e = 0; e < 16; ++e) {
+              p[e] = bf16_pair(s[2 * e], s[2 * e + 1]);
+              if (low) p[e] = bf16_pair(s[2 * e] - bf16lo_to_f32(p[e]), s[2 * e + 1] - bf16hi_to_f32(p[e]));
             }
             tmem_st16(t_s + 16 * q, p);          // over columns whose scores have been read
           }
+          l = f2_add(l, l2);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -532,10 +567,12 @@ QMM_DEV int4 row_warps(const Ctx& x) {
     if (own_tiles) {
       if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
     }
-    float f[2] = {1.f, 1.f}, top = m, sum = l;   // each stream's factor; maximum and sum of the row
+    float l_lo, l_hi;
+    f2_unpack(l, l_lo, l_hi);
+    float f[2] = {1.f, 1.f}, top = m, sum = l_lo + l_hi;   // each stream's factor; maximum and sum of the row
     if constexpr (kRT == 1) {
       x.sh->m[st][trow] = m;
-      x.sh->l[st][trow] = l;
+      x.sh->l[st][trow] = sum;
       if (!sync8()) return owned;                // both streams' O and sums are there
       top = fmaxf(x.sh->m[0][rr], x.sh->m[1][rr]);
       sum = 0.f;
@@ -550,79 +587,79 @@ QMM_DEV int4 row_warps(const Ctx& x) {
     }
     tc_fence_after();
     const bool bad = !kS8 && x.sh->bad[seq & 15] != 0;
-    // chunks of 32 columns of O, of both streams with kRT == 1 (each takes half of the columns)
+    // 16 columns of O at a time, of both streams with kRT == 1 (each takes half
+    // of the columns).  Loops, not straight code: it runs once per item, and
+    // fetching instructions would cost more than running them.
     constexpr int kCols = kRT == 1 ? D / 2 : D;
     const int d_first = kRT == 1 ? st * kCols : 0;
-    float* lows = reinterpret_cast<float*>(x.smem);   // [64][D + 4]: the low rows' part, over the query tile
-    constexpr int kLowPitch = D;
-    auto load_o = [&](int d, float (&o)[32]) {
-      uint32_t r[32];
+    // [64][D]: the low rows' part, over the query tile; 16-byte piece p of row t at p ^ (t & 7)
+    float4* lows = reinterpret_cast<float4*>(x.smem) + (trow & 63) * (D / 4);
+    auto load_o = [&](int d, float (&o)[16]) {
+      uint32_t r[16];
       if constexpr (kRT == 1) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (k >= it.seg) continue;             // stream 1 had no tile
-          tmem_ld32(tlane + kColO + 128 * k + d, r);
+          tmem_ld16(tlane + kColO + 128 * k + d, r);
           tmem_wait_ld();
           if (f[k] != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f[k], o[e]);
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(r[e]), f[k], o[e]);
           }
         }
       } else {
-        tmem_ld32(tlane + kColO + 128 * st + d, r);
+        tmem_ld16(tlane + kColO + 128 * st + d, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]);
+        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(r[e]);
       }
     };
     if (split) {
       if (quarter >= 2 && active) {
-        for (int d = d_first; d < d_first + kCols; d += 32) {
-          float o[32];
+#pragma unroll 1
+        for (int d = d_first; d < d_first + kCols; d += 16) {
+          float o[16];
           load_o(d, o);
-          // 16-byte pieces rotated by the row: the lanes of a phase on different banks
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int at = d / 4 + ((e + trow) & 7);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (((e + trow) & 7) == k) v = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            reinterpret_cast<float4*>(lows + (trow - 64) * kLowPitch)[at] = v;
-          }
+          for (int e = 0; e < 4; ++e)
+            lows[(d / 4 + e) ^ (trow & 7)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (!sync8()) return owned;
     }
     if (active && has && !(split && quarter >= 2)) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
+      const float inv = !it.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
       const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kv0 > 0 ? 0 : 1)) * (128 * kRT) + rr;
-      __nv_bfloat16* out = live ? attn_out_row(a, it.q, it.h, row) : nullptr;
-      for (int d = d_first; d < d_first + kCols; d += 32) {
-        float o[32];
+      __nv_bfloat16* out = live ? attn_out_row(a, it.q.first, it.h, row) : nullptr;
+#pragma unroll 1
+      for (int d = d_first; d < d_first + kCols; d += 16) {
+        float o[16];
         load_o(d, o);
-        if (!live) continue;
-        if (split) {
+        if (live) {
+          if (split) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v = reinterpret_cast<const float4*>(lows + trow * kLowPitch)[d / 4 + e];
-            o[4 * e] += v.x, o[4 * e + 1] += v.y, o[4 * e + 2] += v.z, o[4 * e + 3] += v.w;
+            for (int e = 0; e < 4; ++e) {
+              const float4 v = lows[(d / 4 + e) ^ (trow & 7)];
+              o[4 * e] += v.x, o[4 * e + 1] += v.y, o[4 * e + 2] += v.z, o[4 * e + 3] += v.w;
+            }
+          }
+          if (bad) attn_add_nonfinite(a, it, kTok, node, d, o);
+          if (it.whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(out + d + e) =
+                  make_uint4(bf16_pair(o[e] * inv, o[e + 1] * inv), bf16_pair(o[e + 2] * inv, o[e + 3] * inv),
+                             bf16_pair(o[e + 4] * inv, o[e + 5] * inv), bf16_pair(o[e + 6] * inv, o[e + 7] * inv));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(a.part_o + slot * D + d + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
-        if (bad) attn_add_nonfinite(a, it, kTok, node, d, o);
-        if (it.whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(out + d + e) =
-                make_uint4(bf16_pair(o[e] * inv, o[e + 1] * inv), bf16_pair(o[e + 2] * inv, o[e + 3] * inv),
-                           bf16_pair(o[e + 4] * inv, o[e + 5] * inv), bf16_pair(o[e + 6] * inv, o[e + 7] * inv));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(a.part_o + slot * D + d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
+        __syncwarp();
       }
       if (live && !it.whole && d_first == 0) a.part_ml[slot] = make_float2(top == -INFINITY ? top : top * c, sum);
     }
@@ -684,9 +721,13 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Ctx x{a, &sh, smem, sh.tmem, {}, box};
-  int4 owned = make_int4(0, 0, 0, 0);
-  if (attn_find_work<G::kThreads>(a, 128 * kRT, kTok, &sh.find, x.w)) {
+  Ctx x{a, &sh, smem, sh.tmem, box};
+  AttnOwned owned{};
+  AttnWork work;
+  const bool any = attn_find_work<G::kThreads>(a, 128 * kRT, kTok, &sh.find, work);
+  if (threadIdx.x == 0) sh.work = work;
+  __syncthreads();
+  if (any) {
     if (warp == 0) {
       load_warp<D, kS8, kRT>(x, mk, mv);
     } else if (warp == 1) {
@@ -700,7 +741,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     }
     __syncwarp();
   }
-  if (warp == 4 && lane == 0) a.desc[blockIdx.x] = owned;
+  if (warp == 4 && lane == 0) attn_post_owned(a, owned);
   // ---- teardown ----
   tc_fence_before();
   __syncthreads();
@@ -715,8 +756,8 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     else drain(b.tail_full, G::kSlots);
   }
   if (warp == 1) {
-    if (lane == 0) {
-      umma_commit(&b.done);                      // every product has completed before TMEM is freed
+    if (sh.abort && lane == 0) {                 // else every product has been waited for
+      umma_commit(&b.done);
       mbar_drain(&b.done, 0, 100000000ull);
     }
     __syncwarp();

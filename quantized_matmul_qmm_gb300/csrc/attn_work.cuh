@@ -4,9 +4,11 @@
 // key head are row = i * group + e for new token i and query head e of the
 // head's group.  An item's unit is one tile of `tile_tokens` cached tokens.
 // Units are numbered request by request, then head, row tile and cached tile;
-// block b of G gets units [b U / G, (b + 1) U / G), whatever the lengths, so
-// the load is even without the host knowing them.  An item cut by a block
-// boundary leaves partial results, which the combine kernel joins.
+// each block gets the same number of consecutive units (to one), whatever the
+// lengths, so the load is even without the host knowing them.  An item cut by
+// a block boundary leaves partial results, which the combine kernel joins.
+// Unit numbers are 32-bit, so that the few divisions on a block's way to its
+// first load are short.
 #pragma once
 
 #include "kv_cache.h"
@@ -16,7 +18,7 @@ namespace qmm {
 struct AttnReq {
   int L, n, first;   // cached tokens, new tokens, row of the first new token in q
   int row_tiles, kv_tiles;
-  int64_t units;     // 0: nothing to do
+  int units;         // 0: nothing to do
 };
 
 // Lengths that do not fit the call's buffers give no units, and the status.
@@ -24,8 +26,7 @@ QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_t
   AttnReq q{};
   const int L = a.ctx[r], c0 = a.cu[r], c1 = a.cu[r + 1];
   const int64_t n = (int64_t)c1 - c0, len = (int64_t)L + n;
-  if (L < 0 || c0 < 0 || n < 0 || c1 > a.T || n > a.max_new || len > INT32_MAX - 256 ||
-      len > a.max_blocks * (int64_t)a.cache.page_size) {
+  if (L < 0 || c0 < 0 || n < 0 || c1 > a.T || n > a.max_new || len > INT32_MAX - 256 || len > a.max_len) {
     set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     return q;
   }
@@ -34,31 +35,76 @@ QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_t
   q.first = c0;
   q.row_tiles = ((int)n * a.group + rows_per_tile - 1) / rows_per_tile;
   q.kv_tiles = ((int)len + tile_tokens - 1) / tile_tokens;
-  q.units = (int64_t)a.cache.n_heads * q.row_tiles * q.kv_tiles;
+  const int64_t units = (int64_t)a.cache.n_heads * q.row_tiles * q.kv_tiles;
+  if (units > INT32_MAX) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+  else q.units = (int)units;
   return q;
 }
 
 struct AttnWork {
-  int64_t total;     // units of the call
-  int64_t blocks;    // blocks that share them
-  int64_t u0, u1;    // this block's
-  int r;             // request of u0
-  int64_t off;       // u0's place among the request's units
+  int total, blocks;     // units of the call, and the blocks that share them
+  int per, extra;        // each block has `per` units, the first `extra` blocks one more
+  int u0, u1;            // this block's
+  int r, off;            // request of u0, and u0's place among its units
+  AttnReq q;             // that request
+  QMM_DEV int block_of(int e) const {
+    const int head = extra * (per + 1);
+    return e < head ? e / (per + 1) : extra + (e - head) / per;
+  }
 };
 
 struct AttnFindScratch {
   int64_t warp_sum[32];
-  int64_t off;
-  int r;
+  AttnReq q;
+  int r, off;
 };
+
+QMM_DEV bool attn_share(const AttnArgs& a, int64_t total, AttnWork& w) {
+  if (total > INT32_MAX) {
+    set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+    return false;
+  }
+  w.total = (int)total;
+  w.blocks = min(a.grid, w.total);
+  const int b = blockIdx.x;
+  if (b >= w.blocks) return false;
+  w.per = w.total / w.blocks;
+  w.extra = w.total - w.per * w.blocks;
+  w.u0 = b * w.per + min(b, w.extra);
+  w.u1 = w.u0 + w.per + (b < w.extra ? 1 : 0);
+  return true;
+}
 
 // All kThreads threads of the block; false (for all) when the block has none.
 template <int kThreads>
 QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_tokens, AttnFindScratch* s, AttnWork& w) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (a.R <= 32) {   // every warp for itself: one request per lane, no barrier
+    AttnReq q{};
+    if (lane < a.R) q = attn_req(a, lane, rows_per_tile, tile_tokens);
+    int64_t incl = q.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (!attn_share(a, __shfl_sync(0xffffffffu, incl, 31), w)) return false;
+    const int start = (int)incl - q.units;
+    const int at = __ffs(__ballot_sync(0xffffffffu, w.u0 >= start && w.u0 < (int)incl)) - 1;
+    w.r = at;
+    w.off = w.u0 - __shfl_sync(0xffffffffu, start, at);
+    w.q.L = __shfl_sync(0xffffffffu, q.L, at);
+    w.q.n = __shfl_sync(0xffffffffu, q.n, at);
+    w.q.first = __shfl_sync(0xffffffffu, q.first, at);
+    w.q.row_tiles = __shfl_sync(0xffffffffu, q.row_tiles, at);
+    w.q.kv_tiles = __shfl_sync(0xffffffffu, q.kv_tiles, at);
+    w.q.units = __shfl_sync(0xffffffffu, q.units, at);
+    return true;
+  }
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
   int64_t mine = 0;
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) mine += attn_req(a, r, rows_per_tile, tile_tokens).units;
   int64_t incl = mine;
 #pragma unroll
@@ -75,27 +121,25 @@ QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_token
     if (i < wid) before += v;
     total += v;
   }
-  w.total = total;
-  w.blocks = min((int64_t)a.grid, total);
-  const int64_t b = blockIdx.x;
-  if (b >= w.blocks) return false;
-  w.u0 = b * total / w.blocks;
-  w.u1 = (b + 1) * total / w.blocks;
+  if (!attn_share(a, total, w)) return false;
   int64_t start = before + incl - mine;
   if (w.u0 >= start && w.u0 < start + mine) {   // one thread's requests hold u0
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      const int64_t u = attn_req(a, r, rows_per_tile, tile_tokens).units;
-      if (w.u0 < start + u) {
+      const AttnReq q = attn_req(a, r, rows_per_tile, tile_tokens);
+      if (w.u0 < start + q.units) {
+        s->q = q;
         s->r = r;
-        s->off = w.u0 - start;
+        s->off = (int)(w.u0 - start);
         break;
       }
-      start += u;
+      start += q.units;
     }
   }
   __syncthreads();
   w.r = s->r;
   w.off = s->off;
+  w.q = s->q;
   return true;
 }
 
@@ -111,18 +155,15 @@ struct AttnItem {
 
 // Walks a block's units item by item.
 struct AttnWalk {
-  AttnWork w;
   AttnReq q;
-  int r;
-  int64_t off, u;
-  QMM_DEV void start(const AttnArgs& a, const AttnWork& work, int rows_per_tile, int tile_tokens) {
-    w = work;
+  int r, off, u;
+  QMM_DEV void start(const AttnWork& w) {
+    q = w.q;
     r = w.r;
     off = w.off;
     u = w.u0;
-    q = attn_req(a, r, rows_per_tile, tile_tokens);
   }
-  QMM_DEV bool next(const AttnArgs& a, int rows_per_tile, int tile_tokens, AttnItem& it) {
+  QMM_DEV bool next(const AttnArgs& a, const AttnWork& w, int rows_per_tile, int tile_tokens, AttnItem& it) {
     if (u >= w.u1) return false;
     while (off >= q.units) {   // to the next request that has work
       off -= q.units;
@@ -130,24 +171,36 @@ struct AttnWalk {
     }
     it.q = q;
     it.r = r;
-    it.id = (int)(off / q.kv_tiles);
-    it.kv0 = (int)(off % q.kv_tiles);
+    it.id = off / q.kv_tiles;
+    it.kv0 = off - it.id * q.kv_tiles;
     it.h = it.id / q.row_tiles;
-    it.row0 = (it.id % q.row_tiles) * rows_per_tile;
+    it.row0 = (it.id - it.h * q.row_tiles) * rows_per_tile;
     it.n_rows = min(rows_per_tile, q.n * a.group - it.row0);
-    it.seg = (int)min((int64_t)(q.kv_tiles - it.kv0), w.u1 - u);
+    it.seg = min(q.kv_tiles - it.kv0, w.u1 - u);
     it.len = q.L + q.n;
     it.whole = it.seg == q.kv_tiles;
-    it.pieces = 0;
-    if (!it.whole && it.kv0 == 0) {   // up to the block that has the item's last unit
-      const int64_t e = u + q.kv_tiles - 1;
-      it.pieces = (int)(((e + 1) * w.blocks + w.total - 1) / w.total - 1 - blockIdx.x) + 1;
-    }
+    it.pieces = 0;             // up to the block that has the item's last unit
+    if (!it.whole && it.kv0 == 0) it.pieces = w.block_of(u + q.kv_tiles - 1) - (int)blockIdx.x + 1;
     u += it.seg;
     off += it.seg;
     return true;
   }
 };
+
+// What the combine kernel is told of an item that a block begins and another
+// ends (pieces 0: nothing).  The workspace's descriptors are the numbers of
+// rows of all blocks' items, then the rest.
+struct AttnOwned {
+  int h, row0, pieces, first;
+  int n_rows;
+};
+QMM_DEV AttnOwned attn_owned(const AttnItem& it) {
+  return AttnOwned{it.h, it.row0, it.pieces, it.q.first, it.n_rows};
+}
+QMM_DEV void attn_post_owned(const AttnArgs& a, const AttnOwned& o) {
+  a.owned_rows[blockIdx.x] = o.n_rows;
+  if (o.n_rows > 0) a.owned[blockIdx.x] = make_int4(o.h, o.row0, o.pieces, o.first);
+}
 
 // Whether new token i (of the request whose first new token is row `first`)
 // sees new token j; without a mask the tokens are a chain.
@@ -228,22 +281,39 @@ QMM_DEV float attn_cached_v(const AttnArgs& a, int r, int h, int tok, int d) {
 }
 
 // The non-finite value elements of an item's new tokens (which the products
-// leave out) added to the outputs d0 .. d0 + N - 1 of a row that sees them.
+// leave out) in the outputs d0 .. d0 + n - 1 of new token i: bit e of the
+// results for +inf, -inf and NaN.  Rare: kept out of line.
+struct AttnNonfinite {
+  uint32_t pos, neg, nan;
+};
+static __device__ __noinline__ AttnNonfinite attn_nonfinite(const AttnArgs& a, int r, int h, int L, int first, int j0, int j1,
+                                                     int i, int d0, int n) {
+  AttnNonfinite f{0, 0, 0};
+  for (int j = j0; j < j1; ++j) {
+    if (!attn_sees(a, first, i, j)) continue;
+    for (int e = 0; e < n; ++e) {
+      const float v = attn_cached_v(a, r, h, L + j, d0 + e);
+      if (v == INFINITY) f.pos |= 1u << e;
+      if (v == -INFINITY) f.neg |= 1u << e;
+      if (v != v) f.nan |= 1u << e;
+    }
+  }
+  return f;
+}
 template <int N>
 QMM_DEV void attn_add_nonfinite(const AttnArgs& a, const AttnItem& it, int tile_tokens, int i, int d0, float (&x)[N]) {
-  const int j1 = min(it.len, (it.kv0 + it.seg) * tile_tokens) - it.q.L;
-  for (int j = max(0, it.kv0 * tile_tokens - it.q.L); j < j1; ++j) {
-    if (!attn_sees(a, it.q.first, i, j)) continue;
+  const int j0 = max(0, it.kv0 * tile_tokens - it.q.L), j1 = min(it.len, (it.kv0 + it.seg) * tile_tokens) - it.q.L;
+  const AttnNonfinite f = attn_nonfinite(a, it.r, it.h, it.q.L, it.q.first, j0, j1, i, d0, N);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float v = attn_cached_v(a, it.r, it.h, it.q.L + j, d0 + e);
-      if (!isfinite(v)) x[e] += v;
-    }
+  for (int e = 0; e < N; ++e) {
+    if ((f.pos >> e) & 1) x[e] += INFINITY;
+    if ((f.neg >> e) & 1) x[e] -= INFINITY;
+    if ((f.nan >> e) & 1) x[e] = NAN;
   }
 }
 
-QMM_DEV __nv_bfloat16* attn_out_row(const AttnArgs& a, const AttnReq& q, int h, int row) {
-  return a.out + (int64_t)(q.first + row / a.group) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
+QMM_DEV __nv_bfloat16* attn_out_row(const AttnArgs& a, int first, int h, int row) {
+  return a.out + (int64_t)(first + row / a.group) * a.o_st + (int64_t)(h * a.group + row % a.group) * a.o_sh;
 }
 QMM_DEV int64_t attn_q_row(const AttnArgs& a, const AttnReq& q, int h, int row) {
   return (int64_t)(q.first + row / a.group) * a.q_st + (int64_t)(h * a.group + row % a.group) * a.q_sh;

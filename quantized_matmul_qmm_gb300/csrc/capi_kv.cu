@@ -182,7 +182,7 @@ qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_
   a.q_sh = used(q_stride_head, n_q_heads);
   a.table = block_table;
   a.ld_table = ld_table;
-  a.max_blocks = max_blocks;
+  a.max_len = max_blocks > INT32_MAX / cache->page_size ? INT32_MAX : max_blocks * cache->page_size;
   a.ctx = ctx_lens;
   a.cu = cu_new;
   a.R = (int)R;

@@ -63,7 +63,7 @@ struct AttnArgs {
   KvView cache;
   const int32_t* table;      // [R][ld_table]
   int64_t ld_table;
-  int64_t max_blocks;
+  int64_t max_len;           // tokens that a table row has pages for
   const int32_t* ctx;        // [R]
   const int32_t* cu;         // [R + 1]
   int R, T, max_new;
@@ -75,7 +75,8 @@ struct AttnArgs {
   int64_t o_st, o_sh;        // elements
   float* part_o;             // workspace: [2 * grid][rows][head_dim]
   float2* part_ml;           // workspace: [2 * grid][rows]: running maximum (log2 domain) and sum
-  int4* desc;                // workspace: [grid]: request, head and row tile, segments, unused
+  int4* owned;               // workspace: [grid]: items that a block begins and another ends
+  int* owned_rows;           // workspace: [grid]: their rows, 0 for none
   int grid;
   int32_t* dev_status;
 };
