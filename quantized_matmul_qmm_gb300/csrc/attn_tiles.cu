@@ -83,13 +83,13 @@ struct TShared {
   int abort;
 };
 
-constexpr int kColS = 0, kColO = 256;            // stream st: + 128 * st
+// TMEM columns (the block allocates all 512, which begin at column 0); stream st: + 128 * st
+constexpr int kColS = 0, kColO = 256;
 
 struct Ctx {
   const AttnArgs& a;
   TShared* sh;
   uint8_t* smem;
-  uint32_t tmem;
   uint32_t box;                                  // tokens of a TMA box
   // The first tries suspend the thread until the phase completes; only then
   // does the wait read the clock for its limit (the read itself takes long).
@@ -304,43 +304,42 @@ QMM_DEV void clean_warps(const Ctx& x) {
   }
 }
 
-// ---- warp 1, one thread: the products ----
+// ---- warp 1: the products ----
+// The warp runs in step and one lane issues: operands that only the issuing
+// lane held would each be moved to a uniform register first, and 16 or 32
+// products per tile (64 to 80 cycles each) leave no time for that.
 template <int D, bool kS8, int kRT>
-QMM_DEV void mma_thread(const Ctx& x) {
+QMM_DEV void mma_warp(const Ctx& x) {
   using G = Tg<D, kS8, kRT>;
   const AttnArgs& a = x.a;
   TBars& b = x.sh->bar;
   constexpr uint32_t kIdS = idesc_f16(128, kTok, true), kIdO = idesc_f16(128, D, true) | kIdescBMnMajor;
   const uint32_t q_s = smem_u32(x.smem), slots = q_s + G::kOffSlots;
-  uint32_t slot = 0, phase = 0, seq = 0, p_count[2] = {0, 0};
+  const uint32_t one = elect_one();
+  uint32_t slot = 0, phase = 0, seq = 0, p_phase[2] = {0, 0};
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    if (!x.wait(&b.q_full, seq & 1)) return;
+    if (!x.wait_all(&b.q_full, seq & 1)) return;
     const bool both = kRT == 2 && it.n_rows > 128;   // both streams on every tile
     auto scores = [&](int st, uint32_t tile) {
       // the address fields do not carry past their 14 bits: shared memory ends below 2^18
-      uint64_t q_desc = desc_kmajor_sw128(q_s + (kRT == 2 ? st * G::kTile : 0)), k_desc = desc_kmajor_sw128(tile);
-      const uint32_t d = x.tmem + kColS + 128 * st;
-#pragma unroll 2
+      const uint64_t q_desc = desc_kmajor_sw128(q_s + (kRT == 2 ? st * G::kTile : 0)), k_desc = desc_kmajor_sw128(tile);
+#pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        umma_f16(d, q_desc, k_desc, kIdS, k > 0);
-        const uint32_t step = (k & 3) == 3 ? (kHalf - 96) >> 4 : 32 >> 4;   // the next 16 dimensions
-        q_desc += step;
-        k_desc += step;
+        const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+        umma_f16_one(one, kColS + 128 * st, q_desc + at, k_desc + at, kIdS, k > 0);
       }
-      umma_commit(&b.s_full[st]);
+      umma_commit_one(one, &b.s_full[st]);
     };
     auto values = [&](int st, uint32_t tile, bool first, bool last) {
-      uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
-      const uint32_t d = x.tmem + kColO + 128 * st, p = x.tmem + kColS + 128 * st;
-#pragma unroll 2
-      for (int k = 0; k < kTok / 16; ++k) {
-        umma_f16_ta(d, p + 8 * k, v_desc, kIdO, !(first && k == 0));
-        v_desc += 2048 >> 4;
-      }
-      if (last) umma_commit(&b.o_done[st]);
+      const uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
+#pragma unroll
+      for (int k = 0; k < kTok / 16; ++k)
+        umma_f16_ta_one(one, kColO + 128 * st, kColS + 128 * st + 8 * k, v_desc + k * (2048 >> 4), kIdO,
+                        k > 0 || !first);
+      if (last) umma_commit_one(one, &b.o_done[st]);
     };
     uint32_t v_tile = 0;
     int v_slot = 0, v_i = 0;
@@ -358,10 +357,11 @@ QMM_DEV void mma_thread(const Ctx& x) {
       const uint32_t tile = slots + slot * G::kTile;
       if (more) {
         if (value) {
-          if (!x.wait(&b.p_ready[st], p_count[st]++ & 1)) return;
+          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return;
+          p_phase[st] ^= 1;
           if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return;
         }
-        if (!x.wait(&b.full[slot], phase)) return;
+        if (!x.wait_all(&b.full[slot], phase)) return;
         tc_fence_after();
         if (value) {
           values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg);
@@ -374,15 +374,16 @@ QMM_DEV void mma_thread(const Ctx& x) {
         }
       }
       if (kRT == 2 && v_open && (!more || !value || i == it.seg - 1)) {
-        if (!x.wait(&b.p_ready[1], p_count[1]++ & 1)) return;
+        if (!x.wait_all(&b.p_ready[1], p_phase[1])) return;
+        p_phase[1] ^= 1;
         tc_fence_after();
         values(1, v_tile, v_i == 0, v_i == it.seg - 1);
-        umma_commit(&b.empty[v_slot]);
+        umma_commit_one(one, &b.empty[v_slot]);
         v_open = false;
       }
       if (!more) break;
       if (!value && both) scores(1, tile);
-      if (!value || !both) umma_commit(&b.empty[slot]);
+      if (!value || !both) umma_commit_one(one, &b.empty[slot]);
       if (++slot == G::kSlots) slot = 0, phase ^= 1;
     }
   }
@@ -414,7 +415,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int st = (wid - 4) >> 2, quarter = wid & 3;
   const int trow = 32 * quarter + lane;          // lane of TMEM, row of the tile
-  const uint32_t tlane = x.tmem + ((uint32_t)(32 * quarter) << 16);
+  const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
   const uint32_t t_s = tlane + kColS + 128 * st;
   const float c = a.scale_log2, slack = 8.f / c;
   AttnOwned owned{};
@@ -721,7 +722,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Ctx x{a, &sh, smem, sh.tmem, box};
+  Ctx x{a, &sh, smem, box};
   AttnOwned owned{};
   AttnWork work;
   const bool any = attn_find_work<G::kThreads>(a, 128 * kRT, kTok, &sh.find, work);
@@ -731,7 +732,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     if (warp == 0) {
       load_warp<D, kS8, kRT>(x, mk, mv);
     } else if (warp == 1) {
-      if (lane == 0) mma_thread<D, kS8, kRT>(x);
+      mma_warp<D, kS8, kRT>(x);
     } else if (warp < 4) {
       if constexpr (!kS8) clean_warps<D, kRT>(x);
     } else if (warp < 12) {
