@@ -55,7 +55,8 @@ struct Tg {
   static constexpr int kRaw = kTok * D;          // bytes of a tile of codes
   static constexpr int kSlots = D == 64 ? (kS8 ? 6 : 8) : kS8 ? 3 : (kRT == 1 ? 6 : 5);
   static constexpr int kRawSlots = !kS8 ? 0 : D == 64 ? 8 : (kRT == 1 ? 5 : 3);
-  static constexpr int kThreads = kS8 ? 512 : 384;
+  static constexpr int kConvWarps = kS8 ? 8 : 0;
+  static constexpr int kThreads = 384 + 32 * kConvWarps;
   static constexpr int kOffSlots = kRT * kTile;
   static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
   static constexpr int kOffScale = kOffRaw + kRawSlots * kRaw;
@@ -68,7 +69,7 @@ struct TBars {
   uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2];
   uint64_t q_full, o_free, sync;
   uint64_t done;
 };
@@ -213,36 +214,44 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
   }
 }
 
-// ---- int8: four warps write codes out as bf16 ----
+// ---- int8: eight warps write codes out as bf16 ----
+// Four codes of a word leave in the order 0, 2, 1, 3, which costs no byte
+// permutes: the query tile has its dimensions in the same order, and the
+// outputs' columns are put right at the end.  About 30 instructions per 16
+// codes; four warps took 1.6 us per tile of keys and values, twice what the
+// codes take from HBM.
+QMM_DEV uint4 s8x8_to_bf16(uint32_t w0, uint32_t w1) {
+  return make_uint4(s8_lanes_to_bf16(w0), s8_lanes_to_bf16(w0 >> 8), s8_lanes_to_bf16(w1), s8_lanes_to_bf16(w1 >> 8));
+}
+
 template <int D, int kRT>
 QMM_DEV void convert_warps(const Ctx& x) {
   using G = Tg<D, true, kRT>;
   const AttnArgs& a = x.a;
-  const int lane = threadIdx.x & 31, tid = threadIdx.x & 127;
-  constexpr int kPieces = D / 16;                // 16-code pieces of a row
-  uint32_t n = 0;
+  constexpr int kThr = 32 * G::kConvWarps, kPieces = D / 16;   // 16-code pieces of a row
+  constexpr int kRows = kThr / kPieces;          // rows of a pass: a multiple of 8, so one swizzle for all
+  const int lane = threadIdx.x & 31, tid = threadIdx.x - 384, row = tid / kPieces, p = tid % kPieces;
+  // the second half's lanes store their odd 16 bytes first: no two lanes of a phase on one bank
+  const uint32_t line = (p >> 2) * kHalf + row * 128, u = (p & 3) * 2, odd = p >> 2 & 1;
+  const uint32_t src = smem_u32(x.smem) + G::kOffRaw + tid * 16;
+  const uint32_t dst1 = smem_u32(x.smem) + G::kOffSlots + line + (((u + odd) ^ (row & 7)) << 4);
+  const uint32_t dst2 = smem_u32(x.smem) + G::kOffSlots + line + (((u + 1 - odd) ^ (row & 7)) << 4);
+  uint32_t rs = 0, r_phase = 0, cs = 0, c_phase = 1;
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   while (walk.next(a, x.sh->work, 128 * kRT, kTok, it)) {
-    for (int i = 0; i < 2 * it.seg; ++i, ++n) {
-      const int rs = n % G::kRawSlots, cs = n % G::kSlots;
-      if (!x.wait_all(&x.sh->bar.raw_full[rs], (n / G::kRawSlots) & 1)) return;
-      if (!x.wait_all(&x.sh->bar.empty[cs], ((n / G::kSlots) & 1) ^ 1)) return;
-      const uint32_t src = smem_u32(x.smem) + G::kOffRaw + rs * G::kRaw;
-      const uint32_t dst = smem_u32(x.smem) + G::kOffSlots + cs * G::kTile;
-#pragma unroll 4
-      for (int k = 0; k < kPieces; ++k) {
-        const int id = tid + 128 * k, row = id / kPieces, p = id % kPieces;
-        const uint4 c = lds128(src + id * 16);
-        const uint4 lo = make_uint4(s8_low_pair(c.x), s8_high_pair(c.x), s8_low_pair(c.y), s8_high_pair(c.y));
-        const uint4 hi = make_uint4(s8_low_pair(c.z), s8_high_pair(c.z), s8_low_pair(c.w), s8_high_pair(c.w));
-        const uint32_t line = dst + (p >> 2) * kHalf + row * 128;
-        const int u = (p & 3) * 2;
-        // the second half's lanes store their odd 16 bytes first: no two lanes of a phase on one bank
-        const bool swap = p >= 4;
-        sts128(line + (((u + (swap ? 1 : 0)) ^ (row & 7)) << 4), swap ? hi : lo);
-        sts128(line + (((u + (swap ? 0 : 1)) ^ (row & 7)) << 4), swap ? lo : hi);
+#pragma unroll 1
+    for (int i = 0; i < 2 * it.seg; ++i) {
+      if (!x.wait_all(&x.sh->bar.raw_full[rs], r_phase)) return;
+      if (!x.wait_all(&x.sh->bar.empty[cs], c_phase)) return;
+#pragma unroll
+      for (int k = 0; k < kTok / kRows; ++k) {
+        const uint4 c = lds128(src + rs * G::kRaw + k * kThr * 16);
+        const uint4 lo = s8x8_to_bf16(c.x, c.y), hi = s8x8_to_bf16(c.z, c.w);
+        const uint32_t at = cs * G::kTile + k * kRows * 128;
+        sts128(dst1 + at, odd ? hi : lo);
+        sts128(dst2 + at, odd ? lo : hi);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -250,6 +259,8 @@ QMM_DEV void convert_warps(const Ctx& x) {
         mbar_arrive(&x.sh->bar.full[cs]);
         mbar_arrive(&x.sh->bar.raw_empty[rs]);
       }
+      if (++rs == G::kRawSlots) rs = 0, r_phase ^= 1;
+      if (++cs == G::kSlots) cs = 0, c_phase ^= 1;
     }
   }
 }
@@ -333,13 +344,21 @@ QMM_DEV void mma_warp(const Ctx& x) {
       }
       umma_commit_one(one, &b.s_full[st]);
     };
+    // the products with the first 64 tokens begin while the other weights are made
     auto values = [&](int st, uint32_t tile, bool first, bool last) {
       const uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
 #pragma unroll
-      for (int k = 0; k < kTok / 16; ++k)
+      for (int k = 0; k < kTok / 16; ++k) {
+        if (k == kTok / 32) {
+          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return false;
+          p_phase[st] ^= 1;
+          tc_fence_after();
+        }
         umma_f16_ta_one(one, kColO + 128 * st, kColS + 128 * st + 8 * k, v_desc + k * (2048 >> 4), kIdO,
                         k > 0 || !first);
+      }
       if (last) umma_commit_one(one, &b.o_done[st]);
+      return true;
     };
     uint32_t v_tile = 0;
     int v_slot = 0, v_i = 0;
@@ -357,14 +376,13 @@ QMM_DEV void mma_warp(const Ctx& x) {
       const uint32_t tile = slots + slot * G::kTile;
       if (more) {
         if (value) {
-          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return;
-          p_phase[st] ^= 1;
+          if (!x.wait_all(&b.p_half[st], p_phase[st])) return;
           if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return;
         }
         if (!x.wait_all(&b.full[slot], phase)) return;
         tc_fence_after();
         if (value) {
-          values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg);
+          if (!values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg)) return;
           v_tile = tile;
           v_slot = slot;
           v_i = i;
@@ -374,10 +392,9 @@ QMM_DEV void mma_warp(const Ctx& x) {
         }
       }
       if (kRT == 2 && v_open && (!more || !value || i == it.seg - 1)) {
-        if (!x.wait_all(&b.p_ready[1], p_phase[1])) return;
-        p_phase[1] ^= 1;
+        if (!x.wait_all(&b.p_half[1], p_phase[1])) return;
         tc_fence_after();
-        values(1, v_tile, v_i == 0, v_i == it.seg - 1);
+        if (!values(1, v_tile, v_i == 0, v_i == it.seg - 1)) return;
         umma_commit_one(one, &b.empty[v_slot]);
         v_open = false;
       }
@@ -390,11 +407,12 @@ QMM_DEV void mma_warp(const Ctx& x) {
 }
 
 // ---- warps 4..11: the rows ----
-// s[e] *= the e-th of 32 fp32 values in shared memory; with `guard`, zeros stay
+// s[e] *= the e-th of kN fp32 values in shared memory; with `guard`, zeros stay
 // zeros whatever they meet.
-QMM_DEV void scale32(float (&s)[32], uint32_t addr, bool guard = false) {
+template <int kN>
+QMM_DEV void scale_by(float (&s)[kN], uint32_t addr, bool guard = false) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 4) {
+  for (int e = 0; e < kN; e += 4) {
     const uint4 k = lds128(addr + e * 4);
     const float f[4] = {__uint_as_float(k.x), __uint_as_float(k.y), __uint_as_float(k.z), __uint_as_float(k.w)};
     if (guard) {
@@ -406,6 +424,11 @@ QMM_DEV void scale32(float (&s)[32], uint32_t addr, bool guard = false) {
     }
   }
 }
+
+template <int kRegs>
+QMM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+QMM_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 template <int D, bool kS8, bool kQF32, int kRT>
 QMM_DEV AttnOwned row_warps(const Ctx& x) {
@@ -454,6 +477,9 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
             v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qo + 8 * ch);
           }
         }
+        if constexpr (kS8)                       // the converters' order: 0, 2, 1, 3 of each four
+          v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                         __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
         sts128(line + (ch >> 3) * kHalf + (((ch & 7) ^ (trow & 7)) << 4), v);
       }
       fence_proxy_async_smem();
@@ -480,30 +506,38 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         if (active) {
           const int tok0 = (it.kv0 + i) * kTok;
           const bool masked = tok0 + kTok > it.q.L;
-          // 32 scores of the row (int8: times the keys' scales), hidden ones at
-          // -infinity; they are read twice, for the maximum and for the weights
-          auto load32 = [&](int q, float (&s)[32]) {
-            uint32_t r[32];
-            tmem_ld32(t_s + 32 * q, r);
+          // kW scores of the row (int8: times the keys' scales), hidden ones at
+          // -infinity.  All but the first kW are read twice, for the maximum
+          // and for the weights; the first stay in registers.
+          constexpr int kW = kS8 ? 32 : 64;      // int8: what the rows' registers hold without spills
+          float s[kW], top = -INFINITY;
+          auto load_scores = [&](int part) {
+#pragma unroll
+            for (int q = 0; q < kW / 32; ++q) {
+              uint32_t r[32];
+              tmem_ld32(t_s + kW * part + 32 * q, r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
+            }
             tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(r[e]);
-            if constexpr (kS8) scale32(s, ksc + 128 * q);
+            if constexpr (kS8) scale_by(s, ksc + 4 * kW * part);
             if (masked) {
-              const uint32_t seen = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((seen >> e) & 1)) s[e] = -INFINITY;
+              for (int q = 0; q < kW / 32; ++q) {
+                const uint32_t seen = live ? attn_sees32(a, it.q, node, tok0 + kW * part + 32 * q) : 0u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((seen >> e) & 1)) s[32 * q + e] = -INFINITY;
+              }
             }
           };
-          float s[32], top = -INFINITY;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            load32(q, s);
+          for (int part = kTok / kW - 1; part >= 0; --part) {
+            load_scores(part);
             float t4[4] = {top, s[0], s[1], s[2]};
 #pragma unroll
-            for (int e = 3; e < 31; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
-            top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[31]);
+            for (int e = 3; e < kW - 1; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
+            top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[kW - 1]);
           }
           const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
@@ -527,30 +561,40 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
           const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
           uint64_t l2 = 0;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            load32(q, s);
-            uint32_t p[16];
+          for (int part = 0; part < kTok / kW; ++part) {
+            if (part > 0) load_scores(part);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < kW; e += 2) {
               f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
               s[e] = exp2_approx(s[e]);
               s[e + 1] = exp2_approx(s[e + 1]);
               if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
               else l = f2_add(l, f2_pack(s[e], s[e + 1]));
             }
-            if constexpr (kS8) {
-              // a hidden token's value scale may not be a number: its weight is 0 all the same
-              scale32(s, ksc + kTok * 4 + 128 * q, masked);
-            }
+            // a hidden token's value scale may not be a number: its weight is 0 all the same
+            if constexpr (kS8) scale_by(s, ksc + kTok * 4 + 4 * kW * part, masked);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              p[e] = bf16_pair(s[2 * e], s[2 * e + 1]);
-              if (low) p[e] = bf16_pair(s[2 * e] - bf16lo_to_f32(p[e]), s[2 * e + 1] - bf16hi_to_f32(p[e]));
+            for (int q = 0; q < kW / 32; ++q) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float x0 = s[32 * q + 2 * e], x1 = s[32 * q + 2 * e + 1];
+                p[e] = bf16_pair(x0, x1);
+                if (low) p[e] = bf16_pair(x0 - bf16lo_to_f32(p[e]), x1 - bf16hi_to_f32(p[e]));
+              }
+              tmem_st16(t_s + kW / 2 * part + 16 * q, p);   // over columns whose scores have been read
             }
-            tmem_st16(t_s + 16 * q, p);          // over columns whose scores have been read
+            if (kW * (part + 1) == kTok / 2) {   // the products with the first 64 tokens may begin
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&b.p_half[st]);
+            }
           }
           l = f2_add(l, l2);
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&b.p_half[st]);
         }
         tc_fence_before();
         __syncwarp();
@@ -615,6 +659,14 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(r[e]);
+      }
+      if constexpr (kS8) {                       // columns in order again
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float t = o[e + 1];
+          o[e + 1] = o[e + 2];
+          o[e + 2] = t;
+        }
       }
     };
     if (split) {
@@ -688,13 +740,13 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   TBars& b = sh.bar;
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kSlots; ++i) {
-      mbar_init(&b.full[i], kS8 ? 4 : 1);        // converters, or the loads
+      mbar_init(&b.full[i], kS8 ? G::kConvWarps : 1);   // converters, or the loads
       mbar_init(&b.empty[i], 1);
       mbar_init(&b.tail_full[i], 1);
     }
     for (int i = 0; i < G::kRawSlots; ++i) {
       mbar_init(&b.raw_full[i], 1);
-      mbar_init(&b.raw_empty[i], 4);
+      mbar_init(&b.raw_empty[i], G::kConvWarps);
     }
     for (int i = 0; i < kScaleRing; ++i) {
       mbar_init(&b.sc_full[i], 1);
@@ -702,6 +754,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.s_full[i], 1);
+      mbar_init(&b.p_half[i], 4);
       mbar_init(&b.p_ready[i], 4);
       mbar_init(&b.o_done[i], 1);
     }
@@ -729,16 +782,24 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   if (threadIdx.x == 0) sh.work = work;
   __syncthreads();
   if (any) {
-    if (warp == 0) {
-      load_warp<D, kS8, kRT>(x, mk, mv);
-    } else if (warp == 1) {
-      mma_warp<D, kS8, kRT>(x);
-    } else if (warp < 4) {
-      if constexpr (!kS8) clean_warps<D, kRT>(x);
+    // int8: 640 threads at 96 registers; shares per warpgroup 72 + 2 * 144 + 2 * 56 = 472 <= 5 * 96
+    if (warp < 4) {
+      if constexpr (kS8) regs_dec<72>();
+      if (warp == 0) {
+        load_warp<D, kS8, kRT>(x, mk, mv);
+      } else if (warp == 1) {
+        mma_warp<D, kS8, kRT>(x);
+      } else {
+        if constexpr (!kS8) clean_warps<D, kRT>(x);
+      }
     } else if (warp < 12) {
+      if constexpr (kS8) regs_inc<144>();
       owned = row_warps<D, kS8, kQF32, kRT>(x);
     } else {
-      if constexpr (kS8) convert_warps<D, kRT>(x);
+      if constexpr (kS8) {
+        regs_dec<56>();
+        convert_warps<D, kRT>(x);
+      }
     }
     __syncwarp();
   }
