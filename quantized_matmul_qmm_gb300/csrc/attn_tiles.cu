@@ -407,20 +407,20 @@ QMM_DEV void mma_warp(const Ctx& x) {
 }
 
 // ---- warps 4..11: the rows ----
-// s[e] *= the e-th of kN fp32 values in shared memory; with `guard`, zeros stay
-// zeros whatever they meet.
+// s[e] *= f[e]; with `guard`, zeros stay zeros whatever they meet.
 template <int kN>
-QMM_DEV void scale_by(float (&s)[kN], uint32_t addr, bool guard = false) {
+QMM_DEV void scale_by(float (&s)[kN], const float4 (&f)[kN / 4], bool guard = false) {
 #pragma unroll
   for (int e = 0; e < kN; e += 4) {
-    const uint4 k = lds128(addr + e * 4);
-    const float f[4] = {__uint_as_float(k.x), __uint_as_float(k.y), __uint_as_float(k.z), __uint_as_float(k.w)};
+    const float4 k = f[e / 4];
     if (guard) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[e + j] = s[e + j] == 0.f ? 0.f : s[e + j] * f[j];
+      s[e] = s[e] == 0.f ? 0.f : s[e] * k.x;
+      s[e + 1] = s[e + 1] == 0.f ? 0.f : s[e + 1] * k.y;
+      s[e + 2] = s[e + 2] == 0.f ? 0.f : s[e + 2] * k.z;
+      s[e + 3] = s[e + 3] == 0.f ? 0.f : s[e + 3] * k.w;
     } else {
-      f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(f[0], f[1])), s[e], s[e + 1]);
-      f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(f[2], f[3])), s[e + 2], s[e + 3]);
+      f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(k.x, k.y)), s[e], s[e + 1]);
+      f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(k.z, k.w)), s[e + 2], s[e + 3]);
     }
   }
 }
@@ -458,29 +458,33 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     const int rr = kRT == 2 ? 128 * st + trow : split ? trow & 63 : trow;
     const bool live = rr < it.n_rows, active = __any_sync(0xffffffffu, live);
     const int row = it.row0 + rr, node = row / a.group;
-    // the query row (with kRT == 1 each stream's thread takes half of it)
+    // the query rows, whole rows at a time (with kRT == 1 each stream's warp
+    // takes 16 of its quarter's 32)
     {
-      constexpr int kChunks = kRT == 1 ? D / 16 : D / 8;
-      const int c0 = kRT == 1 ? st * kChunks : 0;
-      const uint32_t line = smem_u32(x.smem) + (kRT == 2 ? st * G::kTile : 0) + trow * 128;
-      const int64_t qo = live ? attn_q_row(a, it.q, it.h, row) : 0;
-#pragma unroll 4
-      for (int j = 0; j < kChunks; ++j) {
-        const int ch = c0 + j;
+      constexpr int kCh = D / 8;                 // 16-byte pieces of a bf16 row
+      constexpr int kAt = 32 / kCh;              // rows of a load
+      constexpr int kLoads = (kRT == 1 ? 16 : 32) / kAt;
+      const int ch = lane % kCh, r_first = kRT == 1 ? 16 * st : 0;
+      const int64_t qo = live ? attn_q_row(a, it.q, it.h, row) : -1;
+      const uint32_t base = smem_u32(x.smem) + (kRT == 2 ? st * G::kTile : 0) + (ch >> 3) * kHalf;
+#pragma unroll 8
+      for (int j = 0; j < kLoads; ++j) {
+        const int rl = r_first + j * kAt + lane / kCh, tr = 32 * quarter + rl;
+        const int64_t at = __shfl_sync(0xffffffffu, qo, rl);
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) {
+        if (at >= 0) {
           if constexpr (kQF32) {
-            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qo + 8 * ch);
+            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 8 * ch);
             const float4 f0 = f[0], f1 = f[1];
             v = make_uint4(bf16_pair(f0.x, f0.y), bf16_pair(f0.z, f0.w), bf16_pair(f1.x, f1.y), bf16_pair(f1.z, f1.w));
           } else {
-            v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qo + 8 * ch);
+            v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + 8 * ch);
           }
         }
         if constexpr (kS8)                       // the converters' order: 0, 2, 1, 3 of each four
           v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
                          __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-        sts128(line + (ch >> 3) * kHalf + (((ch & 7) ^ (trow & 7)) << 4), v);
+        sts128(base + tr * 128 + (((ch & 7) ^ (tr & 7)) << 4), v);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -495,10 +499,10 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     const int step = kRT == 1 ? 2 : 1;
     for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
       const uint32_t sc = (tiles + i) % kScaleRing;
-      uint32_t ksc = 0;
+      const float4* ksc = nullptr;               // the tile's 128 key scales, then its value scales
       if constexpr (kS8) {
         if (!x.wait_all(&b.sc_full[sc], ((tiles + i) / kScaleRing) & 1)) return owned;
-        ksc = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4);
+        ksc = reinterpret_cast<const float4*>(x.smem + G::kOffScale + sc * (2 * kTok * 4));
       }
       if (has) {
         if (!x.wait_all(&b.s_full[st], s_count++ & 1)) return owned;
@@ -512,6 +516,11 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
           constexpr int kW = kS8 ? 32 : 64;      // int8: what the rows' registers hold without spills
           float s[kW], top = -INFINITY;
           auto load_scores = [&](int part) {
+            float4 ks[kS8 ? kW / 4 : 1];
+            if constexpr (kS8) {
+#pragma unroll
+              for (int e = 0; e < kW / 4; ++e) ks[e] = ksc[kW / 4 * part + e];
+            }
 #pragma unroll
             for (int q = 0; q < kW / 32; ++q) {
               uint32_t r[32];
@@ -520,7 +529,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
               for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
             }
             tmem_wait_ld();
-            if constexpr (kS8) scale_by(s, ksc + 4 * kW * part);
+            if constexpr (kS8) scale_by(s, ks);
             if (masked) {
 #pragma unroll
               for (int q = 0; q < kW / 32; ++q) {
@@ -563,6 +572,11 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
 #pragma unroll 1
           for (int part = 0; part < kTok / kW; ++part) {
             if (part > 0) load_scores(part);
+            float4 vs[kS8 ? kW / 4 : 1];
+            if constexpr (kS8) {
+#pragma unroll
+              for (int e = 0; e < kW / 4; ++e) vs[e] = ksc[kTok / 4 + kW / 4 * part + e];
+            }
 #pragma unroll
             for (int e = 0; e < kW; e += 2) {
               f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
@@ -572,7 +586,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
               else l = f2_add(l, f2_pack(s[e], s[e + 1]));
             }
             // a hidden token's value scale may not be a number: its weight is 0 all the same
-            if constexpr (kS8) scale_by(s, ksc + kTok * 4 + 4 * kW * part, masked);
+            if constexpr (kS8) scale_by(s, vs, masked);
 #pragma unroll
             for (int q = 0; q < kW / 32; ++q) {
               uint32_t p[16];
@@ -685,34 +699,44 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     if (active && has && !(split && quarter >= 2)) {
       const float inv = !it.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
       const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kv0 > 0 ? 0 : 1)) * (128 * kRT) + rr;
-      __nv_bfloat16* out = live ? attn_out_row(a, it.q.first, it.h, row) : nullptr;
+      // Rows go out through shared memory, four lanes a row (a store of one
+      // 16-byte piece of 32 rows takes eight times as long): over the warp's
+      // own rows of the query tile, or (split) in place of the low parts.
+      float4* stage = reinterpret_cast<float4*>(x.smem + (kRT == 2 ? st * G::kTile : st * 2048) + quarter * 4096);
+      auto piece = [&](int r, int d, int e) -> float4& {
+        return split ? reinterpret_cast<float4*>(x.smem)[(32 * quarter + r) * (D / 4) + ((d / 4 + e) ^ (r & 7))]
+                     : stage[r * 4 + (e ^ ((r >> 1) & 3))];
+      };
+      const int64_t to = !live ? -1 : it.whole ? attn_out_row(a, it.q.first, it.h, row) - a.out : slot * D;
 #pragma unroll 1
       for (int d = d_first; d < d_first + kCols; d += 16) {
         float o[16];
         load_o(d, o);
-        if (live) {
-          if (split) {
+        if (split) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 v = lows[(d / 4 + e) ^ (trow & 7)];
-              o[4 * e] += v.x, o[4 * e + 1] += v.y, o[4 * e + 2] += v.z, o[4 * e + 3] += v.w;
-            }
-          }
-          if (bad) attn_add_nonfinite(a, it, kTok, node, d, o);
-          if (it.whole) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              *reinterpret_cast<uint4*>(out + d + e) =
-                  make_uint4(bf16_pair(o[e] * inv, o[e + 1] * inv), bf16_pair(o[e + 2] * inv, o[e + 3] * inv),
-                             bf16_pair(o[e + 4] * inv, o[e + 5] * inv), bf16_pair(o[e + 6] * inv, o[e + 7] * inv));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(a.part_o + slot * D + d + e) =
-                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = piece(lane, d, e);
+            o[4 * e] += v.x, o[4 * e + 1] += v.y, o[4 * e + 2] += v.z, o[4 * e + 3] += v.w;
           }
         }
+        if (bad && live) attn_add_nonfinite(a, it, kTok, node, d, o);
         __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          piece(lane, d, e) = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 8 * j + (lane >> 2), e = lane & 3;
+          const int64_t at = __shfl_sync(0xffffffffu, to, r);
+          const float4 v = piece(r, d, e);
+          if (at >= 0) {
+            if (it.whole)
+              *reinterpret_cast<uint2*>(a.out + at + d + 4 * e) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+            else
+              *reinterpret_cast<float4*>(a.part_o + at + d + 4 * e) = v;
+          }
+        }
       }
       if (live && !it.whole && d_first == 0) a.part_ml[slot] = make_float2(top == -INFINITY ? top : top * c, sum);
     }
