@@ -268,6 +268,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
         }
         const bool masked = tok0 + kGroup > L;   // the group holds new tokens, or ends the request
         uint32_t seen[MT];                       // bit nt * 4 + e
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) seen[mt] = 0xFFu;
         if (masked) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -322,11 +324,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
               float p0 = exp2_approx(s[mt][nt][2 * hf] - m_use), p1 = exp2_approx(s[mt][nt][2 * hf + 1] - m_use);
               l[mt][hf] += p0 + p1;
               if constexpr (kS8) {
-                p0 *= vs[nt][0], p1 *= vs[nt][1];
-                if (masked) {                    // a hidden token's scale may not be a number
-                  if (!(seen[mt] >> (nt * 4 + 2 * hf) & 1)) p0 = 0.f;
-                  if (!(seen[mt] >> (nt * 4 + 2 * hf + 1) & 1)) p1 = 0.f;
-                }
+                // a hidden token's scale may not be a number
+                p0 = (seen[mt] >> (nt * 4 + 2 * hf)) & 1 ? p0 * vs[nt][0] : 0.f;
+                p1 = (seen[mt] >> (nt * 4 + 2 * hf + 1)) & 1 ? p1 * vs[nt][1] : 0.f;
               }
               const uint32_t hi = bf16_pair(p0, p1);
               pf[mt][2 * nt + hf] = hi;

@@ -407,21 +407,24 @@ QMM_DEV void mma_warp(const Ctx& x) {
 }
 
 // ---- warps 4..11: the rows ----
-// s[e] *= f[e]; with `guard`, zeros stay zeros whatever they meet.
+// Zeros for the non-finite ones of four scales from number `from` on.
+QMM_DEV bool drop_nonfinite(float4& f, int from) {
+  bool hit = false;
+  if (from <= 0 && !isfinite(f.x)) f.x = 0.f, hit = true;
+  if (from <= 1 && !isfinite(f.y)) f.y = 0.f, hit = true;
+  if (from <= 2 && !isfinite(f.z)) f.z = 0.f, hit = true;
+  if (from <= 3 && !isfinite(f.w)) f.w = 0.f, hit = true;
+  return hit;
+}
+
+// s[e] *= f[e]
 template <int kN>
-QMM_DEV void scale_by(float (&s)[kN], const float4 (&f)[kN / 4], bool guard = false) {
+QMM_DEV void scale_by(float (&s)[kN], const float4 (&f)[kN / 4]) {
 #pragma unroll
   for (int e = 0; e < kN; e += 4) {
     const float4 k = f[e / 4];
-    if (guard) {
-      s[e] = s[e] == 0.f ? 0.f : s[e] * k.x;
-      s[e + 1] = s[e + 1] == 0.f ? 0.f : s[e + 1] * k.y;
-      s[e + 2] = s[e + 2] == 0.f ? 0.f : s[e + 2] * k.z;
-      s[e + 3] = s[e + 3] == 0.f ? 0.f : s[e + 3] * k.w;
-    } else {
-      f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(k.x, k.y)), s[e], s[e + 1]);
-      f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(k.z, k.w)), s[e + 2], s[e + 3]);
-    }
+    f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(k.x, k.y)), s[e], s[e + 1]);
+    f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(k.z, k.w)), s[e + 2], s[e + 3]);
   }
 }
 
@@ -496,6 +499,8 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     float m = -INFINITY;                         // the reference, before the scale
     uint64_t l = 0;                              // sum, in two halves
     const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
+    bool found = false;                          // int8: a scale was left out
+    if (kS8 && wid == 4 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
     const int step = kRT == 1 ? 2 : 1;
     for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
       const uint32_t sc = (tiles + i) % kScaleRing;
@@ -576,6 +581,12 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
             if constexpr (kS8) {
 #pragma unroll
               for (int e = 0; e < kW / 4; ++e) vs[e] = ksc[kTok / 4 + kW / 4 * part + e];
+              // a new token's value scale that is not finite: 0 here, and the
+              // rows that see it get theirs at the end, as for a bf16 cache
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < kW / 4; ++e) found |= drop_nonfinite(vs[e], it.q.L - tok0 - kW * part - 4 * e);
+              }
             }
 #pragma unroll
             for (int e = 0; e < kW; e += 2) {
@@ -585,8 +596,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
               if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
               else l = f2_add(l, f2_pack(s[e], s[e + 1]));
             }
-            // a hidden token's value scale may not be a number: its weight is 0 all the same
-            if constexpr (kS8) scale_by(s, vs, masked);
+            if constexpr (kS8) scale_by(s, vs);
 #pragma unroll
             for (int q = 0; q < kW / 32; ++q) {
               uint32_t p[16];
@@ -626,6 +636,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     if (own_tiles) {
       if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
     }
+    if (kS8 && found) atomicOr(&x.sh->bad[seq & 15], 1);
     float l_lo, l_hi;
     f2_unpack(l, l_lo, l_hi);
     float f[2] = {1.f, 1.f}, top = m, sum = l_lo + l_hi;   // each stream's factor; maximum and sum of the row
@@ -645,7 +656,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       }
     }
     tc_fence_after();
-    const bool bad = !kS8 && x.sh->bad[seq & 15] != 0;
+    const bool bad = x.sh->bad[seq & 15] != 0;   // kRT == 2, int8: this warp's own finding at least
     // 16 columns of O at a time, of both streams with kRT == 1 (each takes half
     // of the columns).  Loops, not straight code: it runs once per item, and
     // fetching instructions would cost more than running them.

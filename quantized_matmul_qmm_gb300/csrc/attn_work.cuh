@@ -271,11 +271,16 @@ QMM_DEV bool bf16_drop_nonfinite(uint4& v) {
   return hit;
 }
 
-// One element of a bf16 cache's value rows.
+// One element of the cache's value rows.
 QMM_DEV float attn_cached_v(const AttnArgs& a, int r, int h, int tok, int d) {
   const int32_t page = a.table[(int64_t)r * a.ld_table + tok / a.cache.page_size];
   const int64_t off = attn_row_offset(a, page, tok);
   if (off < 0) return 0.f;
+  if (a.cache.v_scale != nullptr) {
+    const float s =
+        a.cache.v_scale[((int64_t)page * a.cache.n_heads + h) * a.cache.page_size + (uint32_t)tok % a.cache.page_size];
+    return s * (float)*reinterpret_cast<const int8_t*>(a.cache.v + h * a.cache.st_head + off + d);
+  }
   const uint8_t* p = a.cache.v + h * a.cache.st_head + off + 2 * d;
   return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
