@@ -46,7 +46,7 @@ using namespace umma;
 
 constexpr int kTok = 128;                        // cached tokens per tile
 constexpr int kHalf = 128 * 128;                 // bytes of 128 rows x 64 bf16
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 8;
 
 template <int D, bool kS8, int kRT>
 struct Tg {
@@ -138,7 +138,7 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
   const uint32_t box_bytes = box * D * (kS8 ? 1 : 2);
   const int lane_tok = lane * (int)box;
   const uint32_t step_blk = kTok / P, step_place = kTok % P;
-  uint32_t slot = 0, phase = 1, sc = 0, sc_phase = 1;
+  uint32_t slot = 0, phase = 1;
   if (lane == 0) {
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
@@ -178,10 +178,6 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
       const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
       uint64_t* landed = !kS8 && value && it.q.n + kTok > left ? &x.sh->bar.tail_full[slot] : &full[slot];
       if (lane == 0) mbar_arrive_expect_tx(landed, boxes * box_bytes);
-      if (kS8 && !value) {
-        if (!x.wait_all(&x.sh->bar.sc_empty[sc], sc_phase)) return;
-        if (lane == 0) mbar_arrive_expect_tx(&x.sh->bar.sc_full[sc], boxes * box * 8);
-      }
       __syncwarp();
       if (lane < boxes) {
         if ((uint32_t)pg >= (uint64_t)a.cache.n_pages) {   // reported; page 0 stands in
@@ -192,24 +188,68 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
         const uint32_t dst = base + slot * kStage;
         if constexpr (kS8) {
           tma_load_4d(dst, map, landed, 0, pl, it.h, pg);
-          if (!value) {
-            const uint32_t to = smem_u32(x.smem) + G::kOffScale + sc * (2 * kTok * 4) + lane_tok * 4;
-            const int64_t at = ((int64_t)pg * a.cache.n_heads + it.h) * P + pl;
-            bulk_g2s(to, a.cache.k_scale + at, box * 4, &x.sh->bar.sc_full[sc]);
-            bulk_g2s(to + kTok * 4, a.cache.v_scale + at, box * 4, &x.sh->bar.sc_full[sc]);
-          }
         } else {
 #pragma unroll
           for (int hf = 0; hf < G::kNH; ++hf) tma_load_4d(dst + hf * kHalf, map, landed, 64 * hf, pl, it.h, pg);
         }
       }
       if (++slot == kN) slot = 0, phase ^= 1;
-      if (kS8 && !value && ++sc == kScaleRing) sc = 0, sc_phase ^= 1;
       if (value) {
 #pragma unroll
         for (int j = 0; j < kWin - 1; ++j) page[j] = page[j + 1], places[j] = places[j + 1];
         look_up(page[kWin - 1], places[kWin - 1]);
       }
+    }
+  }
+}
+
+// ---- int8: warps 2 and 3 bring the tiles' key and value scales ----
+// Four tokens per lane.  Bulk copies of a page's few scales each would cost the
+// copy engine as much as the pages' rows.
+template <int D, int kRT>
+QMM_DEV void scale_warps(const Ctx& x) {
+  using G = Tg<D, true, kRT>;
+  const AttnArgs& a = x.a;
+  const int lane = threadIdx.x & 31, side = (threadIdx.x >> 5) & 1;
+  const float* src = side ? a.cache.v_scale : a.cache.k_scale;
+  float4* ring = reinterpret_cast<float4*>(x.smem + G::kOffScale) + side * (kTok / 4) + lane;
+  const uint32_t P = a.cache.page_size, step_blk = kTok / P, step_place = kTok % P;
+  uint32_t sc = 0, phase = 1;
+  AttnWalk walk;
+  walk.start(x.sh->work);
+  AttnItem it;
+  while (walk.next(a, x.sh->work, 128 * kRT, kTok, it)) {
+    const int32_t* trow = a.table + (int64_t)it.r * a.ld_table;
+    const int tok_end = min(it.len, (it.kv0 + it.seg) * kTok);
+    int tok = it.kv0 * kTok + 4 * lane;
+    uint32_t blk = (uint32_t)tok / P, place = (uint32_t)tok % P;
+    // a tile's page entries are read two tiles ahead, its scales one
+    auto page_of = [&](uint32_t& pl) -> int32_t {
+      const int32_t pg = tok < tok_end ? trow[blk] : -1;
+      pl = place;
+      tok += kTok;
+      blk += step_blk;
+      place += step_place;
+      if (place >= P) place -= P, ++blk;
+      return pg;
+    };
+    auto scales = [&](int32_t pg, uint32_t pl) {
+      if ((uint32_t)pg >= (uint64_t)a.cache.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
+      return *reinterpret_cast<const float4*>(src + ((int64_t)pg * a.cache.n_heads + it.h) * P + pl);
+    };
+    uint32_t pl = 0, pl_next = 0;
+    int32_t pg = page_of(pl), pg_next = page_of(pl_next);
+    float4 v = scales(pg, pl);
+#pragma unroll 1
+    for (int i = 0; i < it.seg; ++i) {
+      const float4 v_next = scales(pg_next, pl_next);
+      pg_next = page_of(pl_next);
+      if (!x.wait_all(&x.sh->bar.sc_empty[sc], phase)) return;
+      ring[sc * (2 * kTok / 4)] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x.sh->bar.sc_full[sc]);
+      v = v_next;
+      if (++sc == kScaleRing) sc = 0, phase ^= 1;
     }
   }
 }
@@ -407,26 +447,233 @@ QMM_DEV void mma_warp(const Ctx& x) {
 }
 
 // ---- warps 4..11: the rows ----
-// Zeros for the non-finite ones of four scales from number `from` on.
-QMM_DEV bool drop_nonfinite(float4& f, int from) {
-  bool hit = false;
-  if (from <= 0 && !isfinite(f.x)) f.x = 0.f, hit = true;
-  if (from <= 1 && !isfinite(f.y)) f.y = 0.f, hit = true;
-  if (from <= 2 && !isfinite(f.z)) f.z = 0.f, hit = true;
-  if (from <= 3 && !isfinite(f.w)) f.w = 0.f, hit = true;
-  return hit;
-}
-
-// s[e] *= f[e]
-template <int kN>
-QMM_DEV void scale_by(float (&s)[kN], const float4 (&f)[kN / 4]) {
-#pragma unroll
-  for (int e = 0; e < kN; e += 4) {
-    const float4 k = f[e / 4];
-    f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(k.x, k.y)), s[e], s[e + 1]);
-    f2_unpack(f2_mul(f2_pack(s[e + 2], s[e + 3]), f2_pack(k.z, k.w)), s[e + 2], s[e + 3]);
+// The exponentials of one tile of 128 rows x 128 tokens, by four warps of 32
+// rows: scores of the warp's rows in TMEM at t_s become weights (bf16, in half
+// the columns).  m is a row's reference before the scale c, l its sum.
+//
+// bf16: one row per lane.  The first 64 scores stay in registers between the
+// maximum and the weights, the other 64 are read twice.
+struct RowsBf16 {
+  float m = -INFINITY;
+  uint64_t l = 0;                                // in two halves
+  QMM_DEV void own(float& om, float& ol) const {
+    float lo, hi;
+    f2_unpack(l, lo, hi);
+    om = m;
+    ol = lo + hi;
   }
-}
+  template <typename Seen, typename Rescale, typename Half>
+  QMM_DEV void tile(uint32_t t_s, float c, float slack, bool masked, Seen seen, bool low, bool has_o, Rescale rescale,
+                    Half half_ready) {
+    float s[64], top = -INFINITY;
+    auto load = [&](int part) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t r[32];
+        tmem_ld32(t_s + 64 * part + 32 * q, r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
+      }
+      tmem_wait_ld();
+      if (masked) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t w = seen(2 * part + q);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((w >> e) & 1)) s[32 * q + e] = -INFINITY;
+        }
+      }
+    };
+#pragma unroll 1
+    for (int part = 1; part >= 0; --part) {
+      load(part);
+      float t4[4] = {top, s[0], s[1], s[2]};
+#pragma unroll
+      for (int e = 3; e < 63; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
+      top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[63]);
+    }
+    const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
+    if (__any_sync(0xffffffffu, move)) {
+      const float next = move ? top : m;
+      const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
+      l = f2_mul(l, f2_pack(f, f));
+      if (has_o) rescale(f);
+      m = next;
+    }
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+    uint64_t l2 = 0;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      if (part > 0) load(1);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
+        s[e] = exp2_approx(s[e]);
+        s[e + 1] = exp2_approx(s[e + 1]);
+        if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
+        else l = f2_add(l, f2_pack(s[e], s[e + 1]));
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = bf16_pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
+        if (low) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            p[e] = bf16_pair(s[32 * q + 2 * e] - bf16lo_to_f32(p[e]), s[32 * q + 2 * e + 1] - bf16hi_to_f32(p[e]));
+        }
+        tmem_st16(t_s + 32 * part + 16 * q, p);   // over columns whose scores have been read
+      }
+      if (part == 0) half_ready();
+    }
+    l = f2_add(l, l2);
+  }
+};
+
+// int8: two blocks of 16 rows in the layout of mma.sync accumulators, columns
+// 2c, 2c + 1 of every eight of rows g and g + 8 per thread, so that a token's
+// scales serve two rows of each lane.  Shared memory is what an int8 tile
+// runs out of (codes in and out of the converters, three operands, scales):
+// with a row per lane each scale is a broadcast of its own and the tile took
+// 1.2 times as long.
+struct RowsS8 {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // rows g, g + 8, g + 16, g + 24
+  uint64_t l[4] = {0, 0, 0, 0};
+  QMM_DEV void own(float& om, float& ol) const {
+    const int lane = threadIdx.x & 31;
+    om = ol = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      f2_unpack(l[k], lo, hi);
+      lo += hi;
+      lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+      lo += __shfl_xor_sync(0xffffffffu, lo, 2);
+      const float mk = __shfl_sync(0xffffffffu, m[k], 4 * (lane & 7)), lk = __shfl_sync(0xffffffffu, lo, 4 * (lane & 7));
+      if ((lane >> 3) == k) om = mk, ol = lk;
+    }
+  }
+  // sc: the tile's 128 key scales, then its value scales, in pairs.  Value
+  // scales of new tokens (number >= first_new) that are not finite count as 0,
+  // and the result says so: the rows that see them get theirs at the item's
+  // end, as for a bf16 cache.
+  template <typename Rescale, typename Half>
+  QMM_DEV bool tile(uint32_t t_s, const float2* sc, float c, float slack, bool masked, const uint32_t (&seen)[4],
+                    int first_new, bool low, bool has_o, Rescale rescale, Half half_ready) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c2 = lane & 3;
+    bool moved = false, found = false;
+    float f_other[2] = {1.f, 1.f};               // block 0's factors, in block 1's turn
+#pragma unroll 1
+    for (int blk = 0; blk < 2; ++blk) {
+      float s[64];
+      float2 ks[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ks[i] = sc[4 * i + c2];
+      {
+        uint32_t r[64];
+        tmem_ld_16x256b_x16(t_s + ((uint32_t)(16 * blk) << 16), r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(r[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 64; e += 2)
+        f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(ks[e >> 2].x, ks[e >> 2].y)), s[e], s[e + 1]);
+      if (masked) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t w = __shfl_sync(0xffffffffu, seen[q], 16 * blk + 8 * hf + g) >> (2 * c2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((w >> (8 * j + e)) & 1)) s[16 * q + 4 * j + 2 * hf + e] = -INFINITY;
+          }
+      }
+      float f[2], mc[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float t0 = s[2 * hf], t1 = s[2 * hf + 1];
+#pragma unroll
+        for (int e = 4; e < 64; e += 8) {
+          t0 = fmaxf(fmaxf(t0, s[e + 2 * hf]), s[e + 2 * hf + 1]);
+          if (e + 4 < 64) t1 = fmaxf(fmaxf(t1, s[e + 4 + 2 * hf]), s[e + 5 + 2 * hf]);
+        }
+        float top = fmaxf(t0, t1);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float was = m[hf];
+        const bool move = top > was + slack || (was == -INFINITY && top > -INFINITY);
+        m[hf] = move ? top : was;
+        moved |= move;
+        f[hf] = move ? exp2_approx((was - top) * c) : 1.f;   // was -infinity: 0
+        l[hf] = f2_mul(l[hf], f2_pack(f[hf], f[hf]));
+        mc[hf] = m[hf] == -INFINITY ? 0.f : -m[hf] * c;
+      }
+      if (blk == 1 && has_o && __any_sync(0xffffffffu, moved)) {
+        const int from = 4 * (lane & 7);         // each lane its own row's factor
+        const float f0 = __shfl_sync(0xffffffffu, f_other[0], from), f1 = __shfl_sync(0xffffffffu, f_other[1], from);
+        const float f2 = __shfl_sync(0xffffffffu, f[0], from), f3 = __shfl_sync(0xffffffffu, f[1], from);
+        rescale(lane < 16 ? (lane < 8 ? f0 : f1) : (lane < 24 ? f2 : f3));
+      }
+      f_other[0] = f[0];
+      f_other[1] = f[1];
+      const uint64_t cc = f2_pack(c, c), mc2[2] = {f2_pack(mc[0], mc[0]), f2_pack(mc[1], mc[1])};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {              // 64 tokens at a time, over columns that have been read
+        float2 vs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vs[i] = sc[kTok / 2 + 32 * h + 4 * i + c2];
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int tok = 64 * h + 8 * i + 2 * c2;
+            if (tok >= first_new && !isfinite(vs[i].x)) vs[i].x = 0.f, found = true;
+            if (tok + 1 >= first_new && !isfinite(vs[i].y)) vs[i].y = 0.f, found = true;
+          }
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int hf = j & 1, e = 32 * h + 2 * j;
+          f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), cc, mc2[hf]), s[e], s[e + 1]);
+          s[e] = exp2_approx(s[e]);
+          s[e + 1] = exp2_approx(s[e + 1]);
+          l[hf] = f2_add(l[hf], f2_pack(s[e], s[e + 1]));
+          f2_unpack(f2_mul(f2_pack(s[e], s[e + 1]), f2_pack(vs[j >> 1].x, vs[j >> 1].y)), s[e], s[e + 1]);
+          p[j] = bf16_pair(s[e], s[e + 1]);
+        }
+        if (low) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int e = 32 * h + 2 * j;
+            p[j] = bf16_pair(s[e] - bf16lo_to_f32(p[j]), s[e + 1] - bf16hi_to_f32(p[j]));
+          }
+        }
+        tmem_st_16x128b_x8(t_s + ((uint32_t)(16 * blk) << 16) + 32 * h, p);
+        if (blk == 1 && h == 0) half_ready();
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {           // the blocks take turns in m[0..1], l[0..1]
+        const float t = m[hf];
+        m[hf] = m[2 + hf];
+        m[2 + hf] = t;
+        const uint64_t u = l[hf];
+        l[hf] = l[2 + hf];
+        l[2 + hf] = u;
+      }
+    }
+    return found;
+  }
+};
+
+template <bool kS8> struct RowsOf { using type = RowsBf16; };
+template <> struct RowsOf<true> { using type = RowsS8; };
 
 template <int kRegs>
 QMM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
@@ -496,18 +743,17 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       if (kRT == 2 && !x.wait_all(&b.q_full, seq & 1)) return owned;
     }
 
-    float m = -INFINITY;                         // the reference, before the scale
-    uint64_t l = 0;                              // sum, in two halves
+    typename RowsOf<kS8>::type rows;             // references and sums
     const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
     bool found = false;                          // int8: a scale was left out
     if (kS8 && wid == 4 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
     const int step = kRT == 1 ? 2 : 1;
     for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
       const uint32_t sc = (tiles + i) % kScaleRing;
-      const float4* ksc = nullptr;               // the tile's 128 key scales, then its value scales
+      const float2* ksc = nullptr;               // the tile's 128 key scales, then its value scales
       if constexpr (kS8) {
         if (!x.wait_all(&b.sc_full[sc], ((tiles + i) / kScaleRing) & 1)) return owned;
-        ksc = reinterpret_cast<const float4*>(x.smem + G::kOffScale + sc * (2 * kTok * 4));
+        ksc = reinterpret_cast<const float2*>(x.smem + G::kOffScale + sc * (2 * kTok * 4));
       }
       if (has) {
         if (!x.wait_all(&b.s_full[st], s_count++ & 1)) return owned;
@@ -515,107 +761,35 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         if (active) {
           const int tok0 = (it.kv0 + i) * kTok;
           const bool masked = tok0 + kTok > it.q.L;
-          // kW scores of the row (int8: times the keys' scales), hidden ones at
-          // -infinity.  All but the first kW are read twice, for the maximum
-          // and for the weights; the first stay in registers.
-          constexpr int kW = kS8 ? 32 : 64;      // int8: what the rows' registers hold without spills
-          float s[kW], top = -INFINITY;
-          auto load_scores = [&](int part) {
-            float4 ks[kS8 ? kW / 4 : 1];
-            if constexpr (kS8) {
+          auto half_ready = [&]() {              // the products with the first 64 tokens may begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.p_half[st]);
+          };
+          // O (of this lane's row) to a new reference
+          auto rescale = [&](float f) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t r[16];
+              tmem_ld16(tlane + kColO + 128 * st + 16 * q, r);
+              tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < kW / 4; ++e) ks[e] = ksc[kW / 4 * part + e];
-            }
-#pragma unroll
-            for (int q = 0; q < kW / 32; ++q) {
-              uint32_t r[32];
-              tmem_ld32(t_s + kW * part + 32 * q, r);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
-            }
-            tmem_wait_ld();
-            if constexpr (kS8) scale_by(s, ks);
-            if (masked) {
-#pragma unroll
-              for (int q = 0; q < kW / 32; ++q) {
-                const uint32_t seen = live ? attn_sees32(a, it.q, node, tok0 + kW * part + 32 * q) : 0u;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((seen >> e) & 1)) s[32 * q + e] = -INFINITY;
-              }
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tmem_st16(tlane + kColO + 128 * st + 16 * q, r);
             }
           };
-#pragma unroll 1
-          for (int part = kTok / kW - 1; part >= 0; --part) {
-            load_scores(part);
-            float t4[4] = {top, s[0], s[1], s[2]};
+          if constexpr (kS8) {
+            uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};   // of this lane's row
+            if (masked) {
 #pragma unroll
-            for (int e = 3; e < kW - 1; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
-            top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[kW - 1]);
+              for (int q = 0; q < 4; ++q) seen[q] = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
+            }
+            found |= rows.tile(t_s, ksc, c, slack, masked, seen, it.q.L - tok0, low, i >= step, rescale, half_ready);
+          } else {
+            auto seen = [&](int q) { return live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u; };
+            rows.tile(t_s, c, slack, masked, seen, low, i >= step, rescale, half_ready);
           }
-          const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
-          if (__any_sync(0xffffffffu, move)) {
-            const float next = move ? top : m;
-            const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
-            l = f2_mul(l, f2_pack(f, f));
-            if (i >= step) {                     // O exists: bring it to the new reference
-#pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t r[16];
-                tmem_ld16(tlane + kColO + 128 * st + 16 * q, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                tmem_st16(tlane + kColO + 128 * st + 16 * q, r);
-              }
-            }
-            m = next;
-          }
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
-          uint64_t l2 = 0;
-#pragma unroll 1
-          for (int part = 0; part < kTok / kW; ++part) {
-            if (part > 0) load_scores(part);
-            float4 vs[kS8 ? kW / 4 : 1];
-            if constexpr (kS8) {
-#pragma unroll
-              for (int e = 0; e < kW / 4; ++e) vs[e] = ksc[kTok / 4 + kW / 4 * part + e];
-              // a new token's value scale that is not finite: 0 here, and the
-              // rows that see it get theirs at the end, as for a bf16 cache
-              if (masked) {
-#pragma unroll
-                for (int e = 0; e < kW / 4; ++e) found |= drop_nonfinite(vs[e], it.q.L - tok0 - kW * part - 4 * e);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < kW; e += 2) {
-              f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
-              s[e] = exp2_approx(s[e]);
-              s[e + 1] = exp2_approx(s[e + 1]);
-              if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
-              else l = f2_add(l, f2_pack(s[e], s[e + 1]));
-            }
-            if constexpr (kS8) scale_by(s, vs);
-#pragma unroll
-            for (int q = 0; q < kW / 32; ++q) {
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float x0 = s[32 * q + 2 * e], x1 = s[32 * q + 2 * e + 1];
-                p[e] = bf16_pair(x0, x1);
-                if (low) p[e] = bf16_pair(x0 - bf16lo_to_f32(p[e]), x1 - bf16hi_to_f32(p[e]));
-              }
-              tmem_st16(t_s + kW / 2 * part + 16 * q, p);   // over columns whose scores have been read
-            }
-            if (kW * (part + 1) == kTok / 2) {   // the products with the first 64 tokens may begin
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&b.p_half[st]);
-            }
-          }
-          l = f2_add(l, l2);
           tmem_wait_st();
         } else if (lane == 0) {
           mbar_arrive(&b.p_half[st]);
@@ -637,11 +811,11 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
     }
     if (kS8 && found) atomicOr(&x.sh->bad[seq & 15], 1);
-    float l_lo, l_hi;
-    f2_unpack(l, l_lo, l_hi);
-    float f[2] = {1.f, 1.f}, top = m, sum = l_lo + l_hi;   // each stream's factor; maximum and sum of the row
+    float own_m, sum;                            // of this lane's row
+    rows.own(own_m, sum);
+    float f[2] = {1.f, 1.f}, top = own_m;        // each stream's factor; maximum of the row
     if constexpr (kRT == 1) {
-      x.sh->m[st][trow] = m;
+      x.sh->m[st][trow] = own_m;
       x.sh->l[st][trow] = sum;
       if (!sync8()) return owned;                // both streams' O and sums are there
       top = fmaxf(x.sh->m[0][rr], x.sh->m[1][rr]);
@@ -784,7 +958,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
       mbar_init(&b.raw_empty[i], G::kConvWarps);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&b.sc_full[i], 1);
+      mbar_init(&b.sc_full[i], 2);
       mbar_init(&b.sc_empty[i], kRT == 1 ? 4 : 8);
     }
     for (int i = 0; i < 2; ++i) {
@@ -825,7 +999,8 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
       } else if (warp == 1) {
         mma_warp<D, kS8, kRT>(x);
       } else {
-        if constexpr (!kS8) clean_warps<D, kRT>(x);
+        if constexpr (kS8) scale_warps<D, kRT>(x);
+        else clean_warps<D, kRT>(x);
       }
     } else if (warp < 12) {
       if constexpr (kS8) regs_inc<144>();
@@ -849,8 +1024,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         for (uint32_t ph = 0; ph < 2; ++ph) mbar_drain(&bars[i], ph, 10000000ull);
     };
     drain(kS8 ? b.raw_full : b.full, kS8 ? G::kRawSlots : G::kSlots);
-    if (kS8) drain(b.sc_full, kScaleRing);
-    else drain(b.tail_full, G::kSlots);
+    if (!kS8) drain(b.tail_full, G::kSlots);
   }
   if (warp == 1) {
     if (sh.abort && lane == 0) {                 // else every product has been waited for
