@@ -49,7 +49,7 @@ constexpr int kBlocksPerSm = 2;
 constexpr int kRingBytes = 24576;                // per warp
 constexpr int kCombineMaxOwners = 512;           // blocks of an attention grid, at most
 // More query rows per key head than this go to the tile kernel (attn_tiles.cu).
-constexpr int64_t kRowsKernelMax = 32;
+constexpr int64_t kRowsKernelMax = 16;
 
 template <int D, bool kS8>
 struct Geo {

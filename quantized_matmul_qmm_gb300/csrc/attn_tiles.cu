@@ -47,6 +47,7 @@ using namespace umma;
 constexpr int kTok = 128;                        // cached tokens per tile
 constexpr int kHalf = 128 * 128;                 // bytes of 128 rows x 64 bf16
 constexpr int kScaleRing = 8;
+constexpr int kBadRing = 32;                     // items' flags; the roles are at most 9 items apart
 
 template <int D, bool kS8, int kRT>
 struct Tg {
@@ -69,7 +70,7 @@ struct TBars {
   uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2];
+  uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t q_full, o_free, sync;
   uint64_t done;
 };
@@ -79,7 +80,7 @@ struct TShared {
   AttnFindScratch find;
   AttnWork work;                                 // out of the roles' registers
   float m[2][128], l[2][128];
-  int bad[16];                       // per item, by its number: a non-finite value was taken out
+  int bad[kBadRing];                 // per item, by its number: a non-finite value was taken out
   uint32_t tmem;
   int abort;
 };
@@ -203,9 +204,21 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
   }
 }
 
+// Zeros for the non-finite ones of four scales from number `from` on.
+QMM_DEV bool drop_nonfinite(float4& f, int from) {
+  bool hit = false;
+  if (from <= 0 && !isfinite(f.x)) f.x = 0.f, hit = true;
+  if (from <= 1 && !isfinite(f.y)) f.y = 0.f, hit = true;
+  if (from <= 2 && !isfinite(f.z)) f.z = 0.f, hit = true;
+  if (from <= 3 && !isfinite(f.w)) f.w = 0.f, hit = true;
+  return hit;
+}
+
 // ---- int8: warps 2 and 3 bring the tiles' key and value scales ----
 // Four tokens per lane.  Bulk copies of a page's few scales each would cost the
-// copy engine as much as the pages' rows.
+// copy engine as much as the pages' rows.  Value scales of new tokens that are
+// not finite count as 0 and raise the item's flag: the rows that see them get
+// theirs at the end, as for a bf16 cache.
 template <int D, int kRT>
 QMM_DEV void scale_warps(const Ctx& x) {
   using G = Tg<D, true, kRT>;
@@ -214,11 +227,12 @@ QMM_DEV void scale_warps(const Ctx& x) {
   const float* src = side ? a.cache.v_scale : a.cache.k_scale;
   float4* ring = reinterpret_cast<float4*>(x.smem + G::kOffScale) + side * (kTok / 4) + lane;
   const uint32_t P = a.cache.page_size, step_blk = kTok / P, step_place = kTok % P;
-  uint32_t sc = 0, phase = 1;
+  uint32_t sc = 0, phase = 1, seq = 0;
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
-  while (walk.next(a, x.sh->work, 128 * kRT, kTok, it)) {
+  for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
+    if (side && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
     const int32_t* trow = a.table + (int64_t)it.r * a.ld_table;
     const int tok_end = min(it.len, (it.kv0 + it.seg) * kTok);
     int tok = it.kv0 * kTok + 4 * lane;
@@ -245,6 +259,8 @@ QMM_DEV void scale_warps(const Ctx& x) {
       const float4 v_next = scales(pg_next, pl_next);
       pg_next = page_of(pl_next);
       if (!x.wait_all(&x.sh->bar.sc_empty[sc], phase)) return;
+      const int from = it.q.L - (it.kv0 + i) * kTok - 4 * lane;   // of the lane's four, the first new token
+      if (side && from < 4 && drop_nonfinite(v, from)) atomicOr(&x.sh->bad[seq % kBadRing], 1);
       ring[sc * (2 * kTok / 4)] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.sh->bar.sc_full[sc]);
@@ -318,8 +334,7 @@ QMM_DEV void clean_warps(const Ctx& x) {
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    // an item's flag is cleared eight items ahead: the ring holds four items at most
-    if (mine == 0 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
+    if (mine == 0 && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
     TileOrder<G::kAhead> order{it.seg};
     bool value;
     int i;
@@ -347,7 +362,7 @@ QMM_DEV void clean_warps(const Ctx& x) {
         }
         sts128(at, v);
       }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&x.sh->bad[seq & 15], 1);
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&x.sh->bad[seq % kBadRing], 1);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.sh->bar.full[slot]);
@@ -384,21 +399,13 @@ QMM_DEV void mma_warp(const Ctx& x) {
       }
       umma_commit_one(one, &b.s_full[st]);
     };
-    // the products with the first 64 tokens begin while the other weights are made
     auto values = [&](int st, uint32_t tile, bool first, bool last) {
       const uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
 #pragma unroll
-      for (int k = 0; k < kTok / 16; ++k) {
-        if (k == kTok / 32) {
-          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return false;
-          p_phase[st] ^= 1;
-          tc_fence_after();
-        }
+      for (int k = 0; k < kTok / 16; ++k)
         umma_f16_ta_one(one, kColO + 128 * st, kColS + 128 * st + 8 * k, v_desc + k * (2048 >> 4), kIdO,
                         k > 0 || !first);
-      }
       if (last) umma_commit_one(one, &b.o_done[st]);
-      return true;
     };
     uint32_t v_tile = 0;
     int v_slot = 0, v_i = 0;
@@ -416,13 +423,14 @@ QMM_DEV void mma_warp(const Ctx& x) {
       const uint32_t tile = slots + slot * G::kTile;
       if (more) {
         if (value) {
-          if (!x.wait_all(&b.p_half[st], p_phase[st])) return;
+          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return;
+          p_phase[st] ^= 1;
           if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return;
         }
         if (!x.wait_all(&b.full[slot], phase)) return;
         tc_fence_after();
         if (value) {
-          if (!values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg)) return;
+          values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg);
           v_tile = tile;
           v_slot = slot;
           v_i = i;
@@ -432,9 +440,10 @@ QMM_DEV void mma_warp(const Ctx& x) {
         }
       }
       if (kRT == 2 && v_open && (!more || !value || i == it.seg - 1)) {
-        if (!x.wait_all(&b.p_half[1], p_phase[1])) return;
+        if (!x.wait_all(&b.p_ready[1], p_phase[1])) return;
+        p_phase[1] ^= 1;
         tc_fence_after();
-        if (!values(1, v_tile, v_i == 0, v_i == it.seg - 1)) return;
+        values(1, v_tile, v_i == 0, v_i == it.seg - 1);
         umma_commit_one(one, &b.empty[v_slot]);
         v_open = false;
       }
@@ -449,87 +458,104 @@ QMM_DEV void mma_warp(const Ctx& x) {
 // ---- warps 4..11: the rows ----
 // The exponentials of one tile of 128 rows x 128 tokens, by four warps of 32
 // rows: scores of the warp's rows in TMEM at t_s become weights (bf16, in half
-// the columns).  m is a row's reference before the scale c, l its sum.
+// the columns).
 //
-// bf16: one row per lane.  The first 64 scores stay in registers between the
-// maximum and the weights, the other 64 are read twice.
+// bf16: one row per lane, and one pass over the scores:
+// the weights are made with the reference of the tiles before while the tile's
+// maximum is found beside them, and only if that passes the reference by more
+// than `slack` (2^8 in the weights; the first tile, and rarely later) the
+// maximum is taken first and the pass made again.  The weights wait in
+// registers until then, because they go over the scores.
 struct RowsBf16 {
-  float m = -INFINITY;
-  uint64_t l = 0;                                // in two halves
+  float m = -INFINITY;                           // the row's reference, before the scale c
+  uint64_t l = 0;                                // the weights' sum, in two halves
   QMM_DEV void own(float& om, float& ol) const {
     float lo, hi;
     f2_unpack(l, lo, hi);
     om = m;
     ol = lo + hi;
   }
-  template <typename Seen, typename Rescale, typename Half>
-  QMM_DEV void tile(uint32_t t_s, float c, float slack, bool masked, Seen seen, bool low, bool has_o, Rescale rescale,
-                    Half half_ready) {
-    float s[64], top = -INFINITY;
-    auto load = [&](int part) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t r[32];
-        tmem_ld32(t_s + 64 * part + 32 * q, r);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
-      }
+  template <typename Seen, typename Rescale>
+  QMM_DEV void tile(uint32_t t_s, const float*, float c, float slack, bool masked, Seen seen, bool low, bool has_o,
+                    Rescale rescale) {
+    constexpr int kW = 32;                       // scores at a time
+    float s[kW];
+    auto load = [&](int q) {                     // hidden ones at -infinity
+      uint32_t r[kW];
+      tmem_ld32(t_s + kW * q, r);
       tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < kW; ++e) s[e] = __uint_as_float(r[e]);
       if (masked) {
+        const uint32_t w = seen(kW * q);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t w = seen(2 * part + q);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((w >> e) & 1)) s[32 * q + e] = -INFINITY;
-        }
+        for (int e = 0; e < kW; ++e)
+          if (!((w >> e) & 1)) s[e] = -INFINITY;
       }
     };
-#pragma unroll 1
-    for (int part = 1; part >= 0; --part) {
-      load(part);
-      float t4[4] = {top, s[0], s[1], s[2]};
+    auto top_of = [&](float top) {
+      float t2[2] = {top, s[0]};
 #pragma unroll
-      for (int e = 3; e < 63; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
-      top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), s[63]);
-    }
-    const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
-    if (__any_sync(0xffffffffu, move)) {
-      const float next = move ? top : m;
-      const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
-      l = f2_mul(l, f2_pack(f, f));
-      if (has_o) rescale(f);
-      m = next;
-    }
-    const float mc = m == -INFINITY ? 0.f : m * c;
-    const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
-    uint64_t l2 = 0;
+      for (int e = 1; e < kW - 1; e += 2) t2[(e >> 1) & 1] = fmaxf(fmaxf(t2[(e >> 1) & 1], s[e]), s[e + 1]);
+      return fmaxf(fmaxf(t2[0], t2[1]), s[kW - 1]);
+    };
+    uint32_t p[64];
+    uint64_t lt[2];
+    bool first = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-      if (part > 0) load(1);
-#pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
-        s[e] = exp2_approx(s[e]);
-        s[e + 1] = exp2_approx(s[e + 1]);
-        if (e & 2) l2 = f2_add(l2, f2_pack(s[e], s[e + 1]));
-        else l = f2_add(l, f2_pack(s[e], s[e + 1]));
+    for (;;) {
+      if (first) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < kTok / kW; ++q) {
+          load(q);
+          top = top_of(top);
+        }
+        const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float next = move ? top : m;
+          const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
+          l = f2_mul(l, f2_pack(f, f));
+          if (has_o) rescale(f);
+          m = next;
+        }
       }
+      const float mc = m == -INFINITY ? 0.f : m * c;
+      const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+      lt[0] = lt[1] = 0;
+      float top = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t p[16];
+      for (int q = 0; q < kTok / kW; ++q) {
+        load(q);
+        top = top_of(top);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = bf16_pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
+        for (int e = 0; e < kW; e += 2) {
+          f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
+          s[e] = exp2_approx(s[e]);
+          s[e + 1] = exp2_approx(s[e + 1]);
+          lt[(e >> 1) & 1] = f2_add(lt[(e >> 1) & 1], f2_pack(s[e], s[e + 1]));
+        }
+#pragma unroll
+        for (int e = 0; e < kW / 2; ++e) p[kW / 2 * q + e] = bf16_pair(s[2 * e], s[2 * e + 1]);
         if (low) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            p[e] = bf16_pair(s[32 * q + 2 * e] - bf16lo_to_f32(p[e]), s[32 * q + 2 * e + 1] - bf16hi_to_f32(p[e]));
+          for (int e = 0; e < kW / 2; ++e) {
+            uint32_t& w = p[kW / 2 * q + e];
+            w = bf16_pair(s[2 * e] - bf16lo_to_f32(w), s[2 * e + 1] - bf16hi_to_f32(w));
+          }
         }
-        tmem_st16(t_s + 32 * part + 16 * q, p);   // over columns whose scores have been read
       }
-      if (part == 0) half_ready();
+      if (first || !__any_sync(0xffffffffu, top > m + slack)) break;
+      first = true;
     }
-    l = f2_add(l, l2);
+    l = f2_add(l, f2_add(lt[0], lt[1]));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = p[16 * q + e];
+      tmem_st16(t_s + 16 * q, w);
+    }
   }
 };
 
@@ -542,6 +568,7 @@ struct RowsBf16 {
 struct RowsS8 {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // rows g, g + 8, g + 16, g + 24
   uint64_t l[4] = {0, 0, 0, 0};
+  // this lane's own row: its reference and sum
   QMM_DEV void own(float& om, float& ol) const {
     const int lane = threadIdx.x & 31;
     om = ol = 0.f;
@@ -556,15 +583,18 @@ struct RowsS8 {
       if ((lane >> 3) == k) om = mk, ol = lk;
     }
   }
-  // sc: the tile's 128 key scales, then its value scales, in pairs.  Value
-  // scales of new tokens (number >= first_new) that are not finite count as 0,
-  // and the result says so: the rows that see them get theirs at the item's
-  // end, as for a bf16 cache.
-  template <typename Rescale, typename Half>
-  QMM_DEV bool tile(uint32_t t_s, const float2* sc, float c, float slack, bool masked, const uint32_t (&seen)[4],
-                    int first_new, bool low, bool has_o, Rescale rescale, Half half_ready) {
+  // scales: the tile's 128 key scales, then its value scales.
+  template <typename Seen, typename Rescale>
+  QMM_DEV void tile(uint32_t t_s, const float* scales, float c, float slack, bool masked, Seen seen_at, bool low,
+                    bool has_o, Rescale rescale) {
+    const float2* sc = reinterpret_cast<const float2*>(scales);
+    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};     // of this lane's row
+    if (masked) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) seen[q] = seen_at(32 * q);
+    }
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = lane & 3;
-    bool moved = false, found = false;
+    bool moved = false;
     float f_other[2] = {1.f, 1.f};               // block 0's factors, in block 1's turn
 #pragma unroll 1
     for (int blk = 0; blk < 2; ++blk) {
@@ -629,14 +659,6 @@ struct RowsS8 {
         float2 vs[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) vs[i] = sc[kTok / 2 + 32 * h + 4 * i + c2];
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int tok = 64 * h + 8 * i + 2 * c2;
-            if (tok >= first_new && !isfinite(vs[i].x)) vs[i].x = 0.f, found = true;
-            if (tok + 1 >= first_new && !isfinite(vs[i].y)) vs[i].y = 0.f, found = true;
-          }
-        }
         uint32_t p[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -656,7 +678,6 @@ struct RowsS8 {
           }
         }
         tmem_st_16x128b_x8(t_s + ((uint32_t)(16 * blk) << 16) + 32 * h, p);
-        if (blk == 1 && h == 0) half_ready();
       }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {           // the blocks take turns in m[0..1], l[0..1]
@@ -668,7 +689,6 @@ struct RowsS8 {
         l[2 + hf] = u;
       }
     }
-    return found;
   }
 };
 
@@ -745,15 +765,13 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
 
     typename RowsOf<kS8>::type rows;             // references and sums
     const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
-    bool found = false;                          // int8: a scale was left out
-    if (kS8 && wid == 4 && lane == 0) x.sh->bad[(seq + 8) & 15] = 0;
     const int step = kRT == 1 ? 2 : 1;
     for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
       const uint32_t sc = (tiles + i) % kScaleRing;
-      const float2* ksc = nullptr;               // the tile's 128 key scales, then its value scales
+      const float* ksc = nullptr;                // the tile's 128 key scales, then its value scales
       if constexpr (kS8) {
         if (!x.wait_all(&b.sc_full[sc], ((tiles + i) / kScaleRing) & 1)) return owned;
-        ksc = reinterpret_cast<const float2*>(x.smem + G::kOffScale + sc * (2 * kTok * 4));
+        ksc = reinterpret_cast<const float*>(x.smem + G::kOffScale + sc * (2 * kTok * 4));
       }
       if (has) {
         if (!x.wait_all(&b.s_full[st], s_count++ & 1)) return owned;
@@ -761,12 +779,6 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         if (active) {
           const int tok0 = (it.kv0 + i) * kTok;
           const bool masked = tok0 + kTok > it.q.L;
-          auto half_ready = [&]() {              // the products with the first 64 tokens may begin
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b.p_half[st]);
-          };
           // O (of this lane's row) to a new reference
           auto rescale = [&](float f) {
 #pragma unroll 1
@@ -779,20 +791,9 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
               tmem_st16(tlane + kColO + 128 * st + 16 * q, r);
             }
           };
-          if constexpr (kS8) {
-            uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};   // of this lane's row
-            if (masked) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) seen[q] = live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u;
-            }
-            found |= rows.tile(t_s, ksc, c, slack, masked, seen, it.q.L - tok0, low, i >= step, rescale, half_ready);
-          } else {
-            auto seen = [&](int q) { return live ? attn_sees32(a, it.q, node, tok0 + 32 * q) : 0u; };
-            rows.tile(t_s, c, slack, masked, seen, low, i >= step, rescale, half_ready);
-          }
+          auto seen = [&](int at) { return live ? attn_sees32(a, it.q, node, tok0 + at) : 0u; };
+          rows.tile(t_s, ksc, c, slack, masked, seen, low, i >= step, rescale);
           tmem_wait_st();
-        } else if (lane == 0) {
-          mbar_arrive(&b.p_half[st]);
         }
         tc_fence_before();
         __syncwarp();
@@ -810,7 +811,6 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     if (own_tiles) {
       if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
     }
-    if (kS8 && found) atomicOr(&x.sh->bad[seq & 15], 1);
     float own_m, sum;                            // of this lane's row
     rows.own(own_m, sum);
     float f[2] = {1.f, 1.f}, top = own_m;        // each stream's factor; maximum of the row
@@ -830,7 +830,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       }
     }
     tc_fence_after();
-    const bool bad = x.sh->bad[seq & 15] != 0;   // kRT == 2, int8: this warp's own finding at least
+    const bool bad = x.sh->bad[seq % kBadRing] != 0;
     // 16 columns of O at a time, of both streams with kRT == 1 (each takes half
     // of the columns).  Loops, not straight code: it runs once per item, and
     // fetching instructions would cost more than running them.
@@ -963,7 +963,6 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.s_full[i], 1);
-      mbar_init(&b.p_half[i], 4);
       mbar_init(&b.p_ready[i], 4);
       mbar_init(&b.o_done[i], 1);
     }
@@ -972,7 +971,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     mbar_init(&b.sync, 8);
     mbar_init(&b.done, 1);
     sh.abort = 0;
-    for (int i = 0; i < 16; ++i) sh.bad[i] = 0;
+    for (int i = 0; i < kBadRing; ++i) sh.bad[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
