@@ -24,12 +24,12 @@
 // weights, so that O is rarely rescaled (it is in TMEM, not in registers).
 //
 // Warps: 0 loads (TMA boxes of page_size's power of two; the pages of a tile
-// looked up by one lane each), 1 issues the products, 2 and 3 clean the
-// value tiles that hold the step's own tokens (zeros past the request's end
-// and for non-finite values, see attn_rows.cu), 4..11 are the two streams'
-// rows.  An int8 cache has four more: tiles arrive as codes and are written
-// out as bf16 in the products' layout; a token's key scale multiplies its
-// column of s, its value scale the weight.
+// looked up by one lane each), 1 issues the products, 2 cleans the value tiles
+// that hold the step's own tokens (zeros past the request's end and for
+// non-finite values, see attn_rows.cu), 4..11 are the two streams' rows.  With
+// an int8 cache, tiles arrive as codes, eight more warps write them out as
+// bf16 in the products' layout, and 2 and 3 bring the scales; a token's key
+// scale multiplies its column of s, its value scale the weight.
 //
 // What bounds it: 4 * 128 operations per row and token against 512 (bf16) or
 // 264 (int8) bytes per token: the cache's bytes up to about 128 rows, the
@@ -67,7 +67,7 @@ struct Tg {
 
 struct TBars {
   uint64_t full[8], empty[8];        // bf16 tiles
-  uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
+  uint64_t tail_full[8];             // value tiles that warp 2 hands on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint64_t s_full[2], p_ready[2], o_done[2];
@@ -321,20 +321,21 @@ QMM_DEV void convert_warps(const Ctx& x) {
   }
 }
 
-// ---- bf16: warps 2 and 3 clean the value tiles that reach past the context
-// (one warp each of two consecutive ones) and hand them on ----
+// ---- bf16: warp 2 cleans the value tiles that reach past the context and
+// hands them on ----
+// One warp for all of them: it sees every phase of a slot's barrier in turn (a
+// warp that skipped some could take an old phase for the one it waits for).
 template <int D, int kRT>
-QMM_DEV void clean_warps(const Ctx& x) {
+QMM_DEV void clean_warp(const Ctx& x) {
   using G = Tg<D, false, kRT>;
   const AttnArgs& a = x.a;
   const int lane = threadIdx.x & 31;
-  const uint32_t mine = (threadIdx.x >> 5) & 1;
-  uint32_t n = 0, seq = 0, tails = 0, phases = 0;   // phases: a bit per slot
+  uint32_t n = 0, seq = 0, phases = 0;           // phases: a bit per slot
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    if (mine == 0 && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
+    if (lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
     TileOrder<G::kAhead> order{it.seg};
     bool value;
     int i;
@@ -345,7 +346,6 @@ QMM_DEV void clean_warps(const Ctx& x) {
       if (!value || tok0 + kTok <= it.q.L) continue;
       const uint32_t parity = (phases >> slot) & 1;
       phases ^= 1u << slot;
-      if ((tails++ & 1) != mine) continue;
       if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return;
       const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile;
       bool bad = false;
@@ -999,7 +999,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         mma_warp<D, kS8, kRT>(x);
       } else {
         if constexpr (kS8) scale_warps<D, kRT>(x);
-        else clean_warps<D, kRT>(x);
+        else if (warp == 2) clean_warp<D, kRT>(x);
       }
     } else if (warp < 12) {
       if constexpr (kS8) regs_inc<144>();

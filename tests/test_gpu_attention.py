@@ -173,6 +173,19 @@ def test_long_context_split_between_blocks(qmm, cuda, s8, new, heads):
     assert torch.equal(a, call(qmm, cuda, s))    # fixed order of the sums
 
 
+@pytest.mark.parametrize("s8", [False, True])
+@pytest.mark.parametrize("heads,new", [(16, [33, 28, 22, 32, 26, 19, 30, 23]), (8, [9, 16, 5, 14, 12, 3, 10, 8])])
+def test_many_items_in_a_block(qmm, cuda, s8, heads, new):
+    """Requests of a few tiles each, of which every block walks several, with
+    new tokens across tile boundaries (and, in the first, rows just past 128)."""
+    ctx = [3819, 1346, 3117, 2022, 3793, 2699, 1604, 3375]
+    s = build(cuda, ctx, new, heads, 4, 64, 32, s8, tree=True, seed=11)
+    check(s, call(qmm, cuda, s))
+    s = build(cuda, [120 + i % 16 for i in range(300)], [2 + i % 9 for i in range(300)], heads, 4, 64, 8, s8, tree=True,
+              seed=12)
+    check(s, call(qmm, cuda, s))
+
+
 def test_many_requests(qmm, cuda):
     g = torch.Generator().manual_seed(3)
     ctx = torch.randint(0, 90, (333,), generator=g).tolist()
