@@ -24,8 +24,8 @@
 // weights, so that O is rarely rescaled (it is in TMEM, not in registers).
 //
 // Warps: 0 loads (TMA boxes of page_size's power of two; the pages of a tile
-// looked up by one lane each), 1 issues the products, 2 cleans the value tiles
-// that hold the step's own tokens (zeros past the request's end and for
+// looked up by one lane each), 1 issues the products, 2 and 3 clean the value
+// tiles that hold the step's own tokens (zeros past the request's end and for
 // non-finite values, see attn_rows.cu), 4..11 are the two streams' rows.  With
 // an int8 cache, tiles arrive as codes, eight more warps write them out as
 // bf16 in the products' layout, and 2 and 3 bring the scales; a token's key
@@ -67,7 +67,7 @@ struct Tg {
 
 struct TBars {
   uint64_t full[8], empty[8];        // bf16 tiles
-  uint64_t tail_full[8];             // value tiles that warp 2 hands on
+  uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint64_t s_full[2], p_ready[2], o_done[2];
@@ -178,7 +178,10 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
       const int left = it.len - (it.kv0 + i) * kTok;
       const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
       uint64_t* landed = !kS8 && value && it.q.n + kTok > left ? &x.sh->bar.tail_full[slot] : &full[slot];
-      if (lane == 0) mbar_arrive_expect_tx(landed, boxes * box_bytes);
+      if (lane == 0) {
+        if (!kS8 && landed == &full[slot]) mbar_arrive(landed);   // for the second cleaner
+        mbar_arrive_expect_tx(landed, boxes * box_bytes);
+      }
       __syncwarp();
       if (lane < boxes) {
         if ((uint32_t)pg >= (uint64_t)a.cache.n_pages) {   // reported; page 0 stands in
@@ -321,21 +324,25 @@ QMM_DEV void convert_warps(const Ctx& x) {
   }
 }
 
-// ---- bf16: warp 2 cleans the value tiles that reach past the context and
-// hands them on ----
-// One warp for all of them: it sees every phase of a slot's barrier in turn (a
-// warp that skipped some could take an old phase for the one it waits for).
+// ---- bf16: warps 2 and 3 clean the value tiles that reach past the context,
+// half of the rows each, and hand them on ----
+// Both see every phase of every slot's barrier (a warp that skipped some could
+// take an old phase for the one it waits for).  Eight 16-byte pieces at a time
+// are tested together: exponents of all ones carry into the sign bit.
 template <int D, int kRT>
-QMM_DEV void clean_warp(const Ctx& x) {
+QMM_DEV void clean_warps(const Ctx& x) {
   using G = Tg<D, false, kRT>;
   const AttnArgs& a = x.a;
-  const int lane = threadIdx.x & 31;
+  constexpr int kP = D / 8;                      // pieces of a row
+  constexpr int kBatch = 32 * 8 / kP;            // rows of a batch
+  const int lane = threadIdx.x & 31, t_lane = lane / kP, p = lane % kP;
+  const int t_first = ((threadIdx.x >> 5) & 1) * (kTok / 2);
   uint32_t n = 0, seq = 0, phases = 0;           // phases: a bit per slot
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    if (lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
+    if (t_first == 0 && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
     TileOrder<G::kAhead> order{it.seg};
     bool value;
     int i;
@@ -347,20 +354,36 @@ QMM_DEV void clean_warp(const Ctx& x) {
       const uint32_t parity = (phases >> slot) & 1;
       phases ^= 1u << slot;
       if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return;
-      const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile;
+      const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile + (p >> 3) * kHalf;
       bool bad = false;
-#pragma unroll 4
-      for (int q = lane; q < kTok * (D / 8); q += 32) {
-        const int t = q / (D / 8), p = q % (D / 8);
-        if (tok0 + t < it.q.L) continue;
-        const uint32_t at = base + (p >> 3) * kHalf + t * 128 + (((p & 7) ^ (t & 7)) << 4);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (tok0 + t < it.len) {
-          v = lds128(at);
-          if (!bf16_drop_nonfinite(v)) continue;
-          bad = true;
+#pragma unroll 1
+      for (int t0 = t_first; t0 < t_first + kTok / 2; t0 += kBatch) {
+        if (tok0 + t0 + kBatch <= it.q.L) continue;   // cached tokens only
+        auto at = [&](int k) {
+          const int t = t0 + k * (32 / kP) + t_lane;
+          return base + t * 128 + (((p & 7) ^ (t & 7)) << 4);
+        };
+        uint4 v[8];
+        uint32_t hit = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[k] = lds128(at(k));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hit |= (u4_get(v[k], e) & 0x7F807F80u) + 0x00800080u;
         }
-        sts128(at, v);
+        if (!__any_sync(0xffffffffu, hit & 0x80008000u) && tok0 + t0 + kBatch <= it.len) continue;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int tok = tok0 + t0 + k * (32 / kP) + t_lane;
+          if (tok < it.q.L) continue;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (tok < it.len) {
+            w = lds128(at(k));
+            if (!bf16_drop_nonfinite(w)) continue;
+            bad = true;
+          }
+          sts128(at(k), w);
+        }
       }
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&x.sh->bad[seq % kBadRing], 1);
       fence_proxy_async_smem();
@@ -737,7 +760,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       const int ch = lane % kCh, r_first = kRT == 1 ? 16 * st : 0;
       const int64_t qo = live ? attn_q_row(a, it.q, it.h, row) : -1;
       const uint32_t base = smem_u32(x.smem) + (kRT == 2 ? st * G::kTile : 0) + (ch >> 3) * kHalf;
-#pragma unroll 8
+#pragma unroll (kS8 ? 8 : 16)
       for (int j = 0; j < kLoads; ++j) {
         const int rl = r_first + j * kAt + lane / kCh, tr = 32 * quarter + rl;
         const int64_t at = __shfl_sync(0xffffffffu, qo, rl);
@@ -892,7 +915,10 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         return split ? reinterpret_cast<float4*>(x.smem)[(32 * quarter + r) * (D / 4) + ((d / 4 + e) ^ (r & 7))]
                      : stage[r * 4 + (e ^ ((r >> 1) & 3))];
       };
-      const int64_t to = !live ? -1 : it.whole ? attn_out_row(a, it.q.first, it.h, row) - a.out : slot * D;
+      const int64_t own = !live ? -1 : it.whole ? attn_out_row(a, it.q.first, it.h, row) - a.out : slot * D;
+      int64_t to[4];                             // of the rows that this lane stores a piece of
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[j] = __shfl_sync(0xffffffffu, own, 8 * j + (lane >> 2));
 #pragma unroll 1
       for (int d = d_first; d < d_first + kCols; d += 16) {
         float o[16];
@@ -913,13 +939,13 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = 8 * j + (lane >> 2), e = lane & 3;
-          const int64_t at = __shfl_sync(0xffffffffu, to, r);
           const float4 v = piece(r, d, e);
-          if (at >= 0) {
+          if (to[j] >= 0) {
             if (it.whole)
-              *reinterpret_cast<uint2*>(a.out + at + d + 4 * e) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+              *reinterpret_cast<uint2*>(a.out + to[j] + d + 4 * e) =
+                  make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
             else
-              *reinterpret_cast<float4*>(a.part_o + at + d + 4 * e) = v;
+              *reinterpret_cast<float4*>(a.part_o + to[j] + d + 4 * e) = v;
           }
         }
       }
@@ -949,7 +975,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   TBars& b = sh.bar;
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kSlots; ++i) {
-      mbar_init(&b.full[i], kS8 ? G::kConvWarps : 1);   // converters, or the loads
+      mbar_init(&b.full[i], kS8 ? G::kConvWarps : 2);   // converters, or the loads (twice) or the cleaners
       mbar_init(&b.empty[i], 1);
       mbar_init(&b.tail_full[i], 1);
     }
@@ -999,7 +1025,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         mma_warp<D, kS8, kRT>(x);
       } else {
         if constexpr (kS8) scale_warps<D, kRT>(x);
-        else if (warp == 2) clean_warp<D, kRT>(x);
+        else clean_warps<D, kRT>(x);
       }
     } else if (warp < 12) {
       if constexpr (kS8) regs_inc<144>();
