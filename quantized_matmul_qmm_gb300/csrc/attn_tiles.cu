@@ -7,14 +7,21 @@
 //       reference that follows the row's maximum;
 //   O += P V    with P (bf16) over S's columns in TMEM as the A operand and V
 //       as it lies in memory (MN-major B operand).
-// Two streams of S / P / O fill TMEM's 512 columns, so that one stream's
-// exponentials run under the other's products: with kRT = 1 they take the
-// even and the odd cached tiles of the same rows (joined when the item ends),
-// with kRT = 2 the two halves of 256 rows, and each cached tile is fetched
-// once for both.  All products of a block are issued by one thread, in the
-// order S(i + 2), PV(i) of a stream: the tensor pipe runs them in order, so
-// S(i + 2) may overwrite the columns of P(i) behind PV(i), and when S(i + 2)
-// is there, O holds all of PV(i).
+// Two streams, so that one's exponentials run under the other's products: with
+// kRT = 1 they take the even and the odd cached tiles of the same rows (joined
+// when the item ends), with kRT = 2 the two halves of 256 rows, and each
+// cached tile is fetched once for both.  All products of a block are issued by
+// one warp and run in that order.
+//
+// TMEM has 512 columns, and the two O take 256.  A bf16 cache: one S of 128
+// columns for both streams and a P of 64 for each.  A row's scores go to
+// registers at once, the other stream's scores follow into the same columns,
+// and a stream finds its next scores ready when it has stored its weights; the
+// order is S(q + 2), PV(q).  With S and P of a stream in the same columns the
+// next scores could only follow the product with the weights, which left the
+// tensor pipe idle for a third of a tile.  An int8 cache (with the scales there
+// are no registers for a row of scores): S of 128 columns for each stream, P
+// over it, PV(q) before S(q + 2).
 //
 // Up to 64 rows the tile's other 64 lanes hold the same rows again, and their P
 // the part of each weight that the first bf16 rounding left over: the padded
@@ -35,6 +42,7 @@
 // 264 (int8) bytes per token: the cache's bytes up to about 128 rows, the
 // tensor pipe and the exponentials above.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_work.cuh"
 #include "umma.cuh"
@@ -62,7 +70,8 @@ struct Tg {
   static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
   static constexpr int kOffScale = kOffRaw + kRawSlots * kRaw;
   static constexpr int kBytes = kOffScale + (kS8 ? kScaleRing * 2 * kTok * 4 : 0);
-  static constexpr int kAhead = kRT == 1 ? 2 : 1;   // key tiles fetched ahead of the value tiles
+  static constexpr bool kShared = !kS8;          // one S for both streams (see the top)
+  static constexpr int kAhead = (kRT == 1 ? 2 : 1) + (kShared ? 1 : 0);   // key tiles fetched ahead of value tiles
 };
 
 struct TBars {
@@ -70,7 +79,7 @@ struct TBars {
   uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t s_full[2], s_free, p_ready[2], o_done[2];
   uint64_t q_full, o_free, sync;
   uint64_t done;
 };
@@ -86,7 +95,7 @@ struct TShared {
 };
 
 // TMEM columns (the block allocates all 512, which begin at column 0); stream st: + 128 * st
-constexpr int kColS = 0, kColO = 256;
+constexpr int kColS = 0, kColP = 128, kColO = 256;   // kColP (+ 64 * st): with a shared S
 
 struct Ctx {
   const AttnArgs& a;
@@ -96,6 +105,7 @@ struct Ctx {
   // The first tries suspend the thread until the phase completes; only then
   // does the wait read the clock for its limit (the read itself takes long).
   QMM_DEV bool wait(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i)
       if (mbar_try_wait_suspend(bar, parity, kSuspendHintNs)) return true;
@@ -170,10 +180,12 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
     int i;
 #pragma unroll 1
     while (order.next(value, i)) {
-      // value tile i: page[0]; key tile i: page[i - value tiles], kAhead - 1 but for the first
+      // value tile i: page[0]; key tile i: page[i - value tiles]
       int32_t pg = page[0];
       uint32_t pl = places[0];
-      if (!value && i - order.values > 0) pg = page[G::kAhead - 1], pl = places[G::kAhead - 1];
+#pragma unroll
+      for (int j = 1; j < G::kAhead; ++j)
+        if (!value && i - order.values == j) pg = page[j], pl = places[j];
       if (!x.wait_all(&empty[slot], phase)) return;
       const int left = it.len - (it.kv0 + i) * kTok;
       const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
@@ -405,75 +417,66 @@ QMM_DEV void mma_warp(const Ctx& x) {
   constexpr uint32_t kIdS = idesc_f16(128, kTok, true), kIdO = idesc_f16(128, D, true) | kIdescBMnMajor;
   const uint32_t q_s = smem_u32(x.smem), slots = q_s + G::kOffSlots;
   const uint32_t one = elect_one();
-  uint32_t slot = 0, phase = 0, seq = 0, p_phase[2] = {0, 0};
+  uint32_t slot = 0, phase = 0, seq = 0, s_phase = 1, p_phase[2] = {0, 0};
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
     if (!x.wait_all(&b.q_full, seq & 1)) return;
-    const bool both = kRT == 2 && it.n_rows > 128;   // both streams on every tile
-    auto scores = [&](int st, uint32_t tile) {
+    // Steps: (tile, stream) pairs, with kRT == 1 a tile each, streams in turn.
+    const int streams = kRT == 2 && it.n_rows > 128 ? 2 : 1;   // on every tile (kRT == 2)
+    const int steps = it.seg * streams, lead = kRT == 1 ? 2 : streams;
+    int k_slot = 0, v_slot = 0;
+    auto take = [&](int& held) {                 // the next tile of the ring
+      held = slot;
+      if (!x.wait_all(&b.full[slot], phase)) return false;
+      if (++slot == G::kSlots) slot = 0, phase ^= 1;
+      return true;
+    };
+    auto scores = [&](int q) {
+      const int st = kRT == 1 || streams == 2 ? q & 1 : 0;
+      const bool opens = kRT == 1 || st == 0, closes = kRT == 1 || st == streams - 1;
+      if (opens && !take(k_slot)) return false;
+      if constexpr (G::kShared) {                // the step before has been read
+        if (!x.wait_all(&b.s_free, s_phase)) return false;
+        s_phase ^= 1;
+      }
+      tc_fence_after();
       // the address fields do not carry past their 14 bits: shared memory ends below 2^18
-      const uint64_t q_desc = desc_kmajor_sw128(q_s + (kRT == 2 ? st * G::kTile : 0)), k_desc = desc_kmajor_sw128(tile);
+      const uint64_t q_desc = desc_kmajor_sw128(q_s + (kRT == 2 ? st * G::kTile : 0));
+      const uint64_t k_desc = desc_kmajor_sw128(slots + k_slot * G::kTile);
+      const uint32_t d = G::kShared ? kColS : kColS + 128 * st;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-        umma_f16_one(one, kColS + 128 * st, q_desc + at, k_desc + at, kIdS, k > 0);
+        umma_f16_one(one, d, q_desc + at, k_desc + at, kIdS, k > 0);
       }
       umma_commit_one(one, &b.s_full[st]);
+      if (closes) umma_commit_one(one, &b.empty[k_slot]);
+      return true;
     };
-    auto values = [&](int st, uint32_t tile, bool first, bool last) {
-      const uint64_t v_desc = desc_mnmajor_sw128(tile, kHalf);
+    auto values = [&](int q) {
+      const int st = kRT == 1 || streams == 2 ? q & 1 : 0;
+      const bool opens = kRT == 1 || st == 0, closes = kRT == 1 || st == streams - 1;
+      if (!x.wait_all(&b.p_ready[st], p_phase[st])) return false;
+      p_phase[st] ^= 1;
+      if (q == 0 && !x.wait_all(&b.o_free, (seq & 1) ^ 1)) return false;
+      if (opens && !take(v_slot)) return false;
+      tc_fence_after();
+      const uint64_t v_desc = desc_mnmajor_sw128(slots + v_slot * G::kTile, kHalf);
+      const uint32_t d = kColO + 128 * st, p = G::kShared ? kColP + 64 * st : kColS + 128 * st;
 #pragma unroll
       for (int k = 0; k < kTok / 16; ++k)
-        umma_f16_ta_one(one, kColO + 128 * st, kColS + 128 * st + 8 * k, v_desc + k * (2048 >> 4), kIdO,
-                        k > 0 || !first);
-      if (last) umma_commit_one(one, &b.o_done[st]);
+        umma_f16_ta_one(one, d, p + 8 * k, v_desc + k * (2048 >> 4), kIdO, k > 0 || q >= (kRT == 1 ? 2 : streams));
+      if (G::kShared || q + (kRT == 1 ? 2 : streams) >= steps) umma_commit_one(one, &b.o_done[st]);
+      if (closes) umma_commit_one(one, &b.empty[v_slot]);
+      return true;
     };
-    uint32_t v_tile = 0;
-    int v_slot = 0, v_i = 0;
-    bool v_open = false;                         // kRT == 2: stream 1 has value tile v_i still to come
-    TileOrder<G::kAhead> order{it.seg};
-    bool value;
-    int i;
-    // Key tile i + kAhead comes right behind value tile i.  With both streams
-    // on a tile, stream 1's products of value tile i wait until stream 0's
-    // next scores are queued, and the value tile is released then.
 #pragma unroll 1
-    for (;;) {
-      const bool more = order.next(value, i);
-      const int st = kRT == 1 ? i & 1 : 0;
-      const uint32_t tile = slots + slot * G::kTile;
-      if (more) {
-        if (value) {
-          if (!x.wait_all(&b.p_ready[st], p_phase[st])) return;
-          p_phase[st] ^= 1;
-          if (i == 0 && !x.wait(&b.o_free, (seq & 1) ^ 1)) return;
-        }
-        if (!x.wait_all(&b.full[slot], phase)) return;
-        tc_fence_after();
-        if (value) {
-          values(st, tile, i < G::kAhead, i + G::kAhead >= it.seg);
-          v_tile = tile;
-          v_slot = slot;
-          v_i = i;
-          v_open = both;
-        } else {
-          scores(st, tile);
-        }
-      }
-      if (kRT == 2 && v_open && (!more || !value || i == it.seg - 1)) {
-        if (!x.wait_all(&b.p_ready[1], p_phase[1])) return;
-        p_phase[1] ^= 1;
-        tc_fence_after();
-        values(1, v_tile, v_i == 0, v_i == it.seg - 1);
-        umma_commit_one(one, &b.empty[v_slot]);
-        v_open = false;
-      }
-      if (!more) break;
-      if (!value && both) scores(1, tile);
-      if (!value || !both) umma_commit_one(one, &b.empty[slot]);
-      if (++slot == G::kSlots) slot = 0, phase ^= 1;
+    for (int q = -lead; q < steps; ++q) {
+      if (!G::kShared && q >= 0 && !values(q)) return;
+      if (q + lead < steps && !scores(q + lead)) return;
+      if (G::kShared && q >= 0 && !values(q)) return;
     }
   }
 }
@@ -483,12 +486,8 @@ QMM_DEV void mma_warp(const Ctx& x) {
 // rows: scores of the warp's rows in TMEM at t_s become weights (bf16, in half
 // the columns).
 //
-// bf16: one row per lane, and one pass over the scores:
-// the weights are made with the reference of the tiles before while the tile's
-// maximum is found beside them, and only if that passes the reference by more
-// than `slack` (2^8 in the weights; the first tile, and rarely later) the
-// maximum is taken first and the pass made again.  The weights wait in
-// registers until then, because they go over the scores.
+// bf16: one row per lane, all of its scores in registers at once, so that the
+// columns are free for the other stream's scores as soon as they are read.
 struct RowsBf16 {
   float m = -INFINITY;                           // the row's reference, before the scale c
   uint64_t l = 0;                                // the weights' sum, in two halves
@@ -498,87 +497,77 @@ struct RowsBf16 {
     om = m;
     ol = lo + hi;
   }
-  template <typename Seen, typename Rescale>
-  QMM_DEV void tile(uint32_t t_s, const float*, float c, float slack, bool masked, Seen seen, bool low, bool has_o,
-                    Rescale rescale) {
-    constexpr int kW = 32;                       // scores at a time
-    float s[kW];
-    auto load = [&](int q) {                     // hidden ones at -infinity
-      uint32_t r[kW];
-      tmem_ld32(t_s + kW * q, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < kW; ++e) s[e] = __uint_as_float(r[e]);
-      if (masked) {
-        const uint32_t w = seen(kW * q);
-#pragma unroll
-        for (int e = 0; e < kW; ++e)
-          if (!((w >> e) & 1)) s[e] = -INFINITY;
-      }
-    };
-    auto top_of = [&](float top) {
-      float t2[2] = {top, s[0]};
-#pragma unroll
-      for (int e = 1; e < kW - 1; e += 2) t2[(e >> 1) & 1] = fmaxf(fmaxf(t2[(e >> 1) & 1], s[e]), s[e + 1]);
-      return fmaxf(fmaxf(t2[0], t2[1]), s[kW - 1]);
-    };
-    uint32_t p[64];
-    uint64_t lt[2];
-    bool first = __any_sync(0xffffffffu, m == -INFINITY);
-#pragma unroll 1
-    for (;;) {
-      if (first) {
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < kTok / kW; ++q) {
-          load(q);
-          top = top_of(top);
-        }
-        const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          const float next = move ? top : m;
-          const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
-          l = f2_mul(l, f2_pack(f, f));
-          if (has_o) rescale(f);
-          m = next;
-        }
-      }
-      const float mc = m == -INFINITY ? 0.f : m * c;
-      const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
-      lt[0] = lt[1] = 0;
-      float top = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < kTok / kW; ++q) {
-        load(q);
-        top = top_of(top);
-#pragma unroll
-        for (int e = 0; e < kW; e += 2) {
-          f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), s[e], s[e + 1]);
-          s[e] = exp2_approx(s[e]);
-          s[e + 1] = exp2_approx(s[e + 1]);
-          lt[(e >> 1) & 1] = f2_add(lt[(e >> 1) & 1], f2_pack(s[e], s[e + 1]));
-        }
-#pragma unroll
-        for (int e = 0; e < kW / 2; ++e) p[kW / 2 * q + e] = bf16_pair(s[2 * e], s[2 * e + 1]);
-        if (low) {
-#pragma unroll
-          for (int e = 0; e < kW / 2; ++e) {
-            uint32_t& w = p[kW / 2 * q + e];
-            w = bf16_pair(s[2 * e] - bf16lo_to_f32(w), s[2 * e + 1] - bf16hi_to_f32(w));
-          }
-        }
-      }
-      if (first || !__any_sync(0xffffffffu, top > m + slack)) break;
-      first = true;
-    }
-    l = f2_add(l, f2_add(lt[0], lt[1]));
+  // loaded(): the scores have been read.  pv_done(): waits until the products
+  // with the weights before have run (has_o: there were some).
+  template <typename Seen, typename Loaded, typename PvDone, typename Rescale>
+  QMM_DEV bool tile(uint32_t t_s, uint32_t t_p, float c, float slack, bool masked, Seen seen, bool low, bool has_o,
+                    Loaded loaded, PvDone pv_done, Rescale rescale) {
+    float s[kTok];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      uint32_t w[16];
+      uint32_t r[32];
+      tmem_ld32(t_s + 32 * q, r);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = p[16 * q + e];
-      tmem_st16(t_s + 16 * q, w);
+      for (int e = 0; e < 32; ++e) s[32 * q + e] = __uint_as_float(r[e]);
     }
+    tmem_wait_ld();
+    loaded();
+    if (masked) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t w = seen(32 * q);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!((w >> e) & 1)) s[32 * q + e] = -INFINITY;
+      }
+    }
+    float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int e = 4; e < kTok; e += 2) t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], s[e]), s[e + 1]);
+    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+    const bool move = top > m + slack || (m == -INFINITY && top > -INFINITY);
+    bool wait = has_o;
+    if (__any_sync(0xffffffffu, move)) {
+      const float next = move ? top : m;
+      const float f = move ? exp2_approx((m - next) * c) : 1.f;   // m = -infinity: 0
+      l = f2_mul(l, f2_pack(f, f));
+      if (has_o) {
+        if (!pv_done()) return false;
+        wait = false;
+        rescale(f);
+      }
+      m = next;
+    }
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+    uint64_t l2 = 0;
+    uint32_t p[kTok / 2];
+    auto weights = [&](auto low_parts) {
+#pragma unroll
+      for (int e = 0; e < kTok; e += 2) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, mc2), x0, x1);
+        x0 = exp2_approx(x0);
+        x1 = exp2_approx(x1);
+        if (e & 2) l2 = f2_add(l2, f2_pack(x0, x1));
+        else l = f2_add(l, f2_pack(x0, x1));
+        uint32_t w = bf16_pair(x0, x1);
+        if constexpr (decltype(low_parts)::value) w = bf16_pair(x0 - bf16lo_to_f32(w), x1 - bf16hi_to_f32(w));
+        p[e >> 1] = w;
+      }
+    };
+    if (low) weights(std::true_type{});
+    else weights(std::false_type{});
+    l = f2_add(l, l2);
+    if (wait && !pv_done()) return false;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t w[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) w[e] = p[32 * q + e];
+      tmem_st32(t_p + 32 * q, w);
+    }
+    return true;
   }
 };
 
@@ -732,7 +721,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
   const int st = (wid - 4) >> 2, quarter = wid & 3;
   const int trow = 32 * quarter + lane;          // lane of TMEM, row of the tile
   const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
-  const uint32_t t_s = tlane + kColS + 128 * st;
+  const uint32_t t_s = tlane + kColS + (G::kShared ? 0 : 128 * st);
   const float c = a.scale_log2, slack = 8.f / c;
   AttnOwned owned{};
   uint32_t seq = 0, s_count = 0, o_count = 0, tiles = 0, syncs = 0;
@@ -799,7 +788,22 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       if (has) {
         if (!x.wait_all(&b.s_full[st], s_count++ & 1)) return owned;
         tc_fence_after();
-        if (active) {
+        auto loaded = [&]() {
+          if constexpr (G::kShared) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.s_free);
+          }
+        };
+        auto pv_done = [&]() {
+          if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return false;
+          tc_fence_after();
+          return true;
+        };
+        if (!active) {
+          loaded();
+          if (G::kShared && i >= step && !pv_done()) return owned;
+        } else {
           const int tok0 = (it.kv0 + i) * kTok;
           const bool masked = tok0 + kTok > it.q.L;
           // O (of this lane's row) to a new reference
@@ -815,7 +819,12 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
             }
           };
           auto seen = [&](int at) { return live ? attn_sees32(a, it.q, node, tok0 + at) : 0u; };
-          rows.tile(t_s, ksc, c, slack, masked, seen, low, i >= step, rescale);
+          if constexpr (kS8) {
+            rows.tile(t_s, ksc, c, slack, masked, seen, low, i >= step, rescale);
+          } else if (!rows.tile(t_s, tlane + kColP + 64 * st, c, slack, masked, seen, low, i >= step, loaded, pv_done,
+                                rescale)) {
+            return owned;
+          }
           tmem_wait_st();
         }
         tc_fence_before();
@@ -992,6 +1001,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
       mbar_init(&b.p_ready[i], 4);
       mbar_init(&b.o_done[i], 1);
     }
+    mbar_init(&b.s_free, 4);
     mbar_init(&b.q_full, 8);
     mbar_init(&b.o_free, 8);
     mbar_init(&b.sync, 8);
@@ -1016,9 +1026,10 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   if (threadIdx.x == 0) sh.work = work;
   __syncthreads();
   if (any) {
-    // int8: 640 threads at 96 registers; shares per warpgroup 72 + 2 * 144 + 2 * 56 = 472 <= 5 * 96
+    // Registers per warpgroup, of what the launch has: bf16 72 + 2 * 216 = 504 = 3 * 168;
+    // int8 72 + 2 * 144 + 2 * 56 = 472 <= 5 * 96.
     if (warp < 4) {
-      if constexpr (kS8) regs_dec<72>();
+      regs_dec<72>();
       if (warp == 0) {
         load_warp<D, kS8, kRT>(x, mk, mv);
       } else if (warp == 1) {
@@ -1028,7 +1039,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         else clean_warps<D, kRT>(x);
       }
     } else if (warp < 12) {
-      if constexpr (kS8) regs_inc<144>();
+      regs_inc<kS8 ? 144 : 216>();
       owned = row_warps<D, kS8, kQF32, kRT>(x);
     } else {
       if constexpr (kS8) {
