@@ -10,14 +10,13 @@
 // Two streams, so that one's exponentials run under the other's products: with
 // kRT = 1 they take the even and the odd cached tiles of the same rows (joined
 // when the item ends), with kRT = 2 the two halves of 256 rows, and each
-// cached tile is fetched once for both.  All products of a block are issued by
-// one warp and run in that order.
+// cached tile is fetched once for both.
 //
 // TMEM has 512 columns, and the two O take 256.  A bf16 cache: one S of 128
 // columns for both streams and a P of 64 for each.  A row's scores go to
 // registers at once, the other stream's scores follow into the same columns,
-// and a stream finds its next scores ready when it has stored its weights; the
-// order is S(q + 2), PV(q).  With S and P of a stream in the same columns the
+// and a stream finds its next scores ready when it has stored its weights.
+// With S and P of a stream in the same columns the
 // next scores could only follow the product with the weights, which left the
 // tensor pipe idle for a third of a tile.  An int8 cache (with the scales there
 // are no registers for a row of scores): S of 128 columns for each stream, P
@@ -31,10 +30,10 @@
 // weights, so that O is rarely rescaled (it is in TMEM, not in registers).
 //
 // Warps: 0 loads (TMA boxes of page_size's power of two; the pages of a tile
-// looked up by one lane each), 1 issues the products, 2 and 3 clean the value
+// looked up by one lane each), 1 and 2 issue the products, 3 cleans the value
 // tiles that hold the step's own tokens (zeros past the request's end and for
 // non-finite values, see attn_rows.cu), 4..11 are the two streams' rows.  With
-// an int8 cache, tiles arrive as codes, eight more warps write them out as
+// an int8 cache, 1 issues all products, tiles arrive as codes, eight more warps write them out as
 // bf16 in the products' layout, and 2 and 3 bring the scales; a token's key
 // scale multiplies its column of s, its value scale the weight.
 //
@@ -63,6 +62,7 @@ struct Tg {
   static constexpr int kTile = kNH * kHalf;      // bytes of a bf16 tile
   static constexpr int kRaw = kTok * D;          // bytes of a tile of codes
   static constexpr int kSlots = D == 64 ? (kS8 ? 6 : 8) : kS8 ? 3 : (kRT == 1 ? 6 : 5);
+  static constexpr int kKeySlots = kS8 ? kSlots : kSlots / 2;   // bf16: the first ones for keys, the others for values
   static constexpr int kRawSlots = !kS8 ? 0 : D == 64 ? 8 : (kRT == 1 ? 5 : 3);
   static constexpr int kConvWarps = kS8 ? 8 : 0;
   static constexpr int kThreads = 384 + 32 * kConvWarps;
@@ -76,7 +76,7 @@ struct Tg {
 
 struct TBars {
   uint64_t full[8], empty[8];        // bf16 tiles
-  uint64_t tail_full[8];             // value tiles that warps 2 and 3 hand on
+  uint64_t tail_full[8];             // value tiles that warp 3 hands on
   uint64_t raw_full[8], raw_empty[8];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint64_t s_full[2], s_free, p_ready[2], o_done[2];
@@ -129,6 +129,15 @@ struct TileOrder {
   }
 };
 
+// A ring of n slots from `base` on: the next slot, and its barriers' phase.
+struct Ring {
+  uint32_t base, n, slot, phase;
+  QMM_DEV Ring(uint32_t b, uint32_t count, uint32_t ph) : base(b), n(count), slot(b), phase(ph) {}
+  QMM_DEV void next() {
+    if (++slot == base + n) slot = base, phase ^= 1;
+  }
+};
+
 // ---- warp 0: tiles into shared memory ----
 // One warp's chain of instructions per tile has to stay well under the tile's
 // time at HBM rate (0.8 to 1.5 us): places of a tile follow from the last
@@ -149,7 +158,7 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
   const uint32_t box_bytes = box * D * (kS8 ? 1 : 2);
   const int lane_tok = lane * (int)box;
   const uint32_t step_blk = kTok / P, step_place = kTok % P;
-  uint32_t slot = 0, phase = 1;
+  Ring keys(0, kS8 ? kN : G::kKeySlots, 1), vals(G::kKeySlots, kN - G::kKeySlots, 1);
   if (lane == 0) {
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
@@ -186,14 +195,13 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
 #pragma unroll
       for (int j = 1; j < G::kAhead; ++j)
         if (!value && i - order.values == j) pg = page[j], pl = places[j];
-      if (!x.wait_all(&empty[slot], phase)) return;
+      Ring& ring = !kS8 && value ? vals : keys;
+      const uint32_t slot = ring.slot;
+      if (!x.wait_all(&empty[slot], ring.phase)) return;
       const int left = it.len - (it.kv0 + i) * kTok;
       const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
       uint64_t* landed = !kS8 && value && it.q.n + kTok > left ? &x.sh->bar.tail_full[slot] : &full[slot];
-      if (lane == 0) {
-        if (!kS8 && landed == &full[slot]) mbar_arrive(landed);   // for the second cleaner
-        mbar_arrive_expect_tx(landed, boxes * box_bytes);
-      }
+      if (lane == 0) mbar_arrive_expect_tx(landed, boxes * box_bytes);
       __syncwarp();
       if (lane < boxes) {
         if ((uint32_t)pg >= (uint64_t)a.cache.n_pages) {   // reported; page 0 stands in
@@ -209,7 +217,7 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
           for (int hf = 0; hf < G::kNH; ++hf) tma_load_4d(dst + hf * kHalf, map, landed, 64 * hf, pl, it.h, pg);
         }
       }
-      if (++slot == kN) slot = 0, phase ^= 1;
+      ring.next();
       if (value) {
 #pragma unroll
         for (int j = 0; j < kWin - 1; ++j) page[j] = page[j + 1], places[j] = places[j + 1];
@@ -336,40 +344,37 @@ QMM_DEV void convert_warps(const Ctx& x) {
   }
 }
 
-// ---- bf16: warps 2 and 3 clean the value tiles that reach past the context,
-// half of the rows each, and hand them on ----
-// Both see every phase of every slot's barrier (a warp that skipped some could
-// take an old phase for the one it waits for).  Eight 16-byte pieces at a time
-// are tested together: exponents of all ones carry into the sign bit.
+// ---- bf16: warp 3 cleans the value tiles that reach past the context and
+// hands them on ----
+// Eight 16-byte pieces per lane are tested together: exponents of all ones
+// carry into the sign bit.
 template <int D, int kRT>
-QMM_DEV void clean_warps(const Ctx& x) {
+QMM_DEV void clean_warp(const Ctx& x) {
   using G = Tg<D, false, kRT>;
   const AttnArgs& a = x.a;
   constexpr int kP = D / 8;                      // pieces of a row
   constexpr int kBatch = 32 * 8 / kP;            // rows of a batch
   const int lane = threadIdx.x & 31, t_lane = lane / kP, p = lane % kP;
-  const int t_first = ((threadIdx.x >> 5) & 1) * (kTok / 2);
-  uint32_t n = 0, seq = 0, phases = 0;           // phases: a bit per slot
+  uint32_t seq = 0, phases = 0;                  // phases: a bit per slot
+  Ring vals(G::kKeySlots, G::kSlots - G::kKeySlots, 0);
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    if (t_first == 0 && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
-    TileOrder<G::kAhead> order{it.seg};
-    bool value;
-    int i;
+    if (lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
 #pragma unroll 1
-    while (order.next(value, i)) {
-      const int slot = n++ % G::kSlots;
+    for (int i = 0; i < it.seg; ++i) {
+      const uint32_t slot = vals.slot;
+      vals.next();
       const int tok0 = (it.kv0 + i) * kTok;
-      if (!value || tok0 + kTok <= it.q.L) continue;
+      if (tok0 + kTok <= it.q.L) continue;
       const uint32_t parity = (phases >> slot) & 1;
       phases ^= 1u << slot;
       if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return;
       const uint32_t base = smem_u32(x.smem) + G::kOffSlots + slot * G::kTile + (p >> 3) * kHalf;
       bool bad = false;
 #pragma unroll 1
-      for (int t0 = t_first; t0 < t_first + kTok / 2; t0 += kBatch) {
+      for (int t0 = 0; t0 < kTok; t0 += kBatch) {
         if (tok0 + t0 + kBatch <= it.q.L) continue;   // cached tokens only
         auto at = [&](int k) {
           const int t = t0 + k * (32 / kP) + t_lane;
@@ -405,38 +410,42 @@ QMM_DEV void clean_warps(const Ctx& x) {
   }
 }
 
-// ---- warp 1: the products ----
-// The warp runs in step and one lane issues: operands that only the issuing
+// ---- warp 1 (bf16: 1 and 2): the products ----
+// A bf16 cache has a warp for the scores and one for the products with the
+// values: nothing orders the two but the barriers, so neither waits while the
+// other could issue.  With int8 (P over S) one warp issues both, in order.
+// A warp runs in step and one lane issues: operands that only the issuing
 // lane held would each be moved to a uniform register first, and 16 or 32
 // products per tile (64 to 80 cycles each) leave no time for that.
 template <int D, bool kS8, int kRT>
-QMM_DEV void mma_warp(const Ctx& x) {
+QMM_DEV void mma_warp(const Ctx& x, bool do_scores, bool do_values) {
   using G = Tg<D, kS8, kRT>;
   const AttnArgs& a = x.a;
   TBars& b = x.sh->bar;
   constexpr uint32_t kIdS = idesc_f16(128, kTok, true), kIdO = idesc_f16(128, D, true) | kIdescBMnMajor;
   const uint32_t q_s = smem_u32(x.smem), slots = q_s + G::kOffSlots;
   const uint32_t one = elect_one();
-  uint32_t slot = 0, phase = 0, seq = 0, s_phase = 1, p_phase[2] = {0, 0};
+  uint32_t seq = 0, s_phase = 1, p_phase[2] = {0, 0};
+  Ring keys(0, G::kKeySlots, 0), vals(G::kKeySlots, G::kSlots - G::kKeySlots, 0);   // int8: `keys` for both
   AttnWalk walk;
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
-    if (!x.wait_all(&b.q_full, seq & 1)) return;
+    if (do_scores && !x.wait_all(&b.q_full, seq & 1)) return;
     // Steps: (tile, stream) pairs, with kRT == 1 a tile each, streams in turn.
     const int streams = kRT == 2 && it.n_rows > 128 ? 2 : 1;   // on every tile (kRT == 2)
     const int steps = it.seg * streams, lead = kRT == 1 ? 2 : streams;
-    int k_slot = 0, v_slot = 0;
-    auto take = [&](int& held) {                 // the next tile of the ring
-      held = slot;
-      if (!x.wait_all(&b.full[slot], phase)) return false;
-      if (++slot == G::kSlots) slot = 0, phase ^= 1;
+    uint32_t k_slot = 0, v_slot = 0;
+    auto take = [&](Ring& ring, uint32_t& held) {
+      held = ring.slot;
+      if (!x.wait_all(&b.full[held], ring.phase)) return false;
+      ring.next();
       return true;
     };
     auto scores = [&](int q) {
       const int st = kRT == 1 || streams == 2 ? q & 1 : 0;
       const bool opens = kRT == 1 || st == 0, closes = kRT == 1 || st == streams - 1;
-      if (opens && !take(k_slot)) return false;
+      if (opens && !take(keys, k_slot)) return false;
       if constexpr (G::kShared) {                // the step before has been read
         if (!x.wait_all(&b.s_free, s_phase)) return false;
         s_phase ^= 1;
@@ -461,7 +470,7 @@ QMM_DEV void mma_warp(const Ctx& x) {
       if (!x.wait_all(&b.p_ready[st], p_phase[st])) return false;
       p_phase[st] ^= 1;
       if (q == 0 && !x.wait_all(&b.o_free, (seq & 1) ^ 1)) return false;
-      if (opens && !take(v_slot)) return false;
+      if (opens && !take(kS8 ? keys : vals, v_slot)) return false;
       tc_fence_after();
       const uint64_t v_desc = desc_mnmajor_sw128(slots + v_slot * G::kTile, kHalf);
       const uint32_t d = kColO + 128 * st, p = G::kShared ? kColP + 64 * st : kColS + 128 * st;
@@ -474,9 +483,8 @@ QMM_DEV void mma_warp(const Ctx& x) {
     };
 #pragma unroll 1
     for (int q = -lead; q < steps; ++q) {
-      if (!G::kShared && q >= 0 && !values(q)) return;
-      if (q + lead < steps && !scores(q + lead)) return;
-      if (G::kShared && q >= 0 && !values(q)) return;
+      if (do_values && q >= 0 && !values(q)) return;
+      if (do_scores && q + lead < steps && !scores(q + lead)) return;
     }
   }
 }
@@ -984,7 +992,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
   TBars& b = sh.bar;
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kSlots; ++i) {
-      mbar_init(&b.full[i], kS8 ? G::kConvWarps : 2);   // converters, or the loads (twice) or the cleaners
+      mbar_init(&b.full[i], kS8 ? G::kConvWarps : 1);   // converters, or the loads or the cleaner
       mbar_init(&b.empty[i], 1);
       mbar_init(&b.tail_full[i], 1);
     }
@@ -1005,7 +1013,7 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     mbar_init(&b.q_full, 8);
     mbar_init(&b.o_free, 8);
     mbar_init(&b.sync, 8);
-    mbar_init(&b.done, 1);
+    mbar_init(&b.done, kS8 ? 1 : 2);
     sh.abort = 0;
     for (int i = 0; i < kBadRing; ++i) sh.bad[i] = 0;
     fence_mbar_init();
@@ -1032,11 +1040,11 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
       regs_dec<72>();
       if (warp == 0) {
         load_warp<D, kS8, kRT>(x, mk, mv);
-      } else if (warp == 1) {
-        mma_warp<D, kS8, kRT>(x);
+      } else if (warp == 1 || (!kS8 && warp == 2)) {
+        mma_warp<D, kS8, kRT>(x, warp == 1, kS8 || warp == 2);
       } else {
         if constexpr (kS8) scale_warps<D, kRT>(x);
-        else clean_warps<D, kRT>(x);
+        else clean_warp<D, kRT>(x);
       }
     } else if (warp < 12) {
       regs_inc<kS8 ? 144 : 216>();
@@ -1062,11 +1070,10 @@ attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     drain(kS8 ? b.raw_full : b.full, kS8 ? G::kRawSlots : G::kSlots);
     if (!kS8) drain(b.tail_full, G::kSlots);
   }
+  if (sh.abort && (warp == 1 || (!kS8 && warp == 2))) umma_commit_one(elect_one(), &b.done);
   if (warp == 1) {
-    if (sh.abort && lane == 0) {                 // else every product has been waited for
-      umma_commit(&b.done);
-      mbar_drain(&b.done, 0, 100000000ull);
-    }
+    // without an abort every product has been waited for
+    if (sh.abort && lane == 0) mbar_drain(&b.done, 0, 100000000ull);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(sh.tmem, 512);
