@@ -553,7 +553,8 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   constexpr int kJoin = kWarps * 16 * MT * (D + 8) * 4;
   constexpr int kSmem = 128 + std::max(kWarps * Geo<D, kS8>::kRing, kJoin);
   auto kern = attn_rows_kernel<D, kS8, kQF32, MT>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t err = set_once(set, (const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
   return launch_pdl(kern, dim3(a.grid), dim3(kThreads), kSmem, stream, a);
 }
@@ -580,8 +581,9 @@ template <int D>
 static cudaError_t launch_combine(const AttnArgs& a, int rows_per_tile, cudaStream_t stream) {
   // the attention kernels' shared-memory configuration: an SM that had to
   // change it would drain first
-  cudaError_t err = cudaFuncSetAttribute(attn_combine_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         cudaSharedmemCarveoutMaxShared);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t err = set_once(set, (const void*)attn_combine_kernel<D>,
+                                   cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (err != cudaSuccess) return err;
   return launch_pdl(attn_combine_kernel<D>, dim3(kCombinePerSm * attn_sm_count()), dim3(kCombineThreads), 0, stream, a,
                     rows_per_tile);
@@ -594,8 +596,12 @@ cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_tile, int head_d
 // ---- the choice of a kernel, shared by the size query and the call ----
 
 int attn_sm_count() {
+  static std::atomic<int> known[64] = {};       // per device
   int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaGetDevice(&dev) != cudaSuccess) return sms;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && dev < 64)
+    known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

@@ -1093,7 +1093,8 @@ cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t stream) {
       !make_tmap_kv(&mv, c.v, kS8, D, c.page_size, c.n_heads, c.n_pages, c.st_token, c.st_head, c.st_page, box))
     return cudaErrorInvalidValue;
   auto kern = attn_tiles_kernel<D, kS8, kQF32, kRT>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t err = set_once(set, (const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
   return launch_pdl(kern, dim3(a.grid), dim3(G::kThreads), kSmem, stream, a, mk, mv, box);
 }

@@ -2,9 +2,24 @@
 // append of its rows and the attention that reads them.
 #pragma once
 
+#include <atomic>
+
 #include "qmm_internal.h"
 
 namespace qmm {
+
+// A kernel's attribute, set once per process and device: the runtime call costs
+// about as much as an argument check of the whole entry point.
+inline cudaError_t set_once(std::atomic<uint64_t>& done, const void* kernel, cudaFuncAttribute attr, int value) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, attr, value);
+  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
 
 // ---- plan (kv_plan.cu) ----
 constexpr int64_t kPlanMaxRequests = 16384;   // three int32 per request fit one block's shared memory

@@ -163,14 +163,13 @@ kv_plan_kernel(const KvPlanArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t smem = (size_t)a.R * 12;
-  cudaError_t err = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(kPlanMaxRequests * 12));
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t err = set_once(set, (const void*)kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)(kPlanMaxRequests * 12));
   if (err != cudaSuccess) return err;
   const int64_t blocks = ((int64_t)a.max_tokens + kPlanThreads - 1) / kPlanThreads;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, 2 * sms));
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, 2 * attn_sm_count()));
   return launch_pdl(kv_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, stream, a);
 }
 

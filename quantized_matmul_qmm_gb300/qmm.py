@@ -142,6 +142,12 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _stream_of(t):
+    """The handle of torch's current stream on t's device (a decoding step makes
+    many small calls: _stream's Stream object alone takes 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _size(fn, *args) -> int:
     out = ctypes.c_size_t(0)
     _check(fn, getattr(lib, fn)(*args, ctypes.byref(out)))
@@ -538,7 +544,7 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Te
         ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.shape[0],
         block_table.data_ptr(), block_table.stride(0), block_table.shape[1], page_size, _addr(parents), _addr(mask),
         ld_mask, words, T, cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), pages_taken.data_ptr(),
-        _addr(dev_status), _stream()))
+        _addr(dev_status), _stream_of(slots)))
     return cu_new, pages_taken
 
 
@@ -554,7 +560,7 @@ def kv_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, k_cache: to
         raise ValueError("kv_append: K, V, slots and the cache do not agree")
     _check("qmm_kv_append", lib.qmm_kv_append(
         K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, _ROW_TYPES[K.dtype], K.shape[0], slots.data_ptr(),
-        ctypes.byref(cache), _addr(dev_status), _stream()))
+        cache, _addr(dev_status), _stream_of(k_cache)))
 
 
 def tree_attention_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
@@ -581,11 +587,11 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         workspace = torch.empty(tree_attention_workspace_size(heads, k_cache.shape[2], head_dim, max_new),
                                 dtype=torch.uint8, device=q.device)
     _check("qmm_tree_attention", lib.qmm_tree_attention(
-        q.data_ptr(), _ROW_TYPES[q.dtype], qt, qh, heads, ctypes.byref(cache), block_table.data_ptr(),
+        q.data_ptr(), _ROW_TYPES[q.dtype], qt, qh, heads, cache, block_table.data_ptr(),
         block_table.stride(0), block_table.shape[1], ctx_lens.data_ptr(), cu_new.data_ptr(), ctx_lens.shape[0], T,
         max_new, _addr(mask), 0 if mask is None else mask.stride(0),
         head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _addr(dev_status), _stream()))
+        workspace.nbytes, _addr(dev_status), _stream_of(q)))
     return out
 
 
