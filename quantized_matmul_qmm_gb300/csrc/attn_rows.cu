@@ -46,18 +46,22 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;                       // cached tokens per warp step
 constexpr int kTileTokens = kGroup * kWarps;     // a unit
 constexpr int kBlocksPerSm = 2;
+// int8 with 16 rows: three blocks.  Its loads are half as long and its
+// instructions more, so that the stream waits for issue slots, not bytes.
+constexpr int blocks_per_sm(bool s8, int mt) { return s8 && mt == 1 ? 3 : kBlocksPerSm; }
 constexpr int kRingBytes = 24576;                // per warp
 constexpr int kCombineMaxOwners = 512;           // blocks of an attention grid, at most
 // More query rows per key head than this go to the tile kernel (attn_tiles.cu).
 constexpr int64_t kRowsKernelMax = 16;
 
-template <int D, bool kS8>
+template <int D, bool kS8, int MT>
 struct Geo {
   static constexpr int kRow = D * (kS8 ? 1 : 2);             // bytes of a row
   static constexpr int kPieces = kRow / 16;                  // 16-byte pieces of a row
   static constexpr int kSide = kGroup * kRow;                // K or V of a group
   static constexpr int kStage = 2 * kSide + (kS8 ? 2 * kGroup * 4 : 0);
-  static constexpr int kStages = kRingBytes / kStage < 8 ? kRingBytes / kStage : 8;
+  static constexpr int kRingMax = kRingBytes * kBlocksPerSm / blocks_per_sm(kS8, MT);
+  static constexpr int kStages = kRingMax / kStage < 8 ? kRingMax / kStage : 8;
   static constexpr int kRing = kStages * kStage;
   // Place of piece p of key row t: a quarter warp reads 4 pieces of 2 rows.
   QMM_DEV static uint32_t k_at(int t, int p) {
@@ -94,9 +98,9 @@ QMM_DEV uint2 lds64(uint32_t addr) {
 }
 
 template <int D, bool kS8, bool kQF32, int MT>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(kS8, MT))
 attn_rows_kernel(const __grid_constant__ AttnArgs a) {
-  using G = Geo<D, kS8>;
+  using G = Geo<D, kS8, MT>;
   constexpr int kRows = 16 * MT;
   constexpr int kSteps = D / 16;                 // mma steps over the head's dimensions
   constexpr int kTiles = D / 8;                  // 8-column tiles of the output
@@ -551,7 +555,7 @@ attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
 template <int D, bool kS8, bool kQF32, int MT>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   constexpr int kJoin = kWarps * 16 * MT * (D + 8) * 4;
-  constexpr int kSmem = 128 + std::max(kWarps * Geo<D, kS8>::kRing, kJoin);
+  constexpr int kSmem = 128 + std::max(kWarps * Geo<D, kS8, MT>::kRing, kJoin);
   auto kern = attn_rows_kernel<D, kS8, kQF32, MT>;
   static std::atomic<uint64_t> set{0};
   const cudaError_t err = set_once(set, (const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -613,10 +617,10 @@ bool attn_pages_tile(const KvView& c, bool s8) {
          (!s8 || (aligned(c.k_scale, 16) && aligned(c.v_scale, 16)));
 }
 
-AttnPlan attn_plan(int64_t rows, bool pages_tile) {
-  const int sms = std::min(attn_sm_count(), kCombineMaxOwners / kBlocksPerSm);
+AttnPlan attn_plan(int64_t rows, bool pages_tile, bool s8) {
+  const int sms = std::min(attn_sm_count(), kCombineMaxOwners / 3);
   if (rows > kRowsKernelMax && pages_tile) return {true, rows <= 128 ? 128 : 256, sms};
-  return {false, rows <= 16 ? 16 : 32, kBlocksPerSm * sms};
+  return {false, rows <= 16 ? 16 : 32, blocks_per_sm(s8, rows <= 16 ? 1 : 2) * sms};
 }
 
 namespace {
@@ -627,11 +631,13 @@ size_t plan_bytes(const AttnPlan& p, int head_dim) {
 }  // namespace
 
 size_t attn_workspace_bytes(int64_t rows, int head_dim) {
-  return std::max(plan_bytes(attn_plan(rows, true), head_dim), plan_bytes(attn_plan(rows, false), head_dim));
+  size_t most = 0;                               // whatever the cache's type and pages turn out to be
+  for (int i = 0; i < 4; ++i) most = std::max(most, plan_bytes(attn_plan(rows, i & 1, i & 2), head_dim));
+  return most;
 }
 
 cudaError_t launch_attn(AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, void* workspace, cudaStream_t stream) {
-  const AttnPlan p = attn_plan((int64_t)a.max_new * a.group, attn_pages_tile(a.cache, cache_s8));
+  const AttnPlan p = attn_plan((int64_t)a.max_new * a.group, attn_pages_tile(a.cache, cache_s8), cache_s8);
   a.grid = p.grid;
   const size_t rows = 2 * (size_t)p.grid * p.rows_per_tile;
   a.part_o = static_cast<float*>(workspace);

@@ -109,9 +109,9 @@ struct AttnPlan {
 };
 int attn_sm_count();
 // `pages_tile`: the cache's pages and scales allow TMA boxes (attn_pages_tile).
-AttnPlan attn_plan(int64_t rows, bool pages_tile);
+AttnPlan attn_plan(int64_t rows, bool pages_tile, bool s8);
 bool attn_pages_tile(const KvView& c, bool s8);
-size_t attn_workspace_bytes(int64_t rows, int head_dim);   // for either kernel
+size_t attn_workspace_bytes(int64_t rows, int head_dim);   // for any cache
 cudaError_t launch_attn(AttnArgs& a, bool q_f32, bool cache_s8, int head_dim, void* workspace, cudaStream_t stream);
 // one of the two kernels, and the joining of items that blocks share (attn_rows.cu)
 cudaError_t launch_attn_rows(const AttnArgs& a, int rows_per_tile, bool q_f32, bool cache_s8, int head_dim,
