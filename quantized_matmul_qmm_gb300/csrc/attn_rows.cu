@@ -32,6 +32,7 @@
 // non-finite values among the new tokens are taken out of the ring, and added
 // at the end to the rows that do see them.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_work.cuh"
 #include "umma.cuh"
@@ -134,6 +135,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
 
     // ---- the ring ----
     const int32_t* trow = a.table + (int64_t)im.r * a.ld_table;
+    const bool one_page = a.cache.page_size % kGroup == 0;   // a group of 16 tokens never crosses a page
     const uint8_t* kbase = a.cache.k + h * a.cache.st_head;
     const uint8_t* vbase = a.cache.v + h * a.cache.st_head;
     auto page_of = [&](int it) -> int32_t {      // of this lane's token of step it, -1 past the end
@@ -148,15 +150,31 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
       const uint32_t dst = ring + (it % G::kStages) * G::kStage;
       if (it < seg) {
         constexpr int kRowsPer = 32 / G::kPieces;
-        const int p = lane % G::kPieces;
+        const int p = lane % G::kPieces, t_lane = lane / G::kPieces;
+        if (one_page) {                          // the group's rows lie at one stride
+          const int64_t first = __shfl_sync(0xffffffffu, at, 0);
+          const int left = first >= 0 ? len - (tok_first + it * kTileTokens) : 0;
+          const uint8_t* k = kbase + (first >= 0 ? first : 0) + t_lane * a.cache.st_token + p * 16;
+          const uint8_t* v = vbase + (k - kbase);
 #pragma unroll
-        for (int i = 0; i < kGroup / kRowsPer; ++i) {
-          const int t = lane / G::kPieces + i * kRowsPer;
-          const int64_t ro = __shfl_sync(0xffffffffu, at, t);
-          const uint32_t bytes = ro >= 0 ? 16u : 0u;
-          const int64_t src = ro >= 0 ? ro + p * 16 : 0;
-          cp_async16_zfill(dst + G::k_at(t, p), kbase + src, bytes);
-          cp_async16_zfill(dst + G::kSide + G::v_at(t, p), vbase + src, bytes);
+          for (int i = 0; i < kGroup / kRowsPer; ++i) {
+            const int t = t_lane + i * kRowsPer;
+            const uint32_t bytes = t < left ? 16u : 0u;   // 0: nothing is read
+            cp_async16_zfill(dst + G::k_at(t, p), k, bytes);
+            cp_async16_zfill(dst + G::kSide + G::v_at(t, p), v, bytes);
+            k += kRowsPer * a.cache.st_token;
+            v += kRowsPer * a.cache.st_token;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kGroup / kRowsPer; ++i) {
+            const int t = t_lane + i * kRowsPer;
+            const int64_t ro = __shfl_sync(0xffffffffu, at, t);
+            const uint32_t bytes = ro >= 0 ? 16u : 0u;
+            const int64_t src = ro >= 0 ? ro + p * 16 : 0;
+            cp_async16_zfill(dst + G::k_at(t, p), kbase + src, bytes);
+            cp_async16_zfill(dst + G::kSide + G::v_at(t, p), vbase + src, bytes);
+          }
         }
         if constexpr (kS8) {                     // lanes 0..15: key scales, 16..31: value scales
           const float* sc = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
@@ -179,13 +197,16 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
     }
 
     // ---- the query rows, as A fragments in the order of the key's pieces ----
+    // int8, up to 8 rows: they stand in rows 8..15 again, whose weights are the
+    // low parts, so that the products with those cost no instructions of their own
+    const bool fold = kS8 && MT == 1 && n_rows <= 8;
     uint32_t qf[MT][kSteps][4];
     int node[MT][2];                             // the new token of each of the thread's rows, -1: no row
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int rr = mt * 16 + hf * 8 + g;
+        const int rr = fold ? g : mt * 16 + hf * 8 + g;
         const bool live = rr < n_rows;
         const int row = row0 + rr, i = row / a.group;
         node[mt][hf] = live ? i : -1;
@@ -202,6 +223,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
               v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + qo + d);
             }
           }
+          // int8 codes leave a word in the order 0, 2, 1, 3, which needs no byte permutes
+          if constexpr (kS8) v = make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
           qf[mt][s][hf] = v.x;
           qf[mt][s][2 + hf] = v.y;
         }
@@ -253,7 +276,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4) {
                 const uint32_t word = u4_get(kk, q4);
-                const uint32_t b0 = s8_low_pair(word), b1 = s8_high_pair(word);
+                const uint32_t b0 = s8_lanes_to_bf16(word), b1 = s8_lanes_to_bf16(word >> 8);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) mma_bf16(s[mt][nt], qf[mt][4 * i + q4], b0, b1);
               }
@@ -333,8 +356,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
                 p1 = (seen[mt] >> (nt * 4 + 2 * hf + 1)) & 1 ? p1 * vs[nt][1] : 0.f;
               }
               const uint32_t hi = bf16_pair(p0, p1);
-              pf[mt][2 * nt + hf] = hi;
               pl[mt][2 * nt + hf] = bf16_pair(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
+              pf[mt][2 * nt + hf] = fold && hf == 1 ? pl[mt][2 * nt + hf] : hi;
             }
           }
         }
@@ -370,17 +393,17 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
           }
 #pragma unroll
           for (int q = 0; q < kWords; ++q) {
-            const uint32_t a01 = __byte_perm(x[0][q], x[1][q], 0x5140), a23 = __byte_perm(x[0][q], x[1][q], 0x7362);
-            const uint32_t b01 = __byte_perm(x[2][q], x[3][q], 0x5140), b23 = __byte_perm(x[2][q], x[3][q], 0x7362);
+            // [A0 A1 B0 B1], [A2 A3 B2 B3] of tokens A and B: the odd ones one byte up
+            const uint32_t a01 = __byte_perm(x[0][q], x[1][q], 0x5410), a23 = __byte_perm(x[0][q], x[1][q], 0x7632);
+            const uint32_t b01 = __byte_perm(x[2][q], x[3][q], 0x5410), b23 = __byte_perm(x[2][q], x[3][q], 0x7632);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t aw = e < 2 ? a01 : a23, bw = e < 2 ? b01 : b23;
-              const uint32_t b0 = (e & 1) ? s8_high_pair(aw) : s8_low_pair(aw);
-              const uint32_t b1 = (e & 1) ? s8_high_pair(bw) : s8_low_pair(bw);
+              const uint32_t b0 = s8_lanes_to_bf16(e & 1 ? aw >> 8 : aw), b1 = s8_lanes_to_bf16(e & 1 ? bw >> 8 : bw);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 mma_bf16(o[mt][4 * q + e], pf[mt], b0, b1);
-                mma_bf16(o[mt][4 * q + e], pl[mt], b0, b1);
+                if (!fold) mma_bf16(o[mt][4 * q + e], pl[mt], b0, b1);
               }
             }
           }
@@ -442,6 +465,10 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
         sum += s_ml[1][i][rr] * (mi == -INFINITY ? 0.f : exp2_approx(mi - top));
         const float4 v = *reinterpret_cast<const float4*>(joined + (i * kRows + rr) * kPitch + d);
         x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+        if (fold) {
+          const float4 w = *reinterpret_cast<const float4*>(joined + (i * kRows + rr + 8) * kPitch + d);
+          x[0] += w.x, x[1] += w.y, x[2] += w.z, x[3] += w.w;
+        }
       }
       if (!kS8 && s_bad) attn_add_nonfinite(a, im, kTileTokens, (row0 + rr) / a.group, d, x);
       if (im.whole) {
@@ -461,27 +488,30 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
 // Joins the pieces of the items that several blocks computed: piece 0 is the
 // owner block's slot 1, the others the following blocks' slot 0.  Each block
 // adds up all owners' rows and its warps take rows at the grid's pitch, so that
-// a few long items keep the whole GPU busy; a warp first holds the pieces'
-// maxima and sums, one per lane, then four (two) columns per lane, eight
-// pieces' loads in flight.  What costs is the chain of loads (owners, maxima,
-// values), a few us however little there is to join.
+// a few long items keep the whole GPU busy; a warp holds the pieces' maxima and
+// sums, one per lane, and four (two) columns of them per lane, eight pieces at
+// a time.  What costs is the chain of loads, a few us however little there is
+// to join: the owners, then maxima, sums and the first eight pieces together.
 constexpr int kCombineThreads = 256;
 constexpr int kCombinePerSm = 4;
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads, kCombinePerSm)
 attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
   __shared__ int s_end[kCombineMaxOwners];       // running sum of the owners' rows
+  __shared__ int4 s_own[kCombineMaxOwners];      // h, row0, pieces, first
   __shared__ int s_warp[kCombineThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kV = D / 32;                     // columns per lane
   constexpr int kPer = kCombineMaxOwners / kCombineThreads;
+  using Vec = typename std::conditional<kV == 4, float4, float2>::type;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   int rows[kPer], incl = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int b = threadIdx.x * kPer + k;
     rows[k] = b < a.grid ? a.owned_rows[b] : 0;
+    s_own[b] = b < a.grid ? a.owned[b] : make_int4(0, 0, 0, 0);   // without rows: not looked at
     incl += rows[k];
   }
   const int mine = incl;
@@ -510,34 +540,39 @@ attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
       if (s_end[mid] > i) hi = mid; else lo = mid + 1;
     }
     const int b = lo, rr = i - (lo > 0 ? s_end[lo - 1] : 0);
-    const int4 own = a.owned[b];                 // h, row0, pieces, first
+    const int4 own = s_own[b];
     const int pieces = own.z;
-    auto at = [&](int p, int rr) { return (int64_t)(p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
-    float top = -INFINITY;
-    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, a.part_ml[at(p, rr)].x);
+    auto at = [&](int p) { return (int64_t)(p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
+    Vec v[8];
+    auto fetch = [&](int p0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p0 + k < pieces) v[k] = *reinterpret_cast<const Vec*>(a.part_o + at(p0 + k) * D + lane * kV);
+    };
+    fetch(0);
+    const float2 ml0 = lane < pieces ? a.part_ml[at(lane)] : make_float2(-INFINITY, 0.f);
+    float top = ml0.x;
+#pragma unroll 1
+    for (int p = 32 + lane; p < pieces; p += 32) top = fmaxf(top, a.part_ml[at(p)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float x[kV] = {}, sum = 0.f;
+    float x[kV] = {}, sum = 0.f, f = 0.f;
 #pragma unroll 1
-    for (int p0 = 0; p0 < pieces; p0 += 32) {
-      const int n = min(32, pieces - p0);
-      float f = 0.f;
-      if (lane < n) {
-        const float2 ml = a.part_ml[at(p0 + lane, rr)];
+    for (int p0 = 0; p0 < pieces; p0 += 8) {
+      if ((p0 & 31) == 0) {                      // the next 32 pieces' factors
+        const float2 ml = p0 == 0 ? ml0 : p0 + lane < pieces ? a.part_ml[at(p0 + lane)] : make_float2(-INFINITY, 0.f);
         // a piece without a maximum has no weight, unless its scores were not numbers
         f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
         sum += ml.y * f;
       }
-#pragma unroll 8
-      for (int p = 0; p < n; ++p) {
-        const float fp = __shfl_sync(0xffffffffu, f, p);
-        const float* src = a.part_o + at(p0 + p, rr) * D + lane * kV;
-        if constexpr (kV == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          x[0] += v.x * fp, x[1] += v.y * fp, x[2] += v.z * fp, x[3] += v.w * fp;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          x[0] += v.x * fp, x[1] += v.y * fp;
+      if (p0 > 0) fetch(p0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float fp = __shfl_sync(0xffffffffu, f, (p0 + k) & 31);
+        if (p0 + k < pieces) {
+          const float* e = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+          for (int j = 0; j < kV; ++j) x[j] = fmaf(e[j], fp, x[j]);
         }
       }
     }

@@ -246,8 +246,9 @@ QMM_DEV uint32_t bf16_pair(float lo, float hi) {
   return r;
 }
 
-// Two int8 codes in the low bytes of 16-bit lanes -> bf16x2, exactly: the low
-// seven bits on top of 128, and -128 or (sign bit) -256 added.
+// Two int8 codes in the low bytes of 16-bit lanes (the high bytes may hold
+// anything) -> bf16x2, exactly: the low seven bits on top of 128, and -128 or
+// (sign bit) -256 added.
 QMM_DEV uint32_t s8_lanes_to_bf16(uint32_t x) {
   uint32_t lo, hi, r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(x), "r"(0x007F007Fu), "r"(0x43004300u));
@@ -255,8 +256,6 @@ QMM_DEV uint32_t s8_lanes_to_bf16(uint32_t x) {
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(hi));
   return r;
 }
-QMM_DEV uint32_t s8_low_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4140)); }
-QMM_DEV uint32_t s8_high_pair(uint32_t w) { return s8_lanes_to_bf16(__byte_perm(w, 0, 0x4342)); }
 
 // Zeros in place of the non-finite ones of eight bf16 values; whether there were any.
 QMM_DEV bool bf16_drop_nonfinite(uint4& v) {
