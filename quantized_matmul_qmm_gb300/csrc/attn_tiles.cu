@@ -43,8 +43,8 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "attn_umma.cuh"
 #include "attn_work.cuh"
-#include "umma.cuh"
 
 namespace qmm {
 namespace {

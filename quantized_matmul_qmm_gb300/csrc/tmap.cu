@@ -94,21 +94,4 @@ bool make_tmap_kblocks128_sw(CUtensorMap* map, const void* base, uint64_t rows, 
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_kv(CUtensorMap* map, const void* base, bool s8, int head_dim, uint32_t page_size, uint64_t n_heads,
-                  uint64_t n_pages, int64_t st_token, int64_t st_head, int64_t st_page, uint32_t box_tokens) {
-  std::call_once(g_once, resolve);
-  if (g_encode == nullptr) return false;
-  // A dimension of one row has no stride of its own: any valid one will do.
-  auto stride = [&](int64_t s) { return (cuuint64_t)(s > 0 ? s : head_dim * (s8 ? 1 : 2)); };
-  const cuuint64_t dims[4] = {(cuuint64_t)head_dim, page_size, n_heads, n_pages};
-  const cuuint64_t strides[3] = {stride(st_token), stride(st_head), stride(st_page)};
-  const cuuint32_t box[4] = {s8 ? (cuuint32_t)head_dim : 64u, box_tokens, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(map, s8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
-                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              s8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 }  // namespace qmm
