@@ -31,8 +31,8 @@
 //
 // Warps: 0 loads (TMA boxes of page_size's power of two; the pages of a tile
 // looked up by one lane each), 1 and 2 issue the products, 3 cleans the value
-// tiles that hold the step's own tokens (zeros past the request's end and for
-// non-finite values, see attn_rows.cu), 4..11 are the two streams' rows.  With
+// tiles that hold tokens which a row may not see (zeros past the request's end
+// and for non-finite values, see attn_rows.cu), 4..11 are the two streams' rows.  With
 // an int8 cache, 1 issues all products, tiles arrive as codes, eight more warps write them out as
 // bf16 in the products' layout, and 2 and 3 bring the scales; a token's key
 // scale multiplies its column of s, its value scale the weight.
@@ -198,9 +198,9 @@ QMM_DEV void load_warp(const Ctx& x, const CUtensorMap& mk, const CUtensorMap& m
       Ring& ring = !kS8 && value ? vals : keys;
       const uint32_t slot = ring.slot;
       if (!x.wait_all(&empty[slot], ring.phase)) return;
-      const int left = it.len - (it.kv0 + i) * kTok;
+      const int tok0 = (it.kv0 + i) * kTok, left = it.len - tok0;
       const uint32_t boxes = ((uint32_t)min(left, kTok) + box - 1) / box;
-      uint64_t* landed = !kS8 && value && it.q.n + kTok > left ? &x.sh->bar.tail_full[slot] : &full[slot];
+      uint64_t* landed = !kS8 && value && tok0 + kTok > it.seen ? &x.sh->bar.tail_full[slot] : &full[slot];
       if (lane == 0) mbar_arrive_expect_tx(landed, boxes * box_bytes);
       __syncwarp();
       if (lane < boxes) {
@@ -239,8 +239,8 @@ QMM_DEV bool drop_nonfinite(float4& f, int from) {
 
 // ---- int8: warps 2 and 3 bring the tiles' key and value scales ----
 // Four tokens per lane.  Bulk copies of a page's few scales each would cost the
-// copy engine as much as the pages' rows.  Value scales of new tokens that are
-// not finite count as 0 and raise the item's flag: the rows that see them get
+// copy engine as much as the pages' rows.  Value scales that are not finite, of
+// tokens that a row may not see, count as 0 and raise the item's flag: the rows that see them get
 // theirs at the end, as for a bf16 cache.
 template <int D, int kRT>
 QMM_DEV void scale_warps(const Ctx& x) {
@@ -282,7 +282,7 @@ QMM_DEV void scale_warps(const Ctx& x) {
       const float4 v_next = scales(pg_next, pl_next);
       pg_next = page_of(pl_next);
       if (!x.wait_all(&x.sh->bar.sc_empty[sc], phase)) return;
-      const int from = it.q.L - (it.kv0 + i) * kTok - 4 * lane;   // of the lane's four, the first new token
+      const int from = it.seen - (it.kv0 + i) * kTok - 4 * lane;   // of the lane's four, the first that a row may not see
       if (side && from < 4 && drop_nonfinite(v, from)) atomicOr(&x.sh->bad[seq % kBadRing], 1);
       ring[sc * (2 * kTok / 4)] = v;
       __syncwarp();
@@ -344,8 +344,8 @@ QMM_DEV void convert_warps(const Ctx& x) {
   }
 }
 
-// ---- bf16: warp 3 cleans the value tiles that reach past the context and
-// hands them on ----
+// ---- bf16: warp 3 cleans the value tiles that hold tokens which a row may not
+// see, and hands them on ----
 // Eight 16-byte pieces per lane are tested together: exponents of all ones
 // carry into the sign bit.
 template <int D, int kRT>
@@ -367,7 +367,7 @@ QMM_DEV void clean_warp(const Ctx& x) {
       const uint32_t slot = vals.slot;
       vals.next();
       const int tok0 = (it.kv0 + i) * kTok;
-      if (tok0 + kTok <= it.q.L) continue;
+      if (tok0 + kTok <= it.seen) continue;
       const uint32_t parity = (phases >> slot) & 1;
       phases ^= 1u << slot;
       if (!x.wait_all(&x.sh->bar.tail_full[slot], parity)) return;
@@ -375,7 +375,7 @@ QMM_DEV void clean_warp(const Ctx& x) {
       bool bad = false;
 #pragma unroll 1
       for (int t0 = 0; t0 < kTok; t0 += kBatch) {
-        if (tok0 + t0 + kBatch <= it.q.L) continue;   // cached tokens only
+        if (tok0 + t0 + kBatch <= it.seen) continue;
         auto at = [&](int k) {
           const int t = t0 + k * (32 / kP) + t_lane;
           return base + t * 128 + (((p & 7) ^ (t & 7)) << 4);
@@ -392,7 +392,7 @@ QMM_DEV void clean_warp(const Ctx& x) {
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
           const int tok = tok0 + t0 + k * (32 / kP) + t_lane;
-          if (tok < it.q.L) continue;
+          if (tok < it.seen) continue;
           uint4 w = make_uint4(0, 0, 0, 0);
           if (tok < it.len) {
             w = lds128(at(k));
@@ -813,7 +813,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
           if (G::kShared && i >= step && !pv_done()) return owned;
         } else {
           const int tok0 = (it.kv0 + i) * kTok;
-          const bool masked = tok0 + kTok > it.q.L;
+          const bool masked = tok0 + kTok > it.seen;
           // O (of this lane's row) to a new reference
           auto rescale = [&](float f) {
 #pragma unroll 1

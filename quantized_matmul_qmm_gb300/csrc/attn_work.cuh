@@ -2,7 +2,9 @@
 //
 // An item is one (request, key head, tile of query rows); the query rows of a
 // key head are row = i * group + e for new token i and query head e of the
-// head's group.  An item's unit is one tile of `tile_tokens` cached tokens.
+// head's group.  An item's unit is one tile of `tile_tokens` cached tokens;
+// without a mask (causal chunks) an item has no units past its last row's own
+// token, which halves a prompt that begins at an empty cache.
 // Units are numbered request by request, then head, row tile and cached tile;
 // each block gets the same number of consecutive units (to one), whatever the
 // lengths, so the load is even without the host knowing them.  An item cut by
@@ -17,11 +19,10 @@ namespace qmm {
 
 struct AttnReq {
   int L, n, first;   // cached tokens, new tokens, row of the first new token in q
-  int row_tiles, kv_tiles;
-  int units;         // 0: nothing to do
+  int row_tiles, kv_tiles;   // 0 row tiles: nothing to do
 };
 
-// Lengths that do not fit the call's buffers give no units, and the status.
+// Lengths that do not fit the call's buffers give no work, and the status.
 QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_tokens) {
   AttnReq q{};
   const int L = a.ctx[r], c0 = a.cu[r], c1 = a.cu[r + 1];
@@ -35,18 +36,56 @@ QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_t
   q.first = c0;
   q.row_tiles = ((int)n * a.group + rows_per_tile - 1) / rows_per_tile;
   q.kv_tiles = ((int)len + tile_tokens - 1) / tile_tokens;
-  const int64_t units = (int64_t)a.cache.n_heads * q.row_tiles * q.kv_tiles;
-  if (units > INT32_MAX) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
-  else q.units = (int)units;
   return q;
+}
+
+// Cached tiles of the items of row tile t: up to its last row's own token, or
+// with a mask (any pattern) all.
+QMM_DEV int attn_item_tiles(const AttnArgs& a, const AttnReq& q, int t, int rows_per_tile, int tile_tokens) {
+  if (a.mask != nullptr || t >= q.row_tiles - 1) return q.kv_tiles;
+  return (q.L + ((t + 1) * rows_per_tile - 1) / a.group) / tile_tokens + 1;
+}
+
+// sum of (s * i + b) / m over i = 0 .. n - 1, in as many steps as Euclid's
+// algorithm takes for s and m: the whole parts are sums of i, and the rest
+// counts points below a line, which is the same sum with the axes exchanged.
+QMM_DEV int64_t attn_floor_sum(uint32_t n, uint32_t m, uint32_t s, uint32_t b) {
+  int64_t sum = 0;
+#pragma unroll 1
+  while (n > 0) {
+    sum += (int64_t)n * (n - 1) / 2 * (s / m) + (int64_t)n * (b / m);
+    s %= m;
+    b %= m;
+    const uint32_t top = s * n + b;              // below 2^31: at most the request's rows and m
+    n = top / m;
+    b = top - n * m;
+    const uint32_t old = m;
+    m = s;
+    s = old;
+  }
+  return sum;
+}
+
+// Units of a head's first t < row_tiles row tiles.
+QMM_DEV int64_t attn_units_before(const AttnArgs& a, const AttnReq& q, int t, int rows_per_tile, int tile_tokens) {
+  if (t <= 0) return 0;
+  if (a.mask != nullptr) return (int64_t)t * q.kv_tiles;
+  // attn_item_tiles with the whole tiles of L set apart
+  return (int64_t)t * (q.L / tile_tokens + 1) +
+         attn_floor_sum(t, tile_tokens * a.group, rows_per_tile,
+                        rows_per_tile - 1 + q.L % tile_tokens * a.group);
+}
+QMM_DEV int64_t attn_head_units(const AttnArgs& a, const AttnReq& q, int rows_per_tile, int tile_tokens) {
+  return attn_units_before(a, q, q.row_tiles - 1, rows_per_tile, tile_tokens) + (q.row_tiles > 0 ? q.kv_tiles : 0);
 }
 
 struct AttnWork {
   int total, blocks;     // units of the call, and the blocks that share them
   int per, extra;        // each block has `per` units, the first `extra` blocks one more
   int u0, u1;            // this block's
-  int r, off;            // request of u0, and u0's place among its units
-  AttnReq q;             // that request
+  int r;                 // request of u0
+  AttnReq q;
+  int h, t, kv0;         // u0's key head, row tile and cached tile
   QMM_DEV int block_of(int e) const {
     const int head = extra * (per + 1);
     return e < head ? e / (per + 1) : extra + (e - head) / per;
@@ -56,7 +95,7 @@ struct AttnWork {
 struct AttnFindScratch {
   int64_t warp_sum[32];
   AttnReq q;
-  int r, off;
+  int r, off, head_units;
 };
 
 QMM_DEV bool attn_share(const AttnArgs& a, int64_t total, AttnWork& w) {
@@ -75,6 +114,20 @@ QMM_DEV bool attn_share(const AttnArgs& a, int64_t total, AttnWork& w) {
   return true;
 }
 
+// u0 is unit `off` of request w.q, whose heads have head_units units each.
+QMM_DEV void attn_place(const AttnArgs& a, int off, int head_units, int rows_per_tile, int tile_tokens, AttnWork& w) {
+  w.h = off / head_units;
+  off -= w.h * head_units;
+  int lo = 0, hi = w.q.row_tiles - 1;            // the last row tile that begins at or before `off`
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (attn_units_before(a, w.q, mid, rows_per_tile, tile_tokens) <= off) lo = mid; else hi = mid - 1;
+  }
+  w.t = lo;
+  w.kv0 = off - (int)attn_units_before(a, w.q, lo, rows_per_tile, tile_tokens);
+}
+
 // All kThreads threads of the block; false (for all) when the block has none.
 template <int kThreads>
 QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_tokens, AttnFindScratch* s, AttnWork& w) {
@@ -82,30 +135,33 @@ QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_token
   if (a.R <= 32) {   // every warp for itself: one request per lane, no barrier
     AttnReq q{};
     if (lane < a.R) q = attn_req(a, lane, rows_per_tile, tile_tokens);
-    int64_t incl = q.units;
+    const int64_t head_units = attn_head_units(a, q, rows_per_tile, tile_tokens), units = a.cache.n_heads * head_units;
+    int64_t incl = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
     if (!attn_share(a, __shfl_sync(0xffffffffu, incl, 31), w)) return false;
-    const int start = (int)incl - q.units;
+    const int start = (int)(incl - units);       // all fit 32 bits now
     const int at = __ffs(__ballot_sync(0xffffffffu, w.u0 >= start && w.u0 < (int)incl)) - 1;
     w.r = at;
-    w.off = w.u0 - __shfl_sync(0xffffffffu, start, at);
     w.q.L = __shfl_sync(0xffffffffu, q.L, at);
     w.q.n = __shfl_sync(0xffffffffu, q.n, at);
     w.q.first = __shfl_sync(0xffffffffu, q.first, at);
     w.q.row_tiles = __shfl_sync(0xffffffffu, q.row_tiles, at);
     w.q.kv_tiles = __shfl_sync(0xffffffffu, q.kv_tiles, at);
-    w.q.units = __shfl_sync(0xffffffffu, q.units, at);
+    attn_place(a, w.u0 - __shfl_sync(0xffffffffu, start, at), __shfl_sync(0xffffffffu, (int)head_units, at),
+               rows_per_tile, tile_tokens, w);
     return true;
   }
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
   int64_t mine = 0;
 #pragma unroll 1
-  for (int r = r0; r < r1; ++r) mine += attn_req(a, r, rows_per_tile, tile_tokens).units;
+  for (int r = r0; r < r1; ++r)
+    mine += a.cache.n_heads *
+            attn_head_units(a, attn_req(a, r, rows_per_tile, tile_tokens), rows_per_tile, tile_tokens);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -127,28 +183,31 @@ QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_token
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       const AttnReq q = attn_req(a, r, rows_per_tile, tile_tokens);
-      if (w.u0 < start + q.units) {
+      const int64_t head_units = attn_head_units(a, q, rows_per_tile, tile_tokens);
+      if (w.u0 < start + a.cache.n_heads * head_units) {
         s->q = q;
         s->r = r;
         s->off = (int)(w.u0 - start);
+        s->head_units = (int)head_units;
         break;
       }
-      start += q.units;
+      start += a.cache.n_heads * head_units;
     }
   }
   __syncthreads();
   w.r = s->r;
-  w.off = s->off;
   w.q = s->q;
+  attn_place(a, s->off, s->head_units, rows_per_tile, tile_tokens, w);
   return true;
 }
 
-// A block's part of one item: cached tiles [kv0, kv0 + seg) of kv_tiles.
+// A block's part of one item: cached tiles [kv0, kv0 + seg).
 struct AttnItem {
   AttnReq q;
-  int r, id;          // request; key head * row_tiles + row tile
+  int r;              // request
   int h, row0, n_rows;
   int kv0, seg, len;
+  int seen;           // every row sees the tokens before this one; the step's first rows' own count as not seen
   bool whole;
   int pieces;         // of an item that this block begins and another ends; else 0
 };
@@ -156,33 +215,38 @@ struct AttnItem {
 // Walks a block's units item by item.
 struct AttnWalk {
   AttnReq q;
-  int r, off, u;
+  int r, h, t, kv0, u;   // the next unit
   QMM_DEV void start(const AttnWork& w) {
     q = w.q;
     r = w.r;
-    off = w.off;
+    h = w.h;
+    t = w.t;
+    kv0 = w.kv0;
     u = w.u0;
   }
   QMM_DEV bool next(const AttnArgs& a, const AttnWork& w, int rows_per_tile, int tile_tokens, AttnItem& it) {
     if (u >= w.u1) return false;
-    while (off >= q.units) {   // to the next request that has work
-      off -= q.units;
+    if (t >= q.row_tiles) t = 0, ++h;
+    while (h >= a.cache.n_heads || q.row_tiles == 0) {   // to the next request that has work
       q = attn_req(a, ++r, rows_per_tile, tile_tokens);
+      h = 0;
     }
+    const int tiles = attn_item_tiles(a, q, t, rows_per_tile, tile_tokens);
     it.q = q;
     it.r = r;
-    it.id = off / q.kv_tiles;
-    it.kv0 = off - it.id * q.kv_tiles;
-    it.h = it.id / q.row_tiles;
-    it.row0 = (it.id - it.h * q.row_tiles) * rows_per_tile;
+    it.h = h;
+    it.row0 = t * rows_per_tile;
     it.n_rows = min(rows_per_tile, q.n * a.group - it.row0);
-    it.seg = min(q.kv_tiles - it.kv0, w.u1 - u);
+    it.kv0 = kv0;
+    it.seg = min(tiles - kv0, w.u1 - u);
     it.len = q.L + q.n;
-    it.whole = it.seg == q.kv_tiles;
+    it.seen = q.L + (a.mask != nullptr || t == 0 ? 0 : it.row0 / a.group + 1);
+    it.whole = it.seg == tiles;
     it.pieces = 0;             // up to the block that has the item's last unit
-    if (!it.whole && it.kv0 == 0) it.pieces = w.block_of(u + q.kv_tiles - 1) - (int)blockIdx.x + 1;
+    if (!it.whole && kv0 == 0) it.pieces = w.block_of(u + tiles - 1) - (int)blockIdx.x + 1;
     u += it.seg;
-    off += it.seg;
+    kv0 += it.seg;
+    if (kv0 == tiles) kv0 = 0, ++t;
     return true;
   }
 };

@@ -165,6 +165,24 @@ def test_many_rows(qmm, cuda, tree, page, d, s8):
 
 
 @pytest.mark.parametrize("s8", [False, True])
+@pytest.mark.parametrize("heads,kv", [(2, 2), (6, 2), (10, 2), (16, 2)])
+@pytest.mark.parametrize("page", [16, 20])
+def test_prompts(qmm, cuda, page, heads, kv, s8):
+    """Causal chunks over several row tiles, where later cached tiles are seen
+    by the last rows only: row tiles that end inside a token's group, at empty
+    caches and past them."""
+    s = build(cuda, [0, 127, 300, 64], [519, 257, 1, 384], heads, kv, 64, page, s8, seed=heads)
+    check(s, call(qmm, cuda, s))
+
+
+def test_prompts_of_many_requests(qmm, cuda):
+    """More requests than a warp's lanes, of every length."""
+    new = [(37 * i) % 290 for i in range(41)]
+    s = build(cuda, [(61 * i) % 200 for i in range(41)], new, 3, 1, 64, 32, False, seed=41)
+    check(s, call(qmm, cuda, s))
+
+
+@pytest.mark.parametrize("s8", [False, True])
 @pytest.mark.parametrize("new,heads", [(1, 4), (8, 8), (40, 8)])
 def test_long_context_split_between_blocks(qmm, cuda, s8, new, heads):
     s = build(cuda, [20011], [new], heads, 1, 128, 16, s8, tree=True, seed=new)
