@@ -84,11 +84,22 @@ struct TBars {
   uint64_t done;
 };
 
+struct RowItem {
+  AttnWalk walk;
+  AttnItem it;
+  int more;
+};
+
 struct TShared {
   TBars bar;
-  AttnFindScratch find;
   AttnWork work;                                 // out of the roles' registers
-  float m[2][128], l[2][128];
+  union {
+    struct {
+      float m[2][128], l[2][128];                // kRT == 1
+    };
+    RowItem item[8];                             // of the row warps (see row_warps)
+    AttnFindScratch find;                        // before the roles begin
+  };
   int bad[kBadRing];                 // per item, by its number: a non-finite value was taken out
   uint32_t tmem;
   int abort;
@@ -738,10 +749,27 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     if (lane == 0) mbar_arrive(&b.sync);
     return x.wait_all(&b.sync, syncs++ & 1);
   };
-  AttnWalk walk;
-  walk.start(x.sh->work);
-  AttnItem it;
-  for (; walk.next(a, x.sh->work, 128 * kRT, kTok, it); ++seq) {
+  // A bf16 row's scores fill the registers.  With 256 rows, where the products
+  // leave the least slack, the walk and its item are kept in shared memory (16
+  // trees of 64 nodes over 11k tokens 174 -> 166 us, 4 chunks of 400 over 3k 77
+  // -> 75.5; with 128 rows or int8 the registers last and it would cost 1 to 2 %).
+  constexpr bool kItemOut = kRT == 2 && !kS8;
+  RowItem local;
+  auto now = [&]() -> RowItem& { return kItemOut ? x.sh->item[wid - 4] : local; };
+  auto next = [&](bool first) {
+    RowItem& to = now();
+    if (kItemOut) __syncwarp();
+    if (!kItemOut || lane == 0) {
+      if (first) to.walk.start(x.sh->work);
+      to.more = to.walk.next(a, x.sh->work, 128 * kRT, kTok, to.it);
+    }
+    if (kItemOut) __syncwarp();
+  };
+  next(true);
+  for (;; ++seq) {
+    if (!now().more) break;
+    const AttnItem& it = now().it;
+    const int seg = it.seg;
     if (it.pieces > 0) owned = attn_owned(it);
     const bool split = kRT == 1 && it.n_rows <= 64;   // lanes 64..127: the same rows, the weights' low parts
     const bool low = split && trow >= 64;
@@ -785,8 +813,8 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
 
     typename RowsOf<kS8>::type rows;             // references and sums
     const bool has = kRT == 1 || it.n_rows > 128 * st;   // this stream has products
-    const int step = kRT == 1 ? 2 : 1;
-    for (int i = kRT == 1 ? st : 0; i < it.seg; i += step) {
+    const int step = kRT == 1 ? 2 : 1, first_tok = it.kv0 * kTok, seen_tok = it.seen;
+    for (int i = kRT == 1 ? st : 0; i < seg; i += step) {
       const uint32_t sc = (tiles + i) % kScaleRing;
       const float* ksc = nullptr;                // the tile's 128 key scales, then its value scales
       if constexpr (kS8) {
@@ -812,8 +840,8 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
           loaded();
           if (G::kShared && i >= step && !pv_done()) return owned;
         } else {
-          const int tok0 = (it.kv0 + i) * kTok;
-          const bool masked = tok0 + kTok > it.seen;
+          const int tok0 = first_tok + i * kTok;
+          const bool masked = tok0 + kTok > seen_tok;
           // O (of this lane's row) to a new reference
           auto rescale = [&](float f) {
 #pragma unroll 1
@@ -844,10 +872,10 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         if (lane == 0) mbar_arrive(&b.sc_empty[sc]);
       }
     }
-    tiles += it.seg;
+    tiles += seg;
 
     // ---- the item's end ----
-    const bool own_tiles = has && (kRT == 2 || it.seg > st);
+    const bool own_tiles = has && (kRT == 2 || seg > st);
     if (own_tiles) {
       if (!x.wait_all(&b.o_done[st], o_count++ & 1)) return owned;
     }
@@ -885,7 +913,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
         for (int e = 0; e < 16; ++e) o[e] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (k >= it.seg) continue;             // stream 1 had no tile
+          if (k >= seg) continue;             // stream 1 had no tile
           tmem_ld16(tlane + kColO + 128 * k + d, r);
           tmem_wait_ld();
           if (f[k] != 0.f) {
@@ -973,6 +1001,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
     if (lane == 0) mbar_arrive(&b.o_free);
     // the query tile, the sums and (split) the low parts are written again for the next item
     if (kRT == 1 && !sync8()) return owned;
+    next(false);
   }
   return owned;
 }
