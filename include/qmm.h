@@ -748,12 +748,15 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * workspace at least qmm_tree_attention_workspace_size bytes, 256-byte
  *           aligned, rewritten by the call.
  * What a row does not see never reaches its result, whatever it holds: places
- * past a request's length, and infinities or NaN in hidden tokens.  Products
- * are of bf16 values (int8 codes are exact in bf16; their scales are applied
- * in fp32), and every sum is fp32, in a fixed order: results are the same from
- * run to run.  The weights exp(s - max) multiply v as two bf16 terms (within
- * 2^-16) with up to 32 query rows per key head (max_new * n_q_heads / n_heads),
- * and rounded to bf16 once (2^-8) with more; the output is rounded once.
+ * past a request's length, and infinities or NaN in hidden tokens.  An
+ * infinity or NaN among the values that a row does see makes its output element
+ * non-finite.  Products are of bf16 values (int8 codes are exact in bf16; their
+ * scales are applied in fp32), and every sum is fp32, in a fixed order: results
+ * are the same from run to run.  The weights exp(s - max) multiply v as two
+ * bf16 terms (within 2^-16) for a request of up to 64 query rows per key head
+ * (its new tokens * n_q_heads / n_heads) in a call of up to 128 (max_new *
+ * n_q_heads / n_heads), and rounded to bf16 once (2^-8) otherwise; the output
+ * is rounded once.
  * Device status: QMM_ERR_INVALID_ARG for lengths that do not fit (negative,
  * more than max_new or T, more than max_blocks pages): that request's rows of
  * out are left alone; and for a page id outside [0, n_pages), whose request's
