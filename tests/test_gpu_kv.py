@@ -191,6 +191,59 @@ def test_append_ties_and_slot_out_of_range(qmm, cuda):
     assert (kc.reshape(8, 64)[[0, 1, 2, 4, 5, 6, 7]] == 9).all() and (ks.flatten()[[0, 1, 2, 4, 5, 6, 7]] == 5).all()
 
 
+@pytest.mark.parametrize("rows", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("s8", [False, True])
+def test_append_many_rows(qmm, cuda, s8, rows):
+    """A long prompt: several (token, head) pairs per warp, the last warp short."""
+    T, heads, d, page = 13007, 3, 64, 16
+    g = torch.Generator().manual_seed(7)
+    x = (torch.randn((T, heads, d), generator=g) * torch.exp(torch.randn((T, heads, 1), generator=g))).to(rows)
+    pages = -(-T // page)
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    slots[5::1000] = -1
+    kc, vc = caches(cuda, pages, page, heads, d, torch.int8 if s8 else torch.bfloat16, True, 7)
+    ks, vs = (torch.full((pages, heads, page), 5.0, device=cuda) if s8 else None for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    qmm.kv_append(x.to(cuda), -x.to(cuda), slots.to(cuda), kc, vc, k_scale=ks, v_scale=vs, dev_status=status)
+    assert status.item() == 0
+    keep = slots >= 0
+    for cache, scale, part in ((kc, ks, x), (vc, vs, -x)):
+        want = torch.full((pages * page, heads, d), 7, dtype=cache.dtype)
+        if s8:
+            q, sc = KV.append_s8(part.float().numpy())
+            want[slots[keep]] = torch.from_numpy(q).to(torch.int8)[keep]
+            wsc = torch.full((pages * page, heads), 5.0)
+            wsc[slots[keep]] = torch.from_numpy(sc).float()[keep]
+            assert torch.equal(scale.permute(0, 2, 1).reshape(-1, heads).cpu(), wsc)
+        else:
+            want[slots[keep]] = part.float().to(torch.bfloat16)[keep]
+        assert torch.equal(cache.reshape(-1, heads, d).cpu(), want)
+
+
+def test_append_codes_next_to_ties(qmm, cuda):
+    """Quotients at and a few units in the last place around every half, at
+    scales from subnormal to huge, against the oracle's division."""
+    g = torch.Generator().manual_seed(3)
+    T, heads, d = 400, 2, 128
+    top = torch.exp2(torch.randint(-149, 127, (T, heads, 1), generator=g).float()) \
+        * (1 + torch.rand((T, heads, 1), generator=g))
+    half = torch.randint(-127, 127, (T, heads, d), generator=g) + 0.5
+    x = (half.double() * (top.double() / 127)).float()
+    bits = x.view(torch.int32) + torch.randint(-3, 4, x.shape, generator=g).int() * (x != 0)
+    x = torch.minimum(torch.maximum(bits.view(torch.float32).nan_to_num(0, 0, 0), -top), top)
+    x[..., :1] = top
+    kc, vc = caches(cuda, 25, 16, heads, d, torch.int8, False, 7)
+    ks, vs = (torch.full((25, heads, 16), 5.0, device=cuda) for _ in range(2))
+    qmm.kv_append(x.to(cuda), x.flip(0).to(cuda), torch.arange(T, device=cuda), kc, vc, k_scale=ks, v_scale=vs)
+    q, sc = KV.append_s8(x.numpy())
+    for cache, scale, flip in ((kc, ks, False), (vc, vs, True)):
+        got, gs = cache.reshape(T, heads, d).cpu(), scale.permute(0, 2, 1).reshape(T, heads).cpu()
+        if flip:
+            got, gs = got.flip(0), gs.flip(0)
+        assert torch.equal(gs, torch.from_numpy(sc).float())
+        assert torch.equal(got, torch.from_numpy(q).to(torch.int8))
+
+
 def test_append_nothing(qmm, cuda):
     kc, vc = caches(cuda, 1, 4, 2, 64, torch.bfloat16, False, 3)
     e = torch.empty((0, 2, 64), device=cuda)
