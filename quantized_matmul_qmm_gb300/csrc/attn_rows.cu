@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kS8, MT))
 attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   using G = Geo<D, kS8, MT>;
   constexpr int kRows = 16 * MT;
+  // setup: 64 requests of 3 to 8191 tokens take 185.5 us without, 178.5 with 1 unit, 174 with 2, 3 or 4
+  constexpr AttnShape kShape{kRows, kTileTokens, 2};
   constexpr int kSteps = D / 16;                 // mma steps over the head's dimensions
   constexpr int kTiles = D / 8;                  // 8-column tiles of the output
   constexpr int kPitch = D + 8;                  // fp32 per row of the joining buffer
@@ -119,7 +121,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   AttnWork w;
-  if (!attn_find_work<kThreads>(a, kRows, kTileTokens, &find, w)) {
+  if (!attn_find_work<kThreads>(a, kShape, &find, w)) {
     if (threadIdx.x == 0) attn_post_owned(a, AttnOwned{});
     return;
   }
@@ -127,7 +129,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   AttnWalk walk;
   walk.start(w);
   AttnItem im;
-  while (walk.next(a, w, kRows, kTileTokens, im)) {
+  while (walk.next(a, w, kShape, im)) {
     const AttnReq& rq = im.q;
     const int h = im.h, row0 = im.row0, kv0 = im.kv0, seg = im.seg, L = rq.L, len = im.len, n_rows = im.n_rows;
     if (im.pieces > 0) owned = attn_owned(im);

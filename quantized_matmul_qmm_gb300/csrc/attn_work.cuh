@@ -7,7 +7,13 @@
 // token, which halves a prompt that begins at an empty cache.
 // Units are numbered request by request, then head, row tile and cached tile;
 // each block gets the same number of consecutive units (to one), whatever the
-// lengths, so the load is even without the host knowing them.  An item cut by
+// lengths, so the load is even without the host knowing them.  An item's first
+// `setup` units stand for what it costs besides its tiles (queries in, the
+// pipeline's first and last steps, outputs): a block with many short items
+// would else be the last to end (chunks of 300 to 512 tokens at contexts of 0 to
+// 6000: 118 -> 65 us).  With no more tiles than blocks, every block has one tile
+// of one item, and they count for nothing (4 x 64 tokens at 1000: 18.7 us, with
+// them 21.3).  An item cut by
 // a block boundary leaves partial results, which the combine kernel joins.
 // Unit numbers are 32-bit, so that the few divisions on a block's way to its
 // first load are short.
@@ -17,13 +23,18 @@
 
 namespace qmm {
 
+// A kernel's items: query rows, cached tokens of a unit, units for the setup (at most).
+struct AttnShape {
+  int rows, tokens, setup;
+};
+
 struct AttnReq {
   int L, n, first;   // cached tokens, new tokens, row of the first new token in q
   int row_tiles, kv_tiles;   // 0 row tiles: nothing to do
 };
 
 // Lengths that do not fit the call's buffers give no work, and the status.
-QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_tokens) {
+QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, AttnShape sh) {
   AttnReq q{};
   const int L = a.ctx[r], c0 = a.cu[r], c1 = a.cu[r + 1];
   const int64_t n = (int64_t)c1 - c0, len = (int64_t)L + n;
@@ -34,16 +45,16 @@ QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, int rows_per_tile, int tile_t
   q.L = L;
   q.n = (int)n;
   q.first = c0;
-  q.row_tiles = ((int)n * a.group + rows_per_tile - 1) / rows_per_tile;
-  q.kv_tiles = ((int)len + tile_tokens - 1) / tile_tokens;
+  q.row_tiles = ((int)n * a.group + sh.rows - 1) / sh.rows;
+  q.kv_tiles = ((int)len + sh.tokens - 1) / sh.tokens;
   return q;
 }
 
 // Cached tiles of the items of row tile t: up to its last row's own token, or
 // with a mask (any pattern) all.
-QMM_DEV int attn_item_tiles(const AttnArgs& a, const AttnReq& q, int t, int rows_per_tile, int tile_tokens) {
+QMM_DEV int attn_item_tiles(const AttnArgs& a, const AttnReq& q, int t, AttnShape sh) {
   if (a.mask != nullptr || t >= q.row_tiles - 1) return q.kv_tiles;
-  return (q.L + ((t + 1) * rows_per_tile - 1) / a.group) / tile_tokens + 1;
+  return (q.L + ((t + 1) * sh.rows - 1) / a.group) / sh.tokens + 1;
 }
 
 // sum of (s * i + b) / m over i = 0 .. n - 1, in as many steps as Euclid's
@@ -66,26 +77,26 @@ QMM_DEV int64_t attn_floor_sum(uint32_t n, uint32_t m, uint32_t s, uint32_t b) {
   return sum;
 }
 
-// Units of a head's first t < row_tiles row tiles.
-QMM_DEV int64_t attn_units_before(const AttnArgs& a, const AttnReq& q, int t, int rows_per_tile, int tile_tokens) {
+// Tiles of a head's first t < row_tiles row tiles.
+QMM_DEV int64_t attn_tiles_before(const AttnArgs& a, const AttnReq& q, int t, AttnShape sh) {
   if (t <= 0) return 0;
   if (a.mask != nullptr) return (int64_t)t * q.kv_tiles;
   // attn_item_tiles with the whole tiles of L set apart
-  return (int64_t)t * (q.L / tile_tokens + 1) +
-         attn_floor_sum(t, tile_tokens * a.group, rows_per_tile,
-                        rows_per_tile - 1 + q.L % tile_tokens * a.group);
+  return (int64_t)t * (q.L / sh.tokens + 1) +
+         attn_floor_sum(t, sh.tokens * a.group, sh.rows, sh.rows - 1 + q.L % sh.tokens * a.group);
 }
-QMM_DEV int64_t attn_head_units(const AttnArgs& a, const AttnReq& q, int rows_per_tile, int tile_tokens) {
-  return attn_units_before(a, q, q.row_tiles - 1, rows_per_tile, tile_tokens) + (q.row_tiles > 0 ? q.kv_tiles : 0);
+QMM_DEV int64_t attn_head_tiles(const AttnArgs& a, const AttnReq& q, AttnShape sh) {
+  return q.row_tiles == 0 ? 0 : attn_tiles_before(a, q, q.row_tiles - 1, sh) + q.kv_tiles;
 }
 
 struct AttnWork {
   int total, blocks;     // units of the call, and the blocks that share them
+  int setup;             // units that an item's setup counts for
   int per, extra;        // each block has `per` units, the first `extra` blocks one more
   int u0, u1;            // this block's
   int r;                 // request of u0
   AttnReq q;
-  int h, t, kv0;         // u0's key head, row tile and cached tile
+  int h, t, pos;         // u0's key head, row tile and place among the item's units
   QMM_DEV int block_of(int e) const {
     const int head = extra * (per + 1);
     return e < head ? e / (per + 1) : extra + (e - head) / per;
@@ -93,12 +104,14 @@ struct AttnWork {
 };
 
 struct AttnFindScratch {
-  int64_t warp_sum[32];
+  int64_t warp_tiles[32], warp_items[32];
   AttnReq q;
   int r, off, head_units;
 };
 
-QMM_DEV bool attn_share(const AttnArgs& a, int64_t total, AttnWork& w) {
+QMM_DEV bool attn_share(const AttnArgs& a, int64_t tiles, int64_t items, AttnShape sh, AttnWork& w) {
+  w.setup = tiles > a.grid ? sh.setup : 0;
+  const int64_t total = tiles + w.setup * items;
   if (total > INT32_MAX) {
     set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     return false;
@@ -115,75 +128,80 @@ QMM_DEV bool attn_share(const AttnArgs& a, int64_t total, AttnWork& w) {
 }
 
 // u0 is unit `off` of request w.q, whose heads have head_units units each.
-QMM_DEV void attn_place(const AttnArgs& a, int off, int head_units, int rows_per_tile, int tile_tokens, AttnWork& w) {
+QMM_DEV void attn_place(const AttnArgs& a, int off, int head_units, AttnShape sh, AttnWork& w) {
   w.h = off / head_units;
   off -= w.h * head_units;
   int lo = 0, hi = w.q.row_tiles - 1;            // the last row tile that begins at or before `off`
 #pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (attn_units_before(a, w.q, mid, rows_per_tile, tile_tokens) <= off) lo = mid; else hi = mid - 1;
+    if (attn_tiles_before(a, w.q, mid, sh) + (int64_t)w.setup * mid <= off) lo = mid; else hi = mid - 1;
   }
   w.t = lo;
-  w.kv0 = off - (int)attn_units_before(a, w.q, lo, rows_per_tile, tile_tokens);
+  w.pos = off - (int)attn_tiles_before(a, w.q, lo, sh) - w.setup * lo;
 }
 
 // All kThreads threads of the block; false (for all) when the block has none.
 template <int kThreads>
-QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_tokens, AttnFindScratch* s, AttnWork& w) {
+QMM_DEV bool attn_find_work(const AttnArgs& a, AttnShape sh, AttnFindScratch* s, AttnWork& w) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   if (a.R <= 32) {   // every warp for itself: one request per lane, no barrier
     AttnReq q{};
-    if (lane < a.R) q = attn_req(a, lane, rows_per_tile, tile_tokens);
-    const int64_t head_units = attn_head_units(a, q, rows_per_tile, tile_tokens), units = a.cache.n_heads * head_units;
-    int64_t incl = units;
+    if (lane < a.R) q = attn_req(a, lane, sh);
+    const int64_t head_tiles = attn_head_tiles(a, q, sh), tiles = a.cache.n_heads * head_tiles;
+    const int64_t items = (int64_t)a.cache.n_heads * q.row_tiles;
+    int64_t incl = tiles, incl_items = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o), up_items = __shfl_up_sync(0xffffffffu, incl_items, o);
+      if (lane >= o) incl += up, incl_items += up_items;
     }
-    if (!attn_share(a, __shfl_sync(0xffffffffu, incl, 31), w)) return false;
-    const int start = (int)(incl - units);       // all fit 32 bits now
-    const int at = __ffs(__ballot_sync(0xffffffffu, w.u0 >= start && w.u0 < (int)incl)) - 1;
+    if (!attn_share(a, __shfl_sync(0xffffffffu, incl, 31), __shfl_sync(0xffffffffu, incl_items, 31), sh, w))
+      return false;
+    const int stop = (int)(incl + w.setup * incl_items);   // all fit 32 bits now
+    const int start = stop - (int)(tiles + w.setup * items), head_units = (int)head_tiles + w.setup * q.row_tiles;
+    const int at = __ffs(__ballot_sync(0xffffffffu, w.u0 >= start && w.u0 < stop)) - 1;
     w.r = at;
     w.q.L = __shfl_sync(0xffffffffu, q.L, at);
     w.q.n = __shfl_sync(0xffffffffu, q.n, at);
     w.q.first = __shfl_sync(0xffffffffu, q.first, at);
     w.q.row_tiles = __shfl_sync(0xffffffffu, q.row_tiles, at);
     w.q.kv_tiles = __shfl_sync(0xffffffffu, q.kv_tiles, at);
-    attn_place(a, w.u0 - __shfl_sync(0xffffffffu, start, at), __shfl_sync(0xffffffffu, (int)head_units, at),
-               rows_per_tile, tile_tokens, w);
+    attn_place(a, w.u0 - __shfl_sync(0xffffffffu, start, at), __shfl_sync(0xffffffffu, head_units, at),
+               sh, w);
     return true;
   }
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
-  int64_t mine = 0;
+  int64_t tiles = 0, items = 0;
 #pragma unroll 1
-  for (int r = r0; r < r1; ++r)
-    mine += a.cache.n_heads *
-            attn_head_units(a, attn_req(a, r, rows_per_tile, tile_tokens), rows_per_tile, tile_tokens);
-  int64_t incl = mine;
+  for (int r = r0; r < r1; ++r) {
+    const AttnReq q = attn_req(a, r, sh);
+    tiles += a.cache.n_heads * attn_head_tiles(a, q, sh);
+    items += (int64_t)a.cache.n_heads * q.row_tiles;
+  }
+  int64_t incl = tiles, incl_items = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o), up_items = __shfl_up_sync(0xffffffffu, incl_items, o);
+    if (lane >= o) incl += up, incl_items += up_items;
   }
-  if (lane == 31) s->warp_sum[wid] = incl;
+  if (lane == 31) s->warp_tiles[wid] = incl, s->warp_items[wid] = incl_items;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int64_t before = incl - tiles, before_items = incl_items - items, total = 0, total_items = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
-    const int64_t v = s->warp_sum[i];
-    if (i < wid) before += v;
-    total += v;
+    if (i < wid) before += s->warp_tiles[i], before_items += s->warp_items[i];
+    total += s->warp_tiles[i];
+    total_items += s->warp_items[i];
   }
-  if (!attn_share(a, total, w)) return false;
-  int64_t start = before + incl - mine;
-  if (w.u0 >= start && w.u0 < start + mine) {   // one thread's requests hold u0
+  if (!attn_share(a, total, total_items, sh, w)) return false;
+  int64_t start = before + w.setup * before_items;
+  if (w.u0 >= start && w.u0 < start + tiles + w.setup * items) {   // one thread's requests hold u0
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      const AttnReq q = attn_req(a, r, rows_per_tile, tile_tokens);
-      const int64_t head_units = attn_head_units(a, q, rows_per_tile, tile_tokens);
+      const AttnReq q = attn_req(a, r, sh);
+      const int64_t head_units = attn_head_tiles(a, q, sh) + (int64_t)w.setup * q.row_tiles;
       if (w.u0 < start + a.cache.n_heads * head_units) {
         s->q = q;
         s->r = r;
@@ -197,7 +215,7 @@ QMM_DEV bool attn_find_work(const AttnArgs& a, int rows_per_tile, int tile_token
   __syncthreads();
   w.r = s->r;
   w.q = s->q;
-  attn_place(a, s->off, s->head_units, rows_per_tile, tile_tokens, w);
+  attn_place(a, s->off, s->head_units, sh, w);
   return true;
 }
 
@@ -215,39 +233,43 @@ struct AttnItem {
 // Walks a block's units item by item.
 struct AttnWalk {
   AttnReq q;
-  int r, h, t, kv0, u;   // the next unit
+  int r, h, t, pos, u;   // the next unit
   QMM_DEV void start(const AttnWork& w) {
     q = w.q;
     r = w.r;
     h = w.h;
     t = w.t;
-    kv0 = w.kv0;
+    pos = w.pos;
     u = w.u0;
   }
-  QMM_DEV bool next(const AttnArgs& a, const AttnWork& w, int rows_per_tile, int tile_tokens, AttnItem& it) {
-    if (u >= w.u1) return false;
-    if (t >= q.row_tiles) t = 0, ++h;
-    while (h >= a.cache.n_heads || q.row_tiles == 0) {   // to the next request that has work
-      q = attn_req(a, ++r, rows_per_tile, tile_tokens);
-      h = 0;
+  QMM_DEV bool next(const AttnArgs& a, const AttnWork& w, AttnShape sh, AttnItem& it) {
+    while (u < w.u1) {
+      if (t >= q.row_tiles) t = 0, ++h;
+      while (h >= a.cache.n_heads || q.row_tiles == 0) {   // to the next request that has work
+        q = attn_req(a, ++r, sh);
+        h = 0;
+      }
+      const int tiles = attn_item_tiles(a, q, t, sh), units = w.setup + tiles;
+      const int take = min(units - pos, w.u1 - u), end = pos + take - w.setup;
+      it.kv0 = max(pos - w.setup, 0);
+      it.seg = end - it.kv0;
+      it.h = h;
+      it.row0 = t * sh.rows;
+      it.whole = it.seg == tiles;
+      it.pieces = 0;           // up to the block that has the item's last unit
+      if (!it.whole && it.kv0 == 0) it.pieces = w.block_of(u - pos + units - 1) - (int)blockIdx.x + 1;
+      u += take;
+      pos += take;
+      if (pos == units) pos = 0, ++t;
+      if (it.seg <= 0) continue;   // only of the setup: the next block's item
+      it.q = q;
+      it.r = r;
+      it.n_rows = min(sh.rows, q.n * a.group - it.row0);
+      it.len = q.L + q.n;
+      it.seen = q.L + (a.mask != nullptr || it.row0 == 0 ? 0 : it.row0 / a.group + 1);
+      return true;
     }
-    const int tiles = attn_item_tiles(a, q, t, rows_per_tile, tile_tokens);
-    it.q = q;
-    it.r = r;
-    it.h = h;
-    it.row0 = t * rows_per_tile;
-    it.n_rows = min(rows_per_tile, q.n * a.group - it.row0);
-    it.kv0 = kv0;
-    it.seg = min(tiles - kv0, w.u1 - u);
-    it.len = q.L + q.n;
-    it.seen = q.L + (a.mask != nullptr || t == 0 ? 0 : it.row0 / a.group + 1);
-    it.whole = it.seg == tiles;
-    it.pieces = 0;             // up to the block that has the item's last unit
-    if (!it.whole && kv0 == 0) it.pieces = w.block_of(u + tiles - 1) - (int)blockIdx.x + 1;
-    u += it.seg;
-    kv0 += it.seg;
-    if (kv0 == tiles) kv0 = 0, ++t;
-    return true;
+    return false;
   }
 };
 
