@@ -502,57 +502,72 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a) {
 // adds up all owners' rows and its warps take rows at the grid's pitch, so that
 // a few long items keep the whole GPU busy; a warp holds the pieces' maxima and
 // sums, one per lane, and four (two) columns of them per lane, eight pieces at
-// a time.  What costs is the chain of loads, a few us however little there is
+// a time.  What costs is the chain of loads, 3 to 4 us however little there is
 // to join: the owners, then maxima, sums and the first eight pieces together.
 constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombinePerSm = 4;
-template <int D>
-__global__ void __launch_bounds__(kCombineThreads, kCombinePerSm)
-attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
-  __shared__ int s_end[kCombineMaxOwners];       // running sum of the owners' rows
-  __shared__ int4 s_own[kCombineMaxOwners];      // h, row0, pieces, first
-  __shared__ int s_warp[kCombineThreads / 32];
-  pdl_launch_dependents();
-  pdl_wait();
-  constexpr int kV = D / 32;                     // columns per lane
+// The owners and the running sums of their rows, in shared memory; returns the total.
+struct CombineOwners {
+  int end[kCombineMaxOwners];        // running sum of the owners' rows
+  int4 own[kCombineMaxOwners];       // h, row0, pieces, first
+  int warp[kCombineWarps];
+  // the first owner whose running sum passes row i
+  QMM_DEV int of(int i) const {
+    int lo = 0, hi = kCombineMaxOwners - 1;
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (end[mid] > i) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+  }
+};
+QMM_DEV int combine_owners(const AttnArgs& a, CombineOwners& o) {
   constexpr int kPer = kCombineMaxOwners / kCombineThreads;
-  using Vec = typename std::conditional<kV == 4, float4, float2>::type;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   int rows[kPer], incl = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int b = threadIdx.x * kPer + k;
     rows[k] = b < a.grid ? a.owned_rows[b] : 0;
-    s_own[b] = b < a.grid ? a.owned[b] : make_int4(0, 0, 0, 0);   // without rows: not looked at
+    o.own[b] = b < a.grid ? a.owned[b] : make_int4(0, 0, 0, 0);   // without rows: not looked at
     incl += rows[k];
   }
   const int mine = incl;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += up;
   }
-  if (lane == 31) s_warp[wid] = incl;
+  if (lane == 31) o.warp[wid] = incl;
   __syncthreads();
   int run = incl - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i < kCombineThreads / 32; ++i) {
-    if (i < wid) run += s_warp[i];
-    total += s_warp[i];
+  for (int i = 0; i < kCombineWarps; ++i) {
+    if (i < wid) run += o.warp[i];
+    total += o.warp[i];
   }
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) s_end[threadIdx.x * kPer + k] = run += rows[k];
+  for (int k = 0; k < kPer; ++k) o.end[threadIdx.x * kPer + k] = run += rows[k];
   __syncthreads();
+  return total;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads, kCombinePerSm)
+attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
+  __shared__ CombineOwners s;
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kV = D / 32;                     // columns per lane
+  using Vec = typename std::conditional<kV == 4, float4, float2>::type;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int total = combine_owners(a, s);
 #pragma unroll 1
-  for (int i = wid * gridDim.x + blockIdx.x; i < total; i += gridDim.x * (kCombineThreads / 32)) {
-    int lo = 0, hi = kCombineMaxOwners - 1;      // the first owner whose running sum passes i
-#pragma unroll 1
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_end[mid] > i) hi = mid; else lo = mid + 1;
-    }
-    const int b = lo, rr = i - (lo > 0 ? s_end[lo - 1] : 0);
-    const int4 own = s_own[b];
+  for (int i = wid * gridDim.x + blockIdx.x; i < total; i += gridDim.x * kCombineWarps) {
+    const int b = s.of(i), rr = i - (b > 0 ? s.end[b - 1] : 0);
+    const int4 own = s.own[b];
     const int pieces = own.z;
     auto at = [&](int p) { return (int64_t)(p == 0 ? 2 * b + 1 : 2 * (b + p)) * rows_per_tile + rr; };
     Vec v[8];
@@ -599,6 +614,94 @@ attn_combine_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
   }
 }
 
+// The same with a block per row, whose warps each join a part of the row's pieces;
+// the parts are then joined as pieces in their turn.  For calls of few rows, which
+// may have many pieces (up to one per block of the attention kernel): one token of
+// 8 query heads on one key head at 400k tokens takes 46 us (a warp per row 71), of
+// 32 on 8 at 30k 29.3 (32.4); 512 rows of few pieces are better off with a warp
+// each (18.8 us, here 19.8).
+constexpr int kCombineRowsPerSm = 2;
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads)
+attn_combine_row_kernel(const __grid_constant__ AttnArgs a, int rows_per_tile) {
+  __shared__ CombineOwners s;
+  __shared__ __align__(16) float s_x[kCombineWarps][D];
+  __shared__ float2 s_ml[kCombineWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kV = D / 32;
+  using Vec = typename std::conditional<kV == 4, float4, float2>::type;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if ((int)blockIdx.x >= combine_owners(a, s)) return;
+  const int b = s.of(blockIdx.x), rr = blockIdx.x - (b > 0 ? s.end[b - 1] : 0);
+  const int4 own = s.own[b];
+  const int share = (own.z + kCombineWarps - 1) / kCombineWarps, lo = wid * share, hi = min(own.z, lo + share);
+  const int64_t slot = 2 * (int64_t)b * rows_per_tile + rr;
+  auto at = [&](int p) { return slot + (2 * p + (p == 0)) * rows_per_tile; };
+  // a piece without a maximum has no weight, unless its scores were not numbers
+  auto factor = [](float2 ml, float top) {
+    return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_approx(ml.x - top);
+  };
+  alignas(16) float x[kV] = {};
+  Vec v[8];
+  auto fetch = [&](int p0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (p0 + k < hi) v[k] = *reinterpret_cast<const Vec*>(a.part_o + at(p0 + k) * D + lane * kV);
+  };
+  auto ml_at = [&](int p) { return p < hi ? a.part_ml[at(p)] : make_float2(-INFINITY, 0.f); };
+  fetch(lo);
+  const float2 ml0 = ml_at(lo + (lane & 7));     // of the first eight pieces, four times over
+  float top = ml0.x, sum = 0.f;
+#pragma unroll 1
+  for (int p = lo + 8 + lane; p < hi; p += 32) top = fmaxf(top, a.part_ml[at(p)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 1
+  for (int p0 = lo; p0 < hi; p0 += 8) {
+    const float2 ml = p0 == lo ? ml0 : ml_at(p0 + (lane & 7));
+    if (p0 > lo) fetch(p0);
+    const float f = factor(ml, top);
+    sum += ml.y * f;                             // a lane's sum, four times over as well
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (p0 + k < hi) {
+        const float fp = __shfl_sync(0xffffffffu, f, k);
+        const float* e = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) x[j] = fmaf(e[j], fp, x[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  *reinterpret_cast<Vec*>(&s_x[wid][lane * kV]) = *reinterpret_cast<const Vec*>(x);
+  if (lane == 0) s_ml[wid] = make_float2(top, sum);
+  __syncthreads();
+  if (wid > 0) return;
+  const float2 ml = s_ml[lane % kCombineWarps];
+  top = ml.x;
+#pragma unroll
+  for (int o = kCombineWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float f = factor(ml, top);
+  sum = ml.y * f;
+#pragma unroll
+  for (int o = kCombineWarps / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* out = attn_out_row(a, own.w, own.x, own.y + rr) + lane * kV;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) x[j] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    const float fw = __shfl_sync(0xffffffffu, f, w);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) x[j] = fmaf(s_x[w][lane * kV + j], fw, x[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kV; j += 2)
+    *reinterpret_cast<uint32_t*>(out + j) = bf16_pair(x[j] * inv, x[j + 1] * inv);
+}
+
 template <int D, bool kS8, bool kQF32, int MT>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   constexpr int kJoin = kWarps * 16 * MT * (D + 8) * 4;
@@ -632,11 +735,15 @@ template <int D>
 static cudaError_t launch_combine(const AttnArgs& a, int rows_per_tile, cudaStream_t stream) {
   // the attention kernels' shared-memory configuration: an SM that had to
   // change it would drain first
-  static std::atomic<uint64_t> set{0};
-  const cudaError_t err = set_once(set, (const void*)attn_combine_kernel<D>,
+  const int sms = attn_sm_count();
+  const int64_t rows = a.T * (int64_t)a.n_q_heads;   // to join, at most
+  const bool by_row = rows <= kCombineRowsPerSm * sms;
+  auto kern = by_row ? attn_combine_row_kernel<D> : attn_combine_kernel<D>;
+  static std::atomic<uint64_t> set[2] = {};
+  const cudaError_t err = set_once(set[by_row], (const void*)kern,
                                    cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (err != cudaSuccess) return err;
-  return launch_pdl(attn_combine_kernel<D>, dim3(kCombinePerSm * attn_sm_count()), dim3(kCombineThreads), 0, stream, a,
+  return launch_pdl(kern, dim3(by_row ? (unsigned)rows : kCombinePerSm * sms), dim3(kCombineThreads), 0, stream, a,
                     rows_per_tile);
 }
 
