@@ -929,10 +929,9 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
           if (k >= seg) continue;             // stream 1 had no tile
           tmem_ld16(tlane + kColO + 128 * k + d, r);
           tmem_wait_ld();
-          if (f[k] != 0.f) {
+          // a factor of 0 counts as well: 0 times a visible infinity or NaN
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(r[e]), f[k], o[e]);
-          }
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(r[e]), f[k], o[e]);
         }
       } else {
         tmem_ld16(tlane + kColO + 128 * st + d, r);
