@@ -63,7 +63,10 @@ using namespace umma;
 constexpr int kTok = 128;                        // cached tokens per tile
 constexpr int kHalf = 128 * 128;                 // bytes of 128 rows x 64 bf16
 constexpr int kScaleRing = 8;
-constexpr int kBadRing = 32;                     // items' flags; the roles are at most 9 items apart
+// Items' flags, by number.  One is raised for an item whose tile has been fetched,
+// which is at most 8 items ahead of the rows (a tile each in the rings), so no item
+// that still needs its place; nothing is cleared.
+constexpr int kBadRing = 32;
 
 template <int D, bool kS8, int kRT>
 struct Tg {
@@ -113,7 +116,7 @@ struct TShared {
     RowItem item[8];                             // of the row warps (see row_warps)
     AttnFindScratch find;                        // before the roles begin
   };
-  int bad[kBadRing];                 // per item, by its number: a non-finite value was taken out
+  uint32_t bad[kBadRing];            // the last item + 1 with that number's remainder of which a non-finite value was taken out
   uint32_t tmem;
   int abort;
 };
@@ -279,7 +282,6 @@ QMM_DEV void scale_warps(const Ctx& x) {
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, G::kShape, it); ++seq) {
-    if (side && lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
     const int32_t* trow = a.table + (int64_t)it.r * a.ld_table;
     const int tok_end = min(it.len, (it.kv0 + it.seg) * kTok);
     int tok = it.kv0 * kTok + 4 * lane;
@@ -307,7 +309,7 @@ QMM_DEV void scale_warps(const Ctx& x) {
       pg_next = page_of(pl_next);
       if (!x.wait_all(&x.sh->bar.sc_empty[sc], phase)) return;
       const int from = it.seen - (it.kv0 + i) * kTok - 4 * lane;   // of the lane's four, the first that a row may not see
-      if (side && from < 4 && drop_nonfinite(v, from)) atomicOr(&x.sh->bad[seq % kBadRing], 1);
+      if (side && from < 4 && drop_nonfinite(v, from)) x.sh->bad[seq % kBadRing] = seq + 1;
       ring[sc * (2 * kTok / 4)] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.sh->bar.sc_full[sc]);
@@ -385,7 +387,6 @@ QMM_DEV void clean_warp(const Ctx& x) {
   walk.start(x.sh->work);
   AttnItem it;
   for (; walk.next(a, x.sh->work, G::kShape, it); ++seq) {
-    if (lane == 0) x.sh->bad[(seq + kBadRing / 2) % kBadRing] = 0;   // cleared well ahead
 #pragma unroll 1
     for (int i = 0; i < it.seg; ++i) {
       const uint32_t slot = vals.slot;
@@ -426,7 +427,7 @@ QMM_DEV void clean_warp(const Ctx& x) {
           sts128(at(k), w);
         }
       }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&x.sh->bad[seq % kBadRing], 1);
+      if (__any_sync(0xffffffffu, bad) && lane == 0) x.sh->bad[seq % kBadRing] = seq + 1;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.sh->bar.full[slot]);
@@ -911,7 +912,7 @@ QMM_DEV AttnOwned row_warps(const Ctx& x) {
       }
     }
     tc_fence_after();
-    const bool bad = x.sh->bad[seq % kBadRing] != 0;
+    const bool bad = x.sh->bad[seq % kBadRing] == seq + 1;
     // 16 columns of O at a time, of both streams with kRT == 1 (each takes half
     // of the columns).  Loops, not straight code: it runs once per item, and
     // fetching instructions would cost more than running them.

@@ -61,3 +61,29 @@ def test_seen_values_of_no_weight(qmm, cuda, new, heads, s8, bad):
         assert np.array_equal(~np.isfinite(ref), hit.cpu().numpy()[None].repeat(n, 0))
         assert torch.equal(got_hit[first:first + n], hit[None].expand(n, heads, d)), (c, n)
     assert torch.equal(got[:, ~hit], clean[:, ~hit])
+
+
+@pytest.mark.parametrize("s8", [False, True])
+def test_many_row_tiles_of_one_token(qmm, cuda, s8):
+    """A new token whose 4608 query heads per key head fill 18 tiles of rows, of
+    requests that end with a cached tile: only the first tile of rows has tokens
+    to clean in its cached tiles, and nothing holds that warp back in the next 17.
+    The token's infinity is there for every row all the same."""
+    R, kv, heads, d, page = 16, 14, 14 * 4608, 64, 32
+    s = build(cuda, [127] * R, [1] * R, kv, kv, d, page, s8, seed=3)
+    for _, _, pg, off in s["rows"]:
+        if s8:
+            s["vs"][pg[127], :, off[127]] = float("inf")
+            code = s["v"][pg[127], off[127]]
+            code[code == 0] = 1
+            s["v"][pg[127], off[127]] = code
+        else:
+            s["v"][pg[127], off[127], :, 5] = float("inf")
+    g = torch.Generator(device=cuda).manual_seed(4)
+    s["q"] = torch.randn((R, heads, d), generator=g, device=cuda).to(torch.bfloat16)
+    out = call(qmm, cuda, s)
+    if s8:
+        assert torch.isinf(out).all()
+    else:
+        assert (out[..., 5] == float("inf")).all()
+        assert torch.isfinite(out[..., :5]).all() and torch.isfinite(out[..., 6:]).all()
