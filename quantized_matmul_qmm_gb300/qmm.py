@@ -142,10 +142,13 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_of(t):
     """The handle of torch's current stream on t's device (a decoding step makes
     many small calls: _stream's Stream object alone takes 3 us)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _raw_stream(t.get_device())
 
 
 def _size(fn, *args) -> int:
@@ -509,6 +512,32 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_I32, _I64 = torch.int32, torch.int64
+
+
+def _ints(fn, dtype, *tensors):
+    """Lengths, slots and the like are read as plain arrays: refused unless they are."""
+    for t in tensors:
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{fn}: not a contiguous {dtype} tensor: {t.dtype}, strides {t.stride()}")
+
+
+def _status_addr(fn, t):
+    if t is None:
+        return None
+    if t.dtype is not _I32:
+        raise ValueError(f"{fn}: dev_status is not contiguous int32: {t.dtype}")
+    return t.data_ptr()
+
+
+def _table(fn, t):
+    """(rows, columns, row stride) of a block table or mask (of words without a sign, too)."""
+    (rows, cols), (ld, inner) = t.shape, t.stride()
+    if t.dtype is not _I32 and t.dtype is not torch.uint32 or inner != 1 and cols > 1:
+        raise ValueError(f"{fn}: not a 32-bit table of contiguous rows: {t.dtype}, strides {(ld, inner)}")
+    return rows, cols, ld if rows > 1 else max(ld, cols)
+
+
 def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> QmmKvCache:
     n_pages, page_size, n_heads, head_dim = k_cache.shape
     sp, st, sh, sd = strides = k_cache.stride()
@@ -531,20 +560,32 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Te
     positions int32 [max_tokens] are written, and with parents (int32
     [max_tokens]) the mask int32 [max_tokens][words].  Returns (cu_new int32
     [R+1], pages_taken int32 [1])."""
-    R, T = ctx_lens.shape[0], slots.shape[0]
+    R, T = ctx_lens.numel(), slots.numel()
     if cu_new is None:
-        cu_new = torch.empty(R + 1, dtype=torch.int32, device=ctx_lens.device)
+        cu_new = torch.empty(R + 1, dtype=_I32, device=ctx_lens.device)
     if pages_taken is None:
-        pages_taken = torch.empty(1, dtype=torch.int32, device=ctx_lens.device)
-    if new_lens.shape[0] != R or block_table.shape[0] != R or positions.shape[0] != T or cu_new.shape[0] != R + 1 \
-            or (parents is not None and parents.shape[0] != T) or (mask is not None and mask.shape[0] != T):
+        pages_taken = torch.empty(1, dtype=_I32, device=ctx_lens.device)
+    # one expression: in a decoding step the call's time is the CPU's
+    if not (ctx_lens.dtype is new_lens.dtype is free_pages.dtype is positions.dtype is cu_new.dtype
+            is pages_taken.dtype is _I32 and slots.dtype is _I64 and ctx_lens.is_contiguous()
+            and new_lens.is_contiguous() and free_pages.is_contiguous() and positions.is_contiguous()
+            and cu_new.is_contiguous() and slots.is_contiguous()):
+        raise ValueError("kv_plan: slots must be contiguous int64, the other lists contiguous int32")
+    (rows, blocks, ld_table), words, ld_mask = _table("kv_plan", block_table), 0, 0
+    agree = new_lens.numel() == R == rows and positions.numel() == T and cu_new.numel() == R + 1
+    if parents is not None:
+        _ints("kv_plan", _I32, parents)
+        agree = agree and parents.numel() == T
+    if mask is not None:
+        mask_rows, words, ld_mask = _table("kv_plan", mask)
+        agree = agree and mask_rows == T
+    if not agree:
         raise ValueError("kv_plan: shapes do not agree")
-    ld_mask, words = (0, 0) if mask is None else (mask.stride(0), mask.shape[1])
     _check("qmm_kv_plan", lib.qmm_kv_plan(
-        ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.shape[0],
-        block_table.data_ptr(), block_table.stride(0), block_table.shape[1], page_size, _addr(parents), _addr(mask),
+        ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.numel(),
+        block_table.data_ptr(), ld_table, blocks, page_size, _addr(parents), _addr(mask),
         ld_mask, words, T, cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), pages_taken.data_ptr(),
-        _addr(dev_status), _stream_of(slots)))
+        _status_addr("kv_plan", dev_status), _stream_of(slots)))
     return cu_new, pages_taken
 
 
@@ -555,12 +596,14 @@ def kv_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, k_cache: to
     with scales fp32 [pages][heads][page_size], through qmm_kv_append."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     (kt, kh, kd), (vt, vh, vd) = K.stride(), V.stride()
-    if V.shape != K.shape or V.dtype != K.dtype or kd != 1 or vd != 1 or K.shape[0] != slots.shape[0] \
-            or K.shape[1:] != k_cache.shape[2:]:
+    T, heads, head_dim = shape = K.shape
+    if V.shape != shape or V.dtype != K.dtype or kd != 1 or vd != 1 or T != slots.numel() \
+            or heads != cache.n_heads or head_dim != cache.head_dim:
         raise ValueError("kv_append: K, V, slots and the cache do not agree")
+    _ints("kv_append", _I64, slots)
     _check("qmm_kv_append", lib.qmm_kv_append(
-        K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, _ROW_TYPES[K.dtype], K.shape[0], slots.data_ptr(),
-        cache, _addr(dev_status), _stream_of(k_cache)))
+        K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, _ROW_TYPES[K.dtype], T, slots.data_ptr(),
+        cache, _status_addr("kv_append", dev_status), _stream_of(k_cache)))
 
 
 def tree_attention_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
@@ -575,23 +618,27 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     or None for causal chunks and plain decoding; scale 1 / sqrt(head_dim) by
     default.  Returns out, bf16 [T][q heads][head_dim]."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    T, heads, head_dim = q.shape
+    T, heads, head_dim = shape = q.shape
     if out is None:
-        out = torch.empty((T, heads, head_dim), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     (qt, qh, qd), (ot, oh, od) = q.stride(), out.stride()
-    if head_dim != k_cache.shape[3] or out.shape != q.shape or out.dtype != torch.bfloat16 or qd != 1 or od != 1 \
-            or cu_new.shape[0] != ctx_lens.shape[0] + 1 or block_table.shape[0] != ctx_lens.shape[0] \
-            or (mask is not None and mask.shape[0] != T):
+    R = ctx_lens.numel()
+    rows, blocks, ld_table = _table("tree_attention", block_table)
+    mask_rows, words, ld_mask = (T, None, 0) if mask is None else _table("tree_attention", mask)
+    if head_dim != cache.head_dim or out.shape != shape or out.dtype != torch.bfloat16 or qd != 1 or od != 1 \
+            or cu_new.numel() != R + 1 or rows != R or mask_rows != T \
+            or (mask is not None and words * 32 < max_new):
         raise ValueError("tree_attention: shapes do not agree")
+    _ints("tree_attention", _I32, ctx_lens, cu_new)
     if workspace is None:
-        workspace = torch.empty(tree_attention_workspace_size(heads, k_cache.shape[2], head_dim, max_new),
+        workspace = torch.empty(tree_attention_workspace_size(heads, cache.n_heads, head_dim, max_new),
                                 dtype=torch.uint8, device=q.device)
     _check("qmm_tree_attention", lib.qmm_tree_attention(
         q.data_ptr(), _ROW_TYPES[q.dtype], qt, qh, heads, cache, block_table.data_ptr(),
-        block_table.stride(0), block_table.shape[1], ctx_lens.data_ptr(), cu_new.data_ptr(), ctx_lens.shape[0], T,
-        max_new, _addr(mask), 0 if mask is None else mask.stride(0),
+        ld_table, blocks, ctx_lens.data_ptr(), cu_new.data_ptr(), R, T,
+        max_new, _addr(mask), ld_mask,
         head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, workspace.data_ptr(),
-        workspace.nbytes, _addr(dev_status), _stream_of(q)))
+        workspace.nbytes, _status_addr("tree_attention", dev_status), _stream_of(q)))
     return out
 
 
