@@ -758,8 +758,8 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * n_q_heads / n_heads), and rounded to bf16 once (2^-8) otherwise; the output
  * is rounded once.
  * Device status: QMM_ERR_INVALID_ARG for lengths that do not fit (negative,
- * more than max_new or T, more than max_blocks pages): that request's rows of
- * out are left alone; and for a page id outside [0, n_pages), whose request's
+ * more than max_new or T, more than max_blocks pages, 2^31 - 8192 tokens or
+ * more): that request's rows of out are left alone; and for a page id outside [0, n_pages), whose request's
  * rows are then unspecified.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
  * pointers, bad types, sizes, strides or scale, n_q_heads not a multiple of

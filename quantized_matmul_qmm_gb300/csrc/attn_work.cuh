@@ -33,12 +33,17 @@ struct AttnReq {
   int row_tiles, kv_tiles;   // 0 row tiles: nothing to do
 };
 
+// Token numbers are 32-bit and step past a request's end: the tile kernel looks
+// pages up for the 32 boxes of up to 128 tokens from a tile's first, five tiles
+// ahead of the last (4863 tokens), the row kernel eight steps of 64.
+constexpr int kAttnMaxLen = INT32_MAX - 8192;
+
 // Lengths that do not fit the call's buffers give no work, and the status.
 QMM_DEV AttnReq attn_req(const AttnArgs& a, int r, AttnShape sh) {
   AttnReq q{};
   const int L = a.ctx[r], c0 = a.cu[r], c1 = a.cu[r + 1];
   const int64_t n = (int64_t)c1 - c0, len = (int64_t)L + n;
-  if (L < 0 || c0 < 0 || n < 0 || c1 > a.T || n > a.max_new || len > INT32_MAX - 256 || len > a.max_len) {
+  if (L < 0 || c0 < 0 || n < 0 || c1 > a.T || n > a.max_new || len > kAttnMaxLen || len > a.max_len) {
     set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     return q;
   }
