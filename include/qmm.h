@@ -706,8 +706,9 @@ typedef struct {
  *         (token, head), 16-byte aligned with strides of whole 16 bytes; the
  *         head's elements are contiguous.
  * slots   int64 [T]: -1 skips the token; any other slot outside the cache is
- *         skipped with QMM_ERR_INVALID_ARG in dev_status.  Two tokens with one
- *         slot leave either one's values there.
+ *         skipped with QMM_ERR_INVALID_ARG in dev_status.  What two
+ *         tokens of a call with one slot leave there is unspecified (a row's
+ *         pieces and its scale are written apart).
  * bf16 cache: rounded once to nearest even.  int8 cache, per (token, head):
  *   s = fl(amax / 127), q = clamp(rint_even(fl(x / s)), -127, 127), 0 where
  * s == 0 (packB's rule, bit-exact); x must be finite there, else that row's
