@@ -671,8 +671,8 @@ qmm_status qmm_q8_gemm(const void* tiles, qmm_q8_layout layout, int64_t N, int64
  * slot -1.
  * Errors: QMM_ERR_INVALID_ARG for null or misaligned pointers, R < 1, a short
  * stride, page_size or max_blocks < 1, negative sizes, a mask without parents
- * or the reverse; QMM_ERR_UNSUPPORTED for R > 16384, or page_size or
- * max_tokens >= 2^31.
+ * or the reverse; QMM_ERR_UNSUPPORTED for R > 16384, page_size >= 2^31 (the
+ * cache's own limit is 2^30), max_tokens >= 2^31 - 1 or mask_words > 2^20.
  */
 qmm_status qmm_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t R, const int32_t* free_pages,
                        int64_t n_free, int32_t* block_table, int64_t ld_table, int64_t max_blocks,
@@ -687,7 +687,8 @@ qmm_status qmm_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t
  * type QMM_BF16: the rows as they are.  QMM_S8: int8 codes, value =
  * code * scale with one fp32 scale per (page, head, place):
  * k_scale, v_scale [n_pages][n_heads][page_size] (NULL for QMM_BF16).
- * head_dim 64 or 128 (else QMM_ERR_UNSUPPORTED); k and v 16-byte aligned,
+ * head_dim 64 or 128, page_size < 2^30, n_heads <= 65535 and n_pages < 2^31
+ * (else QMM_ERR_UNSUPPORTED); k and v 16-byte aligned,
  * strides of whole 16 bytes (of a dimension of one row: anything), scales
  * 4-byte aligned; the rows of different (page, place, head) must not overlap. */
 typedef struct {
@@ -714,8 +715,8 @@ typedef struct {
  * s == 0 (packB's rule, bit-exact); x must be finite there, else that row's
  * codes and scale are unspecified.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
- * pointers, bad types, sizes or strides; QMM_ERR_UNSUPPORTED for another
- * head_dim, T * n_heads >= 2^31 * 8 or page_size >= 2^31.
+ * pointers, bad types, sizes or strides; QMM_ERR_UNSUPPORTED for a
+ * cache beyond its limits, T >= 2^31 or T * n_heads >= 8 * (2^31 - 1).
  */
 qmm_status qmm_kv_append(const void* K, int64_t k_stride_token, int64_t k_stride_head, const void* V,
                          int64_t v_stride_token, int64_t v_stride_head, qmm_dtype type, int64_t T,
@@ -764,8 +765,9 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * rows are then unspecified.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
  * pointers, bad types, sizes, strides or scale, n_q_heads not a multiple of
- * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for another head_dim, or
- * max_new * n_q_heads / n_heads, R, T or page_size >= 2^30.
+ * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for a cache
+ * beyond its limits, n_q_heads > 65535, R or T >= 2^30, or max_new >= 2^30 /
+ * (n_q_heads / n_heads), rounded down.
  */
 qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_token, int64_t q_stride_head,
                               int64_t n_q_heads, const qmm_kv_cache* cache, const int32_t* block_table,
