@@ -761,8 +761,11 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * is rounded once.
  * Device status: QMM_ERR_INVALID_ARG for lengths that do not fit (negative,
  * more than max_new or T, more than max_blocks pages, 2^31 - 8192 tokens or
- * more): that request's rows of out are left alone; and for a page id outside [0, n_pages), whose request's
- * rows are then unspecified.
+ * more): that request's rows of out are left alone; for a call whose work,
+ * counted in tiles of query rows times cached tokens (256 x 128; up to 128 query
+ * rows per key head 128 x 128, and where page_size is no multiple of 8, 32 x 64)
+ * plus up to 6 per tile of rows, passes 2^31 - 1: all rows are left alone; and for
+ * a page id outside [0, n_pages), whose request's rows are then unspecified.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
  * pointers, bad types, sizes, strides or scale, n_q_heads not a multiple of
  * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for a cache

@@ -74,3 +74,25 @@ def test_longer_is_refused(qmm, cuda, over, s8, new):
     status, out, _, _ = run(qmm, cuda, s8, new, MOST + over)
     assert status == qmm.QMM_ERR_INVALID_ARG
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("requests", [1, 40])
+@pytest.mark.parametrize("page,heads,new", [(PAGE, 1024, 129), (PAGE - 1, 104, 20)])
+def test_more_work_than_a_call_counts(qmm, cuda, page, heads, new, requests):
+    """2^24 cached tiles of 128 tokens times 516 tiles of 256 rows, or 2^25 of 64
+    times 65 of 32 rows (pages that TMA does not take): reported, nothing written,
+    however many requests share the step."""
+    length = MOST - 1000
+    k = torch.zeros((1, page, 1, D), dtype=torch.bfloat16, device=cuda)
+    q = torch.zeros((new, heads, D), dtype=torch.bfloat16, device=cuda)
+    out = torch.full_like(q, 7.0)
+    table = torch.zeros((requests, -(-length // page)), dtype=torch.int32, device=cuda)
+    ctx = torch.full((requests,), length - new, dtype=torch.int32, device=cuda)
+    cu = torch.full((requests + 1,), new, dtype=torch.int32, device=cuda)
+    cu[0] = 0
+    mask = torch.full((new, (new + 31) // 32), -1, dtype=torch.int32, device=cuda)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    qmm.tree_attention(q, k, k, table, ctx, cu, new, mask=mask, out=out, dev_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == qmm.QMM_ERR_INVALID_ARG
+    assert (out == 7).all()
