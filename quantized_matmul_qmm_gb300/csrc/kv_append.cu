@@ -158,16 +158,16 @@ kv_append_kernel(const KvAppendArgs a) {
 // same (4000 tokens x 8 heads, fp32 to bf16: two pairs 9.2 us, one 10.1; from 8191
 // tokens on four pairs are as fast as two, and 4000 would be below their limit).
 constexpr int kMany = 2;
-constexpr int64_t kManyFrom = (int64_t)152 * 64 * kMany;
+int64_t many_from() { return (int64_t)attn_sm_count() * 64 * kMany; }   // 64 warps per SM
 
 template <bool kBf16, bool kS8, int kN>
 cudaError_t launch_sized(const KvAppendArgs& a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.T * a.cache.n_heads;
-  const int64_t per_block = kAppendThreads / 32 * (rows >= kManyFrom ? kMany : 1);
+  const bool many = rows >= many_from();
+  const int64_t per_block = kAppendThreads / 32 * (many ? kMany : 1);
   const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
-  return rows >= kManyFrom
-             ? launch_pdl(kv_append_kernel<kBf16, kS8, kN, kMany>, grid, dim3(kAppendThreads), 0, stream, a)
-             : launch_pdl(kv_append_kernel<kBf16, kS8, kN, 1>, grid, dim3(kAppendThreads), 0, stream, a);
+  return many ? launch_pdl(kv_append_kernel<kBf16, kS8, kN, kMany>, grid, dim3(kAppendThreads), 0, stream, a)
+              : launch_pdl(kv_append_kernel<kBf16, kS8, kN, 1>, grid, dim3(kAppendThreads), 0, stream, a);
 }
 
 template <bool kBf16, bool kS8>
