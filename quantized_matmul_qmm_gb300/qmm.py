@@ -530,12 +530,12 @@ def _status_addr(fn, t):
     return t.data_ptr()
 
 
-def _table(fn, t):
-    """(rows, columns, row stride) of a block table or mask (of words without a sign, too)."""
+def _row_stride(fn, t):
+    """Of a block table or mask (of words without a sign, too)."""
     (rows, cols), (ld, inner) = t.shape, t.stride()
     if t.dtype is not _I32 and t.dtype is not torch.uint32 or inner != 1 and cols > 1:
         raise ValueError(f"{fn}: not a 32-bit table of contiguous rows: {t.dtype}, strides {(ld, inner)}")
-    return rows, cols, ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> QmmKvCache:
@@ -565,27 +565,42 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Te
         cu_new = torch.empty(R + 1, dtype=_I32, device=ctx_lens.device)
     if pages_taken is None:
         pages_taken = torch.empty(1, dtype=_I32, device=ctx_lens.device)
-    # one expression: in a decoding step the call's time is the CPU's
+    # Checks in line, few calls: a decoding step waits for this code, not for the kernel.
+    rows, blocks = block_table.shape
+    ld_table, inner = block_table.stride()
+    if inner != 1 or rows == 1 or block_table.dtype is not _I32:
+        ld_table = _row_stride("kv_plan", block_table)
+    agree = rows == R == new_lens.numel() and positions.numel() == T and cu_new.numel() == R + 1
+    p_parents = p_mask = p_status = None
+    words = ld_mask = 0
+    if parents is not None:
+        agree = agree and parents.numel() == T
+        if parents.dtype is not _I32 or not parents.is_contiguous():
+            _ints("kv_plan", _I32, parents)
+        p_parents = parents.data_ptr()
+    if mask is not None:
+        mask_rows, words = mask.shape
+        agree = agree and mask_rows == T
+        ld_mask, inner = mask.stride()
+        if inner != 1 or mask_rows == 1 or mask.dtype is not _I32:
+            ld_mask = _row_stride("kv_plan", mask)
+        p_mask = mask.data_ptr()
+    if not agree:
+        raise ValueError("kv_plan: shapes do not agree")
+    if dev_status is not None:
+        p_status = _status_addr("kv_plan", dev_status)
     if not (ctx_lens.dtype is new_lens.dtype is free_pages.dtype is positions.dtype is cu_new.dtype
             is pages_taken.dtype is _I32 and slots.dtype is _I64 and ctx_lens.is_contiguous()
             and new_lens.is_contiguous() and free_pages.is_contiguous() and positions.is_contiguous()
             and cu_new.is_contiguous() and slots.is_contiguous()):
         raise ValueError("kv_plan: slots must be contiguous int64, the other lists contiguous int32")
-    (rows, blocks, ld_table), words, ld_mask = _table("kv_plan", block_table), 0, 0
-    agree = new_lens.numel() == R == rows and positions.numel() == T and cu_new.numel() == R + 1
-    if parents is not None:
-        _ints("kv_plan", _I32, parents)
-        agree = agree and parents.numel() == T
-    if mask is not None:
-        mask_rows, words, ld_mask = _table("kv_plan", mask)
-        agree = agree and mask_rows == T
-    if not agree:
-        raise ValueError("kv_plan: shapes do not agree")
-    _check("qmm_kv_plan", lib.qmm_kv_plan(
+    status = lib.qmm_kv_plan(
         ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.numel(),
-        block_table.data_ptr(), ld_table, blocks, page_size, _addr(parents), _addr(mask),
+        block_table.data_ptr(), ld_table, blocks, page_size, p_parents, p_mask,
         ld_mask, words, T, cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), pages_taken.data_ptr(),
-        _status_addr("kv_plan", dev_status), _stream_of(slots)))
+        p_status, _raw_stream(slots.get_device()))
+    if status != QMM_OK:
+        _check("qmm_kv_plan", status)
     return cu_new, pages_taken
 
 
@@ -623,12 +638,13 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     (qt, qh, qd), (ot, oh, od) = q.stride(), out.stride()
     R = ctx_lens.numel()
-    rows, blocks, ld_table = _table("tree_attention", block_table)
-    mask_rows, words, ld_mask = (T, None, 0) if mask is None else _table("tree_attention", mask)
+    rows, blocks = block_table.shape
     if head_dim != cache.head_dim or out.shape != shape or out.dtype != torch.bfloat16 or qd != 1 or od != 1 \
-            or cu_new.numel() != R + 1 or rows != R or mask_rows != T \
-            or (mask is not None and words * 32 < max_new):
+            or cu_new.numel() != R + 1 or rows != R \
+            or (mask is not None and (mask.shape[0] != T or mask.shape[1] * 32 < max_new)):
         raise ValueError("tree_attention: shapes do not agree")
+    ld_table = _row_stride("tree_attention", block_table)
+    ld_mask = 0 if mask is None else _row_stride("tree_attention", mask)
     _ints("tree_attention", _I32, ctx_lens, cu_new)
     if workspace is None:
         workspace = torch.empty(tree_attention_workspace_size(heads, cache.n_heads, head_dim, max_new),

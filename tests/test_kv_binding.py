@@ -20,7 +20,7 @@ def calls(qmm, monkeypatch):
             return entry
 
     monkeypatch.setattr(qmm, "lib", Lib())
-    monkeypatch.setattr(qmm, "_stream_of", lambda t: 0)
+    monkeypatch.setattr(qmm, "_raw_stream", lambda device: 0)
     return seen
 
 
