@@ -753,8 +753,9 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * past a request's length, and infinities or NaN in hidden tokens.  An
  * infinity or NaN among the values that a row does see makes its output element
  * non-finite.  Products are of bf16 values (int8 codes are exact in bf16; their
- * scales are applied in fp32), and every sum is fp32, in a fixed order: results
- * are the same from run to run.  The weights exp(s - max) multiply v as two
+ * scales are applied in fp32), and every sum is fp32, in a fixed order: the same
+ * call gives the same results from run to run (beside other requests or another
+ * max_new a request's work is cut elsewhere, and its sums round otherwise).  The weights exp(s - max) multiply v as two
  * bf16 terms (within 2^-16) for a request of up to 64 query rows per key head
  * (its new tokens * n_q_heads / n_heads) in a call of up to 128 (max_new *
  * n_q_heads / n_heads), and rounded to bf16 once (2^-8) otherwise; the output
