@@ -754,24 +754,24 @@ qmm_status qmm_tree_attention_workspace_size(int64_t n_q_heads, int64_t n_kv_hea
  * infinity or NaN among the values that a row does see makes its output element
  * non-finite.  Products are of bf16 values (int8 codes are exact in bf16; their
  * scales are applied in fp32), and every sum is fp32, in a fixed order: the same
- * call gives the same results from run to run (beside other requests or another
- * max_new a request's work is cut elsewhere, and its sums round otherwise).  The weights exp(s - max) multiply v as two
- * bf16 terms (within 2^-16) for a request of up to 64 query rows per key head
- * (its new tokens * n_q_heads / n_heads) in a call of up to 128 (max_new *
- * n_q_heads / n_heads), and rounded to bf16 once (2^-8) otherwise; the output
- * is rounded once.
+ * call gives the same results from run to run (beside other requests, or with
+ * another max_new, a request's work is cut elsewhere and its sums round
+ * otherwise).  The weights exp(s - max) multiply v as two bf16 terms (within
+ * 2^-16) for a request of up to 64 query rows per key head (its new tokens *
+ * n_q_heads / n_heads) in a call of up to 128 (max_new * n_q_heads / n_heads),
+ * and rounded to bf16 once (2^-8) otherwise; the output is rounded once.
  * Device status: QMM_ERR_INVALID_ARG for lengths that do not fit (negative,
  * more than max_new or T, more than max_blocks pages, 2^31 - 8192 tokens or
  * more): that request's rows of out are left alone; for a call whose work,
- * counted in tiles of query rows times cached tokens (256 x 128; up to 128 query
- * rows per key head 128 x 128, and where page_size is no multiple of 8, 32 x 64)
- * plus up to 6 per tile of rows, passes 2^31 - 1: all rows are left alone; and for
- * a page id outside [0, n_pages), whose request's rows are then unspecified.
+ * counted in tiles of query rows times cached tokens (of 256 x 128 at most; of
+ * 32 x 64 where page_size is no multiple of 8) plus up to 6 per tile of rows,
+ * passes 2^31 - 1: all rows are left alone; and for a page id outside
+ * [0, n_pages), whose request's rows are then unspecified.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
  * pointers, bad types, sizes, strides or scale, n_q_heads not a multiple of
- * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for a cache
- * beyond its limits, n_q_heads > 65535, R or T >= 2^30, or max_new >= 2^30 /
- * (n_q_heads / n_heads), rounded down.
+ * n_heads; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for a cache beyond its
+ * limits, n_q_heads > 65535, R or T >= 2^30, or max_new >= 2^30 / (n_q_heads /
+ * n_heads), rounded down.
  */
 qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_token, int64_t q_stride_head,
                               int64_t n_q_heads, const qmm_kv_cache* cache, const int32_t* block_table,

@@ -6,8 +6,9 @@
 // that the row's mask (or the chain) names.  One pass over the cache with a
 // running maximum and sum in fp32 (the exponentials in base 2).
 //
-// Decoding has 2 operations per row and cached byte at bf16, so up to 64 rows
-// or so the cache's bytes are all that costs.  The kernel is a stream: four
+// Decoding has one operation per row and cached byte at bf16 (4 D operations, 4 D
+// bytes per token), so for the up to 16 rows that come here the cache's bytes are
+// all that costs.  The kernel is a stream: four
 // warps per block, each with its own ring of 16-token groups (cp.async, no
 // block barrier inside an item), two blocks per SM; a group's rows are
 // multiplied with mma.sync (16 x 8 x 16, bf16 with fp32 sums) straight from
@@ -27,10 +28,18 @@
 // The sums are fp32.
 //
 // Measured, heads of 128: one token of 64 requests at 3 to 8191 cached tokens,
-// bf16, 173 us for 1.08 GB (0.94 of a copy's rate); one token at 400k tokens and
-// 8 key heads, bf16 255 us (0.96), int8 231 us (0.55: half the bytes, and more
-// instructions per byte than issue slots); one token at 777, 9 us: the chains of
-// loads of two launches.
+// bf16, 173 us for 1.08 GB (0.92 of a copy's rate), fp32 queries 1 % more, int8
+// 154 us for 0.54 GB (0.52); one token at 400k tokens and 8 key heads, bf16 252 us
+// (0.96), int8 222 us (0.56: half the bytes, and more instructions per byte than
+// issue slots); one token at 777, 8 to 9 us: the chains of loads of two launches.
+// Heads of 64: 64 requests 119 us for 0.52 GB (0.65, the same steps for half the
+// bytes).
+//
+// More rows come here where pages or scales do not allow the tile kernel's boxes
+// (attn_pages_tile), in items of 32 rows, each of which reads the cache again: 32
+// rows over 200k tokens, pages of 20, 180 us (pages of 16 and tiles 173), int8 190
+// (163); 128 rows over 50k 181 us (54); chunks of 300 to 512 tokens 425 us (64).
+// Pages that are a multiple of 8 avoid it.
 //
 // Rows of the cache past a request's length are never read (cp.async writes
 // zeros in their place).  A new token's value row is read by all query rows
@@ -765,7 +774,7 @@ int attn_sm_count() {
 
 bool attn_pages_tile(const KvView& c, bool s8) {
   // TMA boxes of whole 8-row groups inside a page, strides that a tensor map
-  // holds, and bulk copies of 16-byte aligned scales
+  // holds, and 16-byte loads of four scales
   constexpr int64_t kMaxStride = (int64_t)1 << 40;
   return c.page_size % 8 == 0 && c.st_page < kMaxStride && c.st_token < kMaxStride && c.st_head < kMaxStride &&
          (!s8 || (aligned(c.k_scale, 16) && aligned(c.v_scale, 16)));

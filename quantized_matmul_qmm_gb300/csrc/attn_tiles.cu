@@ -25,6 +25,11 @@
 // Up to 64 rows the tile's other 64 lanes hold the same rows again, and their P
 // the part of each weight that the first bf16 rounding left over: the padded
 // products then give the weights 16 bits for nothing (see attn_rows.cu).
+// With more rows no lane is free and a second term would be a product of its own:
+// half as many operations again where the tensor pipe is 60 % busy, and another
+// 64 columns of TMEM that the two streams do not leave.  There the weights are
+// rounded to bf16 once, and the outputs' error against 64 bits is 0.0020 (chunks)
+// to 0.0023 (512 rows) of their size, 0.0016 of it the outputs' own rounding.
 //
 // The reference m moves only when a tile's maximum passes it by 2^8 in the
 // weights, so that O is rarely rescaled (it is in TMEM, not in registers).
@@ -40,15 +45,21 @@
 // What bounds it: 4 * 128 operations per row and token against 512 (bf16) or
 // 264 (int8) bytes per token: the cache's bytes up to about 128 rows, the
 // tensor pipe and the exponentials above.  Measured, heads of 128:
-//   bf16, 400k tokens, 8 key heads, pages of 64: 128 rows 255 us (0.96 of a copy's
-//   rate); pages of 16: 32 rows 324 to 336 us (0.73: 64 TMA boxes per tile);
+//   bf16, 400k tokens, 8 key heads, pages of 64: 128 rows 254 us (0.95 of a copy's
+//   rate); pages of 16: 32 to 128 rows 324 to 336 us (0.74: 64 TMA boxes per tile);
 //   bf16, 400k tokens, 512 rows: 0.76 of a library product's rate; 16 trees of 64
-//   nodes (512 rows) at 6k to 16k tokens 167 us (0.58; 16 us of it the joining);
-//   int8, 200k tokens, 32 rows: 165 us (0.38 of a copy's rate).  It is bound by the
-//   converters' and rows' shared-memory passes and their issue slots, about 9300
-//   warp instructions per tile;
-//   chunks of 300 to 512 tokens at 0 to 6000: 65 us, of which a block spends about
-//   9 us per item on queries, the first and last steps and fp32 partial outputs.
+//   nodes (512 rows) at 6k to 16k tokens 167 to 170 us (0.60; 16 us of it the joining),
+//   fp32 queries 178, heads of 64 127 us (0.40: the exponentials are as many);
+//   a prompt of 8192 tokens, 32 heads: 508 us (0.57);
+//   int8, 32 rows at 200k tokens 163 us (0.38 of a copy's rate), 128 rows at 400k 290
+//   (0.43), 512 rows at 6k to 16k 258 (0.39 of a library product's rate), a prompt of
+//   8192 tokens 738 us (0.39).  It is bound by the converters' and rows' shared-memory
+//   passes and their issue slots, about 9300 warp instructions per tile;
+//   chunks of 300 to 512 tokens at 0 to 6000: 64 us (int8 86, heads of 64 50, fp32
+//   queries 69), of which a block spends about 9 us per item on queries, the first
+//   and last steps and fp32 partial outputs.
+// The call's max_new chooses the kernel for all of its requests: 63 requests of one
+// token at 3 to 8191 beside a chunk of 512 take 263 us, apart 164 and 44.
 #include <algorithm>
 #include <type_traits>
 
@@ -82,9 +93,13 @@ struct Tg {
   static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
   static constexpr int kOffScale = kOffRaw + kRawSlots * kRaw;
   static constexpr int kBytes = kOffScale + (kS8 ? kScaleRing * 2 * kTok * 4 : 0);
-  // An item's setup takes about 9 us, a tile 1 to 2 (bf16) or 2 (int8).  Chunks of
-  // 300 to 512 tokens, bf16: 2 units 83.5 us, 4 70.9, 6 65.2, 8 66.0; int8 trees of
-  // 9 to 25: 2 35.9, 4 34.1, 6 35.7.
+  // An item's setup takes about 9 us, a tile 1 to 2 (bf16) or 2 (int8).  In us with
+  // 0, 3, 6 and 10 units (bf16), 0, 3, 4 and 10 (int8):
+  //   chunks of 300 to 512 tokens   123  75.5 63.8 65.2     136  84.6 86.0 97.8
+  //   trees of 9 to 25 nodes        37.8 35.7 33.4 34.8     36.8 33.3 31.6 36.0
+  //   512 rows at 6k to 16k         175  171  167  166      265  258  258  275
+  //   a prompt of 8192 tokens       648  523  508  527      872  731  739  790
+  //   128 rows at 400k              259  257  253  251      296  291  290  290
   static constexpr AttnShape kShape{128 * kRT, kTok, kS8 ? 4 : 6};
   static constexpr bool kShared = !kS8;          // one S for both streams (see the top)
   static constexpr int kAhead = (kRT == 1 ? 2 : 1) + (kShared ? 1 : 0);   // key tiles fetched ahead of value tiles
@@ -116,7 +131,7 @@ struct TShared {
     RowItem item[8];                             // of the row warps (see row_warps)
     AttnFindScratch find;                        // before the roles begin
   };
-  uint32_t bad[kBadRing];            // the last item + 1 with that number's remainder of which a non-finite value was taken out
+  uint32_t bad[kBadRing];            // [i % kBadRing] = i + 1: a non-finite value was taken out of item i
   uint32_t tmem;
   int abort;
 };

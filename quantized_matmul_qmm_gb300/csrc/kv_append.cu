@@ -8,10 +8,12 @@
 // 16 lanes and every byte is read and written once, 16 bytes per lane and load.
 // With many pairs a warp takes kPer that follow one another, has all their loads
 // in flight and works out a token's place once.  Into bf16 bound by HBM: 16384
-// tokens of 8 heads x 128 in fp32 30.0 us (201 MB, 1.0 of a copy's rate), in bf16
-// 21.8 (0.92).  Into int8 by issue slots: about 230 instructions per pair, 8191
-// tokens in bf16 21.2 us (0.36 of a copy's rate; with a division per value and a
-// warp per pair 26.0).  A few tokens cost a launch and two dependent loads, 1.6 us.
+// tokens of 8 heads x 128 in fp32 29.7 us (201 MB, 1.0 of a copy's rate, over buffers
+// of 1 GB in turn: half of a call's writes leave the L2 during the next), in bf16
+// 21.5 (0.92).  Into int8 by issue slots: about 230 instructions per pair, 8191
+// tokens in bf16 20.7 us (0.36 of a copy's rate; with a division per value and a
+// warp per pair 26.0), 16384 in fp32 36.0 (0.69).  A few tokens cost a launch and
+// two dependent loads, 1.4 us.
 #include <cuda_bf16.h>
 
 #include "kv_cache.h"

@@ -13,9 +13,12 @@
 // another; then each thread takes tokens and finds its request by bisection.
 // A new page is written by the thread of its first token.  The work is a few
 // bytes per token: what bounds it is the latency of one launch, three loads
-// that depend on one another (lengths, free list, stores) and the sums: 6.0 us a
-// call for 8 requests (with the call itself), 7.0 for trees of up to 64 nodes of
-// 256, 11.8 for 1001 prompts of up to 1023 tokens.
+// that depend on one another (lengths, free list, stores) and two block sums, 3.7
+// us in a graph for 8 requests (a call by itself 6.4, its CPU time); the chain of
+// loads along a tree's parents, 7.3 us for trees of up to 64 nodes of 256 requests
+// (a call 7.5); and, of 1001 prompts of up to 1023 tokens, 9.3 us (a call 11.8),
+// instructions: about three quarters of them per token (a bisection of ten steps,
+// three divisions by the page size, two narrow stores), the others the sums.
 #include <algorithm>
 
 #include "kv_cache.h"
