@@ -220,7 +220,7 @@ def _own(s):
         return {"sum": s["sum"], "x": _values(s, s["x"], s.get("s_x"))}
     if case["op"] == "lora":
         if "workspace" not in s:   # scratch that a server keeps from step to step
-            size = qmm.lora_add_workspace_size(case["rows"], case["n"], s["a"].shape[0], s["a"].shape[1])
+            size = qmm.lora_add_workspace_size(case["rows"], case["k"], case["n"], s["a"].shape[0], s["a"].shape[1])
             s["workspace"] = torch.empty(size, dtype=torch.uint8, device="cuda")
         return qmm.lora_add(s["x"], s["ids"], s["a"], s["b"], base=s["base"], out=s["out"], ranks=s["ranks"],
                             scales=s["scales"], workspace=s["workspace"], dev_status=s["status"])
