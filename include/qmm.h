@@ -1,8 +1,8 @@
 /*
  * qmm.h -- C ABI of the quantized projection matmul library for one GB300 (sm_103a).
  *
- * Two halves, two widenings of the second, and what runs between the
- * projections of a decoding step:
+ * Two halves, two widenings of the second, and what runs between and beside
+ * the projections of a decoding step:
  *   (I)   an exact int8 GEMM with zero-point correction, per-column weight
  *         scale, optional int32 bias and float or requantised output, and the
  *         int8 quantisation of its activations;
@@ -12,7 +12,9 @@
  *   (IV)  more weight formats: Q4_K repacked into q4_1 tiles, and 8-bit (Q8)
  *         tiles in two code layouts;
  *   (V)   a paged key/value cache (bf16 or int8): the plan of a step, the
- *         append of its rows, and attention of drafted token trees over it.
+ *         append of its rows, and attention of drafted token trees over it;
+ *   (VI)  norms fused with the residual stream, low-rank adapters added to a
+ *         projection's output, and log probabilities of its logits.
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -780,6 +782,139 @@ qmm_status qmm_tree_attention(const void* q, qmm_dtype q_type, int64_t q_stride_
                               const uint32_t* mask, int64_t ld_mask, float scale, void* out,
                               int64_t out_stride_token, int64_t out_stride_head, void* workspace,
                               size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/* ========================================================================
+ * (VI) Beside the projections of a decoder
+ *
+ * What stands before, beside and behind a projection: the join of a block's
+ * output to the residual stream with the norm that makes the next projection's
+ * operand, low-rank adapters added to a projection's output, and the log
+ * probabilities of the lm_head projection's logits.  No counterpart on the pages,
+ * which stop at the projections.
+ * ======================================================================== */
+
+typedef enum {
+  QMM_NORM_RMS = 1,   /* v * weight / sqrt(mean(v^2) + eps) + bias */
+  QMM_NORM_LAYER = 2  /* (v - mean(v)) * weight / sqrt(var(v) + eps) + bias, var over D values */
+} qmm_norm_kind;
+
+/* A norm over the D values of a row.  Passed by host pointer. */
+typedef struct {
+  qmm_norm_kind kind;
+  float eps;           /* >= 0, finite */
+  const float* weight; /* [D] fp32 or NULL for 1 */
+  const float* bias;   /* [D] fp32 or NULL for 0 */
+} qmm_norm;
+
+/* A block's output joined to the residual stream, and the next block's input:
+ *     u   = branch_norm(branch)                  (branch itself where branch_norm is NULL)
+ *     sum = residual + scale * gate * u          (residual itself where branch is NULL)
+ *     out = norm(sum)                            (sum itself where norm is NULL)
+ *
+ * residual [T][D] fp32 or bf16 (residual_type), row stride ldr elements.
+ * branch   [T][D] fp32 or bf16, or NULL; branch_norm, gate and scale are then not used.
+ * gate     fp32 or bf16 values that multiply as they are, or NULL for 1: one row for
+ *          all tokens (ldg = 0) or [T][D] (ldg >= D).
+ * sum      [T][D] of residual_type, row stride lds, or NULL to store none.  It may be
+ *          the residual itself (same address and stride); other overlaps of an
+ *          output with an input or output are not allowed.
+ * out      [T][D] QMM_BF16 (the X of the projections), QMM_F32, or QMM_S8: codes by
+ *          qmm_quantize_act_int8's rule per row, s = fl(amax / 127) into s_x[T],
+ *          q = clamp(rint_even(fl(v / s)), -127, 127), 0 where s == 0 (ldo % 16 == 0,
+ *          base 16-byte aligned: what qmm_int8_gemm takes); or NULL to store none.
+ * Arithmetic is fp32 on the values as read; sum and out are rounded once, each from
+ * the fp32 sum (out does not see sum's rounding).  Squares are fp32: a row whose
+ * mean square passes 3e38 gives zeros from a norm.  Infinities and NaN stay in their
+ * row; with QMM_S8 such a row's codes and scale are unspecified.
+ * Results are the same from run to run and do not depend on the other rows.  How a
+ * row's sums are split goes by T, D and alignment.
+ * Pointers are aligned to their element, any stride and D go; rows whose
+ * base and strides are whole 16 bytes, with D % 8 == 0, take the faster form.
+ * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
+ * pointers, neither sum nor out, a bad type, kind, eps, scale or stride;
+ * QMM_ERR_UNSUPPORTED for D > 32768 or T >= 2^31.
+ */
+qmm_status qmm_block_norm(const void* residual, qmm_dtype residual_type, int64_t ldr, const void* branch,
+                          qmm_dtype branch_type, int64_t ldb, const qmm_norm* branch_norm, const void* gate,
+                          qmm_dtype gate_type, int64_t ldg, float scale, void* sum, int64_t lds,
+                          const qmm_norm* norm, void* out, qmm_dtype out_type, int64_t ldo, float* s_x, int64_t T,
+                          int64_t D, cudaStream_t stream);
+
+/* A set of low-rank adapters of one projection (K inputs, N outputs): slot a holds
+ * A [max_rank][K] and B [N][max_rank] in bf16, of which the first ranks[a] rows of A
+ * and columns of B count; what lies behind is never used, whatever it holds.  Passed
+ * by host pointer. */
+typedef struct {
+  const void* A;            /* bf16: element (a, j, k) at a*a_stride_slot + j*a_stride_rank + k */
+  int64_t a_stride_slot, a_stride_rank;
+  const void* B;            /* bf16: element (a, n, j) at a*b_stride_slot + n*b_stride_row + j */
+  int64_t b_stride_slot, b_stride_row;
+  const int32_t* ranks;     /* device [n_adapters], 0..max_rank, or NULL: all max_rank */
+  const float* scales;      /* device [n_adapters], or NULL: all 1 */
+  int64_t n_adapters, max_rank, K, N;
+} qmm_lora_set;
+
+/* Workspace of qmm_lora_add on the current device. */
+qmm_status qmm_lora_add_workspace_size(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank,
+                                       size_t* ws_bytes);
+
+/* Adapters of many requests beside a shared projection:
+ *     out[m][n] = base[m][n] + scales[a] * sum_j (sum_k X[m][k] A[a][j][k]) B[a][n][j],  a = ids[m]
+ *
+ * set     the adapters; A and B 16-byte aligned, strides multiples of 8 elements (of a
+ *         dimension of one: anything), B readable for whole rows of b_stride_row
+ *         elements.
+ * X       bf16 [M][K], row stride ldx elements (ldx >= K, ldx % 8 == 0, base 16-byte
+ *         aligned): the projection's own X.
+ * ids     device int32 [M], the adapter of each row in any order; -1: none.
+ * base    fp32 [M][N], row stride ldb (the projection's Y), or NULL for zeros.
+ * out     fp32 [M][N], row stride ldo; it may be base itself (same address and stride;
+ *         rows without an adapter are then left alone).  Other overlaps of out with
+ *         an input are not allowed.
+ * workspace  at least qmm_lora_add_workspace_size(M, K, N, n_adapters, max_rank)
+ *         bytes, 256-byte aligned, rewritten by the call (NULL when that size is 0).
+ * Products of X and A are exact and summed in fp32; the inner sums times scales[a]
+ * enter the second product as two bf16 terms (within 2^-16 of themselves), which is
+ * summed in fp32 and added to base once.  A row's result does not depend on the other
+ * rows' values and is the same from run to run.
+ * Device status: QMM_ERR_INVALID_ARG for an id outside [-1, n_adapters) or a rank
+ * outside [0, max_rank]; such a row is treated as one without an adapter.
+ * M = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned pointers, bad
+ * sizes or strides; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for K % 8 != 0,
+ * max_rank > 256, n_adapters > 8192, K >= 2^28, or N or M >= 2^24.
+ */
+qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, const int32_t* ids, int64_t M,
+                        const float* base, int64_t ldb, float* out, int64_t ldo, void* workspace, size_t ws_bytes,
+                        int32_t* dev_status, cudaStream_t stream);
+
+/* Log probabilities of rows of logits, with p_i = exp(scale * x_i) / sum_j exp(scale * x_j):
+ *
+ * logits   [M][V] fp32 or bf16 (type), row stride ld elements, aligned to the element.
+ * scale    > 0, finite: 1 / temperature.
+ * tokens   device int32 [M][G], row stride ld_tokens: the tokens to score (NULL with G = 0).
+ * logprobs fp32 [M][G] out, contiguous: log p of each; not written for token -1.
+ * entropy  fp32 [M] out: -sum p log p, or NULL.
+ * top_k    0..32: top_ids int32 and top_logprobs fp32 [M][top_k] out, contiguous (NULL
+ *          with top_k = 0): the tokens of the largest logits in falling order, equal ones
+ *          by rising index (-0 equals 0), with their log probabilities.  Tokens at
+ *          -infinity are no alternatives: places beyond the others hold -1 and -infinity.
+ * A logit of -infinity has probability 0.  A row with a NaN or +infinity, or with
+ * nothing above -infinity, has no distribution: its logprobs, entropy and top_logprobs are
+ * NaN and its top_ids -1.
+ * Sums are fp32, taken relative to the row's largest logit with that logit's own 1 kept
+ * apart, so that log probabilities next to 0 keep their relative accuracy.  top_ids are
+ * exact.  Results are the same from run to run; how a row is split between blocks (and its
+ * sums' last bits) goes by M and V.
+ * Device status: QMM_ERR_INVALID_ARG for a token outside [-1, V), whose logprob is not
+ * written.
+ * M = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned pointers, bad
+ * sizes, strides, type or scale, nothing asked for (no entropy, G = 0 and top_k = 0);
+ * QMM_ERR_UNSUPPORTED for top_k > 32, V >= 2^31 - 2^16, G > 1024 or M >= 2^26.
+ */
+qmm_status qmm_token_logprobs(const void* logits, qmm_dtype type, int64_t M, int64_t V, int64_t ld, float scale,
+                              const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
+                              int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                              cudaStream_t stream);
 
 /* ========================================================================
  * Diagnostics

@@ -49,7 +49,7 @@ const char* qmm_status_string(qmm_status s) {
   return "QMM_ERR_UNKNOWN";
 }
 
-int qmm_version(void) { return 300; }
+int qmm_version(void) { return 400; }
 
 // ---------------------------------------------------------------------------
 // int8

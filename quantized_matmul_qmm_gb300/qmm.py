@@ -50,6 +50,16 @@ class QmmKvCache(ctypes.Structure):
                 ("stride_token", _i64), ("stride_head", _i64)]
 
 
+class QmmNorm(ctypes.Structure):
+    _fields_ = [("kind", _c.c_int), ("eps", _c.c_float), ("weight", _vp), ("bias", _vp)]
+
+
+class QmmLoraSet(ctypes.Structure):
+    _fields_ = [("A", _vp), ("a_stride_slot", _i64), ("a_stride_rank", _i64), ("B", _vp), ("b_stride_slot", _i64),
+                ("b_stride_row", _i64), ("ranks", _vp), ("scales", _vp), ("n_adapters", _i64), ("max_rank", _i64),
+                ("K", _i64), ("N", _i64)]
+
+
 SIGNATURES = {
     "qmm_status_string": (_c.c_char_p, [_c.c_int]),
     "qmm_version": (_c.c_int, []),
@@ -99,6 +109,14 @@ SIGNATURES = {
     "qmm_tree_attention": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.POINTER(QmmKvCache), _vp, _i64, _i64, _vp,
                                       _vp, _i64, _i64, _i64, _vp, _i64, _c.c_float, _vp, _i64, _i64, _vp, _sz, _vp,
                                       _vp]),
+    "qmm_block_norm": (_c.c_int, [_vp, _c.c_int, _i64, _vp, _c.c_int, _i64, _c.POINTER(QmmNorm), _vp, _c.c_int, _i64,
+                                  _c.c_float, _vp, _i64, _c.POINTER(QmmNorm), _vp, _c.c_int, _i64, _vp, _i64, _i64,
+                                  _vp]),
+    "qmm_lora_add_workspace_size": (_c.c_int, [_i64, _i64, _i64, _i64, _i64, _szp]),
+    "qmm_lora_add": (_c.c_int, [_c.POINTER(QmmLoraSet), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp,
+                                _vp]),
+    "qmm_token_logprobs": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.c_float, _vp, _i64, _i64, _vp, _vp, _i64,
+                                      _vp, _vp, _vp, _vp]),
     "qmm_probe_hbm_read": (_c.c_int, [_vp, _sz, _c.c_int, _vp, _vp, _vp]),
     "qmm_selftest_wait_timeout": (_c.c_int, [_c.c_uint64, _vp, _vp, _vp]),
 }
@@ -656,6 +674,187 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, workspace.data_ptr(),
         workspace.nbytes, _status_addr("tree_attention", dev_status), _stream_of(q)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Beside the projections
+# ---------------------------------------------------------------------------
+
+_NORM_KINDS = {"rms": 1, "layer": 2}
+_OUT_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16, torch.int8: QMM_S8}
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
+def _one_device(fn, first, *tensors):
+    """All tensors on one GPU, and that the current one: an address of another
+    device or of the host would reach the kernel as it is."""
+    dev = first.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: tensors on different devices")
+    if dev != _current_device():
+        raise ValueError(f"{fn}: tensors have to be on the current CUDA device")
+    return dev
+
+
+def _current_device():
+    return torch.cuda.current_device()
+
+
+def _rows(fn, t, shape, types):
+    """Row stride of a [rows][width] tensor with contiguous rows."""
+    if t.shape != shape or t.dtype not in types or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{fn}: expected {tuple(shape)} with contiguous rows of {[str(x) for x in types]}, "
+                         f"got {tuple(t.shape)} {t.dtype} with strides {t.stride()}")
+    return t.stride(0)
+
+
+def _vector(fn, t, size, dtype):
+    if t is None:
+        return None
+    if t.numel() != size or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{fn}: expected {size} contiguous values of {dtype}")
+    return t.data_ptr()
+
+
+def block_norm(residual: torch.Tensor, branch=None, *, norm="rms", weight=None, bias=None, eps=1e-6, branch_norm=None,
+               branch_weight=None, branch_bias=None, branch_eps=None, gate=None, scale=1.0, residual_out=None, out=None,
+               out_type="bf16", s_x=None):
+    """Join a block's output to the residual stream and make the next block's
+    input, through qmm_block_norm:
+
+        u = branch_norm(branch); sum = residual + scale * gate * u; out = norm(sum)
+
+    residual and branch fp32 or bf16 [T][D]; norm and branch_norm "rms",
+    "layer" or None with fp32 weights and biases [D] (or None); gate fp32 or bf16
+    [D] or [T][D].  residual_out takes the sum (the residual itself, in place,
+    when a branch is given and residual_out is not); out is "bf16", "f32" or
+    "s8", the last with row scales s_x fp32 [T], made when not given (out=False:
+    the sum alone).  Returns (sum, out), or (sum, out, s_x) for "s8"."""
+    fn = "block_norm"
+    shape = residual.shape
+    T, D = shape
+    dev = _one_device(fn, residual, branch, weight, bias, branch_weight, branch_bias, gate, residual_out,
+                      None if out is False else out, s_x)
+    ldr = _rows(fn, residual, shape, (_F32, _BF16))
+    ldb = ldg = lds = ldo = 0
+    p_branch = p_gate = p_sum = p_out = n_branch = n_out = None
+    b_type = g_type = QMM_F32
+    o_type = QMM_BF16
+    if branch is not None:
+        ldb, p_branch, b_type = _rows(fn, branch, shape, (_F32, _BF16)), branch.data_ptr(), _ROW_TYPES[branch.dtype]
+        if branch_norm is not None:
+            n_branch = QmmNorm(_NORM_KINDS[branch_norm], eps if branch_eps is None else branch_eps,
+                               _vector(fn, branch_weight, D, _F32), _vector(fn, branch_bias, D, _F32))
+        if gate is not None:
+            if gate.dim() == 1:
+                gate = gate.unsqueeze(0)
+                _rows(fn, gate, (1, D), (_F32, _BF16))
+            else:
+                ldg = _rows(fn, gate, shape, (_F32, _BF16))
+            p_gate, g_type = gate.data_ptr(), _ROW_TYPES[gate.dtype]
+        if residual_out is None:
+            residual_out = residual
+    if residual_out is not None:
+        lds, p_sum = _rows(fn, residual_out, shape, (residual.dtype,)), residual_out.data_ptr()
+    if out is not False:
+        if out is None:
+            if out_type == "s8":       # rows of whole 16 bytes, as the int8 GEMM takes them
+                out = torch.empty((T, (D + 15) // 16 * 16), dtype=torch.int8, device=residual.device)[:, :D]
+            else:
+                out = torch.empty(shape, dtype=_BF16 if out_type == "bf16" else _F32, device=residual.device)
+        ldo, p_out, o_type = _rows(fn, out, shape, tuple(_OUT_TYPES)), out.data_ptr(), _OUT_TYPES[out.dtype]
+        if o_type == QMM_S8 and s_x is None:
+            s_x = torch.empty(T, dtype=_F32, device=residual.device)
+        if norm is not None:
+            n_out = QmmNorm(_NORM_KINDS[norm], eps, _vector(fn, weight, D, _F32), _vector(fn, bias, D, _F32))
+    status = lib.qmm_block_norm(
+        residual.data_ptr(), _ROW_TYPES[residual.dtype], ldr, p_branch, b_type, ldb, n_branch, p_gate, g_type, ldg,
+        scale, p_sum, lds, n_out, p_out, o_type, ldo, _vector(fn, s_x, T, _F32), T, D, _raw_stream(dev))
+    if status != QMM_OK:
+        _check("qmm_block_norm", status)
+    total = residual if residual_out is None else residual_out
+    return (total, out, s_x) if o_type == QMM_S8 else (total, None if out is False else out)
+
+
+def lora_add_workspace_size(M: int, K: int, N: int, n_adapters: int, max_rank: int) -> int:
+    return _size("qmm_lora_add_workspace_size", M, K, N, n_adapters, max_rank)
+
+
+def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tensor, base=None, out=None, ranks=None,
+             scales=None, workspace=None, dev_status=None):
+    """Adapters of many requests beside a shared projection, through qmm_lora_add:
+    out[m] = base[m] + scales[a] * B[a] (A[a] X[m]) with a = ids[m] (-1: none).
+    X bf16 [M][K], ids int32 [M], A bf16 [adapters][max_rank][K], B bf16
+    [adapters][N][max_rank], ranks int32 and scales fp32 [adapters] (or None), base
+    fp32 [M][N] (or None for zeros).  out is made when not given; out=base adds in
+    place.  Returns out."""
+    fn = "lora_add"
+    dev = _one_device(fn, X, ids, A, B, base, out, ranks, scales, workspace, dev_status)
+    M, K = shape = X.shape
+    slots, rank, k = A.shape
+    N = B.shape[1]
+    if k != K or B.shape != (slots, N, rank) or A.dtype is not _BF16 or B.dtype is not _BF16 \
+            or (A.stride(2) != 1 and K > 1) or (B.stride(2) != 1 and rank > 1):
+        raise ValueError("lora_add: A has to be bf16 [adapters][rank][K], B bf16 [adapters][N][rank], with "
+                         "contiguous innermost values, for X [M][K]")
+    ldx = _rows(fn, X, shape, (_BF16,))
+    ldb = 0 if base is None else _rows(fn, base, (M, N), (_F32,))
+    if out is None:
+        out = torch.empty((M, N), dtype=_F32, device=X.device)
+    ldo = _rows(fn, out, (M, N), (_F32,))
+    p_ids = _vector(fn, ids, M, _I32)
+    weights = QmmLoraSet(A.data_ptr(), A.stride(0), A.stride(1), B.data_ptr(), B.stride(0), B.stride(1),
+                         _vector(fn, ranks, slots, _I32), _vector(fn, scales, slots, _F32), slots, rank, K, N)
+    if workspace is None:
+        workspace = torch.empty(lora_add_workspace_size(M, K, N, slots, rank), dtype=torch.uint8, device=X.device)
+    status = lib.qmm_lora_add(weights, X.data_ptr(), ldx, p_ids, M, _addr(base), ldb, out.data_ptr(), ldo,
+                              workspace.data_ptr(), workspace.nbytes, _status_addr(fn, dev_status), _raw_stream(dev))
+    if status != QMM_OK:
+        _check("qmm_lora_add", status)
+    return out
+
+
+def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: float = 1.0, logprobs=None, entropy=None,
+                   top_ids=None, top_logprobs=None, dev_status=None):
+    """Log probabilities of tokens (int32 [M][G] or [M], -1: none) under
+    softmax(scale * logits), logits fp32 or bf16 [M][V], with the entropy fp32 [M]
+    (entropy=False: none) and the top_k <= 32 alternatives, through
+    qmm_token_logprobs.  Returns (logprobs, entropy, top_ids, top_logprobs), None
+    for what was not asked for."""
+    fn = "token_logprobs"
+    dev = _one_device(fn, logits, tokens, logprobs, None if entropy is False else entropy, top_ids, top_logprobs,
+                      dev_status)
+    M, V = shape = logits.shape
+    ld, device = _rows(fn, logits, shape, (_F32, _BF16)), logits.device
+    G = ldt = 0
+    p_tokens = p_logprobs = p_ids = p_top = p_entropy = None
+    if tokens is not None:
+        flat = tokens.dim() == 1
+        if flat:
+            tokens = tokens.unsqueeze(1)
+        G = tokens.shape[1]
+        ldt, p_tokens = _rows(fn, tokens, (M, G), (_I32,)), tokens.data_ptr()
+        if logprobs is None:
+            logprobs = torch.empty(M if flat else (M, G), dtype=_F32, device=device)
+        p_logprobs = _vector(fn, logprobs, M * G, _F32)
+    if entropy is not False:
+        if entropy is None:
+            entropy = torch.empty(M, dtype=_F32, device=device)
+        p_entropy = _vector(fn, entropy, M, _F32)
+    if top_k > 0:
+        if top_ids is None:
+            top_ids = torch.empty((M, top_k), dtype=_I32, device=device)
+        if top_logprobs is None:
+            top_logprobs = torch.empty((M, top_k), dtype=_F32, device=device)
+        p_ids, p_top = _vector(fn, top_ids, M * top_k, _I32), _vector(fn, top_logprobs, M * top_k, _F32)
+    status = lib.qmm_token_logprobs(
+        logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy, top_k,
+        p_ids, p_top, _status_addr(fn, dev_status), _raw_stream(dev))
+    if status != QMM_OK:
+        _check("qmm_token_logprobs", status)
+    return (logprobs, None if entropy is False else entropy, top_ids if top_k > 0 else None,
+            top_logprobs if top_k > 0 else None)
 
 
 # ---------------------------------------------------------------------------

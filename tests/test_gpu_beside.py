@@ -1,0 +1,455 @@
+"""GPU parity of what runs beside the projections (qmm_block_norm, qmm_lora_add,
+qmm_token_logprobs) against the fp64 oracle, within its bounds on fp32 arithmetic
+and half a step of the output type."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.beside_oracle as O
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def close(got, want, bound, half, what):
+    got = got.double().cpu().numpy()
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan), what
+    with np.errstate(invalid="ignore"):
+        far = np.abs(got - want) - (bound * (1 + half) + half * np.abs(want))
+    far = np.where(nan | (got == want), -1.0, far)
+    assert far.max() <= 0, f"{what}: {(far > 0).sum()} of {far.size} too far, worst by {far.max():.3g}"
+
+
+def wide(t, cols):
+    """A view of t's values inside rows of `cols` elements."""
+    out = torch.full((t.shape[0], cols), 7.0, dtype=t.dtype, device=t.device)[:, :t.shape[1]]
+    return out.copy_(t)
+
+
+# ---------------------------------------------------------------------------
+# norms
+# ---------------------------------------------------------------------------
+
+NORM_CASES = [
+    # T, D, residual, branch, post, gate, kind, out
+    (1, 1, "f32", "f32", "rms", None, "rms", "bf16"),
+    (3, 8, "bf16", "f32", None, "channel", "layer", "f32"),
+    (5, 24, "f32", "bf16", "layer", "token", "rms", "bf16"),
+    (2, 100, "f32", "f32", None, None, None, "bf16"),
+    (7, 255, "bf16", "bf16", "rms", "token", "layer", "bf16"),
+    (4, 256, "f32", None, None, None, "rms", "bf16"),
+    (9, 1000, "f32", "f32", "rms", "channel", "rms", "s8"),
+    (6, 1001, "bf16", "bf16", "layer", "token", "layer", "s8"),
+    (400, 1024, "f32", "f32", "rms", None, "rms", "bf16"),
+    (1, 4096, "f32", "f32", "rms", "token", "rms", "s8"),
+    (330, 4608, "f32", "f32", "rms", "channel", "rms", "s8"),
+    (320, 2052, "bf16", "f32", None, "token", "layer", "f32"),
+    (3, 8200, "f32", "bf16", "layer", None, "rms", "bf16"),
+    (2, 8193, "f32", "f32", "rms", "token", "layer", "bf16"),
+    (310, 16392, "bf16", "bf16", "rms", "channel", "rms", "bf16"),
+    (2, 32768, "f32", "f32", "layer", "token", "layer", "f32"),
+    (2, 32767, "bf16", "f32", "rms", None, "rms", "s8"),
+]
+
+
+def norm_case(dev, T, D, residual, branch, post, gate, kind, out, stride=0, seed=0):
+    g = torch.Generator().manual_seed(seed + T + 31 * D)
+    r = lambda *s: torch.randn(s, generator=g)
+    loud = torch.where(torch.rand(D, generator=g) < 0.05, 30.0, 1.0)
+    lay = (lambda t: wide(t, D + stride)) if stride else (lambda t: t)
+    a = dict(residual=lay((r(T, D) * loud + 0.5).to(TYPES[residual]).to(dev)), norm=kind, scale=0.7, eps=1e-5)
+    if kind is not None:
+        a.update(weight=(1 + 0.3 * r(D)).to(dev))
+        if kind == "layer" or D % 2:
+            a.update(bias=(0.2 * r(D)).to(dev))
+    if branch is not None:
+        a.update(branch=lay((r(T, D) * torch.exp(r(T, 1))).to(TYPES[branch]).to(dev)))
+    if post is not None:
+        a.update(branch_norm=post, branch_weight=(1 + 0.3 * r(D)).to(dev), branch_eps=1e-6)
+        if post == "layer":
+            a.update(branch_bias=(0.2 * r(D)).to(dev))
+    if gate == "channel":
+        a.update(gate=r(D).to(dev))
+    elif gate == "token":
+        a.update(gate=lay(torch.sigmoid(r(T, D)).to(torch.bfloat16).to(dev)))
+    return a, out
+
+
+def norm_exact(a):
+    return O.block(f64(a["residual"]), f64(a.get("branch")), a.get("branch_norm"), f64(a.get("branch_weight")),
+                   f64(a.get("branch_bias")), a.get("branch_eps", 0.0), f64(a.get("gate")), np.float32(a["scale"]),
+                   a["norm"], f64(a.get("weight")), f64(a.get("bias")), np.float32(a["eps"]))
+
+
+def check_norm(a, out_type, got, half_sum):
+    total, d_total, x, d_x = norm_exact(a)
+    if a.get("branch") is not None:
+        close(got[0], total, d_total, half_sum, "sum")
+    if out_type != "s8":
+        close(got[1], x, d_x, O.HALF[out_type], "out")
+        return
+    codes, s = got[1].double().cpu().numpy(), got[2].double().cpu().numpy()[:, None]
+    amax = np.abs(x).max(1, keepdims=True)
+    assert (np.abs(s * 127 - amax) <= d_x.max(1, keepdims=True) + 2 * O.U32 * amax).all()
+    # a code is within half a step of the value, give or take the value's own error and two roundings
+    assert (np.abs(codes * s - x) <= s * 0.5 * (1 + 256 * O.U32) + d_x + 4 * O.U32 * np.abs(x)).all()
+    assert np.abs(codes).max() <= 127
+
+
+@pytest.mark.parametrize("case", NORM_CASES, ids=lambda c: "-".join(map(str, c)))
+def test_norm(qmm, cuda, case):
+    a, out_type = norm_case(cuda, *case)
+    kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
+    if a.get("branch") is not None:
+        kw["residual_out"] = torch.full_like(a["residual"], 9.0)
+    before = a["residual"].clone()
+    got = qmm.block_norm(a["residual"], a.get("branch"), out_type=out_type, **kw)
+    again = qmm.block_norm(a["residual"], a.get("branch"), out_type=out_type, **kw)
+    assert torch.equal(a["residual"], before)
+    for x, y in zip(got[1:], again[1:]):
+        assert torch.equal(x, y)
+    check_norm(a, out_type, got, O.HALF[case[2]])
+
+
+@pytest.mark.parametrize("stride", [8, 16, 1, 5])
+@pytest.mark.parametrize("case", [NORM_CASES[i] for i in (4, 6, 7, 11, 12)], ids=lambda c: "-".join(map(str, c)))
+def test_norm_strided_in_place(qmm, cuda, case, stride):
+    """Rows inside wider ones, the sum over the residual itself: the same values
+    as apart from it, and nothing written between the rows."""
+    a, out_type = norm_case(cuda, *case, stride=stride)
+    T, D = a["residual"].shape
+    kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
+    store = torch.full((T, (D + 47) // 16 * 16), 5, dtype={"s8": torch.int8}.get(out_type, TYPES.get(out_type)),
+                       device=cuda)
+    apart = qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]),
+                           out=store[:, :D], **kw)
+    check_norm(a, out_type, apart, O.HALF[case[2]])
+    assert (store[:, D:] == 5).all()
+    first = apart[1].clone()
+    total = a["residual"]
+    qmm.block_norm(total, a["branch"], out=store[:, :D], **kw)
+    assert torch.equal(total, apart[0]) and torch.equal(store[:, :D], first)
+    whole = torch.as_strided(total, (T - 1, stride), (D + stride, 1), total.storage_offset() + D)
+    assert (whole == 7.0).all()
+
+
+def test_norm_alone_and_sum_alone(qmm, cuda):
+    a, _ = norm_case(cuda, 5, 72, "f32", "f32", "rms", None, "rms", "bf16")
+    total, out = qmm.block_norm(a["residual"], norm="rms", weight=a["weight"], eps=1e-5)
+    assert total is a["residual"]
+    close(out, *O.block(f64(a["residual"]), None, None, None, None, 0, None, 1, "rms", f64(a["weight"]), None,
+                        np.float32(1e-5))[2:], O.HALF["bf16"], "out")
+    want = f64(a["residual"]) + f64(a["branch"])
+    total, out = qmm.block_norm(a["residual"], a["branch"], out=False)
+    assert out is None and total is a["residual"]
+    close(total, want, O.U32 * np.abs(want), O.U32, "sum")
+
+
+def test_norm_nonfinite_rows_stay_apart(qmm, cuda):
+    a, _ = norm_case(cuda, 6, 512, "f32", "f32", "rms", None, "rms", "bf16")
+    clean = qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]),
+                           **{k: v for k, v in a.items() if k not in ("residual", "branch")})
+    a["branch"][2, 100], a["residual"][4, 7] = float("nan"), float("inf")
+    got = qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]),
+                         **{k: v for k, v in a.items() if k not in ("residual", "branch")})
+    rows = [0, 1, 3, 5]
+    assert torch.equal(got[0][rows], clean[0][rows]) and torch.equal(got[1][rows], clean[1][rows])
+    assert torch.isnan(got[1][2]).all() and torch.isnan(got[1][4, 7])
+
+
+def test_norm_zero_rows(qmm, cuda):
+    z = torch.zeros((4, 640), device=cuda)
+    total, out, s = qmm.block_norm(z, z.clone(), residual_out=torch.empty_like(z), out_type="s8", eps=1e-6)
+    assert not total.any() and not out.any() and not s.any()
+    total, out = qmm.block_norm(z[:0], z[:0])
+    assert total.shape == out.shape == (0, 640)
+
+
+def test_norm_rows_past_32_bits(qmm, cuda):
+    """Element offsets beyond 2^31: rows far apart in memory."""
+    D, T, ld = 64, 5, 1 << 29
+    store = torch.zeros((T - 1) * ld + D, dtype=torch.bfloat16, device=cuda)
+    res = torch.as_strided(store, (T, D), (ld, 1))
+    want = torch.randn((T, D), device=cuda).to(torch.bfloat16)
+    res.copy_(want)
+    _, out = qmm.block_norm(res, norm=None, out_type="f32")
+    assert torch.equal(out, want.float())
+
+
+# ---------------------------------------------------------------------------
+# adapters
+# ---------------------------------------------------------------------------
+
+LORA_CASES = [
+    # M, K, N, adapters, max_rank, prompt
+    (1, 8, 1, 1, 1, False), (1, 1024, 2048, 3, 16, False), (3, 40, 33, 2, 5, False), (16, 256, 100, 1, 8, False),
+    (17, 512, 260, 4, 17, False), (64, 1000, 516, 20, 64, False), (65, 264, 130, 1, 33, True),
+    (200, 2048, 1028, 5, 100, True), (256, 1024, 640, 300, 24, False), (300, 520, 257, 3, 256, True),
+    (700, 320, 1200, 2, 200, True), (1025, 136, 96, 7, 12, False), (2500, 64, 64, 3, 8, True),
+]
+
+
+def lora_case(dev, M, K, N, adapters, rank, prompt, seed=0, none=0.1):
+    g = torch.Generator().manual_seed(seed + M + K + N)
+    r = lambda *s: torch.randn(s, generator=g)
+    ids = torch.randint(0, adapters, (M,), generator=g)
+    ids = torch.sort(ids).values if prompt else ids
+    ids[torch.rand(M, generator=g) < none] = -1
+    ranks = torch.randint(0, rank + 1, (adapters,), generator=g)
+    ranks[0] = rank
+    A = r(adapters, rank, K) / K ** 0.5
+    B = r(adapters, N, -(-rank // 8) * 8)
+    for a in range(adapters):           # what lies behind a rank is never used
+        A[a, int(ranks[a]):] = float("nan")
+        B[a, :, int(ranks[a]):] = float("nan")
+    return dict(X=r(M, K).to(torch.bfloat16).to(dev), ids=ids.to(torch.int32).to(dev), A=A.to(torch.bfloat16).to(dev),
+                B=B.to(torch.bfloat16).to(dev)[:, :, :rank], base=r(M, N).to(dev),
+                ranks=ranks.to(torch.int32).to(dev), scales=(0.1 + r(adapters).abs()).to(dev))
+
+
+def lora_exact(a, **over):
+    a = {**a, **over}
+    clean = lambda t: torch.nan_to_num(t.float(), nan=0.0)
+    return O.lora(f64(a["X"]), a["ids"].cpu().numpy(), f64(clean(a["A"])), f64(clean(a["B"])), f64(a["base"]),
+                  None if a["ranks"] is None else a["ranks"].cpu().numpy(),
+                  None if a["scales"] is None else f64(a["scales"]))
+
+
+@pytest.mark.parametrize("case", LORA_CASES, ids=lambda c: "-".join(map(str, c)))
+def test_lora(qmm, cuda, case):
+    a = lora_case(cuda, *case)
+    want, bound = lora_exact(a)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    out = qmm.lora_add(**a, dev_status=status)
+    close(out, want, bound, 0.0, "out")
+    assert torch.equal(qmm.lora_add(**a), out)
+    inplace = a["base"].clone()
+    assert torch.equal(qmm.lora_add(**{**a, "base": inplace}, out=inplace), out)
+    want0, bound0 = lora_exact(a, base=None)
+    close(qmm.lora_add(**{**a, "base": None}), np.zeros(out.shape) if want0 is None else want0, bound0, 0.0, "no base")
+    assert int(status) == 0
+
+
+def test_lora_rows_do_not_depend_on_each_other(qmm, cuda):
+    """A row's result is the same in another order of rows, and a row of NaN
+    beside it changes nothing."""
+    a = lora_case(cuda, 150, 512, 300, 4, 40, False)
+    out = qmm.lora_add(**a)
+    order = torch.randperm(150, device=cuda)
+    moved = qmm.lora_add(**{**a, "X": a["X"][order], "ids": a["ids"][order], "base": a["base"][order]})
+    assert torch.equal(moved, out[order])
+    X = a["X"].clone()
+    X[77] = float("nan")
+    got = qmm.lora_add(**{**a, "X": X})
+    rows = torch.arange(150, device=cuda) != 77
+    assert torch.equal(got[rows], out[rows])
+
+
+@pytest.mark.parametrize("M", [5, 70, 600])
+def test_lora_without_ranks_and_scales_strided(qmm, cuda, M):
+    a = lora_case(cuda, M, 128, 75, 3, 24, False)
+    a["A"], a["B"] = torch.nan_to_num(a["A"]), torch.nan_to_num(a["B"])
+    a["ranks"] = a["scales"] = None
+    a["X"] = wide(a["X"], 136)
+    a["base"] = wide(a["base"], 81)
+    store = torch.full((M, 90), 3.0, device=cuda)
+    want, bound = lora_exact(a)
+    qmm.lora_add(**a, out=store[:, :75])
+    close(store[:, :75], want, bound, 0.0, "out")
+    assert (store[:, 75:] == 3.0).all()
+
+
+@pytest.mark.parametrize("M", [9, 600])
+def test_lora_bad_ids_and_ranks(qmm, cuda, M):
+    a = lora_case(cuda, M, 64, 40, 4, 8, False, none=0.0)
+    a["ids"][1], a["ids"][4] = 4, -2
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    out = qmm.lora_add(**a, dev_status=status)
+    assert int(status) == qmm.QMM_ERR_INVALID_ARG
+    close(out, *lora_exact(a), 0.0, "out")
+    a["ids"][1] = a["ids"][4] = -1
+    for bad in (9, -1):
+        a["ranks"][2] = bad
+        status.zero_()
+        out = qmm.lora_add(**a, dev_status=status)
+        assert int(status) == (qmm.QMM_ERR_INVALID_ARG if (a["ids"] == 2).any() else 0)
+        close(out, *lora_exact(a), 0.0, "out")
+
+
+def test_lora_nobody_has_an_adapter(qmm, cuda):
+    a = lora_case(cuda, 90, 64, 48, 2, 8, False, none=1.1)
+    assert torch.equal(qmm.lora_add(**a), a["base"])
+    assert not qmm.lora_add(**{**a, "base": None}).any()
+    assert qmm.lora_add(**{**a, "X": a["X"][:0], "ids": a["ids"][:0], "base": a["base"][:0]}).shape == (0, 48)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities
+# ---------------------------------------------------------------------------
+
+def check_logprobs(qmm, x, tokens, k, scale, status=None):
+    got = qmm.token_logprobs(x, tokens, top_k=k, scale=scale, dev_status=status)
+    again = qmm.token_logprobs(x, tokens, top_k=k, scale=scale)
+    want, tol = O.logprobs(f64(x), None if tokens is None else tokens.cpu().numpy(), k, float(np.float32(scale)))
+    for a, b in zip(got, again):
+        assert a is None and b is None or torch.equal(torch.nan_to_num(a, nan=1e9), torch.nan_to_num(b, nan=1e9))
+    if tokens is not None:
+        close(got[0], want["logprobs"], tol["logprobs"], 0.0, "logprobs")
+    close(got[1], want["entropy"], tol["entropy"], 0.0, "entropy")
+    if k:
+        assert np.array_equal(got[2].cpu().numpy(), want["ids"])
+        close(got[3], want["top"], tol["top"], 0.0, "top_logprobs")
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,V,k,scale", [(1, 1, 1, 1.0), (2, 3, 5, 1.0), (3, 7, 0, 0.3), (5, 100, 32, 2.0),
+                                         (1, 4096, 20, 1.0), (4, 4099, 7, 1.0), (2, 16384, 1, 1.0),
+                                         (3, 16389, 20, 0.7), (1, 151936, 20, 1.0), (2, 151936, 32, 1.25),
+                                         (310, 5001, 3, 1.0), (700, 300, 4, 1.0), (9, 70001, 11, 1.0)])
+def test_logprobs(qmm, cuda, M, V, k, scale, dtype):
+    g = torch.Generator().manual_seed(M + V)
+    x = 3.0 * torch.randn((M, V), generator=g)
+    x[torch.arange(M), torch.randint(0, V, (M,), generator=g)] += 8.0
+    tokens = torch.randint(0, V, (M, 3), generator=g).to(torch.int32)
+    tokens[:, 1] = x.argmax(1).to(torch.int32)
+    check_logprobs(qmm, x.to(TYPES[dtype]).to(cuda), tokens.to(cuda), k, scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [1, 2, 3, 8])
+def test_logprobs_rows_inside_wider_ones(qmm, cuda, pad, dtype):
+    """What lies between the rows is not read; rows start at every alignment."""
+    x = torch.full((9, 1237 + pad), float("nan"), dtype=TYPES[dtype], device=cuda)
+    x[:, :1237] = torch.randn((9, 1237), device=cuda) * 2
+    tokens = torch.randint(0, 1237, (9, 5), device=cuda, dtype=torch.int32)
+    check_logprobs(qmm, x[:, :1237], tokens[:, 1:4], 6, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [50, 20000, 151936])
+def test_logprobs_ties(qmm, cuda, V, dtype):
+    """Equal logits fall by rising index; -0 equals 0; a whole row of one value."""
+    x = torch.zeros((5, V))
+    x[1] = torch.randint(0, 3, (V,)).float()
+    x[2, ::2] = -0.0
+    x[3] = torch.finfo(TYPES[dtype]).min
+    x[4] = torch.finfo(TYPES[dtype]).min
+    x[4, V // 2] = 1.0
+    tokens = torch.tensor([[0, V - 1]] * 5, dtype=torch.int32)
+    check_logprobs(qmm, x.to(TYPES[dtype]).to(cuda), tokens.to(cuda), 32, 1.0)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_logprobs_sorted_rows(qmm, cuda, order):
+    """Rows in order of value: every tile replaces the alternatives, or none does."""
+    x = torch.linspace(-20, 20, 120001)
+    x = torch.stack([x if order == "rising" else x.flip(0)] * 170)     # one block per row
+    check_logprobs(qmm, x[:3].to(cuda), None, 32, 1.0)
+    got = qmm.token_logprobs(x.to(cuda), top_k=32)
+    want = torch.arange(120000, 119968, -1) if order == "rising" else torch.arange(32)
+    assert torch.equal(got[2].cpu(), want.to(torch.int32).expand(170, 32))
+
+
+def test_logprobs_masked(qmm, cuda):
+    inf = float("inf")
+    x = torch.randn((8, 33000)) * 2
+    x[0] = -inf
+    x[1, 5:] = -inf
+    x[2, :] = -inf
+    x[2, 32999] = 1.0
+    x[3, 7] = float("nan")
+    x[4, 20000] = inf
+    x[5, 100:32000] = -inf
+    x[6, :16500] = -inf
+    x[7, :] = -inf
+    x[7, 4] = float("nan")
+    tokens = torch.tensor([[0, 7, 32999]] * 8, dtype=torch.int32)
+    got = check_logprobs(qmm, x.to(cuda), tokens.to(cuda), 9, 1.0)
+    assert (got[2][[0, 3, 4, 7]] == -1).all() and torch.isnan(got[1][[0, 3, 4, 7]]).all()
+    assert float(got[0][2, 2]) == 0.0 and float(got[1][2]) == 0.0 and float(got[0][2, 0]) == -inf
+
+
+def test_logprobs_next_to_zero(qmm, cuda):
+    """One token far above the rest: its log probability keeps its relative accuracy."""
+    x = torch.randn((6, 40000))
+    x[torch.arange(6), torch.arange(6) * 7000] += torch.tensor([20.0, 30.0, 40.0, 60.0, 80.0, 120.0])
+    tokens = (torch.arange(6) * 7000).to(torch.int32)[:, None]
+    got = check_logprobs(qmm, x.to(cuda), tokens.to(cuda), 2, 1.0)
+    want, _ = O.logprobs(f64(x), tokens.numpy(), 0, 1.0)
+    rel = np.abs(got[0].double().cpu().numpy() / want["logprobs"] - 1)[:5]
+    assert rel.max() <= (4 + 40000 / 512 + 64 + 3 * 1.4427 * 90) * O.U32
+
+
+def test_logprobs_skipped_and_bad_tokens(qmm, cuda):
+    x = torch.randn((4, 500), device=cuda)
+    tokens = torch.tensor([[3, -1], [-1, -1], [499, 0], [1, 2]], dtype=torch.int32, device=cuda)
+    out = torch.full((4, 2), 55.0, device=cuda)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    qmm.token_logprobs(x, tokens, logprobs=out, dev_status=status)
+    assert int(status) == 0 and (out[tokens == -1] == 55.0).all() and (out[tokens != -1] < 0).all()
+    for bad in (500, -2, 2 ** 31 - 1):
+        tokens[3, 1] = bad
+        out.fill_(55.0)
+        status.zero_()
+        qmm.token_logprobs(x, tokens, logprobs=out, dev_status=status)
+        assert int(status) == qmm.QMM_ERR_INVALID_ARG and float(out[3, 1]) == 55.0 and float(out[3, 0]) < 0
+
+
+def test_logprobs_many_rows_past_32_bits(qmm, cuda):
+    ld = 1 << 30
+    store = torch.empty(2 * ld + 300, dtype=torch.bfloat16, device=cuda)
+    x = torch.as_strided(store, (3, 300), (ld, 1))
+    x.copy_(torch.randn((3, 300), device=cuda))
+    check_logprobs(qmm, x, torch.tensor([[1], [2], [299]], dtype=torch.int32, device=cuda), 4, 1.0)
+
+
+# ---------------------------------------------------------------------------
+# captured, on another stream, and together
+# ---------------------------------------------------------------------------
+
+def test_captured_and_replayed(qmm, cuda):
+    """All three in one graph, replayed on new contents of the same buffers."""
+    a, _ = norm_case(cuda, 30, 256, "f32", "f32", "rms", None, "rms", "bf16")
+    kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
+    b = lora_case(cuda, 30, 256, 520, 4, 16, False)
+    total, x = torch.empty_like(a["residual"]), torch.empty((30, 256), dtype=torch.bfloat16, device=cuda)
+    ws = torch.empty(qmm.lora_add_workspace_size(30, 256, 520, 4, 16), dtype=torch.uint8, device=cuda)
+    out = torch.empty((30, 520), device=cuda)
+    tokens = torch.randint(0, 520, (30, 2), device=cuda, dtype=torch.int32)
+    lp, ent = torch.empty((30, 2), device=cuda), torch.empty(30, device=cuda)
+    ids, top = torch.empty((30, 4), dtype=torch.int32, device=cuda), torch.empty((30, 4), device=cuda)
+
+    def step():
+        qmm.block_norm(a["residual"], a["branch"], residual_out=total, out=x, **kw)
+        qmm.lora_add(x, b["ids"], b["A"], b["B"], base=b["base"], out=out, ranks=b["ranks"], scales=b["scales"],
+                     workspace=ws)
+        qmm.token_logprobs(out, tokens, top_k=4, logprobs=lp, entropy=ent, top_ids=ids, top_logprobs=top)
+        return [t.clone() for t in (total, x, out, lp, ent, ids, top)]
+
+    step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        step()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in (5, 6):
+        fresh, _ = norm_case(cuda, 30, 256, "f32", "f32", "rms", None, "rms", "bf16", seed=seed)
+        a["residual"].copy_(fresh["residual"])
+        a["branch"].copy_(fresh["branch"])
+        b["ids"].copy_(torch.randint(-1, 4, (30,), device=cuda))
+        want = step()
+        for t in (total, x, out, lp, ent, ids, top):
+            t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for w, t in zip(want, (total, x, out, lp, ent, ids, top)):
+            assert torch.equal(w, t)
