@@ -12,6 +12,8 @@
 // as two bf16 terms, h = hi + lo within 2^-16 |h|: with one term (2^-9) the
 // rounding of h would be far above the fp32 rounding of out.
 #include <algorithm>
+#include <atomic>
+#include <climits>
 
 #include "beside.h"
 #include "kv_cache.h"
@@ -23,66 +25,73 @@ namespace {
 constexpr int kTile = 64;                 // rows of an item, all of one adapter
 constexpr int kRouteThreads = 1024;
 constexpr int kThreads = 256;
-constexpr int kColBlock = 512;            // output columns of a block of the second product
-constexpr int kMaxSplit = 8;              // parts of K
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 int64_t max_tiles(int64_t M, int64_t n_adapters) { return M / kTile + std::min(n_adapters + 1, M); }
 int rank_stride(int64_t max_rank) { return (int)((max_rank + 31) / 32 * 32); }
-int k_split(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kTile - 1) / kTile;
-  int64_t split = 1;
-  while (split < kMaxSplit && tiles * split < 2 * attn_sm_count() && K / (2 * split) >= 256) split *= 2;
-  return (int)split;
-}
-
 struct Workspace {
   int* head;      // [0]: tiles of rows with an adapter, [1]: all tiles
   int4* tiles;    // adapter (-1: none), first place in rows, rows
   int* rows;      // [M] row numbers by adapter
-  float* part;    // [split][M][rank_stride] inner sums by place in rows
 };
 
 // ---- rows by adapter ---------------------------------------------------------
-// One block: counts per adapter, their sums, the tiles, then every row's place.
-// Rows of one warp with one adapter stay together, so that a prompt's rows do.
+// One block.  Its first `segs` warps take a stretch of the rows each and count them
+// by adapter in a table of their own; the counts' sums over warps and adapters
+// give every row a place that keeps the rows' order, so that a prompt's rows stay
+// together and the items are the same from run to run.
 __global__ void __launch_bounds__(kRouteThreads)
-lora_route_kernel(LoraArgs a, Workspace w, bool copy_none) {
-  extern __shared__ int counts[];         // [n_adapters + 1]: rows, then the next place
-  __shared__ int2 warp_sums[32];
-  __shared__ int2 carry;
+lora_route_kernel(LoraArgs a, Workspace w, bool copy_none, int segs) {
+  extern __shared__ int smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int buckets = a.n_adapters + 1;   // the last: no adapter
-  for (int i = tid; i < buckets; i += kRouteThreads) counts[i] = 0;
-  if (tid == 0) carry = make_int2(0, 0);
+  int* table = smem;                      // [segs][buckets]
+  int* home = smem + segs * buckets;      // [buckets]: an adapter's bucket (itself, or none), -1 for a bad rank
+  __shared__ int2 warp_sums[32];
+  __shared__ int2 carry;
   umma::pdl_launch_dependents();
-  umma::pdl_wait();
+  for (int i = tid; i < segs * buckets; i += kRouteThreads) table[i] = 0;
+  for (int b = tid; b < buckets; b += kRouteThreads) {
+    const int r = a.ranks != nullptr && b < a.n_adapters ? a.ranks[b] : 1;
+    home[b] = r < 0 || r > a.max_rank ? -1 : r == 0 ? a.n_adapters : b;
+  }
+  if (tid == 0) carry = make_int2(0, 0);
   __syncthreads();
-  auto bucket_of = [&](int m, bool report) {
-    const int id = a.ids[m];
+  const int seg = ((a.M + segs - 1) / segs + 31) / 32 * 32;
+  const int begin = min(warp * seg, a.M), end = warp < segs ? min(begin + seg, a.M) : begin;
+  constexpr int kAhead = 4;               // loads under way
+  // the bucket of row m with adapter `id`; -1 past the rows
+  auto bucket_of = [&](int m, int id, bool report) {
+    if (m >= end) return -1;
     if (id == -1) return a.n_adapters;
-    if (id < 0 || id >= a.n_adapters) {
-      if (report) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
-      return a.n_adapters;
-    }
-    if (a.ranks == nullptr) return id;
-    const int r = a.ranks[id];
-    if (r < 0 || r > a.max_rank) {
-      if (report) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
-      return a.n_adapters;
-    }
-    return r == 0 ? a.n_adapters : id;
+    const int b = id < 0 || id >= a.n_adapters ? -1 : home[id];
+    if (b >= 0) return b;
+    if (report) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+    return a.n_adapters;
   };
-  for (int m0 = 0; m0 < a.M; m0 += kRouteThreads) {
-    const int m = m0 + tid, b = m < a.M ? bucket_of(m, true) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
-    if (b >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[b], __popc(same));
+  for (int m0 = begin; m0 < end; m0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = m0 + u * 32 + lane < end ? a.ids[m0 + u * 32 + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int b = bucket_of(m0 + u * 32 + lane, id[u], true);
+      const uint32_t same = __match_any_sync(0xffffffffu, b);
+      if (b >= 0 && lane == __ffs(same) - 1) table[warp * buckets + b] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   for (int b0 = 0; b0 < buckets; b0 += kRouteThreads) {
     const int b = b0 + tid;
-    const int n = b < buckets ? counts[b] : 0;
+    int n = 0;
+    if (b < buckets)
+      for (int s = 0; s < segs; ++s) {
+        const int c = table[s * buckets + b];
+        table[s * buckets + b] = n;
+        n += c;
+      }
     const bool none = b == a.n_adapters;
     const int t = none && !copy_none ? 0 : (n + kTile - 1) / kTile;
     int2 s = make_int2(n, t);
@@ -96,93 +105,40 @@ lora_route_kernel(LoraArgs a, Workspace w, bool copy_none) {
     int2 before = carry;
     for (int i = 0; i < warp; ++i) before.x += warp_sums[i].x, before.y += warp_sums[i].y;
     const int first = before.x + s.x - n, tile0 = before.y + s.y - t;
-    if (b < buckets) {
-      counts[b] = first;
-      for (int i = 0; i < t; ++i)
-        w.tiles[tile0 + i] = make_int4(none ? -1 : b, first + i * kTile, min(kTile, n - i * kTile), 0);
-      if (none) w.head[0] = tile0, w.head[1] = tile0 + t;
+    if (none) w.head[0] = tile0, w.head[1] = tile0 + t;
+    // an adapter's tiles, by its warp
+    for (uint32_t left = __ballot_sync(0xffffffffu, t > 0); left != 0; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const int lt = __shfl_sync(0xffffffffu, t, l), ln = __shfl_sync(0xffffffffu, n, l);
+      const int lf = __shfl_sync(0xffffffffu, first, l), l0 = __shfl_sync(0xffffffffu, tile0, l);
+      const int lb = b0 + warp * 32 + l;
+      for (int i = lane; i < lt; i += 32)
+        w.tiles[l0 + i] =
+            make_int4(lb == a.n_adapters ? -1 : lb, lf + i * kTile, min(kTile, ln - i * kTile), 0);
     }
+    if (b < buckets)
+      for (int s2 = 0; s2 < segs; ++s2) table[s2 * buckets + b] += first;
     __syncthreads();
     if (tid == kRouteThreads - 1) carry = make_int2(first + n, tile0 + t);
     __syncthreads();
   }
-  for (int m0 = 0; m0 < a.M; m0 += kRouteThreads) {
-    const int m = m0 + tid, b = m < a.M ? bucket_of(m, false) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
-    const int leader = __ffs(same) - 1;
-    int at = 0;
-    if (b >= 0 && lane == leader) at = atomicAdd(&counts[b], __popc(same));
-    at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
-    if (b >= 0) w.rows[at] = m;
+  for (int m0 = begin; m0 < end; m0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = m0 + u * 32 + lane < end ? a.ids[m0 + u * 32 + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int m = m0 + u * 32 + lane, b = bucket_of(m, id[u], false);
+      const uint32_t same = __match_any_sync(0xffffffffu, b);
+      if (b >= 0) w.rows[table[warp * buckets + b] + __popc(same & ((1u << lane) - 1u))] = m;
+      __syncwarp();
+      if (b >= 0 && lane == __ffs(same) - 1) table[warp * buckets + b] += __popc(same);
+      __syncwarp();
+    }
   }
 }
 
-// ---- h = A x ------------------------------------------------------------------
-// A block takes a tile of 64 rows and one part of K; its warps 16 rows by half of
-// that part each.  Both operands come straight from memory as 16-byte loads of
-// eight consecutive k per lane: which k a fragment position stands for is free as
-// long as both operands agree.
-__global__ void __launch_bounds__(kThreads)
-lora_shrink_kernel(LoraArgs a, Workspace w, int rs) {
-  __shared__ float half[4][32][33];
-  umma::pdl_launch_dependents();
-  umma::pdl_wait();
-  const int tile = blockIdx.x;
-  if (tile >= w.head[0]) return;
-  const int4 it = w.tiles[tile];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const int group = warp & 3, kh = warp >> 2;
-  const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
-  const int chunks = (a.K + 31) / 32;                      // of 32 k
-  const int parts = 2 * gridDim.y, part = 2 * blockIdx.y + kh;
-  const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
-  const int r0 = group * 16 + g, r1 = r0 + 8;              // this lane's rows of the tile
-  const __nv_bfloat16* x0 = r0 < it.z ? a.X + (int64_t)w.rows[it.y + r0] * a.ldx : nullptr;
-  const __nv_bfloat16* x1 = r1 < it.z ? a.X + (int64_t)w.rows[it.y + r1] * a.ldx : nullptr;
-  const __nv_bfloat16* A = a.A + it.x * a.a_slot;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int j0 = 0; j0 < rank; j0 += 64) {
-    float acc[8][4] = {};
-    if (group * 16 < it.z) {
-#pragma unroll 2
-      for (int c = c0; c < c1; ++c) {
-        const int k = c * 32 + 8 * tig;
-        const uint4 p = x0 != nullptr && k < a.K ? ldg128(x0 + k) : zero;
-        const uint4 q = x1 != nullptr && k < a.K ? ldg128(x1 + k) : zero;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          if (j0 + 8 * n >= rank) break;
-          const int j = j0 + 8 * n + g;
-          const uint4 b = j < rank && k < a.K ? ldg128(A + j * a.a_rank + k) : zero;
-          mma_bf16_16816(acc[n], p.x, q.x, p.y, q.y, b.x, b.y);
-          mma_bf16_16816(acc[n], p.z, q.z, p.w, q.w, b.z, b.w);
-        }
-      }
-    }
-    if (kh == 1) {
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) half[group][lane][n * 4 + i] = acc[n][i];
-    }
-    __syncthreads();
-    if (kh == 0) {
-      float* to = w.part + ((int64_t)blockIdx.y * a.M + it.y) * rs;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int j = j0 + 8 * n + 2 * tig;
-        if (j0 + 8 * n >= rs) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] += half[group][lane][n * 4 + i];
-        if (r0 < it.z) *reinterpret_cast<float2*>(to + (int64_t)r0 * rs + j) = make_float2(acc[n][0], acc[n][1]);
-        if (r1 < it.z) *reinterpret_cast<float2*>(to + (int64_t)r1 * rs + j) = make_float2(acc[n][2], acc[n][3]);
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// ---- out = base + (s h) B^T -----------------------------------------------------
+// ---- the products ------------------------------------------------------------
 QMM_DEV uint32_t two_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -218,24 +174,222 @@ QMM_DEV void store4(float* row, int col, int N, float4 v) {
   }
 }
 
-// A block takes a tile of 64 rows and 512 columns.  The tile's h lies in shared
-// memory as two bf16 terms; a warp's columns are dealt to fragment positions so
-// that a lane's accumulators are four neighbouring columns of a row.
+// A warp's part of h for 16 rows and 8 kNT ranks from j0: chunks c0..c1 of 32 k.
+// Both operands come straight from memory, 16 bytes (eight consecutive k) per
+// lane: which k a fragment position stands for is free as long as both operands
+// agree.  All loads of kU chunks are under way before the first product.
+template <int kNT, int kU>
+QMM_DEV void inner_part(const LoraArgs& a, const __nv_bfloat16* x0, const __nv_bfloat16* x1,
+                        const __nv_bfloat16* A, int rank, int j0, int c0, int c1, float (&acc)[8][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int c = c0; c < c1; c += kU) {
+    uint4 p[kU], q[kU], b[kU][kNT];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = (c + u) * 32 + 8 * tig;
+      const bool in = c + u < c1 && k < a.K;
+      p[u] = in && x0 != nullptr ? ldg128(x0 + k) : zero;
+      q[u] = in && x1 != nullptr ? ldg128(x1 + k) : zero;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const int j = j0 + 8 * n + g;
+        b[u][n] = in && j < rank ? ldg128(A + j * a.a_rank + k) : zero;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        mma_bf16_16816(acc[n], p[u].x, q[u].x, p[u].y, q[u].y, b[u][n].x, b[u][n].y);
+        mma_bf16_16816(acc[n], p[u].z, q[u].z, p[u].w, q[u].w, b[u][n].z, b[u][n].w);
+      }
+  }
+}
+
+// A warp's part of out: 16 rows, units of 32 columns from u0 in steps of `step`.
+// Columns are dealt to fragment positions so that a lane's accumulators are four
+// neighbouring columns of a row.  The next unit's base is under way during the
+// products of one.  kRC: chunks of 32 ranks, whose h stays in registers; 0: any.
+template <bool kVec, int kRC>
+QMM_DEV void outer_part(const LoraArgs& a, const __nv_bfloat16* B, int rank, const uint16_t* hi, const uint16_t* lo,
+                        int hs, int r0, int64_t m0, int64_t m1, int u0, int u1, int step) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const float4 none = make_float4(0, 0, 0, 0);
+  const int chunks = kRC > 0 ? kRC : (rank + 31) / 32;
+  constexpr int kHeld = kRC > 0 ? kRC : 1;
+  uint4 h[kHeld][4];
+  auto load_h = [&](int c, uint4 (&to)[4]) {
+    const int j = c * 32 + 8 * tig;
+    to[0] = *reinterpret_cast<const uint4*>(hi + r0 * hs + j);
+    to[1] = *reinterpret_cast<const uint4*>(hi + (r0 + 8) * hs + j);
+    to[2] = *reinterpret_cast<const uint4*>(lo + r0 * hs + j);
+    to[3] = *reinterpret_cast<const uint4*>(lo + (r0 + 8) * hs + j);
+  };
+  if constexpr (kRC > 0) {
+#pragma unroll
+    for (int c = 0; c < kRC; ++c) load_h(c, h[c]);
+  }
+  auto load_base = [&](int u, float4 (&y)[2][2]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int col = u * 32 + 16 * p + 4 * tig;
+      y[0][p] = a.base != nullptr && m0 >= 0 && u < u1 ? load4<kVec>(a.base + m0 * a.ldb, col, a.N) : none;
+      y[1][p] = a.base != nullptr && m1 >= 0 && u < u1 ? load4<kVec>(a.base + m1 * a.ldb, col, a.N) : none;
+    }
+  };
+  auto load_b = [&](int u, int c, uint4 (&b)[4]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int col = u * 32 + 16 * (n >> 1) + 4 * (g >> 1) + (g & 1) + 2 * (n & 1), j = c * 32 + 8 * tig;
+      b[n] = j < rank && col < a.N ? ldg128(B + col * a.b_row + j) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  float4 y[2][2], next[2][2];
+  load_base(u0, y);
+  for (int u = u0; u < u1; u += step) {
+    float acc[4][4] = {};
+    if constexpr (kRC > 0) {
+      uint4 b[kRC][4];
+#pragma unroll
+      for (int c = 0; c < kRC; ++c) load_b(u, c, b[c]);
+      load_base(u + step, next);
+#pragma unroll
+      for (int c = 0; c < kRC; ++c)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint4 v = keep8(b[c][n], rank - c * 32 - 8 * tig);
+          mma_bf16_16816(acc[n], h[c][2].x, h[c][3].x, h[c][2].y, h[c][3].y, v.x, v.y);
+          mma_bf16_16816(acc[n], h[c][2].z, h[c][3].z, h[c][2].w, h[c][3].w, v.z, v.w);
+          mma_bf16_16816(acc[n], h[c][0].x, h[c][1].x, h[c][0].y, h[c][1].y, v.x, v.y);
+          mma_bf16_16816(acc[n], h[c][0].z, h[c][1].z, h[c][0].w, h[c][1].w, v.z, v.w);
+        }
+    } else {
+      uint4 b[2][4];
+      load_b(u, 0, b[0]);
+      load_base(u + step, next);
+      for (int c = 0; c < chunks; c += 2) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (c + e >= chunks) break;
+          load_b(u, c + e + 1, b[e ^ 1]);
+          load_h(c + e, h[0]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint4 v = keep8(b[e][n], rank - (c + e) * 32 - 8 * tig);
+            mma_bf16_16816(acc[n], h[0][2].x, h[0][3].x, h[0][2].y, h[0][3].y, v.x, v.y);
+            mma_bf16_16816(acc[n], h[0][2].z, h[0][3].z, h[0][2].w, h[0][3].w, v.z, v.w);
+            mma_bf16_16816(acc[n], h[0][0].x, h[0][1].x, h[0][0].y, h[0][1].y, v.x, v.y);
+            mma_bf16_16816(acc[n], h[0][0].z, h[0][1].z, h[0][0].w, h[0][1].w, v.z, v.w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int col = u * 32 + 16 * p + 4 * tig;
+      const float(&e)[4] = acc[2 * p], (&f)[4] = acc[2 * p + 1];
+      if (m0 >= 0)
+        store4<kVec>(a.out + m0 * a.ldo, col, a.N,
+                     make_float4(y[0][p].x + e[0], y[0][p].y + e[1], y[0][p].z + f[0], y[0][p].w + f[1]));
+      if (m1 >= 0)
+        store4<kVec>(a.out + m1 * a.ldo, col, a.N,
+                     make_float4(y[1][p].x + e[2], y[1][p].y + e[3], y[1][p].z + f[2], y[1][p].w + f[3]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) y[i][p] = next[i][p];
+    }
+  }
+}
+
+// The item of this cluster in a call of few rows, found by every block for
+// itself: row t opens an item when the number of earlier rows with its adapter is a
+// multiple of `tile`, and the item's rows are the next `tile` of them.  Rows without
+// an adapter make items of their own.  Returns {adapter, -, rows} with the row
+// numbers in rows[]; rows = 0: no item left for this cluster.
+QMM_DEV int4 own_item(const LoraArgs& a, int item, int tile, bool copy_none, int* ids, int* rows, int* scratch) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int id = INT_MIN;                       // past the rows
+  if (t < a.M) {
+    id = a.ids[t];
+    bool bad = id < -1 || id >= a.n_adapters;
+    if (!bad && id >= 0 && a.ranks != nullptr) {
+      const int r = a.ranks[id];
+      bad = r < 0 || r > a.max_rank;
+      if (r == 0) id = -1;
+    }
+    if (bad) {
+      if (blockIdx.x == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+      id = -1;
+    }
+    if (id < 0 && !copy_none) id = INT_MIN;
+  }
+  ids[t] = id;
+  if (t < 2) scratch[t] = -1;
+  __syncthreads();
+  int before = 0;
+  for (int s = 0; s < warp * 32; s += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + s);
+    before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+  }
+  before += __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
+  // items are numbered by the rows that open them
+  const bool opens = id != INT_MIN && before % tile == 0;
+  const uint32_t flags = __ballot_sync(0xffffffffu, opens);
+  int* counts = scratch + 2;
+  if (lane == 0) counts[warp] = __popc(flags);
+  __syncthreads();
+  int number = __popc(flags & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) number += counts[w];
+  if (opens && number == item) scratch[0] = id, scratch[1] = before;
+  __syncthreads();
+  const int adapter = scratch[0], first = scratch[1];
+  if (first < 0) return make_int4(0, 0, 0, 0);
+  const bool mine = id == adapter && before >= first && before < first + tile;
+  if (mine) rows[before - first] = t;
+  const int n = __syncthreads_count(mine);
+  return make_int4(adapter, 0, n, 0);
+}
+
+struct alignas(16) Smem {
+  float part[kThreads / 32][16][68];   // sums of a warp: 16 rows by 64 ranks; then of the block
+  int rows[kTile];
+  int ids[kThreads];
+  int scratch[2 + kThreads / 32];
+};
+static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
+
+// A cluster takes an item: up to 64 rows of one adapter.  First its blocks share
+// K and its warps the 16-row groups and the rest of K; the sums meet over shared
+// memory, each block finishing its share of h and writing it, as two bf16 terms,
+// to all blocks.  Then the blocks share the columns of out.
 template <bool kVec>
-__global__ void __launch_bounds__(kThreads)
-lora_expand_kernel(LoraArgs a, Workspace w, int rs, int split) {
+__global__ void __launch_bounds__(kThreads, 2)
+lora_kernel(LoraArgs a, Workspace w, int rs, int cluster, bool routed, bool copy_none) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int hs = rs + 8;                                   // row stride of h: rows fall on different banks
+  uint16_t* hi = reinterpret_cast<uint16_t*>(smem_raw + sizeof(Smem));
+  uint16_t* lo = hi + kTile * hs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
+  const int item = blockIdx.x / cluster, block = blockIdx.x % cluster;
   umma::pdl_wait();
-  const int tile = blockIdx.x;
-  if (tile >= w.head[1]) return;
-  const int4 it = w.tiles[tile];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
-  const int group = warp & 3, ch = warp >> 2;
-  const int col0 = blockIdx.y * kColBlock;
+  int4 it;
+  if (routed) {
+    if (item >= w.head[copy_none ? 1 : 0]) return;
+    it = w.tiles[item];
+    if (tid < it.z) sm.rows[tid] = w.rows[it.y + tid];
+    __syncthreads();
+  } else {
+    it = own_item(a, item, 16, copy_none, sm.ids, sm.rows, sm.scratch);
+    if (it.z == 0) return;
+    __syncthreads();
+  }
+  const int units = (a.N + 31) / 32;
+  const int n0 = (int)((int64_t)units * block / cluster), n1 = (int)((int64_t)units * (block + 1) / cluster);
   if (it.x < 0) {                                          // no adapter: base as it is
     for (int r = warp; r < it.z; r += kThreads / 32) {
-      const int64_t m = w.rows[it.y + r];
-      for (int c = col0 + lane * 4; c < min(col0 + kColBlock, a.N); c += 128)
+      const int64_t m = sm.rows[r];
+      for (int c = n0 * 32 + lane * 4; c < min(n1 * 32, a.N); c += 128)
         store4<kVec>(a.out + m * a.ldo, c, a.N,
                      a.base != nullptr ? load4<kVec>(a.base + m * a.ldb, c, a.N) : make_float4(0, 0, 0, 0));
     }
@@ -243,113 +397,149 @@ lora_expand_kernel(LoraArgs a, Workspace w, int rs, int split) {
   }
   const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
   const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
-  const int chunks = (rank + 31) / 32;
-  const int hs = chunks * 32 + 8;                          // row stride of h: rows fall on different banks
-  uint16_t* hi = reinterpret_cast<uint16_t*>(smem_raw);
-  uint16_t* lo = hi + kTile * hs;
-  for (int i = tid; i < kTile * chunks * 8; i += kThreads) {
-    const int r = i / (chunks * 8), j = i % (chunks * 8) * 4;
-    float4 h = make_float4(0, 0, 0, 0);
-    if (r < it.z) {
-      for (int s = 0; s < split; ++s) {                    // in order: the same sums every time
-        const float4 p = *reinterpret_cast<const float4*>(w.part + ((int64_t)s * a.M + it.y + r) * rs + j);
-        h.x += p.x, h.y += p.y, h.z += p.z, h.w += p.w;
-      }
-      h.x = j < rank ? h.x * scale : 0.f;
-      h.y = j + 1 < rank ? h.y * scale : 0.f;
-      h.z = j + 2 < rank ? h.z * scale : 0.f;
-      h.w = j + 3 < rank ? h.w * scale : 0.f;
-    }
-    const uint32_t a0 = two_bf16(h.x, h.y), a1 = two_bf16(h.z, h.w);
-    *reinterpret_cast<uint2*>(hi + r * hs + j) = make_uint2(a0, a1);
-    *reinterpret_cast<uint2*>(lo + r * hs + j) =
-        make_uint2(two_bf16(h.x - bf16lo_to_f32(a0), h.y - bf16hi_to_f32(a0)),
-                   two_bf16(h.z - bf16lo_to_f32(a1), h.w - bf16hi_to_f32(a1)));
-  }
-  __syncthreads();
-  const int r0 = group * 16 + g, r1 = r0 + 8;
-  if (group * 16 >= it.z) return;
-  const int64_t m0 = r0 < it.z ? w.rows[it.y + r0] : -1, m1 = r1 < it.z ? w.rows[it.y + r1] : -1;
-  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
-  for (int cb = col0 + ch * 64; cb < min(col0 + kColBlock, a.N); cb += 128) {
-    float4 y0[4], y1[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int col = cb + 16 * p + 4 * tig;
-      y0[p] = y1[p] = make_float4(0, 0, 0, 0);
-      if (a.base != nullptr) {
-        if (m0 >= 0) y0[p] = load4<kVec>(a.base + m0 * a.ldb, col, a.N);
-        if (m1 >= 0) y1[p] = load4<kVec>(a.base + m1 * a.ldb, col, a.N);
-      }
-    }
+  const int groups = it.z > 32 ? 4 : it.z > 16 ? 2 : 1;    // of 16 rows; the warps of a group share the rest
+  const int group = warp % groups, share = warp / groups, shares = kThreads / 32 / groups;
+  const int r0 = group * 16 + g, r1 = r0 + 8;              // this lane's rows of the item
+  const int64_t m0 = r0 < it.z ? sm.rows[r0] : -1, m1 = r1 < it.z ? sm.rows[r1] : -1;
+  const __nv_bfloat16* x0 = m0 >= 0 ? a.X + m0 * a.ldx : nullptr;
+  const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
+  const __nv_bfloat16* A = a.A + it.x * a.a_slot;
+  const int chunks = (a.K + 31) / 32;
+  const int p0 = block * shares + share, parts = cluster * shares;
+  const int c0 = (int)((int64_t)chunks * p0 / parts);
+  const int c1 = group * 16 < it.z ? (int)((int64_t)chunks * (p0 + 1) / parts) : c0;   // a group without rows: nothing
+  const uint32_t part_addr = umma::smem_u32(sm.part), hi_addr = umma::smem_u32(hi), lo_addr = umma::smem_u32(lo);
+  for (int j0 = 0; j0 < rank; j0 += 64) {
     float acc[8][4] = {};
-    for (int c = 0; c < chunks; ++c) {
-      const int j = c * 32 + 8 * tig;
-      const uint4 h0 = *reinterpret_cast<const uint4*>(hi + r0 * hs + j);
-      const uint4 h1 = *reinterpret_cast<const uint4*>(hi + r1 * hs + j);
-      const uint4 l0 = *reinterpret_cast<const uint4*>(lo + r0 * hs + j);
-      const uint4 l1 = *reinterpret_cast<const uint4*>(lo + r1 * hs + j);
+    const int left = rank - j0;
+    if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    else if (left <= 32) inner_part<4, 3>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    else inner_part<8, 2>(a, x0, x1, A, rank, j0, c0, c1, acc);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int col = cb + 16 * (n >> 1) + 4 * (g >> 1) + (g & 1) + 2 * (n & 1);
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (j < rank && col < a.N) b = keep8(ldg128(B + col * a.b_row + j), rank - j);
-        mma_bf16_16816(acc[n], l0.x, l1.x, l0.y, l1.y, b.x, b.y);
-        mma_bf16_16816(acc[n], l0.z, l1.z, l0.w, l1.w, b.z, b.w);
-        mma_bf16_16816(acc[n], h0.x, h1.x, h0.y, h1.y, b.x, b.y);
-        mma_bf16_16816(acc[n], h0.z, h1.z, h0.w, h1.w, b.z, b.w);
+    for (int n = 0; n < 8; ++n) {
+      const int j = 8 * n + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(&sm.part[warp][g][j]) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(&sm.part[warp][g + 8][j]) = make_float2(acc[n][2], acc[n][3]);
+    }
+    __syncthreads();
+    // the block's sums, in place of its first warps'
+    const int quads = groups * 16 * 16;                    // of four ranks
+    if (shares > 1) {
+      for (int i = tid; i < quads; i += kThreads) {
+        const int r = i / 16, j = i % 16 * 4;
+        float4 s = *reinterpret_cast<const float4*>(&sm.part[r / 16][r % 16][j]);
+        for (int k = 1; k < shares; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.part[r / 16 + k * groups][r % 16][j]);
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(&sm.part[r / 16][r % 16][j]) = s;
       }
     }
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int col = cb + 16 * p + 4 * tig;
-      const float(&e)[4] = acc[2 * p], (&f)[4] = acc[2 * p + 1];
-      if (m0 >= 0)
-        store4<kVec>(a.out + m0 * a.ldo, col, a.N,
-                     make_float4(y0[p].x + e[0], y0[p].y + e[1], y0[p].z + f[0], y0[p].w + f[1]));
-      if (m1 >= 0)
-        store4<kVec>(a.out + m1 * a.ldo, col, a.N,
-                     make_float4(y1[p].x + e[2], y1[p].y + e[3], y1[p].z + f[2], y1[p].w + f[3]));
+    umma::cluster_sync();
+    for (int i = block + cluster * tid; i < quads; i += cluster * kThreads) {
+      const int r = i / 16, j = i % 16 * 4;
+      const uint32_t at = part_addr + (uint32_t)(((r / 16 * 16 + r % 16) * 68 + j) * 4);
+      float4 s = make_float4(0, 0, 0, 0);
+      for (int o = 0; o < cluster; ++o) {                  // in order: the same sums every time
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(umma::mapa_shared(at, o))
+                     : "memory");
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      s.x = j0 + j < rank ? s.x * scale : 0.f;
+      s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
+      s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
+      s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
+      if (j0 + j < rs) {
+        const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
+        const uint32_t b0 = two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0));
+        const uint32_t b1 = two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1));
+        const uint32_t to = (uint32_t)(r * hs + j0 + j) * 2;
+        for (int o = 0; o < cluster; ++o) {
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(hi_addr + to, o)), "r"(a0),
+                       "r"(a1)
+                       : "memory");
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(lo_addr + to, o)), "r"(b0),
+                       "r"(b1)
+                       : "memory");
+        }
+      }
     }
+    umma::cluster_sync();
   }
+  if (group * 16 >= it.z) return;
+  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
+  if (rank <= 32) outer_part<kVec, 1>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
+  else if (rank <= 64) outer_part<kVec, 2>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
+  else outer_part<kVec, 0>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
+}
+
+// Calls of up to this many rows find their items in the kernel itself.
+constexpr int kOwnRows = kThreads;
+
+template <bool kVec>
+cudaError_t launch_typed(const LoraArgs& a, const Workspace& w, int rs, int items, int cluster, bool routed,
+                         bool copy_none, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t kMost = sizeof(Smem) + 2 * kTile * (kLoraMaxRank + 8) * 2;
+  cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_kernel<kVec>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem) + 2 * kTile * (rs + 8) * 2;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = routed ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, lora_kernel<kVec>, a, w, rs, cluster, routed, copy_none);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank) {
-  if (M == 0) return 0;
-  return 256 + pad256((size_t)max_tiles(M, n_adapters) * sizeof(int4)) + pad256((size_t)M * 4) +
-         pad256((size_t)k_split(M, K) * M * rank_stride(max_rank) * 4);
+  if (M <= kOwnRows) return 0;
+  return 256 + pad256((size_t)max_tiles(M, n_adapters) * sizeof(int4)) + pad256((size_t)M * 4);
 }
 
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream) {
-  const int tiles = (int)max_tiles(a.M, a.n_adapters);
-  const int rs = rank_stride(a.max_rank), split = k_split(a.M, a.K);
-  uint8_t* p = static_cast<uint8_t*>(workspace);
-  Workspace w;
-  w.head = reinterpret_cast<int*>(p);
-  p += 256;
-  w.tiles = reinterpret_cast<int4*>(p);
-  p += pad256((size_t)tiles * sizeof(int4));
-  w.rows = reinterpret_cast<int*>(p);
-  p += pad256((size_t)a.M * 4);
-  w.part = reinterpret_cast<float*>(p);
-  const bool in_place = a.base == a.out;
-  lora_route_kernel<<<1, kRouteThreads, (a.n_adapters + 1) * sizeof(int), stream>>>(a, w, !in_place);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  if ((err = launch_pdl(lora_shrink_kernel, dim3(tiles, split), dim3(kThreads), 0, stream, a, w, rs)) != cudaSuccess)
-    return err;
+  const bool routed = a.M > kOwnRows, copy_none = a.base != a.out;
+  Workspace w{};
+  int items = (int)(std::min<int64_t>(a.n_adapters + 1, a.M) + a.M / 16);
+  if (routed) {
+    items = (int)max_tiles(a.M, a.n_adapters);
+    uint8_t* p = static_cast<uint8_t*>(workspace);
+    w.head = reinterpret_cast<int*>(p);
+    p += 256;
+    w.tiles = reinterpret_cast<int4*>(p);
+    p += pad256((size_t)items * sizeof(int4));
+    w.rows = reinterpret_cast<int*>(p);
+    // counting tables of as many warps as shared memory holds
+    static std::atomic<uint64_t> done{0};
+    constexpr int kRouteSmem = 200 * 1024;
+    cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_route_kernel),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem);
+    if (err != cudaSuccess) return err;
+    const int buckets = a.n_adapters + 1, segs = std::min(32, kRouteSmem / 4 / buckets - 1);
+    lora_route_kernel<<<1, kRouteThreads, (size_t)(segs + 1) * buckets * 4, stream>>>(a, w, copy_none, segs);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  items = std::min(items, a.M);
+  int cluster = 8;                                         // blocks of an item: two per SM in all
+  while (cluster > 1 && items * cluster > 2 * attn_sm_count()) cluster /= 2;
   const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                    (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
-  const size_t smem = (size_t)2 * kTile * (rs + 8) * 2;
-  const dim3 grid(tiles, (a.N + kColBlock - 1) / kColBlock);
-  static std::atomic<uint64_t> done[2];
-  auto kern = vec ? lora_expand_kernel<true> : lora_expand_kernel<false>;
-  err = set_once(done[vec], reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                 2 * kTile * ((int)kLoraMaxRank + 8) * 2);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(kern, grid, dim3(kThreads), smem, stream, a, w, rs, split);
+  const int rs = rank_stride(a.max_rank);
+  return vec ? launch_typed<true>(a, w, rs, items, cluster, routed, copy_none, stream)
+             : launch_typed<false>(a, w, rs, items, cluster, routed, copy_none, stream);
 }
 
 }  // namespace qmm

@@ -46,8 +46,8 @@ def lora_set(qmm, **over):
 
 def test_lora_refusals(qmm):
     I, N, W = qmm.QMM_ERR_INVALID_ARG, qmm.QMM_ERR_UNSUPPORTED, qmm.QMM_ERR_WORKSPACE
-    need = qmm.lora_add_workspace_size(5, 64, 100, 3, 16)
-    base = dict(X=P, ldx=64, ids=P, M=5, base=P, ldb=100, out=P, ldo=100, ws=P, ws_bytes=need)
+    need = qmm.lora_add_workspace_size(500, 64, 100, 3, 16)
+    base = dict(X=P, ldx=64, ids=P, M=500, base=P, ldb=100, out=P, ldo=100, ws=P, ws_bytes=need)
 
     def call(s=None, **over):
         a = {**base, **over}
@@ -65,7 +65,7 @@ def test_lora_refusals(qmm):
         assert call(lora_set(qmm, **over)) == N, over
     assert call(M=1 << 24) == N
     for over in (dict(ws=None), dict(ws=P + 128), dict(ws_bytes=need - 1)):
-        assert call(**over) == (W if need else qmm.QMM_OK), over
+        assert call(**over) == W, over
     assert call(M=0) == qmm.QMM_OK and call(M=0, X=None, ids=None, out=None, base=None, ws=None) == qmm.QMM_OK
     assert qmm.lib.qmm_lora_add(None, *base.values(), None, None) == I
     size = ctypes.c_size_t(7)
