@@ -5,17 +5,22 @@
 // N and R stay apart, so that log S = log N + log1p(R / N) keeps its relative
 // accuracy where one token holds nearly all of a row.
 //
-// Bound: bytes, each logit read once.  A cluster of up to 16 blocks takes a
-// row; a block's tile of it lies in registers while the tile's maximum, sums and
-// candidates for the alternatives are found, and what the blocks found meets in
-// the first block's shared memory: one launch, no workspace.
+// Bound: bytes, each logit read once, by a cluster of up to 16 blocks per row: one
+// launch, no workspace.  A row is cut into segments of 128 16-byte vectors, dealt
+// to the cluster's warps; a warp streams its segments with no barrier, the next
+// one's loads under way, and leaves its statistics and each segment's maximum in
+// the first block's shared memory.
 //
-// Alternatives are kept by a 64-bit key: the logit in an order-preserving
-// integer form, then the complement of its index, so that keys differ, equal
-// logits fall by rising index and the choice is exact whatever the order of work.
+// Alternatives cost the stream nothing but the segments' maxima: the k-th largest
+// maximum of 32 groups of segments is a value that at least k logits reach, so
+// that only the few segments that reach it (about 1.5 k) are read again.  Logits
+// are kept by a 64-bit key, their value in an order-preserving integer form and the
+// complement of their index, so that keys differ, equal logits fall by rising
+// index and the choice is exact whatever the order of work.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <climits>
 
 #include "beside.h"
 #include "kv_cache.h"
@@ -26,12 +31,16 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 8;          // 16-byte vectors of a tile per thread
+constexpr int kAhead = 4;             // vectors of a segment per lane
+constexpr int kSegVecs = 32 * kAhead; // vectors of a segment (of one of its steps in rows of more than kMaxSegs)
+constexpr int kMaxSegs = 2048;
 constexpr int kMaxCluster = 16;
+constexpr int kUnit = 256;            // elements that a warp reads again at a time
+constexpr int kPool = kWarps * kUnit; // candidates of one such step of a block
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Running statistics relative to the maximum m: n terms equal to it, r the sum
-// of the others' 2^t, w the sum of t 2^t (t in the log2 domain).
+// Statistics relative to the maximum m: n terms equal to it, r the sum of the
+// others' 2^t, w the sum of t 2^t (t in the log2 domain).
 struct Stats {
   float m, n, r, w;
 };
@@ -108,37 +117,163 @@ QMM_DEV Vec<kBf16> load_vec(const void* row, int off, int v, int V) {
   return r;
 }
 
-// Block `rank` of the cluster's part of a result, as it lies in the first block.
-struct alignas(16) Part {
-  Stats s;
-  uint32_t count;           // alternatives
-  uint64_t best[kMaxTop];   // falling
-};
-
-struct Shared {
-  Part parts[kMaxCluster];
-  uint64_t best[2][kMaxTop];          // this block's alternatives, falling
-  // Candidates of a tile: at most 2 k threads' elements (64 at most each)
-  uint64_t pool[2 * kMaxTop * 64 + kMaxTop];
-  Stats warp_stats[kWarps];
-  uint64_t warp_max[kWarps];
+struct alignas(16) Shared {
+  Stats stats[kMaxCluster * kWarps];   // of the cluster's warps
+  uint64_t pool[kPool + kMaxTop];      // candidates
+  uint64_t best[kMaxTop];              // the largest so far, falling
+  uint64_t warp_key[kWarps];
+  uint32_t seg_max[kMaxSegs];          // order of a segment's largest logit
+  uint32_t group_max[kWarps][32];
+  int list[kMaxSegs];                  // segments to read again, rising
+  int warp_count[kWarps];
+  Stats row;
   int n_pool;
 };
 
-// The k largest of pool[0..n), falling, into `to`: each key's rank is the
-// number of larger ones (keys differ).
-QMM_DEV void rank_into(const uint64_t* pool, int n, int k, uint64_t* to) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t mine = pool[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += pool[j] > mine;
-    if (rank < k) to[rank] = mine;
+// The k largest of the pool's n keys, falling, into sm.best; returns how many.
+// Many candidates (rows with far more than k equal logits) are thinned first.
+QMM_DEV int settle(Shared& sm, int n, int k) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (n > kThreads) {
+    // Raise a bar until k to 2 k threads' largest keys lie above it, by bisection
+    // over the keys, which differ, so that it ends: at most 2 k threads' keys stay.
+    constexpr int kEach = (kPool + kMaxTop + kThreads - 1) / kThreads;
+    uint64_t mine[kEach], most = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      mine[i] = tid + i * kThreads < n ? sm.pool[tid + i * kThreads] : 0;
+      most = max(most, mine[i]);
+    }
+    uint64_t above = most;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) above = max(above, __shfl_xor_sync(0xffffffffu, above, o));
+    if (lane == 0) sm.warp_key[warp] = above;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) above = max(above, sm.warp_key[w]);   // nothing lies above it
+    uint64_t bar = 0;
+    int count = kThreads;
+    while (count > 2 * k) {
+      const uint64_t mid = bar + (above - bar) / 2;
+      const int c = __syncthreads_count(most > mid);
+      if (c >= k) bar = mid, count = c;
+      else above = mid;
+    }
+    if (tid == 0) sm.n_pool = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (mine[i] > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = mine[i];
+    __syncthreads();
+    n = sm.n_pool;
   }
+  // a key's place is the number of larger ones
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t mine = sm.pool[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += sm.pool[j] > mine;
+    if (place < k) sm.best[place] = mine;
+  }
+  __syncthreads();
+  return min(n, k);
+}
+
+// The k largest logits of a row into sm.best, by the whole block; returns how
+// many there are (logits of -infinity are none).
+template <bool kBf16>
+QMM_DEV int find_top(Shared& sm, const void* x, int off, int V, int k, int segs, int steps) {
+  constexpr int kN = Vec<kBf16>::kN, kUnitVecs = kUnit / kN, kLoads = kUnitVecs / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the k-th largest of 32 groups' maxima
+  uint32_t most = 0;
+  for (int i = tid; i < segs; i += kThreads) most = max(most, sm.seg_max[i]);
+  sm.group_max[warp][lane] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) most = max(most, sm.group_max[w][lane]);
+  int place = 0;
+#pragma unroll
+  for (int l = 0; l < 32; ++l) {
+    const uint32_t o = __shfl_sync(0xffffffffu, most, l);
+    place += o > most || (o == most && l < lane);
+  }
+  const uint32_t floor_order = max(__shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, place == k - 1)) - 1),
+                                   kOrderMinusInf + 1);
+  // the segments that reach it
+  const int each = (segs + kThreads - 1) / kThreads;
+  int mine = 0;
+  for (int i = tid * each; i < min((tid + 1) * each, segs); ++i) mine += sm.seg_max[i] >= floor_order;
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) sm.warp_count[warp] = at;
+  if (tid == 0) sm.n_pool = 0;
+  __syncthreads();
+  at -= mine;
+  int listed = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += sm.warp_count[w];
+    listed += sm.warp_count[w];
+  }
+  for (int i = tid * each; i < min((tid + 1) * each, segs); ++i)
+    if (sm.seg_max[i] >= floor_order) sm.list[at++] = i;
+  __syncthreads();
+  // read again, a unit per warp and step
+  const int per_seg = steps * kSegVecs / kUnitVecs;
+  const int units = listed * per_seg;
+  uint64_t bar = (uint64_t)(floor_order - 1) << 32 | 0xFFFFFFFFu;   // keys above it are candidates
+  int have = 0;                                                     // of sm.best
+  Vec<kBf16> next[kLoads];
+  auto load = [&](int unit) {
+    // a segment that does not reach the bar holds no candidate, nor does one that
+    // equals it: its indexes are larger
+    const int seg = unit < units ? sm.list[unit / per_seg] : -1;
+    const bool skip = seg < 0 || sm.seg_max[seg] <= (uint32_t)(bar >> 32);
+    const int v0 = skip ? INT_MAX / kN : seg * steps * kSegVecs + unit % per_seg * kUnitVecs + lane;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) next[u] = load_vec<kBf16>(x, off, v0 + u * 32, V);
+  };
+  load(warp);
+  for (int u0 = 0; u0 < units; u0 += kWarps) {
+    const int unit = u0 + warp;
+    Vec<kBf16> q[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) q[u] = next[u];
+    load(unit + kWarps);
+    if (unit < units) {
+      const int v0 = sm.list[unit / per_seg] * steps * kSegVecs + unit % per_seg * kUnitVecs;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const float f = q[u].at(i);
+          const uint64_t key = key_of(f, (uint32_t)(v0 + u * 32 + lane) * kN - off + i);
+          if (f == f && key > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = key;
+        }
+    }
+    __syncthreads();
+    const int n = sm.n_pool;
+    if (u0 + kWarps >= units) return settle(sm, n, k);
+    __syncthreads();
+    if (n > kMaxTop) {
+      // the pool has room for one more step beside the best k
+      have = settle(sm, n, k);
+      if (tid < have) sm.pool[tid] = sm.best[tid];
+      if (tid == 0) sm.n_pool = have;
+      if (have == k) bar = sm.best[k - 1];
+      __syncthreads();
+    }
+  }
+  return 0;
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads)
-token_logprobs_kernel(LogprobArgs a, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2)
+token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   constexpr int kN = Vec<kBf16>::kN;
@@ -146,179 +281,150 @@ token_logprobs_kernel(LogprobArgs a, int cluster) {
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const uint8_t* x = static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.ld * (kBf16 ? 2 : 4);
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / (kBf16 ? 2 : 4));
-  const int vecs = (int)(((int64_t)a.V + off + kN - 1) / kN);
-  const int part = (vecs + cluster - 1) / cluster;
-  const int begin = min(rank * part, vecs), end = min(begin + part, vecs);
   const float c = a.scale * kLog2e;
   const int k = a.top_k;
 
-  Stats st = {-FLT_MAX, 0.f, 0.f, 0.f};
-  int have = 0;              // alternatives so far, in sm.best[cur]
-  int cur = 0;
-  for (int base = begin; base < end; base += kUnroll * kThreads) {
-    Vec<kBf16> q[kUnroll];
+  // This warp's segments, in steps of 32 lanes by kAhead vectors.
+  const int wid = rank * kWarps + warp, warps = cluster * kWarps;
+  Vec<kBf16> next[kAhead];
+  auto load = [&](int seg, int step) {
+    const int64_t e = ((int64_t)seg * steps + step) * kSegVecs * kN - off;    // the step's first element
+    if (seg < segs && e >= 0 && e + kSegVecs * kN <= a.V) {
+      const uint8_t* p = x + e * (kBf16 ? 2 : 4) + lane * 16;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int v = base + u * kThreads + tid;
-      q[u] = load_vec<kBf16>(x, off, v < end ? v : vecs + 1, a.V);   // past the row: -infinity
+      for (int u = 0; u < kAhead; ++u) next[u].q = ldg128_stream(p + u * 512);
+    } else {
+      const int v0 = seg < segs ? (seg * steps + step) * kSegVecs : INT_MAX / kN;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) next[u] = load_vec<kBf16>(x, off, v0 + u * 32 + lane, a.V);
     }
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int i = 0; i < kN; ++i) top = fmaxf(top, q[u].at(i));
-    const float m = fmaxf(st.m, top);
-    Stats tile = {m, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const float t = (q[u].at(i) - m) * c, e = exp2_fast(t);
-        if (t < 0.f) tile.r += e;
-        else tile.n += e;                            // 1, or NaN
-        tile.w = fmaf(fmaxf(t, -1e30f), e, tile.w);   // -infinity: -1e30 * 0
-      }
-    st = join(tile, st, c);
-
-    if (k == 0) continue;
-    // Candidates: what exceeds the last of the block's alternatives.
-    const uint64_t least = have == k ? sm.best[cur][k - 1] : (uint64_t)kOrderMinusInf << 32 | 0xFFFFFFFFu;
-    const uint32_t top_order = order_of(top);
-    uint64_t mine = 0;
-    if (top_order >= (uint32_t)(least >> 32) && top_order > kOrderMinusInf) {
-#pragma unroll
-      for (int u = kUnroll - 1; u >= 0; --u)
-#pragma unroll
-        for (int i = kN - 1; i >= 0; --i)
-          if (q[u].at(i) == top) mine = key_of(top, (uint32_t)((base + u * kThreads + tid) * kN - off + i));
-    }
-    uint64_t bar = least;                            // keys above it are candidates
-    int n = __syncthreads_count(mine > bar);
-    if (n == 0) continue;
-    if (n > 2 * k) {
-      // Raise the bar until k to 2 k threads' largest lie above it: bisection over
-      // the keys, which differ, so that it ends.
-      uint64_t best = mine;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-      if (lane == 0) sm.warp_max[warp] = best;
-      __syncthreads();
-      uint64_t above = 0;                            // nothing lies above it
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) above = max(above, sm.warp_max[w]);
-      while (n > 2 * k) {
-        const uint64_t mid = bar + (above - bar) / 2;
-        const int nm = __syncthreads_count(mine > mid);
-        if (nm >= k) bar = mid, n = nm;
-        else above = mid;
-      }
-    }
-    if (tid == 0) sm.n_pool = 0;
-    __syncthreads();
-    if (mine > bar) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint64_t key = key_of(q[u].at(i), (uint32_t)((base + u * kThreads + tid) * kN - off + i));
-          if (q[u].at(i) <= top && key > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = key;   // not NaN
-        }
-    }
-    if (tid < have) {
-      // the block's alternatives so far compete as well
-      const uint64_t key = sm.best[cur][tid];
-      sm.pool[atomicAdd(&sm.n_pool, 1)] = key;
-    }
-    __syncthreads();
-    const int pooled = sm.n_pool;
-    rank_into(sm.pool, pooled, k, sm.best[cur ^ 1]);
-    cur ^= 1;
-    have = min(k, pooled);
-    __syncthreads();
+  };
+  load(wid, 0);
+  // the tokens' logits, long before they are needed
+  int token = -1;
+  float token_x = 0.f;
+  if (rank == 0 && tid < a.G) {
+    token = a.tokens[(int64_t)row * a.ld_tokens + tid];
+    if (token >= 0 && token < a.V) token_x = load_one<kBf16>(x, token);
   }
+  umma::cluster_sync();   // every block of the cluster runs, so that the first one's shared memory can be written
+  const uint32_t first_stats = umma::mapa_shared(umma::smem_u32(&sm.stats[wid]), 0);
+  const uint32_t first_segs = umma::mapa_shared(umma::smem_u32(sm.seg_max), 0);
 
-  // The block's statistics: warps, then the first warp.
+  Stats st = {-FLT_MAX, 0.f, 0.f, 0.f};   // m is the warp's, n, r and w the lane's
+  for (int seg = wid; seg < segs; seg += warps) {
+    uint32_t seg_order = 0;
+    for (int step = 0; step < steps; ++step) {
+      Vec<kBf16> q[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) q[u] = next[u];
+      if (step + 1 < steps) load(seg, step + 1);
+      else load(seg + warps, 0);
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) top = fmaxf(top, q[u].at(i));
+      const uint32_t order = __reduce_max_sync(0xffffffffu, order_of(top));
+      seg_order = max(seg_order, order);
+      const float m = value_of(order);
+      if (m >= st.m) {
+        // a new maximum (or the same again): its own terms are counted apart
+        if (m > st.m) {
+          const float t = fmaxf((st.m - m) * c, -1e30f), f = exp2_fast(t), s = st.n + st.r;
+          st = {m, 0.f, s * f, f > 0.f ? f * fmaf(t, s, st.w) : 0.f};
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const float t = (q[u].at(i) - st.m) * c, e = exp2_fast(t);
+            if (t < 0.f) st.r += e;
+            else st.n += e;                              // 1, or NaN
+            st.w = fmaf(fmaxf(t, -1e30f), e, st.w);       // -infinity: -1e30 * 0
+          }
+      } else {
+        const uint64_t minus_m = f2_pack(-st.m, -st.m), cc = f2_pack(c, c);
+        uint64_t r2 = f2_pack(st.r, 0.f), w2 = f2_pack(st.w, 0.f);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < kN; i += 2) {
+            const uint64_t t2 = f2_mul(f2_add(f2_pack(q[u].at(i), q[u].at(i + 1)), minus_m), cc);
+            float t0, t1;
+            f2_unpack(t2, t0, t1);
+            const uint64_t e2 = f2_pack(exp2_fast(t0), exp2_fast(t1));
+            r2 = f2_add(r2, e2);
+            w2 = f2_fma(f2_pack(fmaxf(t0, -1e30f), fmaxf(t1, -1e30f)), e2, w2);
+          }
+        float lo, hi;
+        f2_unpack(r2, lo, hi);
+        st.r = lo + hi;
+        f2_unpack(w2, lo, hi);
+        st.w = lo + hi;
+      }
+    }
+    if (lane == 0 && k > 0)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_segs + 4u * seg), "r"(seg_order) : "memory");
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Stats b = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.n, o),
-                     __shfl_xor_sync(0xffffffffu, st.r, o), __shfl_xor_sync(0xffffffffu, st.w, o)};
-    st = join(st, b, c);
+    st.n += __shfl_xor_sync(0xffffffffu, st.n, o);
+    st.r += __shfl_xor_sync(0xffffffffu, st.r, o);
+    st.w += __shfl_xor_sync(0xffffffffu, st.w, o);
   }
-  if (lane == 0) sm.warp_stats[warp] = st;
-  umma::cluster_sync();   // also: every block of the cluster runs, and its shared memory can be written
+  if (lane == 0)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(first_stats), "f"(st.m), "f"(st.n), "f"(st.r),
+                 "f"(st.w)
+                 : "memory");
+  umma::cluster_sync();
+  if (rank != 0) return;
+
   if (warp == 0) {
-    st = lane < kWarps ? sm.warp_stats[lane] : Stats{-FLT_MAX, 0.f, 0.f, 0.f};
+    st = lane < warps ? sm.stats[lane] : Stats{-FLT_MAX, 0.f, 0.f, 0.f};
+    for (int i = lane + 32; i < warps; i += 32) st = join(st, sm.stats[i], c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const Stats b = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.n, o),
                        __shfl_xor_sync(0xffffffffu, st.r, o), __shfl_xor_sync(0xffffffffu, st.w, o)};
       st = join(st, b, c);
     }
-    const uint32_t to = umma::mapa_shared(umma::smem_u32(&sm.parts[rank]), 0);
-    if (lane == 0) {
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(st.m), "f"(st.n), "f"(st.r),
-                   "f"(st.w)
-                   : "memory");
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + (uint32_t)offsetof(Part, count)), "r"(have)
-                   : "memory");
-    }
-    if (lane < have)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + (uint32_t)offsetof(Part, best) + 8u * lane),
-                   "l"(sm.best[cur][lane])
-                   : "memory");
+    if (lane == 0) sm.row = st;
   }
-  umma::cluster_sync();
-  if (rank != 0) return;
-
-  // The row's statistics, the same in every thread.
-  st = sm.parts[0].s;
-  for (int p = 1; p < cluster; ++p) st = join(st, sm.parts[p].s, c);
+  __syncthreads();
+  st = sm.row;
   const float total = st.n + st.r;
   const bool sound = total > 0.f && st.m < INFINITY;   // false for NaN as well
   const float log_sum = logf(st.n) + log1pf(st.r / st.n);
   if (tid == 0 && a.entropy != nullptr) a.entropy[row] = sound ? fmaf(-st.w / total, kLn2, log_sum) : NAN;
   for (int g = tid; g < a.G; g += kThreads) {
-    const int token = a.tokens[(int64_t)row * a.ld_tokens + g];
+    if (g >= kThreads) {
+      token = a.tokens[(int64_t)row * a.ld_tokens + g];
+      if (token >= 0 && token < a.V) token_x = load_one<kBf16>(x, token);
+    }
     if (token < 0 || token >= a.V) {
       if (token != -1) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
       continue;
     }
-    const float l = (load_one<kBf16>(x, token) - st.m) * a.scale - log_sum;
-    a.logprobs[(int64_t)row * a.G + g] = sound ? l : NAN;
+    a.logprobs[(int64_t)row * a.G + g] = sound ? (token_x - st.m) * a.scale - log_sum : NAN;
   }
   if (k == 0) return;
-  // A key's place among all is its place in its own list and, in each other
-  // list, the number of larger keys.
-  int all = 0;
-  for (int p = 0; p < cluster; ++p) all += sm.parts[p].count;
-  for (int i = tid; i < cluster * kMaxTop; i += kThreads) {
-    const int p = i / kMaxTop, at = i % kMaxTop;
-    if (at >= (int)sm.parts[p].count) continue;
-    const uint64_t mine = sm.parts[p].best[at];
-    int place = at;
-    for (int o = 0; o < cluster && place < k; ++o) {
-      if (o == p) continue;
-      int lo = 0, hi = sm.parts[o].count;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (sm.parts[o].best[mid] > mine) lo = mid + 1;
-        else hi = mid;
-      }
-      place += lo;
+  const int have = sound ? find_top<kBf16>(sm, x, off, a.V, k, segs, steps) : 0;
+  if (tid < k) {
+    int32_t id = -1;
+    float l = sound ? -INFINITY : NAN;
+    if (tid < have) {
+      const uint64_t key = sm.best[tid];
+      id = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
+      l = (value_of((uint32_t)(key >> 32)) - st.m) * a.scale - log_sum;
     }
-    if (place >= k || !sound) continue;
-    a.top_ids[(int64_t)row * k + place] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-    a.top_logprobs[(int64_t)row * k + place] = (value_of((uint32_t)(mine >> 32)) - st.m) * a.scale - log_sum;
-  }
-  for (int i = tid; i < k; i += kThreads) {
-    if (sound && i < all) continue;
-    a.top_ids[(int64_t)row * k + i] = -1;
-    a.top_logprobs[(int64_t)row * k + i] = sound ? -INFINITY : NAN;
+    a.top_ids[(int64_t)row * k + tid] = id;
+    a.top_logprobs[(int64_t)row * k + tid] = l;
   }
 }
 
 template <bool kBf16>
-cudaError_t launch_typed(const LogprobArgs& a, int cluster, cudaStream_t stream) {
+cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0}, done_size{0};
   const void* kern = reinterpret_cast<const void*>(token_logprobs_kernel<kBf16>);
   cudaError_t err = set_once(done, kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -336,20 +442,25 @@ cudaError_t launch_typed(const LogprobArgs& a, int cluster, cudaStream_t stream)
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<kBf16>, a, cluster);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<kBf16>, a, cluster, segs, steps);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
+  // Segments of a row that begins anywhere between two 16-byte boundaries.
+  const int n = a.bf16 ? 8 : 4;
+  const int64_t vecs = ((int64_t)a.V + 2 * n - 2) / n;
+  const int64_t least = (vecs + kSegVecs - 1) / kSegVecs;
+  const int steps = (int)((least + kMaxSegs - 1) / kMaxSegs);
+  const int segs = (int)((least + steps - 1) / steps);
   // Blocks of a row: enough to fill the SMs twice when there are few rows, while
-  // each keeps at least half a tile.
-  const int sms = attn_sm_count();
-  const int vecs = (int)((a.V + (a.bf16 ? 7 : 3)) / (a.bf16 ? 8 : 4)) + 1;
+  // each warp keeps a segment.
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)a.M * cluster < 2 * sms && vecs / (2 * cluster) >= kUnroll * kThreads / 2)
+  while (cluster < kMaxCluster && (int64_t)a.M * cluster < 2 * attn_sm_count() && segs >= 2 * cluster * kWarps)
     cluster *= 2;
-  return a.bf16 ? launch_typed<true>(a, cluster, stream) : launch_typed<false>(a, cluster, stream);
+  return a.bf16 ? launch_typed<true>(a, cluster, segs, steps, stream)
+                : launch_typed<false>(a, cluster, segs, steps, stream);
 }
 
 }  // namespace qmm
