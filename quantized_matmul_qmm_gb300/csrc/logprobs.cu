@@ -37,6 +37,7 @@ constexpr int kMaxSegs = 2048;
 constexpr int kMaxCluster = 16;
 constexpr int kUnit = 256;            // elements that a warp reads again at a time
 constexpr int kPool = kWarps * kUnit; // candidates of one such step of a block
+constexpr int kKeep = kThreads;       // candidates that may wait for the next step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Statistics relative to the maximum m: n terms equal to it, r the sum of the
@@ -61,6 +62,22 @@ QMM_DEV Stats join(const Stats& a, const Stats& b, float c) {
   return Stats{hi.m, hi.n, fmaf(s, f, hi.r), hi.w + (f > 0.f ? f * fmaf(t, s, lo.w) : 0.f)};
 }
 
+// The same statistics relative to a larger m.
+QMM_DEV Stats raise_to(const Stats& a, float m, float c) {
+  const float t = fmaxf((a.m - m) * c, -1e30f), f = exp2_fast(t), s = a.n + a.r;
+  return Stats{m, 0.f, s * f, f > 0.f ? f * fmaf(t, s, a.w) : 0.f};
+}
+
+QMM_DEV void put_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// A barrier of all blocks of a row.
+QMM_DEV void block_sync(int cluster) {
+  if (cluster > 1) umma::cluster_sync();
+  else __syncthreads();
+}
+
 QMM_DEV uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);   // -0 becomes 0
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
@@ -83,48 +100,47 @@ struct Vec {
   }
 };
 
+// A row as 16-byte vectors: `head` elements before the first boundary, `full`
+// vectors, and what remains.  Elements outside the vectors (at most 14) are the edge,
+// one per lane.
 template <bool kBf16>
-QMM_DEV float load_one(const void* row, int64_t i) {
-  if constexpr (kBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
-  return static_cast<const float*>(row)[i];
-}
-
-// Vector `v` of a row that begins `off` elements after a 16-byte boundary:
-// elements v * kN - off ..; what lies outside the row reads as -infinity.
-template <bool kBf16>
-QMM_DEV Vec<kBf16> load_vec(const void* row, int off, int v, int V) {
-  constexpr int kN = Vec<kBf16>::kN;
-  const int64_t e = (int64_t)v * kN - off;
-  Vec<kBf16> r;
-  if (e >= 0 && e + kN <= V) {
-    r.q = ldg128_stream(static_cast<const uint8_t*>(row) + e * (kBf16 ? 2 : 4));
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = kBf16 ? 0xFF80FF80u : 0xFF800000u;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (e + i < 0 || e + i >= V) continue;
-      if constexpr (kBf16) {
-        const uint32_t b = static_cast<const uint16_t*>(row)[e + i];
-        w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | b << 16 : (w[i / 2] & 0xFFFF0000u) | b;
-      } else {
-        w[i] = static_cast<const uint32_t*>(row)[e + i];
-      }
-    }
-    r.q = make_uint4(w[0], w[1], w[2], w[3]);
+struct Row {
+  const uint8_t* x;
+  const uint8_t* vecs;
+  int head, full, V;
+  QMM_DEV Row(const uint8_t* row, int n) : x(row), V(n) {
+    constexpr int kN = Vec<kBf16>::kN, kSize = kBf16 ? 2 : 4;
+    head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kSize, V);
+    full = (V - head) / kN;
+    vecs = row + head * kSize;
   }
-  return r;
-}
+  QMM_DEV float at(int i) const {
+    if constexpr (kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x)[i]);
+    return reinterpret_cast<const float*>(x)[i];
+  }
+  // Vector v, or -infinity where there is none.
+  QMM_DEV Vec<kBf16> vec(int v) const {
+    const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+    Vec<kBf16> r;
+    r.q = make_uint4(none, none, none, none);
+    if (v < full) r.q = ldg128_stream(vecs + (int64_t)v * 16);
+    return r;
+  }
+  // Lane's edge element, or -1.
+  QMM_DEV int edge(int lane) const {
+    const int behind = head + full * Vec<kBf16>::kN + lane - head;
+    return lane < head ? lane : behind < V ? behind : -1;
+  }
+};
 
 struct alignas(16) Shared {
   Stats stats[kMaxCluster * kWarps];   // of the cluster's warps
-  uint64_t pool[kPool + kMaxTop];      // candidates
+  uint64_t pool[kPool + kKeep];        // candidates
   uint64_t best[kMaxTop];              // the largest so far, falling
-  uint64_t warp_key[kWarps];
-  uint32_t seg_max[kMaxSegs];          // order of a segment's largest logit
+  uint64_t warp_key[kMaxCluster * kWarps];
+  uint32_t seg_max[kMaxSegs + 1];      // order of a segment's largest logit; the edge's behind them
   uint32_t group_max[kWarps][32];
-  int list[kMaxSegs];                  // segments to read again, rising
+  int list[kMaxSegs + 1];              // segments to read again, rising
   int warp_count[kWarps];
   Stats row;
   int n_pool;
@@ -137,7 +153,7 @@ QMM_DEV int settle(Shared& sm, int n, int k) {
   if (n > kThreads) {
     // Raise a bar until k to 2 k threads' largest keys lie above it, by bisection
     // over the keys, which differ, so that it ends: at most 2 k threads' keys stay.
-    constexpr int kEach = (kPool + kMaxTop + kThreads - 1) / kThreads;
+    constexpr int kEach = (kPool + kKeep) / kThreads;
     uint64_t mine[kEach], most = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -181,12 +197,13 @@ QMM_DEV int settle(Shared& sm, int n, int k) {
 // The k largest logits of a row into sm.best, by the whole block; returns how
 // many there are (logits of -infinity are none).
 template <bool kBf16>
-QMM_DEV int find_top(Shared& sm, const void* x, int off, int V, int k, int segs, int steps) {
+QMM_DEV int find_top(Shared& sm, const Row<kBf16>& x, int k, int segs, int steps) {
   constexpr int kN = Vec<kBf16>::kN, kUnitVecs = kUnit / kN, kLoads = kUnitVecs / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the k-th largest of 32 groups' maxima
+  const int all = segs + 1;                 // with the edge
   uint32_t most = 0;
-  for (int i = tid; i < segs; i += kThreads) most = max(most, sm.seg_max[i]);
+  for (int i = tid; i < all; i += kThreads) most = max(most, sm.seg_max[i]);
   sm.group_max[warp][lane] = most;
   __syncthreads();
 #pragma unroll
@@ -200,9 +217,9 @@ QMM_DEV int find_top(Shared& sm, const void* x, int off, int V, int k, int segs,
   const uint32_t floor_order = max(__shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, place == k - 1)) - 1),
                                    kOrderMinusInf + 1);
   // the segments that reach it
-  const int each = (segs + kThreads - 1) / kThreads;
+  const int each = (all + kThreads - 1) / kThreads;
   int mine = 0;
-  for (int i = tid * each; i < min((tid + 1) * each, segs); ++i) mine += sm.seg_max[i] >= floor_order;
+  for (int i = tid * each; i < min((tid + 1) * each, all); ++i) mine += sm.seg_max[i] >= floor_order;
   int at = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -219,7 +236,7 @@ QMM_DEV int find_top(Shared& sm, const void* x, int off, int V, int k, int segs,
     if (w < warp) at += sm.warp_count[w];
     listed += sm.warp_count[w];
   }
-  for (int i = tid * each; i < min((tid + 1) * each, segs); ++i)
+  for (int i = tid * each; i < min((tid + 1) * each, all); ++i)
     if (sm.seg_max[i] >= floor_order) sm.list[at++] = i;
   __syncthreads();
   // read again, a unit per warp and step
@@ -228,39 +245,45 @@ QMM_DEV int find_top(Shared& sm, const void* x, int off, int V, int k, int segs,
   uint64_t bar = (uint64_t)(floor_order - 1) << 32 | 0xFFFFFFFFu;   // keys above it are candidates
   int have = 0;                                                     // of sm.best
   Vec<kBf16> next[kLoads];
+  int next_at;                              // index of the lane's first element
   auto load = [&](int unit) {
     // a segment that does not reach the bar holds no candidate, nor does one that
-    // equals it: its indexes are larger
+    // equals it: its indexes are larger, but for the edge's, which come last in
+    // the list
     const int seg = unit < units ? sm.list[unit / per_seg] : -1;
-    const bool skip = seg < 0 || sm.seg_max[seg] <= (uint32_t)(bar >> 32);
-    const int v0 = skip ? INT_MAX / kN : seg * steps * kSegVecs + unit % per_seg * kUnitVecs + lane;
+    const bool edge = seg == segs && unit % per_seg == 0;
+    const bool skip = seg < 0 || seg == segs || sm.seg_max[seg] <= (uint32_t)(bar >> 32);
+    const int v0 = skip ? x.full : seg * steps * kSegVecs + unit % per_seg * kUnitVecs + lane;
+    next_at = x.head + v0 * kN;
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) next[u] = load_vec<kBf16>(x, off, v0 + u * 32, V);
+    for (int u = 0; u < kLoads; ++u) next[u] = x.vec(skip ? x.full : v0 + u * 32);
+    if (edge && x.edge(lane) >= 0) {
+      next_at = x.edge(lane);
+      const uint32_t w = __float_as_uint(x.at(next_at));
+      next[0].q.x = kBf16 ? w >> 16 | 0xFF800000u : w;
+    }
   };
   load(warp);
   for (int u0 = 0; u0 < units; u0 += kWarps) {
-    const int unit = u0 + warp;
     Vec<kBf16> q[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) q[u] = next[u];
-    load(unit + kWarps);
-    if (unit < units) {
-      const int v0 = sm.list[unit / per_seg] * steps * kSegVecs + unit % per_seg * kUnitVecs;
+    const int at0 = next_at;
+    load(u0 + warp + kWarps);
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u)
+    for (int u = 0; u < kLoads; ++u)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float f = q[u].at(i);
-          const uint64_t key = key_of(f, (uint32_t)(v0 + u * 32 + lane) * kN - off + i);
-          if (f == f && key > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = key;
-        }
-    }
+      for (int i = 0; i < kN; ++i) {
+        const float f = q[u].at(i);
+        const uint64_t key = key_of(f, (uint32_t)(at0 + u * 32 * kN + i));
+        if (f == f && key > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = key;   // not NaN
+      }
     __syncthreads();
     const int n = sm.n_pool;
     if (u0 + kWarps >= units) return settle(sm, n, k);
     __syncthreads();
-    if (n > kMaxTop) {
-      // the pool has room for one more step beside the best k
+    if (n > kKeep) {
+      // the pool has room for one more step beside these
       have = settle(sm, n, k);
       if (tid < have) sm.pool[tid] = sm.best[tid];
       if (tid == 0) sm.n_pool = have;
@@ -279,8 +302,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   constexpr int kN = Vec<kBf16>::kN;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
-  const uint8_t* x = static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.ld * (kBf16 ? 2 : 4);
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / (kBf16 ? 2 : 4));
+  const Row<kBf16> x(static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.ld * (kBf16 ? 2 : 4), a.V);
   const float c = a.scale * kLog2e;
   const int k = a.top_k;
 
@@ -288,16 +310,9 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   const int wid = rank * kWarps + warp, warps = cluster * kWarps;
   Vec<kBf16> next[kAhead];
   auto load = [&](int seg, int step) {
-    const int64_t e = ((int64_t)seg * steps + step) * kSegVecs * kN - off;    // the step's first element
-    if (seg < segs && e >= 0 && e + kSegVecs * kN <= a.V) {
-      const uint8_t* p = x + e * (kBf16 ? 2 : 4) + lane * 16;
+    const int v0 = seg < segs ? (seg * steps + step) * kSegVecs + lane : x.full;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) next[u].q = ldg128_stream(p + u * 512);
-    } else {
-      const int v0 = seg < segs ? (seg * steps + step) * kSegVecs : INT_MAX / kN;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) next[u] = load_vec<kBf16>(x, off, v0 + u * 32 + lane, a.V);
-    }
+    for (int u = 0; u < kAhead; ++u) next[u] = x.vec(v0 + u * 32);
   };
   load(wid, 0);
   // the tokens' logits, long before they are needed
@@ -305,13 +320,18 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   float token_x = 0.f;
   if (rank == 0 && tid < a.G) {
     token = a.tokens[(int64_t)row * a.ld_tokens + tid];
-    if (token >= 0 && token < a.V) token_x = load_one<kBf16>(x, token);
+    if (token >= 0 && token < a.V) token_x = x.at(token);
   }
-  umma::cluster_sync();   // every block of the cluster runs, so that the first one's shared memory can be written
+  // the edge, by the last warp: it has the fewest segments
+  float edge_x = -INFINITY;
+  const bool edge_warp = wid == warps - 1;
+  if (edge_warp && x.edge(lane) >= 0) edge_x = x.at(x.edge(lane));
+  block_sync(cluster);   // every block of the cluster runs, so that the first one's shared memory can be written
   const uint32_t first_stats = umma::mapa_shared(umma::smem_u32(&sm.stats[wid]), 0);
   const uint32_t first_segs = umma::mapa_shared(umma::smem_u32(sm.seg_max), 0);
 
   Stats st = {-FLT_MAX, 0.f, 0.f, 0.f};   // m is the warp's, n, r and w the lane's
+  uint64_t key = 0;                        // of the warp's largest logit, where one alternative is asked for
   for (int seg = wid; seg < segs; seg += warps) {
     uint32_t seg_order = 0;
     for (int step = 0; step < steps; ++step) {
@@ -330,10 +350,17 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
       const float m = value_of(order);
       if (m >= st.m) {
         // a new maximum (or the same again): its own terms are counted apart
-        if (m > st.m) {
-          const float t = fmaxf((st.m - m) * c, -1e30f), f = exp2_fast(t), s = st.n + st.r;
-          st = {m, 0.f, s * f, f > 0.f ? f * fmaf(t, s, st.w) : 0.f};
+        if (k == 1 && (m > st.m || key == 0)) {
+          uint32_t at = 0xFFFFFFFFu;
+          const uint32_t first = x.head + ((seg * steps + step) * kSegVecs + lane) * kN;
+#pragma unroll
+          for (int u = kAhead - 1; u >= 0; --u)
+#pragma unroll
+            for (int i = kN - 1; i >= 0; --i)
+              if (q[u].at(i) == m) at = first + u * 32 * kN + i;
+          key = (uint64_t)order << 32 | (0xFFFFFFFFu - __reduce_min_sync(0xffffffffu, at));
         }
+        if (m > st.m) st = raise_to(st, m, c);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
 #pragma unroll
@@ -364,8 +391,21 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
         st.w = lo + hi;
       }
     }
-    if (lane == 0 && k > 0)
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_segs + 4u * seg), "r"(seg_order) : "memory");
+    if (lane == 0 && k > 1) put_u32(first_segs + 4u * seg, seg_order);
+  }
+  if (edge_warp) {
+    const uint32_t order = __reduce_max_sync(0xffffffffu, order_of(fmaxf(edge_x, -INFINITY)));   // NaN: -infinity
+    if (lane == 0 && k > 1) put_u32(first_segs + 4u * segs, order);
+    const float m = value_of(order);
+    if (k == 1 && order > kOrderMinusInf) {
+      const uint32_t at = edge_x == m ? (uint32_t)x.edge(lane) : 0xFFFFFFFFu;
+      key = max(key, (uint64_t)order << 32 | (0xFFFFFFFFu - __reduce_min_sync(0xffffffffu, at)));
+    }
+    if (m > st.m) st = raise_to(st, m, c);
+    const float t = (edge_x - st.m) * c, e = exp2_fast(t);
+    if (t < 0.f) st.r += e;
+    else st.n += e;
+    st.w = fmaf(fmaxf(t, -1e30f), e, st.w);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -377,7 +417,11 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(first_stats), "f"(st.m), "f"(st.n), "f"(st.r),
                  "f"(st.w)
                  : "memory");
-  umma::cluster_sync();
+  if (lane == 0 && k == 1)
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(umma::mapa_shared(umma::smem_u32(&sm.warp_key[wid]), 0)),
+                 "l"(key)
+                 : "memory");
+  block_sync(cluster);
   if (rank != 0) return;
 
   if (warp == 0) {
@@ -390,6 +434,13 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
       st = join(st, b, c);
     }
     if (lane == 0) sm.row = st;
+    if (k == 1) {
+      key = 0;
+      for (int i = lane; i < warps; i += 32) key = max(key, sm.warp_key[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+      if (lane == 0) sm.best[0] = key;
+    }
   }
   __syncthreads();
   st = sm.row;
@@ -400,7 +451,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   for (int g = tid; g < a.G; g += kThreads) {
     if (g >= kThreads) {
       token = a.tokens[(int64_t)row * a.ld_tokens + g];
-      if (token >= 0 && token < a.V) token_x = load_one<kBf16>(x, token);
+      if (token >= 0 && token < a.V) token_x = x.at(token);
     }
     if (token < 0 || token >= a.V) {
       if (token != -1) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
@@ -409,7 +460,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
     a.logprobs[(int64_t)row * a.G + g] = sound ? (token_x - st.m) * a.scale - log_sum : NAN;
   }
   if (k == 0) return;
-  const int have = sound ? find_top<kBf16>(sm, x, off, a.V, k, segs, steps) : 0;
+  const int have = !sound ? 0 : k == 1 ? 1 : find_top<kBf16>(sm, x, k, segs, steps);
   if (tid < k) {
     int32_t id = -1;
     float l = sound ? -INFINITY : NAN;
@@ -448,16 +499,14 @@ cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps,
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
-  // Segments of a row that begins anywhere between two 16-byte boundaries.
-  const int n = a.bf16 ? 8 : 4;
-  const int64_t vecs = ((int64_t)a.V + 2 * n - 2) / n;
-  const int64_t least = (vecs + kSegVecs - 1) / kSegVecs;
+  const int64_t vecs = a.V / (a.bf16 ? 8 : 4);   // a row's, wherever it begins: no more than this
+  const int64_t least = std::max<int64_t>(1, (vecs + kSegVecs - 1) / kSegVecs);
   const int steps = (int)((least + kMaxSegs - 1) / kMaxSegs);
   const int segs = (int)((least + steps - 1) / steps);
-  // Blocks of a row: enough to fill the SMs twice when there are few rows, while
-  // each warp keeps a segment.
+  // Blocks of a row: as many as fit on the GPU at once (two per SM) when there are
+  // few rows, while each warp keeps a segment.
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)a.M * cluster < 2 * attn_sm_count() && segs >= 2 * cluster * kWarps)
+  while (cluster < kMaxCluster && (int64_t)a.M * 2 * cluster <= 2 * attn_sm_count() && segs >= 2 * cluster * kWarps)
     cluster *= 2;
   return a.bf16 ? launch_typed<true>(a, cluster, segs, steps, stream)
                 : launch_typed<false>(a, cluster, segs, steps, stream);
