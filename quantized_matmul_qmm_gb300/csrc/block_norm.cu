@@ -5,59 +5,47 @@
 // and int8 codes of out by the activation quantiser's rule (s = fl(amax / 127)).
 //
 // Bound: bytes.  Each value of residual, branch and gate is read once and each
-// of sum and out written once; a row stays in its block's registers from the
-// first load to the last store, through up to five reductions (two means, two
-// squares, one maximum), so that nothing is read again.
+// of sum and out written once; a row stays in its threads' registers from the first
+// load to the last store, through up to five reductions (two means, two squares,
+// one maximum), so that nothing is read again.
+//
+// A thread holds groups of four neighbouring values, so that a warp's accesses are
+// whole in every type (16 bytes a lane in fp32, 8 in bf16, 4 in int8), also where
+// rows begin at any element, as long as all tensors' rows do so alike.  Rows of
+// tensors that do not go value by value.
 #include <algorithm>
+#include <atomic>
 
 #include "beside.h"
+#include "kv_cache.h"
+#include "umma.cuh"
 
 namespace qmm {
 namespace {
 
-// Read once, and possibly written later by the same thread (sum may be the
-// residual itself): a coherent load that leaves L1 to the weights.
-QMM_DEV uint4 ld128_once(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-
-// Eight values of a row as they lie in memory.
+// Four values of a row as they lie in memory.  Read once, and possibly written
+// later by the same thread (sum may be the residual itself): coherent loads that
+// leave L1 to the weights.
 template <bool kBf16>
-struct Raw8 {
-  uint4 q[kBf16 ? 1 : 2];
-};
-template <bool kBf16>
-QMM_DEV Raw8<kBf16> load8(const void* base, int64_t elem) {
-  Raw8<kBf16> r;
-  const uint8_t* p = static_cast<const uint8_t*>(base) + elem * (kBf16 ? 2 : 4);
-  r.q[0] = ld128_once(p);
-  if constexpr (!kBf16) r.q[1] = ld128_once(p + 16);
-  return r;
-}
-template <bool kBf16>
-QMM_DEV float value8(const Raw8<kBf16>& r, int i) {
-  if constexpr (kBf16) {
-    const uint32_t w = u4_get(r.q[0], i / 2);
-    return i & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
-  } else {
-    return __uint_as_float(u4_get(r.q[i / 4], i % 4));
+struct Raw4 {
+  uint32_t w[kBf16 ? 2 : 4];
+  QMM_DEV float at(int i) const {
+    if constexpr (kBf16) return i & 1 ? bf16hi_to_f32(w[i / 2]) : bf16lo_to_f32(w[i / 2]);
+    else return __uint_as_float(w[i]);
   }
-}
+  QMM_DEV void load(const uint8_t* p) {
+    if constexpr (kBf16)
+      asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    else
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+  }
+};
 
 QMM_DEV uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Where a thread's values lie: kVec: groups of eight (group threadIdx.x + g *
-// blockDim.x), else single values (threadIdx.x + i * blockDim.x).
-template <bool kVec>
-QMM_DEV int place(int i) {
-  return kVec ? ((int)threadIdx.x + (i / 8) * (int)blockDim.x) * 8 + i % 8 : (int)threadIdx.x + i * (int)blockDim.x;
 }
 
 // Sum (or maximum) over a row's threads; every thread gets the result.  One
@@ -83,233 +71,354 @@ QMM_DEV float row_reduce(float v, float* slot) {
   return v;
 }
 
-// Eight (or single) fp32 values of a weight row that all blocks read: cached.
-template <bool kVec, int kE>
-QMM_DEV void load_row(const float* p, int D, float (&w)[kE]) {
-  if constexpr (kVec) {
+// int8 codes of four values by the activation quantiser's rule, as one word.
+// rint(fl(v / s)) without a division: y = fl(v * fl(1 / s)) is within 2^-23 |y| + 2^-24
+// |y| < 2.3e-5 of fl(v / s) (|y| <= 128, 1 / s neither overflowing nor subnormal), so
+// both round to the same integer unless y is that close to a half.  Adding 1.5 *
+// 2^23 rounds to the nearest even integer and leaves it in the low bits.  Values
+// near a half, and scales out of range, divide.
+QMM_DEV uint32_t codes4(const float* v, float s, float r) {
+  uint32_t q[4];
+  bool divide = !(s > 0x1p-100f && s < 0x1p100f);
 #pragma unroll
-    for (int i = 0; i < kE; i += 4)
-      if (place<kVec>(i) < D) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p + place<kVec>(i)));
-        w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+  for (int i = 0; i < 4; ++i) {
+    const float y = __fmul_rn(v[i], r), t = __fadd_rn(y, 12582912.f);
+    divide |= fabsf(y - __fsub_rn(t, 12582912.f)) > 0.4999f;
+    q[i] = __float_as_uint(t);
+  }
+  if (divide) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = s > 0.f ? (uint32_t)min(max(__float2int_rn(__fdiv_rn(v[i], s)), -127), 127) : 0u;
+  }
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+
+// How a row's groups lie.
+template <int kG, bool kOff>
+struct Place {
+  int e0;        // the first group's first element: a multiple of 4 less the row's offset
+  int step;      // from a thread's group to its next
+  int D;
+  QMM_DEV int at(int g) const { return e0 + g * step; }
+  QMM_DEV bool some(int g) const { return at(g) < D; }   // a group may begin before the row, but not end there
+  QMM_DEV bool whole(int g) const { return kOff ? at(g) >= 0 && at(g) + 4 <= D : at(g) < D; }
+  QMM_DEV bool in(int g, int i) const { return kOff ? at(g) + i >= 0 && at(g) + i < D : at(g) < D; }
+};
+
+// A row's values of one tensor, zeros outside it.
+template <bool kBf16, int kG, bool kOff>
+QMM_DEV void load_row(const void* base, int64_t row, const Place<kG, kOff>& pl, Raw4<kBf16> (&raw)[kG]) {
+  constexpr int kSize = kBf16 ? 2 : 4;
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    raw[g] = {};
+    const uint8_t* p = static_cast<const uint8_t*>(base) + (row + pl.at(g)) * kSize;
+    if (pl.whole(g)) {
+      raw[g].load(p);
+    } else if (kOff && pl.some(g)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!pl.in(g, i)) continue;
+        if constexpr (kBf16) raw[g].w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (i % 2 * 16);
+        else raw[g].w[i] = reinterpret_cast<const uint32_t*>(p)[i];
       }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (place<kVec>(i) < D) w[i] = __ldg(p + place<kVec>(i));
+    }
   }
 }
 
-template <bool kVec, int kE>
-QMM_DEV void apply_norm(const NormSpec& n, int D, float (&v)[kE], float (*slots)[32]) {
+// Four fp32 weights from element e0, cached for all rows.  Where rows begin at any
+// element, two aligned loads and a shift that is the same for the whole row.
+template <int kG, bool kOff>
+QMM_DEV void weights4(const float* w, const Place<kG, kOff>& pl, int g, bool aligned16, float (&x)[4]) {
+  const int e = pl.at(g);
+  if (!kOff && aligned16) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + e));
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  } else if (kOff && aligned16 && e >= 4 && e + 8 <= pl.D) {
+    const float4* p = reinterpret_cast<const float4*>(w + (e & ~3));
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    switch (e & 3) {
+      case 0: x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w; break;
+      case 1: x[0] = a.y, x[1] = a.z, x[2] = a.w, x[3] = b.x; break;
+      case 2: x[0] = a.z, x[1] = a.w, x[2] = b.x, x[3] = b.y; break;
+      default: x[0] = a.w, x[1] = b.x, x[2] = b.y, x[3] = b.z;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pl.in(g, i) ? __ldg(w + e + i) : 0.f;
+  }
+}
+
+// With one group a thread asks for its weights before the reductions: a single
+// row would wait for them after each.
+template <int kG, bool kOff>
+QMM_DEV void apply_norm(const NormSpec& n, const Place<kG, kOff>& pl, bool aligned16, float (&v)[4 * kG],
+                        const float (&ahead)[2][4], float (*slots)[32]) {
   if (n.kind == QMM_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) s += v[i];   // values past D are zeros
-    const float mean = row_reduce<false>(s, slots[0]) / (float)D;
+    for (int i = 0; i < 4 * kG; ++i) s += v[i];   // values outside the row are zeros
+    const float mean = row_reduce<false>(s, slots[0]) / (float)pl.D;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] = place<kVec>(i) < D ? v[i] - mean : 0.f;
+    for (int i = 0; i < 4 * kG; ++i) v[i] = pl.in(i / 4, i % 4) ? v[i] - mean : 0.f;
   }
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < kE; ++i) ss = fmaf(v[i], v[i], ss);
-  const float inv = rsqrtf(row_reduce<false>(ss, slots[1]) / (float)D + n.eps);
-  if (n.weight != nullptr) {
-    float w[kE];
-    load_row<kVec>(n.weight, D, w);
+  for (int i = 0; i < 4 * kG; ++i) ss = fmaf(v[i], v[i], ss);
+  const float inv = rsqrtf(row_reduce<false>(ss, slots[1]) / (float)pl.D + n.eps);
 #pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (place<kVec>(i) < D) v[i] = v[i] * inv * w[i];
-  } else {
+  for (int g = 0; g < kG; ++g) {
+    if (!pl.some(g)) continue;
+    float x[4];
+    if (n.weight != nullptr) {
+      if constexpr (kG > 1) weights4(n.weight, pl, g, aligned16, x);
 #pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] *= inv;
-  }
-  if (n.bias != nullptr) {
-    float w[kE];
-    load_row<kVec>(n.bias, D, w);
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (place<kVec>(i) < D) v[i] += w[i];
-  }
-}
-
-// A row's values of one tensor, zeros past D.
-template <bool kVec, bool kBf16, int kE>
-struct RowLoad {
-  Raw8<kBf16> raw[kVec ? kE / 8 : 1];
-  float one[kVec ? 1 : kE];
-  QMM_DEV void issue(const void* base, int64_t row, int D) {
-    if constexpr (kVec) {
-#pragma unroll
-      for (int i = 0; i < kE; i += 8) {
-        raw[i / 8] = {};
-        if (place<kVec>(i) < D) raw[i / 8] = load8<kBf16>(base, row + place<kVec>(i));
-      }
+      for (int i = 0; i < 4; ++i) v[4 * g + i] = v[4 * g + i] * inv * (kG > 1 ? x[i] : ahead[0][i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        one[i] = 0.f;
-        const int64_t at = row + place<kVec>(i);
-        if (place<kVec>(i) < D)
-          one[i] = kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at])
-                         : static_cast<const float*>(base)[at];
-      }
+      for (int i = 0; i < 4; ++i) v[4 * g + i] *= inv;
     }
-  }
-  QMM_DEV float at(int i) const {
-    if constexpr (kVec) return value8<kBf16>(raw[i / 8], i % 8);
-    return one[i];
-  }
-};
-
-template <bool kVec, int kE>
-QMM_DEV void store_row(void* base, bool bf16, int64_t row, int D, const float (&v)[kE]) {
-  if constexpr (kVec) {
+    if (n.bias != nullptr) {
+      if constexpr (kG > 1) weights4(n.bias, pl, g, aligned16, x);
 #pragma unroll
-    for (int i = 0; i < kE; i += 8) {
-      if (place<kVec>(i) >= D) continue;
-      const int64_t at = row + place<kVec>(i);
-      if (bf16) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) =
-            make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
-                       pack_bf16(v[i + 6], v[i + 7]));
-      } else {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        p[0] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        p[1] = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      if (place<kVec>(i) >= D) continue;
-      const int64_t at = row + place<kVec>(i);
-      if (bf16) static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v[i]);
-      else static_cast<float*>(base)[at] = v[i];
+      for (int i = 0; i < 4; ++i) v[4 * g + i] += kG > 1 ? x[i] : ahead[1][i];
     }
   }
 }
 
-// kE values of a row per thread; blockDim.y rows per block (more than one only
-// where a row has one warp, which needs no barrier).
-template <bool kVec, int kE, bool kResBf16, bool kBrBf16>
+template <int kG, bool kOff>
+QMM_DEV void store_row(void* base, bool bf16, int64_t row, const Place<kG, kOff>& pl, const float (&v)[4 * kG]) {
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    const int64_t at = row + pl.at(g);
+    const float* x = v + 4 * g;
+    if (pl.whole(g)) {
+      if (bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + at) =
+            make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if (kOff && pl.some(g)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!pl.in(g, i)) continue;
+        if (bf16) static_cast<__nv_bfloat16*>(base)[at + i] = __float2bfloat16_rn(x[i]);
+        else static_cast<float*>(base)[at + i] = x[i];
+      }
+    }
+  }
+}
+
+// A row per blockDim.x threads, kG groups of four values each; blockDim.y rows per
+// block (more than one only where a row has one warp, which needs no barrier).
+// kOff: rows begin at any element, row t (t * off_step) % 4 behind a boundary.
+template <bool kResBf16, bool kBrBf16, int kG, bool kOff>
 __global__ void __launch_bounds__(1024)
-block_norm_kernel(NormArgs a) {
+block_norm_kernel(NormArgs a, int off_step, bool weights16) {
   __shared__ float slots[5][32];
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.T) return;   // whole warps, and only where no barrier follows
-  const int D = a.D;
-  float v[kE];
+  const int off = kOff ? (int)(t * off_step & 3) : 0;
+  const Place<kG, kOff> pl{(int)threadIdx.x * 4 - off, (int)blockDim.x * 4, a.D};
+  float v[4 * kG];
+  float post_ahead[2][4] = {}, pre_ahead[2][4] = {};
+  auto ask = [&](const NormSpec& n, float (&to)[2][4]) {
+    if (kG > 1 || !pl.some(0)) return;
+    if (n.weight != nullptr) weights4(n.weight, pl, 0, weights16, to[0]);
+    if (n.bias != nullptr) weights4(n.bias, pl, 0, weights16, to[1]);
+  };
   {
-    RowLoad<kVec, kResBf16, kE> res;
-    res.issue(a.residual, t * a.ldr, D);
+    Raw4<kResBf16> res[kG];
     if (a.branch != nullptr) {
-      RowLoad<kVec, kBrBf16, kE> br;
-      br.issue(a.branch, t * a.ldb, D);
+      Raw4<kBrBf16> br[kG];
+      load_row(a.branch, t * a.ldb, pl, br);
+      load_row(a.residual, t * a.ldr, pl, res);
+      ask(a.post, post_ahead);
+      ask(a.pre, pre_ahead);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = br.at(i);
-      if (a.post.kind != 0) apply_norm<kVec>(a.post, D, v, slots);
+      for (int i = 0; i < 4 * kG; ++i) v[i] = br[i / 4].at(i % 4);
+      if (a.post.kind != 0) apply_norm(a.post, pl, weights16, v, post_ahead, slots);
       if (a.gate != nullptr) {
-        if (a.gate_bf16) {
-          RowLoad<kVec, true, kE> g;
-          g.issue(a.gate, t * a.ldg, D);
+        if (a.ldg == 0 && !a.gate_bf16) {
 #pragma unroll
-          for (int i = 0; i < kE; ++i) v[i] *= g.at(i);
+          for (int g = 0; g < kG; ++g) {
+            if (!pl.some(g)) continue;
+            float x[4];
+            weights4(static_cast<const float*>(a.gate), pl, g, weights16, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * g + i] *= x[i];
+          }
+        } else if (a.gate_bf16) {
+          Raw4<true> x[kG];
+          load_row(a.gate, t * a.ldg, pl, x);
+#pragma unroll
+          for (int i = 0; i < 4 * kG; ++i) v[i] *= x[i / 4].at(i % 4);
         } else {
-          RowLoad<kVec, false, kE> g;
-          g.issue(a.gate, t * a.ldg, D);
+          Raw4<false> x[kG];
+          load_row(a.gate, t * a.ldg, pl, x);
 #pragma unroll
-          for (int i = 0; i < kE; ++i) v[i] *= g.at(i);
+          for (int i = 0; i < 4 * kG; ++i) v[i] *= x[i / 4].at(i % 4);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = place<kVec>(i) < D ? fmaf(a.scale, v[i], res.at(i)) : 0.f;
+      for (int i = 0; i < 4 * kG; ++i)
+        v[i] = pl.in(i / 4, i % 4) ? fmaf(a.scale, v[i], res[i / 4].at(i % 4)) : 0.f;
     } else {
+      load_row(a.residual, t * a.ldr, pl, res);
+      ask(a.pre, pre_ahead);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = res.at(i);
+      for (int i = 0; i < 4 * kG; ++i) v[i] = res[i / 4].at(i % 4);
     }
   }
-  if (a.sum != nullptr) store_row<kVec>(a.sum, kResBf16, t * a.lds, D, v);
+  if (a.sum != nullptr) store_row(a.sum, kResBf16, t * a.lds, pl, v);
   if (a.out == nullptr) return;
-  if (a.pre.kind != 0) apply_norm<kVec>(a.pre, D, v, slots + 2);
+  if (a.pre.kind != 0) apply_norm(a.pre, pl, weights16, v, pre_ahead, slots + 2);
   if (a.out_type != QMM_S8) {
-    store_row<kVec>(a.out, a.out_type == QMM_BF16, t * a.ldo, D, v);
+    store_row(a.out, a.out_type == QMM_BF16, t * a.ldo, pl, v);
     return;
   }
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < kE; ++i)
-    if (place<kVec>(i) < D) amax = fmaxf(amax, fabsf(v[i]));
+  for (int i = 0; i < 4 * kG; ++i)
+    if (pl.in(i / 4, i % 4)) amax = fmaxf(amax, fabsf(v[i]));
+  const float s = __fdiv_rn(row_reduce<true>(amax, slots[4]), 127.0f), r = __frcp_rn(s);
+  if (threadIdx.x == 0) a.s_x[t] = s;
+  int8_t* codes = static_cast<int8_t*>(a.out) + t * a.ldo;
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    if (!pl.some(g)) continue;
+    const uint32_t q = codes4(v + 4 * g, s, r);
+    if (!kOff) {
+      *reinterpret_cast<uint32_t*>(codes + pl.at(g)) = q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pl.in(g, i)) codes[pl.at(g) + i] = (int8_t)(q >> (8 * i));
+    }
+  }
+}
+
+// Tensors whose rows begin each at another place: a block per row, value by value
+// (values of a thread are blockDim.x apart), the row's fp32 values in shared memory.
+__global__ void __launch_bounds__(1024)
+block_norm_any_kernel(NormArgs a) {
+  extern __shared__ float row[];
+  __shared__ float slots[5][32];
+  const int64_t t = blockIdx.x;
+  const int D = a.D, first = threadIdx.x, step = blockDim.x;
+  auto value = [](const void* p, bool bf16, int64_t i) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+  };
+  auto put = [](void* p, bool bf16, int64_t i, float v) {
+    if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<float*>(p)[i] = v;
+  };
+  // each thread reads back only what it wrote
+  auto norm = [&](const NormSpec& n, float (*slot)[32]) {
+    float mean = 0.f;
+    if (n.kind == QMM_NORM_LAYER) {
+      float s = 0.f;
+      for (int e = first; e < D; e += step) s += row[e];
+      mean = row_reduce<false>(s, slot[0]) / (float)D;
+    }
+    float ss = 0.f;
+    for (int e = first; e < D; e += step) ss = fmaf(row[e] - mean, row[e] - mean, ss);
+    const float inv = rsqrtf(row_reduce<false>(ss, slot[1]) / (float)D + n.eps);
+    for (int e = first; e < D; e += step) {
+      float v = (row[e] - mean) * inv;
+      if (n.weight != nullptr) v *= n.weight[e];
+      if (n.bias != nullptr) v += n.bias[e];
+      row[e] = v;
+    }
+  };
+  if (a.branch != nullptr) {
+    for (int e = first; e < D; e += step) row[e] = value(a.branch, a.branch_bf16, t * a.ldb + e);
+    if (a.post.kind != 0) norm(a.post, slots);
+    for (int e = first; e < D; e += step) {
+      float u = row[e];
+      if (a.gate != nullptr) u *= value(a.gate, a.gate_bf16, t * a.ldg + e);
+      row[e] = fmaf(a.scale, u, value(a.residual, a.residual_bf16, t * a.ldr + e));
+    }
+  } else {
+    for (int e = first; e < D; e += step) row[e] = value(a.residual, a.residual_bf16, t * a.ldr + e);
+  }
+  if (a.sum != nullptr)
+    for (int e = first; e < D; e += step) put(a.sum, a.residual_bf16, t * a.lds + e, row[e]);
+  if (a.out == nullptr) return;
+  if (a.pre.kind != 0) norm(a.pre, slots + 2);
+  if (a.out_type != QMM_S8) {
+    for (int e = first; e < D; e += step) put(a.out, a.out_type == QMM_BF16, t * a.ldo + e, row[e]);
+    return;
+  }
+  float amax = 0.f;
+  for (int e = first; e < D; e += step) amax = fmaxf(amax, fabsf(row[e]));
   const float s = __fdiv_rn(row_reduce<true>(amax, slots[4]), 127.0f);
   if (threadIdx.x == 0) a.s_x[t] = s;
   int8_t* codes = static_cast<int8_t*>(a.out) + t * a.ldo;
-  uint32_t q[kE];
-#pragma unroll
-  for (int i = 0; i < kE; ++i)
-    q[i] = s > 0.f ? (uint32_t)min(max(__float2int_rn(__fdiv_rn(v[i], s)), -127), 127) & 0xFFu : 0u;
-  if constexpr (kVec) {
-#pragma unroll
-    for (int i = 0; i < kE; i += 8)
-      if (place<kVec>(i) < D)
-        *reinterpret_cast<uint2*>(codes + place<kVec>(i)) =
-            make_uint2(q[i] | q[i + 1] << 8 | q[i + 2] << 16 | q[i + 3] << 24,
-                       q[i + 4] | q[i + 5] << 8 | q[i + 6] << 16 | q[i + 7] << 24);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (place<kVec>(i) < D) codes[place<kVec>(i)] = (int8_t)q[i];
-  }
+  for (int e = first; e < D; e += step)
+    codes[e] = (int8_t)(s > 0.f ? min(max(__float2int_rn(__fdiv_rn(row[e], s)), -127), 127) : 0);
 }
 
-template <bool kVec, int kE>
-cudaError_t launch_typed(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t stream) {
-  if (a.residual_bf16) {
-    if (a.branch_bf16) block_norm_kernel<kVec, kE, true, true><<<grid, block, 0, stream>>>(a);
-    else block_norm_kernel<kVec, kE, true, false><<<grid, block, 0, stream>>>(a);
-  } else {
-    if (a.branch_bf16) block_norm_kernel<kVec, kE, false, true><<<grid, block, 0, stream>>>(a);
-    else block_norm_kernel<kVec, kE, false, false><<<grid, block, 0, stream>>>(a);
-  }
+template <int kG>
+cudaError_t launch_groups(const NormArgs& a, bool even, int off_step, bool weights16, int groups,
+                          cudaStream_t stream) {
+  void (*kern[8])(NormArgs, int, bool) = {
+      block_norm_kernel<false, false, kG, false>, block_norm_kernel<false, true, kG, false>,
+      block_norm_kernel<true, false, kG, false>, block_norm_kernel<true, true, kG, false>,
+      block_norm_kernel<false, false, kG, true>, block_norm_kernel<false, true, kG, true>,
+      block_norm_kernel<true, false, kG, true>, block_norm_kernel<true, true, kG, true>};
+  const int nt = (groups + 32 * kG - 1) / (32 * kG) * 32;
+  const dim3 block(nt, nt == 32 ? 4 : 1);
+  const dim3 grid((unsigned)((a.T + block.y - 1) / block.y));
+  kern[(even ? 0 : 4) + (a.residual_bf16 ? 2 : 0) + (a.branch_bf16 ? 1 : 0)]<<<grid, block, 0, stream>>>(
+      a, off_step, weights16);
   return cudaGetLastError();
 }
 
-// Whether rows of `size`-byte elements all begin on 16 bytes.
-bool rows16(const void* p, int64_t ld, int size) { return p == nullptr || (aligned(p, 16) && ld * size % 16 == 0); }
+// Whether a tensor's rows begin where those of stride `ld0` do, between two
+// boundaries of four elements (of `size` bytes).
+bool in_step(const void* p, int64_t ld, int64_t ld0, int size) {
+  return p == nullptr || (aligned(p, 4 * size) && (ld - ld0) % 4 == 0);
+}
 
 }  // namespace
 
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
-  const bool vec = a.D % 8 == 0 && rows16(a.residual, a.ldr, a.residual_bf16 ? 2 : 4) &&
-                   rows16(a.branch, a.ldb, a.branch_bf16 ? 2 : 4) && rows16(a.gate, a.ldg, a.gate_bf16 ? 2 : 4) &&
-                   rows16(a.sum, a.lds, a.residual_bf16 ? 2 : 4) &&
-                   rows16(a.out, a.ldo, a.out_type == QMM_F32 ? 4 : a.out_type == QMM_BF16 ? 2 : 1) &&
-                   aligned(a.post.weight, 16) && aligned(a.post.bias, 16) && aligned(a.pre.weight, 16) &&
-                   aligned(a.pre.bias, 16);
-  const int units = vec ? a.D / 8 : a.D;                  // groups or values of a row
-  auto shape = [&](int per_thread, dim3& grid, dim3& block) {
-    const int nt = std::min(1024, (units + 32 * per_thread - 1) / (32 * per_thread) * 32);
-    block = dim3(nt, nt == 32 ? 4 : 1);
-    grid = dim3((unsigned)((a.T + block.y - 1) / block.y));
-  };
-  dim3 grid, block;
-  if (!vec) {
-    if (units <= 8 * 1024) {
-      shape(8, grid, block);
-      return launch_typed<false, 8>(a, grid, block, stream);
-    }
-    shape(32, grid, block);
-    return launch_typed<false, 32>(a, grid, block, stream);
+  const int res_size = a.residual_bf16 ? 2 : 4;
+  const int64_t ld0 = a.ldr;
+  // the row-by-row gate keeps step with the rest; one row for all is read like a weight in fp32
+  const bool gate_row = a.gate != nullptr && a.ldg != 0;
+  const bool even = a.D % 4 == 0 && ld0 % 4 == 0;
+  bool together = in_step(a.residual, a.ldr, ld0, res_size) && in_step(a.sum, a.lds, ld0, res_size) &&
+                  in_step(a.branch, a.ldb, ld0, a.branch_bf16 ? 2 : 4) &&
+                  (!gate_row || in_step(a.gate, a.ldg, ld0, a.gate_bf16 ? 2 : 4)) &&
+                  (a.out_type == QMM_S8 || in_step(a.out, a.ldo, ld0, a.out_type == QMM_BF16 ? 2 : 4));
+  // a bf16 row for all tokens has to begin with the rows
+  if (a.gate != nullptr && !gate_row && a.gate_bf16) together = together && even && aligned(a.gate, 8);
+  const int groups = (a.D + (even ? 0 : 3) + 3) / 4;
+  if (!together || groups > 4096) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t err = set_once(done, reinterpret_cast<const void*>(block_norm_any_kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormMaxD * 4);
+    if (err != cudaSuccess) return err;
+    const int nt = std::min(1024, (a.D + 127) / 128 * 32);
+    block_norm_any_kernel<<<a.T, nt, (size_t)a.D * 4, stream>>>(a);
+    return cudaGetLastError();
   }
-  if (a.T <= 304 && units <= 1024) {
-    shape(1, grid, block);
-    return launch_typed<true, 8>(a, grid, block, stream);
-  }
-  if (units <= 2048) {
-    shape(2, grid, block);
-    return launch_typed<true, 16>(a, grid, block, stream);
-  }
-  shape(4, grid, block);
-  return launch_typed<true, 32>(a, grid, block, stream);
+  const bool weights16 = aligned(a.post.weight, 16) && aligned(a.post.bias, 16) && aligned(a.pre.weight, 16) &&
+                         aligned(a.pre.bias, 16) && (gate_row || aligned(a.gate, 16));
+  const int off_step = (int)(ld0 % 4);
+  // Few rows: a row's latency counts, so four values a thread, as long as two rounds
+  // of the GPU's threads hold them all (2000 rows of 1024: 8.8 us, with 16 values 10.0).
+  // Many: 16, which leaves several rows on an SM at different stages and few warps
+  // to a reduction (16384 rows of 4096 146 us, with eight values 184, with 32
+  // 182); eight where 16 would leave a row one warp (16384 of 512 22.7, with 16 24.4).
+  const int64_t threads = (int64_t)a.T * ((groups + 31) / 32 * 32);
+  if (groups <= 1024 && threads <= (int64_t)2 * 2048 * attn_sm_count())
+    return launch_groups<1>(a, even, off_step, weights16, groups, stream);
+  if (groups <= 128) return launch_groups<2>(a, even, off_step, weights16, groups, stream);
+  return launch_groups<4>(a, even, off_step, weights16, groups, stream);
 }
 
 }  // namespace qmm

@@ -683,37 +683,35 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 _NORM_KINDS = {"rms": 1, "layer": 2}
 _OUT_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16, torch.int8: QMM_S8}
 _F32, _BF16 = torch.float32, torch.bfloat16
+_current_device = getattr(torch._C, "_cuda_getDevice", None)   # None: torch without CUDA
+
+# Every tensor has to lie on the current GPU: an address of another device or of
+# the host would reach the kernel as it is.  The checks stand in few calls: a
+# decoding step waits for this code, not for the kernels.
 
 
-def _one_device(fn, first, *tensors):
-    """All tensors on one GPU, and that the current one: an address of another
-    device or of the host would reach the kernel as it is."""
-    dev = first.get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: tensors on different devices")
-    if dev != _current_device():
-        raise ValueError(f"{fn}: tensors have to be on the current CUDA device")
+def _device_of(fn, t):
+    dev = t.get_device()
+    if _current_device is None or dev != _current_device():
+        raise ValueError(f"{fn}: tensors have to be on the current CUDA device, got {t.device}")
     return dev
 
 
-def _current_device():
-    return torch.cuda.current_device()
-
-
-def _rows(fn, t, shape, types):
+def _rows(fn, dev, t, shape, types):
     """Row stride of a [rows][width] tensor with contiguous rows."""
-    if t.shape != shape or t.dtype not in types or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{fn}: expected {tuple(shape)} with contiguous rows of {[str(x) for x in types]}, "
-                         f"got {tuple(t.shape)} {t.dtype} with strides {t.stride()}")
+    if t.shape != shape or t.dtype not in types or t.get_device() != dev or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{fn}: expected {tuple(shape)} with contiguous rows of {[str(x) for x in types]} on device "
+                         f"{dev}, got {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
     return t.stride(0)
 
 
-def _vector(fn, t, size, dtype):
+def _vector(fn, dev, t, size, dtype):
+    """Address of `size` contiguous values, or None."""
     if t is None:
         return None
-    if t.numel() != size or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{fn}: expected {size} contiguous values of {dtype}")
+    if t.numel() != size or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{fn}: expected {size} contiguous values of {dtype} on device {dev}, got {tuple(t.shape)} "
+                         f"{t.dtype} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
@@ -732,45 +730,47 @@ def block_norm(residual: torch.Tensor, branch=None, *, norm="rms", weight=None, 
     "s8", the last with row scales s_x fp32 [T], made when not given (out=False:
     the sum alone).  Returns (sum, out), or (sum, out, s_x) for "s8"."""
     fn = "block_norm"
+    dev = _device_of(fn, residual)
     shape = residual.shape
     T, D = shape
-    dev = _one_device(fn, residual, branch, weight, bias, branch_weight, branch_bias, gate, residual_out,
-                      None if out is False else out, s_x)
-    ldr = _rows(fn, residual, shape, (_F32, _BF16))
+    ldr = _rows(fn, dev, residual, shape, _ROW_TYPES)
+    r_type = _ROW_TYPES[residual.dtype]
     ldb = ldg = lds = ldo = 0
     p_branch = p_gate = p_sum = p_out = n_branch = n_out = None
     b_type = g_type = QMM_F32
     o_type = QMM_BF16
     if branch is not None:
-        ldb, p_branch, b_type = _rows(fn, branch, shape, (_F32, _BF16)), branch.data_ptr(), _ROW_TYPES[branch.dtype]
+        ldb, p_branch, b_type = _rows(fn, dev, branch, shape, _ROW_TYPES), branch.data_ptr(), _ROW_TYPES[branch.dtype]
         if branch_norm is not None:
             n_branch = QmmNorm(_NORM_KINDS[branch_norm], eps if branch_eps is None else branch_eps,
-                               _vector(fn, branch_weight, D, _F32), _vector(fn, branch_bias, D, _F32))
+                               _vector(fn, dev, branch_weight, D, _F32), _vector(fn, dev, branch_bias, D, _F32))
         if gate is not None:
             if gate.dim() == 1:
-                gate = gate.unsqueeze(0)
-                _rows(fn, gate, (1, D), (_F32, _BF16))
+                _rows(fn, dev, gate.unsqueeze(0), (1, D), _ROW_TYPES)
             else:
-                ldg = _rows(fn, gate, shape, (_F32, _BF16))
+                ldg = _rows(fn, dev, gate, shape, _ROW_TYPES)
             p_gate, g_type = gate.data_ptr(), _ROW_TYPES[gate.dtype]
         if residual_out is None:
             residual_out = residual
     if residual_out is not None:
-        lds, p_sum = _rows(fn, residual_out, shape, (residual.dtype,)), residual_out.data_ptr()
+        lds, p_sum = _rows(fn, dev, residual_out, shape, (residual.dtype,)), residual_out.data_ptr()
+    p_sx = None
     if out is not False:
         if out is None:
             if out_type == "s8":       # rows of whole 16 bytes, as the int8 GEMM takes them
                 out = torch.empty((T, (D + 15) // 16 * 16), dtype=torch.int8, device=residual.device)[:, :D]
             else:
                 out = torch.empty(shape, dtype=_BF16 if out_type == "bf16" else _F32, device=residual.device)
-        ldo, p_out, o_type = _rows(fn, out, shape, tuple(_OUT_TYPES)), out.data_ptr(), _OUT_TYPES[out.dtype]
-        if o_type == QMM_S8 and s_x is None:
-            s_x = torch.empty(T, dtype=_F32, device=residual.device)
+        ldo, p_out, o_type = _rows(fn, dev, out, shape, _OUT_TYPES), out.data_ptr(), _OUT_TYPES[out.dtype]
+        if o_type == QMM_S8:
+            if s_x is None:
+                s_x = torch.empty(T, dtype=_F32, device=residual.device)
+            p_sx = _vector(fn, dev, s_x, T, _F32)
         if norm is not None:
-            n_out = QmmNorm(_NORM_KINDS[norm], eps, _vector(fn, weight, D, _F32), _vector(fn, bias, D, _F32))
+            n_out = QmmNorm(_NORM_KINDS[norm], eps, _vector(fn, dev, weight, D, _F32), _vector(fn, dev, bias, D, _F32))
     status = lib.qmm_block_norm(
-        residual.data_ptr(), _ROW_TYPES[residual.dtype], ldr, p_branch, b_type, ldb, n_branch, p_gate, g_type, ldg,
-        scale, p_sum, lds, n_out, p_out, o_type, ldo, _vector(fn, s_x, T, _F32), T, D, _raw_stream(dev))
+        residual.data_ptr(), r_type, ldr, p_branch, b_type, ldb, n_branch, p_gate, g_type, ldg, scale, p_sum, lds,
+        n_out, p_out, o_type, ldo, p_sx, T, D, _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_block_norm", status)
     total = residual if residual_out is None else residual_out
@@ -790,26 +790,33 @@ def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tenso
     fp32 [M][N] (or None for zeros).  out is made when not given; out=base adds in
     place.  Returns out."""
     fn = "lora_add"
-    dev = _one_device(fn, X, ids, A, B, base, out, ranks, scales, workspace, dev_status)
+    dev = _device_of(fn, X)
     M, K = shape = X.shape
+    ldx = _rows(fn, dev, X, shape, (_BF16,))
     slots, rank, k = A.shape
-    N = B.shape[1]
-    if k != K or B.shape != (slots, N, rank) or A.dtype is not _BF16 or B.dtype is not _BF16 \
-            or (A.stride(2) != 1 and K > 1) or (B.stride(2) != 1 and rank > 1):
+    b_slots, N, b_rank = B.shape
+    a_slot, a_row, a_in = A.stride()
+    b_slot, b_row, b_in = B.stride()
+    if k != K or b_slots != slots or b_rank != rank or A.dtype is not _BF16 or B.dtype is not _BF16 \
+            or (a_in != 1 and K > 1) or (b_in != 1 and rank > 1) or A.get_device() != dev or B.get_device() != dev:
         raise ValueError("lora_add: A has to be bf16 [adapters][rank][K], B bf16 [adapters][N][rank], with "
-                         "contiguous innermost values, for X [M][K]")
-    ldx = _rows(fn, X, shape, (_BF16,))
-    ldb = 0 if base is None else _rows(fn, base, (M, N), (_F32,))
+                         "contiguous innermost values, for X [M][K], all on one device")
+    out_shape = (M, N)
+    p_base, ldb = (None, 0) if base is None else (base.data_ptr(), _rows(fn, dev, base, out_shape, (_F32,)))
     if out is None:
-        out = torch.empty((M, N), dtype=_F32, device=X.device)
-    ldo = _rows(fn, out, (M, N), (_F32,))
-    p_ids = _vector(fn, ids, M, _I32)
-    weights = QmmLoraSet(A.data_ptr(), A.stride(0), A.stride(1), B.data_ptr(), B.stride(0), B.stride(1),
-                         _vector(fn, ranks, slots, _I32), _vector(fn, scales, slots, _F32), slots, rank, K, N)
+        out = torch.empty(out_shape, dtype=_F32, device=X.device)
+        ldo = N
+    else:
+        ldo = _rows(fn, dev, out, out_shape, (_F32,))
+    weights = QmmLoraSet(A.data_ptr(), a_slot, a_row, B.data_ptr(), b_slot, b_row,
+                         _vector(fn, dev, ranks, slots, _I32), _vector(fn, dev, scales, slots, _F32), slots, rank, K, N)
     if workspace is None:
         workspace = torch.empty(lora_add_workspace_size(M, K, N, slots, rank), dtype=torch.uint8, device=X.device)
-    status = lib.qmm_lora_add(weights, X.data_ptr(), ldx, p_ids, M, _addr(base), ldb, out.data_ptr(), ldo,
-                              workspace.data_ptr(), workspace.nbytes, _status_addr(fn, dev_status), _raw_stream(dev))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("lora_add: workspace has to be contiguous, on X's device")
+    status = lib.qmm_lora_add(
+        weights, X.data_ptr(), ldx, _vector(fn, dev, ids, M, _I32), M, p_base, ldb, out.data_ptr(), ldo,
+        workspace.data_ptr(), workspace.nbytes, _vector(fn, dev, dev_status, 1, _I32), _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_lora_add", status)
     return out
@@ -823,38 +830,47 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
     qmm_token_logprobs.  Returns (logprobs, entropy, top_ids, top_logprobs), None
     for what was not asked for."""
     fn = "token_logprobs"
-    dev = _one_device(fn, logits, tokens, logprobs, None if entropy is False else entropy, top_ids, top_logprobs,
-                      dev_status)
+    dev = _device_of(fn, logits)
     M, V = shape = logits.shape
-    ld, device = _rows(fn, logits, shape, (_F32, _BF16)), logits.device
+    ld = _rows(fn, dev, logits, shape, _ROW_TYPES)
     G = ldt = 0
     p_tokens = p_logprobs = p_ids = p_top = p_entropy = None
     if tokens is not None:
-        flat = tokens.dim() == 1
-        if flat:
-            tokens = tokens.unsqueeze(1)
-        G = tokens.shape[1]
-        ldt, p_tokens = _rows(fn, tokens, (M, G), (_I32,)), tokens.data_ptr()
+        t = tokens.unsqueeze(1) if tokens.dim() == 1 else tokens
+        G = t.shape[1]
+        ldt, p_tokens = _rows(fn, dev, t, (M, G), (_I32,)), tokens.data_ptr()
+    if tokens is not None:
         if logprobs is None:
-            logprobs = torch.empty(M if flat else (M, G), dtype=_F32, device=device)
-        p_logprobs = _vector(fn, logprobs, M * G, _F32)
-    if entropy is not False:
-        if entropy is None:
-            entropy = torch.empty(M, dtype=_F32, device=device)
-        p_entropy = _vector(fn, entropy, M, _F32)
+            logprobs = torch.empty(tokens.shape, dtype=_F32, device=logits.device)
+            p_logprobs = logprobs.data_ptr()
+        else:
+            p_logprobs = _vector(fn, dev, logprobs, M * G, _F32)
+    if entropy is False:
+        entropy = None
+    elif entropy is None:
+        entropy = torch.empty(M, dtype=_F32, device=logits.device)
+        p_entropy = entropy.data_ptr()
+    else:
+        p_entropy = _vector(fn, dev, entropy, M, _F32)
     if top_k > 0:
         if top_ids is None:
-            top_ids = torch.empty((M, top_k), dtype=_I32, device=device)
+            top_ids = torch.empty((M, top_k), dtype=_I32, device=logits.device)
+            p_ids = top_ids.data_ptr()
+        else:
+            p_ids = _vector(fn, dev, top_ids, M * top_k, _I32)
         if top_logprobs is None:
-            top_logprobs = torch.empty((M, top_k), dtype=_F32, device=device)
-        p_ids, p_top = _vector(fn, top_ids, M * top_k, _I32), _vector(fn, top_logprobs, M * top_k, _F32)
+            top_logprobs = torch.empty((M, top_k), dtype=_F32, device=logits.device)
+            p_top = top_logprobs.data_ptr()
+        else:
+            p_top = _vector(fn, dev, top_logprobs, M * top_k, _F32)
+    else:
+        top_ids = top_logprobs = None
     status = lib.qmm_token_logprobs(
         logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy, top_k,
-        p_ids, p_top, _status_addr(fn, dev_status), _raw_stream(dev))
+        p_ids, p_top, _vector(fn, dev, dev_status, 1, _I32), _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_token_logprobs", status)
-    return (logprobs, None if entropy is False else entropy, top_ids if top_k > 0 else None,
-            top_logprobs if top_k > 0 else None)
+    return logprobs, entropy, top_ids, top_logprobs
 
 
 # ---------------------------------------------------------------------------

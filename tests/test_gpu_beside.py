@@ -120,13 +120,17 @@ def test_norm(qmm, cuda, case):
 @pytest.mark.parametrize("case", [NORM_CASES[i] for i in (4, 6, 7, 11, 12)], ids=lambda c: "-".join(map(str, c)))
 def test_norm_strided_in_place(qmm, cuda, case, stride):
     """Rows inside wider ones, the sum over the residual itself: the same values
-    as apart from it, and nothing written between the rows."""
+    as in rows laid out the same apart from it (in others the sums may be split
+    otherwise), and nothing written between the rows."""
     a, out_type = norm_case(cuda, *case, stride=stride)
     T, D = a["residual"].shape
     kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
     store = torch.full((T, (D + 47) // 16 * 16), 5, dtype={"s8": torch.int8}.get(out_type, TYPES.get(out_type)),
                        device=cuda)
     apart = qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]),
+                           out=store[:, :D], **kw)
+    check_norm(a, out_type, apart, O.HALF[case[2]])
+    apart = qmm.block_norm(a["residual"], a["branch"], residual_out=wide(a["residual"], D + stride),
                            out=store[:, :D], **kw)
     check_norm(a, out_type, apart, O.HALF[case[2]])
     assert (store[:, D:] == 5).all()
