@@ -122,8 +122,8 @@ qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, con
   const qmm_status st = lora_sizes(M, set->K, set->N, set->n_adapters, set->max_rank);
   if (st != QMM_OK) return st;
   if (!aligned(set->A, 16) || !aligned(set->B, 16) || !aligned(set->ranks, 4) || !aligned(set->scales, 4) ||
-      !stride8(set->a_stride_slot, set->n_adapters, 0) || !stride8(set->a_stride_rank, set->max_rank, set->K) ||
-      !stride8(set->b_stride_slot, set->n_adapters, 0) || !stride8(set->b_stride_row, set->N, set->max_rank))
+      !stride8(set->a_stride_slot, set->n_adapters, 8) || !stride8(set->a_stride_rank, set->max_rank, set->K) ||
+      !stride8(set->b_stride_slot, set->n_adapters, 8) || !stride8(set->b_stride_row, set->N, set->max_rank))
     return QMM_ERR_INVALID_ARG;
   if (!stride8(ldx, M, set->K) || (base != nullptr && !rows_ok(ldb, M, set->N)) || !rows_ok(ldo, M, set->N))
     return QMM_ERR_INVALID_ARG;

@@ -1,0 +1,26 @@
+// What the adapter kernels share: the rows by adapter, and h as it lies between the
+// two products of a routed call.
+#pragma once
+
+#include "beside.h"
+
+namespace qmm {
+
+constexpr int kLoraTile = 128;            // rows of a routed item, all of one adapter
+
+struct LoraWork {
+  int* head;      // [0]: tiles of rows with an adapter, [1]: all tiles
+  int4* tiles;    // adapter (-1: none), first place in rows, rows
+  int* rows;      // [M] row numbers by adapter
+  uint16_t* h;    // [M][2][rank_stride] bf16 by place in rows: s_a A_a x_m as two terms
+};
+
+inline int lora_rank_stride(int64_t max_rank) { return (int)((max_rank + 63) / 64 * 64); }
+inline int64_t lora_max_tiles(int64_t M, int64_t n_adapters) {
+  return M / kLoraTile + (n_adapters + 1 < M ? n_adapters + 1 : M);
+}
+
+// out = base + h B^T on the tensor cores (lora_umma.cu)
+cudaError_t launch_lora_outer(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream);
+
+}  // namespace qmm

@@ -45,6 +45,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 bool make_tmap_2d(CUtensorMap* map, bool is_bf16_or_f16, void* base, uint64_t inner, uint64_t rows,
                   uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
 
+// The same with a third dimension of slots; boxes of one slot.
+bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t slots,
+                     uint64_t row_stride_bytes, uint64_t slot_stride_bytes, uint32_t box_inner, uint32_t box_rows);
+
 // q4 tiles as a 4-D byte tensor {128 bytes, 40 rows, tile_cols, tile_rows},
 // 128-byte swizzle, box {128, box_rows, 1, 4}: rows 0..31 of a tile are its
 // codes, rows 32..39 its (scale, min) pairs; one box covers 4 tile rows.

@@ -42,6 +42,22 @@ bool make_tmap_2d(CUtensorMap* map, bool is_bf16_or_f16, void* base, uint64_t in
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t slots,
+                     uint64_t row_stride_bytes, uint64_t slot_stride_bytes, uint32_t box_inner, uint32_t box_rows) {
+  std::call_once(g_once, resolve);
+  if (g_encode == nullptr) return false;
+  // a dimension of one has no stride of its own: any valid one will do
+  const cuuint64_t row = rows > 1 ? row_stride_bytes : (inner * 2 + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {inner, rows, slots};
+  const cuuint64_t strides[2] = {row, slots > 1 ? slot_stride_bytes : row};
+  const cuuint32_t box[3] = {box_inner, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_q4_tiles(CUtensorMap* map, const void* tiles, uint64_t tile_cols, uint64_t tile_rows,
                         uint32_t box_rows) {
   std::call_once(g_once, resolve);
