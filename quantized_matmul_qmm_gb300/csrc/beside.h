@@ -49,6 +49,10 @@ struct LoraArgs {
   int64_t ldo;
   int32_t* dev_status;
 };
+// tiles of rows and columns that a call's second product walks over, at most
+inline int64_t lora_units(int64_t M, int64_t N, int64_t n_adapters) {
+  return (M / 128 + (n_adapters + 1 < M ? n_adapters + 1 : M)) * ((N + 127) / 128);
+}
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank);
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream);
 

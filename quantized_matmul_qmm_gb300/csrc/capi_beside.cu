@@ -127,6 +127,7 @@ qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, con
     return QMM_ERR_INVALID_ARG;
   if (!stride8(ldx, M, set->K) || (base != nullptr && !rows_ok(ldb, M, set->N)) || !rows_ok(ldo, M, set->N))
     return QMM_ERR_INVALID_ARG;
+  if (lora_units(M, set->N, set->n_adapters) > INT32_MAX) return QMM_ERR_UNSUPPORTED;
   if (M == 0) return QMM_OK;
   if (X == nullptr || ids == nullptr || out == nullptr || !aligned(X, 16) || !aligned(ids, 4) || !aligned(base, 4) ||
       !aligned(out, 4))

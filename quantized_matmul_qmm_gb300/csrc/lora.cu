@@ -23,7 +23,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kTile = 64;                 // rows of an item of the first product (half a routed tile)
+constexpr int kTile = 16;                 // rows of an item of a call of few rows, all of one adapter
 constexpr int kRouteThreads = 1024;
 constexpr int kThreads = 256;
 
@@ -296,10 +296,10 @@ QMM_DEV void outer_part(const LoraArgs& a, const __nv_bfloat16* B, int rank, con
 
 // The item of this cluster in a call of few rows, found by every block for
 // itself: row t opens an item when the number of earlier rows with its adapter is a
-// multiple of `tile`, and the item's rows are the next `tile` of them.  Rows without
+// multiple of 16, and the item's rows are the next 16 of them.  Rows without
 // an adapter make items of their own.  Returns {adapter, -, rows} with the row
 // numbers in rows[]; rows = 0: no item left for this cluster.
-QMM_DEV int4 own_item(const LoraArgs& a, int item, int tile, bool copy_none, int* ids, int* rows, int* scratch) {
+QMM_DEV int4 own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int* rows, int* scratch) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int id = INT_MIN;                       // past the rows
   if (t < a.M) {
@@ -326,7 +326,7 @@ QMM_DEV int4 own_item(const LoraArgs& a, int item, int tile, bool copy_none, int
   }
   before += __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
   // items are numbered by the rows that open them
-  const bool opens = id != INT_MIN && before % tile == 0;
+  const bool opens = id != INT_MIN && before % kTile == 0;
   const uint32_t flags = __ballot_sync(0xffffffffu, opens);
   int* counts = scratch + 2;
   if (lane == 0) counts[warp] = __popc(flags);
@@ -337,13 +337,11 @@ QMM_DEV int4 own_item(const LoraArgs& a, int item, int tile, bool copy_none, int
   __syncthreads();
   const int adapter = scratch[0], first = scratch[1];
   if (first < 0) return make_int4(0, 0, 0, 0);
-  const bool mine = id == adapter && before >= first && before < first + tile;
+  const bool mine = id == adapter && before >= first && before < first + kTile;
   if (mine) rows[before - first] = t;
   const int n = __syncthreads_count(mine);
   return make_int4(adapter, 0, n, 0);
 }
-
-constexpr int kOwnTile = 16;              // rows of an item of a call of few rows
 
 struct alignas(16) Smem {
   float part[kThreads / 32][16][68];   // sums of a warp: 16 rows by 64 ranks; then of the block
@@ -353,172 +351,131 @@ struct alignas(16) Smem {
 };
 static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
 
-// A cluster takes an item: up to 64 rows of one adapter.  First its blocks share
-// K and its warps the 16-row groups and the rest of K; the sums meet over shared
-// memory, each block finishing its share of h, as two bf16 terms.  In a routed call
-// (kRouted) that is left in memory for the tensor cores' second product; else it
-// goes to all blocks, which then share the columns of out.
-template <bool kRouted, bool kVec>
+// A cluster takes an item: up to 16 rows of one adapter.  First its blocks and
+// their warps share K; the sums meet over shared memory, each block finishing its
+// share of h and writing it, as two bf16 terms, to all blocks.  Then the blocks and
+// warps share the columns of out.
+template <bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
-lora_kernel(LoraArgs a, LoraWork w, int rs, int cluster, bool copy_none) {
+lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int hs = rs + 8;                                   // row stride of h: rows fall on different banks
   uint16_t* hi = reinterpret_cast<uint16_t*>(smem_raw + sizeof(Smem));
-  uint16_t* lo = hi + kOwnTile * hs;
+  uint16_t* lo = hi + kTile * hs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
-  int item = blockIdx.x / cluster;
-  const int block = blockIdx.x % cluster;
-  int4 it;
-  if constexpr (kRouted) {
-    umma::pdl_launch_dependents();
-    umma::pdl_wait();
-  }
-  for (;;) {
-    if constexpr (kRouted) {
-      // clusters walk over the halves of tiles: how many there are only the device knows
-      if (item / 2 >= w.head[0]) return;
-      it = w.tiles[item / 2];
-      it.y += item % 2 * kTile;
-      it.z = min(it.z - item % 2 * kTile, kTile);
-      item += gridDim.x / cluster;
-      if (it.z <= 0) continue;
-      if (tid < it.z) sm.rows[tid] = w.rows[it.y + tid];
-      __syncthreads();
-    } else {
-      it = own_item(a, item, kOwnTile, copy_none, sm.ids, sm.rows, sm.scratch);
-      if (it.z == 0) return;
-      __syncthreads();
+  const int item = blockIdx.x / cluster, block = blockIdx.x % cluster;
+  const int4 it = own_item(a, item, copy_none, sm.ids, sm.rows, sm.scratch);
+  if (it.z == 0) return;
+  __syncthreads();
+  const int units = (a.N + 31) / 32;
+  const int n0 = (int)((int64_t)units * block / cluster), n1 = (int)((int64_t)units * (block + 1) / cluster);
+  if (it.x < 0) {                                          // no adapter: base as it is
+    for (int r = warp; r < it.z; r += kThreads / 32) {
+      const int64_t m = sm.rows[r];
+      for (int c = n0 * 32 + lane * 4; c < min(n1 * 32, a.N); c += 128)
+        store4<kVec>(a.out + m * a.ldo, c, a.N,
+                     a.base != nullptr ? load4<kVec>(a.base + m * a.ldb, c, a.N) : make_float4(0, 0, 0, 0));
     }
-    const int units = (a.N + 31) / 32;
-    const int n0 = (int)((int64_t)units * block / cluster), n1 = (int)((int64_t)units * (block + 1) / cluster);
-    if (!kRouted && it.x < 0) {                              // no adapter: base as it is
-      for (int r = warp; r < it.z; r += kThreads / 32) {
-        const int64_t m = sm.rows[r];
-        for (int c = n0 * 32 + lane * 4; c < min(n1 * 32, a.N); c += 128)
-          store4<kVec>(a.out + m * a.ldo, c, a.N,
-                       a.base != nullptr ? load4<kVec>(a.base + m * a.ldb, c, a.N) : make_float4(0, 0, 0, 0));
-      }
-      return;
-    }
-    const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
-    const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
-    const int groups = it.z > 32 ? 4 : it.z > 16 ? 2 : 1;    // of 16 rows; the warps of a group share the rest
-    const int group = warp % groups, share = warp / groups, shares = kThreads / 32 / groups;
-    const int r0 = group * 16 + g, r1 = r0 + 8;              // this lane's rows of the item
-    const int64_t m0 = r0 < it.z ? sm.rows[r0] : -1, m1 = r1 < it.z ? sm.rows[r1] : -1;
-    const __nv_bfloat16* x0 = m0 >= 0 ? a.X + m0 * a.ldx : nullptr;
-    const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
-    const __nv_bfloat16* A = a.A + it.x * a.a_slot;
-    const int chunks = (a.K + 31) / 32;
-    const int p0 = block * shares + share, parts = cluster * shares;
-    const int c0 = (int)((int64_t)chunks * p0 / parts);
-    const int c1 = group * 16 < it.z ? (int)((int64_t)chunks * (p0 + 1) / parts) : c0;   // a group without rows: nothing
-    const uint32_t part_addr = umma::smem_u32(sm.part), hi_addr = umma::smem_u32(hi), lo_addr = umma::smem_u32(lo);
-    for (int j0 = 0; j0 < rank; j0 += 64) {
-      float acc[8][4] = {};
-      const int left = rank - j0;
-      if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
-      else if (left <= 32) inner_part<4, 3>(a, x0, x1, A, rank, j0, c0, c1, acc);
-      else inner_part<8, 2>(a, x0, x1, A, rank, j0, c0, c1, acc);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int j = 8 * n + 2 * (lane & 3);
-        *reinterpret_cast<float2*>(&sm.part[warp][g][j]) = make_float2(acc[n][0], acc[n][1]);
-        *reinterpret_cast<float2*>(&sm.part[warp][g + 8][j]) = make_float2(acc[n][2], acc[n][3]);
-      }
-      __syncthreads();
-      // the block's sums, in place of its first warps'
-      const int quads = groups * 16 * 16;                    // of four ranks
-      if (shares > 1) {
-        for (int i = tid; i < quads; i += kThreads) {
-          const int r = i / 16, j = i % 16 * 4;
-          float4 s = *reinterpret_cast<const float4*>(&sm.part[r / 16][r % 16][j]);
-          for (int k = 1; k < shares; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.part[r / 16 + k * groups][r % 16][j]);
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-          }
-          *reinterpret_cast<float4*>(&sm.part[r / 16][r % 16][j]) = s;
-        }
-      }
-      umma::cluster_sync();
-      for (int i = block + cluster * tid; i < quads; i += cluster * kThreads) {
-        const int r = i / 16, j = i % 16 * 4;
-        const uint32_t at = part_addr + (uint32_t)(((r / 16 * 16 + r % 16) * 68 + j) * 4);
-        float4 s = make_float4(0, 0, 0, 0);
-        for (int o = 0; o < cluster; ++o) {                  // in order: the same sums every time
-          float4 v;
-          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                       : "r"(umma::mapa_shared(at, o))
-                       : "memory");
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        s.x = j0 + j < rank ? s.x * scale : 0.f;
-        s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
-        s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
-        s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
-        if (j0 + j < rs) {
-          const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
-          const uint32_t b0 = two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0));
-          const uint32_t b1 = two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1));
-          if constexpr (kRouted) {
-            if (r >= it.z) continue;
-            uint16_t* to = w.h + (int64_t)(it.y + r) * 2 * rs + j0 + j;
-            *reinterpret_cast<uint2*>(to) = make_uint2(a0, a1);
-            *reinterpret_cast<uint2*>(to + rs) = make_uint2(b0, b1);
-            continue;
-          }
-          const uint32_t to = (uint32_t)(r * hs + j0 + j) * 2;
-          for (int o = 0; o < cluster; ++o) {
-            asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(hi_addr + to, o)), "r"(a0),
-                         "r"(a1)
-                         : "memory");
-            asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(lo_addr + to, o)), "r"(b0),
-                         "r"(b1)
-                         : "memory");
-          }
-        }
-      }
-      umma::cluster_sync();
-    }
-    if constexpr (kRouted) continue;   // every thread has passed the cluster's barrier
-    if (group * 16 >= it.z) return;
-    const __nv_bfloat16* B = a.B + it.x * a.b_slot;
-    if (rank <= 32) outer_part<kVec, 1>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
-    else if (rank <= 64) outer_part<kVec, 2>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
-    else outer_part<kVec, 0>(a, B, rank, hi, lo, hs, r0, m0, m1, n0 + share, n1, shares);
     return;
   }
+  const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
+  const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
+  const int64_t m0 = g < it.z ? sm.rows[g] : -1, m1 = g + 8 < it.z ? sm.rows[g + 8] : -1;   // this lane's rows
+  const __nv_bfloat16* x0 = m0 >= 0 ? a.X + m0 * a.ldx : nullptr;
+  const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
+  const __nv_bfloat16* A = a.A + it.x * a.a_slot;
+  const int chunks = (a.K + 31) / 32;
+  constexpr int kWarps = kThreads / 32;
+  const int part = block * kWarps + warp, parts = cluster * kWarps;
+  const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
+  const uint32_t part_addr = umma::smem_u32(sm.part), hi_addr = umma::smem_u32(hi), lo_addr = umma::smem_u32(lo);
+  for (int j0 = 0; j0 < rank; j0 += 64) {
+    float acc[8][4] = {};
+    const int left = rank - j0;
+    if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    else if (left <= 32) inner_part<4, 3>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    else inner_part<8, 2>(a, x0, x1, A, rank, j0, c0, c1, acc);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int j = 8 * n + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(&sm.part[warp][g][j]) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(&sm.part[warp][g + 8][j]) = make_float2(acc[n][2], acc[n][3]);
+    }
+    __syncthreads();
+    // the block's sums, in place of its first warp's: four ranks a thread
+    {
+      const int r = tid / 16, j = tid % 16 * 4;
+      float4 s = *reinterpret_cast<const float4*>(&sm.part[0][r][j]);
+      for (int k = 1; k < kWarps; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.part[k][r][j]);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      *reinterpret_cast<float4*>(&sm.part[0][r][j]) = s;
+    }
+    umma::cluster_sync();
+    for (int i = block + cluster * tid; i < kTile * 16; i += cluster * kThreads) {
+      const int r = i / 16, j = i % 16 * 4;
+      const uint32_t at = part_addr + (uint32_t)((r * 68 + j) * 4);
+      float4 s = make_float4(0, 0, 0, 0);
+      for (int o = 0; o < cluster; ++o) {                  // in order: the same sums every time
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(umma::mapa_shared(at, o))
+                     : "memory");
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      s.x = j0 + j < rank ? s.x * scale : 0.f;
+      s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
+      s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
+      s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
+      if (j0 + j < rs) {
+        const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
+        const uint32_t b0 = two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0));
+        const uint32_t b1 = two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1));
+        const uint32_t to = (uint32_t)(r * hs + j0 + j) * 2;
+        for (int o = 0; o < cluster; ++o) {
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(hi_addr + to, o)), "r"(a0),
+                       "r"(a1)
+                       : "memory");
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(lo_addr + to, o)), "r"(b0),
+                       "r"(b1)
+                       : "memory");
+        }
+      }
+    }
+    umma::cluster_sync();
+  }
+  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
+  if (rank <= 32) outer_part<kVec, 1>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
+  else if (rank <= 64) outer_part<kVec, 2>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
+  else outer_part<kVec, 0>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
 }
 
 // Calls of up to this many rows find their items in the kernel itself.
 constexpr int kOwnRows = kThreads;
 
-template <bool kRouted, bool kVec>
-cudaError_t launch_typed(const LoraArgs& a, const LoraWork& w, int items, int cluster, bool copy_none,
-                         cudaStream_t stream) {
-  // h in shared memory: only where the same kernel goes on to the second product
-  const int rs = kRouted ? lora_rank_stride(a.max_rank) : (a.max_rank + 31) / 32 * 32;
-  auto bytes = [](int stride) { return sizeof(Smem) + (kRouted ? 0 : (size_t)2 * kOwnTile * (stride + 8) * 2); };
+template <bool kVec>
+cudaError_t launch_rows(const LoraArgs& a, int items, int cluster, bool copy_none, cudaStream_t stream) {
+  const int rs = (a.max_rank + 31) / 32 * 32;
+  auto bytes = [](int stride) { return sizeof(Smem) + (size_t)2 * kTile * (stride + 8) * 2; };
   static std::atomic<uint64_t> done{0};
-  cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_kernel<kRouted, kVec>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank));
+  const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_rows_kernel<kVec>),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes(rs);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kRouted ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<kRouted, kVec>, a, w, rs, cluster, copy_none);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_rows_kernel<kVec>, a, rs, cluster, copy_none);
 }
 
 }  // namespace
@@ -532,26 +489,21 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters,
 
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream) {
   const bool copy_none = a.base != a.out;
-  const int fit = 2 * attn_sm_count();                     // blocks on the GPU at once
-  auto blocks_of = [&](int64_t items) {
-    int cluster = 8;
-    while (cluster > 1 && items * cluster > fit) cluster /= 2;
-    return cluster;
-  };
   if (a.M <= kOwnRows) {
-    const int items = (int)std::min<int64_t>(a.M, std::min<int64_t>(a.n_adapters + 1, a.M) + a.M / kOwnTile);
+    const int items = (int)std::min<int64_t>(a.M, std::min<int64_t>(a.n_adapters + 1, a.M) + a.M / kTile);
+    int cluster = 8;                                       // two blocks per SM in all
+    while (cluster > 1 && items * cluster > 2 * attn_sm_count()) cluster /= 2;
     const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                      (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
-    return vec ? launch_typed<false, true>(a, LoraWork{}, items, blocks_of(items), copy_none, stream)
-               : launch_typed<false, false>(a, LoraWork{}, items, blocks_of(items), copy_none, stream);
+    return vec ? launch_rows<true>(a, items, cluster, copy_none, stream)
+               : launch_rows<false>(a, items, cluster, copy_none, stream);
   }
-  const int tiles = (int)lora_max_tiles(a.M, a.n_adapters);
   uint8_t* p = static_cast<uint8_t*>(workspace);
   LoraWork w;
   w.head = reinterpret_cast<int*>(p);
   p += 256;
   w.tiles = reinterpret_cast<int4*>(p);
-  p += pad256((size_t)tiles * sizeof(int4));
+  p += pad256((size_t)lora_max_tiles(a.M, a.n_adapters) * sizeof(int4));
   w.rows = reinterpret_cast<int*>(p);
   p += pad256((size_t)a.M * 4);
   w.h = reinterpret_cast<uint16_t*>(p);
@@ -564,11 +516,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t str
   const int buckets = a.n_adapters + 1, segs = std::min(32, kRouteSmem / 4 / buckets - 1);
   lora_route_kernel<<<1, kRouteThreads, (size_t)(segs + 1) * buckets * 4, stream>>>(a, w, copy_none, segs);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
-  const int64_t filled = (a.M + kTile - 1) / kTile;        // halves of tiles, if all rows had one adapter
-  const int cluster = blocks_of(filled);
-  const int items = (int)std::min<int64_t>(2 * tiles, std::max<int64_t>(fit / cluster, filled));
-  err = launch_typed<true, true>(a, w, items, cluster, copy_none, stream);
-  return err != cudaSuccess ? err : launch_lora_outer(a, w, copy_none, stream);
+  return launch_lora_products(a, w, copy_none, stream);
 }
 
 }  // namespace qmm

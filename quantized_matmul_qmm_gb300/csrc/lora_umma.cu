@@ -1,16 +1,13 @@
-// The second product of the adapters in calls of many rows, on tcgen05:
-//     out[m] = base[m] + h_m B_a^T,   h_m = s_a A_a x_m as two bf16 terms.
+// The adapters' two products in calls of many rows, on tcgen05:
+//     h_m = s_a A_a x_m,  as two bf16 terms;   out[m] = base[m] + h_m B_a^T.
 //
-// Bound: bytes, 8 a value of out (base in, out back); the two terms' products are 4 r
-// operations per 8 bytes, which mma.sync (600 TFLOP/s measured on this part) could
-// not hide from ranks of about 100 on.
+// Bound: bytes, 2 K a row for the first and 8 a value of out (base in, out back) for
+// the second.  The products are 2 r operations for 2 bytes of X, and 4 r (both
+// terms) for 8 bytes of out: from ranks of about 100 on more than mma.sync (600
+// TFLOP/s measured on this part) does in that time.
 //
-// A block takes 128 rows of one adapter and 128 columns.  Its base values are on
-// their way into registers, in whole rows of 512 bytes, before anything else;
-// meanwhile the terms of h and the rows of B arrive by TMA, 64 ranks at a time, and
-// one thread issues the products of both terms with the same B.  The accumulator
-// goes from tensor memory through shared memory, so that sums are stored in whole
-// rows again.  Two blocks share an SM: one loads while the other stores.
+// Both kernels take 128 rows of one adapter at a time, the tensor cores' height;
+// partly filled tiles cost products, not bytes.
 #include <algorithm>
 #include <atomic>
 
@@ -23,45 +20,256 @@ namespace {
 
 using namespace umma;
 
-constexpr int kThreads = 256;
-constexpr int kCols = 128;
-constexpr int kChunk = 64;                                  // ranks of a stage: 128 bytes, one swizzle row
+constexpr int kChunk = 64;                                  // k or ranks of a stage: 128 bytes, one swizzle row
 constexpr int kTileBytes16 = 128 * kChunk * 2;
+
+QMM_DEV uint32_t two_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---- h = s A x -----------------------------------------------------------------
+// A cluster takes a tile, its blocks a part of K each.  A block's threads copy the
+// rows' 16-byte pieces (rows lie anywhere) and the adapter's into the swizzled
+// layout of the operands, several stages ahead; one thread issues the products of
+// a stage for all ranks at once.  The blocks' sums meet over shared memory, 64
+// ranks at a time: each block adds up its share of the rows, in order, and writes
+// their two terms.
+constexpr int kInnerThreads = 256;
+constexpr int kInnerPitch = 64 + 4;                         // floats of a row of sums
+constexpr int kInnerSums = 128 * kInnerPitch * 4;
+constexpr int kInnerMaxStages = 4;
+
+struct InnerParams {
+  LoraArgs a;
+  LoraWork w;
+  int rs, stages, stage_bytes, cluster;
+  uint32_t tmem_cols;
+};
+
+template <int kPending>
+QMM_DEV void wait_copies(int pending) {
+  if (pending == kPending) cp_async_wait<kPending>();
+  else if constexpr (kPending > 0) wait_copies<kPending - 1>(pending);
+}
+
+__global__ void __launch_bounds__(kInnerThreads, 2)
+lora_inner_kernel(const InnerParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t done[kInnerMaxStages], last;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  uint8_t* smem = smem_align(smem_raw, 1024);
+  const LoraArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int block = blockIdx.x % p.cluster;
+  if (tid == 0) {
+    for (int s = 0; s < kInnerMaxStages; ++s) mbar_init(&done[s], 1);
+    mbar_init(&last, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tiles = p.w.head[0], clusters = gridDim.x / p.cluster;
+  const int piece = tid & 7, row0 = tid >> 3;               // this thread's 16 bytes of rows row0 + 32 i
+  uint32_t done_uses = 0;                                   // stages filled so far
+  uint32_t last_par = 0;
+  bool ok = true;
+
+  for (int tile = blockIdx.x / p.cluster; tile < tiles; tile += clusters) {
+    const int4 it = p.w.tiles[tile];
+    const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
+    const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
+    const int n16 = (rank + 15) / 16 * 16;                  // ranks of the products
+    const int chunks = (a.K + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * block / p.cluster), c1 = (int)((int64_t)chunks * (block + 1) / p.cluster);
+    const __nv_bfloat16* x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + 32 * i;
+      x[i] = r < it.z ? a.X + (int64_t)p.w.rows[it.y + r] * a.ldx : nullptr;
+    }
+    const __nv_bfloat16* A = a.A + it.x * a.a_slot;
+    auto copy = [&](int c, int s) {
+      const uint32_t to = smem_u32(smem) + (uint32_t)s * p.stage_bytes + (uint32_t)((piece ^ (row0 & 7)) << 4);
+      const int k = c * kChunk + piece * 8;
+      const bool in = k < a.K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool there = in && x[i] != nullptr;
+        cp_async16_zfill(to + (uint32_t)(row0 + 32 * i) * 128, there ? x[i] + k : a.X, there ? 16 : 0);
+      }
+      for (int j = row0; j < n16; j += 32) {
+        const bool there = in && j < rank;
+        cp_async16_zfill(to + kTileBytes16 + (uint32_t)j * 128, there ? A + j * a.a_rank + k : a.A, there ? 16 : 0);
+      }
+    };
+    const uint32_t idesc = idesc_f16(128, n16, true);
+    const int n = c1 - c0;
+    for (int i = 0; i < n + p.stages - 1; ++i) {
+      if (i < n) {
+        const uint32_t use = done_uses + i;                 // of the ring
+        const int s = use % p.stages;
+        // the products that read this stage's last contents
+        if (use >= (uint32_t)p.stages) ok = ok && mbar_wait(&done[s], (use / p.stages - 1) & 1, &abort_flag, a.dev_status);
+        if (ok) copy(c0 + i, s);
+      }
+      cp_async_commit();
+      const int j = i - (p.stages - 1);
+      if (j < 0) continue;
+      wait_copies<kInnerMaxStages - 1>(p.stages - 1);
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0 && ok) {
+        tc_fence_after();
+        const int s = (done_uses + j) % p.stages;
+        const uint64_t dx = desc_kmajor_sw128(smem_u32(smem) + s * p.stage_bytes);
+        const uint64_t da = desc_kmajor_sw128(smem_u32(smem) + s * p.stage_bytes + kTileBytes16);
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k) umma_f16(tmem, dx + 2 * k, da + 2 * k, idesc, j > 0 || k > 0);
+        umma_commit(&done[s]);
+        if (j == n - 1) umma_commit(&last);
+      }
+    }
+    done_uses += n;
+    if (n > 0) {
+      ok = ok && mbar_wait(&last, last_par, &abort_flag, a.dev_status);
+      last_par ^= 1;
+    }
+    // A block that gave up goes on with the others: its sums are not valid, and the
+    // status says so.
+    tc_fence_after();
+    __syncthreads();                                        // the stages are free
+    float* sums = reinterpret_cast<float*>(smem);           // [128][kInnerPitch]
+    const uint32_t sums_addr = smem_u32(sums);
+    const int q = warp & 3, half = warp >> 2;
+    for (int j0 = 0; j0 < rank; j0 += 64) {
+      if (32 * q < it.z && j0 + 32 * half < n16) {
+        uint32_t r[32];
+        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(j0 + 32 * half), r);
+        tmem_wait_ld();
+        float* to = sums + (32 * q + lane) * kInnerPitch + 32 * half;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(to + i) =
+              n > 0 ? make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]) : make_uint4(0, 0, 0, 0);
+      }
+      tc_fence_before();
+      cluster_sync();
+      for (int i = block + p.cluster * tid; i < it.z * 16; i += p.cluster * kInnerThreads) {
+        const int r = i / 16, j = i % 16 * 4;
+        float4 s = make_float4(0, 0, 0, 0);
+        if (j0 + j < n16) {
+          const uint32_t at = sums_addr + (uint32_t)(r * kInnerPitch + j) * 4;
+          for (int o = 0; o < p.cluster; ++o) {             // in order: the same sums every time
+            float4 v;
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(mapa_shared(at, o))
+                         : "memory");
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+          }
+        }
+        s.x = j0 + j < rank ? s.x * scale : 0.f;
+        s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
+        s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
+        s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
+        const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
+        uint16_t* to = p.w.h + (int64_t)(it.y + r) * 2 * p.rs + j0 + j;
+        *reinterpret_cast<uint2*>(to) = make_uint2(a0, a1);
+        *reinterpret_cast<uint2*>(to + p.rs) =
+            make_uint2(two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0)),
+                       two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1)));
+      }
+      cluster_sync();
+    }
+    tc_fence_after();
+    fence_proxy_async_smem();
+  }
+  cp_async_wait<0>();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// ---- out = base + h B^T ----------------------------------------------------------
+// A block per SM walks over units of 128 rows by 128 columns.  One warp loads the
+// two terms of h and the rows of B by TMA, 64 ranks a stage, and issues the products
+// of both terms with the same B into one of four accumulators; two groups of eight
+// warps take the units in turn.  A warp owns 32 rows by 64 columns: their base values
+// are on their way into registers half a unit ahead, the accumulator goes through the
+// warp's corner of shared memory so that rows are read and written 128 bytes at a
+// time, and no warp waits for another.
+constexpr int kEpiWarps = 16;
+constexpr int kOuterThreads = (kEpiWarps + 1) * 32;
+constexpr int kCols = 128;
+constexpr int kBuffers = 4;
+constexpr int kStages = 3;
 constexpr int kStageBytes = 3 * kTileBytes16;               // both terms of h, B
-constexpr int kMaxChunks = (int)kLoraMaxRank / kChunk;
-constexpr int kPitch = kCols + 4;                           // floats of a row of the accumulator in shared memory
-constexpr int kOutBytes = 128 * kPitch * 4;
-constexpr uint32_t kTmemCols = kCols;
+constexpr int kPitch = 32 + 4;                              // floats of a row of a warp's corner
+constexpr int kCorner = 32 * kPitch * 4;
+constexpr int kOuterSmem = 1024 + kStages * kStageBytes + kEpiWarps * kCorner;
 
 struct OuterParams {
   LoraArgs a;
   LoraWork w;
-  int rs, stages, col_blocks;
+  int rs, col_blocks;
   bool copy_none;
 };
 
+// A unit of the walk.
+struct Unit {
+  int4 it;         // adapter, first place, rows; rows 0: past the end
+  int col0, rank, chunks;
+};
+
+QMM_DEV Unit unit_at(const OuterParams& p, uint32_t i, uint32_t units) {
+  Unit u;
+  u.it = make_int4(-1, 0, 0, 0);
+  u.col0 = u.rank = u.chunks = 0;
+  if (i < units) {
+    const uint32_t tile = i / (uint32_t)p.col_blocks;
+    u.it = p.w.tiles[tile];
+    u.col0 = (int)(i - tile * p.col_blocks) * kCols;
+    if (u.it.x >= 0) u.rank = p.a.ranks != nullptr ? p.a.ranks[u.it.x] : p.a.max_rank;
+    u.chunks = (u.rank + kChunk - 1) / kChunk;
+  }
+  return u;
+}
+
 template <bool kVec>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kOuterThreads, 1)
 lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmB,
                   const OuterParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kMaxChunks], done[2], last;
+  __shared__ uint64_t full[kStages], empty[kStages], tfull[kBuffers], tempty[kBuffers];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   uint8_t* smem = smem_align(smem_raw, 1024);
   const LoraArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int c = 0; c < kMaxChunks; ++c) mbar_init(&full[c], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&done[s], 1);
-    mbar_init(&last, 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int b = 0; b < kBuffers; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], kEpiWarps / 2);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmH);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
-    tmem_alloc(&tmem_slot, kTmemCols);
+  if (warp == kEpiWarps) {
+    tmem_alloc(&tmem_slot, kBuffers * kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -69,194 +277,263 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
-  // parities of the barriers' next phases: a bit per chunk, per stage, and one
-  uint32_t full_par = 0, done_par = 0, last_par = 0;
-  const int64_t units = (int64_t)p.w.head[p.copy_none ? 1 : 0] * p.col_blocks;
+  const uint32_t units = (uint32_t)p.w.head[p.copy_none ? 1 : 0] * p.col_blocks;
 
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int4 it = p.w.tiles[unit / p.col_blocks];
-    const int col0 = (int)(unit % p.col_blocks) * kCols;
-    const bool none = it.x < 0;
-    const int rank = none ? 0 : a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
-    const int chunks = (rank + kChunk - 1) / kChunk;
-    auto issue = [&](int c) {
-      uint8_t* s = smem + c % p.stages * kStageBytes;
-      mbar_arrive_expect_tx(&full[c], kStageBytes);
-      tma_load_2d(s, &tmH, &full[c], c * kChunk, it.y);
-      tma_load_2d(s + kTileBytes16, &tmH, &full[c], p.rs + c * kChunk, it.y);
-      tma_load_3d(smem_u32(s + 2 * kTileBytes16), &tmB, &full[c], c * kChunk, col0, it.x);
+  if (warp == kEpiWarps) {
+    // two walks over the stages: one fills them, one issues their products
+    uint32_t filled = 0, used = 0;
+    uint32_t buf_used = 0, buf_par = 0;                     // a bit per buffer: used before, parity of its release
+    uint32_t fi = blockIdx.x, mi = blockIdx.x;
+    Unit f = unit_at(p, fi, units), m = f;
+    int fc = 0, n = 0;
+    bool ok = true;
+    auto next_fill = [&] {
+      while (fi < units && fc >= f.chunks) {
+        fi += gridDim.x;
+        f = unit_at(p, fi, units);
+        fc = 0;
+      }
     };
-    if (tid == 0) {
-      fence_proxy_async_smem();   // the last unit's reads of the accumulator precede the copies
-      for (int c = 0; c < min(chunks, p.stages); ++c) issue(c);
-    }
-
-    // base, a whole row of the block's columns per warp and load
-    const int my_row = warp * 16 + (lane & 15);
-    const int row_id = my_row < it.z ? p.w.rows[it.y + my_row] : 0;
-    auto col = [&](int i) { return kVec ? col0 + lane * 4 + i : col0 + lane + 32 * i; };   // of value i
-    float y[16][4];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int64_t m = __shfl_sync(0xffffffffu, row_id, r);
-      const float* from = a.base + m * a.ldb;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[r][i] = 0.f;
-      if (a.base == nullptr || warp * 16 + r >= it.z) continue;
-      if constexpr (kVec) {
-        if (col(0) < a.N) {
-          const float4 v = *reinterpret_cast<const float4*>(from + col(0));
-          y[r][0] = v.x, y[r][1] = v.y, y[r][2] = v.z, y[r][3] = v.w;
+    next_fill();
+    for (; mi < units && ok; mi += gridDim.x, m = unit_at(p, mi, units), ++n) {
+      const int buf = n % kBuffers;
+      for (int c = 0; c < m.chunks && ok; ++c) {
+        while (ok && fi < units && filled < used + kStages - (used > 0)) {
+          const int s = filled % kStages;
+          if (filled >= kStages)
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (filled / kStages - 1) & 1, &abort_flag, a.dev_status));
+          if (ok && lane == 0) {
+            uint8_t* to = smem + s * kStageBytes;
+            mbar_arrive_expect_tx(&full[s], kStageBytes);
+            tma_load_2d(to, &tmH, &full[s], fc * kChunk, f.it.y);
+            tma_load_2d(to + kTileBytes16, &tmH, &full[s], p.rs + fc * kChunk, f.it.y);
+            tma_load_3d(smem_u32(to + 2 * kTileBytes16), &tmB, &full[s], fc * kChunk, f.col0, f.it.x);
+          }
+          if (ok) ++filled, ++fc;
+          next_fill();
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col(i) < a.N) y[r][i] = from[col(i)];
-      }
-    }
-
-    float* acc = reinterpret_cast<float*>(smem);   // [128][kPitch], where the operands lay
-    if (!none) {
-      constexpr uint32_t idesc = idesc_f16(128, kCols, true);
-      auto products = [&](int c) {
-        const uint32_t s = smem_u32(smem + c % p.stages * kStageBytes);
-        const int steps = min(kChunk / 16, (rank - c * kChunk + 15) / 16);
-        const uint64_t b = desc_kmajor_sw128(s + 2 * kTileBytes16);
-        for (int term = 1; term >= 0; --term) {    // the smaller one first
-          const uint64_t h = desc_kmajor_sw128(s + term * kTileBytes16);
-          for (int k = 0; k < steps; ++k)
-            umma_f16(tmem, h + 2 * k, b + 2 * k, idesc, c > 0 || term == 0 || k > 0);
+        const int s = used % kStages;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (used / kStages) & 1, &abort_flag, a.dev_status));
+        if (ok && c == 0 && (buf_used >> buf & 1)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&tempty[buf], buf_par >> buf & 1, &abort_flag, a.dev_status));
+          buf_par ^= 1u << buf;
         }
-      };
-      bool ok = true;
-      if (tid == 0) {
-        for (int c = 0; c + 1 < chunks && ok; ++c) {
-          ok = mbar_wait(&full[c], full_par >> c & 1, &abort_flag, a.dev_status);
-          if (!ok) break;
+        if (!ok) break;
+        uint8_t* at = smem + s * kStageBytes;
+        const int left = m.rank - c * kChunk;
+        if (left < kChunk && left % 16 != 0 && m.rank < a.max_rank) {
+          // what lies behind the adapter's rank in the last step of 16: zeros, since 0
+          // times an infinity or NaN is none (h is zero there)
+          const int piece = left / 8;
+          for (int r = lane; r < kCols; r += 32) {
+            uint8_t* row = at + 2 * kTileBytes16 + r * 128;
+            uint4* v = reinterpret_cast<uint4*>(row + ((piece ^ (r & 7)) << 4));
+            uint32_t w[4] = {v->x, v->y, v->z, v->w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int keep = left % 8 - 2 * i;            // values of this word that stay
+              if (keep <= 0) w[i] = 0;
+              else if (keep == 1) w[i] &= 0xFFFFu;
+            }
+            *v = make_uint4(w[0], w[1], w[2], w[3]);
+            if (piece % 2 == 0)
+              *reinterpret_cast<uint4*>(row + (((piece + 1) ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
           tc_fence_after();
-          products(c);
-          if (c + p.stages < chunks) {
-            const int s = c % p.stages;
-            umma_commit(&done[s]);
-            ok = mbar_wait(&done[s], done_par >> s & 1, &abort_flag, a.dev_status);
-            done_par ^= 1u << s;
-            if (ok) issue(c + p.stages);
+          constexpr uint32_t idesc = idesc_f16(128, kCols, true);
+          const int steps = min(kChunk / 16, (left + 15) / 16);
+          const uint64_t b = desc_kmajor_sw128(smem_u32(at + 2 * kTileBytes16));
+          for (int term = 1; term >= 0; --term) {           // the smaller one first
+            const uint64_t h = desc_kmajor_sw128(smem_u32(at + term * kTileBytes16));
+            for (int k = 0; k < steps; ++k)
+              umma_f16(tmem + buf * kCols, h + 2 * k, b + 2 * k, idesc, c > 0 || term == 0 || k > 0);
           }
+          umma_commit(&empty[s]);
+          if (c == m.chunks - 1) umma_commit(&tfull[buf]);
         }
+        __syncwarp();
+        ++used;
       }
-      const int c = chunks - 1, rem = rank - c * kChunk;
-      ok = ok && mbar_wait(&full[c], full_par >> c & 1, &abort_flag, a.dev_status);
-      if (rem % 16 != 0 && rank < a.max_rank) {
-        // what lies behind the adapter's rank in the last step of 16: zeros, since 0
-        // times an infinity or NaN is none (h is zero there)
-        if (ok && tid < kCols) {
-          uint8_t* row = smem + c % p.stages * kStageBytes + 2 * kTileBytes16 + tid * 128;
-          const int piece = rem / 8;
-          uint4* at = reinterpret_cast<uint4*>(row + ((piece ^ (tid & 7)) << 4));
-          uint32_t w[4] = {at->x, at->y, at->z, at->w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = rem % 8 - 2 * i;         // values of this word that stay
-            if (n <= 0) w[i] = 0;
-            else if (n == 1) w[i] &= 0xFFFFu;
-          }
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
-          if (piece % 2 == 0)
-            *reinterpret_cast<uint4*>(row + (((piece + 1) ^ (tid & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncthreads();
-      }
-      if (tid == 0 && ok) {
-        tc_fence_after();
-        products(c);
-        umma_commit(&last);
-      }
-      ok = ok && mbar_wait(&last, last_par, &abort_flag, a.dev_status);
-      if (__syncthreads_or(!ok)) {
-        // copies already issued land before the block leaves
-        if (tid == 0)
-          for (int i = 0; i < chunks; ++i) mbar_drain(&full[i], full_par >> i & 1);
-        break;
-      }
-      full_par ^= (1u << chunks) - 1;
-      last_par ^= 1;
-      tc_fence_after();
-      const int q = warp & 3, half = warp >> 2;
-      if (32 * q < it.z) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t r[32];
-          tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * 64 + 32 * j), r);
-          tmem_wait_ld();
-          float* to = acc + (32 * q + lane) * kPitch + half * 64 + 32 * j;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(to + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-        }
-      }
-      tc_fence_before();
-      __syncthreads();
-      tc_fence_after();
+      if (m.chunks > 0) buf_used |= 1u << buf;
     }
+    // copies already issued land before the block leaves
+    if (!ok)
+      for (uint32_t u = filled > kStages ? filled - kStages : 0; u < filled; ++u)
+        mbar_drain(&full[u % kStages], (u / kStages) & 1);
+  } else {
+    const int group = warp / (kEpiWarps / 2), q = warp & 3, half = (warp >> 2) & 1;
+    float* corner = reinterpret_cast<float*>(smem + kStages * kStageBytes + warp * kCorner);
+    uint32_t parity = 0;                                    // of this group's buffers' next phases
+    // four values of row 32 q + 4 i + lane / 8: columns col(j) + 0..3, or in steps of eight
+    const int sub = lane >> 3, cl = kVec ? (lane & 7) * 4 : lane & 7;
+    auto row_of = [&](const Unit& u) {
+      const int r = 32 * q + lane;
+      return r < u.it.z ? p.w.rows[u.it.y + r] : -1;
+    };
+    // values of half a unit's columns, asked for half a unit ahead
+    float y[8][4];
+    auto load = [&](const Unit& u, int ids, int j, int v) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int64_t m = __shfl_sync(0xffffffffu, row_id, r);
-      if (warp * 16 + r >= it.z) continue;
-      float* to = a.out + m * a.ldo;
-      const float* v = acc + (warp * 16 + r) * kPitch - col0;
+      for (int e = 0; e < 4; ++e) y[v][e] = 0.f;
+      const int m = __shfl_sync(0xffffffffu, ids, 4 * v + sub);
+      if (a.base == nullptr || m < 0) return;
+      const int col = u.col0 + half * 64 + 32 * j + cl;
+      const float* from = a.base + (int64_t)m * a.ldb + col;
       if constexpr (kVec) {
-        if (col(0) < a.N) {
-          float4 s = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
-          if (!none) {
-            const float4 d = *reinterpret_cast<const float4*>(v + col(0));
-            s.x += d.x, s.y += d.y, s.z += d.z, s.w += d.w;
-          }
-          *reinterpret_cast<float4*>(to + col(0)) = s;
+        if (col < a.N) {
+          const float4 t = *reinterpret_cast<const float4*>(from);
+          y[v][0] = t.x, y[v][1] = t.y, y[v][2] = t.z, y[v][3] = t.w;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col(i) < a.N) to[col(i)] = none ? y[r][i] : y[r][i] + v[col(i)];
+        for (int e = 0; e < 4; ++e)
+          if (col + 8 * e < a.N) y[v][e] = from[8 * e];
       }
+    };
+    uint32_t i = blockIdx.x + group * gridDim.x;
+    Unit u = unit_at(p, i, units);
+    int ids = row_of(u);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) load(u, ids, 0, v);
+    for (int n = group; i < units; n += 2, i += 2 * gridDim.x) {
+      const Unit next = unit_at(p, i + 2 * gridDim.x, units);
+      const int next_ids = row_of(next);
+      const int buf = n % kBuffers;
+      if (u.chunks > 0) {
+        const uint32_t par = parity >> buf & 1;
+        parity ^= 1u << buf;
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], par, &abort_flag, a.dev_status))) break;
+        tc_fence_after();
+      }
+      const bool rows = 32 * q < u.it.z;                    // of this warp
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (u.chunks > 0 && rows) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kCols + half * 64 + 32 * j + c), r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(corner + lane * kPitch + c + e) =
+                  make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+          }
+        }
+        __syncwarp();
+        if (j == 1 && u.chunks > 0) {
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&tempty[buf]);
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const int m = __shfl_sync(0xffffffffu, ids, 4 * v + sub);
+          const int col = u.col0 + half * 64 + 32 * j + cl;
+          const float* d = corner + (4 * v + sub) * kPitch + cl;
+          if (m >= 0) {
+            float* to = a.out + (int64_t)m * a.ldo + col;
+            if constexpr (kVec) {
+              if (col < a.N) {
+                float4 s = make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
+                if (u.chunks > 0) {
+                  const float4 t = *reinterpret_cast<const float4*>(d);
+                  s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+                }
+                *reinterpret_cast<float4*>(to) = s;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col + 8 * e < a.N) to[8 * e] = u.chunks > 0 ? y[v][e] + d[8 * e] : y[v][e];
+            }
+          }
+          if (j == 0) load(u, ids, 1, v);
+          else load(next, next_ids, 0, v);
+        }
+        __syncwarp();
+      }
+      u = next;
+      ids = next_ids;
     }
-    __syncthreads();   // the accumulator has been read
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kEpiWarps) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, kBuffers * kCols);
   }
 }
 
+cudaError_t launch_inner(const LoraArgs& a, const LoraWork& w, cudaStream_t stream) {
+  InnerParams p{};
+  p.a = a;
+  p.w = w;
+  p.rs = lora_rank_stride(a.max_rank);
+  const int n16 = (a.max_rank + 15) / 16 * 16;
+  p.stage_bytes = kTileBytes16 + (n16 * 128 + 1023) / 1024 * 1024;
+  // two blocks per SM: as many stages as 100 KB hold
+  p.stages = std::max(2, std::min(kInnerMaxStages, 100 * 1024 / p.stage_bytes));
+  p.tmem_cols = 32;
+  while ((int)p.tmem_cols < n16) p.tmem_cols *= 2;
+  // blocks of a tile: those of the tiles that the rows fill are on the GPU at once
+  const int64_t filled = (a.M + kLoraTile - 1) / kLoraTile;
+  const int chunks = (a.K + kChunk - 1) / kChunk, fit = 2 * attn_sm_count();
+  p.cluster = 8;
+  while (p.cluster > 1 && (filled * p.cluster > fit || 2 * p.cluster > chunks)) p.cluster /= 2;
+  const int64_t most = lora_max_tiles(a.M, a.n_adapters);
+  const int clusters = (int)std::min<int64_t>(most, std::max(1, fit / p.cluster));
+  const size_t smem = 1024 + (size_t)std::max(kInnerSums, p.stages * p.stage_bytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_inner_kernel),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
+  cfg.blockDim = dim3(kInnerThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, lora_inner_kernel, p);
+}
+
 template <bool kVec>
-cudaError_t launch_typed(const CUtensorMap& tmH, const CUtensorMap& tmB, const OuterParams& p, int grid,
+cudaError_t launch_outer(const CUtensorMap& tmH, const CUtensorMap& tmB, const OuterParams& p, int grid,
                          cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  const size_t smem = 1024 + (size_t)std::max(kOutBytes, p.stages * kStageBytes);
   const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_outer_kernel<kVec>),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   1024 + std::max(kOutBytes, 2 * kStageBytes));
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kOuterSmem);
   if (err != cudaSuccess) return err;
-  return launch_pdl(lora_outer_kernel<kVec>, dim3((unsigned)grid), dim3(kThreads), smem, stream, tmH,
-                    tmB, p);
+  return launch_pdl(lora_outer_kernel<kVec>, dim3((unsigned)grid), dim3(kOuterThreads), kOuterSmem, stream, tmH, tmB,
+                    p);
 }
 
 }  // namespace
 
-cudaError_t launch_lora_outer(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream) {
-  OuterParams p{a, w, lora_rank_stride(a.max_rank), a.max_rank > kChunk ? 2 : 1, (a.N + kCols - 1) / kCols, copy_none};
+cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream) {
+  OuterParams p{a, w, lora_rank_stride(a.max_rank), (a.N + kCols - 1) / kCols, copy_none};
   CUtensorMap tmH, tmB;
   if (!make_tmap_2d(&tmH, true, w.h, (uint64_t)2 * p.rs, (uint64_t)a.M, (uint64_t)4 * p.rs, kChunk, 128) ||
       !make_tmap_rows3(&tmB, a.B, (uint64_t)a.max_rank, (uint64_t)a.N, (uint64_t)a.n_adapters, (uint64_t)a.b_row * 2,
                        (uint64_t)a.b_slot * 2, kChunk, kCols))
     return cudaErrorInvalidValue;
-  // two blocks per SM walk over the units: how many tiles there are only the device knows
-  const int grid = (int)std::min<int64_t>(lora_max_tiles(a.M, a.n_adapters) * p.col_blocks, 2 * attn_sm_count());
+  const cudaError_t err = launch_inner(a, w, stream);
+  if (err != cudaSuccess) return err;
+  // a block per SM: how many units there are only the device knows
+  const int grid = (int)std::min<int64_t>(lora_max_tiles(a.M, a.n_adapters) * p.col_blocks, attn_sm_count());
   const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                    (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
-  return vec ? launch_typed<true>(tmH, tmB, p, grid, stream) : launch_typed<false>(tmH, tmB, p, grid, stream);
+  return vec ? launch_outer<true>(tmH, tmB, p, grid, stream) : launch_outer<false>(tmH, tmB, p, grid, stream);
 }
 
 }  // namespace qmm

@@ -20,7 +20,7 @@ inline int64_t lora_max_tiles(int64_t M, int64_t n_adapters) {
   return M / kLoraTile + (n_adapters + 1 < M ? n_adapters + 1 : M);
 }
 
-// out = base + h B^T on the tensor cores (lora_umma.cu)
-cudaError_t launch_lora_outer(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream);
+// both products of a routed call (lora_umma.cu)
+cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream);
 
 }  // namespace qmm
