@@ -217,6 +217,8 @@ template <bool kResBf16, bool kBrBf16, int kG, bool kOff>
 __global__ void __launch_bounds__(1024)
 block_norm_kernel(NormArgs a, int off_step, bool weights16) {
   __shared__ float slots[5][32];
+  umma::pdl_launch_dependents();
+  umma::pdl_wait();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.T) return;   // whole warps, and only where no barrier follows
   const int off = kOff ? (int)(t * off_step & 3) : 0;
@@ -305,6 +307,8 @@ __global__ void __launch_bounds__(1024)
 block_norm_any_kernel(NormArgs a) {
   extern __shared__ float row[];
   __shared__ float slots[5][32];
+  umma::pdl_launch_dependents();
+  umma::pdl_wait();
   const int64_t t = blockIdx.x;
   const int D = a.D, first = threadIdx.x, step = blockDim.x;
   auto value = [](const void* p, bool bf16, int64_t i) {
@@ -371,9 +375,8 @@ cudaError_t launch_groups(const NormArgs& a, bool even, int off_step, bool weigh
   const int nt = (groups + 32 * kG - 1) / (32 * kG) * 32;
   const dim3 block(nt, nt == 32 ? 4 : 1);
   const dim3 grid((unsigned)((a.T + block.y - 1) / block.y));
-  kern[(even ? 0 : 4) + (a.residual_bf16 ? 2 : 0) + (a.branch_bf16 ? 1 : 0)]<<<grid, block, 0, stream>>>(
-      a, off_step, weights16);
-  return cudaGetLastError();
+  return launch_pdl(kern[(even ? 0 : 4) + (a.residual_bf16 ? 2 : 0) + (a.branch_bf16 ? 1 : 0)], grid, block, 0, stream,
+                    a, off_step, weights16);
 }
 
 // Whether a tensor's rows begin where those of stride `ld0` do, between two
@@ -403,8 +406,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormMaxD * 4);
     if (err != cudaSuccess) return err;
     const int nt = std::min(1024, (a.D + 127) / 128 * 32);
-    block_norm_any_kernel<<<a.T, nt, (size_t)a.D * 4, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(block_norm_any_kernel, dim3((unsigned)a.T), dim3(nt), (size_t)a.D * 4, stream, a);
   }
   const bool weights16 = aligned(a.post.weight, 16) && aligned(a.post.bias, 16) && aligned(a.pre.weight, 16) &&
                          aligned(a.pre.bias, 16) && (gate_row || aligned(a.gate, 16));

@@ -301,6 +301,8 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   constexpr int kN = Vec<kBf16>::kN;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  umma::pdl_launch_dependents();
+  umma::pdl_wait();
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const Row<kBf16> x(static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.ld * (kBf16 ? 2 : 4), a.V);
   const float c = a.scale * kLog2e;
@@ -487,12 +489,14 @@ cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps,
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<kBf16>, a, cluster, segs, steps);
 }
 

@@ -26,12 +26,13 @@ namespace {
 constexpr int kTile = 16;                 // rows of an item of a call of few rows, all of one adapter
 constexpr int kRouteThreads = 1024;
 constexpr int kThreads = 256;
+constexpr int kMaxCluster = kLoraMaxCluster;
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 // ---- rows by adapter ---------------------------------------------------------
 // One block.  Its first `segs` warps take a stretch of the rows each and count them
-// by adapter in a table of their own; the counts' sums over warps and adapters
+// by adapter in a column of the table; the counts' sums over warps and adapters
 // give every row a place that keeps the rows' order, so that a prompt's rows stay
 // together and the items are the same from run to run.
 __global__ void __launch_bounds__(kRouteThreads)
@@ -39,52 +40,67 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
   extern __shared__ int smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int buckets = a.n_adapters + 1;   // the last: no adapter
-  int* table = smem;                      // [segs][buckets]
-  int* home = smem + segs * buckets;      // [buckets]: an adapter's bucket (itself, or none), -1 for a bad rank
+  const int pitch = segs + 1;             // [buckets][segs]: a warp's rows of a bucket, then its next place among them
+  int* table = smem;
+  int* home = smem + pitch * buckets;     // [buckets]: an adapter's bucket (itself, or none), -1 for a bad rank
+  int* first = home + buckets;            // [buckets]: the bucket's first place
   __shared__ int2 warp_sums[32];
   __shared__ int2 carry;
   umma::pdl_launch_dependents();
-  for (int i = tid; i < segs * buckets; i += kRouteThreads) table[i] = 0;
+  umma::pdl_wait();
+  const int seg = ((a.M + segs - 1) / segs + 31) / 32 * 32;
+  const int begin = min(warp * seg, a.M), end = warp < segs ? min(begin + seg, a.M) : begin;
+  constexpr int kAhead = 4;               // loads under way
+  int id[kAhead];
+  auto load_ids = [&](int m0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = m0 + u * 32 + lane < end ? a.ids[m0 + u * 32 + lane] : -1;
+  };
+  load_ids(begin);
+  for (int i = tid; i < pitch * buckets; i += kRouteThreads) table[i] = 0;
   for (int b = tid; b < buckets; b += kRouteThreads) {
     const int r = a.ranks != nullptr && b < a.n_adapters ? a.ranks[b] : 1;
     home[b] = r < 0 || r > a.max_rank ? -1 : r == 0 ? a.n_adapters : b;
   }
   if (tid == 0) carry = make_int2(0, 0);
   __syncthreads();
-  const int seg = ((a.M + segs - 1) / segs + 31) / 32 * 32;
-  const int begin = min(warp * seg, a.M), end = warp < segs ? min(begin + seg, a.M) : begin;
-  constexpr int kAhead = 4;               // loads under way
-  // the bucket of row m with adapter `id`; -1 past the rows
-  auto bucket_of = [&](int m, int id, bool report) {
+  // the bucket of row m with adapter `of`; -1 past the rows
+  auto bucket_of = [&](int m, int of, bool report) {
     if (m >= end) return -1;
-    if (id == -1) return a.n_adapters;
-    const int b = id < 0 || id >= a.n_adapters ? -1 : home[id];
+    if (of == -1) return a.n_adapters;
+    const int b = of < 0 || of >= a.n_adapters ? -1 : home[of];
     if (b >= 0) return b;
     if (report) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     return a.n_adapters;
   };
   for (int m0 = begin; m0 < end; m0 += 32 * kAhead) {
-    int id[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) id[u] = m0 + u * 32 + lane < end ? a.ids[m0 + u * 32 + lane] : -1;
+    if (m0 != begin) load_ids(m0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int b = bucket_of(m0 + u * 32 + lane, id[u], true);
       const uint32_t same = __match_any_sync(0xffffffffu, b);
-      if (b >= 0 && lane == __ffs(same) - 1) table[warp * buckets + b] += __popc(same);
+      if (b >= 0 && lane == __ffs(same) - 1) table[b * pitch + warp] += __popc(same);
       __syncwarp();
     }
   }
   __syncthreads();
+  // per bucket: places of the warps' rows among its rows, and their number behind them
+  for (int b = warp; b < buckets; b += kRouteThreads / 32) {
+    const int n = lane < segs ? table[b * pitch + lane] : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    __syncwarp();
+    if (lane < segs) table[b * pitch + lane] = s - n;
+    if (lane == 31) table[b * pitch + segs] = s;
+  }
+  __syncthreads();
   for (int b0 = 0; b0 < buckets; b0 += kRouteThreads) {
     const int b = b0 + tid;
-    int n = 0;
-    if (b < buckets)
-      for (int s = 0; s < segs; ++s) {
-        const int c = table[s * buckets + b];
-        table[s * buckets + b] = n;
-        n += c;
-      }
+    const int n = b < buckets ? table[b * pitch + segs] : 0;
     const bool none = b == a.n_adapters;
     const int t = none && !copy_none ? 0 : (n + kLoraTile - 1) / kLoraTile;
     int2 s = make_int2(n, t);
@@ -97,35 +113,33 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
     __syncthreads();
     int2 before = carry;
     for (int i = 0; i < warp; ++i) before.x += warp_sums[i].x, before.y += warp_sums[i].y;
-    const int first = before.x + s.x - n, tile0 = before.y + s.y - t;
+    const int start = before.x + s.x - n, tile0 = before.y + s.y - t;
+    if (b < buckets) first[b] = start;
     if (none) w.head[0] = tile0, w.head[1] = tile0 + t;
     // an adapter's tiles, by its warp
     for (uint32_t left = __ballot_sync(0xffffffffu, t > 0); left != 0; left &= left - 1) {
       const int l = __ffs(left) - 1;
       const int lt = __shfl_sync(0xffffffffu, t, l), ln = __shfl_sync(0xffffffffu, n, l);
-      const int lf = __shfl_sync(0xffffffffu, first, l), l0 = __shfl_sync(0xffffffffu, tile0, l);
+      const int lf = __shfl_sync(0xffffffffu, start, l), l0 = __shfl_sync(0xffffffffu, tile0, l);
       const int lb = b0 + warp * 32 + l;
       for (int i = lane; i < lt; i += 32)
         w.tiles[l0 + i] =
             make_int4(lb == a.n_adapters ? -1 : lb, lf + i * kLoraTile, min(kLoraTile, ln - i * kLoraTile), 0);
     }
-    if (b < buckets)
-      for (int s2 = 0; s2 < segs; ++s2) table[s2 * buckets + b] += first;
     __syncthreads();
-    if (tid == kRouteThreads - 1) carry = make_int2(first + n, tile0 + t);
+    if (tid == kRouteThreads - 1) carry = make_int2(start + n, tile0 + t);
     __syncthreads();
   }
+  const bool once = begin + 32 * kAhead >= end;   // the ids are still at hand
   for (int m0 = begin; m0 < end; m0 += 32 * kAhead) {
-    int id[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) id[u] = m0 + u * 32 + lane < end ? a.ids[m0 + u * 32 + lane] : -1;
+    if (!once) load_ids(m0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int m = m0 + u * 32 + lane, b = bucket_of(m, id[u], false);
       const uint32_t same = __match_any_sync(0xffffffffu, b);
-      if (b >= 0) w.rows[table[warp * buckets + b] + __popc(same & ((1u << lane) - 1u))] = m;
+      if (b >= 0) w.rows[first[b] + table[b * pitch + warp] + __popc(same & ((1u << lane) - 1u))] = m;
       __syncwarp();
-      if (b >= 0 && lane == __ffs(same) - 1) table[warp * buckets + b] += __popc(same);
+      if (b >= 0 && lane == __ffs(same) - 1) table[b * pitch + warp] += __popc(same);
       __syncwarp();
     }
   }
@@ -304,13 +318,7 @@ QMM_DEV int4 own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int
   int id = INT_MIN;                       // past the rows
   if (t < a.M) {
     id = a.ids[t];
-    bool bad = id < -1 || id >= a.n_adapters;
-    if (!bad && id >= 0 && a.ranks != nullptr) {
-      const int r = a.ranks[id];
-      bad = r < 0 || r > a.max_rank;
-      if (r == 0) id = -1;
-    }
-    if (bad) {
+    if (id < -1 || id >= a.n_adapters) {
       if (blockIdx.x == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
       id = -1;
     }
@@ -365,12 +373,20 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   uint16_t* lo = hi + kTile * hs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int item = blockIdx.x / cluster, block = blockIdx.x % cluster;
+  umma::pdl_launch_dependents();
+  umma::pdl_wait();
   const int4 it = own_item(a, item, copy_none, sm.ids, sm.rows, sm.scratch);
   if (it.z == 0) return;
   __syncthreads();
   const int units = (a.N + 31) / 32;
   const int n0 = (int)((int64_t)units * block / cluster), n1 = (int)((int64_t)units * (block + 1) / cluster);
-  if (it.x < 0) {                                          // no adapter: base as it is
+  int rank = it.x < 0 ? 0 : a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
+  if (rank < 0 || rank > a.max_rank) {
+    if (block == 0 && tid == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+    rank = 0;
+  }
+  if (rank == 0) {                                         // no adapter: base as it is
+    if (!copy_none) return;
     for (int r = warp; r < it.z; r += kThreads / 32) {
       const int64_t m = sm.rows[r];
       for (int c = n0 * 32 + lane * 4; c < min(n1 * 32, a.N); c += 128)
@@ -379,12 +395,19 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
     }
     return;
   }
-  const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
   const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
   const int64_t m0 = g < it.z ? sm.rows[g] : -1, m1 = g + 8 < it.z ? sm.rows[g + 8] : -1;   // this lane's rows
   const __nv_bfloat16* x0 = m0 >= 0 ? a.X + m0 * a.ldx : nullptr;
   const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
   const __nv_bfloat16* A = a.A + it.x * a.a_slot;
+  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
+  // what the second product reads is on its way into L2 meanwhile
+  const int cols0 = n0 * 32, cols1 = min(n1 * 32, a.N);
+  for (int c = cols0 + tid; c < cols1; c += kThreads)
+    for (int j = 0; j < rank; j += 64) umma::prefetch_l2(B + c * a.b_row + j);
+  if (a.base != nullptr)
+    for (int r = warp; r < it.z; r += kThreads / 32)
+      for (int c = cols0 + lane * 32; c < cols1; c += 1024) umma::prefetch_l2(a.base + (int64_t)sm.rows[r] * a.ldb + c);
   const int chunks = (a.K + 31) / 32;
   constexpr int kWarps = kThreads / 32;
   const int part = block * kWarps + warp, parts = cluster * kWarps;
@@ -417,15 +440,7 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
     for (int i = block + cluster * tid; i < kTile * 16; i += cluster * kThreads) {
       const int r = i / 16, j = i % 16 * 4;
       const uint32_t at = part_addr + (uint32_t)((r * 68 + j) * 4);
-      float4 s = make_float4(0, 0, 0, 0);
-      for (int o = 0; o < cluster; ++o) {                  // in order: the same sums every time
-        float4 v;
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(umma::mapa_shared(at, o))
-                     : "memory");
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-      }
+      float4 s = cluster_sum(at, cluster);
       s.x = j0 + j < rank ? s.x * scale : 0.f;
       s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
       s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
@@ -447,7 +462,6 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
     }
     umma::cluster_sync();
   }
-  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
   if (rank <= 32) outer_part<kVec, 1>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
   else if (rank <= 64) outer_part<kVec, 2>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
   else outer_part<kVec, 0>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
@@ -469,12 +483,14 @@ cudaError_t launch_rows(const LoraArgs& a, int items, int cluster, bool copy_non
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes(rs);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel<kVec>, a, rs, cluster, copy_none);
 }
 
@@ -491,7 +507,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t str
   const bool copy_none = a.base != a.out;
   if (a.M <= kOwnRows) {
     const int items = (int)std::min<int64_t>(a.M, std::min<int64_t>(a.n_adapters + 1, a.M) + a.M / kTile);
-    int cluster = 8;                                       // two blocks per SM in all
+    int cluster = kMaxCluster;                             // two blocks per SM in all
     while (cluster > 1 && items * cluster > 2 * attn_sm_count()) cluster /= 2;
     const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                      (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
@@ -513,9 +529,10 @@ cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t str
   cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_route_kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem);
   if (err != cudaSuccess) return err;
-  const int buckets = a.n_adapters + 1, segs = std::min(32, kRouteSmem / 4 / buckets - 1);
-  lora_route_kernel<<<1, kRouteThreads, (size_t)(segs + 1) * buckets * 4, stream>>>(a, w, copy_none, segs);
-  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  const int buckets = a.n_adapters + 1, segs = std::min(32, kRouteSmem / 4 / buckets - 3);
+  if ((err = launch_pdl(lora_route_kernel, dim3(1), dim3(kRouteThreads), (size_t)(segs + 3) * buckets * 4, stream, a,
+                        w, copy_none, segs)) != cudaSuccess)
+    return err;
   return launch_lora_products(a, w, copy_none, stream);
 }
 

@@ -32,11 +32,12 @@ QMM_DEV uint32_t two_bf16(float lo, float hi) {
 // A cluster takes a tile, its blocks a part of K each.  A block's threads copy the
 // rows' 16-byte pieces (rows lie anywhere) and the adapter's into the swizzled
 // layout of the operands, several stages ahead; one thread issues the products of
-// a stage for all ranks at once.  The blocks' sums meet over shared memory, 64
+// a stage for all ranks at once.  The blocks' sums meet over shared memory, 128
 // ranks at a time: each block adds up its share of the rows, in order, and writes
 // their two terms.
 constexpr int kInnerThreads = 256;
-constexpr int kInnerPitch = 64 + 4;                         // floats of a row of sums
+constexpr int kInnerRanks = 128;                            // whose sums meet at a time
+constexpr int kInnerPitch = kInnerRanks + 4;                // floats of a row of sums
 constexpr int kInnerSums = 128 * kInnerPitch * 4;
 constexpr int kInnerMaxStages = 4;
 
@@ -152,12 +153,12 @@ lora_inner_kernel(const InnerParams p) {
     float* sums = reinterpret_cast<float*>(smem);           // [128][kInnerPitch]
     const uint32_t sums_addr = smem_u32(sums);
     const int q = warp & 3, half = warp >> 2;
-    for (int j0 = 0; j0 < rank; j0 += 64) {
-      if (32 * q < it.z && j0 + 32 * half < n16) {
+    for (int j0 = 0; j0 < rank; j0 += kInnerRanks) {
+      for (int jj = 32 * half; jj < kInnerRanks && 32 * q < it.z && j0 + jj < n16; jj += 64) {
         uint32_t r[32];
-        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(j0 + 32 * half), r);
+        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(j0 + jj), r);
         tmem_wait_ld();
-        float* to = sums + (32 * q + lane) * kInnerPitch + 32 * half;
+        float* to = sums + (32 * q + lane) * kInnerPitch + jj;
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
           *reinterpret_cast<uint4*>(to + i) =
@@ -165,20 +166,11 @@ lora_inner_kernel(const InnerParams p) {
       }
       tc_fence_before();
       cluster_sync();
-      for (int i = block + p.cluster * tid; i < it.z * 16; i += p.cluster * kInnerThreads) {
-        const int r = i / 16, j = i % 16 * 4;
+      const int quads = min(kInnerRanks, p.rs - j0) / 4;    // of four ranks, in a row
+      for (int i = block + p.cluster * tid; i < it.z * quads; i += p.cluster * kInnerThreads) {
+        const int r = i / quads, j = i % quads * 4;
         float4 s = make_float4(0, 0, 0, 0);
-        if (j0 + j < n16) {
-          const uint32_t at = sums_addr + (uint32_t)(r * kInnerPitch + j) * 4;
-          for (int o = 0; o < p.cluster; ++o) {             // in order: the same sums every time
-            float4 v;
-            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                         : "r"(mapa_shared(at, o))
-                         : "memory");
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-          }
-        }
+        if (j0 + j < n16) s = cluster_sum(sums_addr + (uint32_t)(r * kInnerPitch + j) * 4, p.cluster);
         s.x = j0 + j < rank ? s.x * scale : 0.f;
         s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
         s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
@@ -482,7 +474,7 @@ cudaError_t launch_inner(const LoraArgs& a, const LoraWork& w, cudaStream_t stre
   // blocks of a tile: those of the tiles that the rows fill are on the GPU at once
   const int64_t filled = (a.M + kLoraTile - 1) / kLoraTile;
   const int chunks = (a.K + kChunk - 1) / kChunk, fit = 2 * attn_sm_count();
-  p.cluster = 8;
+  p.cluster = kLoraMaxCluster;
   while (p.cluster > 1 && (filled * p.cluster > fit || 2 * p.cluster > chunks)) p.cluster /= 2;
   const int64_t most = lora_max_tiles(a.M, a.n_adapters);
   const int clusters = (int)std::min<int64_t>(most, std::max(1, fit / p.cluster));

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "beside.h"
+#include "umma.cuh"
 
 namespace qmm {
 
@@ -18,6 +19,27 @@ struct LoraWork {
 inline int lora_rank_stride(int64_t max_rank) { return (int)((max_rank + 63) / 64 * 64); }
 inline int64_t lora_max_tiles(int64_t M, int64_t n_adapters) {
   return M / kLoraTile + (n_adapters + 1 < M ? n_adapters + 1 : M);
+}
+
+constexpr int kLoraMaxCluster = 8;
+// The sum over a cluster's blocks, in order, of the four floats at one place of
+// their shared memory; all loads under way before the first addition.
+QMM_DEV float4 cluster_sum(uint32_t addr, int cluster) {
+  float4 v[kLoraMaxCluster];
+#pragma unroll
+  for (int o = 0; o < kLoraMaxCluster; ++o) {
+    v[o] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (o < cluster)
+      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(v[o].x), "=f"(v[o].y), "=f"(v[o].z), "=f"(v[o].w)
+                   : "r"(umma::mapa_shared(addr, o))
+                   : "memory");
+  }
+  float4 s = v[0];
+#pragma unroll
+  for (int o = 1; o < kLoraMaxCluster; ++o)
+    if (o < cluster) s.x += v[o].x, s.y += v[o].y, s.z += v[o].z, s.w += v[o].w;
+  return s;
 }
 
 // both products of a routed call (lora_umma.cu)
