@@ -186,8 +186,8 @@ QMM_DEV void store4(float* row, int col, int N, float4 v) {
 // lane: which k a fragment position stands for is free as long as both operands
 // agree.  All loads of kU chunks are under way before the first product.
 template <int kNT, int kU>
-QMM_DEV void inner_part(const LoraArgs& a, const __nv_bfloat16* x0, const __nv_bfloat16* x1,
-                        const __nv_bfloat16* A, int rank, int j0, int c0, int c1, float (&acc)[8][4]) {
+QMM_DEV void inner_part(const LoraArgs& a, const __nv_bfloat16* x0, const __nv_bfloat16* x1, const __nv_bfloat16* A,
+                        int rank, int j0, int c0, int c1, float (&acc)[8][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int c = c0; c < c1; c += kU) {
@@ -216,106 +216,135 @@ QMM_DEV void inner_part(const LoraArgs& a, const __nv_bfloat16* x0, const __nv_b
 
 // A warp's part of out: 16 rows, units of 32 columns from u0 in steps of `step`.
 // Columns are dealt to fragment positions so that a lane's accumulators are four
-// neighbouring columns of a row.  The next unit's base is under way during the
+// neighbouring columns of a row.  What the first unit reads is asked for by
+// start(), long before h is there; the next unit's base is under way during the
 // products of one.  kRC: chunks of 32 ranks, whose h stays in registers; 0: any.
 template <bool kVec, int kRC>
-QMM_DEV void outer_part(const LoraArgs& a, const __nv_bfloat16* B, int rank, const uint16_t* hi, const uint16_t* lo,
-                        int hs, int r0, int64_t m0, int64_t m1, int u0, int u1, int step) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const float4 none = make_float4(0, 0, 0, 0);
-  const int chunks = kRC > 0 ? kRC : (rank + 31) / 32;
-  constexpr int kHeld = kRC > 0 ? kRC : 1;
-  uint4 h[kHeld][4];
-  auto load_h = [&](int c, uint4 (&to)[4]) {
-    const int j = c * 32 + 8 * tig;
-    to[0] = *reinterpret_cast<const uint4*>(hi + r0 * hs + j);
-    to[1] = *reinterpret_cast<const uint4*>(hi + (r0 + 8) * hs + j);
-    to[2] = *reinterpret_cast<const uint4*>(lo + r0 * hs + j);
-    to[3] = *reinterpret_cast<const uint4*>(lo + (r0 + 8) * hs + j);
-  };
-  if constexpr (kRC > 0) {
-#pragma unroll
-    for (int c = 0; c < kRC; ++c) load_h(c, h[c]);
-  }
-  auto load_base = [&](int u, float4 (&y)[2][2]) {
+struct Outer {
+  const LoraArgs& a;
+  const __nv_bfloat16* B;
+  int rank;
+  int64_t m0, m1;
+  int u0, u1, step;
+  uint4 b[kRC > 0 ? kRC : 2][4];
+  float4 y[2][2];
+
+  QMM_DEV void load_base(int u, float4 (&to)[2][2]) const {
+    const int tig = threadIdx.x & 3;
+    const float4 none = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int col = u * 32 + 16 * p + 4 * tig;
-      y[0][p] = a.base != nullptr && m0 >= 0 && u < u1 ? load4<kVec>(a.base + m0 * a.ldb, col, a.N) : none;
-      y[1][p] = a.base != nullptr && m1 >= 0 && u < u1 ? load4<kVec>(a.base + m1 * a.ldb, col, a.N) : none;
+      to[0][p] = a.base != nullptr && m0 >= 0 && u < u1 ? load4<kVec>(a.base + m0 * a.ldb, col, a.N) : none;
+      to[1][p] = a.base != nullptr && m1 >= 0 && u < u1 ? load4<kVec>(a.base + m1 * a.ldb, col, a.N) : none;
     }
-  };
-  auto load_b = [&](int u, int c, uint4 (&b)[4]) {
+  }
+  QMM_DEV void load_b(int u, int c, uint4 (&to)[4]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int col = u * 32 + 16 * (n >> 1) + 4 * (g >> 1) + (g & 1) + 2 * (n & 1), j = c * 32 + 8 * tig;
-      b[n] = j < rank && col < a.N ? ldg128(B + col * a.b_row + j) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  float4 y[2][2], next[2][2];
-  load_base(u0, y);
-  for (int u = u0; u < u1; u += step) {
-    float acc[4][4] = {};
-    if constexpr (kRC > 0) {
-      uint4 b[kRC][4];
-#pragma unroll
-      for (int c = 0; c < kRC; ++c) load_b(u, c, b[c]);
-      load_base(u + step, next);
-#pragma unroll
-      for (int c = 0; c < kRC; ++c)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 v = keep8(b[c][n], rank - c * 32 - 8 * tig);
-          mma_bf16_16816(acc[n], h[c][2].x, h[c][3].x, h[c][2].y, h[c][3].y, v.x, v.y);
-          mma_bf16_16816(acc[n], h[c][2].z, h[c][3].z, h[c][2].w, h[c][3].w, v.z, v.w);
-          mma_bf16_16816(acc[n], h[c][0].x, h[c][1].x, h[c][0].y, h[c][1].y, v.x, v.y);
-          mma_bf16_16816(acc[n], h[c][0].z, h[c][1].z, h[c][0].w, h[c][1].w, v.z, v.w);
-        }
-    } else {
-      uint4 b[2][4];
-      load_b(u, 0, b[0]);
-      load_base(u + step, next);
-      for (int c = 0; c < chunks; c += 2) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (c + e >= chunks) break;
-          load_b(u, c + e + 1, b[e ^ 1]);
-          load_h(c + e, h[0]);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint4 v = keep8(b[e][n], rank - (c + e) * 32 - 8 * tig);
-            mma_bf16_16816(acc[n], h[0][2].x, h[0][3].x, h[0][2].y, h[0][3].y, v.x, v.y);
-            mma_bf16_16816(acc[n], h[0][2].z, h[0][3].z, h[0][2].w, h[0][3].w, v.z, v.w);
-            mma_bf16_16816(acc[n], h[0][0].x, h[0][1].x, h[0][0].y, h[0][1].y, v.x, v.y);
-            mma_bf16_16816(acc[n], h[0][0].z, h[0][1].z, h[0][0].w, h[0][1].w, v.z, v.w);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int col = u * 32 + 16 * p + 4 * tig;
-      const float(&e)[4] = acc[2 * p], (&f)[4] = acc[2 * p + 1];
-      if (m0 >= 0)
-        store4<kVec>(a.out + m0 * a.ldo, col, a.N,
-                     make_float4(y[0][p].x + e[0], y[0][p].y + e[1], y[0][p].z + f[0], y[0][p].w + f[1]));
-      if (m1 >= 0)
-        store4<kVec>(a.out + m1 * a.ldo, col, a.N,
-                     make_float4(y[1][p].x + e[2], y[1][p].y + e[3], y[1][p].z + f[2], y[1][p].w + f[3]));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) y[i][p] = next[i][p];
+      to[n] = j < rank && col < a.N && u < u1 ? ldg128(B + col * a.b_row + j) : make_uint4(0, 0, 0, 0);
     }
   }
-}
+  QMM_DEV void start() {
+    if constexpr (kRC > 0) {
+#pragma unroll
+      for (int c = 0; c < kRC; ++c) load_b(u0, c, b[c]);
+    } else {
+      load_b(u0, 0, b[0]);
+    }
+    load_base(u0, y);
+  }
+  QMM_DEV void products(float (&acc)[4][4], const uint4 (&h)[4], const uint4 (&w)[4], int left) const {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const uint4 v = keep8(w[n], left);
+      mma_bf16_16816(acc[n], h[2].x, h[3].x, h[2].y, h[3].y, v.x, v.y);
+      mma_bf16_16816(acc[n], h[2].z, h[3].z, h[2].w, h[3].w, v.z, v.w);
+      mma_bf16_16816(acc[n], h[0].x, h[1].x, h[0].y, h[1].y, v.x, v.y);
+      mma_bf16_16816(acc[n], h[0].z, h[1].z, h[0].w, h[1].w, v.z, v.w);
+    }
+  }
+  // h: rows of hs values, the two terms
+  QMM_DEV void finish(const uint16_t* hi, const uint16_t* lo, int hs) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    const int chunks = kRC > 0 ? kRC : (rank + 31) / 32;
+    uint4 h[kRC > 0 ? kRC : 1][4];
+    auto load_h = [&](int c, uint4 (&to)[4]) {
+      const int j = c * 32 + 8 * tig;
+      to[0] = *reinterpret_cast<const uint4*>(hi + g * hs + j);
+      to[1] = *reinterpret_cast<const uint4*>(hi + (g + 8) * hs + j);
+      to[2] = *reinterpret_cast<const uint4*>(lo + g * hs + j);
+      to[3] = *reinterpret_cast<const uint4*>(lo + (g + 8) * hs + j);
+    };
+    if constexpr (kRC > 0) {
+#pragma unroll
+      for (int c = 0; c < kRC; ++c) load_h(c, h[c]);
+    }
+    for (int u = u0; u < u1; u += step) {
+      float acc[4][4] = {};
+      float4 next[2][2];
+      if constexpr (kRC > 0) {
+        load_base(u + step, next);
+#pragma unroll
+        for (int c = 0; c < kRC; ++c) {
+          products(acc, h[c], b[c], rank - c * 32 - 8 * tig);
+          load_b(u + step, c, b[c]);
+        }
+      } else {
+        load_base(u + step, next);
+        for (int c = 0; c < chunks; c += 2) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (c + e >= chunks) break;
+            load_b(u, c + e + 1, b[e ^ 1]);
+            load_h(c + e, h[0]);
+            products(acc, h[0], b[e], rank - (c + e) * 32 - 8 * tig);
+          }
+        }
+        load_b(u + step, 0, b[0]);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int col = u * 32 + 16 * p + 4 * tig;
+        const float(&e)[4] = acc[2 * p], (&f)[4] = acc[2 * p + 1];
+        if (m0 >= 0)
+          store4<kVec>(a.out + m0 * a.ldo, col, a.N,
+                       make_float4(y[0][p].x + e[0], y[0][p].y + e[1], y[0][p].z + f[0], y[0][p].w + f[1]));
+        if (m1 >= 0)
+          store4<kVec>(a.out + m1 * a.ldo, col, a.N,
+                       make_float4(y[1][p].x + e[2], y[1][p].y + e[3], y[1][p].z + f[2], y[1][p].w + f[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[i][p] = next[i][p];
+      }
+    }
+  }
+};
 
-// The item of this cluster in a call of few rows, found by every block for
-// itself: row t opens an item when the number of earlier rows with its adapter is a
-// multiple of 16, and the item's rows are the next 16 of them.  Rows without
-// an adapter make items of their own.  Returns {adapter, -, rows} with the row
-// numbers in rows[]; rows = 0: no item left for this cluster.
-QMM_DEV int4 own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int* rows, int* scratch) {
+// An item of a call of few rows: up to 16 rows of one adapter.
+struct Item {
+  int rows, rank;   // rows 0: none left for this cluster; rank 0: no adapter
+  int adapter;
+  float scale;
+};
+
+// The item of this cluster, found by every block for itself: row t opens an item
+// when the number of earlier rows with its adapter is a multiple of 16, and the
+// item's rows are the next 16 of them.  Rows without an adapter make items of their
+// own.  The row numbers go to rows[].
+QMM_DEV Item own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int* rows, int* counts, int* ranks,
+                      float* scales, Item* found) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int id = INT_MIN;                       // past the rows
+  // the ids' loads and those of a small set's ranks and scales go together
+  const bool few = a.n_adapters <= kThreads;
+  int table_rank = a.max_rank;
+  float table_scale = 1.f;
+  if (few && t < a.n_adapters) {
+    if (a.ranks != nullptr) table_rank = a.ranks[t];
+    if (a.scales != nullptr) table_scale = a.scales[t];
+  }
   if (t < a.M) {
     id = a.ids[t];
     if (id < -1 || id >= a.n_adapters) {
@@ -325,44 +354,66 @@ QMM_DEV int4 own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int
     if (id < 0 && !copy_none) id = INT_MIN;
   }
   ids[t] = id;
-  if (t < 2) scratch[t] = -1;
+  ranks[t] = table_rank, scales[t] = table_scale;
+  if (t == 0) found->rows = 0;
   __syncthreads();
-  int before = 0;
-  for (int s = 0; s < warp * 32; s += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(ids + s);
-    before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+  int rank = 0;
+  float scale = 1.f;
+  if (id >= 0 && few) {
+    rank = ranks[id], scale = scales[id];
+  } else if (id >= 0) {
+    rank = a.ranks != nullptr ? a.ranks[id] : a.max_rank;
+    if (a.scales != nullptr) scale = a.scales[id];
   }
-  before += __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
+  int before = __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
+  if (warp * 32 < a.M) {
+#pragma unroll 8
+    for (int s = 0; s < warp * 32; s += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(ids + s);
+      before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+    }
+  }
   // items are numbered by the rows that open them
   const bool opens = id != INT_MIN && before % kTile == 0;
   const uint32_t flags = __ballot_sync(0xffffffffu, opens);
-  int* counts = scratch + 2;
   if (lane == 0) counts[warp] = __popc(flags);
   __syncthreads();
   int number = __popc(flags & ((1u << lane) - 1u));
   for (int w = 0; w < warp; ++w) number += counts[w];
-  if (opens && number == item) scratch[0] = id, scratch[1] = before;
+  if (opens && number == item) *found = Item{1 + before, rank, id, scale};   // rows: the first one's number, for now
   __syncthreads();
-  const int adapter = scratch[0], first = scratch[1];
-  if (first < 0) return make_int4(0, 0, 0, 0);
-  const bool mine = id == adapter && before >= first && before < first + kTile;
+  Item it = *found;
+  if (it.rows == 0) return it;
+  const int first = it.rows - 1;
+  const bool mine = id == it.adapter && before >= first && before < first + kTile;
   if (mine) rows[before - first] = t;
-  const int n = __syncthreads_count(mine);
-  return make_int4(adapter, 0, n, 0);
+  it.rows = __syncthreads_count(mine);
+  if (it.rank < 0 || it.rank > a.max_rank) {
+    if (t == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+    it.rank = 0;
+  }
+  return it;
 }
 
 struct alignas(16) Smem {
   float part[kThreads / 32][16][68];   // sums of a warp: 16 rows by 64 ranks; then of the block
   int rows[kTile];
   int ids[kThreads];
-  int scratch[2 + kThreads / 32];
+  int counts[kThreads / 32];
+  int ranks[kThreads];
+  float scales[kThreads];
+  Item found;
 };
 static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
 
+// The two halves of a barrier of the cluster's blocks.
+QMM_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+QMM_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // A cluster takes an item: up to 16 rows of one adapter.  First its blocks and
-// their warps share K; the sums meet over shared memory, each block finishing its
-// share of h and writing it, as two bf16 terms, to all blocks.  Then the blocks and
-// warps share the columns of out.
+// their warps share K; every block adds up the blocks' sums over shared memory, in
+// order, and keeps h as two bf16 terms.  Then the blocks and warps share the columns
+// of out.
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
 lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
@@ -375,19 +426,14 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   const int item = blockIdx.x / cluster, block = blockIdx.x % cluster;
   umma::pdl_launch_dependents();
   umma::pdl_wait();
-  const int4 it = own_item(a, item, copy_none, sm.ids, sm.rows, sm.scratch);
-  if (it.z == 0) return;
-  __syncthreads();
+  const Item it = own_item(a, item, copy_none, sm.ids, sm.rows, sm.counts, sm.ranks, sm.scales, &sm.found);
+  if (it.rows == 0) return;
+  const int rank = it.rank;
   const int units = (a.N + 31) / 32;
   const int n0 = (int)((int64_t)units * block / cluster), n1 = (int)((int64_t)units * (block + 1) / cluster);
-  int rank = it.x < 0 ? 0 : a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
-  if (rank < 0 || rank > a.max_rank) {
-    if (block == 0 && tid == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
-    rank = 0;
-  }
   if (rank == 0) {                                         // no adapter: base as it is
     if (!copy_none) return;
-    for (int r = warp; r < it.z; r += kThreads / 32) {
+    for (int r = warp; r < it.rows; r += kThreads / 32) {
       const int64_t m = sm.rows[r];
       for (int c = n0 * 32 + lane * 4; c < min(n1 * 32, a.N); c += 128)
         store4<kVec>(a.out + m * a.ldo, c, a.N,
@@ -395,101 +441,116 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
     }
     return;
   }
-  const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
-  const int64_t m0 = g < it.z ? sm.rows[g] : -1, m1 = g + 8 < it.z ? sm.rows[g + 8] : -1;   // this lane's rows
+  const int64_t m0 = g < it.rows ? sm.rows[g] : -1, m1 = g + 8 < it.rows ? sm.rows[g + 8] : -1;   // this lane's rows
   const __nv_bfloat16* x0 = m0 >= 0 ? a.X + m0 * a.ldx : nullptr;
   const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
-  const __nv_bfloat16* A = a.A + it.x * a.a_slot;
-  const __nv_bfloat16* B = a.B + it.x * a.b_slot;
-  // what the second product reads is on its way into L2 meanwhile
-  const int cols0 = n0 * 32, cols1 = min(n1 * 32, a.N);
-  for (int c = cols0 + tid; c < cols1; c += kThreads)
-    for (int j = 0; j < rank; j += 64) umma::prefetch_l2(B + c * a.b_row + j);
-  if (a.base != nullptr)
-    for (int r = warp; r < it.z; r += kThreads / 32)
-      for (int c = cols0 + lane * 32; c < cols1; c += 1024) umma::prefetch_l2(a.base + (int64_t)sm.rows[r] * a.ldb + c);
+  const __nv_bfloat16* A = a.A + it.adapter * a.a_slot;
+  const __nv_bfloat16* B = a.B + it.adapter * a.b_slot;
+  auto nothing = [] {};
   const int chunks = (a.K + 31) / 32;
   constexpr int kWarps = kThreads / 32;
   const int part = block * kWarps + warp, parts = cluster * kWarps;
   const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
-  const uint32_t part_addr = umma::smem_u32(sm.part), hi_addr = umma::smem_u32(hi), lo_addr = umma::smem_u32(lo);
-  for (int j0 = 0; j0 < rank; j0 += 64) {
+  const uint32_t part_addr = umma::smem_u32(sm.part);
+  // ranks j0 .. j0 + 63: the warp's sums, then all blocks'; `then` runs while these meet
+  auto inner = [&](int j0, auto then) {
     float acc[8][4] = {};
     const int left = rank - j0;
     if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
     else if (left <= 32) inner_part<4, 3>(a, x0, x1, A, rank, j0, c0, c1, acc);
     else inner_part<8, 2>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    if (j0 > 0) cluster_wait();                            // the last ranks' sums have been read everywhere
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       const int j = 8 * n + 2 * (lane & 3);
       *reinterpret_cast<float2*>(&sm.part[warp][g][j]) = make_float2(acc[n][0], acc[n][1]);
       *reinterpret_cast<float2*>(&sm.part[warp][g + 8][j]) = make_float2(acc[n][2], acc[n][3]);
     }
+    then();
     __syncthreads();
     // the block's sums, in place of its first warp's: four ranks a thread
-    {
-      const int r = tid / 16, j = tid % 16 * 4;
-      float4 s = *reinterpret_cast<const float4*>(&sm.part[0][r][j]);
-      for (int k = 1; k < kWarps; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.part[k][r][j]);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-      }
-      *reinterpret_cast<float4*>(&sm.part[0][r][j]) = s;
+    const int r = tid / 16, j = tid % 16 * 4;
+    float4 s = *reinterpret_cast<const float4*>(&sm.part[0][r][j]);
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(&sm.part[k][r][j]);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    umma::cluster_sync();
-    for (int i = block + cluster * tid; i < kTile * 16; i += cluster * kThreads) {
-      const int r = i / 16, j = i % 16 * 4;
-      const uint32_t at = part_addr + (uint32_t)((r * 68 + j) * 4);
-      float4 s = cluster_sum(at, cluster);
-      s.x = j0 + j < rank ? s.x * scale : 0.f;
-      s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
-      s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
-      s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
-      if (j0 + j < rs) {
-        const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
-        const uint32_t b0 = two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0));
-        const uint32_t b1 = two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1));
-        const uint32_t to = (uint32_t)(r * hs + j0 + j) * 2;
-        for (int o = 0; o < cluster; ++o) {
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(hi_addr + to, o)), "r"(a0),
-                       "r"(a1)
-                       : "memory");
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(umma::mapa_shared(lo_addr + to, o)), "r"(b0),
-                       "r"(b1)
-                       : "memory");
-        }
-      }
+    *reinterpret_cast<float4*>(&sm.part[0][r][j]) = s;
+    cluster_arrive();
+    cluster_wait();
+    s = cluster_sum(part_addr + (uint32_t)((r * 68 + j) * 4), cluster);
+    cluster_arrive();
+    s.x = j0 + j < rank ? s.x * it.scale : 0.f;
+    s.y = j0 + j + 1 < rank ? s.y * it.scale : 0.f;
+    s.z = j0 + j + 2 < rank ? s.z * it.scale : 0.f;
+    s.w = j0 + j + 3 < rank ? s.w * it.scale : 0.f;
+    if (j0 + j < rs) {
+      const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
+      *reinterpret_cast<uint2*>(hi + r * hs + j0 + j) = make_uint2(a0, a1);
+      *reinterpret_cast<uint2*>(lo + r * hs + j0 + j) =
+          make_uint2(two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0)),
+                     two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1)));
     }
-    umma::cluster_sync();
-  }
-  if (rank <= 32) outer_part<kVec, 1>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
-  else if (rank <= 64) outer_part<kVec, 2>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
-  else outer_part<kVec, 0>(a, B, rank, hi, lo, hs, g, m0, m1, n0 + warp, n1, kWarps);
+    __syncthreads();
+  };
+  auto all = [&](auto outer) {
+    inner(0, [&] { outer.start(); });
+    for (int j0 = 64; j0 < rank; j0 += 64) inner(j0, nothing);
+    outer.finish(hi, lo, hs);
+  };
+  if (rank <= 32) all(Outer<kVec, 1>{a, B, rank, m0, m1, n0 + warp, n1, kWarps});
+  else if (rank <= 64) all(Outer<kVec, 2>{a, B, rank, m0, m1, n0 + warp, n1, kWarps});
+  else all(Outer<kVec, 0>{a, B, rank, m0, m1, n0 + warp, n1, kWarps});
+  __syncwarp();
+  cluster_wait();                                          // no block leaves while another reads its sums
 }
 
 // Calls of up to this many rows find their items in the kernel itself.
 constexpr int kOwnRows = kThreads;
 
 template <bool kVec>
-cudaError_t launch_rows(const LoraArgs& a, int items, int cluster, bool copy_none, cudaStream_t stream) {
+cudaError_t launch_rows(const LoraArgs& a, int items, bool copy_none, cudaStream_t stream) {
   const int rs = (a.max_rank + 31) / 32 * 32;
   auto bytes = [](int stride) { return sizeof(Smem) + (size_t)2 * kTile * (stride + 8) * 2; };
   static std::atomic<uint64_t> done{0};
-  const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_rows_kernel<kVec>),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank));
+  cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_rows_kernel<kVec>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes(rs);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  // Blocks of an item: the more the better, as long as all items' are on the GPU at
+  // once (64 rows over 40 adapters at K = N = 4096: 4 blocks 17.4 us, 6 16.0, 8, which do
+  // not all fit, 21.7).  How many clusters of a size fit goes by how they pack into
+  // the GPU's parts: asked once per device and size, for the largest rank.
+  static std::atomic<int> fit[64][kMaxCluster + 1];
+  int dev = 0;
+  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+  int cluster = kMaxCluster;
+  for (; cluster > 1; --cluster) {
+    std::atomic<int>& known = fit[dev & 63][cluster];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      attr[0].val.clusterDim.x = cluster;
+      cfg.gridDim = dim3((unsigned)cluster);
+      cfg.numAttrs = 1;
+      cfg.dynamicSmemBytes = bytes((int)kLoraMaxRank);
+      if ((err = cudaOccupancyMaxActiveClusters(&n, lora_rows_kernel<kVec>, &cfg)) != cudaSuccess) return err;
+      known.store(n, std::memory_order_relaxed);
+      cfg.dynamicSmemBytes = bytes(rs);
+    }
+    if (items <= n) break;
+  }
+  attr[0].val.clusterDim.x = cluster;
+  cfg.gridDim = dim3((unsigned)(items * cluster));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel<kVec>, a, rs, cluster, copy_none);
 }
@@ -506,13 +567,11 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters,
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream) {
   const bool copy_none = a.base != a.out;
   if (a.M <= kOwnRows) {
-    const int items = (int)std::min<int64_t>(a.M, std::min<int64_t>(a.n_adapters + 1, a.M) + a.M / kTile);
-    int cluster = kMaxCluster;                             // two blocks per SM in all
-    while (cluster > 1 && items * cluster > 2 * attn_sm_count()) cluster /= 2;
+    // d adapters in use make d + (M - d) / 16 items at most
+    const int d = (int)std::min<int64_t>(a.n_adapters + 1, a.M), items = d + (a.M - d) / kTile;
     const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                      (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
-    return vec ? launch_rows<true>(a, items, cluster, copy_none, stream)
-               : launch_rows<false>(a, items, cluster, copy_none, stream);
+    return vec ? launch_rows<true>(a, items, copy_none, stream) : launch_rows<false>(a, items, copy_none, stream);
   }
   uint8_t* p = static_cast<uint8_t*>(workspace);
   LoraWork w;

@@ -166,9 +166,12 @@ lora_inner_kernel(const InnerParams p) {
       }
       tc_fence_before();
       cluster_sync();
+      // this block's rows, neighbouring lanes at neighbouring ranks: the other blocks'
+      // memory is read in whole rows (scattered 16-byte reads took 10 times as long)
+      const int share = (it.z + p.cluster - 1) / p.cluster, r0 = block * share;
       const int quads = min(kInnerRanks, p.rs - j0) / 4;    // of four ranks, in a row
-      for (int i = block + p.cluster * tid; i < it.z * quads; i += p.cluster * kInnerThreads) {
-        const int r = i / quads, j = i % quads * 4;
+      for (int i = tid; i < min(share, it.z - r0) * quads; i += kInnerThreads) {
+        const int r = r0 + i / quads, j = i % quads * 4;
         float4 s = make_float4(0, 0, 0, 0);
         if (j0 + j < n16) s = cluster_sum(sums_addr + (uint32_t)(r * kInnerPitch + j) * 4, p.cluster);
         s.x = j0 + j < rank ? s.x * scale : 0.f;
