@@ -11,9 +11,9 @@
 #include <algorithm>
 #include <atomic>
 
+#include "attn_umma.cuh"
 #include "kv_cache.h"
 #include "lora_work.cuh"
-#include "umma.cuh"
 
 namespace qmm {
 namespace {
@@ -201,14 +201,14 @@ lora_inner_kernel(const InnerParams p) {
 
 // ---- out = base + h B^T ----------------------------------------------------------
 // A block per SM walks over units of 128 rows by 128 columns.  One warp loads the
-// two terms of h and the rows of B by TMA, 64 ranks a stage, and issues the products
-// of both terms with the same B into one of four accumulators; two groups of eight
-// warps take the units in turn.  A warp owns 32 rows by 64 columns: their base values
+// two terms of h and the rows of B by TMA, 64 ranks a stage, and another issues the
+// products of both terms with the same B into one of four accumulators; two groups of
+// eight warps take the units in turn.  A warp owns 32 rows by 64 columns: their base values
 // are on their way into registers half a unit ahead, the accumulator goes through the
 // warp's corner of shared memory so that rows are read and written 128 bytes at a
 // time, and no warp waits for another.
 constexpr int kEpiWarps = 16;
-constexpr int kOuterThreads = (kEpiWarps + 1) * 32;
+constexpr int kOuterThreads = (kEpiWarps + 2) * 32;
 constexpr int kCols = 128;
 constexpr int kBuffers = 4;
 constexpr int kStages = 3;
@@ -226,23 +226,49 @@ struct OuterParams {
 
 // A unit of the walk.
 struct Unit {
-  int4 it;         // adapter, first place, rows; rows 0: past the end
-  int col0, rank, chunks;
+  int adapter, first, rows;   // -1: none; first place; 0: past the end
+  int rank, col0;
+  QMM_DEV int chunks() const { return (rank + kChunk - 1) / kChunk; }
 };
 
-QMM_DEV Unit unit_at(const OuterParams& p, uint32_t i, uint32_t units) {
-  Unit u;
-  u.it = make_int4(-1, 0, 0, 0);
-  u.col0 = u.rank = u.chunks = 0;
-  if (i < units) {
-    const uint32_t tile = i / (uint32_t)p.col_blocks;
-    u.it = p.w.tiles[tile];
-    u.col0 = (int)(i - tile * p.col_blocks) * kCols;
-    if (u.it.x >= 0) u.rank = p.a.ranks != nullptr ? p.a.ranks[u.it.x] : p.a.max_rank;
-    u.chunks = (u.rank + kChunk - 1) / kChunk;
+// The units first, first + step, .. of a warp's walk.  What they are is read for 32 of
+// them at a time, one per lane: one chain of dependent loads in 32 units.
+struct Walk {
+  const OuterParams& p;
+  uint32_t units, first, step;
+  uint32_t n = 0, batch = 0;   // of this walk: the unit at hand, the first of those in the lanes
+  Unit mine, at;
+
+  QMM_DEV Walk(const OuterParams& params, uint32_t all, uint32_t from, uint32_t by)
+      : p(params), units(all), first(from), step(by) {
+    fetch();
+    take();
   }
-  return u;
-}
+  QMM_DEV void fetch() {
+    const uint32_t i = first + (batch + (threadIdx.x & 31)) * step;
+    mine = Unit{-1, 0, 0, 0, 0};
+    if (i < units) {
+      const uint32_t tile = i / (uint32_t)p.col_blocks;
+      const int4 t = p.w.tiles[tile];
+      mine = Unit{t.x, t.y, t.z, 0, (int)(i - tile * p.col_blocks) * kCols};
+      if (t.x >= 0) mine.rank = p.a.ranks != nullptr ? p.a.ranks[t.x] : p.a.max_rank;
+    }
+  }
+  QMM_DEV void take() {
+    const int l = (int)(n - batch);
+    at = Unit{__shfl_sync(0xffffffffu, mine.adapter, l), __shfl_sync(0xffffffffu, mine.first, l),
+              __shfl_sync(0xffffffffu, mine.rows, l), __shfl_sync(0xffffffffu, mine.rank, l),
+              __shfl_sync(0xffffffffu, mine.col0, l)};
+  }
+  QMM_DEV bool there() const { return first + n * step < units; }
+  QMM_DEV void next() {
+    if (++n == batch + 32) {
+      batch = n;
+      fetch();
+    }
+    take();
+  }
+};
 
 template <bool kVec>
 __global__ void __launch_bounds__(kOuterThreads, 1)
@@ -275,48 +301,56 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
   const uint32_t units = (uint32_t)p.w.head[p.copy_none ? 1 : 0] * p.col_blocks;
 
   if (warp == kEpiWarps) {
-    // two walks over the stages: one fills them, one issues their products
-    uint32_t filled = 0, used = 0;
-    uint32_t buf_used = 0, buf_par = 0;                     // a bit per buffer: used before, parity of its release
-    uint32_t fi = blockIdx.x, mi = blockIdx.x;
-    Unit f = unit_at(p, fi, units), m = f;
-    int fc = 0, n = 0;
+    // fills the stages
+    Walk f(p, units, blockIdx.x, gridDim.x);
+    uint32_t filled = 0;
     bool ok = true;
-    auto next_fill = [&] {
-      while (fi < units && fc >= f.chunks) {
-        fi += gridDim.x;
-        f = unit_at(p, fi, units);
-        fc = 0;
-      }
-    };
-    next_fill();
-    for (; mi < units && ok; mi += gridDim.x, m = unit_at(p, mi, units), ++n) {
-      const int buf = n % kBuffers;
-      for (int c = 0; c < m.chunks && ok; ++c) {
-        while (ok && fi < units && filled < used + kStages - (used > 0)) {
-          const int s = filled % kStages;
-          if (filled >= kStages)
-            ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (filled / kStages - 1) & 1, &abort_flag, a.dev_status));
-          if (ok && lane == 0) {
-            uint8_t* to = smem + s * kStageBytes;
-            mbar_arrive_expect_tx(&full[s], kStageBytes);
-            tma_load_2d(to, &tmH, &full[s], fc * kChunk, f.it.y);
-            tma_load_2d(to + kTileBytes16, &tmH, &full[s], p.rs + fc * kChunk, f.it.y);
-            tma_load_3d(smem_u32(to + 2 * kTileBytes16), &tmB, &full[s], fc * kChunk, f.col0, f.it.x);
-          }
-          if (ok) ++filled, ++fc;
-          next_fill();
+    for (; f.there() && ok; f.next()) {
+      const int chunks = f.at.chunks();
+      for (int c = 0; c < chunks && ok; ++c, ++filled) {
+        const int s = filled % kStages;
+        if (filled >= kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (filled / kStages - 1) & 1, &abort_flag, a.dev_status));
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* to = smem + s * kStageBytes;
+          mbar_arrive_expect_tx(&full[s], kStageBytes);
+          tma_load_2d(to, &tmH, &full[s], c * kChunk, f.at.first);
+          tma_load_2d(to + kTileBytes16, &tmH, &full[s], p.rs + c * kChunk, f.at.first);
+          tma_load_3d(smem_u32(to + 2 * kTileBytes16), &tmB, &full[s], c * kChunk, f.at.col0, f.at.adapter);
         }
-        const int s = used % kStages;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (used / kStages) & 1, &abort_flag, a.dev_status));
-        if (ok && c == 0 && (buf_used >> buf & 1)) {
+        __syncwarp();
+      }
+    }
+    // copies already issued land before the block leaves
+    if (!ok)
+      for (uint32_t u = filled > kStages ? filled - kStages : 0; u < filled; ++u)
+        mbar_drain(&full[u % kStages], (u / kStages) & 1);
+  } else if (warp == kEpiWarps + 1) {
+    // issues the products: all lanes in step, one elected
+    const uint32_t one = elect_one();
+    uint32_t used = 0;
+    uint32_t buf_used = 0, buf_par = 0;                     // a bit per buffer: used before, parity of its release
+    Walk m(p, units, blockIdx.x, gridDim.x);
+    bool ok = true;
+    for (int n = 0; m.there() && ok; m.next(), ++n) {
+      const int chunks = m.at.chunks(), rank = m.at.rank;
+      const int buf = n % kBuffers;
+      if (chunks > 0) {
+        if (buf_used >> buf & 1) {
           ok = __all_sync(0xffffffffu, mbar_wait(&tempty[buf], buf_par >> buf & 1, &abort_flag, a.dev_status));
           buf_par ^= 1u << buf;
         }
+        buf_used |= 1u << buf;
+      }
+      const uint32_t d = tmem + buf * kCols;
+      for (int c = 0; c < chunks && ok; ++c, ++used) {
+        const int s = used % kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (used / kStages) & 1, &abort_flag, a.dev_status));
         if (!ok) break;
         uint8_t* at = smem + s * kStageBytes;
-        const int left = m.rank - c * kChunk;
-        if (left < kChunk && left % 16 != 0 && m.rank < a.max_rank) {
+        const int left = rank - c * kChunk;
+        if (left < kChunk && left % 16 != 0 && rank < a.max_rank) {
           // what lies behind the adapter's rank in the last step of 16: zeros, since 0
           // times an infinity or NaN is none (h is zero there)
           const int piece = left / 8;
@@ -337,47 +371,47 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) {
-          tc_fence_after();
-          constexpr uint32_t idesc = idesc_f16(128, kCols, true);
-          const int steps = min(kChunk / 16, (left + 15) / 16);
-          const uint64_t b = desc_kmajor_sw128(smem_u32(at + 2 * kTileBytes16));
-          for (int term = 1; term >= 0; --term) {           // the smaller one first
-            const uint64_t h = desc_kmajor_sw128(smem_u32(at + term * kTileBytes16));
-            for (int k = 0; k < steps; ++k)
-              umma_f16(tmem + buf * kCols, h + 2 * k, b + 2 * k, idesc, c > 0 || term == 0 || k > 0);
-          }
-          umma_commit(&empty[s]);
-          if (c == m.chunks - 1) umma_commit(&tfull[buf]);
-        }
-        __syncwarp();
-        ++used;
+        tc_fence_after();
+        constexpr uint32_t idesc = idesc_f16(128, kCols, true);
+        const uint64_t b = desc_kmajor_sw128(smem_u32(at + 2 * kTileBytes16));
+        const uint64_t hi = desc_kmajor_sw128(smem_u32(at)), lo = desc_kmajor_sw128(smem_u32(at + kTileBytes16));
+        const int steps = min(kChunk / 16, (left + 15) / 16);
+        // the smaller term first
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          if (k < steps) umma_f16_one(one, d, lo + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          if (k < steps) umma_f16_one(one, d, hi + 2 * k, b + 2 * k, idesc, 1);
+        umma_commit_one(one, &empty[s]);
+        if (c == chunks - 1) umma_commit_one(one, &tfull[buf]);
       }
-      if (m.chunks > 0) buf_used |= 1u << buf;
     }
-    // copies already issued land before the block leaves
-    if (!ok)
-      for (uint32_t u = filled > kStages ? filled - kStages : 0; u < filled; ++u)
-        mbar_drain(&full[u % kStages], (u / kStages) & 1);
   } else {
     const int group = warp / (kEpiWarps / 2), q = warp & 3, half = (warp >> 2) & 1;
     float* corner = reinterpret_cast<float*>(smem + kStages * kStageBytes + warp * kCorner);
     uint32_t parity = 0;                                    // of this group's buffers' next phases
-    // four values of row 32 q + 4 i + lane / 8: columns col(j) + 0..3, or in steps of eight
-    const int sub = lane >> 3, cl = kVec ? (lane & 7) * 4 : lane & 7;
-    auto row_of = [&](const Unit& u) {
-      const int r = 32 * q + lane;
-      return r < u.it.z ? p.w.rows[u.it.y + r] : -1;
+    // four values of row 32 q + 4 v + lane / 8: columns cl + 0..3, or in steps of eight
+    const int sub = lane >> 3, cl = half * 64 + (kVec ? (lane & 7) * 4 : lane & 7);
+    // The warp's rows of a unit: how many, and row numbers by lane; `run`: they follow
+    // one another, as a prompt's do, so that an address is the last one's plus a step.
+    struct Rows {
+      int n, id;
+      bool run;
+    };
+    auto rows_of = [&](const Unit& u) {
+      Rows r;
+      r.n = min(max(u.rows - 32 * q, 0), 32);
+      r.id = lane < r.n ? p.w.rows[u.first + 32 * q + lane] : 0;
+      return r;
+    };
+    auto runs = [&](Rows& r) {
+      const int id0 = __shfl_sync(0xffffffffu, r.id, 0);    // by all lanes, whatever they hold
+      r.run = __all_sync(0xffffffffu, lane >= r.n || r.id == id0 + lane);
     };
     // values of half a unit's columns, asked for half a unit ahead
-    float y[8][4];
-    auto load = [&](const Unit& u, int ids, int j, int v) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[v][e] = 0.f;
-      const int m = __shfl_sync(0xffffffffu, ids, 4 * v + sub);
-      if (a.base == nullptr || m < 0) return;
-      const int col = u.col0 + half * 64 + 32 * j + cl;
-      const float* from = a.base + (int64_t)m * a.ldb + col;
+    float y[8][4] = {};
+    auto load4 = [&](int v, const float* from, int col) {
       if constexpr (kVec) {
         if (col < a.N) {
           const float4 t = *reinterpret_cast<const float4*>(from);
@@ -389,25 +423,42 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
           if (col + 8 * e < a.N) y[v][e] = from[8 * e];
       }
     };
-    uint32_t i = blockIdx.x + group * gridDim.x;
-    Unit u = unit_at(p, i, units);
-    int ids = row_of(u);
+    auto load = [&](const Unit& u, const Rows& r, int j) {
+      if (a.base == nullptr) return;
+      const int col = u.col0 + 32 * j + cl;
+      if (r.run) {
+        const float* from = a.base + (int64_t)(__shfl_sync(0xffffffffu, r.id, 0) + sub) * a.ldb + col;
 #pragma unroll
-    for (int v = 0; v < 8; ++v) load(u, ids, 0, v);
-    for (int n = group; i < units; n += 2, i += 2 * gridDim.x) {
-      const Unit next = unit_at(p, i + 2 * gridDim.x, units);
-      const int next_ids = row_of(next);
+        for (int v = 0; v < 8; ++v, from += 4 * a.ldb)
+          if (4 * v + sub < r.n) load4(v, from, col);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const int m = __shfl_sync(0xffffffffu, r.id, 4 * v + sub);
+          if (4 * v + sub < r.n) load4(v, a.base + (int64_t)m * a.ldb + col, col);
+        }
+      }
+    };
+    Walk walk(p, units, blockIdx.x + group * gridDim.x, 2 * gridDim.x);
+    Unit u = walk.at;
+    Rows ur = rows_of(u);
+    runs(ur);
+    load(u, ur, 0);
+    for (int n = group; u.rows > 0; n += 2) {
+      walk.next();                                          // its rows are asked for long before they are needed
+      const Unit next = walk.at;
+      Rows nr = rows_of(next);
       const int buf = n % kBuffers;
-      if (u.chunks > 0) {
+      const bool sums = u.rank > 0;
+      if (sums) {
         const uint32_t par = parity >> buf & 1;
         parity ^= 1u << buf;
         if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], par, &abort_flag, a.dev_status))) break;
         tc_fence_after();
       }
-      const bool rows = 32 * q < u.it.z;                    // of this warp
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (u.chunks > 0 && rows) {
+        if (sums && ur.n > 0) {
 #pragma unroll
           for (int c = 0; c < 32; c += 16) {
             uint32_t r[16];
@@ -420,39 +471,46 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
           }
         }
         __syncwarp();
-        if (j == 1 && u.chunks > 0) {
+        if (j == 1 && sums) {
           tc_fence_before();
           if (lane == 0) mbar_arrive(&tempty[buf]);
         }
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const int m = __shfl_sync(0xffffffffu, ids, 4 * v + sub);
-          const int col = u.col0 + half * 64 + 32 * j + cl;
-          const float* d = corner + (4 * v + sub) * kPitch + cl;
-          if (m >= 0) {
-            float* to = a.out + (int64_t)m * a.ldo + col;
-            if constexpr (kVec) {
-              if (col < a.N) {
-                float4 s = make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
-                if (u.chunks > 0) {
-                  const float4 t = *reinterpret_cast<const float4*>(d);
-                  s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
-                }
-                *reinterpret_cast<float4*>(to) = s;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (col + 8 * e < a.N) to[8 * e] = u.chunks > 0 ? y[v][e] + d[8 * e] : y[v][e];
+        const int col = u.col0 + 32 * j + cl;
+        const float* d = corner + sub * kPitch + (cl & 31);
+        auto store4 = [&](int v, float* to) {
+          if constexpr (kVec) {
+            float4 s = make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
+            if (sums) {
+              const float4 t = *reinterpret_cast<const float4*>(d + 4 * v * kPitch);
+              s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
             }
+            if (4 * v + sub < ur.n && col < a.N) *reinterpret_cast<float4*>(to) = s;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (4 * v + sub < ur.n && col + 8 * e < a.N)
+                to[8 * e] = sums ? y[v][e] + d[4 * v * kPitch + 8 * e] : y[v][e];
           }
-          if (j == 0) load(u, ids, 1, v);
-          else load(next, next_ids, 0, v);
+        };
+        if (ur.run) {
+          float* to = a.out + (int64_t)(__shfl_sync(0xffffffffu, ur.id, 0) + sub) * a.ldo + col;
+#pragma unroll
+          for (int v = 0; v < 8; ++v, to += 4 * a.ldo) store4(v, to);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            store4(v, a.out + (int64_t)__shfl_sync(0xffffffffu, ur.id, 4 * v + sub) * a.ldo + col);
         }
         __syncwarp();
+        if (j == 0) {
+          load(u, ur, 1);
+        } else {
+          runs(nr);
+          load(next, nr, 0);
+        }
       }
       u = next;
-      ids = next_ids;
+      ur = nr;
     }
   }
   tc_fence_before();
