@@ -683,6 +683,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 _NORM_KINDS = {"rms": 1, "layer": 2}
 _OUT_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16, torch.int8: QMM_S8}
 _F32, _BF16 = torch.float32, torch.bfloat16
+_F32_ONLY, _BF16_ONLY, _INT32_ONLY = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+_empty = torch.empty
 _current_device = getattr(torch._C, "_cuda_getDevice", None)   # None: torch without CUDA
 
 # Every tensor has to lie on the current GPU: an address of another device or of
@@ -699,10 +701,12 @@ def _device_of(fn, t):
 
 def _rows(fn, dev, t, shape, types):
     """Row stride of a [rows][width] tensor with contiguous rows."""
-    if t.shape != shape or t.dtype not in types or t.get_device() != dev or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{fn}: expected {tuple(shape)} with contiguous rows of {[str(x) for x in types]} on device "
-                         f"{dev}, got {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
-    return t.stride(0)
+    if t.shape == shape and t.dtype in types and t.get_device() == dev:
+        ld, inner = t.stride()
+        if inner == 1 or shape[1] <= 1:
+            return ld
+    raise ValueError(f"{fn}: expected {tuple(shape)} with contiguous rows of {[str(x) for x in types]} on device "
+                     f"{dev}, got {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
 
 
 def _vector(fn, dev, t, size, dtype):
@@ -792,7 +796,7 @@ def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tenso
     fn = "lora_add"
     dev = _device_of(fn, X)
     M, K = shape = X.shape
-    ldx = _rows(fn, dev, X, shape, (_BF16,))
+    ldx = _rows(fn, dev, X, shape, _BF16_ONLY)
     slots, rank, k = A.shape
     b_slots, N, b_rank = B.shape
     a_slot, a_row, a_in = A.stride()
@@ -802,12 +806,12 @@ def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tenso
         raise ValueError("lora_add: A has to be bf16 [adapters][rank][K], B bf16 [adapters][N][rank], with "
                          "contiguous innermost values, for X [M][K], all on one device")
     out_shape = (M, N)
-    p_base, ldb = (None, 0) if base is None else (base.data_ptr(), _rows(fn, dev, base, out_shape, (_F32,)))
+    p_base, ldb = (None, 0) if base is None else (base.data_ptr(), _rows(fn, dev, base, out_shape, _F32_ONLY))
     if out is None:
         out = torch.empty(out_shape, dtype=_F32, device=X.device)
         ldo = N
     else:
-        ldo = _rows(fn, dev, out, out_shape, (_F32,))
+        ldo = _rows(fn, dev, out, out_shape, _F32_ONLY)
     weights = QmmLoraSet(A.data_ptr(), a_slot, a_row, B.data_ptr(), b_slot, b_row,
                          _vector(fn, dev, ranks, slots, _I32), _vector(fn, dev, scales, slots, _F32), slots, rank, K, N)
     if workspace is None:
@@ -833,41 +837,49 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
     dev = _device_of(fn, logits)
     M, V = shape = logits.shape
     ld = _rows(fn, dev, logits, shape, _ROW_TYPES)
+    device = logits.device
     G = ldt = 0
-    p_tokens = p_logprobs = p_ids = p_top = p_entropy = None
+    p_tokens = p_logprobs = p_ids = p_top = p_entropy = p_status = None
     if tokens is not None:
-        t = tokens.unsqueeze(1) if tokens.dim() == 1 else tokens
-        G = t.shape[1]
-        ldt, p_tokens = _rows(fn, dev, t, (M, G), (_I32,)), tokens.data_ptr()
-    if tokens is not None:
+        if tokens.dim() == 2:
+            G = tokens.shape[1]
+            ldt = _rows(fn, dev, tokens, (M, G), _INT32_ONLY)
+        else:
+            if tokens.shape != (M,) or tokens.dtype is not _I32 or tokens.get_device() != dev:
+                raise ValueError(f"{fn}: expected int32 tokens [{M}] or [{M}][G] on device {dev}, got "
+                                 f"{tuple(tokens.shape)} {tokens.dtype} on {tokens.device}")
+            G, ldt = 1, tokens.stride(0)
+        p_tokens = tokens.data_ptr()
         if logprobs is None:
-            logprobs = torch.empty(tokens.shape, dtype=_F32, device=logits.device)
+            logprobs = _empty(tokens.shape, dtype=_F32, device=device)
             p_logprobs = logprobs.data_ptr()
         else:
             p_logprobs = _vector(fn, dev, logprobs, M * G, _F32)
     if entropy is False:
         entropy = None
     elif entropy is None:
-        entropy = torch.empty(M, dtype=_F32, device=logits.device)
+        entropy = _empty(M, dtype=_F32, device=device)
         p_entropy = entropy.data_ptr()
     else:
         p_entropy = _vector(fn, dev, entropy, M, _F32)
     if top_k > 0:
         if top_ids is None:
-            top_ids = torch.empty((M, top_k), dtype=_I32, device=logits.device)
+            top_ids = _empty((M, top_k), dtype=_I32, device=device)
             p_ids = top_ids.data_ptr()
         else:
             p_ids = _vector(fn, dev, top_ids, M * top_k, _I32)
         if top_logprobs is None:
-            top_logprobs = torch.empty((M, top_k), dtype=_F32, device=logits.device)
+            top_logprobs = _empty((M, top_k), dtype=_F32, device=device)
             p_top = top_logprobs.data_ptr()
         else:
             p_top = _vector(fn, dev, top_logprobs, M * top_k, _F32)
     else:
         top_ids = top_logprobs = None
+    if dev_status is not None:
+        p_status = _vector(fn, dev, dev_status, 1, _I32)
     status = lib.qmm_token_logprobs(
         logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy, top_k,
-        p_ids, p_top, _vector(fn, dev, dev_status, 1, _I32), _raw_stream(dev))
+        p_ids, p_top, p_status, _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_token_logprobs", status)
     return logprobs, entropy, top_ids, top_logprobs
