@@ -15,6 +15,7 @@
 // tensors that do not go value by value.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "beside.h"
 #include "kv_cache.h"
@@ -100,20 +101,23 @@ struct Place {
   int e0;        // the first group's first element: a multiple of 4 less the row's offset
   int step;      // from a thread's group to its next
   int D;
+  float inv_d;
   QMM_DEV int at(int g) const { return e0 + g * step; }
   QMM_DEV bool some(int g) const { return at(g) < D; }   // a group may begin before the row, but not end there
   QMM_DEV bool whole(int g) const { return kOff ? at(g) >= 0 && at(g) + 4 <= D : at(g) < D; }
   QMM_DEV bool in(int g, int i) const { return kOff ? at(g) + i >= 0 && at(g) + i < D : at(g) < D; }
+  // no value of this thread's groups lies outside the row
+  QMM_DEV bool all() const { return kOff ? e0 >= 0 && at(kG - 1) + 4 <= D : at(kG - 1) < D; }
 };
 
 // A row's values of one tensor, zeros outside it.
 template <bool kBf16, int kG, bool kOff>
 QMM_DEV void load_row(const void* base, int64_t row, const Place<kG, kOff>& pl, Raw4<kBf16> (&raw)[kG]) {
   constexpr int kSize = kBf16 ? 2 : 4;
+  const uint8_t* p = static_cast<const uint8_t*>(base) + (row + pl.e0) * kSize;
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
+  for (int g = 0; g < kG; ++g, p += pl.step * kSize) {
     raw[g] = {};
-    const uint8_t* p = static_cast<const uint8_t*>(base) + (row + pl.at(g)) * kSize;
     if (pl.whole(g)) {
       raw[g].load(p);
     } else if (kOff && pl.some(g)) {
@@ -127,26 +131,38 @@ QMM_DEV void load_row(const void* base, int64_t row, const Place<kG, kOff>& pl, 
   }
 }
 
-// Four fp32 weights from element e0, cached for all rows.  Where rows begin at any
-// element, two aligned loads and a shift that is the same for the whole row.
+// Four fp32 weights of group g, cached for all rows; zeros outside the row.
 template <int kG, bool kOff>
 QMM_DEV void weights4(const float* w, const Place<kG, kOff>& pl, int g, bool aligned16, float (&x)[4]) {
-  const int e = pl.at(g);
+  const float* p = w + pl.at(g);
   if (!kOff && aligned16) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w + e));
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  } else if (kOff && aligned16 && e >= 4 && e + 8 <= pl.D) {
-    const float4* p = reinterpret_cast<const float4*>(w + (e & ~3));
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    switch (e & 3) {
-      case 0: x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w; break;
-      case 1: x[0] = a.y, x[1] = a.z, x[2] = a.w, x[3] = b.x; break;
-      case 2: x[0] = a.z, x[1] = a.w, x[2] = b.x, x[3] = b.y; break;
-      default: x[0] = a.w, x[1] = b.x, x[2] = b.y, x[3] = b.z;
+  } else if (pl.whole(g)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(p + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pl.in(g, i) ? __ldg(p + i) : 0.f;
+  }
+}
+
+// Those of all groups, all under way before the first is used.
+template <int kG, bool kOff>
+QMM_DEV void weights(const float* w, const Place<kG, kOff>& pl, bool aligned16, float (&x)[kG][4]) {
+  if (!kOff && aligned16) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      // past the row: the last group's, which multiply zeros
+      const float4 a = __ldg(reinterpret_cast<const float4*>(w + min(pl.at(g), pl.D - 4)));
+      x[g][0] = a.x, x[g][1] = a.y, x[g][2] = a.z, x[g][3] = a.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = pl.in(g, i) ? __ldg(w + e + i) : 0.f;
+    for (int g = 0; g < kG; ++g) {
+      x[g][0] = x[g][1] = x[g][2] = x[g][3] = 0.f;
+      if (pl.some(g)) weights4(w, pl, g, aligned16, x[g]);
+    }
   }
 }
 
@@ -159,146 +175,246 @@ QMM_DEV void apply_norm(const NormSpec& n, const Place<kG, kOff>& pl, bool align
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * kG; ++i) s += v[i];   // values outside the row are zeros
-    const float mean = row_reduce<false>(s, slots[0]) / (float)pl.D;
+    const float mean = row_reduce<false>(s, slots[0]) * pl.inv_d;
 #pragma unroll
-    for (int i = 0; i < 4 * kG; ++i) v[i] = pl.in(i / 4, i % 4) ? v[i] - mean : 0.f;
+    for (int i = 0; i < 4 * kG; ++i) v[i] -= mean;
+    if (!pl.all()) {
+#pragma unroll
+      for (int i = 0; i < 4 * kG; ++i)
+        if (!pl.in(i / 4, i % 4)) v[i] = 0.f;
+    }
   }
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 4 * kG; ++i) ss = fmaf(v[i], v[i], ss);
-  const float inv = rsqrtf(row_reduce<false>(ss, slots[1]) / (float)pl.D + n.eps);
+  const float inv = rsqrtf(fmaf(row_reduce<false>(ss, slots[1]), pl.inv_d, n.eps));
+  float x[kG][4];
+  if (n.weight != nullptr) {
+    if constexpr (kG > 1) weights(n.weight, pl, aligned16, x);
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    if (!pl.some(g)) continue;
-    float x[4];
-    if (n.weight != nullptr) {
-      if constexpr (kG > 1) weights4(n.weight, pl, g, aligned16, x);
+    for (int i = 0; i < 4 * kG; ++i) v[i] = v[i] * inv * (kG > 1 ? x[i / 4][i % 4] : ahead[0][i % 4]);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * g + i] = v[4 * g + i] * inv * (kG > 1 ? x[i] : ahead[0][i]);
-    } else {
+    for (int i = 0; i < 4 * kG; ++i) v[i] *= inv;
+  }
+  if (n.bias != nullptr) {
+    if constexpr (kG > 1) weights(n.bias, pl, aligned16, x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * g + i] *= inv;
-    }
-    if (n.bias != nullptr) {
-      if constexpr (kG > 1) weights4(n.bias, pl, g, aligned16, x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * g + i] += kG > 1 ? x[i] : ahead[1][i];
-    }
+    for (int i = 0; i < 4 * kG; ++i)
+      if (kOff || pl.some(i / 4)) v[i] += kG > 1 ? x[i / 4][i % 4] : ahead[1][i % 4];   // zeros stay outside the row
   }
 }
 
 template <int kG, bool kOff>
 QMM_DEV void store_row(void* base, bool bf16, int64_t row, const Place<kG, kOff>& pl, const float (&v)[4 * kG]) {
+  const int size = bf16 ? 2 : 4;
+  uint8_t* p = static_cast<uint8_t*>(base) + (row + pl.e0) * size;
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    const int64_t at = row + pl.at(g);
+  for (int g = 0; g < kG; ++g, p += pl.step * size) {
     const float* x = v + 4 * g;
     if (pl.whole(g)) {
-      if (bf16)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + at) =
-            make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-      else
-        *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(x[0], x[1], x[2], x[3]);
+      if (bf16) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      else *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
     } else if (kOff && pl.some(g)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (!pl.in(g, i)) continue;
-        if (bf16) static_cast<__nv_bfloat16*>(base)[at + i] = __float2bfloat16_rn(x[i]);
-        else static_cast<float*>(base)[at + i] = x[i];
+        if (bf16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x[i]);
+        else reinterpret_cast<float*>(p)[i] = x[i];
       }
     }
   }
 }
 
+// A thread's groups of a row on their way through shared memory: it copies just what
+// it reads itself, so that no barrier guards the copies.
+template <bool kBf16, int kG, bool kOff>
+struct Copies {
+  static constexpr int kSize = kBf16 ? 2 : 4, kBytes = 4 * kSize;
+  // one group of the thread at `to`, the next blockDim.x groups on
+  QMM_DEV static void issue(const void* base, int64_t row, const Place<kG, kOff>& pl, uint32_t to) {
+    const uint8_t* p = static_cast<const uint8_t*>(base) + (row + pl.e0) * kSize;
+#pragma unroll
+    for (int g = 0; g < kG; ++g, p += pl.step * kSize, to += blockDim.x * kBytes) {
+      if (!pl.some(g)) continue;
+      // up to the row's end; before its start lies the row before
+      const uint32_t bytes = kOff ? (uint32_t)min((pl.D - pl.at(g)) * kSize, kBytes) : (uint32_t)kBytes;
+      if constexpr (kBf16)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(bytes) : "memory");
+      else
+        umma::cp_async16_zfill(to, p, bytes);
+    }
+  }
+  QMM_DEV static void fetch(uint32_t from, const Place<kG, kOff>& pl, Raw4<kBf16> (&raw)[kG]) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g, from += blockDim.x * kBytes) {
+      raw[g] = {};
+      if (!pl.some(g)) continue;
+      if constexpr (kBf16)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(raw[g].w[0]), "=r"(raw[g].w[1]) : "r"(from) : "memory");
+      else
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(raw[g].w[0]), "=r"(raw[g].w[1]), "=r"(raw[g].w[2]), "=r"(raw[g].w[3])
+                     : "r"(from)
+                     : "memory");
+      if (kOff && !pl.whole(g)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (pl.in(g, i)) continue;
+          if constexpr (kBf16) raw[g].w[i / 2] &= i & 1 ? 0xFFFFu : 0xFFFF0000u;
+          else raw[g].w[i] = 0;
+        }
+      }
+    }
+  }
+};
+
 // A row per blockDim.x threads, kG groups of four values each; blockDim.y rows per
 // block (more than one only where a row has one warp, which needs no barrier).
 // kOff: rows begin at any element, row t (t * off_step) % 4 behind a boundary.
-template <bool kResBf16, bool kBrBf16, int kG, bool kOff>
+// kRing: blocks walk over the rows, and while they work on one the next one's values
+// are on their way into shared memory.
+template <bool kResBf16, bool kBrBf16, int kG, bool kOff, bool kRing>
 __global__ void __launch_bounds__(1024)
-block_norm_kernel(NormArgs a, int off_step, bool weights16) {
-  __shared__ float slots[5][32];
+block_norm_kernel(NormArgs a, int off_step, bool weights16, float inv_d) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float all_slots[kRing ? 2 : 1][5][32];
   umma::pdl_launch_dependents();
   umma::pdl_wait();
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.T) return;   // whole warps, and only where no barrier follows
-  const int off = kOff ? (int)(t * off_step & 3) : 0;
-  const Place<kG, kOff> pl{(int)threadIdx.x * 4 - off, (int)blockDim.x * 4, a.D};
-  float v[4 * kG];
-  float post_ahead[2][4] = {}, pre_ahead[2][4] = {};
-  auto ask = [&](const NormSpec& n, float (&to)[2][4]) {
-    if (kG > 1 || !pl.some(0)) return;
-    if (n.weight != nullptr) weights4(n.weight, pl, 0, weights16, to[0]);
-    if (n.bias != nullptr) weights4(n.bias, pl, 0, weights16, to[1]);
+  auto place = [&](int64_t row) {
+    const int off = kOff ? (int)(row * off_step & 3) : 0;
+    return Place<kG, kOff>{(int)threadIdx.x * 4 - off, (int)blockDim.x * 4, a.D, inv_d};
   };
-  {
-    Raw4<kResBf16> res[kG];
-    if (a.branch != nullptr) {
+  const bool has_branch = a.branch != nullptr;
+  // a gate that is read like a weight, or like the rows
+  const bool gate_row = has_branch && a.gate != nullptr && (a.ldg != 0 || a.gate_bf16);
+  const uint32_t res_at = umma::smem_u32(ring) + threadIdx.x * (4 * (kResBf16 ? 2 : 4));
+  const uint32_t br_at = umma::smem_u32(ring) + kG * blockDim.x * (4 * (kResBf16 ? 2 : 4)) +
+                         threadIdx.x * (4 * (kBrBf16 ? 2 : 4));
+  const uint32_t gate_at = umma::smem_u32(ring) + kG * blockDim.x * (4 * (kResBf16 ? 2 : 4) + 4 * (kBrBf16 ? 2 : 4)) +
+                           threadIdx.x * (a.gate_bf16 ? 8 : 16);
+  auto issue = [&](int64_t row) {
+    if (row < a.T) {
+      const Place<kG, kOff> pl = place(row);
+      if (has_branch) Copies<kBrBf16, kG, kOff>::issue(a.branch, row * a.ldb, pl, br_at);
+      Copies<kResBf16, kG, kOff>::issue(a.residual, row * a.ldr, pl, res_at);
+      if (gate_row) {
+        if (a.gate_bf16) Copies<true, kG, kOff>::issue(a.gate, row * a.ldg, pl, gate_at);
+        else Copies<false, kG, kOff>::issue(a.gate, row * a.ldg, pl, gate_at);
+      }
+    }
+    umma::cp_async_commit();
+  };
+  if constexpr (kRing) issue(t);
+  int parity = 0;
+  do {
+    const Place<kG, kOff> pl = place(t);
+    // two rows' slots: a warp may be one reduction ahead of another that still reads
+    float (*slots)[32] = all_slots[parity];
+    float v[4 * kG];
+    float post_ahead[2][4] = {}, pre_ahead[2][4] = {};
+    auto ask = [&](const NormSpec& n, float (&to)[2][4]) {
+      if (kG > 1 || !pl.some(0)) return;
+      if (n.weight != nullptr) weights4(n.weight, pl, 0, weights16, to[0]);
+      if (n.bias != nullptr) weights4(n.bias, pl, 0, weights16, to[1]);
+    };
+    {
+      Raw4<kResBf16> res[kG];
       Raw4<kBrBf16> br[kG];
-      load_row(a.branch, t * a.ldb, pl, br);
-      load_row(a.residual, t * a.ldr, pl, res);
-      ask(a.post, post_ahead);
-      ask(a.pre, pre_ahead);
-#pragma unroll
-      for (int i = 0; i < 4 * kG; ++i) v[i] = br[i / 4].at(i % 4);
-      if (a.post.kind != 0) apply_norm(a.post, pl, weights16, v, post_ahead, slots);
-      if (a.gate != nullptr) {
-        if (a.ldg == 0 && !a.gate_bf16) {
-#pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            if (!pl.some(g)) continue;
-            float x[4];
-            weights4(static_cast<const float*>(a.gate), pl, g, weights16, x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * g + i] *= x[i];
-          }
-        } else if (a.gate_bf16) {
+      Raw4<false> gate[kG];    // bf16 rows take half of it
+      // what waits in shared memory is fetched where it is needed, what comes from
+      // memory is asked for before anything else
+      auto get_branch = [&] {
+        if constexpr (kRing) Copies<kBrBf16, kG, kOff>::fetch(br_at, pl, br);
+        else load_row(a.branch, t * a.ldb, pl, br);
+      };
+      auto get_residual = [&] {
+        if constexpr (kRing) Copies<kResBf16, kG, kOff>::fetch(res_at, pl, res);
+        else load_row(a.residual, t * a.ldr, pl, res);
+      };
+      auto get_gate = [&] {
+        if (!gate_row) return;
+        if (a.gate_bf16) {
           Raw4<true> x[kG];
-          load_row(a.gate, t * a.ldg, pl, x);
+          if constexpr (kRing) Copies<true, kG, kOff>::fetch(gate_at, pl, x);
+          else load_row(a.gate, t * a.ldg, pl, x);
 #pragma unroll
-          for (int i = 0; i < 4 * kG; ++i) v[i] *= x[i / 4].at(i % 4);
+          for (int g = 0; g < kG; ++g) gate[g].w[0] = x[g].w[0], gate[g].w[1] = x[g].w[1];
         } else {
-          Raw4<false> x[kG];
-          load_row(a.gate, t * a.ldg, pl, x);
+          if constexpr (kRing) Copies<false, kG, kOff>::fetch(gate_at, pl, gate);
+          else load_row(a.gate, t * a.ldg, pl, gate);
+        }
+      };
+      if constexpr (kRing) {
+        umma::cp_async_wait<0>();
+      } else {
+        if (has_branch) get_branch();
+        get_residual();
+        get_gate();
+        if (has_branch) ask(a.post, post_ahead);
+        ask(a.pre, pre_ahead);
+      }
+      if (has_branch) {
+        if constexpr (kRing) get_branch();
 #pragma unroll
-          for (int i = 0; i < 4 * kG; ++i) v[i] *= x[i / 4].at(i % 4);
+        for (int i = 0; i < 4 * kG; ++i) v[i] = br[i / 4].at(i % 4);
+        if (a.post.kind != 0) apply_norm(a.post, pl, weights16, v, post_ahead, slots);
+        if (gate_row) {
+          if constexpr (kRing) get_gate();
+#pragma unroll
+          for (int i = 0; i < 4 * kG; ++i) {
+            const uint32_t w = gate[i / 4].w[i % 4 / 2];
+            v[i] *= a.gate_bf16 ? (i & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w)) : gate[i / 4].at(i % 4);
+          }
+        } else if (a.gate != nullptr) {
+          float x[kG][4];
+          weights(static_cast<const float*>(a.gate), pl, weights16, x);
+#pragma unroll
+          for (int i = 0; i < 4 * kG; ++i) v[i] *= x[i / 4][i % 4];
+        }
+        if constexpr (kRing) get_residual();
+#pragma unroll
+        for (int i = 0; i < 4 * kG; ++i)
+          v[i] = fmaf(a.scale, v[i], res[i / 4].at(i % 4));   // outside the row: zeros throughout
+      } else {
+        if constexpr (kRing) get_residual();
+#pragma unroll
+        for (int i = 0; i < 4 * kG; ++i) v[i] = res[i / 4].at(i % 4);
+      }
+    }
+    if constexpr (kRing) issue(t + gridDim.x);   // this row's values have been read and used
+    if (a.sum != nullptr) store_row(a.sum, kResBf16, t * a.lds, pl, v);
+    if (a.out != nullptr) {
+      if (a.pre.kind != 0) apply_norm(a.pre, pl, weights16, v, pre_ahead, slots + 2);
+      if (a.out_type != QMM_S8) {
+        store_row(a.out, a.out_type == QMM_BF16, t * a.ldo, pl, v);
+      } else {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * kG; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        const float s = __fdiv_rn(row_reduce<true>(amax, slots[4]), 127.0f), r = __frcp_rn(s);
+        if (threadIdx.x == 0) a.s_x[t] = s;
+        int8_t* codes = static_cast<int8_t*>(a.out) + t * a.ldo;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          if (!pl.some(g)) continue;
+          const uint32_t q = codes4(v + 4 * g, s, r);
+          if (!kOff) {
+            *reinterpret_cast<uint32_t*>(codes + pl.at(g)) = q;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (pl.in(g, i)) codes[pl.at(g) + i] = (int8_t)(q >> (8 * i));
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4 * kG; ++i)
-        v[i] = pl.in(i / 4, i % 4) ? fmaf(a.scale, v[i], res[i / 4].at(i % 4)) : 0.f;
-    } else {
-      load_row(a.residual, t * a.ldr, pl, res);
-      ask(a.pre, pre_ahead);
-#pragma unroll
-      for (int i = 0; i < 4 * kG; ++i) v[i] = res[i / 4].at(i % 4);
     }
-  }
-  if (a.sum != nullptr) store_row(a.sum, kResBf16, t * a.lds, pl, v);
-  if (a.out == nullptr) return;
-  if (a.pre.kind != 0) apply_norm(a.pre, pl, weights16, v, pre_ahead, slots + 2);
-  if (a.out_type != QMM_S8) {
-    store_row(a.out, a.out_type == QMM_BF16, t * a.ldo, pl, v);
-    return;
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4 * kG; ++i)
-    if (pl.in(i / 4, i % 4)) amax = fmaxf(amax, fabsf(v[i]));
-  const float s = __fdiv_rn(row_reduce<true>(amax, slots[4]), 127.0f), r = __frcp_rn(s);
-  if (threadIdx.x == 0) a.s_x[t] = s;
-  int8_t* codes = static_cast<int8_t*>(a.out) + t * a.ldo;
-#pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    if (!pl.some(g)) continue;
-    const uint32_t q = codes4(v + 4 * g, s, r);
-    if (!kOff) {
-      *reinterpret_cast<uint32_t*>(codes + pl.at(g)) = q;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (pl.in(g, i)) codes[pl.at(g) + i] = (int8_t)(q >> (8 * i));
-    }
-  }
+    t += gridDim.x;
+    parity ^= 1;
+  } while (kRing && t < a.T);
+  if constexpr (kRing) umma::cp_async_wait<0>();
 }
 
 // Tensors whose rows begin each at another place: a block per row, value by value
@@ -311,6 +427,7 @@ block_norm_any_kernel(NormArgs a) {
   umma::pdl_wait();
   const int64_t t = blockIdx.x;
   const int D = a.D, first = threadIdx.x, step = blockDim.x;
+  const float inv_d = 1.0f / (float)D;
   auto value = [](const void* p, bool bf16, int64_t i) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
   };
@@ -324,11 +441,11 @@ block_norm_any_kernel(NormArgs a) {
     if (n.kind == QMM_NORM_LAYER) {
       float s = 0.f;
       for (int e = first; e < D; e += step) s += row[e];
-      mean = row_reduce<false>(s, slot[0]) / (float)D;
+      mean = row_reduce<false>(s, slot[0]) * inv_d;
     }
     float ss = 0.f;
     for (int e = first; e < D; e += step) ss = fmaf(row[e] - mean, row[e] - mean, ss);
-    const float inv = rsqrtf(row_reduce<false>(ss, slot[1]) / (float)D + n.eps);
+    const float inv = rsqrtf(fmaf(row_reduce<false>(ss, slot[1]), inv_d, n.eps));
     for (int e = first; e < D; e += step) {
       float v = (row[e] - mean) * inv;
       if (n.weight != nullptr) v *= n.weight[e];
@@ -364,19 +481,33 @@ block_norm_any_kernel(NormArgs a) {
     codes[e] = (int8_t)(s > 0.f ? min(max(__float2int_rn(__fdiv_rn(row[e], s)), -127), 127) : 0);
 }
 
-template <int kG>
+template <int kG, bool kRing>
 cudaError_t launch_groups(const NormArgs& a, bool even, int off_step, bool weights16, int groups,
                           cudaStream_t stream) {
-  void (*kern[8])(NormArgs, int, bool) = {
-      block_norm_kernel<false, false, kG, false>, block_norm_kernel<false, true, kG, false>,
-      block_norm_kernel<true, false, kG, false>, block_norm_kernel<true, true, kG, false>,
-      block_norm_kernel<false, false, kG, true>, block_norm_kernel<false, true, kG, true>,
-      block_norm_kernel<true, false, kG, true>, block_norm_kernel<true, true, kG, true>};
+  void (*kern[8])(NormArgs, int, bool, float) = {
+      block_norm_kernel<false, false, kG, false, kRing>, block_norm_kernel<false, true, kG, false, kRing>,
+      block_norm_kernel<true, false, kG, false, kRing>,  block_norm_kernel<true, true, kG, false, kRing>,
+      block_norm_kernel<false, false, kG, true, kRing>,  block_norm_kernel<false, true, kG, true, kRing>,
+      block_norm_kernel<true, false, kG, true, kRing>,   block_norm_kernel<true, true, kG, true, kRing>};
   const int nt = (groups + 32 * kG - 1) / (32 * kG) * 32;
-  const dim3 block(nt, nt == 32 ? 4 : 1);
-  const dim3 grid((unsigned)((a.T + block.y - 1) / block.y));
-  return launch_pdl(kern[(even ? 0 : 4) + (a.residual_bf16 ? 2 : 0) + (a.branch_bf16 ? 1 : 0)], grid, block, 0, stream,
-                    a, off_step, weights16);
+  const int which = (even ? 0 : 4) + (a.residual_bf16 ? 2 : 0) + (a.branch_bf16 ? 1 : 0);
+  const float inv_d = 1.0f / (float)a.D;
+  if constexpr (!kRing) {
+    const dim3 block(nt, nt == 32 ? 4 : 1);
+    return launch_pdl(kern[which], dim3((unsigned)((a.T + block.y - 1) / block.y)), block, 0, stream, a, off_step,
+                      weights16, inv_d);
+  }
+  const int bytes = (a.residual_bf16 ? 2 : 4) + (a.branch_bf16 ? 2 : 4) +
+                    (a.gate != nullptr && (a.ldg != 0 || a.gate_bf16) ? (a.gate_bf16 ? 2 : 4) : 0);
+  const size_t smem = (size_t)kG * nt * 4 * bytes;
+  static std::atomic<uint64_t> done[8];
+  cudaError_t err = set_once(done[which], reinterpret_cast<const void*>(kern[which]),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kG * 1024 * 4 * 12);
+  if (err != cudaSuccess) return err;
+  int per_sm = 0;
+  if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern[which], nt, smem)) != cudaSuccess) return err;
+  const int grid = std::min(a.T, std::max(1, per_sm) * attn_sm_count());
+  return launch_pdl(kern[which], dim3((unsigned)grid), dim3(nt), smem, stream, a, off_step, weights16, inv_d);
 }
 
 // Whether a tensor's rows begin where those of stride `ld0` do, between two
@@ -386,6 +517,8 @@ bool in_step(const void* p, int64_t ld, int64_t ld0, int size) {
 }
 
 }  // namespace
+
+constexpr int kRingGroups = 1536;
 
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
   const int res_size = a.residual_bf16 ? 2 : 4;
@@ -418,9 +551,13 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
   // 182); eight where 16 would leave a row one warp (16384 of 512 22.7, with 16 24.4).
   const int64_t threads = (int64_t)a.T * ((groups + 31) / 32 * 32);
   if (groups <= 1024 && threads <= (int64_t)2 * 2048 * attn_sm_count())
-    return launch_groups<1>(a, even, off_step, weights16, groups, stream);
-  if (groups <= 128) return launch_groups<2>(a, even, off_step, weights16, groups, stream);
-  return launch_groups<4>(a, even, off_step, weights16, groups, stream);
+    return launch_groups<1, false>(a, even, off_step, weights16, groups, stream);
+  if (groups <= 128) return launch_groups<2, false>(a, even, off_step, weights16, groups, stream);
+  // Rows of many threads leave an SM few blocks, all waiting for memory at once: there
+  // the next row's values come ahead (4096 rows of 16384 199 -> 169 us, 8192 of 8192 149 ->
+  // 147, but 16384 of 4096 142 -> 158).
+  if (groups > kRingGroups) return launch_groups<4, true>(a, even, off_step, weights16, groups, stream);
+  return launch_groups<4, false>(a, even, off_step, weights16, groups, stream);
 }
 
 }  // namespace qmm
