@@ -13,7 +13,6 @@
 // rounding of h would be far above the fp32 rounding of out.
 #include <algorithm>
 #include <atomic>
-#include <climits>
 
 #include "beside.h"
 #include "kv_cache.h"
@@ -226,7 +225,7 @@ struct Outer {
   int rank;
   int64_t m0, m1;
   int u0, u1, step;
-  uint4 b[kRC > 0 ? kRC : 2][4];
+  uint4 b[kRC > 0 ? kRC : 3][4];
   float4 y[2][2];
 
   QMM_DEV void load_base(int u, float4 (&to)[2][2]) const {
@@ -251,8 +250,9 @@ struct Outer {
     if constexpr (kRC > 0) {
 #pragma unroll
       for (int c = 0; c < kRC; ++c) load_b(u0, c, b[c]);
-    } else {
+    } else {                                              // two chunks ahead of the products
       load_b(u0, 0, b[0]);
+      load_b(u0, 1, b[1]);
     }
     load_base(u0, y);
   }
@@ -278,33 +278,7 @@ struct Outer {
       to[2] = *reinterpret_cast<const uint4*>(lo + g * hs + j);
       to[3] = *reinterpret_cast<const uint4*>(lo + (g + 8) * hs + j);
     };
-    if constexpr (kRC > 0) {
-#pragma unroll
-      for (int c = 0; c < kRC; ++c) load_h(c, h[c]);
-    }
-    for (int u = u0; u < u1; u += step) {
-      float acc[4][4] = {};
-      float4 next[2][2];
-      if constexpr (kRC > 0) {
-        load_base(u + step, next);
-#pragma unroll
-        for (int c = 0; c < kRC; ++c) {
-          products(acc, h[c], b[c], rank - c * 32 - 8 * tig);
-          load_b(u + step, c, b[c]);
-        }
-      } else {
-        load_base(u + step, next);
-        for (int c = 0; c < chunks; c += 2) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (c + e >= chunks) break;
-            load_b(u, c + e + 1, b[e ^ 1]);
-            load_h(c + e, h[0]);
-            products(acc, h[0], b[e], rank - (c + e) * 32 - 8 * tig);
-          }
-        }
-        load_b(u + step, 0, b[0]);
-      }
+    auto store = [&](int u, const float (&acc)[4][4]) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int col = u * 32 + 16 * p + 4 * tig;
@@ -315,8 +289,43 @@ struct Outer {
         if (m1 >= 0)
           store4<kVec>(a.out + m1 * a.ldo, col, a.N,
                        make_float4(y[1][p].x + e[2], y[1][p].y + e[3], y[1][p].z + f[2], y[1][p].w + f[3]));
+      }
+    };
+    if constexpr (kRC > 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) y[i][p] = next[i][p];
+      for (int c = 0; c < kRC; ++c) load_h(c, h[c]);
+      for (int u = u0; u < u1; u += step) {
+        float acc[4][4] = {};
+        float4 next[2][2];
+        load_base(u + step, next);
+#pragma unroll
+        for (int c = 0; c < kRC; ++c) {
+          products(acc, h[c], b[c], rank - c * 32 - 8 * tig);
+          load_b(u + step, c, b[c]);
+        }
+        store(u, acc);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) y[i][p] = next[i][p];
+      }
+    } else {
+      float acc[4][4] = {};
+      for (int u = u0, c = 0, ahead = u0, chunk = 2; u < u1;) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          if (u >= u1) break;
+          if (chunk == chunks) chunk = 0, ahead += step;
+          load_b(ahead, chunk++, b[(e + 2) % 3]);
+          load_h(c, h[0]);
+          products(acc, h[0], b[e], rank - c * 32 - 8 * tig);
+          if (++c < chunks) continue;
+          store(u, acc);
+          c = 0, u += step;
+          load_base(u, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] = 0.f;
+        }
       }
     }
   }
@@ -329,82 +338,115 @@ struct Item {
   float scale;
 };
 
-// The item of this cluster, found by every block for itself: row t opens an item
-// when the number of earlier rows with its adapter is a multiple of 16, and the
-// item's rows are the next 16 of them.  Rows without an adapter make items of their
-// own.  The row numbers go to rows[].
-QMM_DEV Item own_item(const LoraArgs& a, int item, bool copy_none, int* ids, int* rows, int* counts, int* ranks,
-                      float* scales, Item* found) {
+struct alignas(16) Smem {
+  float part[kThreads / 32 * 16 * 68];   // sums of a warp: 16 rows by 64 ranks, beside or above the others'
+  int rows[kTile];
+  int counts[kThreads / 32];
+  int ranks[kThreads];
+  float scales[kThreads];
+};
+static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
+
+constexpr int kOwnRows = 1536;            // rows of a call whose items are found in the kernel itself, at most
+// rows counted by adapter, in words
+__host__ __device__ __forceinline__ int table_size(int n_adapters) { return (n_adapters + 1 + 127) / 128 * 128; }
+
+// The item of this cluster, found by every block for itself: the rows are counted by
+// adapter, an adapter's rows make items of 16 in their order, numbered by adapter and
+// the rows without one last.  The row numbers go to rows[]; table holds
+// table_size(n_adapters) words.
+QMM_DEV Item own_item(const LoraArgs& a, int item, bool copy_none, int* table, Smem& sm) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  int id = INT_MIN;                       // past the rows
+  const int buckets = a.n_adapters + (copy_none ? 1 : 0), size = table_size(a.n_adapters);
+  const int per = (a.M + kThreads - 1) / kThreads;         // groups of 32 rows per warp
   // the ids' loads and those of a small set's ranks and scales go together
+  int id[kOwnRows / kThreads];                             // -1: past the rows, or nothing to do for the row
+#pragma unroll
+  for (int i = 0; i < kOwnRows / kThreads; ++i) {
+    const int m = (warp * per + i) * 32 + lane;
+    id[i] = -1;
+    if (i < per && m < a.M) {
+      id[i] = a.ids[m];
+      if (id[i] < -1 || id[i] >= a.n_adapters) {
+        if (blockIdx.x == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+        id[i] = -1;
+      }
+      if (id[i] < 0 && copy_none) id[i] = a.n_adapters;
+    }
+  }
   const bool few = a.n_adapters <= kThreads;
-  int table_rank = a.max_rank;
-  float table_scale = 1.f;
   if (few && t < a.n_adapters) {
-    if (a.ranks != nullptr) table_rank = a.ranks[t];
-    if (a.scales != nullptr) table_scale = a.scales[t];
+    sm.ranks[t] = a.ranks != nullptr ? a.ranks[t] : a.max_rank;
+    sm.scales[t] = a.scales != nullptr ? a.scales[t] : 1.f;
   }
-  if (t < a.M) {
-    id = a.ids[t];
-    if (id < -1 || id >= a.n_adapters) {
-      if (blockIdx.x == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
-      id = -1;
+  for (int i = t * 4; i < size; i += kThreads * 4) *reinterpret_cast<int4*>(table + i) = make_int4(0, 0, 0, 0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kOwnRows / kThreads; ++i)
+    if (id[i] >= 0) atomicAdd(&table[id[i]], 1);
+  __syncthreads();
+  // every warp looks for the item's adapter, 128 of them at a time
+  Item it{0, 0, -1, 1.f};
+  int first = 0;
+  for (int b0 = 0, before = 0; b0 < buckets; b0 += 128) {
+    const int4 n = *reinterpret_cast<const int4*>(table + b0 + lane * 4);
+    const int x = (n.x + kTile - 1) / kTile, y = x + (n.y + kTile - 1) / kTile, z = y + (n.z + kTile - 1) / kTile;
+    const int w = z + (n.w + kTile - 1) / kTile;
+    const int all = __reduce_add_sync(0xffffffffu, w);
+    if (item >= before + all) {
+      before += all;
+      continue;
     }
-    if (id < 0 && !copy_none) id = INT_MIN;
+    int s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    const int at = item - before - (s - w);                // the item among this lane's four
+    const int owner = __ffs(__ballot_sync(0xffffffffu, at >= 0 && at < w)) - 1;
+    const int q = at < x ? 0 : at < y ? 1 : at < z ? 2 : 3;
+    const int tile = at - (q == 0 ? 0 : q == 1 ? x : q == 2 ? y : z);
+    const int rows = q == 0 ? n.x : q == 1 ? n.y : q == 2 ? n.z : n.w;
+    it.adapter = __shfl_sync(0xffffffffu, b0 + lane * 4 + q, owner);
+    first = __shfl_sync(0xffffffffu, tile * kTile, owner);
+    it.rows = min(kTile, __shfl_sync(0xffffffffu, rows, owner) - first);
+    break;
   }
-  ids[t] = id;
-  ranks[t] = table_rank, scales[t] = table_scale;
-  if (t == 0) found->rows = 0;
-  __syncthreads();
-  int rank = 0;
-  float scale = 1.f;
-  if (id >= 0 && few) {
-    rank = ranks[id], scale = scales[id];
-  } else if (id >= 0) {
-    rank = a.ranks != nullptr ? a.ranks[id] : a.max_rank;
-    if (a.scales != nullptr) scale = a.scales[id];
-  }
-  int before = __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
-  if (warp * 32 < a.M) {
-#pragma unroll 8
-    for (int s = 0; s < warp * 32; s += 4) {
-      const int4 v = *reinterpret_cast<const int4*>(ids + s);
-      before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+  if (it.rows == 0) return it;                             // alike in every thread
+  if (it.adapter < a.n_adapters) {
+    if (few) {
+      it.rank = sm.ranks[it.adapter], it.scale = sm.scales[it.adapter];
+    } else {
+      it.rank = a.ranks != nullptr ? a.ranks[it.adapter] : a.max_rank;
+      if (a.scales != nullptr) it.scale = a.scales[it.adapter];
     }
   }
-  // items are numbered by the rows that open them
-  const bool opens = id != INT_MIN && before % kTile == 0;
-  const uint32_t flags = __ballot_sync(0xffffffffu, opens);
-  if (lane == 0) counts[warp] = __popc(flags);
+  // the rows' places among the adapter's
+  uint32_t mine[kOwnRows / kThreads];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kOwnRows / kThreads; ++i) {
+    mine[i] = __ballot_sync(0xffffffffu, id[i] == it.adapter);
+    n += __popc(mine[i]);
+  }
+  if (lane == 0) sm.counts[warp] = n;
   __syncthreads();
-  int number = __popc(flags & ((1u << lane) - 1u));
-  for (int w = 0; w < warp; ++w) number += counts[w];
-  if (opens && number == item) *found = Item{1 + before, rank, id, scale};   // rows: the first one's number, for now
+  int place = -first;
+  for (int w = 0; w < warp; ++w) place += sm.counts[w];
+#pragma unroll
+  for (int i = 0; i < kOwnRows / kThreads; ++i) {
+    const int at = place + __popc(mine[i] & ((1u << lane) - 1u));
+    if (id[i] == it.adapter && at >= 0 && at < kTile) sm.rows[at] = (warp * per + i) * 32 + lane;
+    place += __popc(mine[i]);
+  }
   __syncthreads();
-  Item it = *found;
-  if (it.rows == 0) return it;
-  const int first = it.rows - 1;
-  const bool mine = id == it.adapter && before >= first && before < first + kTile;
-  if (mine) rows[before - first] = t;
-  it.rows = __syncthreads_count(mine);
   if (it.rank < 0 || it.rank > a.max_rank) {
     if (t == 0) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     it.rank = 0;
   }
   return it;
 }
-
-struct alignas(16) Smem {
-  float part[kThreads / 32][16][68];   // sums of a warp: 16 rows by 64 ranks; then of the block
-  int rows[kTile];
-  int ids[kThreads];
-  int counts[kThreads / 32];
-  int ranks[kThreads];
-  float scales[kThreads];
-  Item found;
-};
-static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
 
 // The two halves of a barrier of the cluster's blocks.
 QMM_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -426,7 +468,7 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   const int item = blockIdx.x / cluster, block = blockIdx.x % cluster;
   umma::pdl_launch_dependents();
   umma::pdl_wait();
-  const Item it = own_item(a, item, copy_none, sm.ids, sm.rows, sm.counts, sm.ranks, sm.scales, &sm.found);
+  const Item it = own_item(a, item, copy_none, reinterpret_cast<int*>(lo + kTile * hs), sm);
   if (it.rows == 0) return;
   const int rank = it.rank;
   const int units = (a.N + 31) / 32;
@@ -446,57 +488,58 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   const __nv_bfloat16* x1 = m1 >= 0 ? a.X + m1 * a.ldx : nullptr;
   const __nv_bfloat16* A = a.A + it.adapter * a.a_slot;
   const __nv_bfloat16* B = a.B + it.adapter * a.b_slot;
-  auto nothing = [] {};
   const int chunks = (a.K + 31) / 32;
   constexpr int kWarps = kThreads / 32;
-  const int part = block * kWarps + warp, parts = cluster * kWarps;
-  const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
   const uint32_t part_addr = umma::smem_u32(sm.part);
-  // ranks j0 .. j0 + 63: the warp's sums, then all blocks'; `then` runs while these meet
-  auto inner = [&](int j0, auto then) {
+  auto all = [&](auto outer) {
+    // The warps share K, and the ranks by 64 where there are more.  Sums lie by share
+    // of K, row, rank.
+    const int groups = rank <= 64 ? 1 : rank <= 128 ? 2 : 4, shares = kWarps / groups, pitch = groups * 64 + 4;
+    const int share = block * shares + warp / groups, j0 = warp % groups * 64, left = rank - j0;
+    const int c0 = (int)((int64_t)chunks * share / (cluster * shares));
+    const int c1 = (int)((int64_t)chunks * (share + 1) / (cluster * shares));
     float acc[8][4] = {};
-    const int left = rank - j0;
-    if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
+    if (left <= 0) {
+    } else if (left <= 16) inner_part<2, 4>(a, x0, x1, A, rank, j0, c0, c1, acc);
     else if (left <= 32) inner_part<4, 3>(a, x0, x1, A, rank, j0, c0, c1, acc);
     else inner_part<8, 2>(a, x0, x1, A, rank, j0, c0, c1, acc);
-    if (j0 > 0) cluster_wait();                            // the last ranks' sums have been read everywhere
+    float* mine = sm.part + (warp / groups * 16 + g) * pitch + j0 + 2 * (lane & 3);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const int j = 8 * n + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(&sm.part[warp][g][j]) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(&sm.part[warp][g + 8][j]) = make_float2(acc[n][2], acc[n][3]);
+      *reinterpret_cast<float2*>(mine + 8 * n) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(mine + 8 * pitch + 8 * n) = make_float2(acc[n][2], acc[n][3]);
     }
-    then();
+    outer.start();
     __syncthreads();
-    // the block's sums, in place of its first warp's: four ranks a thread
-    const int r = tid / 16, j = tid % 16 * 4;
-    float4 s = *reinterpret_cast<const float4*>(&sm.part[0][r][j]);
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(&sm.part[k][r][j]);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    // the block's sums, in place of its first share's: four ranks of a row at a time
+    for (int i = tid; i < groups * 256; i += kThreads) {
+      float* at = sm.part + i / (groups * 16) * pitch + i % (groups * 16) * 4;
+      float4 s = *reinterpret_cast<const float4*>(at);
+      for (int k = 1; k < shares; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(at + k * 16 * pitch);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      *reinterpret_cast<float4*>(at) = s;
     }
-    *reinterpret_cast<float4*>(&sm.part[0][r][j]) = s;
     cluster_arrive();
     cluster_wait();
-    s = cluster_sum(part_addr + (uint32_t)((r * 68 + j) * 4), cluster);
-    cluster_arrive();
-    s.x = j0 + j < rank ? s.x * it.scale : 0.f;
-    s.y = j0 + j + 1 < rank ? s.y * it.scale : 0.f;
-    s.z = j0 + j + 2 < rank ? s.z * it.scale : 0.f;
-    s.w = j0 + j + 3 < rank ? s.w * it.scale : 0.f;
-    if (j0 + j < rs) {
+    for (int i = tid; i < groups * 256; i += kThreads) {
+      const int r = i / (groups * 16), j = i % (groups * 16) * 4;
+      if (j >= rs) continue;
+      float4 s = cluster_sum(part_addr + (uint32_t)((r * pitch + j) * 4), cluster);
+      s.x = j < rank ? s.x * it.scale : 0.f;
+      s.y = j + 1 < rank ? s.y * it.scale : 0.f;
+      s.z = j + 2 < rank ? s.z * it.scale : 0.f;
+      s.w = j + 3 < rank ? s.w * it.scale : 0.f;
       const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
-      *reinterpret_cast<uint2*>(hi + r * hs + j0 + j) = make_uint2(a0, a1);
-      *reinterpret_cast<uint2*>(lo + r * hs + j0 + j) =
+      *reinterpret_cast<uint2*>(hi + r * hs + j) = make_uint2(a0, a1);
+      *reinterpret_cast<uint2*>(lo + r * hs + j) =
           make_uint2(two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0)),
                      two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1)));
     }
+    __syncwarp();
+    cluster_arrive();
     __syncthreads();
-  };
-  auto all = [&](auto outer) {
-    inner(0, [&] { outer.start(); });
-    for (int j0 = 64; j0 < rank; j0 += 64) inner(j0, nothing);
     outer.finish(hi, lo, hs);
   };
   if (rank <= 32) all(Outer<kVec, 1>{a, B, rank, m0, m1, n0 + warp, n1, kWarps});
@@ -506,20 +549,19 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
   cluster_wait();                                          // no block leaves while another reads its sums
 }
 
-// Calls of up to this many rows find their items in the kernel itself.
-constexpr int kOwnRows = kThreads;
-
 template <bool kVec>
 cudaError_t launch_rows(const LoraArgs& a, int items, bool copy_none, cudaStream_t stream) {
   const int rs = (a.max_rank + 31) / 32 * 32;
-  auto bytes = [](int stride) { return sizeof(Smem) + (size_t)2 * kTile * (stride + 8) * 2; };
+  auto bytes = [](int stride, int adapters) {
+    return sizeof(Smem) + (size_t)2 * kTile * (stride + 8) * 2 + (size_t)table_size(adapters) * 4;
+  };
   static std::atomic<uint64_t> done{0};
   cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_rows_kernel<kVec>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank));
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes((int)kLoraMaxRank, (int)kLoraMaxAdapters));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes(rs);
+  cfg.dynamicSmemBytes = bytes(rs, a.n_adapters);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -542,10 +584,10 @@ cudaError_t launch_rows(const LoraArgs& a, int items, bool copy_none, cudaStream
       attr[0].val.clusterDim.x = cluster;
       cfg.gridDim = dim3((unsigned)cluster);
       cfg.numAttrs = 1;
-      cfg.dynamicSmemBytes = bytes((int)kLoraMaxRank);
+      cfg.dynamicSmemBytes = bytes((int)kLoraMaxRank, (int)kLoraMaxAdapters);
       if ((err = cudaOccupancyMaxActiveClusters(&n, lora_rows_kernel<kVec>, &cfg)) != cudaSuccess) return err;
       known.store(n, std::memory_order_relaxed);
-      cfg.dynamicSmemBytes = bytes(rs);
+      cfg.dynamicSmemBytes = bytes(rs, a.n_adapters);
     }
     if (items <= n) break;
   }
@@ -555,18 +597,32 @@ cudaError_t launch_rows(const LoraArgs& a, int items, bool copy_none, cudaStream
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel<kVec>, a, rs, cluster, copy_none);
 }
 
+// Calls of few rows go without a routing launch and sums in memory, at the cost of
+// reading an adapter's matrices once per 16 rows instead of once per 128 and of
+// mma.sync, so the limit falls as ranks grow.  At K = N = 4096, routed and not: ranks up
+// to 64 over 40 adapters, 512 rows 49 and 20 us, 1500 rows 55 and 33; over 6 in prompts,
+// 1500 rows 33 and 35; ranks up to 128 over 40, 512 rows 52 and 32, 1000 rows 56 and
+// 52, over 4 29 and 32; ranks up to 256 over 40, 256 rows 61 and 48, 512 rows 64 and
+// 52, over 4 33 and 38.  At K = 8192, N = 12288 and ranks up to 64, 1000 rows 47 and 42,
+// 2000 rows 69 and 76.
+bool own_rows(int64_t M, int64_t max_rank) { return M * std::max<int64_t>(max_rank, 64) <= (int64_t)kOwnRows * 64; }
+
+// No call of up to this many rows is routed, whatever its ranks.
+constexpr int kNoWorkspace = 256;
+static_assert(kNoWorkspace * kLoraMaxRank <= kOwnRows * 64, "own_rows");
+
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank) {
   (void)K, (void)N;
-  if (M <= kOwnRows) return 0;
+  if (M <= kNoWorkspace) return 0;   // from there on asked for either way: own_rows' limit is a matter of speed
   return 256 + pad256((size_t)lora_max_tiles(M, n_adapters) * sizeof(int4)) + pad256((size_t)M * 4) +
          pad256((size_t)M * 2 * lora_rank_stride(max_rank) * 2);
 }
 
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream) {
   const bool copy_none = a.base != a.out;
-  if (a.M <= kOwnRows) {
+  if (own_rows(a.M, a.max_rank)) {
     // d adapters in use make d + (M - d) / 16 items at most
     const int d = (int)std::min<int64_t>(a.n_adapters + 1, a.M), items = d + (a.M - d) / kTile;
     const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&

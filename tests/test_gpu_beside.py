@@ -166,6 +166,31 @@ def test_norm_nonfinite_rows_stay_apart(qmm, cuda):
     assert torch.isnan(got[1][2]).all() and torch.isnan(got[1][4, 7])
 
 
+# widths where a row's threads, groups and their order of loading change, and enough rows to fill the GPU
+@pytest.mark.parametrize("case", [
+    (1300, 64, "f32", "f32", "rms", "token", "rms", "bf16"), (5000, 72, "bf16", "bf16", None, None, "layer", "s8"),
+    (700, 1032, "f32", "bf16", "layer", "token", "rms", "s8"), (640, 3001, "f32", "f32", "rms", "token", "rms", "bf16"),
+    (500, 8192, "bf16", "f32", "rms", "channel", "layer", "bf16"),
+    (400, 12288, "f32", "f32", "rms", "token", "rms", "bf16"),
+    (400, 12296, "f32", "f32", "layer", "token", "rms", "s8"), (330, 20000, "f32", "bf16", "rms", "token", "rms", "f32"),
+    (5, 16384, "bf16", "f32", "rms", None, "layer", "bf16"), (320, 32768, "f32", "f32", None, "token", "rms", "bf16"),
+    (310, 9999, "f32", "bf16", "rms", "channel", "layer", "bf16"),
+], ids=lambda c: "-".join(map(str, c)))
+def test_norm_many(qmm, cuda, case):
+    test_norm(qmm, cuda, case)
+
+
+@pytest.mark.parametrize("T,D", [(5, 96), (3, 101), (330, 4608), (310, 16384)])
+def test_norm_gates_of_the_other_type(qmm, cuda, T, D):
+    """A channel gate in bf16, a gate of rows in fp32."""
+    a, out_type = norm_case(cuda, T, D, "f32", "f32", "rms", "channel", "rms", "bf16")
+    for gate in (a["gate"].to(torch.bfloat16), torch.randn((T, D), device=cuda)):
+        a["gate"] = gate
+        kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
+        check_norm(a, out_type, qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]),
+                                               **kw), 0.0)
+
+
 def test_norm_zero_rows(qmm, cuda):
     z = torch.zeros((4, 640), device=cuda)
     total, out, s = qmm.block_norm(z, z.clone(), residual_out=torch.empty_like(z), out_type="s8", eps=1e-6)
@@ -237,6 +262,76 @@ def test_lora(qmm, cuda, case):
     want0, bound0 = lora_exact(a, base=None)
     close(qmm.lora_add(**{**a, "base": None}), np.zeros(out.shape) if want0 is None else want0, bound0, 0.0, "no base")
     assert int(status) == 0
+
+
+# many rows, ranks and adapters: rows routed to tiles of 128, and the limits on either side
+@pytest.mark.parametrize("case", [
+    (384, 264, 68, 5, 256, False), (385, 520, 130, 3, 256, False), (1536, 264, 100, 700, 8, False),
+    (1537, 72, 40, 3000, 8, False), (1000, 64, 36, 8192, 5, False), (1700, 72, 36, 8192, 5, False),
+    (1700, 328, 517, 5, 16, True), (2100, 512, 388, 40, 40, False), (600, 1024, 260, 2, 200, True),
+    (5000, 128, 132, 1, 7, True), (1900, 1000, 65, 9, 64, True), (40, 4096, 33, 3, 250, False),
+    (200, 520, 70, 7, 129, False), (4000, 2048, 300, 6, 65, True),
+], ids=lambda c: "-".join(map(str, c)))
+def test_lora_many(qmm, cuda, case):
+    test_lora(qmm, cuda, case)
+
+
+@pytest.mark.parametrize("M", [400, 2000])
+def test_lora_many_rows_in_another_order(qmm, cuda, M):
+    a = lora_case(cuda, M, 512, 300, 4, 40, True)
+    out = qmm.lora_add(**a)
+    order = torch.randperm(M, device=cuda)
+    moved = qmm.lora_add(**{**a, "X": a["X"][order], "ids": a["ids"][order], "base": a["base"][order]})
+    assert torch.equal(moved, out[order])
+    X = a["X"].clone()
+    X[77] = float("inf")
+    got = qmm.lora_add(**{**a, "X": X})
+    rows = torch.arange(M, device=cuda) != 77
+    assert torch.equal(got[rows], out[rows])
+
+
+def test_lora_many_rows_without_ranks_and_scales_strided(qmm, cuda):
+    test_lora_without_ranks_and_scales_strided(qmm, cuda, 2000)
+
+
+def test_lora_many_rows_bad_ids_and_ranks(qmm, cuda):
+    test_lora_bad_ids_and_ranks(qmm, cuda, 2000)
+
+
+@pytest.mark.parametrize("M", [500, 2000])
+def test_lora_many_rows_nobody_has_an_adapter(qmm, cuda, M):
+    a = lora_case(cuda, M, 64, 48, 2, 8, False, none=1.1)
+    assert torch.equal(qmm.lora_add(**a), a["base"])
+    assert not qmm.lora_add(**{**a, "base": None}).any()
+    store = a["base"].clone()
+    assert qmm.lora_add(**{**a, "base": store}, out=store) is store and torch.equal(store, a["base"])
+
+
+@pytest.mark.parametrize("M", [3, 500, 2000])
+def test_lora_slots_past_32_bits(qmm, cuda, M):
+    """Slots, and rows of X, base and out, far apart."""
+    a = lora_case(cuda, M, 64, 48, 3, 8, False)
+    want = qmm.lora_add(**a)
+    slot = (1 << 31) + 8
+    for name in ("A", "B"):
+        t = a[name]
+        store = torch.empty(2 * slot + t[0].numel() + 8 * t.shape[1], dtype=torch.bfloat16, device=cuda)
+        far = torch.as_strided(store, t.shape, (slot, t.stride(1), 1))
+        far.copy_(t)
+        a[name] = far
+    assert torch.equal(qmm.lora_add(**a), want)
+
+
+def test_lora_rows_past_32_bits(qmm, cuda):
+    a = lora_case(cuda, 3, 64, 48, 3, 8, False)
+    want = qmm.lora_add(**a)
+    ld = (1 << 30) + 8
+    for name in ("X", "base"):
+        t = a[name]
+        far = torch.as_strided(torch.empty(2 * ld + 64, dtype=t.dtype, device=cuda), t.shape, (ld, 1))
+        a[name] = far.copy_(t)
+    assert torch.equal(qmm.lora_add(**a), want)
+    assert qmm.lora_add(**a, out=a["base"]) is a["base"] and torch.equal(a["base"], want)
 
 
 def test_lora_rows_do_not_depend_on_each_other(qmm, cuda):
@@ -457,3 +552,57 @@ def test_captured_and_replayed(qmm, cuda):
         torch.cuda.synchronize()
         for w, t in zip(want, (total, x, out, lp, ent, ids, top)):
             assert torch.equal(w, t)
+
+
+def test_on_two_streams_at_once(qmm, cuda):
+    """Calls on two streams, none of them the default, with a workspace each."""
+    cases = [(lora_case(cuda, 600, 512, 516, 4, 200, True, seed=i), lora_case(cuda, 90, 512, 516, 4, 30, False, seed=i),
+              norm_case(cuda, 300, 1024, "f32", "f32", "rms", "token", "rms", "bf16", seed=i)[0]) for i in (0, 1)]
+
+    def step(i):
+        many, few, a = cases[i]
+        kw = {k: v for k, v in a.items() if k not in ("residual", "branch")}
+        x, y = qmm.lora_add(**many), qmm.lora_add(**few)
+        z = qmm.block_norm(a["residual"], a["branch"], residual_out=torch.empty_like(a["residual"]), **kw)
+        return [x, y, *z[:2], *qmm.token_logprobs(x, top_k=5)[1:]]
+
+    want = [step(0), step(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for run in got[i]:
+            for w, t in zip(want[i], run):
+                assert torch.equal(w, t)
+
+
+def test_two_graphs_share_a_workspace(qmm, cuda):
+    """Two captured calls of different sizes in one workspace, replayed in turn."""
+    cases = [lora_case(cuda, 2000, 512, 516, 6, 40, False), lora_case(cuda, 500, 256, 260, 3, 200, True)]
+    ws = torch.empty(max(qmm.lora_add_workspace_size(2000, 512, 516, 6, 40),
+                         qmm.lora_add_workspace_size(500, 256, 260, 3, 200)), dtype=torch.uint8, device=cuda)
+    want = [qmm.lora_add(**a) for a in cases]
+    outs, graphs = [torch.empty_like(w) for w in want], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for a, out in zip(cases, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                qmm.lora_add(**a, out=out, workspace=ws)
+        graphs.append(graph)
+    torch.cuda.current_stream().wait_stream(side)
+    ws.fill_(0xFF)                           # nothing is expected of a workspace's contents
+    for _ in range(4):
+        for out in outs:
+            out.fill_(0)
+        for graph in graphs:
+            graph.replay()
+        for w, out in zip(want, outs):
+            assert torch.equal(w, out)
