@@ -518,8 +518,6 @@ bool in_step(const void* p, int64_t ld, int64_t ld0, int size) {
 
 }  // namespace
 
-constexpr int kRingGroups = 1536;
-
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
   const int res_size = a.residual_bf16 ? 2 : 4;
   const int64_t ld0 = a.ldr;
@@ -544,20 +542,28 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
   const bool weights16 = aligned(a.post.weight, 16) && aligned(a.post.bias, 16) && aligned(a.pre.weight, 16) &&
                          aligned(a.pre.bias, 16) && (gate_row || aligned(a.gate, 16));
   const int off_step = (int)(ld0 % 4);
-  // Few rows: a row's latency counts, so four values a thread, as long as two rounds
-  // of the GPU's threads hold them all (2000 rows of 1024: 8.8 us, with 16 values 10.0).
-  // Many: 16, which leaves several rows on an SM at different stages and few warps
-  // to a reduction (16384 rows of 4096 146 us, with eight values 184, with 32
-  // 182); eight where 16 would leave a row one warp (16384 of 512 22.7, with 16 24.4).
+  // Times are of a post norm and a residual in fp32 where no other is named.
+  // Few rows: a row's latency counts, so four values a thread, as long as the GPU holds
+  // all threads at once (300 rows of 1024: 2.8 us, by the rules below 3.1; 1200, which
+  // no longer fit: 6.4 and 5.4).
   const int64_t threads = (int64_t)a.T * ((groups + 31) / 32 * 32);
-  if (groups <= 1024 && threads <= (int64_t)2 * 2048 * attn_sm_count())
+  if (groups <= 1024 && threads <= (int64_t)1280 * attn_sm_count())
     return launch_groups<1, false>(a, even, off_step, weights16, groups, stream);
-  if (groups <= 128) return launch_groups<2, false>(a, even, off_step, weights16, groups, stream);
-  // Rows of many threads leave an SM few blocks, all waiting for memory at once: there
-  // the next row's values come ahead (4096 rows of 16384 199 -> 169 us, 8192 of 8192 149 ->
-  // 147, but 16384 of 4096 142 -> 158).
-  if (groups > kRingGroups) return launch_groups<4, true>(a, even, off_step, weights16, groups, stream);
-  return launch_groups<4, false>(a, even, off_step, weights16, groups, stream);
+  // A row that one warp holds has no barrier, and many such rows are on an SM: nothing
+  // comes ahead (8000 rows of 256 7.8 us, ahead 9.2).  16 values a lane rather than
+  // half-empty warps of eight (20000 layer norms of 255 25.7 us, with eight 33.5).
+  if (groups <= 64) return launch_groups<2, false>(a, even, off_step, weights16, groups, stream);
+  if (groups <= 96) return launch_groups<4, false>(a, even, off_step, weights16, groups, stream);
+  // Other rows' warps wait for one another, so that without the next row's values on their
+  // way an SM's memory traffic pauses: 2500 rows of 1024 8.6 us, with nothing ahead 9.1,
+  // 4096 rows of 16384 146 and 199.  Very many short rows do without: they come and go at
+  // different times (65536 of 1024 141 us, ahead 152; 30000 68.5 and 69.5, of 2048 131 and 129).
+  if (a.T > 32768 && groups <= 384) return launch_groups<4, false>(a, even, off_step, weights16, groups, stream);
+  // Eight values a thread up to 4608 in a row, 16 beyond (8000 rows of 4096 73.7 and 77.5 us,
+  // 2500 of 6144 43.2 and 37.2).  Rows out of line take 16 earlier, for their ends' sake
+  // (5000 of 2049 31.4 and 33.4, of 4095 63.5 and 59.2).
+  if (groups <= (even ? 1152 : 640)) return launch_groups<2, true>(a, even, off_step, weights16, groups, stream);
+  return launch_groups<4, true>(a, even, off_step, weights16, groups, stream);
 }
 
 }  // namespace qmm
