@@ -49,7 +49,7 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
   umma::pdl_wait();
   const int seg = ((a.M + segs - 1) / segs + 31) / 32 * 32;
   const int begin = min(warp * seg, a.M), end = warp < segs ? min(begin + seg, a.M) : begin;
-  constexpr int kAhead = 4;               // loads under way
+  constexpr int kAhead = 8;               // loads under way
   int id[kAhead];
   auto load_ids = [&](int m0) {
 #pragma unroll
@@ -72,12 +72,18 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
     if (report) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
     return a.n_adapters;
   };
+  // lanes of the same bucket; in a prompt all are, which is found out faster
+  auto same_as = [&](int b) {
+    const bool one = __all_sync(0xffffffffu, b == __shfl_sync(0xffffffffu, b, 0));
+    return one ? 0xffffffffu : __match_any_sync(0xffffffffu, b);
+  };
   for (int m0 = begin; m0 < end; m0 += 32 * kAhead) {
     if (m0 != begin) load_ids(m0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      if (m0 + u * 32 >= end) break;
       const int b = bucket_of(m0 + u * 32 + lane, id[u], true);
-      const uint32_t same = __match_any_sync(0xffffffffu, b);
+      const uint32_t same = same_as(b);
       if (b >= 0 && lane == __ffs(same) - 1) table[b * pitch + warp] += __popc(same);
       __syncwarp();
     }
@@ -110,8 +116,9 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
     }
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
+    const int2 sums = lane < warp ? warp_sums[lane] : make_int2(0, 0);
     int2 before = carry;
-    for (int i = 0; i < warp; ++i) before.x += warp_sums[i].x, before.y += warp_sums[i].y;
+    before.x += __reduce_add_sync(0xffffffffu, sums.x), before.y += __reduce_add_sync(0xffffffffu, sums.y);
     const int start = before.x + s.x - n, tile0 = before.y + s.y - t;
     if (b < buckets) first[b] = start;
     if (none) w.head[0] = tile0, w.head[1] = tile0 + t;
@@ -134,8 +141,9 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
     if (!once) load_ids(m0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      if (m0 + u * 32 >= end) break;
       const int m = m0 + u * 32 + lane, b = bucket_of(m, id[u], false);
-      const uint32_t same = __match_any_sync(0xffffffffu, b);
+      const uint32_t same = same_as(b);
       if (b >= 0) w.rows[first[b] + table[b * pitch + warp] + __popc(same & ((1u << lane) - 1u))] = m;
       __syncwarp();
       if (b >= 0 && lane == __ffs(same) - 1) table[b * pitch + warp] += __popc(same);
