@@ -8,15 +8,15 @@
 // Bound: bytes, each logit read once, by a cluster of up to 16 blocks per row: one
 // launch, no workspace.  A row is cut into segments of 128 16-byte vectors, dealt
 // to the cluster's warps; a warp streams its segments with no barrier, the next
-// one's loads under way, and leaves its statistics and each segment's maximum in
-// the first block's shared memory.
+// one's loads under way, and leaves its statistics in the first block's shared memory.
 //
-// Alternatives cost the stream nothing but the segments' maxima: the k-th largest
-// maximum of 32 groups of segments is a value that at least k logits reach, so
-// that only the few segments that reach it (about 1.5 k) are read again.  Logits
-// are kept by a 64-bit key, their value in an order-preserving integer form and the
-// complement of their index, so that keys differ, equal logits fall by rising
-// index and the choice is exact whatever the order of work.
+// Alternatives cost the stream the maxima of pieces, four to a segment: the k-th
+// largest of 64 groups' maxima (of threads' logits, or of segments in a cluster) is a
+// value that at least k logits reach, so that only the pieces that reach it (about
+// 1.3 k) are read again.  Logits are kept by a 64-bit key, their value in an
+// order-preserving integer form and the complement of their index, so that keys
+// differ, equal logits fall by rising index and the choice is exact whatever the
+// order of work.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -29,15 +29,20 @@
 namespace qmm {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;             // vectors of a segment per lane
-constexpr int kSegVecs = 32 * kAhead; // vectors of a segment (of one of its steps in rows of more than kMaxSegs)
-constexpr int kMaxSegs = 2048;
+constexpr int kAhead = 4;             // vectors of a segment per lane, each of another piece
+constexpr int kSegVecs = 32 * kAhead; // vectors of a segment (of one of its steps in rows of more than Block::kSegs)
 constexpr int kMaxCluster = 16;
 constexpr int kUnit = 256;            // elements that a warp reads again at a time
-constexpr int kPool = kWarps * kUnit; // candidates of one such step of a block
-constexpr int kKeep = kThreads;       // candidates that may wait for the next step
+
+// The two blocks: of long rows, alone or in a cluster, and of short ones.
+template <bool kLong, bool kTop>
+struct Block {
+  static constexpr int kThreads = kLong ? 512 : 128, kWarps = kThreads / 32, kPerSm = kLong ? 2 : 8;
+  static constexpr int kSegs = 512, kPieces = kTop ? kSegs * kAhead : 4;
+  static constexpr int kCluster = kLong ? kMaxCluster : 1;
+  static constexpr int kPool = kTop ? kWarps * kUnit : 1;   // candidates of one step of reading again
+  static constexpr int kKeep = kTop ? kThreads : 1;         // candidates that may wait for the next step
+};
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Statistics relative to the maximum m: n terms equal to it, r the sum of the
@@ -133,27 +138,31 @@ struct Row {
   }
 };
 
+template <typename B>
 struct alignas(16) Shared {
-  Stats stats[kMaxCluster * kWarps];   // of the cluster's warps
-  uint64_t pool[kPool + kKeep];        // candidates
-  uint64_t best[kMaxTop];              // the largest so far, falling
-  uint64_t warp_key[kMaxCluster * kWarps];
-  uint32_t seg_max[kMaxSegs + 1];      // order of a segment's largest logit; the edge's behind them
-  uint32_t group_max[kWarps][32];
-  int list[kMaxSegs + 1];              // segments to read again, rising
-  int warp_count[kWarps];
+  Stats stats[B::kCluster * B::kWarps];   // of the cluster's warps
+  uint32_t piece_max[B::kPieces + 4];     // order of a piece's largest logit; the edge's behind them
+  uint64_t pool[B::kPool + B::kKeep];     // candidates
+  uint64_t best[kMaxTop];                 // the largest so far, falling
+  uint64_t warp_key[B::kCluster * B::kWarps];
+  uint32_t group_max[B::kWarps][32];
+  uint16_t list[B::kPieces + 1];          // pieces to read again, rising
+  int warp_count[B::kWarps];
   Stats row;
   int n_pool;
+  uint32_t floor_order;
 };
 
 // The k largest of the pool's n keys, falling, into sm.best; returns how many.
 // Many candidates (rows with far more than k equal logits) are thinned first.
-QMM_DEV int settle(Shared& sm, int n, int k) {
+template <typename B>
+QMM_DEV int settle(Shared<B>& sm, int n, int k) {
+  constexpr int kThreads = B::kThreads, kWarps = B::kWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (n > kThreads) {
     // Raise a bar until k to 2 k threads' largest keys lie above it, by bisection
     // over the keys, which differ, so that it ends: at most 2 k threads' keys stay.
-    constexpr int kEach = (kPool + kKeep) / kThreads;
+    constexpr int kEach = (B::kPool + B::kKeep) / kThreads;
     uint64_t mine[kEach], most = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -195,31 +204,49 @@ QMM_DEV int settle(Shared& sm, int n, int k) {
 }
 
 // The k largest logits of a row into sm.best, by the whole block; returns how
-// many there are (logits of -infinity are none).
-template <bool kBf16>
-QMM_DEV int find_top(Shared& sm, const Row<kBf16>& x, int k, int segs, int steps) {
-  constexpr int kN = Vec<kBf16>::kN, kUnitVecs = kUnit / kN, kLoads = kUnitVecs / 32;
+// many there are (logits of -infinity are none).  lane_top: the largest of those that
+// this thread has seen, in rows of one block.
+template <bool kBf16, typename B>
+QMM_DEV int find_top(Shared<B>& sm, const Row<kBf16>& x, int k, int segs, int steps, int cluster, float lane_top) {
+  constexpr int kThreads = B::kThreads, kWarps = B::kWarps;
+  constexpr int kN = Vec<kBf16>::kN, kLoads = kUnit / kN / 32;   // pieces' steps that a warp reads at a time
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the k-th largest of 32 groups' maxima
-  const int all = segs + 1;                 // with the edge
-  uint32_t most = 0;
-  for (int i = tid; i < all; i += kThreads) most = max(most, sm.seg_max[i]);
+  // the k-th largest of 64 groups' maxima: groups of threads, or of segments
+  const int pieces = segs * kAhead, all = pieces + 1;   // with the edge
+  uint32_t most = order_of(lane_top);
+  if (cluster > 1) {
+    most = 0;
+    for (int i = tid; i < segs; i += kThreads) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sm.piece_max + i * kAhead);
+      most = max(most, max(max(v.x, v.y), max(v.z, v.w)));
+    }
+  }
   sm.group_max[warp][lane] = most;
   __syncthreads();
+  if (warp == 0) {                        // by one warp: by all of them it took longer
+    uint32_t even = 0, odd = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) most = max(most, sm.group_max[w][lane]);
-  int place = 0;
+    for (int w = 0; w < kWarps; w += 2) {
+      even = max(even, sm.group_max[w][lane]);
+      odd = max(odd, sm.group_max[w + 1][lane]);
+    }
+    int even_place = 0, odd_place = 0;    // how many come before; of equals, the even warps' first
 #pragma unroll
-  for (int l = 0; l < 32; ++l) {
-    const uint32_t o = __shfl_sync(0xffffffffu, most, l);
-    place += o > most || (o == most && l < lane);
+    for (int l = 0; l < 32; ++l) {
+      const uint32_t e = __shfl_sync(0xffffffffu, even, l), o = __shfl_sync(0xffffffffu, odd, l);
+      even_place += (e > even || (e == even && l < lane)) + (o > even);
+      odd_place += (e >= odd) + (o > odd || (o == odd && l < lane));
+    }
+    const uint32_t kth = even_place == k - 1 ? even : odd_place == k - 1 ? odd : 0u;
+    const uint32_t order = __reduce_max_sync(0xffffffffu, kth);
+    if (lane == 0) sm.floor_order = max(order, kOrderMinusInf + 1), sm.n_pool = 0;
   }
-  const uint32_t floor_order = max(__shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, place == k - 1)) - 1),
-                                   kOrderMinusInf + 1);
-  // the segments that reach it
+  __syncthreads();
+  const uint32_t floor_order = sm.floor_order;
+  // the pieces that reach it
   const int each = (all + kThreads - 1) / kThreads;
   int mine = 0;
-  for (int i = tid * each; i < min((tid + 1) * each, all); ++i) mine += sm.seg_max[i] >= floor_order;
+  for (int i = tid * each; i < min((tid + 1) * each, all); ++i) mine += sm.piece_max[i] >= floor_order;
   int at = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -227,7 +254,6 @@ QMM_DEV int find_top(Shared& sm, const Row<kBf16>& x, int k, int segs, int steps
     if (lane >= o) at += v;
   }
   if (lane == 31) sm.warp_count[warp] = at;
-  if (tid == 0) sm.n_pool = 0;
   __syncthreads();
   at -= mine;
   int listed = 0;
@@ -237,52 +263,53 @@ QMM_DEV int find_top(Shared& sm, const Row<kBf16>& x, int k, int segs, int steps
     listed += sm.warp_count[w];
   }
   for (int i = tid * each; i < min((tid + 1) * each, all); ++i)
-    if (sm.seg_max[i] >= floor_order) sm.list[at++] = i;
+    if (sm.piece_max[i] >= floor_order) sm.list[at++] = (uint16_t)i;
   __syncthreads();
-  // read again, a unit per warp and step
-  const int per_seg = steps * kSegVecs / kUnitVecs;
-  const int units = listed * per_seg;
+  // read again, kLoads steps of pieces per warp at a time
+  const int units = listed * steps;
   uint64_t bar = (uint64_t)(floor_order - 1) << 32 | 0xFFFFFFFFu;   // keys above it are candidates
   int have = 0;                                                     // of sm.best
   Vec<kBf16> next[kLoads];
-  int next_at;                              // index of the lane's first element
-  auto load = [&](int unit) {
-    // a segment that does not reach the bar holds no candidate, nor does one that
-    // equals it: its indexes are larger, but for the edge's, which come last in
-    // the list
-    const int seg = unit < units ? sm.list[unit / per_seg] : -1;
-    const bool edge = seg == segs && unit % per_seg == 0;
-    const bool skip = seg < 0 || seg == segs || sm.seg_max[seg] <= (uint32_t)(bar >> 32);
-    const int v0 = skip ? x.full : seg * steps * kSegVecs + unit % per_seg * kUnitVecs + lane;
-    next_at = x.head + v0 * kN;
+  int next_at[kLoads];                    // index of the lane's first element
+  auto load = [&](int unit0) {
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) next[u] = x.vec(skip ? x.full : v0 + u * 32);
-    if (edge && x.edge(lane) >= 0) {
-      next_at = x.edge(lane);
-      const uint32_t w = __float_as_uint(x.at(next_at));
-      next[0].q.x = kBf16 ? w >> 16 | 0xFF800000u : w;
+    for (int u = 0; u < kLoads; ++u) {
+      // a piece that does not reach the bar holds no candidate, nor does one that
+      // equals it: its indexes are larger, but for the edge's, which come last in
+      // the list
+      const int unit = unit0 + u, i = steps == 1 ? unit : unit / steps, step = unit - i * steps;
+      const int piece = unit < units ? sm.list[i] : -1;
+      const bool skip = piece < 0 || piece == pieces || sm.piece_max[piece] <= (uint32_t)(bar >> 32);
+      const int v = skip ? x.full : (piece / kAhead * steps + step) * kSegVecs + piece % kAhead * 32 + lane;
+      next_at[u] = x.head + v * kN;
+      next[u] = x.vec(v);
+      if (piece == pieces && step == 0 && x.edge(lane) >= 0) {
+        next_at[u] = x.edge(lane);
+        const uint32_t w = __float_as_uint(x.at(next_at[u]));
+        next[u].q.x = kBf16 ? w >> 16 | 0xFF800000u : w;
+      }
     }
   };
-  load(warp);
-  for (int u0 = 0; u0 < units; u0 += kWarps) {
+  load(warp * kLoads);
+  for (int u0 = 0; u0 < units; u0 += kWarps * kLoads) {
     Vec<kBf16> q[kLoads];
+    int at0[kLoads];
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) q[u] = next[u];
-    const int at0 = next_at;
-    load(u0 + warp + kWarps);
+    for (int u = 0; u < kLoads; ++u) q[u] = next[u], at0[u] = next_at[u];
+    load(u0 + (kWarps + warp) * kLoads);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const float f = q[u].at(i);
-        const uint64_t key = key_of(f, (uint32_t)(at0 + u * 32 * kN + i));
+        const uint64_t key = key_of(f, (uint32_t)(at0[u] + i));
         if (f == f && key > bar) sm.pool[atomicAdd(&sm.n_pool, 1)] = key;   // not NaN
       }
     __syncthreads();
     const int n = sm.n_pool;
-    if (u0 + kWarps >= units) return settle(sm, n, k);
+    if (u0 + kWarps * kLoads >= units) return settle(sm, n, k);
     __syncthreads();
-    if (n > kKeep) {
+    if (n > B::kKeep) {
       // the pool has room for one more step beside these
       have = settle(sm, n, k);
       if (tid < have) sm.pool[tid] = sm.best[tid];
@@ -294,12 +321,13 @@ QMM_DEV int find_top(Shared& sm, const Row<kBf16>& x, int k, int segs, int steps
   return 0;
 }
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2)
+template <bool kBf16, bool kLong, bool kTop>
+__global__ void __launch_bounds__(Block<kLong, kTop>::kThreads, Block<kLong, kTop>::kPerSm)
 token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
-  constexpr int kN = Vec<kBf16>::kN;
+  using B = Block<kLong, kTop>;
+  Shared<B>& sm = *reinterpret_cast<Shared<B>*>(smem_raw);
+  constexpr int kN = Vec<kBf16>::kN, kThreads = B::kThreads, kWarps = B::kWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   umma::pdl_launch_dependents();
   umma::pdl_wait();
@@ -330,29 +358,43 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   if (edge_warp && x.edge(lane) >= 0) edge_x = x.at(x.edge(lane));
   block_sync(cluster);   // every block of the cluster runs, so that the first one's shared memory can be written
   const uint32_t first_stats = umma::mapa_shared(umma::smem_u32(&sm.stats[wid]), 0);
-  const uint32_t first_segs = umma::mapa_shared(umma::smem_u32(sm.seg_max), 0);
+  const uint32_t first_pieces = umma::mapa_shared(umma::smem_u32(sm.piece_max), 0);
 
   Stats st = {-FLT_MAX, 0.f, 0.f, 0.f};   // m is the warp's, n, r and w the lane's
   uint64_t key = 0;                        // of the warp's largest logit, where one alternative is asked for
+  float lane_top = edge_x;                 // the lane's largest
   for (int seg = wid; seg < segs; seg += warps) {
-    uint32_t seg_order = 0;
+    uint32_t piece_order[kAhead] = {};
     for (int step = 0; step < steps; ++step) {
       Vec<kBf16> q[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) q[u] = next[u];
       if (step + 1 < steps) load(seg, step + 1);
       else load(seg + warps, 0);
+      uint32_t order = 0;
       float top = -INFINITY;
+      if constexpr (kTop) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < kAhead; ++u) {
+          float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) top = fmaxf(top, q[u].at(i));
-      const uint32_t order = __reduce_max_sync(0xffffffffu, order_of(top));
-      seg_order = max(seg_order, order);
+          for (int i = 0; i < kN; ++i) most = fmaxf(most, q[u].at(i));
+          top = fmaxf(top, most);
+          const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(most));
+          piece_order[u] = max(piece_order[u], o), order = max(order, o);
+        }
+        lane_top = fmaxf(lane_top, top);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) top = fmaxf(top, q[u].at(i));
+        order = __reduce_max_sync(0xffffffffu, order_of(top));
+      }
       const float m = value_of(order);
       if (m >= st.m) {
         // a new maximum (or the same again): its own terms are counted apart
-        if (k == 1 && (m > st.m || key == 0)) {
+        if (!kTop && k == 1 && (m > st.m || key == 0)) {
           uint32_t at = 0xFFFFFFFFu;
           const uint32_t first = x.head + ((seg * steps + step) * kSegVecs + lane) * kN;
 #pragma unroll
@@ -393,13 +435,16 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
         st.w = lo + hi;
       }
     }
-    if (lane == 0 && k > 1) put_u32(first_segs + 4u * seg, seg_order);
+    if (kTop && lane == 0)
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first_pieces + 16u * seg), "r"(piece_order[0]),
+                   "r"(piece_order[1]), "r"(piece_order[2]), "r"(piece_order[3])
+                   : "memory");
   }
   if (edge_warp) {
     const uint32_t order = __reduce_max_sync(0xffffffffu, order_of(fmaxf(edge_x, -INFINITY)));   // NaN: -infinity
-    if (lane == 0 && k > 1) put_u32(first_segs + 4u * segs, order);
+    if (kTop && lane == 0) put_u32(first_pieces + 16u * segs, order);
     const float m = value_of(order);
-    if (k == 1 && order > kOrderMinusInf) {
+    if (!kTop && k == 1 && order > kOrderMinusInf) {
       const uint32_t at = edge_x == m ? (uint32_t)x.edge(lane) : 0xFFFFFFFFu;
       key = max(key, (uint64_t)order << 32 | (0xFFFFFFFFu - __reduce_min_sync(0xffffffffu, at)));
     }
@@ -419,7 +464,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(first_stats), "f"(st.m), "f"(st.n), "f"(st.r),
                  "f"(st.w)
                  : "memory");
-  if (lane == 0 && k == 1)
+  if (!kTop && lane == 0 && k == 1)
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(umma::mapa_shared(umma::smem_u32(&sm.warp_key[wid]), 0)),
                  "l"(key)
                  : "memory");
@@ -436,7 +481,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
       st = join(st, b, c);
     }
     if (lane == 0) sm.row = st;
-    if (k == 1) {
+    if (!kTop && k == 1) {
       key = 0;
       for (int i = lane; i < warps; i += 32) key = max(key, sm.warp_key[i]);
 #pragma unroll
@@ -462,7 +507,8 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
     a.logprobs[(int64_t)row * a.G + g] = sound ? (token_x - st.m) * a.scale - log_sum : NAN;
   }
   if (k == 0) return;
-  const int have = !sound ? 0 : k == 1 ? 1 : find_top<kBf16>(sm, x, k, segs, steps);
+  int have = sound ? 1 : 0;
+  if constexpr (kTop) have = sound ? find_top(sm, x, k, segs, steps, cluster, lane_top) : 0;
   if (tid < k) {
     int32_t id = -1;
     float l = sound ? -INFINITY : NAN;
@@ -476,18 +522,20 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
   }
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kLong, bool kTop>
 cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0}, done_size{0};
-  const void* kern = reinterpret_cast<const void*>(token_logprobs_kernel<kBf16>);
+  constexpr auto kern_typed = token_logprobs_kernel<kBf16, kLong, kTop>;
+  const void* kern = reinterpret_cast<const void*>(kern_typed);
   cudaError_t err = set_once(done, kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
-  if ((err = set_once(done_size, kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared))) != cudaSuccess)
+  if ((err = set_once(done_size, kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                      (int)sizeof(Shared<Block<kLong, kTop>>))) != cudaSuccess)
     return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.M * cluster);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.blockDim = dim3(Block<kLong, kTop>::kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared<Block<kLong, kTop>>);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -497,7 +545,16 @@ cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps,
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<kBf16>, a, cluster, segs, steps);
+  return cudaLaunchKernelEx(&cfg, kern_typed, a, cluster, segs, steps);
+}
+
+template <bool kLong>
+cudaError_t launch_block(const LogprobArgs& a, int cluster, int segs, int steps, cudaStream_t stream) {
+  if (a.top_k > 1)
+    return a.bf16 ? launch_typed<true, kLong, true>(a, cluster, segs, steps, stream)
+                  : launch_typed<false, kLong, true>(a, cluster, segs, steps, stream);
+  return a.bf16 ? launch_typed<true, kLong, false>(a, cluster, segs, steps, stream)
+                : launch_typed<false, kLong, false>(a, cluster, segs, steps, stream);
 }
 
 }  // namespace
@@ -505,15 +562,28 @@ cudaError_t launch_typed(const LogprobArgs& a, int cluster, int segs, int steps,
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
   const int64_t vecs = a.V / (a.bf16 ? 8 : 4);   // a row's, wherever it begins: no more than this
   const int64_t least = std::max<int64_t>(1, (vecs + kSegVecs - 1) / kSegVecs);
-  const int steps = (int)((least + kMaxSegs - 1) / kMaxSegs);
+  using Long = Block<true, true>;
+  using Short = Block<false, true>;
+  static_assert(Long::kSegs == Short::kSegs, "one way to cut rows");
+  const int steps = (int)((least + Long::kSegs - 1) / Long::kSegs);
   const int segs = (int)((least + steps - 1) / steps);
+  // Short blocks, eight to an SM, where a row gives no more than their warps work, or
+  // where there are more rows than the long ones take at once: many rows then stand at
+  // different steps, and the alternatives' latency is spread over them.  Long and short
+  // blocks, fp32 without padding: 1000 rows of 8000, one alternative 17.3 and 10.4 us, 20 of
+  // them 34.6 and 18.7; 2000 rows of 100000 131 and 129, 171 and 149; 400 rows of 8000 9.0
+  // and 7.0, 16.7 and 13.7, of 32000 14.9 and 16.7, 22.9 and 24.0; but 512 rows of 151936, which
+  // leave an SM four of them, 54.5 and 87.4.
+  const int64_t at_once = (int64_t)Long::kPerSm * attn_sm_count();
+  if (segs <= Short::kWarps || (a.M > at_once && segs <= 32) || a.M > 3 * at_once)
+    return launch_block<false>(a, 1, segs, steps, stream);
   // Blocks of a row: as many as fit on the GPU at once (two per SM) when there are
   // few rows, while each warp keeps a segment.
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)a.M * 2 * cluster <= 2 * attn_sm_count() && segs >= 2 * cluster * kWarps)
+  while (cluster < kMaxCluster && (int64_t)a.M * 2 * cluster <= at_once &&
+         segs >= 2 * cluster * Long::kWarps)
     cluster *= 2;
-  return a.bf16 ? launch_typed<true>(a, cluster, segs, steps, stream)
-                : launch_typed<false>(a, cluster, segs, steps, stream);
+  return launch_block<true>(a, cluster, segs, steps, stream);
 }
 
 }  // namespace qmm
