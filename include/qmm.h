@@ -861,9 +861,9 @@ qmm_status qmm_lora_add_workspace_size(int64_t M, int64_t K, int64_t N, int64_t 
 /* Adapters of many requests beside a shared projection:
  *     out[m][n] = base[m][n] + scales[a] * sum_j (sum_k X[m][k] A[a][j][k]) B[a][n][j],  a = ids[m]
  *
- * set     the adapters; A and B 16-byte aligned, strides multiples of 8 elements (of a
- *         dimension of one: anything), B readable for whole rows of b_stride_row
- *         elements.
+ * set     the adapters; A and B 16-byte aligned, strides multiples of 8 elements and at
+ *         least 8 (of a dimension of one: anything), B readable for max_rank rounded up
+ *         to 8 elements in every row.
  * X       bf16 [M][K], row stride ldx elements (ldx >= K, ldx % 8 == 0, base 16-byte
  *         aligned): the projection's own X.
  * ids     device int32 [M], the adapter of each row in any order; -1: none.
@@ -879,9 +879,11 @@ qmm_status qmm_lora_add_workspace_size(int64_t M, int64_t K, int64_t N, int64_t 
  * rows' values and is the same from run to run.
  * Device status: QMM_ERR_INVALID_ARG for an id outside [-1, n_adapters) or a rank
  * outside [0, max_rank]; such a row is treated as one without an adapter.
+ * QMM_ERR_TIMEOUT where a wait for a copy or product gave up: out is then not valid.
  * M = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned pointers, bad
  * sizes or strides; QMM_ERR_WORKSPACE; QMM_ERR_UNSUPPORTED for K % 8 != 0,
- * max_rank > 256, n_adapters > 8192, K >= 2^28, or N or M >= 2^24.
+ * max_rank > 256, n_adapters > 8192, K >= 2^28, N or M >= 2^24, or 2^31 tiles of
+ * 128 x 128 or more in out, with a started one per adapter (M and N near their limits).
  */
 qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, const int32_t* ids, int64_t M,
                         const float* base, int64_t ldb, float* out, int64_t ldo, void* workspace, size_t ws_bytes,

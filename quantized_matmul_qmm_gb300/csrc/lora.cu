@@ -153,11 +153,6 @@ lora_route_kernel(LoraArgs a, LoraWork w, bool copy_none, int segs) {
 }
 
 // ---- the products ------------------------------------------------------------
-QMM_DEV uint32_t two_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // The first n of eight bf16 values, zeros behind them.
 QMM_DEV uint4 keep8(uint4 v, int n) {
   uint32_t* p = &v.x;
@@ -539,11 +534,7 @@ lora_rows_kernel(LoraArgs a, int rs, int cluster, bool copy_none) {
       s.y = j + 1 < rank ? s.y * it.scale : 0.f;
       s.z = j + 2 < rank ? s.z * it.scale : 0.f;
       s.w = j + 3 < rank ? s.w * it.scale : 0.f;
-      const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
-      *reinterpret_cast<uint2*>(hi + r * hs + j) = make_uint2(a0, a1);
-      *reinterpret_cast<uint2*>(lo + r * hs + j) =
-          make_uint2(two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0)),
-                     two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1)));
+      put_terms(hi + r * hs + j, lo + r * hs + j, s);
     }
     __syncwarp();
     cluster_arrive();

@@ -23,11 +23,6 @@ using namespace umma;
 constexpr int kChunk = 64;                                  // k or ranks of a stage: 128 bytes, one swizzle row
 constexpr int kTileBytes16 = 128 * kChunk * 2;
 
-QMM_DEV uint32_t two_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // ---- h = s A x -----------------------------------------------------------------
 // A cluster takes a tile, its blocks a part of K each.  A block's threads copy the
 // rows' 16-byte pieces (rows lie anywhere) and the adapter's into the swizzled
@@ -178,12 +173,8 @@ lora_inner_kernel(const InnerParams p) {
         s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
         s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
         s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
-        const uint32_t a0 = two_bf16(s.x, s.y), a1 = two_bf16(s.z, s.w);
         uint16_t* to = p.w.h + (int64_t)(it.y + r) * 2 * p.rs + j0 + j;
-        *reinterpret_cast<uint2*>(to) = make_uint2(a0, a1);
-        *reinterpret_cast<uint2*>(to + p.rs) =
-            make_uint2(two_bf16(s.x - bf16lo_to_f32(a0), s.y - bf16hi_to_f32(a0)),
-                       two_bf16(s.z - bf16lo_to_f32(a1), s.w - bf16hi_to_f32(a1)));
+        put_terms(to, to + p.rs, s);
       }
       cluster_sync();
     }

@@ -42,6 +42,25 @@ QMM_DEV float4 cluster_sum(uint32_t addr, int cluster) {
   return s;
 }
 
+// h as the two bf16 terms that the second product takes, four ranks at a time: the
+// value rounded, and what that left.  An infinity (or a value that rounds to one) leaves
+// nothing: infinity less infinity would make NaN of it.
+QMM_DEV uint32_t two_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+QMM_DEV float left_of(float x, float rounded) {
+  const float d = x - rounded;
+  return fabsf(d) < INFINITY ? d : 0.f;
+}
+QMM_DEV void put_terms(uint16_t* hi, uint16_t* lo, const float4& s) {
+  const uint32_t a = two_bf16(s.x, s.y), b = two_bf16(s.z, s.w);
+  *reinterpret_cast<uint2*>(hi) = make_uint2(a, b);
+  *reinterpret_cast<uint2*>(lo) =
+      make_uint2(two_bf16(left_of(s.x, bf16lo_to_f32(a)), left_of(s.y, bf16hi_to_f32(a))),
+                 two_bf16(left_of(s.z, bf16lo_to_f32(b)), left_of(s.w, bf16hi_to_f32(b))));
+}
+
 // both products of a routed call (lora_umma.cu)
 cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream);
 

@@ -308,6 +308,21 @@ def test_lora_many_rows_nobody_has_an_adapter(qmm, cuda, M):
 
 
 @pytest.mark.parametrize("M", [3, 500, 2000])
+def test_lora_infinities(qmm, cuda, M):
+    """Infinities in rows of X reach out as the formula has them, beside an adapter's
+    zeros as NaN."""
+    a = lora_case(cuda, M, 64, 48, 3, 1, False, none=0.0)
+    a["ranks"][:] = 1                       # adapters of rank 0 before: all zeros
+    a["A"].nan_to_num_(), a["B"].nan_to_num_()
+    a["ids"][1:3] = 0                       # one that is not
+    a["X"][1, 3], a["X"][2, 60] = float("inf"), -float("inf")
+    with np.errstate(invalid="ignore"):
+        want, bound = lora_exact(a)
+    assert np.isinf(want[1:3]).all()
+    close(qmm.lora_add(**a), want, bound, 0.0, "out")
+
+
+@pytest.mark.parametrize("M", [3, 500, 2000])
 def test_lora_slots_past_32_bits(qmm, cuda, M):
     """Slots, and rows of X, base and out, far apart."""
     a = lora_case(cuda, M, 64, 48, 3, 8, False)
