@@ -10,6 +10,12 @@
 // to the cluster's warps; a warp streams its segments with no barrier, the next
 // one's loads under way, and leaves its statistics in the first block's shared memory.
 //
+// Measured against a copy's rate: 1024 rows of 151936 in fp32 with one alternative
+// (623 MB) 98 us, 0.95; 512 rows in bf16 44 us, 0.53, there bound by issue slots, an
+// exponential and about six instructions a logit.  Few rows wait for one another's
+// steps: 64 rows 12.2 us, with five alternatives 15.7 (5.8 at that rate); a row with
+// 20 of them 8.8.
+//
 // Alternatives cost the stream the maxima of pieces, four to a segment: the k-th
 // largest of 64 groups' maxima (of threads' logits, or of segments in a cluster) is a
 // value that at least k logits reach, so that only the pieces that reach it (about
@@ -436,8 +442,8 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
       }
     }
     if (kTop && lane == 0)
-      asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first_pieces + 16u * seg), "r"(piece_order[0]),
-                   "r"(piece_order[1]), "r"(piece_order[2]), "r"(piece_order[3])
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first_pieces + 16u * seg),
+                   "r"(piece_order[0]), "r"(piece_order[1]), "r"(piece_order[2]), "r"(piece_order[3])
                    : "memory");
   }
   if (edge_warp) {

@@ -172,7 +172,8 @@ def test_norm_nonfinite_rows_stay_apart(qmm, cuda):
     (700, 1032, "f32", "bf16", "layer", "token", "rms", "s8"), (640, 3001, "f32", "f32", "rms", "token", "rms", "bf16"),
     (500, 8192, "bf16", "f32", "rms", "channel", "layer", "bf16"),
     (400, 12288, "f32", "f32", "rms", "token", "rms", "bf16"),
-    (400, 12296, "f32", "f32", "layer", "token", "rms", "s8"), (330, 20000, "f32", "bf16", "rms", "token", "rms", "f32"),
+    (400, 12296, "f32", "f32", "layer", "token", "rms", "s8"),
+    (330, 20000, "f32", "bf16", "rms", "token", "rms", "f32"),
     (5, 16384, "bf16", "f32", "rms", None, "layer", "bf16"), (320, 32768, "f32", "f32", None, "token", "rms", "bf16"),
     (310, 9999, "f32", "bf16", "rms", "channel", "layer", "bf16"),
 ], ids=lambda c: "-".join(map(str, c)))
