@@ -7,7 +7,7 @@
 // TFLOP/s measured on this part) does in that time.
 //
 // Measured: 4097 prompt rows over 6 adapters of ranks 8 to 64 at K = N = 4608 (192 MB)
-// 57 us with the routing's 7, half of a copy's rate; 16000 rows 171 us, 0.64, of which
+// 57 us with the routing's 7, 0.51 of a copy's rate; 16000 rows 171 us, 0.64, of which
 // the second product 115 (0.77).  2048 rows at K = 2048, N = 12288 and ranks 100 to 256
 // 71 us, 0.47.  What is lost: three launches that cannot overlap (the second product's
 // blocks take a whole SM's shared memory), and in the second the pauses between a unit's
@@ -82,14 +82,17 @@ lora_inner_kernel(const InnerParams p) {
   const uint32_t tmem = tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  const int tiles = p.w.head[0], clusters = gridDim.x / p.cluster;
+  const int clusters = gridDim.x / p.cluster;
+  // the first tile is read beside their number: there is room for as many as clusters
+  int4 it = p.w.tiles[blockIdx.x / p.cluster];
+  const int tiles = p.w.head[0];
   const int piece = tid & 7, row0 = tid >> 3;               // this thread's 16 bytes of rows row0 + 32 i
   uint32_t done_uses = 0;                                   // stages filled so far
   uint32_t last_par = 0;
   bool ok = true;
 
   for (int tile = blockIdx.x / p.cluster; tile < tiles; tile += clusters) {
-    const int4 it = p.w.tiles[tile];
+    if (tile >= clusters) it = p.w.tiles[tile];
     const int rank = a.ranks != nullptr ? a.ranks[it.x] : a.max_rank;
     const float scale = a.scales != nullptr ? a.scales[it.x] : 1.f;
     const int n16 = (rank + 15) / 16 * 16;                  // ranks of the products
@@ -173,16 +176,31 @@ lora_inner_kernel(const InnerParams p) {
       // memory is read in whole rows (scattered 16-byte reads took 10 times as long)
       const int share = (it.z + p.cluster - 1) / p.cluster, r0 = block * share;
       const int quads = min(kInnerRanks, p.rs - j0) / 4;    // of four ranks, in a row
-      for (int i = tid; i < min(share, it.z - r0) * quads; i += kInnerThreads) {
-        const int r = r0 + i / quads, j = i % quads * 4;
-        float4 s = make_float4(0, 0, 0, 0);
-        if (j0 + j < n16) s = cluster_sum(sums_addr + (uint32_t)(r * kInnerPitch + j) * 4, p.cluster);
-        s.x = j0 + j < rank ? s.x * scale : 0.f;
-        s.y = j0 + j + 1 < rank ? s.y * scale : 0.f;
-        s.z = j0 + j + 2 < rank ? s.z * scale : 0.f;
-        s.w = j0 + j + 3 < rank ? s.w * scale : 0.f;
-        uint16_t* to = p.w.h + (int64_t)(it.y + r) * 2 * p.rs + j0 + j;
-        put_terms(to, to + p.rs, s);
+      const int all = min(share, it.z - r0) * quads;
+      for (int i0 = tid; i0 < all; i0 += 2 * kInnerThreads) {
+        int r[2], j[2];
+        uint32_t at[2];
+        bool in[2];
+        float4 s[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = i0 + e * kInnerThreads;
+          r[e] = r0 + i / quads, j[e] = i % quads * 4;
+          at[e] = sums_addr + (uint32_t)(r[e] * kInnerPitch + j[e]) * 4;
+          in[e] = i < all && j0 + j[e] < n16;
+        }
+        cluster_sums(at, in, p.cluster, s);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int left = rank - j0 - j[e];
+          s[e].x = left > 0 ? s[e].x * scale : 0.f;
+          s[e].y = left > 1 ? s[e].y * scale : 0.f;
+          s[e].z = left > 2 ? s[e].z * scale : 0.f;
+          s[e].w = left > 3 ? s[e].w * scale : 0.f;
+          if (e == 1 && i0 + kInnerThreads >= all) break;
+          uint16_t* to = p.w.h + (int64_t)(it.y + r[e]) * 2 * p.rs + j0 + j[e];
+          put_terms(to, to + p.rs, s[e]);
+        }
       }
       cluster_sync();
     }

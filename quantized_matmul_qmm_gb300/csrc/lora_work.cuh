@@ -22,24 +22,37 @@ inline int64_t lora_max_tiles(int64_t M, int64_t n_adapters) {
 }
 
 constexpr int kLoraMaxCluster = 8;
-// The sum over a cluster's blocks, in order, of the four floats at one place of
-// their shared memory; all loads under way before the first addition.
-QMM_DEV float4 cluster_sum(uint32_t addr, int cluster) {
-  float4 v[kLoraMaxCluster];
+// The sums over a cluster's blocks, in order, of the four floats at each of kN places
+// of their shared memory, zeros where `in` is not set; all loads under way before the
+// first addition.
+template <int kN>
+QMM_DEV void cluster_sums(const uint32_t (&addr)[kN], const bool (&in)[kN], int cluster, float4 (&s)[kN]) {
+  float4 v[kN][kLoraMaxCluster];
 #pragma unroll
-  for (int o = 0; o < kLoraMaxCluster; ++o) {
-    v[o] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (o < cluster)
-      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(v[o].x), "=f"(v[o].y), "=f"(v[o].z), "=f"(v[o].w)
-                   : "r"(umma::mapa_shared(addr, o))
-                   : "memory");
+  for (int o = 0; o < kLoraMaxCluster; ++o)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      v[i][o] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (o < cluster && in[i])
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v[i][o].x), "=f"(v[i][o].y), "=f"(v[i][o].z), "=f"(v[i][o].w)
+                     : "r"(umma::mapa_shared(addr[i], o))
+                     : "memory");
+    }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    s[i] = v[i][0];
+#pragma unroll
+    for (int o = 1; o < kLoraMaxCluster; ++o)
+      if (o < cluster) s[i].x += v[i][o].x, s[i].y += v[i][o].y, s[i].z += v[i][o].z, s[i].w += v[i][o].w;
   }
-  float4 s = v[0];
-#pragma unroll
-  for (int o = 1; o < kLoraMaxCluster; ++o)
-    if (o < cluster) s.x += v[o].x, s.y += v[o].y, s.z += v[o].z, s.w += v[o].w;
-  return s;
+}
+QMM_DEV float4 cluster_sum(uint32_t addr, int cluster) {
+  const uint32_t at[1] = {addr};
+  const bool in[1] = {true};
+  float4 s[1];
+  cluster_sums(at, in, cluster, s);
+  return s[0];
 }
 
 // h as the two bf16 terms that the second product takes, four ranks at a time: the
