@@ -460,6 +460,35 @@ def test_logprobs_ties(qmm, cuda, V, dtype):
     check_logprobs(qmm, x.to(TYPES[dtype]).to(cuda), tokens.to(cuda), 32, 1.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,V,k", [(2, 600001, 32), (1, 1100003, 20), (1, 262144, 2), (3, 2048, 32), (5, 2052, 31),
+                                   (930, 2500, 32), (930, 700, 1), (320, 16380, 20), (320, 17001, 20), (2, 33, 32)])
+def test_logprobs_many(qmm, cuda, M, V, k, dtype):
+    """Rows of several steps, and the limits between the blocks that take them."""
+    test_logprobs(qmm, cuda, M, V, k, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logprobs_many_long_rows(qmm, cuda, dtype):
+    """More long rows than the GPU takes at once; a few of them against the oracle,
+    the others against calls of few rows, whose alternatives are the same."""
+    g = torch.Generator(device=cuda).manual_seed(3)
+    x = torch.randn((1000, 140001), generator=g, device=cuda).to(TYPES[dtype])
+    x[5] = -float("inf")
+    x[7, :-3] = torch.finfo(TYPES[dtype]).min
+    x[9] = 1.0
+    tokens = torch.randint(0, 140001, (1000, 2), generator=g, device=cuda, dtype=torch.int32)
+    got = qmm.token_logprobs(x, tokens, top_k=32)
+    rows = torch.tensor([0, 5, 7, 9, 500, 999], device=cuda)
+    want, tol = O.logprobs(f64(x[rows]), tokens[rows].cpu().numpy(), 32, 1.0)
+    close(got[0][rows], want["logprobs"], tol["logprobs"], 0.0, "logprobs")
+    close(got[1][rows], want["entropy"], tol["entropy"], 0.0, "entropy")
+    assert np.array_equal(got[2][rows].cpu().numpy(), want["ids"])
+    close(got[3][rows], want["top"], tol["top"], 0.0, "top_logprobs")
+    few = torch.cat([qmm.token_logprobs(x[i:i + 200], top_k=32)[2] for i in range(0, 1000, 200)])
+    assert torch.equal(got[2], few)
+
+
 @pytest.mark.parametrize("order", ["rising", "falling"])
 def test_logprobs_sorted_rows(qmm, cuda, order):
     """Rows in order of value: every tile replaces the alternatives, or none does."""
