@@ -356,7 +356,7 @@ struct alignas(16) Smem {
 };
 static_assert(sizeof(Smem) % 16 == 0, "h follows, read 16 bytes at a time");
 
-constexpr int kOwnRows = 1536;            // rows of a call whose items are found in the kernel itself, at most
+constexpr int kOwnRows = 1536;            // rows of a call that may find its items in the kernel itself
 // rows counted by adapter, in words
 __host__ __device__ __forceinline__ int table_size(int n_adapters) { return (n_adapters + 1 + 127) / 128 * 128; }
 
@@ -603,32 +603,37 @@ cudaError_t launch_rows(const LoraArgs& a, int items, bool copy_none, cudaStream
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel<kVec>, a, rs, cluster, copy_none);
 }
 
-// Calls of few rows go without a routing launch and sums in memory, at the cost of
-// reading an adapter's matrices once per 16 rows instead of once per 128 and of
-// mma.sync, so the limit falls as ranks grow.  At K = N = 4096, routed and not: ranks up
-// to 64 over 40 adapters, 512 rows 49 and 20 us, 1500 rows 55 and 33; over 6 in prompts,
-// 1500 rows 33 and 35; ranks up to 128 over 40, 512 rows 52 and 32, 1000 rows 56 and
-// 52, over 4 29 and 32; ranks up to 256 over 40, 256 rows 61 and 48, 512 rows 64 and
-// 52, over 4 33 and 38.  At K = 8192, N = 12288 and ranks up to 64, 1000 rows 47 and 42,
-// 2000 rows 69 and 76.
-bool own_rows(int64_t M, int64_t max_rank) { return M * std::max<int64_t>(max_rank, 64) <= (int64_t)kOwnRows * 64; }
-
-// No call of up to this many rows is routed, whatever its ranks.
+// No call of up to this many rows is routed.
 constexpr int kNoWorkspace = 256;
-static_assert(kNoWorkspace * kLoraMaxRank <= kOwnRows * 64, "own_rows");
+
+// Calls of few rows go without a routing launch and sums in memory, at the cost of
+// reading an adapter's matrices once per 16 rows instead of once per 128, mostly from
+// L2, and of mma.sync.  So the limit is one of the bytes read again, and a higher one
+// where adapters have few rows each, which leave tiles of 128 nearly empty.  Not routed
+// and routed: 512 rows over 40 adapters at K = N = 4096 and ranks up to 64 20 and 41 us, up
+// to 128 32 and 47, up to 256 (134 MB) 52 and 60; 1500 rows, ranks up to 64 (98 MB) 34 and
+// 49; 1500 rows over 5 at K = 1024, N = 2048 and rank 16 17 and 22.  The other way, few
+// adapters: 1500 prompt rows at 4608, ranks up to 64 (111 MB) 35 and 33, 380 rows at 4096, up
+// to 256 (100 MB) 36 and 32, 1500 at K = 8192, N = 12288, up to 64 (246 MB) 74 and 56.
+bool own_rows(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank) {
+  if (M <= kNoWorkspace) return true;
+  if (M > kOwnRows) return false;
+  const int64_t again = M / kTile * std::max<int64_t>(max_rank, 16) * (K + N) * 2;
+  return again <= (M <= 48 * n_adapters ? 140 : 96) * (int64_t)1000000;
+}
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t n_adapters, int64_t max_rank) {
   (void)K, (void)N;
-  if (M <= kNoWorkspace) return 0;   // from there on asked for either way: own_rows' limit is a matter of speed
+  if (M <= kNoWorkspace) return 0;   // from there on asked for either way: own_rows' limits are a matter of speed
   return 256 + pad256((size_t)lora_max_tiles(M, n_adapters) * sizeof(int4)) + pad256((size_t)M * 4) +
          pad256((size_t)M * 2 * lora_rank_stride(max_rank) * 2);
 }
 
 cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t stream) {
   const bool copy_none = a.base != a.out;
-  if (own_rows(a.M, a.max_rank)) {
+  if (own_rows(a.M, a.K, a.N, a.n_adapters, a.max_rank)) {
     // d adapters in use make d + (M - d) / 16 items at most
     const int d = (int)std::min<int64_t>(a.n_adapters + 1, a.M), items = d + (a.M - d) / kTile;
     const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&

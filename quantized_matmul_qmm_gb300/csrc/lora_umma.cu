@@ -7,11 +7,11 @@
 // TFLOP/s measured on this part) does in that time.
 //
 // Measured: 4097 prompt rows over 6 adapters of ranks 8 to 64 at K = N = 4608 (192 MB)
-// 57 us with the routing's 7, 0.51 of a copy's rate; 16000 rows 171 us, 0.64, of which
-// the second product 115 (0.77).  2048 rows at K = 2048, N = 12288 and ranks 100 to 256
-// 71 us, 0.47.  What is lost: three launches that cannot overlap (the second product's
-// blocks take a whole SM's shared memory), and in the second the pauses between a unit's
-// accumulator and the next unit's base, half a unit of which is under way.
+// 55 us with the routing's 7, 0.52 of a copy's rate; 16000 rows 170 us, 0.66.  2048 rows at
+// K = 2048, N = 12288 and ranks 100 to 256 70 us, 0.48.  What is lost: three launches
+// that cannot overlap (the second product's blocks take a whole SM's shared memory), the
+// first's meeting over the cluster, and in the second what its registers hold of base
+// under way.
 //
 // Both kernels take 128 rows of one adapter at a time, the tensor cores' height;
 // partly filled tiles cost products, not bytes.
@@ -219,12 +219,15 @@ lora_inner_kernel(const InnerParams p) {
 // ---- out = base + h B^T ----------------------------------------------------------
 // A block per SM walks over units of 128 rows by 128 columns.  One warp loads the
 // two terms of h and the rows of B by TMA, 64 ranks a stage, and another issues the
-// products of both terms with the same B into one of four accumulators; two groups of
-// eight warps take the units in turn.  A warp owns 32 rows by 64 columns: their base values
-// are on their way into registers half a unit ahead, the accumulator goes through the
-// warp's corner of shared memory so that rows are read and written 128 bytes at a
-// time, and no warp waits for another.
-constexpr int kEpiWarps = 16;
+// products of both terms with the same B into one of four accumulators; three groups of
+// four warps take the units in turn.  A warp owns 32 rows, 32 columns at a time: their base
+// values are on their way into registers two such steps ahead, the accumulator goes
+// through the warp's corner of shared memory so that rows are read and written 128
+// bytes at a time, and no warp waits for another.  14 warps leave a thread 128
+// registers, where two steps' values fit; with 16 of these warps and one step ahead
+// 4097 rows at K = N = 4608 took 56.6 us, so 55.0.
+constexpr int kGroups = 3;
+constexpr int kEpiWarps = 4 * kGroups;
 constexpr int kOuterThreads = (kEpiWarps + 2) * 32;
 constexpr int kCols = 128;
 constexpr int kBuffers = 4;
@@ -241,56 +244,57 @@ struct OuterParams {
   bool copy_none;
 };
 
-// A unit of the walk.
+// A unit of the walk, in few registers.
 struct Unit {
-  int adapter, first, rows;   // -1: none; first place; 0: past the end
-  int rank, col0;
-  QMM_DEV int chunks() const { return (rank + kChunk - 1) / kChunk; }
+  int adapter, first, size, col0;   // -1: none; first place; rows and the rank above them, 0: past the end
+  QMM_DEV int rows() const { return size & 0xFFFF; }
+  QMM_DEV int rank() const { return size >> 16; }
+  QMM_DEV int chunks() const { return (rank() + kChunk - 1) / kChunk; }
+  // Blocks of 32 rows that the accumulator holds: where one or two hold the rows they
+  // are there four times or twice, so that all warps of a group have columns to take.
+  QMM_DEV int blocks() const { return rows() <= 32 ? 1 : rows() <= 64 ? 2 : 4; }
 };
 
 // The units first, first + step, .. of a warp's walk.  What they are is read for 32 of
 // them at a time, one per lane: one chain of dependent loads in 32 units.
+template <bool kAdapters>
 struct Walk {
   const OuterParams& p;
-  uint32_t units, first, step;
-  uint32_t n = 0, batch = 0;   // of this walk: the unit at hand, the first of those in the lanes
-  Unit mine, at;
+  uint32_t units, at, step;   // the unit at hand
+  int left = 0;               // of those in the lanes, behind it
+  Unit mine;
 
   QMM_DEV Walk(const OuterParams& params, uint32_t all, uint32_t from, uint32_t by)
-      : p(params), units(all), first(from), step(by) {
+      : p(params), units(all), at(from), step(by) {
     fetch();
-    take();
   }
   QMM_DEV void fetch() {
-    const uint32_t i = first + (batch + (threadIdx.x & 31)) * step;
-    mine = Unit{-1, 0, 0, 0, 0};
+    const uint32_t i = at + (threadIdx.x & 31) * step;
+    mine = Unit{-1, 0, 0, 0};
+    left = 31;
     if (i < units) {
       const uint32_t tile = i / (uint32_t)p.col_blocks;
       const int4 t = p.w.tiles[tile];
-      mine = Unit{t.x, t.y, t.z, 0, (int)(i - tile * p.col_blocks) * kCols};
-      if (t.x >= 0) mine.rank = p.a.ranks != nullptr ? p.a.ranks[t.x] : p.a.max_rank;
+      const int rank = t.x < 0 ? 0 : p.a.ranks != nullptr ? p.a.ranks[t.x] : p.a.max_rank;
+      mine = Unit{t.x, t.y, t.z | rank << 16, (int)(i - tile * p.col_blocks) * kCols};
     }
   }
-  QMM_DEV void take() {
-    const int l = (int)(n - batch);
-    at = Unit{__shfl_sync(0xffffffffu, mine.adapter, l), __shfl_sync(0xffffffffu, mine.first, l),
-              __shfl_sync(0xffffffffu, mine.rows, l), __shfl_sync(0xffffffffu, mine.rank, l),
-              __shfl_sync(0xffffffffu, mine.col0, l)};
+  QMM_DEV Unit unit() const {
+    const int l = 31 - left;
+    return Unit{kAdapters ? __shfl_sync(0xffffffffu, mine.adapter, l) : 0, __shfl_sync(0xffffffffu, mine.first, l),
+                __shfl_sync(0xffffffffu, mine.size, l), __shfl_sync(0xffffffffu, mine.col0, l)};
   }
-  QMM_DEV bool there() const { return first + n * step < units; }
+  QMM_DEV bool there() const { return at < units; }
   QMM_DEV void next() {
-    if (++n == batch + 32) {
-      batch = n;
-      fetch();
-    }
-    take();
+    at += step;
+    if (--left < 0) fetch();
   }
 };
 
 template <bool kVec>
 __global__ void __launch_bounds__(kOuterThreads, 1)
-lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmB,
-                  const OuterParams p) {
+lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmH32,
+                  const __grid_constant__ CUtensorMap tmB, const OuterParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kStages], empty[kStages], tfull[kBuffers], tempty[kBuffers];
   __shared__ uint32_t tmem_slot;
@@ -300,7 +304,7 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int b = 0; b < kBuffers; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], kEpiWarps / 2);
+    for (int b = 0; b < kBuffers; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], 4);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmH);
@@ -319,11 +323,12 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
 
   if (warp == kEpiWarps) {
     // fills the stages
-    Walk f(p, units, blockIdx.x, gridDim.x);
+    Walk<true> f(p, units, blockIdx.x, gridDim.x);
     uint32_t filled = 0;
     bool ok = true;
     for (; f.there() && ok; f.next()) {
-      const int chunks = f.at.chunks();
+      const Unit u = f.unit();
+      const int chunks = u.chunks();
       for (int c = 0; c < chunks && ok; ++c, ++filled) {
         const int s = filled % kStages;
         if (filled >= kStages)
@@ -332,9 +337,16 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
         if (lane == 0) {
           uint8_t* to = smem + s * kStageBytes;
           mbar_arrive_expect_tx(&full[s], kStageBytes);
-          tma_load_2d(to, &tmH, &full[s], c * kChunk, f.at.first);
-          tma_load_2d(to + kTileBytes16, &tmH, &full[s], p.rs + c * kChunk, f.at.first);
-          tma_load_3d(smem_u32(to + 2 * kTileBytes16), &tmB, &full[s], c * kChunk, f.at.col0, f.at.adapter);
+          const int blocks = u.blocks();
+          if (blocks == 4) {
+            tma_load_2d(to, &tmH, &full[s], c * kChunk, u.first);
+            tma_load_2d(to + kTileBytes16, &tmH, &full[s], p.rs + c * kChunk, u.first);
+          } else {
+            for (int i = 0; i < 8; ++i)
+              tma_load_2d(to + i * (kTileBytes16 / 4), &tmH32, &full[s], (i >> 2) * p.rs + c * kChunk,
+                          u.first + 32 * (i & (blocks - 1)));
+          }
+          tma_load_3d(smem_u32(to + 2 * kTileBytes16), &tmB, &full[s], c * kChunk, u.col0, u.adapter);
         }
         __syncwarp();
       }
@@ -347,19 +359,14 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
     // issues the products: all lanes in step, one elected
     const uint32_t one = elect_one();
     uint32_t used = 0;
-    uint32_t buf_used = 0, buf_par = 0;                     // a bit per buffer: used before, parity of its release
-    Walk m(p, units, blockIdx.x, gridDim.x);
+    Walk<true> m(p, units, blockIdx.x, gridDim.x);
     bool ok = true;
     for (int n = 0; m.there() && ok; m.next(), ++n) {
-      const int chunks = m.at.chunks(), rank = m.at.rank;
+      const Unit u = m.unit();
+      const int chunks = u.chunks(), rank = u.rank();
       const int buf = n % kBuffers;
-      if (chunks > 0) {
-        if (buf_used >> buf & 1) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&tempty[buf], buf_par >> buf & 1, &abort_flag, a.dev_status));
-          buf_par ^= 1u << buf;
-        }
-        buf_used |= 1u << buf;
-      }
+      if (n >= kBuffers)
+        ok = __all_sync(0xffffffffu, mbar_wait(&tempty[buf], (n / kBuffers - 1) & 1, &abort_flag, a.dev_status));
       const uint32_t d = tmem + buf * kCols;
       for (int c = 0; c < chunks && ok; ++c, ++used) {
         const int s = used % kStages;
@@ -401,112 +408,108 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
         for (int k = 0; k < kChunk / 16; ++k)
           if (k < steps) umma_f16_one(one, d, hi + 2 * k, b + 2 * k, idesc, 1);
         umma_commit_one(one, &empty[s]);
-        if (c == chunks - 1) umma_commit_one(one, &tfull[buf]);
       }
+      if (ok) umma_commit_one(one, &tfull[buf]);            // also without products: buffers take turns
     }
   } else {
-    const int group = warp / (kEpiWarps / 2), q = warp & 3, half = (warp >> 2) & 1;
+    const int group = warp / 4, q = warp & 3;
     float* corner = reinterpret_cast<float*>(smem + kStages * kStageBytes + warp * kCorner);
-    uint32_t parity = 0;                                    // of this group's buffers' next phases
     // four values of row 32 q + 4 v + lane / 8: columns cl + 0..3, or in steps of eight
-    const int sub = lane >> 3, cl = half * 64 + (kVec ? (lane & 7) * 4 : lane & 7);
+    const int sub = lane >> 3, cl = kVec ? (lane & 7) * 4 : lane & 7;
     // The warp's rows of a unit: how many, and row numbers by lane; `run`: they follow
     // one another, as a prompt's do, so that an address is the last one's plus a step.
     struct Rows {
-      int n, id;
+      int id;
       bool run;
     };
+    auto rows_in = [&](const Unit& u) { return min(max(u.rows() - 32 * (q & (u.blocks() - 1)), 0), 32); };
     auto rows_of = [&](const Unit& u) {
-      Rows r;
-      r.n = min(max(u.rows - 32 * q, 0), 32);
-      r.id = lane < r.n ? p.w.rows[u.first + 32 * q + lane] : 0;
-      return r;
+      return Rows{lane < rows_in(u) ? p.w.rows[u.first + 32 * (q & (u.blocks() - 1)) + lane] : 0, false};
     };
-    auto runs = [&](Rows& r) {
+    auto runs = [&](const Unit& u, Rows& r) {
       const int id0 = __shfl_sync(0xffffffffu, r.id, 0);    // by all lanes, whatever they hold
-      r.run = __all_sync(0xffffffffu, lane >= r.n || r.id == id0 + lane);
+      r.run = __all_sync(0xffffffffu, lane >= rows_in(u) || r.id == id0 + lane);
     };
-    // values of half a unit's columns, asked for half a unit ahead
-    float y[8][4] = {};
-    auto load4 = [&](int v, const float* from, int col) {
+    // values of two steps
+    float y[2][8][4] = {};
+    auto load4 = [&](float (&to)[4], const float* from, int col) {
       if constexpr (kVec) {
         if (col < a.N) {
           const float4 t = *reinterpret_cast<const float4*>(from);
-          y[v][0] = t.x, y[v][1] = t.y, y[v][2] = t.z, y[v][3] = t.w;
+          to[0] = t.x, to[1] = t.y, to[2] = t.z, to[3] = t.w;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + 8 * e < a.N) y[v][e] = from[8 * e];
+          if (col + 8 * e < a.N) to[e] = from[8 * e];
       }
     };
-    auto load = [&](const Unit& u, const Rows& r, int j) {
-      if (a.base == nullptr) return;
-      const int col = u.col0 + 32 * j + cl;
+    auto load = [&](const Unit& u, const Rows& r, int j, float (&to)[8][4]) {
+      const int blocks = u.blocks(), rows = rows_in(u);
+      if (a.base == nullptr || j >= blocks) return;
+      const int col = u.col0 + 32 * ((q & -blocks) + j) + cl;
       if (r.run) {
         const float* from = a.base + (int64_t)(__shfl_sync(0xffffffffu, r.id, 0) + sub) * a.ldb + col;
 #pragma unroll
         for (int v = 0; v < 8; ++v, from += 4 * a.ldb)
-          if (4 * v + sub < r.n) load4(v, from, col);
+          if (4 * v + sub < rows) load4(to[v], from, col);
       } else {
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           const int m = __shfl_sync(0xffffffffu, r.id, 4 * v + sub);
-          if (4 * v + sub < r.n) load4(v, a.base + (int64_t)m * a.ldb + col, col);
+          if (4 * v + sub < rows) load4(to[v], a.base + (int64_t)m * a.ldb + col, col);
         }
       }
     };
-    Walk walk(p, units, blockIdx.x + group * gridDim.x, 2 * gridDim.x);
-    Unit u = walk.at;
+    Walk<false> walk(p, units, blockIdx.x + group * gridDim.x, kGroups * gridDim.x);
+    Unit u = walk.unit();
     Rows ur = rows_of(u);
-    runs(ur);
-    load(u, ur, 0);
-    for (int n = group; u.rows > 0; n += 2) {
+    runs(u, ur);
+    load(u, ur, 0, y[0]);
+    load(u, ur, 1, y[1]);
+    for (int n = group; u.rows() > 0; n += kGroups) {
       walk.next();                                          // its rows are asked for long before they are needed
-      const Unit next = walk.at;
+      const Unit next = walk.unit();
       Rows nr = rows_of(next);
       const int buf = n % kBuffers;
-      const bool sums = u.rank > 0;
-      if (sums) {
-        const uint32_t par = parity >> buf & 1;
-        parity ^= 1u << buf;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], par, &abort_flag, a.dev_status))) break;
-        tc_fence_after();
-      }
+      const bool sums = u.rank() > 0;
+      const int rows = rows_in(u);
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (n / kBuffers) & 1, &abort_flag, a.dev_status))) break;
+      tc_fence_after();
+      // columns 32 c .. of the unit: the sums and the base values at hand to out
+      auto step = [&](int c, const float(&have)[8][4], bool last) {
+        if (sums && rows > 0) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (sums && ur.n > 0) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 16) {
+          for (int i = 0; i < 32; i += 16) {
             uint32_t r[16];
-            tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kCols + half * 64 + 32 * j + c), r);
+            tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kCols + 32 * c + i), r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(corner + lane * kPitch + c + e) =
+              *reinterpret_cast<uint4*>(corner + lane * kPitch + i + e) =
                   make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
           }
         }
         __syncwarp();
-        if (j == 1 && sums) {
+        if (last) {
           tc_fence_before();
           if (lane == 0) mbar_arrive(&tempty[buf]);
         }
-        const int col = u.col0 + 32 * j + cl;
-        const float* d = corner + sub * kPitch + (cl & 31);
+        const int col = u.col0 + 32 * c + cl;
+        const float* d = corner + sub * kPitch + cl;
         auto store4 = [&](int v, float* to) {
           if constexpr (kVec) {
-            float4 s = make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
+            float4 s = make_float4(have[v][0], have[v][1], have[v][2], have[v][3]);
             if (sums) {
               const float4 t = *reinterpret_cast<const float4*>(d + 4 * v * kPitch);
               s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
             }
-            if (4 * v + sub < ur.n && col < a.N) *reinterpret_cast<float4*>(to) = s;
+            if (4 * v + sub < rows && col < a.N) *reinterpret_cast<float4*>(to) = s;
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (4 * v + sub < ur.n && col + 8 * e < a.N)
-                to[8 * e] = sums ? y[v][e] + d[4 * v * kPitch + 8 * e] : y[v][e];
+              if (4 * v + sub < rows && col + 8 * e < a.N)
+                to[8 * e] = sums ? have[v][e] + d[4 * v * kPitch + 8 * e] : have[v][e];
           }
         };
         if (ur.run) {
@@ -519,13 +522,21 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
             store4(v, a.out + (int64_t)__shfl_sync(0xffffffffu, ur.id, 4 * v + sub) * a.ldo + col);
         }
         __syncwarp();
-        if (j == 0) {
-          load(u, ur, 1);
-        } else {
-          runs(nr);
-          load(next, nr, 0);
-        }
+      };
+      const int blocks = u.blocks();
+      if (blocks == 4) {
+        step(0, y[0], false);
+        load(u, ur, 2, y[0]);
+        step(1, y[1], false);
+        load(u, ur, 3, y[1]);
       }
+      // the last two steps of this warp, or its only one
+      const int c = blocks == 4 ? 2 : q & -blocks;
+      step(c, y[0], blocks == 1);
+      runs(next, nr);
+      load(next, nr, 0, y[0]);
+      if (blocks > 1) step(c + 1, y[1], true);
+      load(next, nr, 1, y[1]);
       u = next;
       ur = nr;
     }
@@ -578,22 +589,23 @@ cudaError_t launch_inner(const LoraArgs& a, const LoraWork& w, cudaStream_t stre
 }
 
 template <bool kVec>
-cudaError_t launch_outer(const CUtensorMap& tmH, const CUtensorMap& tmB, const OuterParams& p, int grid,
-                         cudaStream_t stream) {
+cudaError_t launch_outer(const CUtensorMap& tmH, const CUtensorMap& tmH32, const CUtensorMap& tmB,
+                         const OuterParams& p, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_outer_kernel<kVec>),
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kOuterSmem);
   if (err != cudaSuccess) return err;
-  return launch_pdl(lora_outer_kernel<kVec>, dim3((unsigned)grid), dim3(kOuterThreads), kOuterSmem, stream, tmH, tmB,
-                    p);
+  return launch_pdl(lora_outer_kernel<kVec>, dim3((unsigned)grid), dim3(kOuterThreads), kOuterSmem, stream, tmH,
+                    tmH32, tmB, p);
 }
 
 }  // namespace
 
 cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream) {
   OuterParams p{a, w, lora_rank_stride(a.max_rank), (a.N + kCols - 1) / kCols, copy_none};
-  CUtensorMap tmH, tmB;
+  CUtensorMap tmH, tmH32, tmB;
   if (!make_tmap_2d(&tmH, true, w.h, (uint64_t)2 * p.rs, (uint64_t)a.M, (uint64_t)4 * p.rs, kChunk, 128) ||
+      !make_tmap_2d(&tmH32, true, w.h, (uint64_t)2 * p.rs, (uint64_t)a.M, (uint64_t)4 * p.rs, kChunk, 32) ||
       !make_tmap_rows3(&tmB, a.B, (uint64_t)a.max_rank, (uint64_t)a.N, (uint64_t)a.n_adapters, (uint64_t)a.b_row * 2,
                        (uint64_t)a.b_slot * 2, kChunk, kCols))
     return cudaErrorInvalidValue;
@@ -603,7 +615,8 @@ cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy
   const int grid = (int)std::min<int64_t>(lora_max_tiles(a.M, a.n_adapters) * p.col_blocks, attn_sm_count());
   const bool vec = a.N % 4 == 0 && aligned(a.out, 16) && a.ldo % 4 == 0 &&
                    (a.base == nullptr || (aligned(a.base, 16) && a.ldb % 4 == 0));
-  return vec ? launch_outer<true>(tmH, tmB, p, grid, stream) : launch_outer<false>(tmH, tmB, p, grid, stream);
+  return vec ? launch_outer<true>(tmH, tmH32, tmB, p, grid, stream)
+             : launch_outer<false>(tmH, tmH32, tmB, p, grid, stream);
 }
 
 }  // namespace qmm

@@ -272,6 +272,9 @@ def test_lora(qmm, cuda, case):
     (1700, 328, 517, 5, 16, True), (2100, 512, 388, 40, 40, False), (600, 1024, 260, 2, 200, True),
     (5000, 128, 132, 1, 7, True), (1900, 1000, 65, 9, 64, True), (40, 4096, 33, 3, 250, False),
     (200, 520, 70, 7, 129, False), (4000, 2048, 300, 6, 65, True),
+    (1600, 520, 130, 3, 256, False), (1600, 1032, 260, 2, 200, True), (2000, 256, 300, 60, 150, False),
+    (1600, 128, 200, 70, 24, False), (1700, 72, 131, 40, 96, False), (1540, 64, 257, 1500, 70, False),
+    (900, 4096, 2052, 2, 256, True), (300, 8192, 4100, 3, 256, True),
 ], ids=lambda c: "-".join(map(str, c)))
 def test_lora_many(qmm, cuda, case):
     test_lora(qmm, cuda, case)
@@ -599,9 +602,10 @@ def test_captured_and_replayed(qmm, cuda):
             assert torch.equal(w, t)
 
 
-def test_on_two_streams_at_once(qmm, cuda):
+@pytest.mark.parametrize("M", [600, 1700])
+def test_on_two_streams_at_once(qmm, cuda, M):
     """Calls on two streams, none of them the default, with a workspace each."""
-    cases = [(lora_case(cuda, 600, 512, 516, 4, 200, True, seed=i), lora_case(cuda, 90, 512, 516, 4, 30, False, seed=i),
+    cases = [(lora_case(cuda, M, 512, 516, 4, 200, True, seed=i), lora_case(cuda, 90, 512, 516, 4, 30, False, seed=i),
               norm_case(cuda, 300, 1024, "f32", "f32", "rms", "token", "rms", "bf16", seed=i)[0]) for i in (0, 1)]
 
     def step(i):
