@@ -351,10 +351,9 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
         __syncwarp();
       }
     }
-    // copies already issued land before the block leaves
-    if (!ok)
-      for (uint32_t u = filled > kStages ? filled - kStages : 0; u < filled; ++u)
-        mbar_drain(&full[u % kStages], (u / kStages) & 1);
+    // copies already issued land before the block leaves, also where a wait gave up
+    for (uint32_t u = filled > kStages ? filled - kStages : 0; u < filled; ++u)
+      mbar_drain(&full[u % kStages], (u / kStages) & 1);
   } else if (warp == kEpiWarps + 1) {
     // issues the products: all lanes in step, one elected
     const uint32_t one = elect_one();
