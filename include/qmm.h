@@ -23,9 +23,10 @@
  *   pointers.
  * - The caller allocates and owns every buffer.  No entry point allocates or
  *   frees device memory, synchronises the stream, or keeps mutable state
- *   between calls.  There are three exceptions: a per-process cache of the
+ *   between calls.  There are four exceptions: a per-process cache of the
  *   driver entry point used to build TMA descriptors, a per-process cache of
- *   the grouped GEMV's launch plans (keyed by the problems' shapes), and the
+ *   the grouped GEMV's launch plans (keyed by the problems' shapes), one of how
+ *   many clusters of qmm_lora_add's blocks each device holds, and the
  *   fixed scratch array of qmm_q4_gemm_id_noalloc (see there).  Pointers are
  *   borrowed until the work queued on `stream` has finished.
  * - Work is queued on `stream` and runs asynchronously.  Argument errors are
@@ -36,9 +37,10 @@
  *   (QMM_ERR_TIMEOUT), an expert id outside [0, n_expert)
  *   (QMM_ERR_BAD_EXPERT_ID), a per-axis zero point outside its operand's
  *   domain (QMM_ERR_INVALID_ARG), a weight block that the f16 tensor-core
- *   route cannot form (QMM_ERR_RANGE), and lengths, slots, parents or page ids
+ *   route cannot form (QMM_ERR_RANGE), lengths, slots, parents or page ids
  *   of a step that do not fit its buffers (QMM_ERR_INVALID_ARG,
- *   QMM_ERR_NO_PAGES).  The library only ever replaces a 0
+ *   QMM_ERR_NO_PAGES), and adapters, their ranks, or tokens outside what there is
+ *   (QMM_ERR_INVALID_ARG).  The library only ever replaces a 0
  *   there with an error code, so the caller reads it after synchronising.
  * - Shapes the library has no kernel for return QMM_ERR_UNSUPPORTED.  There
  *   is no fallback path.
