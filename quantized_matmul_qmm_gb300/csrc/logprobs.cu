@@ -274,19 +274,19 @@ QMM_DEV int find_top(Shared<B>& sm, const Row<kBf16>& x, int k, int segs, int st
   // read again, kLoads steps of pieces per warp at a time
   const int units = listed * steps;
   uint64_t bar = (uint64_t)(floor_order - 1) << 32 | 0xFFFFFFFFu;   // keys above it are candidates
-  int have = 0;                                                     // of sm.best
+  uint32_t skip = floor_order - 1;        // pieces that do not come above it hold no candidate
+  int bar_seg = -1;                       // of several steps: the segment that the bar lies in
+  int have = 0;                           // of sm.best
   Vec<kBf16> next[kLoads];
   int next_at[kLoads];                    // index of the lane's first element
   auto load = [&](int unit0) {
+    if (steps > 1 && unit0 < units && sm.list[unit0 / steps] / kAhead > bar_seg) skip = (uint32_t)(bar >> 32);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      // a piece that does not reach the bar holds no candidate, nor does one that
-      // equals it: its indexes are larger, but for the edge's, which come last in
-      // the list
       const int unit = unit0 + u, i = steps == 1 ? unit : unit / steps, step = unit - i * steps;
       const int piece = unit < units ? sm.list[i] : -1;
-      const bool skip = piece < 0 || piece == pieces || sm.piece_max[piece] <= (uint32_t)(bar >> 32);
-      const int v = skip ? x.full : (piece / kAhead * steps + step) * kSegVecs + piece % kAhead * 32 + lane;
+      const bool none = piece < 0 || piece == pieces || sm.piece_max[piece] <= skip;
+      const int v = none ? x.full : (piece / kAhead * steps + step) * kSegVecs + piece % kAhead * 32 + lane;
       next_at[u] = x.head + v * kN;
       next[u] = x.vec(v);
       if (piece == pieces && step == 0 && x.edge(lane) >= 0) {
@@ -320,7 +320,14 @@ QMM_DEV int find_top(Shared<B>& sm, const Row<kBf16>& x, int k, int segs, int st
       have = settle(sm, n, k);
       if (tid < have) sm.pool[tid] = sm.best[tid];
       if (tid == 0) sm.n_pool = have;
-      if (have == k) bar = sm.best[k - 1];
+      if (have == k) {
+        // A piece that equals the bar has larger indexes and is skipped, but for the edge,
+        // which comes last in the list, and for the bar's own segment where it has several
+        // steps: a later piece's first step lies before an earlier one's second.
+        bar = sm.best[k - 1];
+        skip = (uint32_t)(bar >> 32) - (steps > 1);
+        bar_seg = (int)((0xFFFFFFFFu - (uint32_t)bar - x.head) / ((uint32_t)steps * kSegVecs * kN));
+      }
       __syncthreads();
     }
   }
