@@ -877,8 +877,9 @@ qmm_status qmm_lora_add_workspace_size(int64_t M, int64_t K, int64_t N, int64_t 
  *         bytes, 256-byte aligned, rewritten by the call (NULL when that size is 0).
  * Products of X and A are exact and summed in fp32; the inner sums times scales[a]
  * enter the second product as two bf16 terms (within 2^-16 of themselves), which is
- * summed in fp32 and added to base once.  A row's result does not depend on the other
- * rows' values and is the same from run to run.
+ * summed in fp32 and added to base once.  Infinities and NaN in X, A and B reach out as
+ * the formula has them.  A row's result does not depend on the other rows' values and is
+ * the same from run to run.
  * Device status: QMM_ERR_INVALID_ARG for an id outside [-1, n_adapters) or a rank
  * outside [0, max_rank]; such a row is treated as one without an adapter.
  * QMM_ERR_TIMEOUT where a wait for a copy or product gave up: out is then not valid.

@@ -288,16 +288,32 @@ struct Outer {
       to[3] = *reinterpret_cast<const uint4*>(lo + (g + 8) * hs + j);
     };
     auto store = [&](int u, const float (&acc)[4][4]) {
+      bool nan0 = false, nan1 = false;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        nan0 |= acc[n][0] != acc[n][0] || acc[n][1] != acc[n][1];
+        nan1 |= acc[n][2] != acc[n][2] || acc[n][3] != acc[n][3];
+      }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int col = u * 32 + 16 * p + 4 * tig;
         const float(&e)[4] = acc[2 * p], (&f)[4] = acc[2 * p + 1];
-        if (m0 >= 0)
+        if (m0 >= 0 && !nan0)
           store4<kVec>(a.out + m0 * a.ldo, col, a.N,
                        make_float4(y[0][p].x + e[0], y[0][p].y + e[1], y[0][p].z + f[0], y[0][p].w + f[1]));
-        if (m1 >= 0)
+        if (m1 >= 0 && !nan1)
           store4<kVec>(a.out + m1 * a.ldo, col, a.N,
                        make_float4(y[1][p].x + e[2], y[1][p].y + e[3], y[1][p].z + f[2], y[1][p].w + f[3]));
+      }
+      if (nan0 || nan1) {                                  // an infinity in B, or NaN all the same
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          const int64_t m = i < 8 ? m0 : m1;
+          const int col = u * 32 + i / 4 % 2 * 16 + 4 * tig + i % 4, at = (g + (i < 8 ? 0 : 8)) * hs;
+          if ((i < 8 ? nan0 : nan1) && m >= 0 && col < a.N)
+            a.out[m * a.ldo + col] = (a.base != nullptr ? a.base[m * a.ldb + col] : 0.f) +
+                                     sum_of_terms(hi + at, lo + at, B + col * a.b_row, rank);
+        }
       }
     };
     if constexpr (kRC > 0) {

@@ -478,15 +478,28 @@ lora_outer_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant
       // columns 32 c .. of the unit: the sums and the base values at hand to out
       auto step = [&](int c, const float(&have)[8][4], bool last) {
         if (sums && rows > 0) {
+          bool nan = false;
 #pragma unroll
           for (int i = 0; i < 32; i += 16) {
             uint32_t r[16];
             tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kCols + 32 * c + i), r);
             tmem_wait_ld();
 #pragma unroll
+            for (int e = 0; e < 16; ++e) nan |= __uint_as_float(r[e]) != __uint_as_float(r[e]);
+#pragma unroll
             for (int e = 0; e < 16; e += 4)
               *reinterpret_cast<uint4*>(corner + lane * kPitch + i + e) =
                   make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+          }
+          if (nan && lane < rows) {
+            const int adapter = p.w.tiles[(blockIdx.x + (uint32_t)n * gridDim.x) / (uint32_t)p.col_blocks].x;
+            const uint16_t* h = p.w.h + (int64_t)(u.first + 32 * (q & (u.blocks() - 1)) + lane) * 2 * p.rs;
+            const __nv_bfloat16* B = a.B + adapter * a.b_slot;
+#pragma unroll 1
+            for (int i = 0, col = u.col0 + 32 * c; i < 32 && col < a.N; ++i, ++col) {
+              float* s = corner + lane * kPitch + i;
+              if (*s != *s) *s = sum_of_terms(h, h + p.rs, B + col * a.b_row, u.rank());
+            }
           }
         }
         __syncwarp();

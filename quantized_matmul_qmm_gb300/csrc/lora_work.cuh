@@ -74,6 +74,17 @@ QMM_DEV void put_terms(uint16_t* hi, uint16_t* lo, const float4& s) {
                  two_bf16(left_of(s.z, bf16lo_to_f32(b)), left_of(s.w, bf16hi_to_f32(b))));
 }
 
+// A row's sum over the ranks for one column, value by value, where the products gave NaN: an
+// infinity in B times h's two terms can be infinities of both signs, or 0 times infinity
+// for one of them, while it is an infinity times their sum.
+QMM_DEV float sum_of_terms(const uint16_t* hi, const uint16_t* lo, const __nv_bfloat16* b, int rank) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < rank && s == s; ++j)
+    s = fmaf(bf16lo_to_f32(hi[j]) + bf16lo_to_f32(lo[j]), __bfloat162float(b[j]), s);
+  return s;
+}
+
 // both products of a routed call (lora_umma.cu)
 cudaError_t launch_lora_products(const LoraArgs& a, const LoraWork& w, bool copy_none, cudaStream_t stream);
 
