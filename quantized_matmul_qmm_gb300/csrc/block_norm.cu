@@ -167,7 +167,7 @@ QMM_DEV void weights(const float* w, const Place<kG, kOff>& pl, bool aligned16, 
   if (!kOff && aligned16) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      // past the row: the last group's, which multiply zeros
+      // past the row: the last group's, whose products are not used
       const float4 a = __ldg(reinterpret_cast<const float4*>(w + min(pl.at(g), pl.D - 4)));
       x[g][0] = a.x, x[g][1] = a.y, x[g][2] = a.z, x[g][3] = a.w;
     }
@@ -400,7 +400,13 @@ block_norm_kernel(NormArgs a, int off_step, bool weights16, float inv_d) {
         if constexpr (kRing) get_residual();
 #pragma unroll
         for (int i = 0; i < 4 * kG; ++i)
-          v[i] = fmaf(a.scale, v[i], res[i / 4].at(i % 4));   // outside the row: zeros throughout
+          v[i] = fmaf(a.scale, v[i], res[i / 4].at(i % 4));
+        // outside the row: zeros, also where the last weights or gates there are no numbers
+        if (!kOff && !pl.all()) {
+#pragma unroll
+          for (int i = 0; i < 4 * kG; ++i)
+            if (!pl.some(i / 4)) v[i] = 0.f;
+        }
       } else {
         if constexpr (kRing) get_residual();
 #pragma unroll
