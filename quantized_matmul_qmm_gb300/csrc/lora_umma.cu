@@ -42,6 +42,13 @@ constexpr int kInnerRanks = 128;                            // whose sums meet a
 constexpr int kInnerPitch = kInnerRanks + 4;                // floats of a row of sums
 constexpr int kInnerSums = 128 * kInnerPitch * 4;
 constexpr int kInnerMaxStages = 4;
+// Two blocks on an SM and never three, of whichever calls: each may hold 256 columns of
+// TMEM while it waits for its cluster, so that a third would wait for columns, and two
+// clusters' blocks could wait for one another's.  By shared memory, whatever registers
+// they take: an SM has 228 KB, of which a block uses one besides its own.
+constexpr int kInnerLeast = 77 * 1024, kInnerMost = 112 * 1024;
+static_assert(3 * (kInnerLeast + 1024) > 228 * 1024 && 2 * (kInnerMost + 1024) <= 228 * 1024, "two blocks on an SM");
+static_assert(1024 + kInnerSums <= kInnerLeast, "the sums");
 
 struct InnerParams {
   LoraArgs a;
@@ -568,7 +575,7 @@ cudaError_t launch_inner(const LoraArgs& a, const LoraWork& w, cudaStream_t stre
   p.rs = lora_rank_stride(a.max_rank);
   const int n16 = (a.max_rank + 15) / 16 * 16;
   p.stage_bytes = kTileBytes16 + (n16 * 128 + 1023) / 1024 * 1024;
-  // two blocks per SM: as many stages as 100 KB hold
+  // as many stages as 100 KB hold
   p.stages = std::max(2, std::min(kInnerMaxStages, 100 * 1024 / p.stage_bytes));
   p.tmem_cols = 32;
   while ((int)p.tmem_cols < n16) p.tmem_cols *= 2;
@@ -579,10 +586,10 @@ cudaError_t launch_inner(const LoraArgs& a, const LoraWork& w, cudaStream_t stre
   while (p.cluster > 1 && (filled * p.cluster > fit || 2 * p.cluster > chunks)) p.cluster /= 2;
   const int64_t most = lora_max_tiles(a.M, a.n_adapters);
   const int clusters = (int)std::min<int64_t>(most, std::max(1, fit / p.cluster));
-  const size_t smem = 1024 + (size_t)std::max(kInnerSums, p.stages * p.stage_bytes);
+  const size_t smem = std::max(kInnerLeast, 1024 + p.stages * p.stage_bytes);
   static std::atomic<uint64_t> done{0};
   const cudaError_t err = set_once(done, reinterpret_cast<const void*>(lora_inner_kernel),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kInnerMost);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
