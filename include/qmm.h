@@ -920,6 +920,12 @@ qmm_status qmm_token_logprobs(const void* logits, qmm_dtype type, int64_t M, int
                               const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
                               int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
                               cudaStream_t stream);
+/* The same, with `other` (any value) in logprobs where qmm_token_logprobs writes nothing:
+ * for a token of -1 or outside [-1, V). */
+qmm_status qmm_token_logprobs_or(const void* logits, qmm_dtype type, int64_t M, int64_t V, int64_t ld, float scale,
+                                 const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
+                                 int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                                 float other, cudaStream_t stream);
 
 /* ========================================================================
  * Diagnostics

@@ -68,6 +68,8 @@ struct LogprobArgs {
   int64_t ld_tokens;
   int G;
   float* logprobs;
+  bool write_other;    // `other` for tokens that are not scored
+  float other;
   float* entropy;      // or null
   int top_k;
   int32_t* top_ids;

@@ -45,6 +45,43 @@ bool stride8(int64_t stride, int64_t count, int64_t least) {
   return count <= 1 || (stride >= least && stride <= (INT64_MAX >> 5) / count && stride % 8 == 0);
 }
 
+qmm_status token_logprobs(const void* logits, qmm_dtype type, int64_t M, int64_t V, int64_t ld, float scale,
+                          const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
+                          int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                          const float* other, cudaStream_t stream) {
+  if (!float_type(type) || M < 0 || V < 1 || G < 0 || top_k < 0 || !(scale > 0.f) || !std::isfinite(scale))
+    return QMM_ERR_INVALID_ARG;
+  if (!rows_ok(ld, M, V) || (G > 0 && !rows_ok(ld_tokens, M, G))) return QMM_ERR_INVALID_ARG;
+  if (entropy == nullptr && G == 0 && top_k == 0) return QMM_ERR_INVALID_ARG;
+  if (top_k > kMaxTop || V >= INT32_MAX - 65536 || G > 1024 || M >= (int64_t)1 << 26) return QMM_ERR_UNSUPPORTED;
+  if (M == 0) return QMM_OK;
+  if (logits == nullptr || !aligned(logits, size_of(type)) || !aligned(entropy, 4)) return QMM_ERR_INVALID_ARG;
+  if (G > 0 && (tokens == nullptr || logprobs == nullptr || !aligned(tokens, 4) || !aligned(logprobs, 4)))
+    return QMM_ERR_INVALID_ARG;
+  if (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr || !aligned(top_ids, 4) ||
+                    !aligned(top_logprobs, 4)))
+    return QMM_ERR_INVALID_ARG;
+  LogprobArgs a{};
+  a.logits = logits;
+  a.bf16 = type == QMM_BF16;
+  a.M = (int)M;
+  a.V = (int)V;
+  a.ld = M > 1 ? ld : 0;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.ld_tokens = M > 1 ? ld_tokens : 0;
+  a.G = (int)G;
+  a.logprobs = logprobs;
+  a.write_other = other != nullptr;
+  a.other = other != nullptr ? *other : 0.f;
+  a.entropy = entropy;
+  a.top_k = (int)top_k;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.dev_status = dev_status;
+  return beside_status(launch_token_logprobs(a, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,35 +201,16 @@ qmm_status qmm_token_logprobs(const void* logits, qmm_dtype type, int64_t M, int
                               const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
                               int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
                               cudaStream_t stream) {
-  if (!float_type(type) || M < 0 || V < 1 || G < 0 || top_k < 0 || !(scale > 0.f) || !std::isfinite(scale))
-    return QMM_ERR_INVALID_ARG;
-  if (!rows_ok(ld, M, V) || (G > 0 && !rows_ok(ld_tokens, M, G))) return QMM_ERR_INVALID_ARG;
-  if (entropy == nullptr && G == 0 && top_k == 0) return QMM_ERR_INVALID_ARG;
-  if (top_k > kMaxTop || V >= INT32_MAX - 65536 || G > 1024 || M >= (int64_t)1 << 26) return QMM_ERR_UNSUPPORTED;
-  if (M == 0) return QMM_OK;
-  if (logits == nullptr || !aligned(logits, size_of(type)) || !aligned(entropy, 4)) return QMM_ERR_INVALID_ARG;
-  if (G > 0 && (tokens == nullptr || logprobs == nullptr || !aligned(tokens, 4) || !aligned(logprobs, 4)))
-    return QMM_ERR_INVALID_ARG;
-  if (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr || !aligned(top_ids, 4) ||
-                    !aligned(top_logprobs, 4)))
-    return QMM_ERR_INVALID_ARG;
-  LogprobArgs a{};
-  a.logits = logits;
-  a.bf16 = type == QMM_BF16;
-  a.M = (int)M;
-  a.V = (int)V;
-  a.ld = M > 1 ? ld : 0;
-  a.scale = scale;
-  a.tokens = tokens;
-  a.ld_tokens = M > 1 ? ld_tokens : 0;
-  a.G = (int)G;
-  a.logprobs = logprobs;
-  a.entropy = entropy;
-  a.top_k = (int)top_k;
-  a.top_ids = top_ids;
-  a.top_logprobs = top_logprobs;
-  a.dev_status = dev_status;
-  return beside_status(launch_token_logprobs(a, stream));
+  return token_logprobs(logits, type, M, V, ld, scale, tokens, ld_tokens, G, logprobs, entropy, top_k, top_ids,
+                        top_logprobs, dev_status, nullptr, stream);
+}
+
+qmm_status qmm_token_logprobs_or(const void* logits, qmm_dtype type, int64_t M, int64_t V, int64_t ld, float scale,
+                                 const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
+                                 int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                                 float other, cudaStream_t stream) {
+  return token_logprobs(logits, type, M, V, ld, scale, tokens, ld_tokens, G, logprobs, entropy, top_k, top_ids,
+                        top_logprobs, dev_status, &other, stream);
 }
 
 }  // extern "C"

@@ -515,6 +515,7 @@ token_logprobs_kernel(LogprobArgs a, int cluster, int segs, int steps) {
     }
     if (token < 0 || token >= a.V) {
       if (token != -1) set_status(a.dev_status, QMM_ERR_INVALID_ARG);
+      if (a.write_other) a.logprobs[(int64_t)row * a.G + g] = a.other;
       continue;
     }
     a.logprobs[(int64_t)row * a.G + g] = sound ? (token_x - st.m) * a.scale - log_sum : NAN;

@@ -117,6 +117,8 @@ SIGNATURES = {
                                 _vp]),
     "qmm_token_logprobs": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.c_float, _vp, _i64, _i64, _vp, _vp, _i64,
                                       _vp, _vp, _vp, _vp]),
+    "qmm_token_logprobs_or": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.c_float, _vp, _i64, _i64, _vp, _vp, _i64,
+                                         _vp, _vp, _vp, _c.c_float, _vp]),
     "qmm_probe_hbm_read": (_c.c_int, [_vp, _sz, _c.c_int, _vp, _vp, _vp]),
     "qmm_selftest_wait_timeout": (_c.c_int, [_c.c_uint64, _vp, _vp, _vp]),
 }
@@ -685,6 +687,7 @@ _OUT_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16, torch.int8: QMM_
 _F32, _BF16 = torch.float32, torch.bfloat16
 _F32_ONLY, _BF16_ONLY, _INT32_ONLY = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 _empty = torch.empty
+_NAN = float("nan")
 _current_device = getattr(torch._C, "_cuda_getDevice", None)   # None: torch without CUDA
 
 # Every tensor has to lie on the current GPU: an address of another device or of
@@ -831,14 +834,17 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
     """Log probabilities of tokens (int32 [M][G] or [M], -1: none) under
     softmax(scale * logits), logits fp32 or bf16 [M][V], with the entropy fp32 [M]
     (entropy=False: none) and the top_k <= 32 alternatives, through
-    qmm_token_logprobs.  Returns (logprobs, entropy, top_ids, top_logprobs), None
-    for what was not asked for."""
+    qmm_token_logprobs.  A token of -1 (or outside the vocabulary, which dev_status
+    tells) leaves its place in a logprobs tensor given as it was; in one made here it
+    is NaN.  Returns (logprobs, entropy, top_ids, top_logprobs), None for what was not
+    asked for."""
     fn = "token_logprobs"
     dev = _device_of(fn, logits)
     M, V = shape = logits.shape
     ld = _rows(fn, dev, logits, shape, _ROW_TYPES)
     device = logits.device
     G = ldt = 0
+    made = False
     p_tokens = p_logprobs = p_ids = p_top = p_entropy = p_status = None
     if tokens is not None:
         if tokens.dim() == 2:
@@ -851,7 +857,7 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
             G, ldt = 1, tokens.stride(0)
         p_tokens = tokens.data_ptr()
         if logprobs is None:
-            logprobs = _empty(tokens.shape, dtype=_F32, device=device)
+            logprobs, made = _empty(tokens.shape, dtype=_F32, device=device), True
             p_logprobs = logprobs.data_ptr()
         else:
             p_logprobs = _vector(fn, dev, logprobs, M * G, _F32)
@@ -877,9 +883,12 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
         top_ids = top_logprobs = None
     if dev_status is not None:
         p_status = _vector(fn, dev, dev_status, 1, _I32)
-    status = lib.qmm_token_logprobs(
-        logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy, top_k,
-        p_ids, p_top, p_status, _raw_stream(dev))
+    args = (logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy,
+            top_k, p_ids, p_top, p_status)
+    if made:
+        status = lib.qmm_token_logprobs_or(*args, _NAN, _raw_stream(dev))
+    else:
+        status = lib.qmm_token_logprobs(*args, _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_token_logprobs", status)
     return logprobs, entropy, top_ids, top_logprobs

@@ -1,0 +1,51 @@
+"""CPU tests of the binding of what runs beside the projections: what it makes itself
+and what it says of a call that it or the library refuses."""
+import math
+
+import pytest
+import torch
+
+F, BF, I32 = torch.float32, torch.bfloat16, torch.int32
+P = 1 << 20          # an aligned address that nothing reads
+
+
+@pytest.fixture
+def calls(qmm, monkeypatch):
+    """The calls that reach the library; host tensors pass for the device's."""
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args)) or qmm.QMM_OK
+
+    monkeypatch.setattr(qmm, "lib", Lib())
+    monkeypatch.setattr(qmm, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(qmm, "_current_device", lambda: -1)
+    return seen
+
+
+def test_log_probabilities_made_here_are_written_throughout(qmm, calls):
+    """Skipped tokens' places are NaN where the binding makes them, not what the memory
+    held, and as they were where they are given."""
+    for tokens in (torch.full((64, 3), -1, dtype=I32), torch.full((64,), -1, dtype=I32)):
+        lp = qmm.token_logprobs(torch.zeros(64, 16), tokens)[0]
+        name, args = calls.pop()
+        assert name == "qmm_token_logprobs_or" and math.isnan(args[15]) and args[9] == lp.data_ptr()
+        given = torch.full(tokens.shape, 5.0)
+        assert qmm.token_logprobs(torch.zeros(64, 16), tokens, logprobs=given)[0] is given
+        assert calls.pop()[0] == "qmm_token_logprobs"
+    qmm.token_logprobs(torch.zeros(64, 16), top_k=3)
+    assert calls.pop()[0] == "qmm_token_logprobs"
+
+
+def test_refusals_with_a_value_for_other_tokens(qmm):
+    base = dict(x=P, type=qmm.QMM_F32, M=3, V=50, ld=50, scale=1.0, tokens=P, ldt=2, G=2, lp=P, ent=P, k=4, ids=P, top=P,
+                status=None, other=math.nan)
+
+    def call(**over):
+        return qmm.lib.qmm_token_logprobs_or(*{**base, **over}.values(), None)
+
+    for over in (dict(x=None), dict(type=qmm.QMM_S8), dict(ld=49), dict(scale=0.0), dict(tokens=None), dict(lp=P + 2),
+                 dict(k=-1), dict(top=None), dict(ent=None, G=0, k=0)):
+        assert call(**over) == qmm.QMM_ERR_INVALID_ARG, over
+    assert call(k=33) == qmm.QMM_ERR_UNSUPPORTED and call(M=0) == qmm.QMM_OK
