@@ -895,7 +895,7 @@ qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, con
 /* Log probabilities of rows of logits, with p_i = exp(scale * x_i) / sum_j exp(scale * x_j):
  *
  * logits   [M][V] fp32 or bf16 (type), row stride ld elements, aligned to the element.
- * scale    > 0, finite: 1 / temperature.
+ * scale    > 0, at most 2^127: 1 / temperature.
  * tokens   device int32 [M][G], row stride ld_tokens: the tokens to score (NULL with G = 0).
  * logprobs fp32 [M][G] out, contiguous: log p of each; not written for token -1.
  * entropy  fp32 [M] out: -sum p log p, or NULL.
@@ -903,9 +903,9 @@ qmm_status qmm_lora_add(const qmm_lora_set* set, const void* X, int64_t ldx, con
  *          with top_k = 0): the tokens of the largest logits in falling order, equal ones
  *          by rising index (-0 equals 0), with their log probabilities.  Tokens at
  *          -infinity are no alternatives: places beyond the others hold -1 and -infinity.
- * A logit of -infinity has probability 0.  A row with a NaN or +infinity, or with
- * nothing above -infinity, has no distribution: its logprobs, entropy and top_logprobs are
- * NaN and its top_ids -1.
+ * A logit of -infinity has probability 0, as one has whose difference from the largest
+ * passes fp32's range.  A row with a NaN or +infinity, or with nothing above -infinity, has
+ * no distribution: its logprobs, entropy and top_logprobs are NaN and its top_ids -1.
  * Sums are fp32, taken relative to the row's largest logit with that logit's own 1 kept
  * apart, so that log probabilities next to 0 keep their relative accuracy.  top_ids are
  * exact.  Results are the same from run to run; how a row is split between blocks (and its

@@ -58,6 +58,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, void* workspace, cudaStream_t str
 
 // ---- token log probabilities (logprobs.cu) ----
 constexpr int kMaxTop = 32;
+constexpr float kMaxScale = 0x1p127f;   // times log2(e) it is still finite
 struct LogprobArgs {
   const void* logits;
   bool bf16;

@@ -49,7 +49,7 @@ qmm_status token_logprobs(const void* logits, qmm_dtype type, int64_t M, int64_t
                           const int32_t* tokens, int64_t ld_tokens, int64_t G, float* logprobs, float* entropy,
                           int64_t top_k, int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
                           const float* other, cudaStream_t stream) {
-  if (!float_type(type) || M < 0 || V < 1 || G < 0 || top_k < 0 || !(scale > 0.f) || !std::isfinite(scale))
+  if (!float_type(type) || M < 0 || V < 1 || G < 0 || top_k < 0 || !(scale > 0.f && scale <= kMaxScale))
     return QMM_ERR_INVALID_ARG;
   if (!rows_ok(ld, M, V) || (G > 0 && !rows_ok(ld_tokens, M, G))) return QMM_ERR_INVALID_ARG;
   if (entropy == nullptr && G == 0 && top_k == 0) return QMM_ERR_INVALID_ARG;

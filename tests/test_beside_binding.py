@@ -49,3 +49,15 @@ def test_refusals_with_a_value_for_other_tokens(qmm):
                  dict(k=-1), dict(top=None), dict(ent=None, G=0, k=0)):
         assert call(**over) == qmm.QMM_ERR_INVALID_ARG, over
     assert call(k=33) == qmm.QMM_ERR_UNSUPPORTED and call(M=0) == qmm.QMM_OK
+
+
+def test_scales_whose_product_with_log2_e_is_infinite(qmm):
+    """0 times that product would be NaN for a row's largest logit."""
+    def call(entry, scale, *more):
+        return getattr(qmm.lib, entry)(P, qmm.QMM_F32, 0, 50, 50, scale, P, 2, 2, P, P, 4, P, P, None, *more, None)
+
+    for scale in (1.702e38, 2.4e38, 3.4e38, math.inf):
+        assert call("qmm_token_logprobs", scale) == qmm.QMM_ERR_INVALID_ARG
+        assert call("qmm_token_logprobs_or", scale, 0.0) == qmm.QMM_ERR_INVALID_ARG
+    for scale in (2.0 ** 127, 1e30, 1e-45):
+        assert call("qmm_token_logprobs", scale) == qmm.QMM_OK

@@ -40,3 +40,19 @@ def test_skipped_tokens_in_a_graph(qmm, cuda):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.isnan(got[:, skipped]).all() and torch.isfinite(got[:, 1 - skipped]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [5, 3001])
+def test_the_largest_scale(qmm, cuda, V, dtype):
+    """All of a row's probability at its largest logits, whatever lies between them."""
+    x = torch.full((3, V), -2.0, dtype=dtype, device=cuda)
+    x[0, 2] = x[1, 1] = x[1, 4] = 0.5
+    x[2, 3] = -float("inf")
+    tokens = torch.tensor([[2, 0], [4, 0], [0, 3]], dtype=torch.int32, device=cuda)
+    lp, entropy, ids, top = qmm.token_logprobs(x, tokens, top_k=3, scale=2.0 ** 127)
+    n = torch.tensor([1.0, 2.0, V - 1.0], device=cuda)
+    torch.testing.assert_close(entropy, n.log(), rtol=1e-6, atol=0)
+    torch.testing.assert_close(lp[:, 0], -n.log(), rtol=1e-6, atol=0)
+    assert (lp[:, 1] == -float("inf")).all() and ids[0].tolist() == [2, 0, 1] and ids[1].tolist() == [1, 4, 0]
+    assert float(top[0, 1]) == -float("inf") and ids[2].tolist() == [0, 1, 2]
