@@ -825,9 +825,12 @@ typedef struct {
  *          q = clamp(rint_even(fl(v / s)), -127, 127), 0 where s == 0 (ldo % 16 == 0,
  *          base 16-byte aligned: what qmm_int8_gemm takes); or NULL to store none.
  * Arithmetic is fp32 on the values as read; sum and out are rounded once, each from
- * the fp32 sum (out does not see sum's rounding).  Squares are fp32: a row whose
- * mean square passes 3e38 gives zeros from a norm.  Infinities and NaN stay in their
- * row; with QMM_S8 such a row's codes and scale are unspecified.
+ * the fp32 sum (out does not see sum's rounding).  Sums of squares are fp32 too: a row
+ * whose squares (QMM_NORM_LAYER: of the values less their mean) add up to more than 3.4e38
+ * gives zeros from a norm, times its weight and with its bias, and one whose values do so
+ * gives NaN from a layer norm.  Squares below 1.2e-38 lose bits or are 0, which counts
+ * where eps does not cover them: with eps = 0 a row of zeros is NaN.  Infinities and NaN
+ * stay in their row; with QMM_S8 such a row's codes and scale are unspecified.
  * Results are the same from run to run and do not depend on the other rows.  How a
  * row's sums are split goes by T, D and alignment.
  * Pointers are aligned to their element, any stride and D go; rows whose
