@@ -795,7 +795,10 @@ def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tenso
     X bf16 [M][K], ids int32 [M], A bf16 [adapters][max_rank][K], B bf16
     [adapters][N][max_rank], ranks int32 and scales fp32 [adapters] (or None), base
     fp32 [M][N] (or None for zeros).  out is made when not given; out=base adds in
-    place.  Returns out."""
+    place.  X, A and B are read 16 bytes at a time: their data has to begin at 16 bytes,
+    the strides of all their dimensions but the last to be multiples of 8 elements (a B
+    of another rank is the first columns of one that is wider), and B's last row to be
+    readable up to the next multiple of 8.  Returns out."""
     fn = "lora_add"
     dev = _device_of(fn, X)
     M, K = shape = X.shape
@@ -825,6 +828,11 @@ def lora_add(X: torch.Tensor, ids: torch.Tensor, A: torch.Tensor, B: torch.Tenso
         weights, X.data_ptr(), ldx, _vector(fn, dev, ids, M, _I32), M, p_base, ldb, out.data_ptr(), ldo,
         workspace.data_ptr(), workspace.nbytes, _vector(fn, dev, dev_status, 1, _I32), _raw_stream(dev))
     if status != QMM_OK:
+        if status == QMM_ERR_INVALID_ARG:
+            for name, t in (("X", X), ("A", A), ("B", B)):
+                if t.data_ptr() % 16 or any(s % 8 for s, n in zip(t.stride()[:-1], t.shape) if n > 1):
+                    raise ValueError(f"{fn}: {name} has to begin at 16 bytes and its strides but the last to be "
+                                     f"multiples of 8 elements, got {tuple(t.shape)} with strides {t.stride()}")
         _check("qmm_lora_add", status)
     return out
 

@@ -61,3 +61,17 @@ def test_scales_whose_product_with_log2_e_is_infinite(qmm):
         assert call("qmm_token_logprobs_or", scale, 0.0) == qmm.QMM_ERR_INVALID_ARG
     for scale in (2.0 ** 127, 1e30, 1e-45):
         assert call("qmm_token_logprobs", scale) == qmm.QMM_OK
+
+
+def test_adapters_off_the_16_bytes_are_named(qmm, monkeypatch):
+    """The library refuses them; the binding says which tensor and why."""
+    monkeypatch.setattr(qmm, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(qmm, "_current_device", lambda: -1)
+    z = lambda *shape: torch.zeros(shape, dtype=BF)
+    ok = dict(X=z(4, 16), ids=torch.zeros(4, dtype=I32), A=z(3, 5, 16), B=z(3, 24, 8)[:, :, :5])
+    for name, bad in (("B", z(3, 24, 5)), ("B", z(3, 24, 12)[:, :, :5]), ("A", z(3, 5, 20)[:, :, :16]),
+                      ("X", z(4, 20)[:, :16]), ("X", z(4, 32)[:, 3:19]), ("A", z(3, 5, 24)[:, :, 4:20])):
+        with pytest.raises(ValueError, match=f"lora_add: {name} has to begin at 16 bytes"):
+            qmm.lora_add(**{**ok, name: bad})
+    with pytest.raises(qmm.QmmError, match="qmm_lora_add"):  # another reason keeps the library's own word
+        qmm.lora_add(**ok, base=torch.zeros(1, 24).expand(4, 24))
