@@ -684,6 +684,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
 _NORM_KINDS = {"rms": 1, "layer": 2}
 _OUT_TYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16, torch.int8: QMM_S8}
+_OUT_NAMES = {"bf16": torch.bfloat16, "f32": torch.float32}
 _F32, _BF16 = torch.float32, torch.bfloat16
 _F32_ONLY, _BF16_ONLY, _INT32_ONLY = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 _empty = torch.empty
@@ -767,7 +768,7 @@ def block_norm(residual: torch.Tensor, branch=None, *, norm="rms", weight=None, 
             if out_type == "s8":       # rows of whole 16 bytes, as the int8 GEMM takes them
                 out = torch.empty((T, (D + 15) // 16 * 16), dtype=torch.int8, device=residual.device)[:, :D]
             else:
-                out = torch.empty(shape, dtype=_BF16 if out_type == "bf16" else _F32, device=residual.device)
+                out = torch.empty(shape, dtype=_OUT_NAMES[out_type], device=residual.device)
         ldo, p_out, o_type = _rows(fn, dev, out, shape, _OUT_TYPES), out.data_ptr(), _OUT_TYPES[out.dtype]
         if o_type == QMM_S8:
             if s_x is None:

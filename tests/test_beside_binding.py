@@ -75,3 +75,13 @@ def test_adapters_off_the_16_bytes_are_named(qmm, monkeypatch):
             qmm.lora_add(**{**ok, name: bad})
     with pytest.raises(qmm.QmmError, match="qmm_lora_add"):  # another reason keeps the library's own word
         qmm.lora_add(**ok, base=torch.zeros(1, 24).expand(4, 24))
+
+
+def test_an_unknown_output_type_is_refused(qmm, calls):
+    """As an unknown norm is; it gave fp32."""
+    for name in ("fp32", "f16", "int8", None):
+        with pytest.raises(KeyError):
+            qmm.block_norm(torch.zeros(4, 16), out_type=name)
+    assert not calls
+    for name, dtype in (("bf16", BF), ("f32", F), ("s8", torch.int8)):
+        assert qmm.block_norm(torch.zeros(4, 16), out_type=name)[1].dtype == dtype
