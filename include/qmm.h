@@ -833,8 +833,12 @@ typedef struct {
  * stay in their row; with QMM_S8 such a row's codes and scale are unspecified.
  * Results are the same from run to run and do not depend on the other rows.  How a
  * row's sums are split goes by T, D and alignment.
- * Pointers are aligned to their element, any stride and D go; rows whose
- * base and strides are whole 16 bytes, with D % 8 == 0, take the faster form.
+ * Pointers are aligned to their element, any stride and D go.  Rows are read and
+ * written four values at a time where every tensor (but QMM_S8 codes) begins at four
+ * elements, their strides differ by multiples of four, and D is at most 16380; a bf16 gate
+ * of one row wants D and the strides to be multiples of four for that.  Fastest are D (up
+ * to 16384 then) and strides of such multiples with weights at 16 bytes.  Everything else
+ * goes value by value.
  * T = 0 does nothing.  Errors: QMM_ERR_INVALID_ARG for null or misaligned
  * pointers, neither sum nor out, a bad type, kind, eps, scale or stride;
  * QMM_ERR_UNSUPPORTED for D > 32768 or T >= 2^31.

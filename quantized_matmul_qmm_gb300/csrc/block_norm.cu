@@ -10,8 +10,8 @@
 // one maximum), so that nothing is read again.
 //
 // Measured against a copy's rate: 16384 rows of 4096 with a norm on either side, all
-// fp32 but for out (940 MB), 145 us, 0.97; 4096 of 16384 146; 2049 of 4608 to int8 with a
-// channel gate 28 us, 0.65; 5000 layer norms of 1000 over bf16 with a gate of rows 12.0 us,
+// fp32 but for out (940 MB), 146 us, 0.96; 4096 of 16384 150; 2049 of 4608 to int8 with a
+// channel gate 27.5 us, 0.67; 5000 layer norms of 1000 over bf16 with a gate of rows 12.0 us,
 // 0.62, of 1001 16.1, 0.46: rows that begin anywhere touch more sectors, and their ends
 // go value by value.  Eight rows of 1024 1.7 us.
 //
@@ -284,8 +284,9 @@ struct Copies {
 };
 
 // Threads of a block at most, and blocks per SM that the registers have to allow: two
-// of rows of up to 4608 in line (2049 of them 25.7 us, with one of 576 threads 34), eight
-// of one-warp rows (20000 layer norms of 255 25.9 us, with six 29.1).
+// of rows of up to 4608 in line (2049 of them to int8 without a gate 25.8 us, with one block
+// of 576 threads 34), eight of one-warp rows (20000 layer norms of 255 25.9 us, with six 29.1,
+// although 16 values a lane then spill 48 to 224 bytes).
 template <int kG, bool kOff, bool kRing>
 struct Bounds {
   static constexpr int kThreads = kRing ? (kG == 2 && !kOff ? 576 : 1024) : kG == 1 ? 1024 : 128;

@@ -11,10 +11,10 @@
 // one's loads under way, and leaves its statistics in the first block's shared memory.
 //
 // Measured against a copy's rate: 1024 rows of 151936 in fp32 with one alternative
-// (623 MB) 98 us, 0.95; 512 rows in bf16 44 us, 0.53, there bound by issue slots, an
-// exponential and about six instructions a logit.  Few rows wait for one another's
-// steps: 64 rows 12.2 us, with five alternatives 15.7 (5.8 at that rate); a row with
-// 20 of them 8.8.
+// (623 MB) 98 us, 0.95; 512 rows in bf16 43 us, 0.54: two rounds of the 304 blocks that the
+// GPU holds (304 rows take 24 us, 608 44), in which 13 to 14 instructions a logit, as many
+// as in fp32, keep 72 % of the issue slots busy.  Few rows wait for one another's steps: 64
+// rows 12 us, with five alternatives 15.7 (5.8 at that rate); a row with 20 of them 8.9.
 //
 // Alternatives cost the stream the maxima of pieces, four to a segment: the k-th
 // largest of 64 groups' maxima (of threads' logits, or of segments in a cluster) is a

@@ -15,7 +15,7 @@
 // second (4.9 at a copy's rate); 8 rows at K = 1024, N = 2048 and rank 16 6.3 us.
 //
 // The inner sums h = A x are fp32.  For the second product h * s_a is written
-// as two bf16 terms, h = hi + lo within 2^-16 |h|: with one term (2^-9) the
+// as two bf16 terms, h = hi + lo within 2^-16 |h|: with one term (2^-8) the
 // rounding of h would be far above the fp32 rounding of out.
 #include <algorithm>
 #include <atomic>

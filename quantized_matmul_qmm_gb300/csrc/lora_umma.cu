@@ -7,7 +7,7 @@
 // TFLOP/s measured on this part) does in that time.
 //
 // Measured: 4097 prompt rows over 6 adapters of ranks 8 to 64 at K = N = 4608 (192 MB)
-// 55 us with the routing's 7, 0.52 of a copy's rate; 16000 rows 170 us, 0.66.  2048 rows at
+// 55 us with the routing's 7, 0.52 of a copy's rate; 16000 rows 168 us, 0.66.  2048 rows at
 // K = 2048, N = 12288 and ranks 100 to 256 70 us, 0.48.  What is lost: three launches
 // that cannot overlap (the second product's blocks take a whole SM's shared memory), the
 // first's meeting over the cluster, and in the second what its registers hold of base
