@@ -39,8 +39,8 @@ def test_log_probabilities_made_here_are_written_throughout(qmm, calls):
 
 
 def test_refusals_with_a_value_for_other_tokens(qmm):
-    base = dict(x=P, type=qmm.QMM_F32, M=3, V=50, ld=50, scale=1.0, tokens=P, ldt=2, G=2, lp=P, ent=P, k=4, ids=P, top=P,
-                status=None, other=math.nan)
+    base = dict(x=P, type=qmm.QMM_F32, M=3, V=50, ld=50, scale=1.0, tokens=P, ldt=2, G=2, lp=P, ent=P, k=4, ids=P,
+                top=P, status=None, other=math.nan)
 
     def call(**over):
         return qmm.lib.qmm_token_logprobs_or(*{**base, **over}.values(), None)

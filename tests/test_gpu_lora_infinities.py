@@ -34,8 +34,8 @@ def case(dev, M, K, N, adapters, rank, seed=0):
     scales = 0.1 + r(adapters).abs()
     scales[0] = 1.0
     b16 = torch.bfloat16
-    return dict(X=X.to(b16).to(dev), ids=ids.to(torch.int32).to(dev), A=A.to(b16).to(dev), B=B.to(b16).to(dev)[:, :, :rank],
-                base=r(M, N).to(dev), ranks=ranks.to(torch.int32).to(dev), scales=scales.to(dev))
+    return dict(X=X.to(b16).to(dev), ids=ids.to(torch.int32).to(dev), A=A.to(b16).to(dev),
+                B=B.to(b16).to(dev)[:, :, :rank], base=r(M, N).to(dev), ranks=ranks.to(torch.int32).to(dev), scales=scales.to(dev))
 
 
 def exact(a):
@@ -56,8 +56,8 @@ def exact(a):
 # few rows with ranks of each form, and rows routed to tiles of 128 with partly filled and full ones
 @pytest.mark.parametrize("M,K,N,adapters,rank", [
     (5, 64, 48, 1, 1), (5, 64, 48, 2, 8), (40, 264, 100, 3, 24), (30, 128, 131, 3, 50), (60, 512, 260, 2, 100),
-    (20, 96, 75, 2, 201), (300, 64, 257, 5, 16), (2000, 64, 48, 3, 8), (1600, 264, 131, 2, 40), (1700, 128, 300, 4, 150),
-    (1540, 72, 129, 30, 17)])
+    (20, 96, 75, 2, 201), (300, 64, 257, 5, 16), (2000, 64, 48, 3, 8), (1600, 264, 131, 2, 40),
+    (1700, 128, 300, 4, 150), (1540, 72, 129, 30, 17)])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_infinities_in_b(qmm, cuda, M, K, N, adapters, rank, inplace):
     a = case(cuda, M, K, N, adapters, rank)
