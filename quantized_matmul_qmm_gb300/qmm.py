@@ -892,12 +892,14 @@ def token_logprobs(logits: torch.Tensor, tokens=None, top_k: int = 0, scale: flo
         top_ids = top_logprobs = None
     if dev_status is not None:
         p_status = _vector(fn, dev, dev_status, 1, _I32)
-    args = (logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy,
-            top_k, p_ids, p_top, p_status)
     if made:
-        status = lib.qmm_token_logprobs_or(*args, _NAN, _raw_stream(dev))
+        status = lib.qmm_token_logprobs_or(
+            logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy,
+            top_k, p_ids, p_top, p_status, _NAN, _raw_stream(dev))
     else:
-        status = lib.qmm_token_logprobs(*args, _raw_stream(dev))
+        status = lib.qmm_token_logprobs(
+            logits.data_ptr(), _ROW_TYPES[logits.dtype], M, V, ld, scale, p_tokens, ldt, G, p_logprobs, p_entropy,
+            top_k, p_ids, p_top, p_status, _raw_stream(dev))
     if status != QMM_OK:
         _check("qmm_token_logprobs", status)
     return logprobs, entropy, top_ids, top_logprobs
