@@ -56,18 +56,22 @@ QMM_DEV float4 cluster_sum(uint32_t addr, int cluster) {
 }
 
 // h as the two bf16 terms that the second product takes, four ranks at a time: the
-// value rounded, and what that left.  An infinity (or a value that rounds to one) leaves
-// nothing: infinity less infinity would make NaN of it.
+// value rounded, and what that left.  A finite value does not round to infinity, which 0 in
+// B would make NaN of; an infinity leaves nothing, since infinity less infinity is NaN.
 QMM_DEV uint32_t two_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+QMM_DEV float below_inf(float x) {
+  constexpr float kMost = 0x1.FEp127f;   // of bf16
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kMost), kMost) : x;
 }
 QMM_DEV float left_of(float x, float rounded) {
   const float d = x - rounded;
   return fabsf(d) < INFINITY ? d : 0.f;
 }
 QMM_DEV void put_terms(uint16_t* hi, uint16_t* lo, const float4& s) {
-  const uint32_t a = two_bf16(s.x, s.y), b = two_bf16(s.z, s.w);
+  const uint32_t a = two_bf16(below_inf(s.x), below_inf(s.y)), b = two_bf16(below_inf(s.z), below_inf(s.w));
   *reinterpret_cast<uint2*>(hi) = make_uint2(a, b);
   *reinterpret_cast<uint2*>(lo) =
       make_uint2(two_bf16(left_of(s.x, bf16lo_to_f32(a)), left_of(s.y, bf16hi_to_f32(a))),

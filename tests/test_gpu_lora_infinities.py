@@ -81,3 +81,24 @@ def test_infinities_in_both(qmm, cuda, M):
     got = qmm.lora_add(**a).double().cpu().numpy()
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isinf(got), np.isinf(want))
     assert np.array_equal(np.sign(got[np.isinf(want)]), np.sign(want[np.isinf(want)]))
+
+
+@pytest.mark.parametrize("M", [6, 2000])
+def test_inner_sums_next_to_the_largest_number(qmm, cuda, M):
+    """Inner sums that are finite but above bf16's largest value: finite products, and
+    zeros beside B's zeros."""
+    K, N, rank = 64, 48, 3
+    A = torch.zeros((1, rank, K))
+    A[0, :, 0], A[0, :, 1] = (2.0 - 2.0 ** -7) * 2.0 ** 127, 2.0 ** 119   # half a step beyond it
+    A[0, 1] *= -1.0
+    B = torch.zeros((1, N, 8))
+    B[0, ::2, 0], B[0, ::3, 1] = 2.0 ** -100, 2.0 ** -101
+    X = torch.zeros((M, K))
+    X[:, :2] = 1.0
+    X[1, 1] = 0.0                                            # bf16's largest value itself
+    b16 = torch.bfloat16
+    got = qmm.lora_add(X.to(b16).to(cuda), torch.zeros(M, dtype=torch.int32, device=cuda), A.to(b16).to(cuda),
+                       B.to(b16).to(cuda)[:, :, :rank])
+    want = (X.double() @ A[0].double().t()) @ B[0, :, :rank].double().t()
+    assert torch.isfinite(got).all() and (got.cpu()[want == 0] == 0).all()
+    assert ((got.double().cpu() - want).abs() <= (2.0 ** -16 + 100 * O.U32) * 2 * want.abs().max()).all()
